@@ -23,7 +23,9 @@ __all__ = [
     "nsa_indexer_logits", "nsa_topk_transform", "nsa_topk_launches", "nsa_sparse_mla",
     "nsa_sparse_mla_workspace_bytes", "nsa_sparse_mla_plan", "nsa_set_mla_kv", "nsa_quantize_kv_cache", "nsa_dequantize_kv_paged",
     "nsa_set_index_k", "nsa_topk_transform_ragged", "nsa_flatten_page_table", "nsa_copy_buffers",
-    "nsa_check_bounded_wait", "nsa_local_attention", "nsa_status_read", "nsa_status_string", "nsa_abi_version",
+    "nsa_check_bounded_wait", "nsa_local_attention", "nsa_paged_mla", "nsa_paged_mla_workspace_bytes",
+    "alloc_paged_mla_workspace", "nsa_mla_key_weights", "nsa_evict_select", "nsa_evict_compact",
+    "nsa_evict_compact_workspace_bytes", "alloc_evict_workspace", "nsa_status_read", "nsa_status_string", "nsa_abi_version",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -38,7 +40,8 @@ EXPORTED_SYMBOLS = [
     "nsa_sparse_mla_workspace_bytes",
     "nsa_sparse_mla_plan", "nsa_set_mla_kv", "nsa_quantize_kv_cache", "nsa_dequantize_kv_paged", "nsa_set_index_k",
     "nsa_topk_transform_ragged", "nsa_flatten_page_table", "nsa_copy_buffers",
-    "nsa_check_bounded_wait", "nsa_local_attention",
+    "nsa_check_bounded_wait", "nsa_local_attention", "nsa_paged_mla", "nsa_paged_mla_workspace_bytes",
+    "nsa_mla_key_weights", "nsa_evict_select", "nsa_evict_compact", "nsa_evict_compact_workspace_bytes",
 ]
 
 _lib = None
@@ -85,6 +88,12 @@ def load(build_if_missing: bool = True):
         "nsa_copy_buffers": ([I, P, P, P, P], I),
         "nsa_check_bounded_wait": ([P, C.c_longlong, P], I),
         "nsa_local_attention": ([P, L, P, P, L, I, P, L, P, P, I, I, I, I, I, F, P, P, P, P], I),
+        "nsa_paged_mla": ([I, I, P, L, L, P, L, L, P, L, I, P, L, P, I, I, I, I, I, I, F, P, P, P, S, P, P], I),
+        "nsa_paged_mla_workspace_bytes": ([I, I, I, I, I, I, I, I], S),
+        "nsa_mla_key_weights": ([I, I, P, L, L, P, L, L, P, L, I, P, L, P, I, I, I, I, I, I, F, P, P, L, P, P], I),
+        "nsa_evict_select": ([P, L, P, I, I, I, I, I, P, L, P, P, P], I),
+        "nsa_evict_compact": ([I, P, L, I, P, P, I, P, L, I, L, I, P, P, P, L, P, S, P, P], I),
+        "nsa_evict_compact_workspace_bytes": ([I, I], S),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -420,3 +429,187 @@ def nsa_local_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
                                     nvb, total_q, Hq, Hkv, D, float(sm_scale), _ptr(out), _ptr(lse), _ptr(status),
                                     _stream(stream))
     _check("nsa_local_attention", rc)
+
+
+# ---------------------------------------------------------------- dense paged MLA attention
+
+def _paged_q(q_dtype: int, q_nope: torch.Tensor, q_rope: torch.Tensor):
+    """The query arguments of the C calls; a single row's or head's stride, which is
+    arbitrary, is replaced by what a packed tensor would have."""
+    R, H, dl = q_nope.shape
+    dr = q_rope.shape[2]
+    if tuple(q_rope.shape[:2]) != (R, H):
+        raise ValueError(f"q_rope {tuple(q_rope.shape)} does not match q_nope {tuple(q_nope.shape)}")
+    if (dl > 1 and q_nope.stride(2) != 1) or (dr > 1 and q_rope.stride(2) != 1):
+        raise ValueError("the elements of each query head must be adjacent (stride 1 in the last dimension)")
+    want = {DT_F32: torch.float32, DT_BF16: torch.bfloat16}.get(q_dtype)
+    if q_nope.dtype != want or q_rope.dtype != want:
+        raise ValueError(f"q must be {want} for this q_dtype, got {q_nope.dtype} and {q_rope.dtype}")
+    out = []
+    for q, d in ((q_nope, dl), (q_rope, dr)):
+        h = q.stride(1) if H > 1 else d
+        out += [_ptr(q), q.stride(0) if R > 1 else H * h, h]
+    return out
+
+
+def _paged_cache(kv_dtype: int, kv: torch.Tensor, page_size: int, d_latent: int, d_rope: int) -> int:
+    """Checks a cache of [slots, row] (or [pages, page_size, row]) and returns its page count."""
+    want = {DT_F32: 4 * (d_latent + d_rope), DT_BF16: 2 * (d_latent + d_rope),
+            DT_E4M3: d_latent + 4 * (d_latent // 128) + 2 * d_rope}[kv_dtype]
+    if not kv.is_contiguous() or kv.dim() not in (2, 3) or kv.shape[-1] * kv.element_size() != want:
+        raise ValueError(f"the cache must be contiguous rows of {want} bytes, got shape {tuple(kv.shape)} of {kv.dtype}")
+    slots = kv.numel() // kv.shape[-1]
+    if page_size < 1 or slots % page_size:
+        raise ValueError(f"{slots} slots are no whole pages of {page_size}")
+    return slots // page_size
+
+
+def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
+    """The library launches on the current device: every tensor must live there."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"expected CUDA tensors, got one on {t.device}")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _i32(name: str, t: torch.Tensor, n: int) -> torch.Tensor:
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous int32 values, got shape {tuple(t.shape)} of {t.dtype}")
+    return t
+
+
+def _table(t: torch.Tensor, B: int) -> torch.Tensor:
+    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B:
+        raise ValueError(f"page_table must be int32 [{B}, pages], got shape {tuple(t.shape)} of {t.dtype}")
+    return t
+
+
+def _table_ld(t: torch.Tensor, max_len: int, page_size: int) -> int:
+    if t.shape[1] * page_size < max_len:
+        raise ValueError(f"a page-table row of {t.shape[1]} pages of {page_size} does not hold {max_len} positions")
+    return _ld(t)
+
+
+def nsa_paged_mla_workspace_bytes(q_dtype: int, kv_dtype: int, R: int, rows_per_req: int, H: int, max_row_len: int,
+                                  d_latent: int = 512, d_rope: int = 64) -> int:
+    return int(load().nsa_paged_mla_workspace_bytes(q_dtype, kv_dtype, R, rows_per_req, H, d_latent, d_rope, max_row_len))
+
+
+def alloc_paged_mla_workspace(q_dtype: int, kv_dtype: int, R: int, rows_per_req: int, H: int, max_row_len: int,
+                              d_latent: int = 512, d_rope: int = 64, device="cuda") -> Optional[torch.Tensor]:
+    """Scratch for nsa_paged_mla calls of this shape (None if they need none)."""
+    n = nsa_paged_mla_workspace_bytes(q_dtype, kv_dtype, R, rows_per_req, H, max_row_len, d_latent, d_rope)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def nsa_paged_mla(q_dtype: int, kv_dtype: int, q_nope: torch.Tensor, q_rope: torch.Tensor, kv: torch.Tensor,
+                  page_size: int, page_table: torch.Tensor, row_len: torch.Tensor, rows_per_req: int, max_row_len: int,
+                  sm_scale: float, out: torch.Tensor, lse: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q_nope [R, H, d_latent] and q_rope [R, H, d_rope] (any row / head strides); kv [slots, row];
+    page_table int32 [R / rows_per_req, pages]; row_len int32 [R]; out [R, H, d_latent] (q's type) and
+    lse float32 [R, H].  workspace: alloc_paged_mla_workspace's, for this shape or a larger one."""
+    R, H, dl = q_nope.shape
+    dr = q_rope.shape[2]
+    if rows_per_req < 1 or R % rows_per_req:
+        raise ValueError(f"{R} rows are no whole requests of {rows_per_req}")
+    pages = _paged_cache(kv_dtype, kv, page_size, dl, dr)
+    pt = _table(page_table, R // rows_per_req)
+    if tuple(out.shape) != (R, H, dl) or tuple(lse.shape) != (R, H) or lse.dtype != torch.float32 or \
+            out.dtype != q_nope.dtype or not out.is_contiguous() or not lse.is_contiguous():
+        raise ValueError("out must be [R, H, d_latent] in q's type and lse float32 [R, H], both contiguous")
+    _on_current_device(q_nope, q_rope, kv, page_table, row_len, out, lse, workspace, status)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = load().nsa_paged_mla(q_dtype, kv_dtype, *_paged_q(q_dtype, q_nope, q_rope), _ptr(kv), pages, page_size, _ptr(pt),
+                              _table_ld(pt, max_row_len, page_size), _ptr(_i32("row_len", row_len, R)), R, rows_per_req,
+                              H, dl, dr, max_row_len, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+                              _ptr(status), _stream(stream))
+    _check("nsa_paged_mla", rc)
+
+
+# ---------------------------------------------------------------- eviction
+
+def nsa_mla_key_weights(q_dtype: int, kv_dtype: int, q_nope: torch.Tensor, q_rope: torch.Tensor, kv: torch.Tensor,
+                        page_size: int, page_table: torch.Tensor, row_len: torch.Tensor, rows_per_req: int,
+                        max_row_len: int, sm_scale: float, lse: torch.Tensor, total: torch.Tensor,
+                        status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Adds to total (float32 [requests, positions]) the attention weight each cached position got
+    from its request's rows; the other arguments as nsa_paged_mla's, lse as that call wrote it."""
+    R, H, dl = q_nope.shape
+    dr = q_rope.shape[2]
+    if rows_per_req < 1 or R % rows_per_req:
+        raise ValueError(f"{R} rows are no whole requests of {rows_per_req}")
+    B = R // rows_per_req
+    pages = _paged_cache(kv_dtype, kv, page_size, dl, dr)
+    pt = _table(page_table, B)
+    if tuple(lse.shape) != (R, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [R, H]")
+    total_ld = _total_ld(total, B, max_row_len)
+    _on_current_device(q_nope, q_rope, kv, page_table, row_len, lse, total, status)
+    rc = load().nsa_mla_key_weights(q_dtype, kv_dtype, *_paged_q(q_dtype, q_nope, q_rope), _ptr(kv), pages, page_size,
+                                    _ptr(pt), _table_ld(pt, max_row_len, page_size), _ptr(_i32("row_len", row_len, R)), R,
+                                    rows_per_req, H, dl, dr, max_row_len, float(sm_scale), _ptr(lse), _ptr(total),
+                                    total_ld, _ptr(status), _stream(stream))
+    _check("nsa_mla_key_weights", rc)
+
+
+def _total_ld(total: torch.Tensor, B: int, max_len: int) -> int:
+    if total.dtype != torch.float32 or total.dim() != 2 or total.shape[0] != B or total.shape[1] < max_len:
+        raise ValueError(f"total must be float32 [{B}, >= {max_len}], got shape {tuple(total.shape)} of {total.dtype}")
+    return _ld(total)
+
+
+def nsa_evict_select(total: torch.Tensor, lens: torch.Tensor, max_len: int, sinks: int, recent: int, budget: int,
+                     keep: torch.Tensor, new_len: torch.Tensor, status: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """keep int32 [B, >= budget]: the kept positions of each request, ascending, then -1; new_len int32 [B]."""
+    B = lens.shape[0]
+    if keep.dtype != torch.int32 or keep.dim() != 2 or keep.shape[0] != B or keep.shape[1] < budget:
+        raise ValueError(f"keep must be int32 [{B}, >= {budget}], got shape {tuple(keep.shape)} of {keep.dtype}")
+    total_ld = _total_ld(total, B, max_len)
+    _on_current_device(total, lens, keep, new_len, status)
+    rc = load().nsa_evict_select(_ptr(total), total_ld, _ptr(_i32("lens", lens, B)), B, max_len, sinks, recent, budget,
+                                 _ptr(keep), _ld(keep), _ptr(_i32("new_len", new_len, B)), _ptr(status), _stream(stream))
+    _check("nsa_evict_select", rc)
+
+
+def nsa_evict_compact_workspace_bytes(B: int, max_len: int) -> int:
+    return int(load().nsa_evict_compact_workspace_bytes(B, max_len))
+
+
+def alloc_evict_workspace(B: int, max_len: int, device="cuda") -> torch.Tensor:
+    """Scratch for nsa_evict_compact calls of at most B requests and max_len positions."""
+    return torch.empty(max(16, nsa_evict_compact_workspace_bytes(B, max_len)), dtype=torch.uint8, device=device)
+
+
+def nsa_evict_compact(keep: torch.Tensor, new_len: torch.Tensor, old_len: torch.Tensor, max_len: int,
+                      page_table: torch.Tensor, page_size: int, arrays, total: Optional[torch.Tensor],
+                      workspace: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Moves, in place, position keep[b, i] of every paged array to position i, and total likewise.
+    arrays: contiguous tensors whose first dimension is the slot (a cache kept as [pages, page_size, ...]
+    is passed as a view(-1, ...) of it); workspace: alloc_evict_workspace's."""
+    B = old_len.shape[0]
+    if keep.dtype != torch.int32 or keep.dim() != 2 or keep.shape[0] != B:
+        raise ValueError(f"keep must be int32 [{B}, budget], got shape {tuple(keep.shape)} of {keep.dtype}")
+    pt = _table(page_table, B)
+    slots = arrays[0].shape[0] if len(arrays) else pt.shape[1] * page_size
+    for a in arrays:
+        if not a.is_contiguous() or a.shape[0] != slots or slots % page_size:
+            raise ValueError(f"the arrays must be contiguous with one first dimension of whole pages of {page_size}, "
+                             f"got shape {tuple(a.shape)}")
+    total_ld = 0 if total is None else _total_ld(total, B, max_len)
+    _on_current_device(keep, new_len, old_len, page_table, total, workspace, status, *arrays)
+    n = len(arrays)
+    ptrs = (C.c_void_p * max(1, n))(*[a.data_ptr() for a in arrays])
+    nb = (C.c_int64 * max(1, n))(*[a.numel() * a.element_size() // slots for a in arrays])
+    rc = load().nsa_evict_compact(B, _ptr(keep), _ld(keep), keep.shape[1], _ptr(_i32("new_len", new_len, B)),
+                                  _ptr(_i32("old_len", old_len, B)), max_len, _ptr(pt), _table_ld(pt, max_len, page_size),
+                                  page_size, slots // page_size, n, ptrs, nb, _ptr(total), total_ld, _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    _check("nsa_evict_compact", rc)

@@ -7,6 +7,9 @@
  *   nsa_indexer_logits  lightning-indexer scores  sum_h w * ReLU(q . k)
  *   nsa_topk_transform  per-row top-k of the scores, mapped to KV slots
  *   nsa_sparse_mla      MLA attention over only the selected KV rows
+ *   nsa_paged_mla       MLA attention over the whole paged cache, and the eviction
+ *                       of its least attended positions (nsa_mla_key_weights,
+ *                       nsa_evict_select, nsa_evict_compact)
  *
  * Sources, cited by page title and the function shown on the page:
  *   [NSA-diff] "sglang 0.5.3rc2 -> 0.5.4 diff: sglang/srt/layers/attention/nsa_backend.py"
@@ -531,6 +534,137 @@ nsa_status nsa_local_attention(const void *q_dev, int64_t q_ld, const void *k_ca
                                const int32_t *cu_seqlens_q_dev, const int32_t *seqused_k_dev, int nvb,
                                int total_q, int Hq, int Hkv, int D, float sm_scale, void *out_dev,
                                float *lse_dev, int32_t *status_dev, nsa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A whole paged latent cache: dense attention, and eviction by the attention
+ * weight its positions have received.
+ *
+ * nsa_paged_mla is the dense counterpart of nsa_sparse_mla (rows whose context
+ * is no longer than the top-k, models without an indexer): it reads the same
+ * cache rows through the request's page table instead of an index list.
+ * nsa_mla_key_weights, nsa_evict_select and nsa_evict_compact keep a request
+ * inside a budget of positions: the weights of a step are added to a running
+ * total per position, the positions to keep are chosen from the totals, and
+ * the kept rows of every paged array move to the front of the request's pages.
+ * The pages have no counterpart of these calls.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Attention of each request's newest token(s) over its whole paged cache.
+ * Row r belongs to request b = r / rows_per_req (decode: rows_per_req 1;
+ * target-verify: n_draft, with nsa_metadata's seqlens_expanded as row_len) and
+ * sees the positions s < row_len[r], kept at slot
+ * page_table[b, s / page_size] * page_size + s % page_size.  Per head h:
+ *   x_s      = sm_scale * (q_nope[r,h] . K_s[0:d_latent] + q_rope[r,h] . K_s[d_latent:])
+ *   lse[r,h] = ln sum_s exp(x_s)         (natural log; -inf if the row sees no key)
+ *   out[r,h] = sum_s exp(x_s - lse) K_s[0:d_latent]   (0 if the row sees no key)
+ *
+ *   q_dtype, kv_dtype  as nsa_sparse_mla (F32 q takes F32 rows; BF16 q takes BF16 or
+ *                      E4M3 rows); `out` has q's dtype.  An E4M3 row stands for the
+ *                      values nsa_dequantize_kv_paged gives (code x scale rounded to
+ *                      fp32, then to bf16), so attending a quantised cache equals
+ *                      attending its dequantised copy
+ *   q_nope_dev, q_rope_dev  [R, H, d_latent] and [R, H, d_rope] with element strides
+ *                      (ld_r, ld_h, 1), as nsa_sparse_mla
+ *   kv_dev             [num_pages, page_size, row] in the row layouts of nsa_sparse_mla
+ *   page_table_dev     [R / rows_per_req, pt_ld] page ids (nsa_metadata's
+ *                      real_page_table); entries past a request's last page are not read
+ *   row_len_dev        [R]; 0 is a row of a padded batch
+ *   max_row_len        host-known upper bound of row_len; pt_ld >= ceil(max_row_len / page_size)
+ *   out_dev            [R, H, d_latent] contiguous; lse_dev [R, H] float32
+ *   workspace_dev      scratch of nsa_paged_mla_workspace_bytes(...) bytes, 16-byte aligned
+ *                      (may be NULL if that is 0).  Calls that may overlap on the GPU need
+ *                      workspaces of their own; nothing in it needs to start at zero and
+ *                      nothing is kept in it between calls
+ * Positions at or past row_len are never used, whatever they hold, as long as no
+ * other row of the same request sees them: a NaN or infinity at a position that
+ * some row of the request does see reaches all rows of that request.
+ * Returns NSA_ERR_INVALID_ARG for R not a multiple of rows_per_req, a bad size, a
+ * NULL or misaligned buffer, or too small a workspace; NSA_ERR_UNSUPPORTED for a
+ * dtype combination or size the kernels do not take (more than 2^30 positions or
+ * 2^31 slots, d_latent beyond 8192, E4M3 with d_latent % 128 != 0 or odd d_rope).
+ * Device errors (NSA_ERR_BOUNDS): a row_len outside [0, max_row_len] makes its row
+ * see no key; the positions of a page outside [0, num_pages) are left out.
+ */
+nsa_status nsa_paged_mla(nsa_dtype q_dtype, nsa_dtype kv_dtype, const void *q_nope_dev, int64_t nope_ld_r,
+                         int64_t nope_ld_h, const void *q_rope_dev, int64_t rope_ld_r, int64_t rope_ld_h,
+                         const void *kv_dev, int64_t num_pages, int page_size, const int32_t *page_table_dev,
+                         int64_t pt_ld, const int32_t *row_len_dev, int R, int rows_per_req, int H, int d_latent,
+                         int d_rope, int max_row_len, float sm_scale, void *out_dev, float *lse_dev,
+                         void *workspace_dev, size_t workspace_bytes, int32_t *status_dev, nsa_stream_t stream);
+
+/* Scratch bytes nsa_paged_mla needs on the current device for this problem (0 if
+ * none, and for arguments the call would refuse).  A workspace serves every call
+ * that needs no more than its size. */
+size_t nsa_paged_mla_workspace_bytes(nsa_dtype q_dtype, nsa_dtype kv_dtype, int R, int rows_per_req, int H,
+                                     int d_latent, int d_rope, int max_row_len);
+
+/*
+ * The attention weight each cached position received from its request's rows,
+ * added to a running total:
+ *   total[b, s] += sum_{rows r of b with s < row_len[r]} sum_h exp(x_{r,h,s} - lse[r,h])
+ * with x as in nsa_paged_mla and lse [R, H] as that call wrote it (a row whose
+ * lse is -inf gives no weight).  total_dev is [R / rows_per_req, total_ld] float32
+ * with total_ld >= max_row_len; positions that no row sees keep their totals.
+ * The sums run in a fixed order: equal inputs give equal bits.  Other arguments,
+ * refusals and device errors as nsa_paged_mla (no workspace).
+ */
+nsa_status nsa_mla_key_weights(nsa_dtype q_dtype, nsa_dtype kv_dtype, const void *q_nope_dev, int64_t nope_ld_r,
+                               int64_t nope_ld_h, const void *q_rope_dev, int64_t rope_ld_r, int64_t rope_ld_h,
+                               const void *kv_dev, int64_t num_pages, int page_size, const int32_t *page_table_dev,
+                               int64_t pt_ld, const int32_t *row_len_dev, int R, int rows_per_req, int H,
+                               int d_latent, int d_rope, int max_row_len, float sm_scale, const float *lse_dev,
+                               float *total_dev, int64_t total_ld, int32_t *status_dev, nsa_stream_t stream);
+
+/*
+ * The positions each request keeps.  A request of L = len[b] <= budget positions
+ * keeps them all; a longer one keeps its first `sinks`, its last `recent` and, of
+ * those between, the budget - sinks - recent with the largest total[b, s] (equal
+ * totals prefer the lower position; -0 equals +0; NaN ranks lowest).
+ *   total_dev  [B, total_ld] float32, total_ld >= max_len (only s < len[b] is read)
+ *   len_dev    [B]; max_len: host-known upper bound (at most 2^30)
+ *   keep_dev   [B, keep_ld] int32, keep_ld >= budget: the kept positions in ascending
+ *              order, then -1 up to `budget`; new_len_dev [B]: min(len, budget)
+ * sinks + recent <= budget, else NSA_ERR_INVALID_ARG.  Device error: a len outside
+ * [0, max_len] sets NSA_ERR_BOUNDS and is treated as 0.
+ */
+nsa_status nsa_evict_select(const float *total_dev, int64_t total_ld, const int32_t *len_dev, int B, int max_len,
+                            int sinks, int recent, int budget, int32_t *keep_dev, int64_t keep_ld,
+                            int32_t *new_len_dev, int32_t *status_dev, nsa_stream_t stream);
+
+/*
+ * Moves the kept positions of each request to the front of its pages, in place:
+ * for every array and i < new_len[b], the row at position i becomes the row that
+ * was at position keep[b, i]; total[b, i] becomes total[b, keep[b, i]], and
+ * total[b, s] becomes 0 for new_len[b] <= s < old_len[b].  Rows past new_len keep
+ * their bytes.  Attention does not depend on the order of the cache and the rope
+ * part is in the rows, so the request goes on with new_len positions and its
+ * first ceil(new_len / page_size) pages.
+ *   keep_dev        [B, keep_ld] int32, new_len_dev [B], old_len_dev [B]: of
+ *                   nsa_evict_select (any strictly ascending positions below old_len);
+ *                   `budget` (<= keep_ld) bounds new_len
+ *   page_table_dev  [B, pt_ld] page ids, pt_ld >= ceil(max_len / page_size).  No page
+ *                   may belong to two requests of the call
+ *   arrays_dev      host array of n_arrays (at most 8) device pointers, each to
+ *                   [num_pages * page_size] rows of row_bytes[i] bytes (the KV cache, the
+ *                   indexer's keys, their scales, ...), not overlapping
+ *   total_dev       [B, total_ld] float32 or NULL
+ *   workspace_dev   nsa_evict_compact_workspace_bytes(B, max_len) bytes, 16-byte aligned;
+ *                   the call clears what it uses.  Calls that may overlap on the GPU need
+ *                   workspaces of their own
+ * NSA_ERR_UNSUPPORTED when the rows of one position take more than 24 KB.  Device
+ * errors (NSA_ERR_BOUNDS): lengths out of range (the request is left as it is), a
+ * keep list that does not ascend within old_len or a page outside the cache (that
+ * row stays); NSA_ERR_TIMEOUT if a bounded wait between blocks runs out (the
+ * request's rows are then partly moved).
+ */
+nsa_status nsa_evict_compact(int B, const int32_t *keep_dev, int64_t keep_ld, int budget, const int32_t *new_len_dev,
+                             const int32_t *old_len_dev, int max_len, const int32_t *page_table_dev, int64_t pt_ld,
+                             int page_size, int64_t num_pages, int n_arrays, void *const *arrays_dev,
+                             const int64_t *row_bytes, float *total_dev, int64_t total_ld, void *workspace_dev,
+                             size_t workspace_bytes, int32_t *status_dev, nsa_stream_t stream);
+
+size_t nsa_evict_compact_workspace_bytes(int B, int max_len);
 
 #ifdef __cplusplus
 }
