@@ -9,8 +9,9 @@
 // bytes a key and pass, written and read) cost about what reading the key
 // again does.
 //
-// This file holds the entry point and the CUDA-core kernel for any dims.
-#include "paged_mla.cuh"
+// This file holds the entry point and the CUDA-core kernel for any dims; the
+// tensor-core kernel of the 512 + 64 shape is in mla_key_weights_tc.cu.
+#include "mla_key_weights_tc.cuh"
 
 namespace nsa {
 namespace {
@@ -113,6 +114,8 @@ extern "C" nsa_status nsa_mla_key_weights(nsa_dtype q_dtype, nsa_dtype kv_dtype,
     if (!lse_dev || !total_dev || (((uintptr_t)lse_dev | (uintptr_t)total_dev) & 3) || total_ld < max_row_len)
         return NSA_ERR_INVALID_ARG;
     const cudaStream_t s = (cudaStream_t)stream;
+    const nsa_status st = key_weights_tc_try_launch(a, lse_dev, total_dev, total_ld, s);
+    if (st != NSA_ERR_UNSUPPORTED) return st;
     if (q_dtype == NSA_DT_F32) return launch_simt<NSA_DT_F32, NSA_DT_F32>(a, lse_dev, total_dev, total_ld, s);
     if (kv_dtype == NSA_DT_BF16) return launch_simt<NSA_DT_BF16, NSA_DT_BF16>(a, lse_dev, total_dev, total_ld, s);
     return launch_simt<NSA_DT_BF16, NSA_DT_E4M3>(a, lse_dev, total_dev, total_ld, s);

@@ -1,0 +1,384 @@
+// Tensor-core kernel of nsa_mla_key_weights for the 512 + 64 latent cache.
+//
+//   total[b, s] += sum_c 2^(x_{c,s} - lse2_c),   x = scale * log2(e) * (q_c . K_s)
+//
+// over the columns c = (row, head) of request b.  S[128 keys, N columns] =
+// K_tile . Q^T accumulates in TMEM (tcgen05, bf16, fp32 accumulate), keys in the
+// lanes: one epilogue thread owns one key and sums its columns in registers, so
+// the sum over heads needs no exchange and runs in a fixed order.
+//
+// Each cache row is read once per pass over up to 128 columns, which is once for
+// one row of 128 heads: 1152 (fp8: 656) bytes against 147 kflop a key, so the
+// kernel is bound by HBM where one pass suffices.  More columns (verify) take several
+// passes, made over four tiles at a time so that the tiles come from L2 after the
+// first pass.
+//
+// One CTA per SM, persistent; the tiles of all requests are cut into equal shares.
+// Roles: warp 0 issues TMA loads of Q and (bf16) of the tiles' blocks into a ring of
+// 16 KB stages; warp 1 issues the MMAs into two TMEM buffers; warps 4..7 are the
+// epilogue; with fp8 rows warps 8..23 expand them into the ring instead of TMA.
+#include <cstddef>
+
+#include "mla_key_weights_tc.cuh"
+#include "paged_tc.cuh"
+
+namespace nsa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kCols = 128;       // columns of one pass
+constexpr int kMaxStages = 12;   // ring stages: as many as shared memory holds beside Q
+constexpr int kPassTiles = 4;    // tiles per round of passes, when there are several
+constexpr uint32_t kTmemCols = 256;
+
+struct WShared {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t q_full, q_empty, s_full[2], s_empty[2];
+    float lse2[kCols];   // lse in log2 units; +inf: no weight (padding, an empty row)
+    int len[kCols];      // positions the column's row sees
+    int min_len[4];
+    TileShare share;
+    uint32_t tmem_base;
+    volatile int abort;
+};
+constexpr size_t kAux = (sizeof(WShared) + 15) / 16 * 16;
+
+struct WParams {
+    PagedTc t;
+    const float *lse;
+    float *total;
+    int64_t total_ld;
+    int cols, passes, N, stages;  // columns per request, passes, MMA columns of a pass, ring stages
+};
+
+// The tiles of a share as (request, pass, tile range) pieces, the same for every role.
+struct Walk {
+    int b, t0, t1, c0, c1, pass, tiles, len;
+    int64_t left;  // tiles of the share from c0 on
+
+    __device__ __forceinline__ bool start(const WParams &p, const TileShare &s)
+    {
+        left = s.g1 - s.g0;
+        if (left <= 0) return false;
+        b = s.b;
+        t0 = (int)s.off;
+        enter(p);
+        return true;
+    }
+    __device__ __forceinline__ void enter(const WParams &p)
+    {
+        len = request_len(p.t, b);
+        tiles = tiles_of(len);
+        t1 = (int)min((int64_t)tiles, t0 + left);
+        c0 = t0;
+        c1 = p.passes == 1 ? t1 : min(t1, c0 + kPassTiles);
+        pass = 0;
+    }
+    __device__ __forceinline__ bool next(const WParams &p)
+    {
+        if (++pass < p.passes) return true;
+        pass = 0;
+        left -= c1 - c0;
+        if (left <= 0) return false;
+        if (c1 < t1) {
+            c0 = c1;
+            c1 = min(t1, c0 + kPassTiles);
+            return true;
+        }
+        do {
+            ++b;
+            t0 = 0;
+            enter(p);
+        } while (tiles == 0 && b + 1 < p.t.B);
+        return tiles > 0;
+    }
+};
+
+template <bool FP8>
+__global__ void __launch_bounds__(FP8 ? 256 + kDqThreads : 256, 1)
+key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
+                      const __grid_constant__ CUtensorMap kv_map)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *q_s = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t q_blk = (uint32_t)p.N * 128;
+    uint8_t *ring = q_s + 9 * q_blk;
+    WShared *sm = (WShared *)(ring + (size_t)p.stages * kPtBlk);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nst = p.stages;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < nst; ++i) {
+            mbar_init(&sm->full[i], FP8 ? kDqThreads / 32 : 1);
+            mbar_init(&sm->empty[i], 1);
+        }
+        mbar_init(&sm->q_full, 1);
+        mbar_init(&sm->q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->s_full[i], 1);
+            mbar_init(&sm->s_empty[i], 128);
+        }
+        sm->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm->tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    if (blockIdx.x == 0) report_lengths(p.t);
+    tc_fence_before();
+    find_share(p.t, 1, blockIdx.x, gridDim.x, &sm->share);  // ends with a block barrier
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem_base;
+    auto fail = [&]() {
+        sm->abort = 1;
+        set_status(p.t.status, NSA_ERR_TIMEOUT);
+    };
+    Walk w;
+    const bool work = w.start(p, sm->share);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA
+        if (work) {
+            const int boxes = kPtTok / p.t.box_rows;  // at most 16, one a lane
+            const uint32_t box_bytes = (uint32_t)p.t.box_rows * 128;
+            int st = 0, uses = 0;
+            uint32_t ph = 0;
+            auto stop = [&]() { return __any_sync(0xffffffffu, sm->abort) != 0; };  // one answer for the warp
+            for (bool more = true; more && !stop(); more = w.next(p)) {
+                if (lane == 0) {
+                    if (uses > 0 && !mbar_wait(&sm->q_empty, (uses - 1) & 1, kPtWait)) fail();
+                    mbar_arrive_expect_tx(&sm->q_full, 9 * q_blk);
+                    const int row = w.b * p.cols + w.pass * kCols;
+                    for (int c = 0; c < 8; ++c) tma_load_2d(q_s + c * q_blk, &qn_map, 64 * c, row, &sm->q_full);
+                    tma_load_2d(q_s + 8 * q_blk, &qr_map, 0, row, &sm->q_full);
+                }
+                ++uses;
+                if (!FP8) {
+                    const int32_t *pt = p.t.page_table + (int64_t)w.b * p.t.pt_ld;
+                    for (int t = w.c0; t < w.c1; ++t) {
+                        const int pos = t * kPtTok + lane * p.t.box_rows;
+                        const int page = lane < boxes ? checked_page(p.t, pt, pos, w.len) : -1;
+                        const int y = page < 0 ? 0 : (int)((int64_t)page * p.t.ps + pos % p.t.ps);
+                        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box_bytes;
+                        int c = 0;
+                        for (; c < 9; ++c) {
+                            if (lane == 0 && !mbar_wait(&sm->empty[st], ph ^ 1, kPtWait)) fail();
+                            if (stop()) break;
+                            if (lane == 0) mbar_arrive_expect_tx(&sm->full[st], bytes);
+                            __syncwarp();
+                            if (page >= 0)
+                                tma_load_2d(ring + st * kPtBlk + lane * box_bytes, &kv_map, 64 * c, y, &sm->full[st]);
+                            if (++st == nst) {
+                                st = 0;
+                                ph ^= 1;
+                            }
+                        }
+                        if (c < 9) break;
+                    }
+                }
+            }
+            // nothing is in flight at the end: stages before st were filled last with phase ph, the others before
+            if (lane == 0) {
+                if (!FP8)
+                    for (int i = 0; i < nst; ++i) mbar_wait(&sm->full[i], i < st ? ph : ph ^ 1, kPtWait);
+                mbar_wait(&sm->q_full, (uses - 1) & 1, kPtWait);
+            }
+            __syncwarp();
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        if (work && lane == 0) {
+            const uint32_t idesc = instr_desc(1, 1, 0, 0, kPtTok, (uint32_t)p.N);
+            const uint32_t q_addr = smem_u32(q_s), r_addr = smem_u32(ring);
+            int st = 0, uses = 0;
+            uint32_t ph = 0, tile = 0;
+            bool more = true;
+            while (more && !sm->abort) {
+                if (!mbar_wait(&sm->q_full, uses & 1, kPtWait)) { fail(); break; }
+                ++uses;
+                for (int t = w.c0; t < w.c1 && !sm->abort; ++t, ++tile) {
+                    const uint32_t buf = tile & 1, bph = (tile >> 1) & 1;
+                    if (!mbar_wait(&sm->s_empty[buf], bph ^ 1, kPtWait)) { fail(); break; }
+                    tc_fence_after();
+                    for (int c = 0; c < 9; ++c) {
+                        if (!mbar_wait(&sm->full[st], ph, kPtWait)) { fail(); break; }
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16(tmem + buf * kCols, smem_desc(r_addr + st * kPtBlk + k * 32, 16, 1024, kSwizzle128B),
+                                    smem_desc(q_addr + c * q_blk + k * 32, 16, 1024, kSwizzle128B), idesc, (c | k) != 0);
+                        mma_commit(&sm->empty[st]);
+                        if (++st == nst) {
+                            st = 0;
+                            ph ^= 1;
+                        }
+                    }
+                    mma_commit(&sm->s_full[buf]);
+                }
+                mma_commit(&sm->q_empty);
+                more = w.next(p);
+            }
+            // the last commit tracks every MMA before it: nothing is in flight at the end
+            mbar_wait(&sm->q_empty, (uses - 1) & 1, kPtWait);
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 8) {
+        // ------------------------------------------------------------ epilogue: one key a thread
+        if (work) {
+            const int key = threadIdx.x - 128;
+            const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+            uint32_t tile = 0;
+            bool more = true;
+            while (more) {
+                bar_sync(1, 128);  // the previous piece's columns are read out
+                {
+                    const int c = w.pass * kCols + key;
+                    float l2 = INFINITY;
+                    int len = 0x7fffffff;
+                    if (c < p.cols) {
+                        const int64_t r = (int64_t)w.b * p.t.n + c / p.t.H;
+                        const float l = p.lse[r * p.t.H + c % p.t.H];
+                        if (l != -INFINITY) l2 = l * 1.4426950408889634f;
+                        const int L = p.t.row_len[r];
+                        len = L >= 0 && L <= p.t.max_row_len ? L : 0;
+                    }
+                    sm->lse2[key] = l2;
+                    sm->len[key] = len;
+                    const int mn = __reduce_min_sync(0xffffffffu, len);
+                    if (lane == 0) sm->min_len[warp & 3] = mn;
+                }
+                bar_sync(1, 128);
+                const int min_len = min(min(sm->min_len[0], sm->min_len[1]), min(sm->min_len[2], sm->min_len[3]));
+                const int32_t *pt = p.t.page_table + (int64_t)w.b * p.t.pt_ld;
+                float *total = p.total + (int64_t)w.b * p.total_ld;
+                for (int t = w.c0; t < w.c1; ++t, ++tile) {
+                    const uint32_t buf = tile & 1, bph = (tile >> 1) & 1;
+                    const int pos = t * kPtTok + key;
+                    const bool valid = checked_page(p.t, pt, pos, w.len) >= 0;
+                    const float old = valid ? total[pos] : 0.f;
+                    const bool ok = mbar_wait(&sm->s_full[buf], bph, kPtWait);
+                    if (!ok) fail();
+                    if (bar_red_or(2, 128, !ok || sm->abort)) { more = false; break; }
+                    tc_fence_after();
+                    const bool whole = (t + 1) * kPtTok <= min_len;  // every column sees the whole tile
+                    float sum = 0.f;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < p.N; c0 += 32) {
+                        uint32_t s[32];
+                        tmem_ld32(lanes + buf * kCols + c0, s);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float l2 = sm->lse2[c0 + j];
+                            const float e = exp2f(fmaf(__uint_as_float(s[j]), p.t.scale_log2, -l2));
+                            // a column without weight may hold anything: selected away, not multiplied
+                            if (l2 != INFINITY && (whole || pos < sm->len[c0 + j])) sum += e;
+                        }
+                    }
+                    tc_fence_before();
+                    mbar_arrive(&sm->s_empty[buf]);
+                    if (valid) total[pos] = old + sum;
+                }
+                if (more) more = w.next(p);
+            }
+        }
+    } else if (FP8 && warp >= 8) {
+        // ------------------------------------------------------------ fp8 rows into the ring
+        if (work) {
+            const int d = threadIdx.x - 256;
+            Fp8Rows x;
+            int st = 0;
+            uint32_t ph = 0;
+            x.set_rows(p.t, d, w.b, w.c0, w.len);
+            x.load<0>(p.t, d); x.load<1>(p.t, d); x.load<2>(p.t, d); x.load<3>(p.t, d); x.load<4>(p.t, d);
+            bool more = true;
+            int t = w.c0;
+            auto slot = [&]() -> uint8_t * {
+                if (!mbar_wait(&sm->empty[st], ph ^ 1, kPtWait)) fail();
+                return ring + st * kPtBlk;
+            };
+            auto release = [&]() {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->full[st]);
+                if (++st == nst) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            };
+            // the step's one or two stages, then its registers for the next tile
+            auto peek2 = [&]() -> uint8_t * {
+                const int s2 = st + 1 == nst ? 0 : st + 1;
+                const uint32_t p2 = st + 1 == nst ? ph ^ 1 : ph;
+                if (!mbar_wait(&sm->empty[s2], p2 ^ 1, kPtWait)) fail();
+                return ring + s2 * kPtBlk;
+            };
+            while (more) {
+                if (++t >= w.c1) {
+                    more = w.next(p);
+                    t = w.c0;
+                }
+                if (more)
+                    x.set_rows(p.t, d, w.b, t, w.len);
+                else
+                    x.no_rows();
+                uint8_t *a = slot(), *b2 = peek2();
+                x.store<0>(d, a, b2); x.load<0>(p.t, d); release(); release();
+                a = slot(); b2 = peek2();
+                x.store<1>(d, a, b2); x.load<1>(p.t, d); release(); release();
+                a = slot(); b2 = peek2();
+                x.store<2>(d, a, b2); x.load<2>(p.t, d); release(); release();
+                a = slot(); b2 = peek2();
+                x.store<3>(d, a, b2); x.load<3>(p.t, d); release(); release();
+                a = slot();
+                x.store<4>(d, a, nullptr); x.load<4>(p.t, d); release();
+                if (sm->abort) break;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+}  // namespace
+
+nsa_status key_weights_tc_try_launch(const PagedMlaArgs &a, const float *lse, float *total, int64_t total_ld,
+                                     cudaStream_t stream)
+{
+    if (!paged_tc_applicable(a)) return NSA_ERR_UNSUPPORTED;
+    const bool fp8 = a.kv_dtype == NSA_DT_E4M3;
+    const int sms = current_sm_count();
+    if (sms <= 0) return NSA_ERR_CUDA;
+    WParams p;
+    p.t = paged_tc_params(a);
+    p.lse = lse;
+    p.total = total;
+    p.total_ld = total_ld;
+    p.cols = a.rows_per_req * a.H;
+    p.passes = (int)ceil_div(p.cols, kCols);
+    p.N = p.passes > 1 ? kCols : (int)ceil_div(p.cols, 16) * 16;
+    const size_t q_bytes = (size_t)9 * p.N * 128, most = 232448 - 1024 - kAux - q_bytes;
+    p.stages = (int)(most / kPtBlk) < kMaxStages ? (int)(most / kPtBlk) : kMaxStages;
+    const size_t smem = 1024 + q_bytes + (size_t)p.stages * kPtBlk + kAux;
+    CUtensorMap qn, qr, kv = {};
+    if (!paged_tc_maps(a, p.t, (uint32_t)p.N, &qn, &qr, &kv)) return NSA_ERR_CUDA;
+    const int64_t tiles = (int64_t)p.t.B * ceil_div(a.max_row_len, kPtTok);
+    const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
+    if (fp8) {
+        NSA_CUDA_TRY(cudaFuncSetAttribute(key_weights_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448));
+        key_weights_tc_kernel<true><<<grid, 256 + kDqThreads, smem, stream>>>(p, qn, qr, kv);
+    } else {
+        NSA_CUDA_TRY(cudaFuncSetAttribute(key_weights_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448));
+        key_weights_tc_kernel<false><<<grid, 256, smem, stream>>>(p, qn, qr, kv);
+    }
+    return launch_status();
+}
+
+}  // namespace nsa

@@ -1,0 +1,257 @@
+// Pieces that the tensor-core kernels over a paged latent cache share
+// (paged_mla_tc.cu, mla_key_weights_tc.cu): how the tiles of all requests are
+// cut into equal shares, and how a tile of 128 cache rows reaches shared memory.
+//
+// A tile is 128 consecutive positions of one request as nine K-major blocks of
+// 128 rows x 64 bf16 (16 KB, 128-byte swizzle): blocks 0..7 the latent, block 8
+// the rope part.  bf16 rows come by TMA in boxes of box_rows rows x 64 columns
+// that never cross a page; fp8 rows are loaded into registers a whole tile
+// ahead, expanded to bf16 and stored by kDqThreads threads.
+#pragma once
+
+#include "paged_mla.cuh"
+#include "sm100.cuh"
+#include "tma_host.h"
+
+namespace nsa {
+
+constexpr int kPtTok = 128;                     // positions per tile
+constexpr int kPtDl = 512, kPtDr = 64;
+constexpr uint32_t kPtBlk = kPtTok * 128;       // bytes of a block
+constexpr int kPtFp8Row = kPtDl + 16 + 2 * kPtDr;  // 656
+constexpr long long kPtWait = 2000000000LL;     // ~1 s of SM clocks
+constexpr int kDqThreads = 512;                 // fp8: threads that expand rows
+
+struct PagedTc {
+    const uint8_t *kv;
+    int64_t num_pages;
+    int ps, box_rows;
+    const int32_t *page_table;
+    int64_t pt_ld;
+    const int32_t *row_len;
+    int B, n, H, max_row_len;  // n rows per request
+    float scale_log2;
+    int32_t *status;
+};
+
+// The longest row of request b (0 for lengths out of range).
+__device__ __forceinline__ int request_len(const PagedTc &p, int b)
+{
+    int len = 0;
+    for (int i = 0; i < p.n; ++i) {
+        const int L = p.row_len[(int64_t)b * p.n + i];
+        if (L >= 0 && L <= p.max_row_len) len = max(len, L);
+    }
+    return len;
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kPtTok - 1) / kPtTok; }
+
+// Reports row lengths out of range (one CTA does it for the launch).
+__device__ __forceinline__ void report_lengths(const PagedTc &p)
+{
+    for (int64_t r = threadIdx.x; r < (int64_t)p.B * p.n; r += blockDim.x) {
+        const int L = p.row_len[r];
+        if (L < 0 || L > p.max_row_len) set_status(p.status, NSA_ERR_BOUNDS);
+    }
+}
+
+// Where a share of the launch's tiles starts.  The tiles of all requests (each
+// counted `mult` times) in request order are cut into `parts` equal shares;
+// share `part` is [g0, g1) and its first tile is tile `off` of request `b`.
+struct TileShare {
+    int64_t warp[32];
+    int64_t total, g0, g1, off;
+    int b;
+};
+
+__device__ __forceinline__ void find_share(const PagedTc &p, int mult, int part, int parts, TileShare *sh)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    int64_t sum = 0;
+    for (int b = tid; b < p.B; b += blockDim.x) sum += (int64_t)tiles_of(request_len(p, b)) * mult;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sh->warp[warp] = sum;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < nw; ++w) total += sh->warp[w];
+    const int64_t g0 = total * part / parts, g1 = total * (part + 1) / parts;
+    if (tid == 0) {
+        sh->total = total;
+        sh->g0 = g0;
+        sh->g1 = g1;
+        sh->b = p.B;
+        sh->off = 0;
+    }
+    int64_t before = 0;  // tiles of the requests below `base`
+    for (int base = 0; base < p.B && g0 < g1; base += blockDim.x) {
+        __syncthreads();  // warp[] is free
+        const int b = base + tid;
+        const int64_t v = b < p.B ? (int64_t)tiles_of(request_len(p, b)) * mult : 0;
+        int64_t inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        if (lane == 31) sh->warp[warp] = inc;
+        __syncthreads();
+        int64_t lo = before, all = 0;
+        for (int w = 0; w < nw; ++w) {
+            if (w < warp) lo += sh->warp[w];
+            all += sh->warp[w];
+        }
+        lo += inc - v;
+        if (v > 0 && g0 >= lo && g0 < lo + v) {
+            sh->b = b;
+            sh->off = g0 - lo;
+        }
+        before += all;
+        if (before > g0) break;  // uniform
+    }
+    __syncthreads();
+}
+
+// Page of position `pos` if the position is below `len` and its page exists, else -1.
+__device__ __forceinline__ int checked_page(const PagedTc &p, const int32_t *pt, int pos, int len)
+{
+    if (pos >= len) return -1;
+    const int page = __ldg(pt + pos / p.ps);
+    if (page >= 0 && page < p.num_pages) return page;
+    set_status(p.status, NSA_ERR_BOUNDS);
+    return -1;
+}
+
+// ------------------------------------------------------------------ fp8 rows
+//
+// Thread d of kDqThreads owns rows d / 8 and d / 8 + 64 and chunk d % 8 of each
+// step of a tile: step m < 4 is 128 latent codes (16 a thread and row; blocks
+// 2m, 2m + 1), step 4 the rope part (8 values; block 8).  A step is stored from
+// registers and its registers are loaded with the same step of the next tile at
+// once, so a whole tile (84 KB) is in flight per SM, which covers the latency
+// of HBM at its share of the bandwidth.
+struct Fp8Rows {
+    uint4 w[5][2];
+    float sc[4][2];
+    int slot[2];  // the rows that loads refer to; -1: a row of zeros
+
+    __device__ __forceinline__ void set_rows(const PagedTc &p, int d, int b, int tile, int len)
+    {
+        const int32_t *pt = p.page_table + (int64_t)b * p.pt_ld;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int pos = tile * kPtTok + (d >> 3) + 64 * u;
+            const int page = checked_page(p, pt, pos, len);
+            slot[u] = page < 0 ? -1 : page * p.ps + pos % p.ps;
+        }
+    }
+    __device__ __forceinline__ void no_rows() { slot[0] = slot[1] = -1; }
+
+    template <int M>
+    __device__ __forceinline__ void load(const PagedTc &p, int d)
+    {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            w[M][u] = make_uint4(0u, 0u, 0u, 0u);
+            if (M < 4) sc[M & 3][u] = 0.f;
+            if (slot[u] >= 0) {
+                const uint8_t *row = p.kv + (int64_t)slot[u] * kPtFp8Row;
+                w[M][u] = __ldg(reinterpret_cast<const uint4 *>(row + (M < 4 ? 128 * M : kPtDl + 16) + 16 * (d & 7)));
+                if (M < 4) sc[M & 3][u] = __ldg(reinterpret_cast<const float *>(row + kPtDl + 4 * M));
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void expand8(uint32_t a, uint32_t b, float s, uint4 &out)
+    {
+        const uint32_t in[2] = {a, b};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2_raw h =
+                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((in[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            // code x scale rounded to fp32, then to bf16: the row's value by definition
+            const __nv_bfloat162 v = __floats2bfloat162_rn(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
+            o[i] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        out = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+
+    // Step M into its blocks (blk1 unused for the rope step).  Codes 16k .. 16k+15 of
+    // a step become chunks 2k, 2k+1 of its 16; lanes with k >= 4 store the odd chunk
+    // first, so that eight neighbouring lanes store to eight distinct bank groups.
+    template <int M>
+    __device__ __forceinline__ void store(int d, uint8_t *blk0, uint8_t *blk1) const
+    {
+        const int k = d & 7;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = (d >> 3) + 64 * u;
+            if (M == 4) {
+                *reinterpret_cast<uint4 *>(blk0 + sm100::sw128_offset(r, k)) = w[4][u];
+            } else {
+                uint4 lo, hi;
+                expand8(w[M][u].x, w[M][u].y, sc[M & 3][u], lo);
+                expand8(w[M][u].z, w[M][u].w, sc[M & 3][u], hi);
+                uint8_t *blk = k < 4 ? blk0 : blk1;
+                const int c0 = (2 * k) & 7;
+                *reinterpret_cast<uint4 *>(blk + sm100::sw128_offset(r, k < 4 ? c0 : c0 + 1)) = k < 4 ? lo : hi;
+                *reinterpret_cast<uint4 *>(blk + sm100::sw128_offset(r, k < 4 ? c0 + 1 : c0)) = k < 4 ? hi : lo;
+            }
+        }
+    }
+};
+
+// ------------------------------------------------------------------ host
+
+// Whether the tensor-core kernels take this problem: the 512 + 64 shape with bf16
+// queries, whole boxes of 8 rows in a page, 16-byte aligned buffers and query rows
+// that follow one another at one pitch (contiguous, or the two parts of a
+// concatenated [R, H, 576] query).
+inline bool paged_tc_applicable(const PagedMlaArgs &a)
+{
+    return a.q_dtype == NSA_DT_BF16 && (a.kv_dtype == NSA_DT_BF16 || a.kv_dtype == NSA_DT_E4M3) &&
+           a.d_latent == kPtDl && a.d_rope == kPtDr && a.page_size % 8 == 0 && a.max_row_len > 0 &&
+           (((uintptr_t)a.q_nope | (uintptr_t)a.q_rope | (uintptr_t)a.kv) & 15) == 0 && a.nope_ld_h % 8 == 0 &&
+           a.rope_ld_h % 8 == 0 && a.nope_ld_h >= kPtDl && a.rope_ld_h >= kPtDr &&
+           (a.R == 1 || (a.nope_ld_r == a.H * a.nope_ld_h && a.rope_ld_r == a.H * a.rope_ld_h));
+}
+
+inline PagedTc paged_tc_params(const PagedMlaArgs &a)
+{
+    PagedTc p;
+    p.kv = (const uint8_t *)a.kv;
+    p.num_pages = a.num_pages;
+    p.ps = a.page_size;
+    p.box_rows = kPtTok;
+    while (a.page_size % p.box_rows != 0) p.box_rows /= 2;
+    p.page_table = a.page_table;
+    p.pt_ld = a.pt_ld;
+    p.row_len = a.row_len;
+    p.B = a.R / a.rows_per_req;
+    p.n = a.rows_per_req;
+    p.H = a.H;
+    p.max_row_len = a.max_row_len;
+    p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+    p.status = a.status;
+    return p;
+}
+
+// Maps of the query parts (boxes of 64 columns x `rows` rows over the R * H query
+// heads) and of a bf16 cache (boxes of 64 columns x box_rows rows).
+inline bool paged_tc_maps(const PagedMlaArgs &a, const PagedTc &p, uint32_t rows, CUtensorMap *qn, CUtensorMap *qr,
+                          CUtensorMap *kv)
+{
+    const uint64_t heads = (uint64_t)a.R * a.H;
+    return make_tma_2d(qn, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q_nope, kPtDl, heads, (uint64_t)a.nope_ld_h * 2, 64, rows,
+                       CU_TENSOR_MAP_SWIZZLE_128B) &&
+           make_tma_2d(qr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q_rope, kPtDr, heads, (uint64_t)a.rope_ld_h * 2, 64, rows,
+                       CU_TENSOR_MAP_SWIZZLE_128B) &&
+           (a.kv_dtype != NSA_DT_BF16 ||
+            make_tma_2d(kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, kPtDl + kPtDr, (uint64_t)a.num_pages * a.page_size,
+                        2 * (kPtDl + kPtDr), 64, (uint32_t)p.box_rows, CU_TENSOR_MAP_SWIZZLE_128B));
+}
+
+}  // namespace nsa
