@@ -334,7 +334,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                 x.store<3>(d, a, b2); x.load<3>(p.t, d); release(); release();
                 a = slot();
                 x.store<4>(d, a, nullptr); x.load<4>(p.t, d); release();
-                if (sm->abort) break;
+                if (__any_sync(0xffffffffu, sm->abort)) break;
             }
         }
     }

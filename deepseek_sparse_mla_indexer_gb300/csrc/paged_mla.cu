@@ -9,8 +9,10 @@
 //   lse = ln sum_s exp(x_s)        out = sum_s exp(x_s - lse) K_s[0:d_latent]
 //
 // This file holds the entry points and the CUDA-core kernel for any dims, any
-// page size and fp32.
+// page size and fp32; the tensor-core kernel of the 512 + 64 shape is in
+// paged_mla_tc.cu.
 #include "paged_mla.cuh"
+#include "paged_mla_tc.cuh"
 
 namespace nsa {
 namespace {
@@ -141,8 +143,7 @@ nsa_status launch_simt(const PagedMlaArgs &a, void *out, float *lse, cudaStream_
 extern "C" size_t nsa_paged_mla_workspace_bytes(nsa_dtype q_dtype, nsa_dtype kv_dtype, int R, int rows_per_req, int H,
                                                 int d_latent, int d_rope, int max_row_len)
 {
-    (void)q_dtype, (void)kv_dtype, (void)R, (void)rows_per_req, (void)H, (void)d_latent, (void)d_rope, (void)max_row_len;
-    return 0;
+    return nsa::paged_mla_tc_workspace_bytes(q_dtype, kv_dtype, R, rows_per_req, H, d_latent, d_rope, max_row_len);
 }
 
 extern "C" nsa_status nsa_paged_mla(nsa_dtype q_dtype, nsa_dtype kv_dtype, const void *q_nope_dev, int64_t nope_ld_r,
@@ -166,6 +167,8 @@ extern "C" nsa_status nsa_paged_mla(nsa_dtype q_dtype, nsa_dtype kv_dtype, const
     if (need > 0 && (workspace_bytes < need || !workspace_dev || ((uintptr_t)workspace_dev & 15)))
         return NSA_ERR_INVALID_ARG;
     const cudaStream_t s = (cudaStream_t)stream;
+    const nsa_status st = paged_mla_tc_try_launch(a, out_dev, lse_dev, workspace_dev, s);
+    if (st != NSA_ERR_UNSUPPORTED) return st;
     if (q_dtype == NSA_DT_F32) return launch_simt<NSA_DT_F32, NSA_DT_F32>(a, out_dev, lse_dev, s);
     if (kv_dtype == NSA_DT_BF16) return launch_simt<NSA_DT_BF16, NSA_DT_BF16>(a, out_dev, lse_dev, s);
     return launch_simt<NSA_DT_BF16, NSA_DT_E4M3>(a, out_dev, lse_dev, s);

@@ -1,0 +1,709 @@
+// Tensor-core kernel of nsa_paged_mla for the 512 + 64 latent cache.
+//
+// A column is one (row, head) of a request; a CTA owns 64 columns.  Per tile of
+// 128 positions, as the sparse kernel does for its gathered rows:
+//   S^T[128 keys, 64 cols] = K_tile . Q^T                       (tcgen05, bf16)
+//   P^T = 2^(scale S^T - m), m a lazily refreshed running maximum per column
+//   O^T[512, 64 cols] += V^T . P^T, V the first eight blocks of the same tile
+// with O^T and S^T in TMEM (256 + 64 columns).  The sums of the unrounded P stay in
+// fp32 registers (each thread its key's part) and are joined once at the end, so
+// lse is good to fp32; P itself is rounded to bf16 for the product with V, whose
+// operands must have one type (each weight off by at most 2^-8 of itself).
+//
+// Shared memory holds Q (72 KB) and one tile (144 KB), so tiles are pipelined by
+// block pairs: pair m is loaded again as soon as O^T's d-block m, its last reader,
+// is done, and S^T of the next tile starts on the pairs that have landed.  P^T lies
+// in the rope block, which S^T has finished with.  Two CTAs with neighbouring
+// columns of the same request run as a cluster: each loads half of every tile into
+// both (TMA multicast), which halves the traffic from L2; a pair is loaded again
+// when both are done with it.  fp8 rows are expanded into the tile by 512 threads
+// of each CTA from registers that hold the whole next tile.
+//
+// The tiles of all requests are cut into equal shares over the CTAs (teams of up to
+// eight CTAs take the same tiles for different columns, so that a tile is read from
+// HBM once).  A share that covers a request's columns only in part leaves raw sums,
+// maxima and fp32 accumulators in the workspace, which paged_mla_join_kernel joins.
+#include <cstddef>
+
+#include "paged_mla_tc.cuh"
+#include "paged_tc.cuh"
+
+namespace nsa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kCols = 64;                 // columns per CTA
+constexpr uint32_t kQBlk = kCols * 128;   // 8 KB
+constexpr uint32_t kQBytes = 9 * kQBlk, kKvBytes = 9 * kPtBlk;
+constexpr int kGrp = 32;                  // columns per softmax group
+constexpr uint32_t kColS = 256;           // S^T behind O^T's four blocks of 64 columns
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescale = 8.0f;          // log2 units
+constexpr int kMaxTeam = 8;
+constexpr int kThreadsBf16 = 384, kThreadsFp8 = 384 + kDqThreads;
+// fp8: registers per thread at launch and per role: 7 warpgroups x 72 = 40 + 2 x 104 + 4 x 64
+constexpr int kRegsLaunch = 72, kRegsCtl = 40, kRegsSoftmax = 104, kRegsRows = 64;
+static_assert(kRegsCtl + 2 * kRegsSoftmax + 4 * kRegsRows <= 7 * kRegsLaunch, "the split fits what the block has");
+
+struct AShared {
+    alignas(16) float m_run[kCols];   // running maximum, log2 units
+    alignas(16) float alpha[kCols];
+    float red[4][kCols];
+    float l_col[kCols];
+    int len[kCols];                   // positions the column's row sees
+    int min_len[2];
+    uint64_t pair_full[5];            // block pair m of the tile landed (m = 4: the rope block)
+    uint64_t pair_free[5];            // its readers are done (m = 4: every product of the tile)
+    uint64_t q_full, q_empty, s_full, p_full, o_fin;
+    TileShare share;
+    uint32_t tmem_base;
+    volatile int abort;
+};
+constexpr size_t kSmem = 1024 + kQBytes + kKvBytes + sizeof(AShared);
+static_assert(kSmem <= 232448, "shared memory per CTA");
+
+struct AParams {
+    PagedTc t;
+    int cols, groups, team, mult;  // columns per request, groups of 64, CTAs per team, groups / team
+    int teams;
+    int slot_cols;                 // columns of a partial slot
+    __nv_bfloat16 *out;
+    float *lse;
+    int64_t *head;                 // [B + 1] tiles of the requests before b
+    float *part;                   // [2 * CTAs][slot_cols][512] raw accumulators
+    float2 *part_ml;               // [2 * CTAs][slot_cols] maximum (log2 units) and sum
+};
+
+// The pieces of a share: tiles [t0, t1) of group set j of request b.
+struct Seg {
+    int b, j, t0, t1, tiles, len;
+    int64_t left;
+
+    __device__ __forceinline__ bool start(const AParams &p, const TileShare &s)
+    {
+        left = s.g1 - s.g0;
+        if (left <= 0) return false;
+        b = s.b;
+        len = request_len(p.t, b);
+        tiles = tiles_of(len);
+        j = (int)(s.off / tiles);
+        t0 = (int)(s.off - (int64_t)j * tiles);
+        t1 = (int)min((int64_t)tiles, t0 + left);
+        return true;
+    }
+    __device__ __forceinline__ bool next(const AParams &p)
+    {
+        left -= t1 - t0;
+        if (left <= 0) return false;
+        t0 = 0;
+        if (++j == p.mult) {
+            j = 0;
+            do {
+                ++b;
+                len = request_len(p.t, b);
+                tiles = tiles_of(len);
+            } while (tiles == 0 && b + 1 < p.t.B);
+        }
+        t1 = (int)min((int64_t)tiles, left);
+        return tiles > 0;
+    }
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <bool FP8, bool PAIR>
+__global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreadsBf16, 1)
+paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
+                    const __grid_constant__ CUtensorMap kv_map)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *q_s = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *kv_s = q_s + kQBytes;
+    uint8_t *p_s = kv_s + 8 * kPtBlk;  // P^T in the rope block
+    AShared *sm = (AShared *)(kv_s + kKvBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int team = blockIdx.x / p.team, rank = blockIdx.x - team * p.team;  // rank: column group in the set
+    const int peer = PAIR ? (int)cluster_ctarank() : 0;
+
+    if (threadIdx.x == 0) {
+        for (int m = 0; m < 5; ++m) {
+            mbar_init(&sm->pair_full[m], FP8 ? kDqThreads / 32 : 1);
+            mbar_init(&sm->pair_free[m], PAIR ? 2 : 1);
+        }
+        mbar_init(&sm->q_full, 1);
+        mbar_init(&sm->q_empty, 1);
+        mbar_init(&sm->s_full, 1);
+        mbar_init(&sm->p_full, 256);
+        mbar_init(&sm->o_fin, 1);
+        sm->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm->tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    if (blockIdx.x == 0) report_lengths(p.t);
+    tc_fence_before();
+    find_share(p.t, p.mult, team, p.teams, &sm->share);  // ends with a block barrier
+    if (PAIR) cluster_sync_all();  // the peer's barriers are ready before anything reaches them
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem_base;
+    auto fail = [&]() {
+        sm->abort = 1;
+        set_status(p.t.status, NSA_ERR_TIMEOUT);
+    };
+    Seg s;
+    const bool work = s.start(p, sm->share);
+
+    if (warp < 4) {
+        if (FP8) regs_down<kRegsCtl>();
+        if (warp == 0 && work) {
+            // -------------------------------------------------------- TMA
+            const int boxes = kPtTok / p.t.box_rows;  // at most 16, one a lane
+            const uint32_t box_bytes = (uint32_t)p.t.box_rows * 128;
+            auto stop = [&]() { return __any_sync(0xffffffffu, sm->abort) != 0; };
+            // a pair's boxes are shared out by halves of the tile
+            const bool mine = lane < boxes && (!PAIR || (lane >= boxes / 2) == (peer == 1));
+            uint32_t i = 0, seg = 0;
+            for (bool more = true; more && !stop(); more = s.next(p), ++seg) {
+                if (lane == 0) {
+                    if (seg > 0 && !mbar_wait(&sm->q_empty, (seg - 1) & 1, kPtWait)) fail();
+                    mbar_arrive_expect_tx(&sm->q_full, kQBytes);
+                    const int row = s.b * p.cols + (s.j * p.team + rank) * kCols;
+                    for (int c = 0; c < 8; ++c) tma_load_2d(q_s + c * kQBlk, &qn_map, 64 * c, row, &sm->q_full);
+                    tma_load_2d(q_s + 8 * kQBlk, &qr_map, 0, row, &sm->q_full);
+                }
+                if (FP8) continue;
+                const int32_t *pt = p.t.page_table + (int64_t)s.b * p.t.pt_ld;
+                // row of this lane's box of tile t, or -1
+                auto box_row = [&](int t) -> int {
+                    const int pos = t * kPtTok + lane * p.t.box_rows;
+                    const int page = lane < boxes && t < s.t1 ? checked_page(p.t, pt, pos, s.len) : -1;
+                    return page < 0 ? -1 : page * p.t.ps + pos % p.t.ps;
+                };
+                int y = box_row(s.t0), y1 = box_row(s.t0 + 1);
+                bool stopped = false;
+                for (int t = s.t0; t < s.t1 && !stopped; ++t, ++i) {
+                    const uint32_t blk_bytes = __popc(__ballot_sync(0xffffffffu, y >= 0)) * box_bytes;
+                    for (int m = 0; m < 5; ++m) {
+                        if (lane == 0 && !mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) fail();
+                        if (stop()) {
+                            stopped = true;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&sm->pair_full[m], (m < 4 ? 2 : 1) * blk_bytes);
+                        __syncwarp();
+                        if (mine && y >= 0) {
+                            for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c) {
+                                uint8_t *dst = kv_s + c * kPtBlk + lane * box_bytes;
+                                if (PAIR)
+                                    tma_load_2d_multicast(dst, &kv_map, 64 * c, y, &sm->pair_full[m], 3);
+                                else
+                                    tma_load_2d(dst, &kv_map, 64 * c, y, &sm->pair_full[m]);
+                            }
+                        }
+                    }
+                    // the tile after the next one into L2 while this one is worked on
+                    const int y2 = box_row(t + 2);
+                    if (mine && y2 >= 0)
+                        prefetch_l2_bulk(p.t.kv + (int64_t)y2 * (2 * (kPtDl + kPtDr)),
+                                         (uint32_t)p.t.box_rows * (2 * (kPtDl + kPtDr)));
+                    y = y1;
+                    y1 = y2;
+                }
+            }
+            if (lane == 0) {  // nothing is in flight at the end
+                if (!FP8 && i > 0)
+                    for (int m = 0; m < 5; ++m) {
+                        mbar_wait(&sm->pair_full[m], (i - 1) & 1, kPtWait);
+                        mbar_wait(&sm->pair_free[m], (i - 1) & 1, kPtWait);  // the peer's arrivals too
+                    }
+                if (seg > 0) mbar_wait(&sm->q_full, (seg - 1) & 1, kPtWait);
+            }
+            __syncwarp();
+        } else if (warp == 1 && work) {
+            // -------------------------------------------------------- MMA
+            if (lane == 0) {
+                const uint32_t idesc_s = instr_desc(1, 1, 0, 0, kPtTok, kCols);  // K-major A and B
+                const uint32_t idesc_o = instr_desc(1, 1, 1, 1, 128, kCols);     // MN-major A and B
+                const uint32_t q_addr = smem_u32(q_s), kv_addr = smem_u32(kv_s), p_addr = smem_u32(p_s);
+                auto free_pair = [&](int m) {
+                    if (PAIR)
+                        mma_commit_multicast(&sm->pair_free[m], 3);
+                    else
+                        mma_commit(&sm->pair_free[m]);
+                };
+                uint32_t i = 0, seg = 0;
+                bool ok = true;
+                for (bool more = true; more && ok; more = s.next(p), ++seg) {
+                    if (!mbar_wait(&sm->q_full, seg & 1, kPtWait)) ok = false;
+                    for (int t = s.t0; t < s.t1 && ok && !sm->abort; ++t, ++i) {
+#pragma unroll 1
+                        for (int m = 0; m < 5; ++m) {
+                            if (!mbar_wait(&sm->pair_full[m], i & 1, kPtWait)) { ok = false; break; }
+                            tc_fence_after();
+                            for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_f16(tmem + kColS, smem_desc(kv_addr + c * kPtBlk + k * 32, 16, 1024, kSwizzle128B),
+                                            smem_desc(q_addr + c * kQBlk + k * 32, 16, 1024, kSwizzle128B), idesc_s,
+                                            (c | k) != 0);
+                            }
+                        }
+                        if (!ok) break;
+                        mma_commit(&sm->s_full);
+                        if (t + 1 == s.t1) mma_commit(&sm->q_empty);
+                        if (!mbar_wait(&sm->p_full, i & 1, kPtWait)) { ok = false; break; }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                            for (int k = 0; k < kPtTok / 16; ++k)
+                                mma_f16(tmem + m * kCols,
+                                        smem_desc(kv_addr + 2 * m * kPtBlk + k * 2048, kPtBlk, 1024, kSwizzle128B),
+                                        smem_desc(p_addr + k * 2048, kPtBlk, 1024, kSwizzle128B), idesc_o,
+                                        (t > s.t0 || k > 0) ? 1u : 0u);
+                            free_pair(m);
+                        }
+                        free_pair(4);
+                        if (t + 1 == s.t1) mma_commit(&sm->o_fin);
+                    }
+                    if (sm->abort) ok = false;
+                }
+                if (!ok) {
+                    fail();
+                    // whatever was issued is done before shared memory and TMEM are given up
+                    mma_commit(&sm->o_fin);
+                    for (int w = 0; w < 2; ++w) mbar_wait(&sm->o_fin, w, kPtWait / 100);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 2 && blockIdx.x == 0) {
+            // -------------------------------------------------------- where each request's tiles start, for the join
+            int64_t before = 0;
+            for (int base = 0; base < p.t.B; base += 32) {
+                const int b = base + lane;
+                const int64_t v = b < p.t.B ? (int64_t)tiles_of(request_len(p.t, b)) : 0;
+                int64_t inc = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += x;
+                }
+                if (b < p.t.B) p.head[b] = before + inc - v;
+                before += __shfl_sync(0xffffffffu, inc, 31);
+            }
+            if (lane == 0) p.head[p.t.B] = before;
+        } else if (warp == 3) {
+            // -------------------------------------------------------- requests without a key
+            for (int b = blockIdx.x; b < p.t.B; b += gridDim.x) {
+                if (request_len(p.t, b) > 0) continue;
+                const int64_t row0 = (int64_t)b * p.cols;
+                uint4 *o = reinterpret_cast<uint4 *>(p.out + row0 * kPtDl);
+                if (((uintptr_t)p.out & 15) == 0)
+                    for (int64_t e = lane; e < (int64_t)p.cols * (kPtDl / 8); e += 32) o[e] = make_uint4(0u, 0u, 0u, 0u);
+                else
+                    for (int64_t e = lane; e < (int64_t)p.cols * kPtDl; e += 32) p.out[row0 * kPtDl + e] = __float2bfloat16_rn(0.f);
+                for (int c = lane; c < p.cols; c += 32) p.lse[row0 + c] = -INFINITY;
+            }
+        }
+    } else if (warp < 12) {
+        if (FP8) regs_up<kRegsSoftmax>();
+        if (work) {
+            // -------------------------------------------------------- softmax: one key a thread, 32 columns a group
+            const int grp = (warp - 4) >> 2, quad = warp & 3, cb = grp * kGrp, bar = 1 + grp;
+            const int key = quad * 32 + lane, et = (threadIdx.x - 128) & 127;
+            const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+            const float4 *m4 = reinterpret_cast<const float4 *>(sm->m_run + cb);
+            uint32_t i = 0, seg = 0;
+            bool ok = true;
+            for (bool more = true; more && ok; more = s.next(p), ++seg) {
+                const int col0 = (s.j * p.team + rank) * kCols;  // first column of this CTA in the request
+                if (et < kGrp) {
+                    const int c = col0 + cb + et;
+                    int len = 0x7fffffff;  // padding: never masked, never written
+                    if (c < p.cols) {
+                        const int L = p.t.row_len[(int64_t)s.b * p.t.n + c / p.t.H];
+                        len = L >= 0 && L <= p.t.max_row_len ? L : 0;
+                    }
+                    sm->len[cb + et] = len;
+                    sm->m_run[cb + et] = -INFINITY;
+                    const int mn = __reduce_min_sync(0xffffffffu, len);  // et < 32: one whole warp
+                    if (lane == 0) sm->min_len[grp] = mn;
+                }
+                bar_sync(bar, 128);
+                const int min_len = sm->min_len[grp];
+                const int32_t *pt = p.t.page_table + (int64_t)s.b * p.t.pt_ld;
+                float l[kGrp];
+#pragma unroll
+                for (int c = 0; c < kGrp; ++c) l[c] = 0.f;
+                for (int t = s.t0; t < s.t1; ++t, ++i) {
+                    const int pos = t * kPtTok + key;
+                    const bool valid = checked_page(p.t, pt, pos, s.len) >= 0;
+                    ok = mbar_wait(&sm->s_full, i & 1, kPtWait);
+                    if (!ok) fail();
+                    if (bar_red_or(bar, 128, !ok || sm->abort)) { ok = false; break; }
+                    tc_fence_after();
+                    uint32_t sa[kGrp];
+                    tmem_ld32(lanes + kColS + cb, sa);
+                    tmem_ld_wait();
+                    float x[kGrp];
+                    if ((t + 1) * kPtTok <= min_len && __all_sync(0xffffffffu, valid)) {
+#pragma unroll
+                        for (int c = 0; c < kGrp; ++c) x[c] = __uint_as_float(sa[c]) * p.t.scale_log2;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kGrp; ++c)
+                            x[c] = valid && pos < sm->len[cb + c] ? __uint_as_float(sa[c]) * p.t.scale_log2 : -INFINITY;
+                    }
+                    bool exceed = false;
+#pragma unroll
+                    for (int c = 0; c < kGrp / 4; ++c) {
+                        const float4 m = m4[c];
+                        exceed |= x[4 * c] > m.x + kRescale || x[4 * c + 1] > m.y + kRescale ||
+                                  x[4 * c + 2] > m.z + kRescale || x[4 * c + 3] > m.w + kRescale;
+                    }
+                    if (bar_red_or(bar, 128, exceed)) {
+                        // new maxima from this tile; sums and accumulators so far are rescaled
+#pragma unroll
+                        for (int c = 0; c < kGrp; ++c) {
+                            float v = x[c];
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                            if (lane == 0) sm->red[quad][cb + c] = v;
+                        }
+                        bar_sync(bar, 128);
+                        if (et < kGrp) {
+                            const int c = cb + et;
+                            const float cm = fmaxf(fmaxf(sm->red[0][c], sm->red[1][c]), fmaxf(sm->red[2][c], sm->red[3][c]));
+                            const float mo = sm->m_run[c], mn = fmaxf(mo, cm);
+                            sm->alpha[c] = mn == -INFINITY ? 1.f : exp2f(mo - mn);
+                            sm->m_run[c] = mn;
+                        }
+                        bar_sync(bar, 128);
+                        if (t > s.t0) {
+                            // S^T of this tile is done, and with it the products of the tile before
+#pragma unroll 1
+                            for (int m = 0; m < 4; ++m) {
+                                uint32_t v[kGrp];
+                                tmem_ld32(lanes + m * kCols + cb, v);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int c = 0; c < kGrp; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * sm->alpha[cb + c]);
+                                tmem_st32(lanes + m * kCols + cb, v);
+                            }
+                            tmem_st_wait();
+#pragma unroll
+                            for (int c = 0; c < kGrp; ++c) l[c] *= sm->alpha[cb + c];
+                        }
+                    }
+#pragma unroll
+                    for (int c8 = 0; c8 < kGrp / 8; ++c8) {
+                        const float4 ma = m4[2 * c8], mb = m4[2 * c8 + 1];
+                        const float mv[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int c = 8 * c8 + 2 * k;
+                            const float p0 = x[c] == -INFINITY ? 0.f : exp2f(x[c] - mv[2 * k]);
+                            const float p1 = x[c + 1] == -INFINITY ? 0.f : exp2f(x[c + 1] - mv[2 * k + 1]);
+                            l[c] += p0;
+                            l[c + 1] += p1;
+                            pk[k] = pack2(p0, p1);
+                        }
+                        *reinterpret_cast<uint4 *>(p_s + sw128_offset(key, cb / 8 + c8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                    if (!FP8 && !valid) {
+                        // what lies behind the length may be NaN, which a weight of 0 would not hide: this
+                        // group's half of the key's latent blocks becomes 0 (S^T has read them)
+                        for (int m = 0; m < 4; ++m) mbar_wait(&sm->pair_full[m], i & 1, kPtWait);
+#pragma unroll 1
+                        for (int c = 4 * grp; c < 4 * grp + 4; ++c) {
+                            uint4 *r = reinterpret_cast<uint4 *>(kv_s + c * kPtBlk + key * 128);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) r[k] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    mbar_arrive(&sm->p_full);
+                }
+                if (!ok) break;
+                // ---------------------------------------------------- the piece's sums and accumulators
+                // column sums over the lanes: after the exchange lane c holds column c
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const bool up = (lane & o) != 0;
+#pragma unroll
+                    for (int c = 0; c < o; ++c) {
+                        const float give = up ? l[c] : l[c + o];
+                        const float got = __shfl_xor_sync(0xffffffffu, give, o);
+                        l[c] = (up ? l[c + o] : l[c]) + got;
+                    }
+                }
+                sm->red[quad][cb + lane] = l[0];
+                bar_sync(bar, 128);
+                const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+                const int nc = min(kGrp, p.cols - col0 - cb);  // real columns of this group (may be <= 0)
+                const int64_t row0 = (int64_t)s.b * p.cols + col0 + cb;
+                const int64_t slot = (int64_t)blockIdx.x * 2 + (seg > 0 ? 1 : 0);
+                if (et < kGrp) {
+                    const int c = cb + et;
+                    const float sum = (sm->red[0][c] + sm->red[1][c]) + (sm->red[2][c] + sm->red[3][c]);
+                    sm->l_col[c] = sum;
+                    if (et < nc) {
+                        if (whole)
+                            p.lse[row0 + et] = sum > 0.f ? (sm->m_run[c] + log2f(sum)) * 0.69314718055994531f
+                                                         : (sum == sum ? -INFINITY : sum);
+                        else
+                            p.part_ml[slot * p.slot_cols + c] = make_float2(sm->m_run[c], sum);
+                    }
+                }
+                bar_sync(bar, 128);
+                if (!mbar_wait(&sm->o_fin, seg & 1, kPtWait)) {
+                    fail();
+                    ok = false;
+                }
+                if (bar_red_or(bar, 128, !ok)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll 1
+                for (int m = 0; m < 4; ++m) {
+                    uint32_t v[kGrp];
+                    tmem_ld32(lanes + m * kCols + cb, v);
+                    tmem_ld_wait();
+                    if (whole) {
+                        __nv_bfloat16 *o = p.out + row0 * kPtDl + m * 128 + key;
+#pragma unroll
+                        for (int c = 0; c < kGrp; ++c) {
+                            const float sum = sm->l_col[cb + c];
+                            const float r = sum > 0.f ? __uint_as_float(v[c]) / sum : (sum == sum ? 0.f : sum);
+                            if (c < nc) o[(int64_t)c * kPtDl] = __float2bfloat16_rn(r);
+                        }
+                    } else {
+                        float *o = p.part + (slot * p.slot_cols + cb) * kPtDl + m * 128 + key;
+#pragma unroll
+                        for (int c = 0; c < kGrp; ++c)
+                            if (c < nc) o[(int64_t)c * kPtDl] = __uint_as_float(v[c]);
+                    }
+                }
+                tc_fence_before();
+            }
+        }
+    } else if constexpr (FP8) {
+        regs_down<kRegsRows>();
+        if (work) {
+            // -------------------------------------------------------- fp8 rows into the tile
+            const int d = threadIdx.x - 384;
+            Fp8Rows x;
+            x.set_rows(p.t, d, s.b, s.t0, s.len);
+            x.load<0>(p.t, d); x.load<1>(p.t, d); x.load<2>(p.t, d); x.load<3>(p.t, d); x.load<4>(p.t, d);
+            uint32_t i = 0;
+            int t = s.t0;
+            auto wait_free = [&](int m) {
+                if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) fail();
+            };
+            auto release = [&](int m) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->pair_full[m]);
+            };
+            for (bool more = true; more; ++i) {
+                if (++t >= s.t1) {
+                    more = s.next(p);
+                    t = s.t0;
+                }
+                if (more)
+                    x.set_rows(p.t, d, s.b, t, s.len);
+                else
+                    x.no_rows();
+                wait_free(0);
+                x.store<0>(d, kv_s, kv_s + kPtBlk); x.load<0>(p.t, d); release(0);
+                wait_free(1);
+                x.store<1>(d, kv_s + 2 * kPtBlk, kv_s + 3 * kPtBlk); x.load<1>(p.t, d); release(1);
+                wait_free(2);
+                x.store<2>(d, kv_s + 4 * kPtBlk, kv_s + 5 * kPtBlk); x.load<2>(p.t, d); release(2);
+                wait_free(3);
+                x.store<3>(d, kv_s + 6 * kPtBlk, kv_s + 7 * kPtBlk); x.load<3>(p.t, d); release(3);
+                wait_free(4);
+                x.store<4>(d, kv_s + 8 * kPtBlk, nullptr); x.load<4>(p.t, d); release(4);
+                if (__any_sync(0xffffffffu, sm->abort)) break;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    if (PAIR) cluster_sync_all();  // the peer's copies and arrivals into this CTA are over
+}
+
+// Columns that several shares worked on: with M the largest maximum,
+//   l = sum_q l_q 2^(m_q - M), out = sum_q O_q 2^(m_q - M) / l, lse = (M + log2 l) ln 2,
+// in share order.  One CTA per column, four quarters of the shares at a time.
+constexpr int kJoinThreads = 512;
+
+__global__ void __launch_bounds__(kJoinThreads) paged_mla_join_kernel(AParams p)
+{
+    __shared__ float4 acc_s[3][128];
+    __shared__ float wl[kJoinThreads / 32], wm[kJoinThreads / 32];
+    const int64_t row = blockIdx.x;
+    const int b = (int)(row / p.cols), c = (int)(row - (int64_t)b * p.cols);
+    const int64_t before = p.head[b], tiles = p.head[b + 1] - before, total = p.head[p.t.B] * p.mult;
+    if (tiles == 0) return;
+    const int group = c / kCols, set = group / p.team, rank = group - set * p.team, cc = c - group * kCols;
+    const int64_t u0 = before * p.mult + set * tiles, u1 = u0 + tiles;  // the unit's tiles among all
+    const int64_t np = share_count(total, p.teams);  // share k is [total * k / np, total * (k + 1) / np)
+    auto share_of = [&](int64_t g) -> int {
+        int k = (int)(g * np / total);
+        while (k + 1 < np && total * (k + 1) / np <= g) ++k;
+        while (k > 0 && total * k / np > g) --k;
+        return k;
+    };
+    const int k0 = share_of(u0), k1 = share_of(u1 - 1);
+    if (k0 == k1) return;  // one share had it whole
+    auto slot_of = [&](int k) -> int64_t {
+        const int64_t g0 = total * k / np;
+        const int64_t slot = ((int64_t)k * p.team + rank) * 2 + (g0 >= u0 ? 0 : 1);  // its first piece, or its last
+        return slot * p.slot_cols + cc;
+    };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ns = k1 - k0 + 1;
+    float m = -INFINITY;
+    for (int q = tid; q < ns; q += kJoinThreads) m = fmaxf(m, p.part_ml[slot_of(k0 + q)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) wm[warp] = m;
+    __syncthreads();
+    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, wm[w]);
+    const int part = tid >> 7, d4 = tid & 127;
+    const int per = (ns + 3) / 4, q0 = min(ns, part * per), q1 = min(ns, q0 + per);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int q = q0; q < q1; ++q) {
+        const int64_t s = slot_of(k0 + q);
+        const float2 ml = p.part_ml[s];
+        const float4 v = *reinterpret_cast<const float4 *>(p.part + s * kPtDl + 4 * d4);
+        // a share whose keys were all masked has maximum -inf and zeros
+        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+        l += w * ml.y;
+        acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+    }
+    if (d4 == 0) wl[part] = l;
+    if (part > 0) acc_s[part - 1][d4] = acc;
+    __syncthreads();
+    if (part == 0) {
+        l = ((wl[0] + wl[1]) + wl[2]) + wl[3];
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            const float4 v = acc_s[x][d4];
+            acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+        }
+        const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+        __nv_bfloat16 *o = p.out + row * kPtDl + 4 * d4;
+        const float r[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[x] = __float2bfloat16_rn(r[x]);
+        if (d4 == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == l ? -INFINITY : l);
+    }
+}
+
+// How the columns of a request are spread over CTAs: teams of the largest power of two
+// up to kMaxTeam that divides the number of 64-column groups, as many as the SMs hold and
+// the tiles fill.
+struct Plan {
+    int cols, groups, team, mult, teams, slot_cols;
+    size_t head_bytes, ml_bytes, part_bytes;
+};
+
+Plan make_plan(int R, int n, int H, int max_row_len, int sms)
+{
+    Plan q;
+    q.cols = n * H;
+    q.groups = (int)ceil_div(q.cols, kCols);
+    q.team = 1;
+    while (q.team < kMaxTeam && q.groups % (2 * q.team) == 0) q.team *= 2;
+    q.mult = q.groups / q.team;
+    const int64_t most = (int64_t)(R / n) * q.mult * ceil_div(max_row_len, kPtTok);
+    const int fit = sms / q.team > 0 ? sms / q.team : 1;
+    q.teams = (int)(most < fit ? most : fit);
+    q.slot_cols = q.cols < kCols ? q.cols : kCols;
+    const size_t slots = (size_t)q.teams * q.team * 2 * q.slot_cols;
+    q.head_bytes = ((size_t)(R / n + 1) * sizeof(int64_t) + 15) / 16 * 16;
+    q.ml_bytes = (slots * sizeof(float2) + 15) / 16 * 16;
+    q.part_bytes = slots * kPtDl * sizeof(float);
+    return q;
+}
+
+template <bool FP8, bool PAIR>
+nsa_status launch(const AParams &p, const CUtensorMap &qn, const CUtensorMap &qr, const CUtensorMap &kv, cudaStream_t stream)
+{
+    auto kern = paged_mla_tc_kernel<FP8, PAIR>;
+    NSA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+    if (FP8) {
+        // the register split needs the registers the kernel was compiled to be launched with
+        cudaFuncAttributes fa;
+        NSA_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
+        if (fa.numRegs < kRegsLaunch) return NSA_ERR_UNSUPPORTED;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.teams * p.team));
+    cfg.blockDim = dim3(FP8 ? kThreadsFp8 : kThreadsBf16);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, qn, qr, kv));
+    paged_mla_join_kernel<<<(unsigned)((int64_t)p.t.B * p.cols), kJoinThreads, 0, stream>>>(p);
+    return launch_status();
+}
+
+}  // namespace
+
+size_t paged_mla_tc_workspace_bytes(nsa_dtype q_dtype, nsa_dtype kv_dtype, int R, int rows_per_req, int H, int d_latent,
+                                    int d_rope, int max_row_len)
+{
+    if (q_dtype != NSA_DT_BF16 || (kv_dtype != NSA_DT_BF16 && kv_dtype != NSA_DT_E4M3) || d_latent != kPtDl ||
+        d_rope != kPtDr || R <= 0 || rows_per_req <= 0 || R % rows_per_req != 0 || H <= 0 || max_row_len <= 0)
+        return 0;
+    const Plan q = make_plan(R, rows_per_req, H, max_row_len, current_sm_count());
+    return q.head_bytes + q.ml_bytes + q.part_bytes;
+}
+
+nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse, void *workspace, cudaStream_t stream)
+{
+    if (!paged_tc_applicable(a)) return NSA_ERR_UNSUPPORTED;
+    if ((int64_t)a.R * a.H > 0x7fffffffLL) return NSA_ERR_UNSUPPORTED;
+    const int sms = current_sm_count();
+    if (sms <= 0) return NSA_ERR_CUDA;
+    const Plan q = make_plan(a.R, a.rows_per_req, a.H, a.max_row_len, sms);
+    const bool fp8 = a.kv_dtype == NSA_DT_E4M3, pair = !fp8 && q.team >= 2;
+    AParams p;
+    p.t = paged_tc_params(a);
+    if (p.t.box_rows > 64) p.t.box_rows = 64;  // half a tile for each CTA of a pair
+    p.cols = q.cols; p.groups = q.groups; p.team = q.team; p.mult = q.mult; p.teams = q.teams; p.slot_cols = q.slot_cols;
+    p.out = (__nv_bfloat16 *)out;
+    p.lse = lse;
+    p.head = (int64_t *)workspace;
+    p.part_ml = (float2 *)((uint8_t *)workspace + q.head_bytes);
+    p.part = (float *)((uint8_t *)workspace + q.head_bytes + q.ml_bytes);
+    CUtensorMap qn, qr, kv = {};
+    if (!paged_tc_maps(a, p.t, kCols, &qn, &qr, &kv)) return NSA_ERR_CUDA;
+    if (fp8) return launch<true, false>(p, qn, qr, kv, stream);
+    return pair ? launch<false, true>(p, qn, qr, kv, stream) : launch<false, false>(p, qn, qr, kv, stream);
+}
+
+}  // namespace nsa

@@ -57,13 +57,18 @@ __device__ __forceinline__ void report_lengths(const PagedTc &p)
 }
 
 // Where a share of the launch's tiles starts.  The tiles of all requests (each
-// counted `mult` times) in request order are cut into `parts` equal shares;
+// counted `mult` times) in request order are cut into up to `parts` equal shares;
 // share `part` is [g0, g1) and its first tile is tile `off` of request `b`.
 struct TileShare {
     int64_t warp[32];
     int64_t total, g0, g1, off;
     int b;
 };
+
+__device__ __forceinline__ int64_t share_count(int64_t total, int parts)
+{
+    return total < 1 ? 1 : total < parts ? total : parts;
+}
 
 __device__ __forceinline__ void find_share(const PagedTc &p, int mult, int part, int parts, TileShare *sh)
 {
@@ -76,7 +81,9 @@ __device__ __forceinline__ void find_share(const PagedTc &p, int mult, int part,
     __syncthreads();
     int64_t total = 0;
     for (int w = 0; w < nw; ++w) total += sh->warp[w];
-    const int64_t g0 = total * part / parts, g1 = total * (part + 1) / parts;
+    // no more shares than tiles, so that every share that has a neighbour has a tile
+    const int64_t np = share_count(total, parts);
+    const int64_t g0 = part < np ? total * part / np : total, g1 = part < np ? total * (part + 1) / np : total;
     if (tid == 0) {
         sh->total = total;
         sh->g0 = g0;
