@@ -189,41 +189,48 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        if (work && lane == 0) {
+        // the whole warp walks and waits; one lane issues, with descriptors in uniform registers
+        if (work) {
             const uint32_t idesc = instr_desc(1, 1, 0, 0, kPtTok, (uint32_t)p.N);
-            const uint32_t q_addr = smem_u32(q_s), r_addr = smem_u32(ring);
-            int st = 0, uses = 0;
-            uint32_t ph = 0, tile = 0;
-            bool more = true;
-            while (more && !sm->abort) {
-                if (!mbar_wait(&sm->q_full, uses & 1, kPtWait)) { fail(); break; }
+            const uint64_t q_desc = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
+            const uint64_t r_desc = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
+            int st = 0;
+            uint32_t ph = 0, tile = 0, uses = 0;
+            bool ok = true;
+            for (bool more = true; more && ok; more = w.next(p)) {
+                if (!mbar_wait(&sm->q_full, uses & 1, kPtWait)) ok = false;
                 ++uses;
-                for (int t = w.c0; t < w.c1 && !sm->abort; ++t, ++tile) {
+                for (int t = w.c0; t < w.c1 && ok; ++t, ++tile) {
                     const uint32_t buf = tile & 1, bph = (tile >> 1) & 1;
-                    if (!mbar_wait(&sm->s_empty[buf], bph ^ 1, kPtWait)) { fail(); break; }
-                    tc_fence_after();
+                    if (!mbar_wait(&sm->s_empty[buf], bph ^ 1, kPtWait)) ok = false;
                     for (int c = 0; c < 9; ++c) {
-                        if (!mbar_wait(&sm->full[st], ph, kPtWait)) { fail(); break; }
+                        if (!mbar_wait(&sm->full[st], ph, kPtWait)) ok = false;
                         tc_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16(tmem + buf * kCols, smem_desc(r_addr + st * kPtBlk + k * 32, 16, 1024, kSwizzle128B),
-                                    smem_desc(q_addr + c * q_blk + k * 32, 16, 1024, kSwizzle128B), idesc, (c | k) != 0);
-                        mma_commit(&sm->empty[st]);
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16(tmem + buf * kCols, r_desc + (st * kPtBlk + k * 32) / 16,
+                                        q_desc + (c * q_blk + k * 32) / 16, idesc, (c | k) != 0);
+                            mma_commit(&sm->empty[st]);
+                            if (c == 8) mma_commit(&sm->s_full[buf]);
+                        }
+                        __syncwarp();
                         if (++st == nst) {
                             st = 0;
                             ph ^= 1;
                         }
                     }
-                    mma_commit(&sm->s_full[buf]);
+                    ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
                 }
-                mma_commit(&sm->q_empty);
-                more = w.next(p);
+                if (elect_one()) mma_commit(&sm->q_empty);
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
             }
+            if (!ok && lane == 0) fail();
             // the last commit tracks every MMA before it: nothing is in flight at the end
             mbar_wait(&sm->q_empty, (uses - 1) & 1, kPtWait);
+            __syncwarp();
         }
-        __syncwarp();
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------ epilogue: one key a thread
         if (work) {
@@ -272,7 +279,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const float l2 = sm->lse2[c0 + j];
-                            const float e = exp2f(fmaf(__uint_as_float(s[j]), p.t.scale_log2, -l2));
+                            const float e = ex2_approx(fmaf(__uint_as_float(s[j]), p.t.scale_log2, -l2));
                             // a column without weight may hold anything: selected away, not multiplied
                             if (l2 != INFINITY && (whole || pos < sm->len[c0 + j])) sum += e;
                         }

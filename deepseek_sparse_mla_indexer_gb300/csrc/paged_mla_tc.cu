@@ -33,18 +33,21 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kCols = 64;                 // columns per CTA
-constexpr uint32_t kQBlk = kCols * 128;   // 8 KB
-constexpr uint32_t kQBytes = 9 * kQBlk, kKvBytes = 9 * kPtBlk;
-constexpr int kGrp = 32;                  // columns per softmax group
-constexpr uint32_t kColS = 256;           // S^T behind O^T's four blocks of 64 columns
+constexpr int kCols = 64;                 // columns per CTA at most
+constexpr uint32_t kQBytes = 9 * kCols * 128, kKvBytes = 9 * kPtBlk;
+constexpr uint32_t kColS = 256;           // S^T behind O^T's four blocks
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f;          // log2 units
 constexpr int kMaxTeam = 8;
 constexpr int kThreadsBf16 = 384, kThreadsFp8 = 384 + kDqThreads;
-// fp8: registers per thread at launch and per role: 7 warpgroups x 72 = 40 + 2 x 104 + 4 x 64
-constexpr int kRegsLaunch = 72, kRegsCtl = 40, kRegsSoftmax = 104, kRegsRows = 64;
-static_assert(kRegsCtl + 2 * kRegsSoftmax + 4 * kRegsRows <= 7 * kRegsLaunch, "the split fits what the block has");
+// fp8: registers per thread at launch and per role (one control, two softmax and four row
+// warpgroups); the softmax needs two per column, the rest goes to the rows
+constexpr int kRegsLaunch = 72;
+template <int NC>
+struct Regs {
+    static constexpr int kCtl = NC == 64 ? 40 : 56, kSoftmax = NC == 64 ? 104 : 64, kRows = NC == 64 ? 64 : 80;
+    static_assert(kCtl + 2 * kSoftmax + 4 * kRows <= 7 * kRegsLaunch, "the split fits what the block has");
+};
 
 struct AShared {
     alignas(16) float m_run[kCols];   // running maximum, log2 units
@@ -65,7 +68,7 @@ static_assert(kSmem <= 232448, "shared memory per CTA");
 
 struct AParams {
     PagedTc t;
-    int cols, groups, team, mult;  // columns per request, groups of 64, CTAs per team, groups / team
+    int cols, nc, groups, team, mult;  // columns per request and per CTA, groups of nc, CTAs per team, groups / team
     int teams;
     int slot_cols;                 // columns of a partial slot
     __nv_bfloat16 *out;
@@ -116,11 +119,31 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <bool FP8, bool PAIR>
+// G columns of the accumulator at `taddr` from or into TMEM, one lane a thread.
+template <int G>
+__device__ __forceinline__ void tmem_ldg(uint32_t taddr, uint32_t (&r)[G])
+{
+    if constexpr (G == 32) tmem_ld32(taddr, r);
+    else if constexpr (G == 16) tmem_ld16(taddr, r);
+    else tmem_ld8(taddr, r);
+    tmem_ld_wait();
+}
+template <int G>
+__device__ __forceinline__ void tmem_stg(uint32_t taddr, const uint32_t (&r)[G])
+{
+    if constexpr (G == 32) tmem_st32(taddr, r);
+    else if constexpr (G == 16) tmem_st16(taddr, r);
+    else tmem_st8(taddr, r);
+}
+
+// NC: columns of the CTA's products (16, 32 or 64), two softmax groups of half as many.
+template <bool FP8, bool PAIR, int NC>
 __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreadsBf16, 1)
 paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
                     const __grid_constant__ CUtensorMap kv_map)
 {
+    constexpr int kGrp = NC / 2;
+    constexpr uint32_t kQBlk = NC * 128;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *q_s = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *kv_s = q_s + kQBytes;
@@ -161,7 +184,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
     const bool work = s.start(p, sm->share);
 
     if (warp < 4) {
-        if (FP8) regs_down<kRegsCtl>();
+        if (FP8) regs_down<Regs<NC>::kCtl>();
         if (warp == 0 && work) {
             // -------------------------------------------------------- TMA
             const int boxes = kPtTok / p.t.box_rows;  // at most 16, one a lane
@@ -173,8 +196,8 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             for (bool more = true; more && !stop(); more = s.next(p), ++seg) {
                 if (lane == 0) {
                     if (seg > 0 && !mbar_wait(&sm->q_empty, (seg - 1) & 1, kPtWait)) fail();
-                    mbar_arrive_expect_tx(&sm->q_full, kQBytes);
-                    const int row = s.b * p.cols + (s.j * p.team + rank) * kCols;
+                    mbar_arrive_expect_tx(&sm->q_full, 9 * kQBlk);
+                    const int row = s.b * p.cols + (s.j * p.team + rank) * NC;
                     for (int c = 0; c < 8; ++c) tma_load_2d(q_s + c * kQBlk, &qn_map, 64 * c, row, &sm->q_full);
                     tma_load_2d(q_s + 8 * kQBlk, &qr_map, 0, row, &sm->q_full);
                 }
@@ -228,59 +251,69 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             __syncwarp();
         } else if (warp == 1 && work) {
             // -------------------------------------------------------- MMA
-            if (lane == 0) {
-                const uint32_t idesc_s = instr_desc(1, 1, 0, 0, kPtTok, kCols);  // K-major A and B
-                const uint32_t idesc_o = instr_desc(1, 1, 1, 1, 128, kCols);     // MN-major A and B
-                const uint32_t q_addr = smem_u32(q_s), kv_addr = smem_u32(kv_s), p_addr = smem_u32(p_s);
-                auto free_pair = [&](int m) {
-                    if (PAIR)
-                        mma_commit_multicast(&sm->pair_free[m], 3);
-                    else
-                        mma_commit(&sm->pair_free[m]);
-                };
-                uint32_t i = 0, seg = 0;
-                bool ok = true;
-                for (bool more = true; more && ok; more = s.next(p), ++seg) {
-                    if (!mbar_wait(&sm->q_full, seg & 1, kPtWait)) ok = false;
-                    for (int t = s.t0; t < s.t1 && ok && !sm->abort; ++t, ++i) {
-#pragma unroll 1
-                        for (int m = 0; m < 5; ++m) {
-                            if (!mbar_wait(&sm->pair_full[m], i & 1, kPtWait)) { ok = false; break; }
-                            tc_fence_after();
-                            for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c) {
+            // The whole warp walks and waits; one lane issues, with descriptors in uniform registers
+            // (a lane-0 branch around the loop took 90 - 110 cycles an instruction).
+            const uint32_t idesc_s = instr_desc(1, 1, 0, 0, kPtTok, NC);  // K-major A and B
+            const uint32_t idesc_o = instr_desc(1, 1, 1, 1, 128, NC);     // MN-major A and B
+            const uint64_t k_desc = smem_desc(smem_u32(kv_s), 16, 1024, kSwizzle128B);
+            const uint64_t q_desc = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
+            const uint64_t v_desc = smem_desc(smem_u32(kv_s), kPtBlk, 1024, kSwizzle128B);
+            const uint64_t p_desc = smem_desc(smem_u32(p_s), kPtBlk, 1024, kSwizzle128B);
+            auto free_pair = [&](int m) {
+                if (PAIR)
+                    mma_commit_multicast(&sm->pair_free[m], 3);
+                else
+                    mma_commit(&sm->pair_free[m]);
+            };
+            uint32_t i = 0, seg = 0;
+            bool ok = true;
+            for (bool more = true; more && ok; more = s.next(p), ++seg) {
+                if (!mbar_wait(&sm->q_full, seg & 1, kPtWait)) ok = false;
+                for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
+#pragma unroll
+                    for (int m = 0; m < 5; ++m) {
+                        if (!mbar_wait(&sm->pair_full[m], i & 1, kPtWait)) ok = false;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    mma_f16(tmem + kColS, smem_desc(kv_addr + c * kPtBlk + k * 32, 16, 1024, kSwizzle128B),
-                                            smem_desc(q_addr + c * kQBlk + k * 32, 16, 1024, kSwizzle128B), idesc_s,
-                                            (c | k) != 0);
+                                    mma_f16(tmem + kColS, k_desc + (c * kPtBlk + k * 32) / 16,
+                                            q_desc + (c * kQBlk + k * 32) / 16, idesc_s, (c | k) != 0);
+                            if (m == 4) {
+                                mma_commit(&sm->s_full);
+                                if (t + 1 == s.t1) mma_commit(&sm->q_empty);
                             }
                         }
-                        if (!ok) break;
-                        mma_commit(&sm->s_full);
-                        if (t + 1 == s.t1) mma_commit(&sm->q_empty);
-                        if (!mbar_wait(&sm->p_full, i & 1, kPtWait)) { ok = false; break; }
-                        tc_fence_after();
-#pragma unroll 1
+                        __syncwarp();
+                    }
+                    if (!mbar_wait(&sm->p_full, i & 1, kPtWait)) ok = false;
+                    ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
                         for (int m = 0; m < 4; ++m) {
 #pragma unroll
                             for (int k = 0; k < kPtTok / 16; ++k)
-                                mma_f16(tmem + m * kCols,
-                                        smem_desc(kv_addr + 2 * m * kPtBlk + k * 2048, kPtBlk, 1024, kSwizzle128B),
-                                        smem_desc(p_addr + k * 2048, kPtBlk, 1024, kSwizzle128B), idesc_o,
-                                        (t > s.t0 || k > 0) ? 1u : 0u);
+                                mma_f16(tmem + m * NC, v_desc + (2 * m * kPtBlk + k * 2048) / 16, p_desc + k * 2048 / 16,
+                                        idesc_o, k > 0 ? 1u : (uint32_t)(t > s.t0));
                             free_pair(m);
                         }
                         free_pair(4);
                         if (t + 1 == s.t1) mma_commit(&sm->o_fin);
                     }
-                    if (sm->abort) ok = false;
+                    __syncwarp();
                 }
-                if (!ok) {
-                    fail();
-                    // whatever was issued is done before shared memory and TMEM are given up
-                    mma_commit(&sm->o_fin);
-                    for (int w = 0; w < 2; ++w) mbar_wait(&sm->o_fin, w, kPtWait / 100);
-                }
+                ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
+            }
+            if (!ok) {
+                if (lane == 0) fail();
+                // whatever was issued is done before shared memory and TMEM are given up
+                if (elect_one()) mma_commit(&sm->o_fin);
+                __syncwarp();
+                for (int w = 0; w < 2; ++w) mbar_wait(&sm->o_fin, w, kPtWait / 100);
             }
             __syncwarp();
         } else if (warp == 2 && blockIdx.x == 0) {
@@ -313,7 +346,10 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             }
         }
     } else if (warp < 12) {
-        if (FP8) regs_up<kRegsSoftmax>();
+        if (FP8) {
+            if constexpr (Regs<NC>::kSoftmax > kRegsLaunch) regs_up<Regs<NC>::kSoftmax>();
+            else regs_down<Regs<NC>::kSoftmax>();
+        }
         if (work) {
             // -------------------------------------------------------- softmax: one key a thread, 32 columns a group
             const int grp = (warp - 4) >> 2, quad = warp & 3, cb = grp * kGrp, bar = 1 + grp;
@@ -323,7 +359,9 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             uint32_t i = 0, seg = 0;
             bool ok = true;
             for (bool more = true; more && ok; more = s.next(p), ++seg) {
-                const int col0 = (s.j * p.team + rank) * kCols;  // first column of this CTA in the request
+                const int col0 = (s.j * p.team + rank) * NC;  // first column of this CTA in the request
+                if (et == 0) sm->min_len[grp] = 0x7fffffff;
+                __syncwarp();  // et 0 .. kGrp-1 are lanes of one warp
                 if (et < kGrp) {
                     const int c = col0 + cb + et;
                     int len = 0x7fffffff;  // padding: never masked, never written
@@ -333,49 +371,60 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     }
                     sm->len[cb + et] = len;
                     sm->m_run[cb + et] = -INFINITY;
-                    const int mn = __reduce_min_sync(0xffffffffu, len);  // et < 32: one whole warp
-                    if (lane == 0) sm->min_len[grp] = mn;
+                    atomicMin(&sm->min_len[grp], len);
                 }
                 bar_sync(bar, 128);
                 const int min_len = sm->min_len[grp];
                 const int32_t *pt = p.t.page_table + (int64_t)s.b * p.t.pt_ld;
-                float l[kGrp];
+                float2 l[kGrp / 2];
 #pragma unroll
-                for (int c = 0; c < kGrp; ++c) l[c] = 0.f;
+                for (int c = 0; c < kGrp / 2; ++c) l[c] = make_float2(0.f, 0.f);
                 for (int t = s.t0; t < s.t1; ++t, ++i) {
                     const int pos = t * kPtTok + key;
                     const bool valid = checked_page(p.t, pt, pos, s.len) >= 0;
                     ok = mbar_wait(&sm->s_full, i & 1, kPtWait);
                     if (!ok) fail();
-                    if (bar_red_or(bar, 128, !ok || sm->abort)) { ok = false; break; }
                     tc_fence_after();
-                    uint32_t sa[kGrp];
-                    tmem_ld32(lanes + kColS + cb, sa);
-                    tmem_ld_wait();
-                    float x[kGrp];
-                    if ((t + 1) * kPtTok <= min_len && __all_sync(0xffffffffu, valid)) {
+                    const bool whole = (t + 1) * kPtTok <= min_len && __all_sync(0xffffffffu, valid);
+                    // exponents d = x - m; a key above its column's maximum by 2^8 asks for new maxima
+                    float2 d[kGrp / 2];
+                    auto exponents = [&]() {
+                        uint32_t sa[kGrp];
+                        tmem_ldg<kGrp>(lanes + kColS + cb, sa);
+                        const float2 sc = make_float2(p.t.scale_log2, p.t.scale_log2);
 #pragma unroll
-                        for (int c = 0; c < kGrp; ++c) x[c] = __uint_as_float(sa[c]) * p.t.scale_log2;
-                    } else {
+                        for (int c = 0; c < kGrp / 4; ++c) {
+                            const float4 m = m4[c];
+                            d[2 * c] = fma2(make_float2(__uint_as_float(sa[4 * c]), __uint_as_float(sa[4 * c + 1])), sc,
+                                            make_float2(-m.x, -m.y));
+                            d[2 * c + 1] = fma2(make_float2(__uint_as_float(sa[4 * c + 2]), __uint_as_float(sa[4 * c + 3])),
+                                                sc, make_float2(-m.z, -m.w));
+                        }
+                        if (!whole) {
 #pragma unroll
-                        for (int c = 0; c < kGrp; ++c)
-                            x[c] = valid && pos < sm->len[cb + c] ? __uint_as_float(sa[c]) * p.t.scale_log2 : -INFINITY;
-                    }
-                    bool exceed = false;
+                            for (int c = 0; c < kGrp / 2; ++c) {
+                                if (!valid || pos >= sm->len[cb + 2 * c]) d[c].x = -INFINITY;
+                                if (!valid || pos >= sm->len[cb + 2 * c + 1]) d[c].y = -INFINITY;
+                            }
+                        }
+                    };
+                    exponents();
+                    float top = d[0].x;
 #pragma unroll
-                    for (int c = 0; c < kGrp / 4; ++c) {
-                        const float4 m = m4[c];
-                        exceed |= x[4 * c] > m.x + kRescale || x[4 * c + 1] > m.y + kRescale ||
-                                  x[4 * c + 2] > m.z + kRescale || x[4 * c + 3] > m.w + kRescale;
-                    }
-                    if (bar_red_or(bar, 128, exceed)) {
+                    for (int c = 0; c < kGrp / 2; ++c) top = fmaxf(fmaxf(top, d[c].x), d[c].y);
+                    if (bar_red_or(bar, 128, !ok || sm->abort || top > kRescale)) {
+                        if (bar_red_or(bar, 128, !ok || sm->abort)) { ok = false; break; }
                         // new maxima from this tile; sums and accumulators so far are rescaled
+                        {
+                            uint32_t sa[kGrp];
+                            tmem_ldg<kGrp>(lanes + kColS + cb, sa);
 #pragma unroll
-                        for (int c = 0; c < kGrp; ++c) {
-                            float v = x[c];
+                            for (int c = 0; c < kGrp; ++c) {
+                                float v = valid && pos < sm->len[cb + c] ? __uint_as_float(sa[c]) * p.t.scale_log2 : -INFINITY;
 #pragma unroll
-                            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                            if (lane == 0) sm->red[quad][cb + c] = v;
+                                for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                                if (lane == 0) sm->red[quad][cb + c] = v;
+                            }
                         }
                         bar_sync(bar, 128);
                         if (et < kGrp) {
@@ -391,30 +440,29 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
 #pragma unroll 1
                             for (int m = 0; m < 4; ++m) {
                                 uint32_t v[kGrp];
-                                tmem_ld32(lanes + m * kCols + cb, v);
-                                tmem_ld_wait();
+                                tmem_ldg<kGrp>(lanes + m * NC + cb, v);
 #pragma unroll
                                 for (int c = 0; c < kGrp; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * sm->alpha[cb + c]);
-                                tmem_st32(lanes + m * kCols + cb, v);
+                                tmem_stg<kGrp>(lanes + m * NC + cb, v);
                             }
                             tmem_st_wait();
 #pragma unroll
-                            for (int c = 0; c < kGrp; ++c) l[c] *= sm->alpha[cb + c];
+                            for (int c = 0; c < kGrp / 2; ++c) {
+                                l[c].x *= sm->alpha[cb + 2 * c];
+                                l[c].y *= sm->alpha[cb + 2 * c + 1];
+                            }
                         }
+                        exponents();
                     }
 #pragma unroll
                     for (int c8 = 0; c8 < kGrp / 8; ++c8) {
-                        const float4 ma = m4[2 * c8], mb = m4[2 * c8 + 1];
-                        const float mv[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
                         uint32_t pk[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const int c = 8 * c8 + 2 * k;
-                            const float p0 = x[c] == -INFINITY ? 0.f : exp2f(x[c] - mv[2 * k]);
-                            const float p1 = x[c + 1] == -INFINITY ? 0.f : exp2f(x[c + 1] - mv[2 * k + 1]);
-                            l[c] += p0;
-                            l[c + 1] += p1;
-                            pk[k] = pack2(p0, p1);
+                            const int c = 4 * c8 + k;
+                            const float2 e = make_float2(ex2_approx(d[c].x), ex2_approx(d[c].y));
+                            l[c] = add2(l[c], e);
+                            pk[k] = pack2(e.x, e.y);
                         }
                         *reinterpret_cast<uint4 *>(p_s + sw128_offset(key, cb / 8 + c8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
@@ -435,18 +483,26 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 }
                 if (!ok) break;
                 // ---------------------------------------------------- the piece's sums and accumulators
-                // column sums over the lanes: after the exchange lane c holds column c
+                // column sums over the lanes, by halving exchanges: lane x ends with column x % kGrp
+                float ls[kGrp];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
+                for (int c = 0; c < kGrp / 2; ++c) {
+                    ls[2 * c] = l[c].x;
+                    ls[2 * c + 1] = l[c].y;
+                }
+#pragma unroll
+                for (int o = kGrp / 2; o > 0; o >>= 1) {
                     const bool up = (lane & o) != 0;
 #pragma unroll
                     for (int c = 0; c < o; ++c) {
-                        const float give = up ? l[c] : l[c + o];
+                        const float give = up ? ls[c] : ls[c + o];
                         const float got = __shfl_xor_sync(0xffffffffu, give, o);
-                        l[c] = (up ? l[c + o] : l[c]) + got;
+                        ls[c] = (up ? ls[c + o] : ls[c]) + got;
                     }
                 }
-                sm->red[quad][cb + lane] = l[0];
+#pragma unroll
+                for (int o = kGrp; o < 32; o <<= 1) ls[0] += __shfl_xor_sync(0xffffffffu, ls[0], o);
+                if (lane < kGrp) sm->red[quad][cb + lane] = ls[0];
                 bar_sync(bar, 128);
                 const bool whole = s.t0 == 0 && s.t1 == s.tiles;
                 const int nc = min(kGrp, p.cols - col0 - cb);  // real columns of this group (may be <= 0)
@@ -474,8 +530,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
 #pragma unroll 1
                 for (int m = 0; m < 4; ++m) {
                     uint32_t v[kGrp];
-                    tmem_ld32(lanes + m * kCols + cb, v);
-                    tmem_ld_wait();
+                    tmem_ldg<kGrp>(lanes + m * NC + cb, v);
                     if (whole) {
                         __nv_bfloat16 *o = p.out + row0 * kPtDl + m * 128 + key;
 #pragma unroll
@@ -495,7 +550,8 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             }
         }
     } else if constexpr (FP8) {
-        regs_down<kRegsRows>();
+        if constexpr (Regs<NC>::kRows > kRegsLaunch) regs_up<Regs<NC>::kRows>();
+        else regs_down<Regs<NC>::kRows>();
         if (work) {
             // -------------------------------------------------------- fp8 rows into the tile
             const int d = threadIdx.x - 384;
@@ -558,7 +614,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_mla_join_kernel(AParams p)
     const int b = (int)(row / p.cols), c = (int)(row - (int64_t)b * p.cols);
     const int64_t before = p.head[b], tiles = p.head[b + 1] - before, total = p.head[p.t.B] * p.mult;
     if (tiles == 0) return;
-    const int group = c / kCols, set = group / p.team, rank = group - set * p.team, cc = c - group * kCols;
+    const int group = c / p.nc, set = group / p.team, rank = group - set * p.team, cc = c - group * p.nc;
     const int64_t u0 = before * p.mult + set * tiles, u1 = u0 + tiles;  // the unit's tiles among all
     const int64_t np = share_count(total, p.teams);  // share k is [total * k / np, total * (k + 1) / np)
     auto share_of = [&](int64_t g) -> int {
@@ -620,7 +676,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_mla_join_kernel(AParams p)
 // up to kMaxTeam that divides the number of 64-column groups, as many as the SMs hold and
 // the tiles fill.
 struct Plan {
-    int cols, groups, team, mult, teams, slot_cols;
+    int cols, nc, groups, team, mult, teams, slot_cols;
     size_t head_bytes, ml_bytes, part_bytes;
 };
 
@@ -628,7 +684,8 @@ Plan make_plan(int R, int n, int H, int max_row_len, int sms)
 {
     Plan q;
     q.cols = n * H;
-    q.groups = (int)ceil_div(q.cols, kCols);
+    q.nc = q.cols <= 16 ? 16 : q.cols <= 32 ? 32 : kCols;
+    q.groups = (int)ceil_div(q.cols, q.nc);
     q.team = 1;
     while (q.team < kMaxTeam && q.groups % (2 * q.team) == 0) q.team *= 2;
     q.mult = q.groups / q.team;
@@ -643,10 +700,10 @@ Plan make_plan(int R, int n, int H, int max_row_len, int sms)
     return q;
 }
 
-template <bool FP8, bool PAIR>
+template <bool FP8, bool PAIR, int NC>
 nsa_status launch(const AParams &p, const CUtensorMap &qn, const CUtensorMap &qr, const CUtensorMap &kv, cudaStream_t stream)
 {
-    auto kern = paged_mla_tc_kernel<FP8, PAIR>;
+    auto kern = paged_mla_tc_kernel<FP8, PAIR, NC>;
     NSA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
     if (FP8) {
         // the register split needs the registers the kernel was compiled to be launched with
@@ -694,16 +751,22 @@ nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse,
     AParams p;
     p.t = paged_tc_params(a);
     if (p.t.box_rows > 64) p.t.box_rows = 64;  // half a tile for each CTA of a pair
-    p.cols = q.cols; p.groups = q.groups; p.team = q.team; p.mult = q.mult; p.teams = q.teams; p.slot_cols = q.slot_cols;
+    p.cols = q.cols; p.nc = q.nc; p.groups = q.groups; p.team = q.team; p.mult = q.mult; p.teams = q.teams; p.slot_cols = q.slot_cols;
     p.out = (__nv_bfloat16 *)out;
     p.lse = lse;
     p.head = (int64_t *)workspace;
     p.part_ml = (float2 *)((uint8_t *)workspace + q.head_bytes);
     p.part = (float *)((uint8_t *)workspace + q.head_bytes + q.ml_bytes);
     CUtensorMap qn, qr, kv = {};
-    if (!paged_tc_maps(a, p.t, kCols, &qn, &qr, &kv)) return NSA_ERR_CUDA;
-    if (fp8) return launch<true, false>(p, qn, qr, kv, stream);
-    return pair ? launch<false, true>(p, qn, qr, kv, stream) : launch<false, false>(p, qn, qr, kv, stream);
+    if (!paged_tc_maps(a, p.t, (uint32_t)q.nc, &qn, &qr, &kv)) return NSA_ERR_CUDA;
+    if (fp8)
+        return q.nc == 16   ? launch<true, false, 16>(p, qn, qr, kv, stream)
+               : q.nc == 32 ? launch<true, false, 32>(p, qn, qr, kv, stream)
+                            : launch<true, false, 64>(p, qn, qr, kv, stream);
+    if (pair) return launch<false, true, 64>(p, qn, qr, kv, stream);
+    return q.nc == 16   ? launch<false, false, 16>(p, qn, qr, kv, stream)
+           : q.nc == 32 ? launch<false, false, 32>(p, qn, qr, kv, stream)
+                        : launch<false, false, 64>(p, qn, qr, kv, stream);
 }
 
 }  // namespace nsa

@@ -178,9 +178,9 @@ struct Fp8Rows {
         for (int i = 0; i < 4; ++i) {
             const __half2_raw h =
                 __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((in[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
             // code x scale rounded to fp32, then to bf16: the row's value by definition
-            const __nv_bfloat162 v = __floats2bfloat162_rn(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
+            const float2 f = sm100::mul2(__half22float2(*reinterpret_cast<const __half2 *>(&h)), make_float2(s, s));
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
             o[i] = *reinterpret_cast<const uint32_t *>(&v);
         }
         out = make_uint4(o[0], o[1], o[2], o[3]);
