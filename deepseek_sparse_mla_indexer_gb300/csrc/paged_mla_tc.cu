@@ -189,18 +189,19 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             // -------------------------------------------------------- TMA
             const int boxes = kPtTok / p.t.box_rows;  // at most 16, one a lane
             const uint32_t box_bytes = (uint32_t)p.t.box_rows * 128;
-            auto stop = [&]() { return __any_sync(0xffffffffu, sm->abort) != 0; };
             // a pair's boxes are shared out by halves of the tile
-            const bool mine = lane < boxes && (!PAIR || (lane >= boxes / 2) == (peer == 1));
+            const int box0 = PAIR && peer == 1 ? boxes / 2 : 0, box1 = PAIR && peer == 0 ? boxes / 2 : boxes;
             uint32_t i = 0, seg = 0;
-            for (bool more = true; more && !stop(); more = s.next(p), ++seg) {
-                if (lane == 0) {
-                    if (seg > 0 && !mbar_wait(&sm->q_empty, (seg - 1) & 1, kPtWait)) fail();
+            bool ok = true;
+            for (bool more = true; more && ok; more = s.next(p), ++seg) {
+                if (seg > 0 && !mbar_wait(&sm->q_empty, (seg - 1) & 1, kPtWait)) ok = false;
+                const int row = s.b * p.cols + (s.j * p.team + rank) * NC;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&sm->q_full, 9 * kQBlk);
-                    const int row = s.b * p.cols + (s.j * p.team + rank) * NC;
                     for (int c = 0; c < 8; ++c) tma_load_2d(q_s + c * kQBlk, &qn_map, 64 * c, row, &sm->q_full);
                     tma_load_2d(q_s + 8 * kQBlk, &qr_map, 0, row, &sm->q_full);
                 }
+                __syncwarp();
                 if (FP8) continue;
                 const int32_t *pt = p.t.page_table + (int64_t)s.b * p.t.pt_ld;
                 // row of this lane's box of tile t, or -1
@@ -210,36 +211,44 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     return page < 0 ? -1 : page * p.t.ps + pos % p.t.ps;
                 };
                 int y = box_row(s.t0), y1 = box_row(s.t0 + 1);
-                bool stopped = false;
-                for (int t = s.t0; t < s.t1 && !stopped; ++t, ++i) {
+                for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
                     const uint32_t blk_bytes = __popc(__ballot_sync(0xffffffffu, y >= 0)) * box_bytes;
+                    const int y_first = __shfl_sync(0xffffffffu, y, box0);
+#pragma unroll
                     for (int m = 0; m < 5; ++m) {
-                        if (lane == 0 && !mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) fail();
-                        if (stop()) {
-                            stopped = true;
-                            break;
-                        }
-                        if (lane == 0) mbar_arrive_expect_tx(&sm->pair_full[m], (m < 4 ? 2 : 1) * blk_bytes);
+                        if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) ok = false;
+                        if (elect_one()) mbar_arrive_expect_tx(&sm->pair_full[m], (m < 4 ? 2 : 1) * blk_bytes);
                         __syncwarp();
-                        if (mine && y >= 0) {
-                            for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c) {
-                                uint8_t *dst = kv_s + c * kPtBlk + lane * box_bytes;
-                                if (PAIR)
-                                    tma_load_2d_multicast(dst, &kv_map, 64 * c, y, &sm->pair_full[m], 3);
-                                else
-                                    tma_load_2d(dst, &kv_map, 64 * c, y, &sm->pair_full[m]);
+                        // one lane issues a box at a time from uniform registers: a box's coordinates and
+                        // addresses per lane took 350 cycles a pair
+                        int yb = y_first;
+                        for (int x = box0; x < box1; ++x) {
+                            if (x > box0) yb = __shfl_sync(0xffffffffu, y, x);
+                            if (yb >= 0 && elect_one()) {
+#pragma unroll
+                                for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c) {
+                                    uint8_t *dst = kv_s + c * kPtBlk + x * box_bytes;
+                                    if (PAIR)
+                                        tma_load_2d_multicast(dst, &kv_map, 64 * c, yb, &sm->pair_full[m], 3);
+                                    else
+                                        tma_load_2d(dst, &kv_map, 64 * c, yb, &sm->pair_full[m]);
+                                }
                             }
+                            __syncwarp();
                         }
                     }
                     // the tile after the next one into L2 while this one is worked on
                     const int y2 = box_row(t + 2);
-                    if (mine && y2 >= 0)
+                    if (lane >= box0 && lane < box1 && y2 >= 0)
                         prefetch_l2_bulk(p.t.kv + (int64_t)y2 * (2 * (kPtDl + kPtDr)),
                                          (uint32_t)p.t.box_rows * (2 * (kPtDl + kPtDr)));
                     y = y1;
                     y1 = y2;
+                    ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
                 }
+                ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
             }
+            if (!ok && lane == 0) fail();
             if (lane == 0) {  // nothing is in flight at the end
                 if (!FP8 && i > 0)
                     for (int m = 0; m < 5; ++m) {
