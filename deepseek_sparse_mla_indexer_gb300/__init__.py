@@ -445,11 +445,10 @@ def _paged_q(q_dtype: int, q_nope: torch.Tensor, q_rope: torch.Tensor):
     want = {DT_F32: torch.float32, DT_BF16: torch.bfloat16}.get(q_dtype)
     if q_nope.dtype != want or q_rope.dtype != want:
         raise ValueError(f"q must be {want} for this q_dtype, got {q_nope.dtype} and {q_rope.dtype}")
-    out = []
-    for q, d in ((q_nope, dl), (q_rope, dr)):
-        h = q.stride(1) if H > 1 else d
-        out += [_ptr(q), q.stride(0) if R > 1 else H * h, h]
-    return out
+    sn, sr = q_nope.stride(), q_rope.stride()
+    hn, hr = (sn[1], sr[1]) if H > 1 else (dl, dr)
+    rn, rr = (sn[0], sr[0]) if R > 1 else (H * hn, H * hr)
+    return q_nope.data_ptr(), rn, hn, q_rope.data_ptr(), rr, hr
 
 
 def _paged_cache(kv_dtype: int, kv: torch.Tensor, page_size: int, d_latent: int, d_rope: int) -> int:
@@ -464,18 +463,23 @@ def _paged_cache(kv_dtype: int, kv: torch.Tensor, page_size: int, d_latent: int,
     return slots // page_size
 
 
-def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
-    """The library launches on the current device: every tensor must live there."""
-    dev = None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch_on(stream, *tensors: Optional[torch.Tensor]):
+    """The stream handle of a call on these tensors, which must live on the current device (the
+    library launches there)."""
+    dev = torch.cuda.current_device() if tensors[0].is_cuda else -1
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"expected CUDA tensors, got one on {t.device}")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.device.index != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError(f"expected CUDA tensors on the current device, got one on {t.device}")
+    if stream is None and _raw_stream is not None:  # the current stream without building its object
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _i32(name: str, t: torch.Tensor, n: int) -> torch.Tensor:
@@ -524,12 +528,12 @@ def nsa_paged_mla(q_dtype: int, kv_dtype: int, q_nope: torch.Tensor, q_rope: tor
     if tuple(out.shape) != (R, H, dl) or tuple(lse.shape) != (R, H) or lse.dtype != torch.float32 or \
             out.dtype != q_nope.dtype or not out.is_contiguous() or not lse.is_contiguous():
         raise ValueError("out must be [R, H, d_latent] in q's type and lse float32 [R, H], both contiguous")
-    _on_current_device(q_nope, q_rope, kv, page_table, row_len, out, lse, workspace, status)
+    handle = _launch_on(stream, q_nope, q_rope, kv, page_table, row_len, out, lse, workspace, status)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    rc = load().nsa_paged_mla(q_dtype, kv_dtype, *_paged_q(q_dtype, q_nope, q_rope), _ptr(kv), pages, page_size, _ptr(pt),
-                              _table_ld(pt, max_row_len, page_size), _ptr(_i32("row_len", row_len, R)), R, rows_per_req,
-                              H, dl, dr, max_row_len, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
-                              _ptr(status), _stream(stream))
+    rc = load().nsa_paged_mla(q_dtype, kv_dtype, *_paged_q(q_dtype, q_nope, q_rope), _at(kv), pages, page_size, _at(pt),
+                              _table_ld(pt, max_row_len, page_size), _at(_i32("row_len", row_len, R)), R, rows_per_req,
+                              H, dl, dr, max_row_len, float(sm_scale), _at(out), _at(lse), _at(workspace), ws_bytes,
+                              _at(status), handle)
     _check("nsa_paged_mla", rc)
 
 
@@ -551,11 +555,11 @@ def nsa_mla_key_weights(q_dtype: int, kv_dtype: int, q_nope: torch.Tensor, q_rop
     if tuple(lse.shape) != (R, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [R, H]")
     total_ld = _total_ld(total, B, max_row_len)
-    _on_current_device(q_nope, q_rope, kv, page_table, row_len, lse, total, status)
-    rc = load().nsa_mla_key_weights(q_dtype, kv_dtype, *_paged_q(q_dtype, q_nope, q_rope), _ptr(kv), pages, page_size,
-                                    _ptr(pt), _table_ld(pt, max_row_len, page_size), _ptr(_i32("row_len", row_len, R)), R,
-                                    rows_per_req, H, dl, dr, max_row_len, float(sm_scale), _ptr(lse), _ptr(total),
-                                    total_ld, _ptr(status), _stream(stream))
+    handle = _launch_on(stream, q_nope, q_rope, kv, page_table, row_len, lse, total, status)
+    rc = load().nsa_mla_key_weights(q_dtype, kv_dtype, *_paged_q(q_dtype, q_nope, q_rope), _at(kv), pages, page_size,
+                                    _at(pt), _table_ld(pt, max_row_len, page_size), _at(_i32("row_len", row_len, R)), R,
+                                    rows_per_req, H, dl, dr, max_row_len, float(sm_scale), _at(lse), _at(total),
+                                    total_ld, _at(status), handle)
     _check("nsa_mla_key_weights", rc)
 
 
@@ -573,9 +577,9 @@ def nsa_evict_select(total: torch.Tensor, lens: torch.Tensor, max_len: int, sink
     if keep.dtype != torch.int32 or keep.dim() != 2 or keep.shape[0] != B or keep.shape[1] < budget:
         raise ValueError(f"keep must be int32 [{B}, >= {budget}], got shape {tuple(keep.shape)} of {keep.dtype}")
     total_ld = _total_ld(total, B, max_len)
-    _on_current_device(total, lens, keep, new_len, status)
-    rc = load().nsa_evict_select(_ptr(total), total_ld, _ptr(_i32("lens", lens, B)), B, max_len, sinks, recent, budget,
-                                 _ptr(keep), _ld(keep), _ptr(_i32("new_len", new_len, B)), _ptr(status), _stream(stream))
+    handle = _launch_on(stream, total, lens, keep, new_len, status)
+    rc = load().nsa_evict_select(_at(total), total_ld, _at(_i32("lens", lens, B)), B, max_len, sinks, recent, budget,
+                                 _at(keep), _ld(keep), _at(_i32("new_len", new_len, B)), _at(status), handle)
     _check("nsa_evict_select", rc)
 
 
@@ -604,12 +608,12 @@ def nsa_evict_compact(keep: torch.Tensor, new_len: torch.Tensor, old_len: torch.
             raise ValueError(f"the arrays must be contiguous with one first dimension of whole pages of {page_size}, "
                              f"got shape {tuple(a.shape)}")
     total_ld = 0 if total is None else _total_ld(total, B, max_len)
-    _on_current_device(keep, new_len, old_len, page_table, total, workspace, status, *arrays)
+    handle = _launch_on(stream, keep, new_len, old_len, page_table, total, workspace, status, *arrays)
     n = len(arrays)
     ptrs = (C.c_void_p * max(1, n))(*[a.data_ptr() for a in arrays])
     nb = (C.c_int64 * max(1, n))(*[a.numel() * a.element_size() // slots for a in arrays])
-    rc = load().nsa_evict_compact(B, _ptr(keep), _ld(keep), keep.shape[1], _ptr(_i32("new_len", new_len, B)),
-                                  _ptr(_i32("old_len", old_len, B)), max_len, _ptr(pt), _table_ld(pt, max_len, page_size),
-                                  page_size, slots // page_size, n, ptrs, nb, _ptr(total), total_ld, _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    rc = load().nsa_evict_compact(B, _at(keep), _ld(keep), keep.shape[1], _at(_i32("new_len", new_len, B)),
+                                  _at(_i32("old_len", old_len, B)), max_len, _at(pt), _table_ld(pt, max_len, page_size),
+                                  page_size, slots // page_size, n, ptrs, nb, _at(total), total_ld, _at(workspace),
+                                  workspace.numel() * workspace.element_size(), _at(status), handle)
     _check("nsa_evict_compact", rc)

@@ -18,30 +18,29 @@ using namespace sm100;
 // ------------------------------------------------------------------ select
 //
 // One thread-block cluster per request; its CTAs own equal slices of the
-// positions.  The threshold key of the middle range is found by a radix
-// selection over 11 + 11 + 10 bits of the order-preserving key: each CTA counts
-// its slice's digits in shared memory, each sums one part of the bins over the
-// cluster (distributed shared memory), and the CTA whose part holds the
-// threshold tells the others the digit and how many keys remain to be taken
-// from it.  Then every CTA writes its kept positions behind those of the CTAs
+// positions and its warps contiguous parts of them, a key per lane and step, kept
+// in registers (slices up to 16 K; longer ones are read again from L2).  The
+// threshold key of the middle range is found by a radix selection over 11 + 11 +
+// 10 bits of the order-preserving key: each CTA counts its slice's digits in
+// shared memory, and after one cluster barrier every CTA sums all counts
+// (distributed shared memory) and finds the same digit, so a pass costs one
+// barrier.  Then every CTA writes its kept positions behind those of the CTAs
 // before it: positions above the threshold, and of those equal to it the lowest
-// ones.  Keys are read from HBM once (they stay in shared memory where a slice
-// fits), so a long row costs one pass plus about ten cluster barriers; whole
-// numbers throughout, so the result does not depend on scheduling.
-constexpr int kSelThreads = 512;
+// ones.  The totals are read from HBM once.  Whole numbers throughout: the result
+// does not depend on scheduling.  Bound by the latency of its dozen dependent
+// steps, not by its bytes.
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelKeys = 16;              // keys a thread holds in registers
 constexpr int kSelMaxCluster = 8;         // the portable limit
-constexpr int kSelCache = 48 * 1024;      // keys of a slice kept in shared memory
-constexpr int kSelSlice = 4096;           // positions per CTA that the cluster size aims for
-constexpr int kSelPer = 2048 / kSelThreads;  // consecutive bins a thread sums
+constexpr int kSelSlice = kSelThreads * kSelKeys;
 
 struct SelShared {
-    uint32_t hist[2048];
-    uint32_t seg[kSelMaxCluster];          // bins summed over the cluster, per part
-    uint32_t digit, need;                  // written by the part that holds the threshold
+    alignas(16) uint32_t hist[3][2048];    // one per pass: none is cleared while a peer may read it
+    uint32_t scan[kSelWarps];
+    uint32_t digit, need;
     uint32_t warp_sure[kSelWarps], warp_eq[kSelWarps];
     uint32_t cta_sure, cta_eq;             // this CTA's counts, read by the others
-    uint32_t scan[kSelWarps];
 };
 
 __device__ __forceinline__ uint32_t dsmem_ld_u32(const uint32_t *local, uint32_t rank)
@@ -50,29 +49,31 @@ __device__ __forceinline__ uint32_t dsmem_ld_u32(const uint32_t *local, uint32_t
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(dsmem_addr(local, rank)) : "memory");
     return v;
 }
-__device__ __forceinline__ void dsmem_st_u32(uint32_t *local, uint32_t rank, uint32_t v)
+__device__ __forceinline__ uint2 dsmem_ld_u32x2(const uint32_t *local, uint32_t rank)
 {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_addr(local, rank)), "r"(v) : "memory");
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(dsmem_addr(local, rank)) : "memory");
+    return v;
 }
 
 // Adds 1 to hist[bin] for every lane with `on`; a warp whose lanes all name one
 // bin (rows of equal totals) adds once.
 __device__ __forceinline__ void count_digit(uint32_t *hist, uint32_t bin, bool on, int lane)
 {
-    int all;
-    __match_all_sync(0xffffffffu, on ? bin : 0xffffffffu, &all);
-    if (all) {
-        if (on && lane == 0) atomicAdd(hist + bin, 32u);
+    const uint32_t first = __shfl_sync(0xffffffffu, bin, 0);
+    if (__all_sync(0xffffffffu, on && bin == first)) {
+        if (lane == 0) atomicAdd(hist + bin, 32u);
     } else if (on) {
         atomicAdd(hist + bin, 1u);
     }
 }
 
+// REGS: the slice's keys stay in registers; else they are read from L2 in every pass.
+template <bool REGS>
 __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, int max_len, int sinks, int recent,
-                    int budget, int slice, int cached, int32_t *keep, int64_t keep_ld, int32_t *new_len, int32_t *status)
+                    int budget, int slice, int32_t *keep, int64_t keep_ld, int32_t *new_len, int32_t *status)
 {
-    extern __shared__ uint32_t key_s[];  // [slice] order keys when `cached`
     __shared__ SelShared sm;
     const int nc = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
     const int b = blockIdx.x / nc;
@@ -91,49 +92,59 @@ evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, i
     const float *row = total + (int64_t)b * total_ld;
     const int mid0 = sinks, mid1 = L - recent;  // the middle range; sinks + recent <= budget < L
     const int p0 = min(L, rank * slice), p1 = min(L, p0 + slice);
-    const int m0 = min(p1, max(p0, mid0)), m1 = max(m0, min(p1, mid1));  // its part of this slice
-    auto key_at = [&](int i) -> uint32_t { return cached ? key_s[i - p0] : order_key(__ldg(row + i)); };
+    // this warp's part: steps of 32 consecutive positions from w0
+    const int steps = (p1 - p0 + kSelThreads - 1) / kSelThreads;
+    const int w0 = p0 + warp * steps * 32 + lane;  // position of this lane in step 0
+    auto in_mid = [&](int pos) { return pos < p1 && pos >= mid0 && pos < mid1; };
+    uint32_t key[REGS ? kSelKeys : 1];
+    if (REGS) {
+#pragma unroll
+        for (int j = 0; j < kSelKeys; ++j) {
+            const int pos = w0 + 32 * j;
+            key[j] = j < steps && in_mid(pos) ? __float_as_uint(__ldg(row + pos)) : 0u;
+        }
+    }
+    for (int i = tid; i < 3 * 2048 / 4; i += kSelThreads) reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (REGS) {
+#pragma unroll
+        for (int j = 0; j < kSelKeys; ++j) key[j] = order_key(__uint_as_float(key[j]));
+    }
+    // f(position, key) for every step of the warp, all lanes together
+    auto each = [&](auto f) {
+        if constexpr (REGS) {
+#pragma unroll
+            for (int j = 0; j < kSelKeys; ++j)
+                if (j < steps) f(w0 + 32 * j, key[j]);
+        } else {
+            for (int j = 0; j < steps; ++j) {
+                const int pos = w0 + 32 * j;
+                f(pos, in_mid(pos) ? order_key(__ldg(row + pos)) : 0u);
+            }
+        }
+    };
+    __syncthreads();
 
     uint32_t need = (uint32_t)(budget - sinks - recent), prefix = 0;
     const bool any = need > 0;  // else nothing between the ends is kept
     if (any) {
+#pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const int bins = pass == 2 ? 1024 : 2048;
-            for (int i = tid; i < bins; i += kSelThreads) sm.hist[i] = 0;
-            __syncthreads();
-            // whole warps step together (count_digit is a warp operation)
-            for (int i0 = m0 + warp * 32; i0 < m1; i0 += kSelThreads * 4) {
-                uint32_t k[4];
-                bool on[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = i0 + u * kSelThreads + lane;
-                    on[u] = i < m1;
-                    k[u] = on[u] ? (pass == 0 ? order_key(__ldg(row + i)) : key_at(i)) : 0u;
-                    if (pass == 0 && cached && on[u]) key_s[i - p0] = k[u];
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const bool in = on[u] && (pass == 0 || (k[u] >> (shift + (pass == 1 ? 11 : 10))) == prefix);
-                    count_digit(sm.hist, (k[u] >> shift) & (uint32_t)(bins - 1), in, lane);
-                }
-            }
+            const uint32_t mask = pass == 2 ? 1023u : 2047u;
+            uint32_t *hist = sm.hist[pass];
+            each([&](int pos, uint32_t k) {
+                const bool on = in_mid(pos) && (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == prefix);
+                if (pass == 0 || __any_sync(0xffffffffu, on)) count_digit(hist, (k >> shift) & mask, on, lane);
+            });
             cluster_sync_all();  // every CTA's counts are complete
-            // part `rank` of the bins, summed over the cluster, kSelPer consecutive bins a thread
-            const int per = bins / nc;
-            uint32_t tot[kSelPer];
-            uint32_t sum = 0;
-#pragma unroll
-            for (int u = 0; u < kSelPer; ++u) {
-                tot[u] = 0;
-                const int x = tid * kSelPer + u;
-                if (x < per)
-                    for (int q = 0; q < nc; ++q) tot[u] += dsmem_ld_u32(sm.hist + rank * per + x, (uint32_t)q);
-                sum += tot[u];
+            // bins 2 tid, 2 tid + 1 over the cluster, then counts from the top
+            uint2 c = make_uint2(0u, 0u);
+            for (int q = 0; q < nc; ++q) {
+                const uint2 v = dsmem_ld_u32x2(hist + 2 * tid, (uint32_t)q);
+                c.x += v.x;
+                c.y += v.y;
             }
-            // suffix sums over the threads (higher bins first)
-            uint32_t suf = sum;
+            uint32_t suf = c.x + c.y;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t v = __shfl_down_sync(0xffffffffu, suf, o);
@@ -141,104 +152,95 @@ evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, i
             }
             if (lane == 0) sm.scan[warp] = suf;
             __syncthreads();
-            uint32_t above = suf - sum;
-            for (int w = warp + 1; w < kSelWarps; ++w) above += sm.scan[w];
-            if (tid < nc) {
-                uint32_t all = 0;
-                for (int w = 0; w < kSelWarps; ++w) all += sm.scan[w];
-                dsmem_st_u32(sm.seg + rank, (uint32_t)tid, all);
+            uint32_t above = lane > warp ? sm.scan[lane] : 0u;
+            above = __reduce_add_sync(0xffffffffu, above) + suf - (c.x + c.y);
+            // the bin where the count from the top reaches `need`: exactly one thread has it
+            if (above < need && above + c.y >= need) {
+                sm.digit = 2 * tid + 1;
+                sm.need = need - above;
+            } else if (above + c.y < need && above + c.y + c.x >= need) {
+                sm.digit = 2 * tid;
+                sm.need = need - above - c.y;
             }
-            cluster_sync_all();  // every part's sum is known everywhere
-            for (int q = rank + 1; q < nc; ++q) above += sm.seg[q];
-            // the bin where the count from the top reaches `need`: exactly one thread of the cluster has it
-#pragma unroll
-            for (int u = kSelPer - 1; u >= 0; --u) {
-                if (above < need && above + tot[u] >= need) {
-                    const uint32_t d = (uint32_t)(rank * per + tid * kSelPer + u);
-                    for (int q = 0; q < nc; ++q) {
-                        dsmem_st_u32(&sm.digit, (uint32_t)q, d);
-                        dsmem_st_u32(&sm.need, (uint32_t)q, need - above);
-                    }
-                }
-                above += tot[u];
-            }
-            cluster_sync_all();  // digit and need have arrived; hist may be cleared
+            __syncthreads();
             prefix = (prefix << (pass == 2 ? 10 : 11)) | sm.digit;
             need = sm.need;
         }
     }
     const uint32_t threshold = prefix;
-    // count, per warp over its contiguous part, the positions surely kept and those equal to the threshold
-    const int len = p1 - p0, per_warp = ((len + kSelWarps * 32 - 1) / (kSelWarps * 32)) * 32;
-    const int w0 = min(p1, p0 + warp * per_warp), w1 = min(p1, w0 + per_warp);
-    auto classify = [&](int i, bool &sure, bool &eq) {
-        const bool in = i < w1, mid = in && i >= mid0 && i < mid1;
-        const uint32_t k = mid && any ? key_at(i) : 0u;
-        sure = in && (!mid || (any && k > threshold));
+    auto classify = [&](int pos, uint32_t k, bool &sure, bool &eq) {
+        const bool mid = in_mid(pos);
+        sure = pos < p1 && (!mid || (any && k > threshold));
         eq = mid && any && k == threshold;
     };
     uint32_t n_sure = 0, n_eq = 0;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
+    each([&](int pos, uint32_t k) {
         bool sure, eq;
-        classify(i0 + lane, sure, eq);
+        classify(pos, k, sure, eq);
         n_sure += __popc(__ballot_sync(0xffffffffu, sure));
         n_eq += __popc(__ballot_sync(0xffffffffu, eq));
-    }
+    });
     if (lane == 0) {
         sm.warp_sure[warp] = n_sure;
         sm.warp_eq[warp] = n_eq;
     }
     __syncthreads();
-    uint32_t eq_before = 0, sure_before = 0, cta_eq = 0, cta_sure = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-        if (w < warp) {
-            eq_before += sm.warp_eq[w];
-            sure_before += sm.warp_sure[w];
+    const uint32_t ws = sm.warp_sure[lane], we = sm.warp_eq[lane];
+    uint32_t sure_before = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0u);
+    uint32_t eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0u);
+    if (nc > 1) {
+        if (warp == 0) {
+            const uint32_t all_sure = __reduce_add_sync(0xffffffffu, ws), all_eq = __reduce_add_sync(0xffffffffu, we);
+            if (lane == 0) {
+                sm.cta_sure = all_sure;
+                sm.cta_eq = all_eq;
+            }
         }
-        cta_eq += sm.warp_eq[w];
-        cta_sure += sm.warp_sure[w];
-    }
-    if (tid == 0) {
-        sm.cta_eq = cta_eq;
-        sm.cta_sure = cta_sure;
-    }
-    cluster_sync_all();
-    for (int q = 0; q < rank; ++q) {
-        eq_before += dsmem_ld_u32(&sm.cta_eq, (uint32_t)q);
-        sure_before += dsmem_ld_u32(&sm.cta_sure, (uint32_t)q);
+        cluster_sync_all();
+        const uint32_t cs = lane < rank ? dsmem_ld_u32(&sm.cta_sure, (uint32_t)lane) : 0u;
+        const uint32_t ce = lane < rank ? dsmem_ld_u32(&sm.cta_eq, (uint32_t)lane) : 0u;
+        sure_before += __reduce_add_sync(0xffffffffu, cs);
+        eq_before += __reduce_add_sync(0xffffffffu, ce);
     }
     // a position's place: the sure ones before it plus the equal ones taken before it
-    for (int i0 = w0; i0 < w1; i0 += 32) {
+    each([&](int pos, uint32_t k) {
         bool sure, eq;
-        classify(i0 + lane, sure, eq);
+        classify(pos, k, sure, eq);
         const uint32_t below = (1u << lane) - 1u;
         const uint32_t bs = __ballot_sync(0xffffffffu, sure), be = __ballot_sync(0xffffffffu, eq);
         const uint32_t e = eq_before + __popc(be & below);
-        const uint32_t at = sure_before + __popc(bs & below) + min(e, need);
-        if (sure || (eq && e < need)) out[at] = i0 + lane;
+        if (sure || (eq && e < need)) out[sure_before + __popc(bs & below) + min(e, need)] = pos;
         eq_before += __popc(be);
         sure_before += __popc(bs);
-    }
+    });
     if (rank == 0 && tid == 0) new_len[b] = budget;
-    cluster_sync_all();  // a peer may still read this CTA's counts
+    if (nc > 1) cluster_sync_all();  // a peer may still read this CTA's counts
 }
 
 // ------------------------------------------------------------------ compact
 //
 // Position i of a request's front takes the row of position keep[i], in place.
 // keep ascends, so keep[i] >= i: rows only move towards the front, and a row
-// may be overwritten as soon as it has been read.  The positions are cut into
+// may be overwritten as soon as it has been read.  The kept positions are cut into
 // chunks of T; a CTA stages its chunk's source rows in shared memory, announces
 // that it has read them, waits until every chunk that reads rows from its own
 // destination range has announced the same, and writes.  Those are chunks with
 // lower numbers (keep[j] >= j), at most two besides itself (each spans at least
-// T source positions), and chunks are handed out in ascending order, so the
-// waits end: the lowest unfinished chunk never waits.  Bound by HBM: every row
-// that moves is read and written once; rows that stay are not touched.
+// T source positions).  The totals behind the kept positions are cleared by chunks
+// of kCpTail positions under the same rule.  Chunks are handed out in ascending
+// order, the clearing ones last, so the waits end: a CTA waits only for chunks that
+// were handed out before its own, and the lowest unfinished one never waits.
+//
+// Bound by HBM: every row that moves is read and written once; rows that stay are
+// not touched.  A chunk is a chain of dependent loads (ticket, lengths, kept
+// positions, pages, rows), so the chain of a CTA's next chunk is walked while the
+// rows of the current one are on their way, and several CTAs share an SM.
 constexpr int kMaxArrays = 8;
 constexpr int kCpThreads = 256;
 constexpr int kCpMinT = 8, kCpMaxT = 128;
-constexpr int kCpStage = 56 * 1024;      // bytes staged per CTA: four CTAs per SM
+constexpr int kCpTail = 4096;            // totals cleared by one chunk
+constexpr int kCpStage = 44 * 1024;      // bytes staged per CTA: five CTAs per SM
+constexpr int kCpPerSm = 5;
 constexpr int kCpMaxRow = 24 * 1024;     // bytes of one position over all arrays
 constexpr long long kCpWait = 2000000000LL;  // ~1 s of SM clocks
 
@@ -246,6 +248,8 @@ struct CompactParams {
     uint8_t *array[kMaxArrays];
     int row_bytes[kMaxArrays];
     int unit[kMaxArrays];       // bytes per copy step: 16, 4 or 1
+    uint32_t per[kMaxArrays];   // steps per row
+    uint32_t magic[kMaxArrays]; // ceil(2^32 / per): step / per is its high product; 0: divide
     int offset[kMaxArrays];     // of the array's rows within the stage
     int n_arrays;
     const int32_t *keep;
@@ -257,7 +261,7 @@ struct CompactParams {
     int64_t num_pages;
     float *total;
     int64_t total_ld;
-    int T, chunks, B;
+    int T, chunks, tails, B;    // per request: chunks of T kept positions, tails of kCpTail positions
     int32_t *read_done;  // [B][chunks], zero at the start
     int32_t *ticket;     // zero at the start
     int32_t *status;
@@ -274,20 +278,88 @@ __device__ __forceinline__ void st_release(int32_t *p, int v)
     asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// The number of entries of the ascending keep[0 .. n) below `v`, by the whole CTA.
-__device__ __forceinline__ int block_lower_bound(const int32_t *keep, int n, int v)
+// The number of entries of the ascending keep[0 .. n) below `v`, by one warp.
+__device__ __forceinline__ int warp_lower_bound(const int32_t *keep, int n, int v, int lane)
 {
     int lo = 0, len = n;  // the answer lies in [lo, lo + len]
     while (len > 0) {
-        const int step = (len + kCpThreads - 1) / kCpThreads;
-        const int i = (int)threadIdx.x * step;
-        const int c = __syncthreads_count(i < len && keep[lo + i] < v);
+        const int step = (len + 31) / 32;
+        const int i = lane * step;
+        const int c = __popc(__ballot_sync(0xffffffffu, i < len && keep[lo + i] < v));
         if (c == 0) return lo;
         if (step == 1) return lo + c;
         lo += (c - 1) * step + 1;  // entry (c - 1) * step is below v
         len = min(step - 1, len - (c - 1) * step - 1);
     }
     return lo;
+}
+
+// What a CTA knows of a chunk before it moves its rows.
+struct Chunk {
+    int64_t src[kCpMaxT], dst[kCpMaxT];  // slots; -1: the row does not move
+    int32_t from[kCpMaxT];               // position whose total moves here, -1: cleared, -2: not of this chunk
+    int ticket, b, c;                    // c < 0: tail chunk -c - 1
+    int lo, hi;                          // destination positions
+    int w0, w1;                          // chunks w0 .. w1-1 read from there
+    int run;                             // 0: nothing to do
+};
+
+// The chunk of `ticket` (all threads; ends without a barrier).
+__device__ __forceinline__ void describe(const CompactParams &p, Chunk &k, int ticket)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // tickets go round the requests first: a chunk's predecessors are then well ahead of it
+    const int rows = p.B * p.chunks;
+    const bool tail = ticket >= rows;
+    const int x = tail ? ticket - rows : ticket;
+    const int c = x / p.B, b = x - c * p.B;
+    const int old = p.old_len[b], n = p.new_len[b];
+    const bool bad = old < 0 || old > p.max_len || n < 0 || n > old || n > p.budget;
+    if (bad && tid == 0 && c == 0 && !tail) set_status(p.status, NSA_ERR_BOUNDS);
+    const int lo = tail ? max(n, c * kCpTail) : c * p.T;
+    const int hi = tail ? min(old, (c + 1) * kCpTail) : min(n, lo + p.T);
+    const bool run = !bad && n < old && lo < hi && (!tail || p.total);
+    const int32_t *keep = p.keep + (int64_t)b * p.keep_ld;
+    if (tid < p.T) {
+        int64_t s = -1, d = -1;
+        int32_t from = -2;
+        const int i = lo + tid;
+        if (run && !tail && i < hi) {
+            const int32_t *pt = p.page_table + (int64_t)b * p.pt_ld;
+            const int q = keep[i];
+            from = q;
+            if (q < i || q >= old || (i > 0 && keep[i - 1] >= q)) {
+                set_status(p.status, NSA_ERR_BOUNDS);  // not an ascending list of positions: the row stays
+                from = i;
+            } else if (q != i && p.n_arrays > 0) {
+                const int32_t ps = pt[q / p.page_size], pd = pt[i / p.page_size];
+                if (ps < 0 || ps >= p.num_pages || pd < 0 || pd >= p.num_pages) {
+                    set_status(p.status, NSA_ERR_BOUNDS);
+                } else {
+                    s = (int64_t)ps * p.page_size + q % p.page_size;
+                    d = (int64_t)pd * p.page_size + i % p.page_size;
+                }
+            }
+        }
+        k.src[tid] = s;
+        k.dst[tid] = d;
+        k.from[tid] = from;
+    }
+    // rows j with lo <= keep[j] < hi are read from the destination range, by chunks j / T
+    int w = 0;
+    if (warp >= kCpThreads / 32 - 2) {
+        const bool second = warp == kCpThreads / 32 - 1;
+        const int j = run ? warp_lower_bound(keep, n, second ? hi : lo, lane) : 0;
+        w = second ? (j + p.T - 1) / p.T : j / p.T;
+        if (lane == 0) (second ? k.w1 : k.w0) = w;
+    }
+    if (tid == 0) {
+        k.b = b;
+        k.c = tail ? -c - 1 : c;
+        k.lo = lo;
+        k.hi = hi;
+        k.run = run ? 1 : 0;
+    }
 }
 
 template <int UNIT> struct CopyUnit;
@@ -297,17 +369,20 @@ template <> struct CopyUnit<1> { using type = uint8_t; };
 
 // Rows of one array between the cache and the stage.
 template <int UNIT, bool READ>
-__device__ __forceinline__ void move_rows(uint8_t *array, int row_bytes, uint8_t *stage, const int64_t *slot, int T)
+__device__ __forceinline__ void move_rows(uint8_t *array, int row_bytes, uint32_t per, uint32_t magic, uint8_t *stage,
+                                          const int64_t *slot, int T)
 {
     using U = typename CopyUnit<UNIT>::type;
-    const int per = row_bytes / UNIT;
-    for (int e = threadIdx.x; e < T * per; e += kCpThreads) {
-        const int i = e / per, c = e - i * per;
-        if (slot[i] < 0) continue;
-        U *g = reinterpret_cast<U *>(array + slot[i] * row_bytes) + c;
-        U *s = reinterpret_cast<U *>(stage + (int64_t)i * row_bytes) + c;
+    for (uint32_t e = threadIdx.x; e < T * per; e += kCpThreads) {
+        const uint32_t i = magic ? __umulhi(e, magic) : e / per, c = e - i * per;
+        const int64_t at = slot[i];
+        if (at < 0) continue;
+        U *g = reinterpret_cast<U *>(array + at * row_bytes) + c;
+        U *s = reinterpret_cast<U *>(stage) + e;  // rows of the stage follow one another
         if constexpr (READ && UNIT == 16)
             cp_async16(s, g);
+        else if constexpr (READ && UNIT == 4)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s)), "l"(g) : "memory");
         else if constexpr (READ)
             *s = __ldcg(g);
         else
@@ -320,92 +395,71 @@ __device__ __forceinline__ void move_all(const CompactParams &p, uint8_t *stage,
 {
     for (int a = 0; a < p.n_arrays; ++a) {
         if (p.unit[a] == 16)
-            move_rows<16, READ>(p.array[a], p.row_bytes[a], stage + p.offset[a], slot, p.T);
+            move_rows<16, READ>(p.array[a], p.row_bytes[a], p.per[a], p.magic[a], stage + p.offset[a], slot, p.T);
         else if (p.unit[a] == 4)
-            move_rows<4, READ>(p.array[a], p.row_bytes[a], stage + p.offset[a], slot, p.T);
+            move_rows<4, READ>(p.array[a], p.row_bytes[a], p.per[a], p.magic[a], stage + p.offset[a], slot, p.T);
         else
-            move_rows<1, READ>(p.array[a], p.row_bytes[a], stage + p.offset[a], slot, p.T);
+            move_rows<1, READ>(p.array[a], p.row_bytes[a], p.per[a], p.magic[a], stage + p.offset[a], slot, p.T);
     }
 }
 
 __global__ void __launch_bounds__(kCpThreads) evict_compact_kernel(CompactParams p)
 {
     extern __shared__ __align__(16) uint8_t stage[];
-    __shared__ int64_t src[kCpMaxT], dst[kCpMaxT];  // slots of the chunk's rows; -1: does not move
-    __shared__ int s_ticket, s_timeout;
+    __shared__ Chunk chunk[2];
+    __shared__ int next_ticket, timed_out;
     const int tid = threadIdx.x;
-    const int n_tickets = p.B * p.chunks;
-    if (tid == 0) s_timeout = 0;
-    for (;;) {
-        __syncthreads();  // the stage and the slot lists are free
-        if (tid == 0) s_ticket = atomicAdd(p.ticket, 1);
-        __syncthreads();
-        const int ticket = s_ticket;
-        if (ticket >= n_tickets) return;
-        // tickets go round the requests first: a chunk's predecessors are then well ahead of it
-        const int c = ticket / p.B, b = ticket - c * p.B;
-        const int old = p.old_len[b], n = p.new_len[b];
-        const bool bad = old < 0 || old > p.max_len || n < 0 || n > old || n > p.budget;
-        if (bad && tid == 0 && c == 0) set_status(p.status, NSA_ERR_BOUNDS);
-        const int lo = c * p.T, hi = min(old, lo + p.T);
-        if (bad || n == old || lo >= (p.total ? old : n)) continue;  // uniform over the CTA
-        const int32_t *keep = p.keep + (int64_t)b * p.keep_ld;
-        const int32_t *pt = p.page_table + (int64_t)b * p.pt_ld;
-        float *total = p.total ? p.total + (int64_t)b * p.total_ld : nullptr;
-        float t = 0.f;  // the total that moves to (or, past the kept rows, clears) position lo + tid
-        if (tid < p.T) {
-            const int i = lo + tid;
-            int64_t s = -1, d = -1;
-            if (i < n) {
-                const int k = keep[i];
-                if (k < i || k >= old || (i > 0 && keep[i - 1] >= k)) {
-                    set_status(p.status, NSA_ERR_BOUNDS);  // not an ascending list of positions
-                    if (total) t = __ldcg(total + i);
-                } else {
-                    if (total) t = __ldcg(total + k);
-                    if (k != i && p.n_arrays > 0) {
-                        const int32_t ps = pt[k / p.page_size], pd = pt[i / p.page_size];
-                        if (ps < 0 || ps >= p.num_pages || pd < 0 || pd >= p.num_pages) {
-                            set_status(p.status, NSA_ERR_BOUNDS);
-                        } else {
-                            s = (int64_t)ps * p.page_size + k % p.page_size;
-                            d = (int64_t)pd * p.page_size + i % p.page_size;
-                        }
-                    }
-                }
-            }
-            src[tid] = s;
-            dst[tid] = d;
+    const int n_tickets = p.B * (p.chunks + p.tails);
+    if (tid == 0) {
+        timed_out = 0;
+        next_ticket = atomicAdd(p.ticket, 1);
+    }
+    __syncthreads();
+    int ticket = next_ticket;
+    if (ticket < n_tickets) describe(p, chunk[0], ticket);
+    for (int it = 0; ticket < n_tickets; ++it) {
+        __syncthreads();  // the chunk is described, the stage free, next_ticket read
+        const Chunk &k = chunk[it & 1];
+        // a ticket held while this chunk is worked on: it is higher than this one, so no wait on it is circular
+        if (tid == 0) next_ticket = atomicAdd(p.ticket, 1);
+        float t = 0.f;
+        float *total = p.total ? p.total + (int64_t)k.b * p.total_ld : nullptr;
+        if (k.run && k.c >= 0) {
+            move_all<true>(p, stage, k.src);
+            if (total && tid < p.T && k.from[tid] >= 0) t = __ldcg(total + k.from[tid]);
         }
-        __syncthreads();
-        move_all<true>(p, stage, src);
         cp_async_commit();
-        // while the rows are under way: rows j0 .. j1-1 are those read from this chunk's range
-        const int j0 = block_lower_bound(keep, n, lo), j1 = block_lower_bound(keep, n, hi);
+        __syncthreads();
+        ticket = next_ticket;
+        if (ticket < n_tickets) describe(p, chunk[(it + 1) & 1], ticket);  // while the rows are on their way
+        if (!k.run) continue;
         cp_async_wait_all();
         __syncthreads();  // every thread's reads (rows and totals) have arrived
-        int32_t *done = p.read_done + (int64_t)b * p.chunks;
-        if (tid == 0) {
+        int32_t *done = p.read_done + (int64_t)k.b * p.chunks;
+        if (tid == 0 && k.c >= 0) {
             __threadfence();
-            st_release(done + c, 1);
-            if (j1 > j0) {
-                for (int x = j0 / p.T; x <= (j1 - 1) / p.T && x < c; ++x) {
-                    const long long t0 = clock64();
-                    while (!ld_acquire(done + x)) {
-                        if (clock64() - t0 > kCpWait) {
-                            set_status(p.status, NSA_ERR_TIMEOUT);
-                            s_timeout = 1;
-                            break;
-                        }
-                        __nanosleep(64);
-                    }
+            st_release(done + k.c, 1);
+        }
+        const int w1 = k.c >= 0 ? min(k.w1, k.c) : k.w1;  // later chunks read behind this one's destination
+        for (int x = k.w0 + tid; x < w1; x += kCpThreads) {
+            const long long t0 = clock64();
+            while (!ld_acquire(done + x)) {
+                if (clock64() - t0 > kCpWait) {
+                    set_status(p.status, NSA_ERR_TIMEOUT);
+                    timed_out = 1;
+                    break;
                 }
+                __nanosleep(32);
             }
         }
         __syncthreads();
-        if (s_timeout) return;  // rows that another chunk may not have read are left as they are
-        move_all<false>(p, stage, dst);
-        if (total && tid < p.T && lo + tid < hi) total[lo + tid] = t;
+        if (timed_out) return;  // rows that another chunk may not have read are left as they are
+        if (k.c >= 0) {
+            move_all<false>(p, stage, k.dst);
+            if (total && tid < p.T && k.from[tid] >= 0) total[k.lo + tid] = t;
+        } else {
+            for (int i = k.lo + tid; i < k.hi; i += kCpThreads) total[i] = 0.f;
+        }
     }
 }
 
@@ -430,12 +484,9 @@ extern "C" nsa_status nsa_evict_select(const float *total_dev, int64_t total_ld,
     while (nc < kSelMaxCluster && (int64_t)nc * kSelSlice < max_len) nc *= 2;
     if ((int64_t)B * nc > 0x7fffffffLL) return NSA_ERR_UNSUPPORTED;
     const int slice = max_len > 0 ? (int)ceil_div(max_len, nc) : 1;
-    const int cached = slice <= kSelCache ? 1 : 0;
-    NSA_CUDA_TRY(cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCache * 4));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(B * nc));
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = cached ? (size_t)slice * 4 : 0;
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -444,8 +495,9 @@ extern "C" nsa_status nsa_evict_select(const float *total_dev, int64_t total_ld,
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, evict_select_kernel, total_dev, total_ld, len_dev, max_len, sinks, recent,
-                                    budget, slice, cached, keep_dev, keep_ld, new_len_dev, status_dev));
+    auto kern = slice <= kSelSlice ? evict_select_kernel<true> : evict_select_kernel<false>;
+    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, total_dev, total_ld, len_dev, max_len, sinks, recent, budget, slice,
+                                    keep_dev, keep_ld, new_len_dev, status_dev));
     return NSA_OK;
 }
 
@@ -493,6 +545,9 @@ extern "C" nsa_status nsa_evict_compact(int B, const int32_t *keep_dev, int64_t 
         p.row_bytes[a] = (int)row_bytes[a];
         const uintptr_t both = (uintptr_t)arrays_dev[a] | (uintptr_t)row_bytes[a];
         p.unit[a] = both % 16 == 0 ? 16 : both % 4 == 0 ? 4 : 1;
+        p.per[a] = (uint32_t)(row_bytes[a] / p.unit[a]);
+        // exact while step * per < 2^32, which short rows keep (at most kCpMinT * kCpMaxRow steps)
+        p.magic[a] = p.per[a] > 1 && p.per[a] < 4096 ? (uint32_t)((0x100000000ULL + p.per[a] - 1) / p.per[a]) : 0;
         p.offset[a] = (int)stage;
         stage += ceil_div(p.T * row_bytes[a], 16) * 16;
     }
@@ -502,8 +557,12 @@ extern "C" nsa_status nsa_evict_compact(int B, const int32_t *keep_dev, int64_t 
     p.page_table = page_table_dev; p.pt_ld = pt_ld; p.page_size = page_size; p.num_pages = num_pages;
     p.max_len = max_len; p.budget = budget;
     p.total = total_dev; p.total_ld = total_ld;
-    p.chunks = (int)ceil_div(max_len, p.T); p.B = B;
-    if ((int64_t)B * p.chunks > 0x7fffffffLL - 0x100000) return NSA_ERR_UNSUPPORTED;
+    p.chunks = (int)ceil_div(budget < max_len ? budget : max_len, p.T);
+    p.tails = total_dev ? (int)ceil_div(max_len, kCpTail) : 0;
+    p.B = B;
+    const int64_t tickets = (int64_t)B * (p.chunks + p.tails);
+    if (tickets > 0x7fffffffLL - 0x100000) return NSA_ERR_UNSUPPORTED;
+    if (tickets == 0) return NSA_OK;
     p.ticket = (int32_t *)workspace_dev;
     p.read_done = p.ticket + 4;
     p.status = status_dev;
@@ -511,9 +570,8 @@ extern "C" nsa_status nsa_evict_compact(int B, const int32_t *keep_dev, int64_t 
     if (sms <= 0) return NSA_ERR_CUDA;
     const cudaStream_t s = (cudaStream_t)stream;
     NSA_CUDA_TRY(cudaMemsetAsync(workspace_dev, 0, 16 + (size_t)B * p.chunks * sizeof(int32_t), s));
-    NSA_CUDA_TRY(cudaFuncSetAttribute(evict_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      kCpMinT * kCpMaxRow));
-    const int64_t tickets = (int64_t)B * p.chunks, most = (int64_t)sms * 4;
+    NSA_CUDA_TRY(max_dynamic_smem<evict_compact_kernel>(kCpMinT * kCpMaxRow));
+    const int64_t most = (int64_t)sms * kCpPerSm;
     evict_compact_kernel<<<(unsigned)(tickets < most ? tickets : most), kCpThreads, (size_t)stage, s>>>(p);
     return launch_status();
 }

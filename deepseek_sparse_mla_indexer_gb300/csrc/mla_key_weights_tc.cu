@@ -379,10 +379,10 @@ nsa_status key_weights_tc_try_launch(const PagedMlaArgs &a, const float *lse, fl
     const int64_t tiles = (int64_t)p.t.B * ceil_div(a.max_row_len, kPtTok);
     const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
     if (fp8) {
-        NSA_CUDA_TRY(cudaFuncSetAttribute(key_weights_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448));
+        NSA_CUDA_TRY(max_dynamic_smem<key_weights_tc_kernel<true>>(232448));
         key_weights_tc_kernel<true><<<grid, 256 + kDqThreads, smem, stream>>>(p, qn, qr, kv);
     } else {
-        NSA_CUDA_TRY(cudaFuncSetAttribute(key_weights_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448));
+        NSA_CUDA_TRY(max_dynamic_smem<key_weights_tc_kernel<false>>(232448));
         key_weights_tc_kernel<false><<<grid, 256, smem, stream>>>(p, qn, qr, kv);
     }
     return launch_status();

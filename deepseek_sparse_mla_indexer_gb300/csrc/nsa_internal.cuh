@@ -6,6 +6,8 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/nsa.h"
 
 #define NSA_CUDA_TRY(expr)                                   \
@@ -86,6 +88,21 @@ inline int current_sm_count()
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
     return n > 0 ? n : 0;
+}
+
+// Allows `Kern` that much dynamic shared memory, asked of the runtime once per device.
+template <auto Kern>
+inline cudaError_t max_dynamic_smem(int bytes)
+{
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> allowed[kMaxDev];
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDev && allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    const cudaError_t f = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (f == cudaSuccess && dev < kMaxDev) allowed[dev].store(bytes, std::memory_order_relaxed);
+    return f;
 }
 
 inline nsa_status launch_status()

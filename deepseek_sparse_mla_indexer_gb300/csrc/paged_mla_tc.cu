@@ -73,7 +73,7 @@ struct AParams {
     int slot_cols;                 // columns of a partial slot
     __nv_bfloat16 *out;
     float *lse;
-    int64_t *head;                 // [B + 1] tiles of the requests before b
+    int4 *unit;                    // [B * mult] of each (request, group set): first and last share, whether the first began earlier
     float *part;                   // [2 * CTAs][slot_cols][512] raw accumulators
     float2 *part_ml;               // [2 * CTAs][slot_cols] maximum (log2 units) and sum
 };
@@ -326,7 +326,15 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             }
             __syncwarp();
         } else if (warp == 2 && blockIdx.x == 0) {
-            // -------------------------------------------------------- where each request's tiles start, for the join
+            // -------------------------------------------------------- the shares of every unit, for the join
+            const int64_t total = sm->share.total, np = share_count(total, p.teams);
+            // share k is [total * k / np, total * (k + 1) / np)
+            auto share_of = [&](int64_t g) -> int {
+                int k = (int)(g * np / total);
+                while (k + 1 < np && total * (k + 1) / np <= g) ++k;
+                while (k > 0 && total * k / np > g) --k;
+                return k;
+            };
             int64_t before = 0;
             for (int base = 0; base < p.t.B; base += 32) {
                 const int b = base + lane;
@@ -337,10 +345,20 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
                     if (lane >= o) inc += x;
                 }
-                if (b < p.t.B) p.head[b] = before + inc - v;
+                if (b < p.t.B) {
+                    int64_t u0 = (before + inc - v) * p.mult;
+                    for (int j = 0; j < p.mult; ++j, u0 += v) {
+                        int4 u = make_int4(0, 0, 0, 0);
+                        if (v > 0) {
+                            u.x = share_of(u0);
+                            u.y = share_of(u0 + v - 1);
+                            u.z = total * u.x / np < u0 ? 1 : 0;
+                        }
+                        p.unit[(int64_t)b * p.mult + j] = u;
+                    }
+                }
                 before += __shfl_sync(0xffffffffu, inc, 31);
             }
-            if (lane == 0) p.head[p.t.B] = before;
         } else if (warp == 3) {
             // -------------------------------------------------------- requests without a key
             for (int b = blockIdx.x; b < p.t.B; b += gridDim.x) {
@@ -612,73 +630,82 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
 
 // Columns that several shares worked on: with M the largest maximum,
 //   l = sum_q l_q 2^(m_q - M), out = sum_q O_q 2^(m_q - M) / l, lse = (M + log2 l) ln 2,
-// in share order.  One CTA per column, four quarters of the shares at a time.
-constexpr int kJoinThreads = 512;
+// in share order.  W warps a column (each a quarter, say, of the shares), 16 values of
+// the latent a lane; one warp where requests are split in few shares, eight where one
+// request is spread over the whole GPU.
+constexpr int kJoinThreads = 256;
 
+template <int W>
 __global__ void __launch_bounds__(kJoinThreads) paged_mla_join_kernel(AParams p)
 {
-    __shared__ float4 acc_s[3][128];
-    __shared__ float wl[kJoinThreads / 32], wm[kJoinThreads / 32];
-    const int64_t row = blockIdx.x;
+    __shared__ float4 acc_s[W > 1 ? W - 1 : 1][128];
+    __shared__ float wl[W];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * (kJoinThreads / 32 / W) + warp / W;
+    if (row >= (int64_t)p.t.B * p.cols) return;  // only with W == 1: whole warps leave, no barrier follows
     const int b = (int)(row / p.cols), c = (int)(row - (int64_t)b * p.cols);
-    const int64_t before = p.head[b], tiles = p.head[b + 1] - before, total = p.head[p.t.B] * p.mult;
-    if (tiles == 0) return;
     const int group = c / p.nc, set = group / p.team, rank = group - set * p.team, cc = c - group * p.nc;
-    const int64_t u0 = before * p.mult + set * tiles, u1 = u0 + tiles;  // the unit's tiles among all
-    const int64_t np = share_count(total, p.teams);  // share k is [total * k / np, total * (k + 1) / np)
-    auto share_of = [&](int64_t g) -> int {
-        int k = (int)(g * np / total);
-        while (k + 1 < np && total * (k + 1) / np <= g) ++k;
-        while (k > 0 && total * k / np > g) --k;
-        return k;
+    const int4 unit = p.unit[(int64_t)b * p.mult + set];  // its shares x .. y; z: share x started before it
+    const int ns = unit.y - unit.x + 1;
+    if (ns <= 1) return;  // one share had it whole, or there is no key (uniform over the block when W > 1)
+    auto slot_of = [&](int q) -> int64_t {
+        return (((int64_t)(unit.x + q) * p.team + rank) * 2 + (q == 0 ? unit.z : 0)) * p.slot_cols + cc;
     };
-    const int k0 = share_of(u0), k1 = share_of(u1 - 1);
-    if (k0 == k1) return;  // one share had it whole
-    auto slot_of = [&](int k) -> int64_t {
-        const int64_t g0 = total * k / np;
-        const int64_t slot = ((int64_t)k * p.team + rank) * 2 + (g0 >= u0 ? 0 : 1);  // its first piece, or its last
-        return slot * p.slot_cols + cc;
-    };
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int ns = k1 - k0 + 1;
     float m = -INFINITY;
-    for (int q = tid; q < ns; q += kJoinThreads) m = fmaxf(m, p.part_ml[slot_of(k0 + q)].x);
+    for (int q = lane; q < ns; q += 32) m = fmaxf(m, p.part_ml[slot_of(q)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) wm[warp] = m;
-    __syncthreads();
-    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, wm[w]);
-    const int part = tid >> 7, d4 = tid & 127;
-    const int per = (ns + 3) / 4, q0 = min(ns, part * per), q1 = min(ns, q0 + per);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int part = W > 1 ? warp : 0, per = (ns + W - 1) / W, q0 = min(ns, part * per), q1 = min(ns, q0 + per);
+    float4 acc[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
-#pragma unroll 4
+#pragma unroll 2
     for (int q = q0; q < q1; ++q) {
-        const int64_t s = slot_of(k0 + q);
+        const int64_t s = slot_of(q);
         const float2 ml = p.part_ml[s];
-        const float4 v = *reinterpret_cast<const float4 *>(p.part + s * kPtDl + 4 * d4);
+        const float4 *src = reinterpret_cast<const float4 *>(p.part + s * kPtDl) + lane;
         // a share whose keys were all masked has maximum -inf and zeros
         const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
         l += w * ml.y;
-        acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
-    }
-    if (d4 == 0) wl[part] = l;
-    if (part > 0) acc_s[part - 1][d4] = acc;
-    __syncthreads();
-    if (part == 0) {
-        l = ((wl[0] + wl[1]) + wl[2]) + wl[3];
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
-            const float4 v = acc_s[x][d4];
-            acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+        for (int x = 0; x < 4; ++x) {
+            const float4 v = __ldcg(src + 32 * x);
+            acc[x].x += w * v.x; acc[x].y += w * v.y; acc[x].z += w * v.z; acc[x].w += w * v.w;
         }
-        const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-        __nv_bfloat16 *o = p.out + row * kPtDl + 4 * d4;
-        const float r[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[x] = __float2bfloat16_rn(r[x]);
-        if (d4 == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == l ? -INFINITY : l);
     }
+    if constexpr (W > 1) {
+        if (lane == 0) wl[part] = l;
+        if (part > 0) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc_s[part - 1][lane + 32 * x] = acc[x];
+        }
+        __syncthreads();
+        if (part > 0) return;
+        l = 0.f;
+        for (int w = 0; w < W; ++w) l += wl[w];
+        for (int w = 0; w < W - 1; ++w) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float4 v = acc_s[w][lane + 32 * x];
+                acc[x].x += v.x; acc[x].y += v.y; acc[x].z += v.z; acc[x].w += v.w;
+            }
+        }
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    __nv_bfloat16 *o = p.out + row * kPtDl + 4 * lane;
+    const bool wide = ((uintptr_t)p.out & 7) == 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const uint2 v = make_uint2(pack2(acc[x].x * inv, acc[x].y * inv), pack2(acc[x].z * inv, acc[x].w * inv));
+        if (wide) {
+            *reinterpret_cast<uint2 *>(o + 128 * x) = v;
+        } else {
+            const __nv_bfloat16 *e = reinterpret_cast<const __nv_bfloat16 *>(&v);
+            for (int y = 0; y < 4; ++y) o[128 * x + y] = e[y];
+        }
+    }
+    if (lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == l ? -INFINITY : l);
 }
 
 // How the columns of a request are spread over CTAs: teams of the largest power of two
@@ -703,7 +730,7 @@ Plan make_plan(int R, int n, int H, int max_row_len, int sms)
     q.teams = (int)(most < fit ? most : fit);
     q.slot_cols = q.cols < kCols ? q.cols : kCols;
     const size_t slots = (size_t)q.teams * q.team * 2 * q.slot_cols;
-    q.head_bytes = ((size_t)(R / n + 1) * sizeof(int64_t) + 15) / 16 * 16;
+    q.head_bytes = (size_t)(R / n) * q.mult * sizeof(int4);
     q.ml_bytes = (slots * sizeof(float2) + 15) / 16 * 16;
     q.part_bytes = slots * kPtDl * sizeof(float);
     return q;
@@ -712,13 +739,17 @@ Plan make_plan(int R, int n, int H, int max_row_len, int sms)
 template <bool FP8, bool PAIR, int NC>
 nsa_status launch(const AParams &p, const CUtensorMap &qn, const CUtensorMap &qr, const CUtensorMap &kv, cudaStream_t stream)
 {
-    auto kern = paged_mla_tc_kernel<FP8, PAIR, NC>;
-    NSA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+    constexpr auto kern = paged_mla_tc_kernel<FP8, PAIR, NC>;
+    NSA_CUDA_TRY(max_dynamic_smem<kern>((int)kSmem));
     if (FP8) {
         // the register split needs the registers the kernel was compiled to be launched with
-        cudaFuncAttributes fa;
-        NSA_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
-        if (fa.numRegs < kRegsLaunch) return NSA_ERR_UNSUPPORTED;
+        static std::atomic<int> regs{0};
+        if (regs.load(std::memory_order_relaxed) == 0) {
+            cudaFuncAttributes fa;
+            NSA_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
+            regs.store(fa.numRegs, std::memory_order_relaxed);
+        }
+        if (regs.load(std::memory_order_relaxed) < kRegsLaunch) return NSA_ERR_UNSUPPORTED;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.teams * p.team));
@@ -733,7 +764,12 @@ nsa_status launch(const AParams &p, const CUtensorMap &qn, const CUtensorMap &qr
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, qn, qr, kv));
-    paged_mla_join_kernel<<<(unsigned)((int64_t)p.t.B * p.cols), kJoinThreads, 0, stream>>>(p);
+    // shares per request on average: below four, a warp joins a column faster than a block (both measured)
+    const int64_t rows = (int64_t)p.t.B * p.cols;
+    if (p.teams < 4 * (int64_t)p.t.B * p.mult)
+        paged_mla_join_kernel<1><<<(unsigned)ceil_div(rows, kJoinThreads / 32), kJoinThreads, 0, stream>>>(p);
+    else
+        paged_mla_join_kernel<8><<<(unsigned)rows, kJoinThreads, 0, stream>>>(p);
     return launch_status();
 }
 
@@ -763,7 +799,7 @@ nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse,
     p.cols = q.cols; p.nc = q.nc; p.groups = q.groups; p.team = q.team; p.mult = q.mult; p.teams = q.teams; p.slot_cols = q.slot_cols;
     p.out = (__nv_bfloat16 *)out;
     p.lse = lse;
-    p.head = (int64_t *)workspace;
+    p.unit = (int4 *)workspace;
     p.part_ml = (float2 *)((uint8_t *)workspace + q.head_bytes);
     p.part = (float *)((uint8_t *)workspace + q.head_bytes + q.ml_bytes);
     CUtensorMap qn, qr, kv = {};
