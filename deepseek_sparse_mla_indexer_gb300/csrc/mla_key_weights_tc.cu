@@ -16,7 +16,8 @@
 // One CTA per SM, persistent; the tiles of all requests are cut into equal shares.
 // Roles: warp 0 issues TMA loads of Q and (bf16) of the tiles' blocks into a ring of
 // 16 KB stages; warp 1 issues the MMAs into two TMEM buffers; warps 4..7 are the
-// epilogue; with fp8 rows warps 8..23 expand them into the ring instead of TMA.
+// epilogue; fp8 rows come raw into slots of their own, from which warps 8..23 expand
+// them into the ring.
 #include <cstddef>
 
 #include "mla_key_weights_tc.cuh"
@@ -35,6 +36,7 @@ constexpr uint32_t kTmemCols = 256;
 struct WShared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full, q_empty, s_full[2], s_empty[2];
+    RawShared raw;
     float lse2[kCols];   // lse in log2 units; +inf: no weight (padding, an empty row)
     int len[kCols];      // positions the column's row sees
     int min_len[4];
@@ -50,6 +52,7 @@ struct WParams {
     float *total;
     int64_t total_ld;
     int cols, passes, N, stages;  // columns per request, passes, MMA columns of a pass, ring stages
+    int raw;                      // fp8: slots of raw codes
 };
 
 // The tiles of a share as (request, pass, tile range) pieces, the same for every role.
@@ -98,13 +101,16 @@ struct Walk {
 template <bool FP8>
 __global__ void __launch_bounds__(FP8 ? 256 + kDqThreads : 256, 1)
 key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
-                      const __grid_constant__ CUtensorMap kv_map)
+                      const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
+                      const __grid_constant__ CUtensorMap rope_map)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *q_s = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t q_blk = (uint32_t)p.N * 128;
     uint8_t *ring = q_s + 9 * q_blk;
-    WShared *sm = (WShared *)(ring + (size_t)p.stages * kPtBlk);
+    uint8_t *raw_s = ring + (size_t)p.stages * kPtBlk;     // fp8: raw codes, then the scales of two tiles
+    uint8_t *sc_s = raw_s + (FP8 ? p.raw * kRawSlot : 0);
+    WShared *sm = (WShared *)(sc_s + (FP8 ? 2 * kScaleSlot : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nst = p.stages;
 
@@ -112,6 +118,10 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
         for (int i = 0; i < nst; ++i) {
             mbar_init(&sm->full[i], FP8 ? kDqThreads / 32 : 1);
             mbar_init(&sm->empty[i], 1);
+        }
+        for (int i = 0; i < kMaxRaw; ++i) {
+            mbar_init(&sm->raw.full[i], 1);
+            mbar_init(&sm->raw.empty[i], kDqThreads / 32);
         }
         mbar_init(&sm->q_full, 1);
         mbar_init(&sm->q_empty, 1);
@@ -143,46 +153,75 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
         if (work) {
             const int boxes = kPtTok / p.t.box_rows;  // at most 16, one a lane
             const uint32_t box_bytes = (uint32_t)p.t.box_rows * 128;
-            int st = 0, uses = 0;
-            uint32_t ph = 0;
-            auto stop = [&]() { return __any_sync(0xffffffffu, sm->abort) != 0; };  // one answer for the warp
-            for (bool more = true; more && !stop(); more = w.next(p)) {
-                if (lane == 0) {
-                    if (uses > 0 && !mbar_wait(&sm->q_empty, (uses - 1) & 1, kPtWait)) fail();
+            int st = 0;
+            uint32_t ph = 0, uses = 0, tile = 0;
+            bool ok = true;
+            for (bool more = true; more && ok; more = w.next(p)) {
+                if (uses > 0 && !mbar_wait(&sm->q_empty, (uses - 1) & 1, kPtWait)) ok = false;
+                const int row = w.b * p.cols + w.pass * kCols;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&sm->q_full, 9 * q_blk);
-                    const int row = w.b * p.cols + w.pass * kCols;
                     for (int c = 0; c < 8; ++c) tma_load_2d(q_s + c * q_blk, &qn_map, 64 * c, row, &sm->q_full);
                     tma_load_2d(q_s + 8 * q_blk, &qr_map, 0, row, &sm->q_full);
                 }
+                __syncwarp();
                 ++uses;
-                if (!FP8) {
-                    const int32_t *pt = p.t.page_table + (int64_t)w.b * p.t.pt_ld;
-                    for (int t = w.c0; t < w.c1; ++t) {
-                        const int pos = t * kPtTok + lane * p.t.box_rows;
-                        const int page = lane < boxes ? checked_page(p.t, pt, pos, w.len) : -1;
-                        const int y = page < 0 ? 0 : (int)((int64_t)page * p.t.ps + pos % p.t.ps);
-                        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box_bytes;
-                        int c = 0;
-                        for (; c < 9; ++c) {
-                            if (lane == 0 && !mbar_wait(&sm->empty[st], ph ^ 1, kPtWait)) fail();
-                            if (stop()) break;
-                            if (lane == 0) mbar_arrive_expect_tx(&sm->full[st], bytes);
+                const int32_t *pt = p.t.page_table + (int64_t)w.b * p.t.pt_ld;
+                auto box_row = [&](int t) -> int {  // row of this lane's box of tile t, or -1
+                    const int pos = t * kPtTok + lane * p.t.box_rows;
+                    const int page = lane < boxes && t < w.c1 ? checked_page(p.t, pt, pos, w.len) : -1;
+                    return page < 0 ? -1 : page * p.t.ps + pos % p.t.ps;
+                };
+                int y = box_row(w.c0);
+                for (int t = w.c0; t < w.c1 && ok; ++t, ++tile) {
+                    const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
+                    const uint32_t bytes = __popc(live) * box_bytes;
+                    const int y_first = __shfl_sync(0xffffffffu, y, 0);
+                    const int y_next = box_row(t + 1);  // its latency under this tile's waits
+                    // one lane issues a box at a time from uniform registers
+                    auto boxes_of = [&](auto issue) {
+                        int yb = y_first;
+                        for (int x = 0; x < boxes; ++x) {
+                            if (x > 0) yb = __shfl_sync(0xffffffffu, y, x);
+                            if (yb >= 0 && elect_one()) issue(x, yb);
                             __syncwarp();
-                            if (page >= 0)
-                                tma_load_2d(ring + st * kPtBlk + lane * box_bytes, &kv_map, 64 * c, y, &sm->full[st]);
-                            if (++st == nst) {
-                                st = 0;
-                                ph ^= 1;
-                            }
                         }
-                        if (c < 9) break;
+                    };
+                    for (int c = 0; c < (FP8 ? 5 : 9); ++c) {
+                        uint64_t *full = FP8 ? sm->raw.full : sm->full, *empty = FP8 ? sm->raw.empty : sm->empty;
+                        if (!mbar_wait(&empty[st], ph ^ 1, kPtWait)) ok = false;
+                        if (elect_one()) {
+                            if (FP8 && c == 0) sm->raw.boxes[tile & 1] = live;
+                            mbar_arrive_expect_tx(&full[st], bytes + (FP8 && c == 0 ? bytes / 8 : 0));
+                        }
+                        __syncwarp();
+                        boxes_of([&](int x, int yb) {
+                            if (!FP8) {
+                                tma_load_2d(ring + st * kPtBlk + x * box_bytes, &kv_map, 64 * c, yb, &full[st]);
+                            } else if (c < 4) {
+                                tma_load_2d(raw_s + st * kRawSlot + x * box_bytes, &kv_map, 128 * c, yb, &full[st]);
+                                if (c == 0)
+                                    tma_load_2d(sc_s + (tile & 1) * kScaleSlot + x * (box_bytes / 8), &sc_map, kPtDl, yb,
+                                                &full[st]);
+                            } else {
+                                tma_load_2d(raw_s + st * kRawSlot + x * box_bytes, &rope_map, kFp8RopeX, yb, &full[st]);
+                            }
+                        });
+                        if (++st == (FP8 ? p.raw : nst)) {
+                            st = 0;
+                            ph ^= 1;
+                        }
                     }
+                    y = y_next;
+                    ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
                 }
+                ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
             }
-            // nothing is in flight at the end: stages before st were filled last with phase ph, the others before
+            if (!ok && lane == 0) fail();
+            // nothing is in flight at the end: slots before st were filled last with phase ph, the others before
             if (lane == 0) {
-                if (!FP8)
-                    for (int i = 0; i < nst; ++i) mbar_wait(&sm->full[i], i < st ? ph : ph ^ 1, kPtWait);
+                for (int i = 0; i < (FP8 ? p.raw : nst); ++i)
+                    mbar_wait(FP8 ? &sm->raw.full[i] : &sm->full[i], i < st ? ph : ph ^ 1, kPtWait);
                 mbar_wait(&sm->q_full, (uses - 1) & 1, kPtWait);
             }
             __syncwarp();
@@ -292,57 +331,66 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
             }
         }
     } else if (FP8 && warp >= 8) {
-        // ------------------------------------------------------------ fp8 rows into the ring
+        // ------------------------------------------------------------ raw rows expanded into the ring
         if (work) {
             const int d = threadIdx.x - 256;
-            Fp8Rows x;
-            int st = 0;
-            uint32_t ph = 0;
-            x.set_rows(p.t, d, w.b, w.c0, w.len);
-            x.load<0>(p.t, d); x.load<1>(p.t, d); x.load<2>(p.t, d); x.load<3>(p.t, d); x.load<4>(p.t, d);
-            bool more = true;
-            int t = w.c0;
-            auto slot = [&]() -> uint8_t * {
-                if (!mbar_wait(&sm->empty[st], ph ^ 1, kPtWait)) fail();
-                return ring + st * kPtBlk;
-            };
-            auto release = [&]() {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->full[st]);
+            int st = 0, rs = 0;
+            uint32_t ph = 0, rph = 0, tile = 0;
+            bool ok = true;
+            auto stage = [&]() -> uint8_t * {  // the next stage once it is empty
+                if (!mbar_wait(&sm->empty[st], ph ^ 1, kPtWait)) ok = false;
+                uint8_t *at = ring + st * kPtBlk;
                 if (++st == nst) {
                     st = 0;
                     ph ^= 1;
                 }
+                return at;
             };
-            // the step's one or two stages, then its registers for the next tile
-            auto peek2 = [&]() -> uint8_t * {
-                const int s2 = st + 1 == nst ? 0 : st + 1;
-                const uint32_t p2 = st + 1 == nst ? ph ^ 1 : ph;
-                if (!mbar_wait(&sm->empty[s2], p2 ^ 1, kPtWait)) fail();
-                return ring + s2 * kPtBlk;
-            };
-            while (more) {
-                if (++t >= w.c1) {
-                    more = w.next(p);
-                    t = w.c0;
+            for (bool more = true; more && ok; more = w.next(p)) {
+                for (int t = w.c0; t < w.c1 && ok; ++t, ++tile) {
+                    uint32_t live = 0;
+                    const float *scales = reinterpret_cast<const float *>(sc_s + (tile & 1) * kScaleSlot);
+#pragma unroll 1
+                    for (int m = 0; m < 5; ++m) {
+                        if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;
+                        if (m == 0) live = live_rows(p.t, sm->raw.boxes[tile & 1], d, t, w.len);
+                        RawStep x;
+                        x.read(raw_s + rs * kRawSlot, scales, m & 3, d, live);
+                        const int s0 = st;
+                        uint8_t *blk0 = stage();
+                        if (m < 4) {
+                            const int s1 = st;
+                            uint8_t *blk1 = stage();
+                            x.store(d, blk0, blk1);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(&sm->raw.empty[rs]);
+                                mbar_arrive(&sm->full[s0]);
+                                mbar_arrive(&sm->full[s1]);
+                            }
+                        } else {
+                            // the rope part lies in its slot as the operand wants it (swizzled): moved as it is
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+                                *reinterpret_cast<uint4 *>(blk0 + ((d >> 3) + 64 * u) * 128 + 16 * (d & 7)) = x.w[u];
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(&sm->raw.empty[rs]);
+                                mbar_arrive(&sm->full[s0]);
+                            }
+                        }
+                        if (++rs == p.raw) {
+                            rs = 0;
+                            rph ^= 1;
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
                 }
-                if (more)
-                    x.set_rows(p.t, d, w.b, t, w.len);
-                else
-                    x.no_rows();
-                uint8_t *a = slot(), *b2 = peek2();
-                x.store<0>(d, a, b2); x.load<0>(p.t, d); release(); release();
-                a = slot(); b2 = peek2();
-                x.store<1>(d, a, b2); x.load<1>(p.t, d); release(); release();
-                a = slot(); b2 = peek2();
-                x.store<2>(d, a, b2); x.load<2>(p.t, d); release(); release();
-                a = slot(); b2 = peek2();
-                x.store<3>(d, a, b2); x.load<3>(p.t, d); release(); release();
-                a = slot();
-                x.store<4>(d, a, nullptr); x.load<4>(p.t, d); release();
-                if (__any_sync(0xffffffffu, sm->abort)) break;
+                ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
             }
+            if (!ok && lane == 0) fail();
         }
     }
 
@@ -371,19 +419,25 @@ nsa_status key_weights_tc_try_launch(const PagedMlaArgs &a, const float *lse, fl
     p.cols = a.rows_per_req * a.H;
     p.passes = (int)ceil_div(p.cols, kCols);
     p.N = p.passes > 1 ? kCols : (int)ceil_div(p.cols, 16) * 16;
-    const size_t q_bytes = (size_t)9 * p.N * 128, most = 232448 - 1024 - kAux - q_bytes;
-    p.stages = (int)(most / kPtBlk) < kMaxStages ? (int)(most / kPtBlk) : kMaxStages;
-    const size_t smem = 1024 + q_bytes + (size_t)p.stages * kPtBlk + kAux;
-    CUtensorMap qn, qr, kv = {};
-    if (!paged_tc_maps(a, p.t, (uint32_t)p.N, &qn, &qr, &kv)) return NSA_ERR_CUDA;
+    const size_t q_bytes = (size_t)9 * p.N * 128, left = 232448 - 1024 - kAux - q_bytes;
+    // fp8: about two raw slots to three stages (a step fills two), at least two of each
+    const int blocks = (int)((left - (fp8 ? 2 * kScaleSlot : 0)) / kPtBlk);
+    p.raw = fp8 ? (blocks >= 8 ? 4 : blocks >= 6 ? 3 : 2) : 0;
+    p.stages = blocks - p.raw < kMaxStages ? blocks - p.raw : kMaxStages;
+    const size_t smem = 1024 + q_bytes + (size_t)(p.stages + p.raw) * kPtBlk + (fp8 ? 2 * kScaleSlot : 0) + kAux;
+    CUtensorMap qn, qr, kv, sc = {}, rope = {};
+    if (!paged_tc_q_maps(a, (uint32_t)p.N, &qn, &qr)) return NSA_ERR_CUDA;
+    if (fp8 ? !fp8_maps(a, (uint32_t)p.t.box_rows, &kv, &sc, &rope)
+            : !bf16_rows_map(a.kv, (uint64_t)a.num_pages * a.page_size, (uint32_t)p.t.box_rows, &kv))
+        return NSA_ERR_CUDA;
     const int64_t tiles = (int64_t)p.t.B * ceil_div(a.max_row_len, kPtTok);
     const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
     if (fp8) {
         NSA_CUDA_TRY(max_dynamic_smem<key_weights_tc_kernel<true>>(232448));
-        key_weights_tc_kernel<true><<<grid, 256 + kDqThreads, smem, stream>>>(p, qn, qr, kv);
+        key_weights_tc_kernel<true><<<grid, 256 + kDqThreads, smem, stream>>>(p, qn, qr, kv, sc, rope);
     } else {
         NSA_CUDA_TRY(max_dynamic_smem<key_weights_tc_kernel<false>>(232448));
-        key_weights_tc_kernel<false><<<grid, 256, smem, stream>>>(p, qn, qr, kv);
+        key_weights_tc_kernel<false><<<grid, 256, smem, stream>>>(p, qn, qr, kv, sc, rope);
     }
     return launch_status();
 }

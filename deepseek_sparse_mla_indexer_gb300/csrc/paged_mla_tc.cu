@@ -34,20 +34,20 @@ namespace {
 using namespace sm100;
 
 constexpr int kCols = 64;                 // columns per CTA at most
-constexpr uint32_t kQBytes = 9 * kCols * 128, kKvBytes = 9 * kPtBlk;
+constexpr uint32_t kKvBytes = 9 * kPtBlk;
 constexpr uint32_t kColS = 256;           // S^T behind O^T's four blocks
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f;          // log2 units
 constexpr int kMaxTeam = 8;
-constexpr int kThreadsBf16 = 384, kThreadsFp8 = 384 + kDqThreads;
-// fp8: registers per thread at launch and per role (one control, two softmax and four row
-// warpgroups); the softmax needs two per column, the rest goes to the rows
-constexpr int kRegsLaunch = 72;
-template <int NC>
-struct Regs {
-    static constexpr int kCtl = NC == 64 ? 40 : 56, kSoftmax = NC == 64 ? 104 : 64, kRows = NC == 64 ? 64 : 80;
-    static_assert(kCtl + 2 * kSoftmax + 4 * kRows <= 7 * kRegsLaunch, "the split fits what the block has");
-};
+// How the tile's rows come: a bf16 cache by TMA; raw fp8 rows by TMA into slots beside the
+// tile and expanded from there; or fp8 rows expanded into the CTA's scratch in global memory
+// (half a tile for each CTA of a pair) and loaded from it as bf16 rows are.
+enum Rows { kBf16Rows, kRawRows, kScratchRows };
+constexpr int threads_of(Rows rows) { return rows == kBf16Rows ? 384 : 384 + (rows == kRawRows ? kDqThreads : kScrThreads); }
+// Registers per thread at launch and per role of the scratch kernel (one control, two softmax
+// and two row warpgroups): the softmax of 64 columns needs more than a fifth of the file.
+constexpr int kRegsLaunch = 96, kRegsCtl = 80, kRegsSoftmax = 120, kRegsRows = 80;
+static_assert(kRegsCtl + 2 * kRegsSoftmax + 2 * kRegsRows <= 5 * kRegsLaunch, "the split fits what the block has");
 
 struct AShared {
     alignas(16) float m_run[kCols];   // running maximum, log2 units
@@ -59,12 +59,20 @@ struct AShared {
     uint64_t pair_full[5];            // block pair m of the tile landed (m = 4: the rope block)
     uint64_t pair_free[5];            // its readers are done (m = 4: every product of the tile)
     uint64_t q_full, q_empty, s_full, p_full, o_fin;
+    RawShared raw;
+    uint64_t scr_full[kScrSlots], scr_free[kScrSlots];  // half tiles of the scratch
     TileShare share;
     uint32_t tmem_base;
     volatile int abort;
 };
-constexpr size_t kSmem = 1024 + kQBytes + kKvBytes + sizeof(AShared);
-static_assert(kSmem <= 232448, "shared memory per CTA");
+constexpr int raw_slots(int nc) { return nc == 16 ? 3 : 2; }  // as many as fit beside Q and the tile
+constexpr size_t smem_of(Rows rows, int nc)
+{
+    return 1024 + 9 * (size_t)nc * 128 + kKvBytes + (rows == kRawRows ? raw_slots(nc) * kRawSlot + 2 * kScaleSlot : 0) +
+           sizeof(AShared);
+}
+static_assert(smem_of(kBf16Rows, 64) <= 232448 && smem_of(kRawRows, 32) <= 232448 && smem_of(kRawRows, 16) <= 232448,
+              "shared memory per CTA");
 
 struct AParams {
     PagedTc t;
@@ -76,6 +84,7 @@ struct AParams {
     int4 *unit;                    // [B * mult] of each (request, group set): first and last share, whether the first began earlier
     float *part;                   // [2 * CTAs][slot_cols][512] raw accumulators
     float2 *part_ml;               // [2 * CTAs][slot_cols] maximum (log2 units) and sum
+    uint8_t *scratch;              // [CTAs][kScrSlots][64][576] bf16 (fp8 rows of CTA pairs)
 };
 
 // The pieces of a share: tiles [t0, t1) of group set j of request b.
@@ -137,25 +146,29 @@ __device__ __forceinline__ void tmem_stg(uint32_t taddr, const uint32_t (&r)[G])
 }
 
 // NC: columns of the CTA's products (16, 32 or 64), two softmax groups of half as many.
-template <bool FP8, bool PAIR, int NC>
-__global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreadsBf16, 1)
+// kv_map: bf16 rows of the cache or of the scratch, or the fp8 codes; sc_map, rope_map: of raw rows.
+template <Rows ROWS, bool PAIR, int NC>
+__global__ void __launch_bounds__(threads_of(ROWS), 1)
 paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
-                    const __grid_constant__ CUtensorMap kv_map)
+                    const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
+                    const __grid_constant__ CUtensorMap rope_map)
 {
-    constexpr int kGrp = NC / 2;
+    constexpr bool RAW = ROWS == kRawRows, SCR = ROWS == kScratchRows;
+    constexpr int kGrp = NC / 2, kRaw = raw_slots(NC);
     constexpr uint32_t kQBlk = NC * 128;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *q_s = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t *kv_s = q_s + kQBytes;
+    uint8_t *kv_s = q_s + (9 * kQBlk + 1023) / 1024 * 1024;
     uint8_t *p_s = kv_s + 8 * kPtBlk;  // P^T in the rope block
-    AShared *sm = (AShared *)(kv_s + kKvBytes);
+    uint8_t *raw_s = kv_s + kKvBytes, *sc_s = raw_s + (RAW ? kRaw * kRawSlot : 0);
+    AShared *sm = (AShared *)(sc_s + (RAW ? 2 * kScaleSlot : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = blockIdx.x / p.team, rank = blockIdx.x - team * p.team;  // rank: column group in the set
     const int peer = PAIR ? (int)cluster_ctarank() : 0;
 
     if (threadIdx.x == 0) {
         for (int m = 0; m < 5; ++m) {
-            mbar_init(&sm->pair_full[m], FP8 ? kDqThreads / 32 : 1);
+            mbar_init(&sm->pair_full[m], RAW && m < 4 ? kDqThreads / 32 : 1);
             mbar_init(&sm->pair_free[m], PAIR ? 2 : 1);
         }
         mbar_init(&sm->q_full, 1);
@@ -163,6 +176,14 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
         mbar_init(&sm->s_full, 1);
         mbar_init(&sm->p_full, 256);
         mbar_init(&sm->o_fin, 1);
+        for (int i = 0; i < kMaxRaw; ++i) {
+            mbar_init(&sm->raw.full[i], 1);
+            mbar_init(&sm->raw.empty[i], kDqThreads / 32);
+        }
+        for (int i = 0; i < kScrSlots; ++i) {
+            mbar_init(&sm->scr_full[i], kScrThreads / 32);
+            mbar_init(&sm->scr_free[i], 1);
+        }
         sm->abort = 0;
         fence_mbar_init();
     }
@@ -184,14 +205,16 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
     const bool work = s.start(p, sm->share);
 
     if (warp < 4) {
-        if (FP8) regs_down<Regs<NC>::kCtl>();
+        if (SCR) regs_down<kRegsCtl>();
         if (warp == 0 && work) {
             // -------------------------------------------------------- TMA
             const int boxes = kPtTok / p.t.box_rows;  // at most 16, one a lane
             const uint32_t box_bytes = (uint32_t)p.t.box_rows * 128;
             // a pair's boxes are shared out by halves of the tile
             const int box0 = PAIR && peer == 1 ? boxes / 2 : 0, box1 = PAIR && peer == 0 ? boxes / 2 : boxes;
-            uint32_t i = 0, seg = 0;
+            constexpr uint32_t kRowBytes = ROWS == kBf16Rows ? 2 * (kPtDl + kPtDr) : kPtFp8Row;
+            uint32_t i = 0, seg = 0, rph = 0, sph = 0;
+            int rs = 0, ss = 0;
             bool ok = true;
             for (bool more = true; more && ok; more = s.next(p), ++seg) {
                 if (seg > 0 && !mbar_wait(&sm->q_empty, (seg - 1) & 1, kPtWait)) ok = false;
@@ -202,7 +225,6 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     tma_load_2d(q_s + 8 * kQBlk, &qr_map, 0, row, &sm->q_full);
                 }
                 __syncwarp();
-                if (FP8) continue;
                 const int32_t *pt = p.t.page_table + (int64_t)s.b * p.t.pt_ld;
                 // row of this lane's box of tile t, or -1
                 auto box_row = [&](int t) -> int {
@@ -212,36 +234,91 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 };
                 int y = box_row(s.t0), y1 = box_row(s.t0 + 1);
                 for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
-                    const uint32_t blk_bytes = __popc(__ballot_sync(0xffffffffu, y >= 0)) * box_bytes;
+                    const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
+                    const uint32_t blk_bytes = SCR ? kPtBlk : __popc(live) * box_bytes;
+                    // one lane issues a box at a time from uniform registers: a box's coordinates and
+                    // addresses per lane took 350 cycles a pair
                     const int y_first = __shfl_sync(0xffffffffu, y, box0);
-#pragma unroll
-                    for (int m = 0; m < 5; ++m) {
-                        if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) ok = false;
-                        if (elect_one()) mbar_arrive_expect_tx(&sm->pair_full[m], (m < 4 ? 2 : 1) * blk_bytes);
-                        __syncwarp();
-                        // one lane issues a box at a time from uniform registers: a box's coordinates and
-                        // addresses per lane took 350 cycles a pair
+                    auto boxes_of = [&](auto issue) {
                         int yb = y_first;
                         for (int x = box0; x < box1; ++x) {
                             if (x > box0) yb = __shfl_sync(0xffffffffu, y, x);
-                            if (yb >= 0 && elect_one()) {
-#pragma unroll
-                                for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c) {
-                                    uint8_t *dst = kv_s + c * kPtBlk + x * box_bytes;
-                                    if (PAIR)
-                                        tma_load_2d_multicast(dst, &kv_map, 64 * c, yb, &sm->pair_full[m], 3);
-                                    else
-                                        tma_load_2d(dst, &kv_map, 64 * c, yb, &sm->pair_full[m]);
-                                }
+                            if (yb >= 0 && elect_one()) issue(x, yb);
+                            __syncwarp();
+                        }
+                    };
+                    if constexpr (RAW) {
+#pragma unroll 1
+                        for (int m = 0; m < 4; ++m) {
+                            if (!mbar_wait(&sm->raw.empty[rs], rph ^ 1, kPtWait)) ok = false;
+                            if (elect_one()) {
+                                if (m == 0) sm->raw.boxes[i & 1] = live;
+                                mbar_arrive_expect_tx(&sm->raw.full[rs], blk_bytes + (m == 0 ? blk_bytes / 8 : 0));
                             }
                             __syncwarp();
+                            boxes_of([&](int x, int yb) {
+                                tma_load_2d(raw_s + rs * kRawSlot + x * box_bytes, &kv_map, 128 * m, yb, &sm->raw.full[rs]);
+                                if (m == 0)
+                                    tma_load_2d(sc_s + (i & 1) * kScaleSlot + x * (box_bytes / 8), &sc_map, kPtDl, yb,
+                                                &sm->raw.full[rs]);
+                            });
+                            if (++rs == kRaw) {
+                                rs = 0;
+                                rph ^= 1;
+                            }
+                        }
+                        if (!mbar_wait(&sm->pair_free[4], (i & 1) ^ 1, kPtWait)) ok = false;
+                        if (elect_one()) mbar_arrive_expect_tx(&sm->pair_full[4], blk_bytes);
+                        __syncwarp();
+                        boxes_of([&](int x, int yb) {
+                            tma_load_2d(kv_s + 8 * kPtBlk + x * box_bytes, &rope_map, kFp8RopeX, yb, &sm->pair_full[4]);
+                        });
+                    } else {
+                        if constexpr (SCR) {
+                            // this CTA's half of the tile is in its scratch: written by the row warps
+                            if (!mbar_wait(&sm->scr_full[ss], sph, kPtWait)) ok = false;
+                            asm volatile("fence.proxy.async.global;" ::: "memory");
+                        }
+#pragma unroll
+                        for (int m = 0; m < 5; ++m) {
+                            if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) ok = false;
+                            if (elect_one()) {
+                                mbar_arrive_expect_tx(&sm->pair_full[m], (m < 4 ? 2 : 1) * blk_bytes);
+                                // both CTAs are done with the tile before: its scratch may be written again
+                                if (SCR && m == 4 && i > 0) mbar_arrive(&sm->scr_free[ss == 0 ? kScrSlots - 1 : ss - 1]);
+                            }
+                            __syncwarp();
+                            if constexpr (SCR) {
+                                if (elect_one()) {
+#pragma unroll
+                                    for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c)
+                                        tma_load_2d_multicast(kv_s + c * kPtBlk + peer * (kPtBlk / 2), &kv_map, 64 * c,
+                                                              ((int)blockIdx.x * kScrSlots + ss) * kScrRows,
+                                                              &sm->pair_full[m], 3);
+                                }
+                                __syncwarp();
+                            } else {
+                                boxes_of([&](int x, int yb) {
+#pragma unroll
+                                    for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c) {
+                                        uint8_t *dst = kv_s + c * kPtBlk + x * box_bytes;
+                                        if (PAIR)
+                                            tma_load_2d_multicast(dst, &kv_map, 64 * c, yb, &sm->pair_full[m], 3);
+                                        else
+                                            tma_load_2d(dst, &kv_map, 64 * c, yb, &sm->pair_full[m]);
+                                    }
+                                });
+                            }
+                        }
+                        if (SCR && ++ss == kScrSlots) {
+                            ss = 0;
+                            sph ^= 1;
                         }
                     }
                     // the tile after the next one into L2 while this one is worked on
                     const int y2 = box_row(t + 2);
                     if (lane >= box0 && lane < box1 && y2 >= 0)
-                        prefetch_l2_bulk(p.t.kv + (int64_t)y2 * (2 * (kPtDl + kPtDr)),
-                                         (uint32_t)p.t.box_rows * (2 * (kPtDl + kPtDr)));
+                        prefetch_l2_bulk(p.t.kv + (int64_t)y2 * kRowBytes, (uint32_t)p.t.box_rows * kRowBytes);
                     y = y1;
                     y1 = y2;
                     ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
@@ -250,11 +327,13 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             }
             if (!ok && lane == 0) fail();
             if (lane == 0) {  // nothing is in flight at the end
-                if (!FP8 && i > 0)
+                if (i > 0)
                     for (int m = 0; m < 5; ++m) {
                         mbar_wait(&sm->pair_full[m], (i - 1) & 1, kPtWait);
                         mbar_wait(&sm->pair_free[m], (i - 1) & 1, kPtWait);  // the peer's arrivals too
                     }
+                if (RAW)
+                    for (int x = 0; x < kRaw; ++x) mbar_wait(&sm->raw.full[x], x < rs ? rph : rph ^ 1, kPtWait);
                 if (seg > 0) mbar_wait(&sm->q_full, (seg - 1) & 1, kPtWait);
             }
             __syncwarp();
@@ -373,10 +452,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             }
         }
     } else if (warp < 12) {
-        if (FP8) {
-            if constexpr (Regs<NC>::kSoftmax > kRegsLaunch) regs_up<Regs<NC>::kSoftmax>();
-            else regs_down<Regs<NC>::kSoftmax>();
-        }
+        if (SCR) regs_up<kRegsSoftmax>();
         if (work) {
             // -------------------------------------------------------- softmax: one key a thread, 32 columns a group
             const int grp = (warp - 4) >> 2, quad = warp & 3, cb = grp * kGrp, bar = 1 + grp;
@@ -493,7 +569,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         }
                         *reinterpret_cast<uint4 *>(p_s + sw128_offset(key, cb / 8 + c8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
-                    if (!FP8 && !valid) {
+                    if (ROWS == kBf16Rows && !valid) {
                         // what lies behind the length may be NaN, which a weight of 0 would not hide: this
                         // group's half of the key's latent blocks becomes 0 (S^T has read them)
                         for (int m = 0; m < 4; ++m) mbar_wait(&sm->pair_full[m], i & 1, kPtWait);
@@ -576,46 +652,76 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 tc_fence_before();
             }
         }
-    } else if constexpr (FP8) {
-        if constexpr (Regs<NC>::kRows > kRegsLaunch) regs_up<Regs<NC>::kRows>();
-        else regs_down<Regs<NC>::kRows>();
+    } else if constexpr (RAW) {
         if (work) {
-            // -------------------------------------------------------- fp8 rows into the tile
+            // -------------------------------------------------------- raw rows expanded into the tile
             const int d = threadIdx.x - 384;
-            Fp8Rows x;
-            x.set_rows(p.t, d, s.b, s.t0, s.len);
-            x.load<0>(p.t, d); x.load<1>(p.t, d); x.load<2>(p.t, d); x.load<3>(p.t, d); x.load<4>(p.t, d);
-            uint32_t i = 0;
-            int t = s.t0;
-            auto wait_free = [&](int m) {
-                if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) fail();
-            };
-            auto release = [&](int m) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->pair_full[m]);
-            };
-            for (bool more = true; more; ++i) {
+            uint32_t i = 0, rph = 0;
+            int rs = 0;
+            bool ok = true;
+            for (bool more = true; more && ok; more = s.next(p)) {
+                for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
+                    uint32_t live = 0;
+                    const float *scales = reinterpret_cast<const float *>(sc_s + (i & 1) * kScaleSlot);
+#pragma unroll 1
+                    for (int m = 0; m < 4; ++m) {
+                        if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;
+                        if (m == 0) live = live_rows(p.t, sm->raw.boxes[i & 1], d, t, s.len);
+                        RawStep x;
+                        x.read(raw_s + rs * kRawSlot, scales, m, d, live);
+                        if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) ok = false;
+                        x.store(d, kv_s + 2 * m * kPtBlk, kv_s + (2 * m + 1) * kPtBlk);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&sm->raw.empty[rs]);
+                            mbar_arrive(&sm->pair_full[m]);
+                        }
+                        if (++rs == kRaw) {
+                            rs = 0;
+                            rph ^= 1;
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
+                }
+                ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
+            }
+            if (!ok && lane == 0) fail();
+        }
+    } else if constexpr (SCR) {
+        regs_down<kRegsRows>();
+        if (work) {
+            // -------------------------------------------------------- rows expanded into the scratch
+            const int d = threadIdx.x - 384;
+            uint8_t *scr = p.scratch + (int64_t)blockIdx.x * kScrSlots * kScrRows * kScrRow;
+            const int off = peer * kScrRows;  // this CTA's half of a tile
+            ScrRows x;
+            x.set_rows(p.t, d, s.b, s.t0 * kPtTok + off, s.len);
+            x.load(p.t, d);
+            uint32_t sph = 0;
+            int ss = 0, t = s.t0;
+            bool ok = true;
+            for (bool more = true; more && ok;) {
                 if (++t >= s.t1) {
                     more = s.next(p);
                     t = s.t0;
                 }
-                if (more)
-                    x.set_rows(p.t, d, s.b, t, s.len);
-                else
-                    x.no_rows();
-                wait_free(0);
-                x.store<0>(d, kv_s, kv_s + kPtBlk); x.load<0>(p.t, d); release(0);
-                wait_free(1);
-                x.store<1>(d, kv_s + 2 * kPtBlk, kv_s + 3 * kPtBlk); x.load<1>(p.t, d); release(1);
-                wait_free(2);
-                x.store<2>(d, kv_s + 4 * kPtBlk, kv_s + 5 * kPtBlk); x.load<2>(p.t, d); release(2);
-                wait_free(3);
-                x.store<3>(d, kv_s + 6 * kPtBlk, kv_s + 7 * kPtBlk); x.load<3>(p.t, d); release(3);
-                wait_free(4);
-                x.store<4>(d, kv_s + 8 * kPtBlk, nullptr); x.load<4>(p.t, d); release(4);
-                if (__any_sync(0xffffffffu, sm->abort)) break;
+                if (!mbar_wait(&sm->scr_free[ss], sph ^ 1, kPtWait)) ok = false;
+                x.store(scr + ss * (kScrRows * kScrRow), d);
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->scr_full[ss]);
+                if (++ss == kScrSlots) {
+                    ss = 0;
+                    sph ^= 1;
+                }
+                if (more) {
+                    x.set_rows(p.t, d, s.b, t * kPtTok + off, s.len);
+                    x.load(p.t, d);
+                }
+                ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
             }
+            if (!ok && lane == 0) fail();
         }
     }
 
@@ -712,36 +818,45 @@ __global__ void __launch_bounds__(kJoinThreads) paged_mla_join_kernel(AParams p)
 // up to kMaxTeam that divides the number of 64-column groups, as many as the SMs hold and
 // the tiles fill.
 struct Plan {
+    Rows rows;
     int cols, nc, groups, team, mult, teams, slot_cols;
-    size_t head_bytes, ml_bytes, part_bytes;
+    size_t head_bytes, ml_bytes, part_bytes, scratch_bytes;
 };
 
-Plan make_plan(int R, int n, int H, int max_row_len, int sms)
+Plan make_plan(bool fp8, int R, int n, int H, int max_row_len, int sms)
 {
     Plan q;
     q.cols = n * H;
-    q.nc = q.cols <= 16 ? 16 : q.cols <= 32 ? 32 : kCols;
+    q.nc = q.cols <= 16 ? 16 : q.cols <= 32 || (fp8 && q.cols <= kCols) ? 32 : kCols;
     q.groups = (int)ceil_div(q.cols, q.nc);
+    q.rows = !fp8 ? kBf16Rows : q.cols <= 32 ? kRawRows : kScratchRows;
+    if (q.rows == kScratchRows) q.groups = (q.groups + 1) / 2 * 2;  // pairs only: the last group may be padding
     q.team = 1;
     while (q.team < kMaxTeam && q.groups % (2 * q.team) == 0) q.team *= 2;
     q.mult = q.groups / q.team;
     const int64_t most = (int64_t)(R / n) * q.mult * ceil_div(max_row_len, kPtTok);
     const int fit = sms / q.team > 0 ? sms / q.team : 1;
     q.teams = (int)(most < fit ? most : fit);
-    q.slot_cols = q.cols < kCols ? q.cols : kCols;
+    q.slot_cols = q.cols < q.nc ? q.cols : q.nc;
     const size_t slots = (size_t)q.teams * q.team * 2 * q.slot_cols;
     q.head_bytes = (size_t)(R / n) * q.mult * sizeof(int4);
     q.ml_bytes = (slots * sizeof(float2) + 15) / 16 * 16;
     q.part_bytes = slots * kPtDl * sizeof(float);
+    q.scratch_bytes = q.rows == kScratchRows ? (size_t)q.teams * q.team * kScrSlots * kScrRows * kScrRow : 0;
     return q;
 }
 
-template <bool FP8, bool PAIR, int NC>
-nsa_status launch(const AParams &p, const CUtensorMap &qn, const CUtensorMap &qr, const CUtensorMap &kv, cudaStream_t stream)
+struct Maps {
+    CUtensorMap qn, qr, kv, sc, rope;
+};
+
+template <Rows ROWS, bool PAIR, int NC>
+nsa_status launch(const AParams &p, const Maps &m, cudaStream_t stream)
 {
-    constexpr auto kern = paged_mla_tc_kernel<FP8, PAIR, NC>;
-    NSA_CUDA_TRY(max_dynamic_smem<kern>((int)kSmem));
-    if (FP8) {
+    constexpr auto kern = paged_mla_tc_kernel<ROWS, PAIR, NC>;
+    constexpr int smem = (int)smem_of(ROWS, NC);
+    NSA_CUDA_TRY(max_dynamic_smem<kern>(smem));
+    if (ROWS == kScratchRows) {
         // the register split needs the registers the kernel was compiled to be launched with
         static std::atomic<int> regs{0};
         if (regs.load(std::memory_order_relaxed) == 0) {
@@ -753,8 +868,8 @@ nsa_status launch(const AParams &p, const CUtensorMap &qn, const CUtensorMap &qr
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.teams * p.team));
-    cfg.blockDim = dim3(FP8 ? kThreadsFp8 : kThreadsBf16);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.blockDim = dim3(threads_of(ROWS));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -763,7 +878,7 @@ nsa_status launch(const AParams &p, const CUtensorMap &qn, const CUtensorMap &qr
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, qn, qr, kv));
+    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, m.qn, m.qr, m.kv, m.sc, m.rope));
     // shares per request on average: below four, a warp joins a column faster than a block (both measured)
     const int64_t rows = (int64_t)p.t.B * p.cols;
     if (p.teams < 4 * (int64_t)p.t.B * p.mult)
@@ -781,8 +896,8 @@ size_t paged_mla_tc_workspace_bytes(nsa_dtype q_dtype, nsa_dtype kv_dtype, int R
     if (q_dtype != NSA_DT_BF16 || (kv_dtype != NSA_DT_BF16 && kv_dtype != NSA_DT_E4M3) || d_latent != kPtDl ||
         d_rope != kPtDr || R <= 0 || rows_per_req <= 0 || R % rows_per_req != 0 || H <= 0 || max_row_len <= 0)
         return 0;
-    const Plan q = make_plan(R, rows_per_req, H, max_row_len, current_sm_count());
-    return q.head_bytes + q.ml_bytes + q.part_bytes;
+    const Plan q = make_plan(kv_dtype == NSA_DT_E4M3, R, rows_per_req, H, max_row_len, current_sm_count());
+    return q.head_bytes + q.ml_bytes + q.part_bytes + q.scratch_bytes;
 }
 
 nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse, void *workspace, cudaStream_t stream)
@@ -791,27 +906,38 @@ nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse,
     if ((int64_t)a.R * a.H > 0x7fffffffLL) return NSA_ERR_UNSUPPORTED;
     const int sms = current_sm_count();
     if (sms <= 0) return NSA_ERR_CUDA;
-    const Plan q = make_plan(a.R, a.rows_per_req, a.H, a.max_row_len, sms);
-    const bool fp8 = a.kv_dtype == NSA_DT_E4M3, pair = !fp8 && q.team >= 2;
+    const bool fp8 = a.kv_dtype == NSA_DT_E4M3;
+    const Plan q = make_plan(fp8, a.R, a.rows_per_req, a.H, a.max_row_len, sms);
     AParams p;
     p.t = paged_tc_params(a);
     if (p.t.box_rows > 64) p.t.box_rows = 64;  // half a tile for each CTA of a pair
-    p.cols = q.cols; p.nc = q.nc; p.groups = q.groups; p.team = q.team; p.mult = q.mult; p.teams = q.teams; p.slot_cols = q.slot_cols;
+    p.cols = q.cols; p.nc = q.nc; p.groups = q.groups; p.team = q.team; p.mult = q.mult; p.teams = q.teams;
+    p.slot_cols = q.slot_cols;
     p.out = (__nv_bfloat16 *)out;
     p.lse = lse;
-    p.unit = (int4 *)workspace;
-    p.part_ml = (float2 *)((uint8_t *)workspace + q.head_bytes);
-    p.part = (float *)((uint8_t *)workspace + q.head_bytes + q.ml_bytes);
-    CUtensorMap qn, qr, kv = {};
-    if (!paged_tc_maps(a, p.t, (uint32_t)q.nc, &qn, &qr, &kv)) return NSA_ERR_CUDA;
-    if (fp8)
-        return q.nc == 16   ? launch<true, false, 16>(p, qn, qr, kv, stream)
-               : q.nc == 32 ? launch<true, false, 32>(p, qn, qr, kv, stream)
-                            : launch<true, false, 64>(p, qn, qr, kv, stream);
-    if (pair) return launch<false, true, 64>(p, qn, qr, kv, stream);
-    return q.nc == 16   ? launch<false, false, 16>(p, qn, qr, kv, stream)
-           : q.nc == 32 ? launch<false, false, 32>(p, qn, qr, kv, stream)
-                        : launch<false, false, 64>(p, qn, qr, kv, stream);
+    uint8_t *ws = (uint8_t *)workspace;
+    p.unit = (int4 *)ws;
+    p.part_ml = (float2 *)(ws += q.head_bytes);
+    p.part = (float *)(ws += q.ml_bytes);
+    p.scratch = ws += q.part_bytes;
+    Maps m = {};
+    if (!paged_tc_q_maps(a, (uint32_t)q.nc, &m.qn, &m.qr)) return NSA_ERR_CUDA;
+    const bool mapped =
+        q.rows == kBf16Rows ? bf16_rows_map(a.kv, (uint64_t)a.num_pages * a.page_size, (uint32_t)p.t.box_rows, &m.kv)
+        : q.rows == kRawRows
+            ? fp8_maps(a, (uint32_t)p.t.box_rows, &m.kv, &m.sc, &m.rope)
+            : bf16_rows_map(p.scratch, (uint64_t)q.teams * q.team * kScrSlots * kScrRows, kScrRows, &m.kv);
+    if (!mapped) return NSA_ERR_CUDA;
+    switch (q.rows) {
+    case kRawRows: return q.nc == 16 ? launch<kRawRows, false, 16>(p, m, stream) : launch<kRawRows, false, 32>(p, m, stream);
+    case kScratchRows:
+        return q.nc == 32 ? launch<kScratchRows, true, 32>(p, m, stream) : launch<kScratchRows, true, 64>(p, m, stream);
+    default: break;
+    }
+    if (q.team >= 2) return launch<kBf16Rows, true, 64>(p, m, stream);
+    return q.nc == 16   ? launch<kBf16Rows, false, 16>(p, m, stream)
+           : q.nc == 32 ? launch<kBf16Rows, false, 32>(p, m, stream)
+                        : launch<kBf16Rows, false, 64>(p, m, stream);
 }
 
 }  // namespace nsa

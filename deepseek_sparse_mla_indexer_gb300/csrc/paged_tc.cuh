@@ -5,8 +5,7 @@
 // A tile is 128 consecutive positions of one request as nine K-major blocks of
 // 128 rows x 64 bf16 (16 KB, 128-byte swizzle): blocks 0..7 the latent, block 8
 // the rope part.  bf16 rows come by TMA in boxes of box_rows rows x 64 columns
-// that never cross a page; fp8 rows are loaded into registers a whole tile
-// ahead, expanded to bf16 and stored by kDqThreads threads.
+// that never cross a page; fp8 rows come raw and are expanded to bf16 by threads of the CTA.
 #pragma once
 
 #include "paged_mla.cuh"
@@ -131,82 +130,139 @@ __device__ __forceinline__ int checked_page(const PagedTc &p, const int32_t *pt,
 }
 
 // ------------------------------------------------------------------ fp8 rows
-//
-// Thread d of kDqThreads owns rows d / 8 and d / 8 + 64 and chunk d % 8 of each
-// step of a tile: step m < 4 is 128 latent codes (16 a thread and row; blocks
-// 2m, 2m + 1), step 4 the rope part (8 values; block 8).  A step is stored from
-// registers and its registers are loaded with the same step of the next tile at
-// once, so a whole tile (84 KB) is in flight per SM, which covers the latency
-// of HBM at its share of the bandwidth.
-struct Fp8Rows {
+
+// Eight e4m3 codes times their block's scale: code x scale rounded to fp32, then to
+// bf16, the row's values by definition.
+__device__ __forceinline__ uint4 expand8(uint32_t a, uint32_t b, float s)
+{
+    const uint32_t in[2] = {a, b};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2_raw h =
+            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((in[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
+        const float2 f = sm100::mul2(__half22float2(*reinterpret_cast<const __half2 *>(&h)), make_float2(s, s));
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+        o[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Raw fp8 rows in shared memory: the codes of one 128-value block of a tile's rows
+// (128 x 128 bytes) a slot, loaded by TMA ahead of the threads that expand them, and
+// the scales of a tile ([128][4] floats).  Plain 16-byte loads into registers reached
+// 14 GB/s per SM from HBM; these boxes keep up with the SM's share of it.
+constexpr uint32_t kRawSlot = kPtTok * 128;
+constexpr uint32_t kScaleSlot = kPtTok * 16;
+constexpr int kMaxRaw = 4;
+
+struct RawShared {
+    uint64_t full[kMaxRaw], empty[kMaxRaw];
+    uint32_t boxes[2];  // boxes of the tile (by parity) that were loaded
+};
+
+// Thread d of kDqThreads expands rows d / 8 and d / 8 + 64, chunk d % 8 (16 codes) of a
+// step into blocks blk0 (chunks 0..3) and blk1; rows without a key become zeros.  Codes
+// 16k .. 16k+15 become chunks 2k, 2k+1 of the step's 16; lanes with k >= 4 store the
+// odd chunk first, so that eight neighbouring lanes store to eight distinct bank groups.
+struct RawStep {
+    uint4 w[2];
+    float sc[2];
+
+    __device__ __forceinline__ void read(const uint8_t *raw, const float *scales, int m, int d, uint32_t live)
+    {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = (d >> 3) + 64 * u;
+            w[u] = *reinterpret_cast<const uint4 *>(raw + r * 128 + 16 * (d & 7));
+            sc[u] = scales[4 * r + m];
+            if (!(live >> u & 1)) {
+                w[u] = make_uint4(0u, 0u, 0u, 0u);
+                sc[u] = 0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(int d, uint8_t *blk0, uint8_t *blk1) const
+    {
+        const int k = d & 7, c0 = (2 * k) & 7;
+        uint8_t *blk = k < 4 ? blk0 : blk1;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = (d >> 3) + 64 * u;
+            // the first store's half of the codes is chosen before it is expanded
+            const uint2 a = k < 4 ? make_uint2(w[u].x, w[u].y) : make_uint2(w[u].z, w[u].w);
+            const uint2 b = k < 4 ? make_uint2(w[u].z, w[u].w) : make_uint2(w[u].x, w[u].y);
+            *reinterpret_cast<uint4 *>(blk + sm100::sw128_offset(r, k < 4 ? c0 : c0 + 1)) = expand8(a.x, a.y, sc[u]);
+            *reinterpret_cast<uint4 *>(blk + sm100::sw128_offset(r, k < 4 ? c0 + 1 : c0)) = expand8(b.x, b.y, sc[u]);
+        }
+    }
+};
+
+// Which of thread d's two rows of a tile hold a key (bit u: row d / 8 + 64 u).
+__device__ __forceinline__ uint32_t live_rows(const PagedTc &p, uint32_t boxes, int d, int tile, int len)
+{
+    uint32_t live = 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int r = (d >> 3) + 64 * u;
+        if (tile * kPtTok + r < len && (boxes >> (r / p.box_rows) & 1)) live |= 1u << u;
+    }
+    return live;
+}
+
+// Rows expanded from registers into a scratch copy of half a tile in global memory
+// (which stays in L2), for CTA pairs: thread d of kScrThreads owns rows d / 8 and
+// d / 8 + 32 of the CTA's 64 and chunk d % 8 of each step.  A step's registers are
+// loaded with the same step of the next tile as soon as it is stored.
+constexpr int kScrThreads = 256;
+constexpr int kScrSlots = 3;                    // half tiles a CTA's scratch holds
+constexpr int kScrRow = 2 * (kPtDl + kPtDr);    // bytes
+constexpr int kScrRows = kPtTok / 2;
+
+struct ScrRows {
     uint4 w[5][2];
-    float sc[4][2];
+    float4 sc[2];
     int slot[2];  // the rows that loads refer to; -1: a row of zeros
 
-    __device__ __forceinline__ void set_rows(const PagedTc &p, int d, int b, int tile, int len)
+    __device__ __forceinline__ void set_rows(const PagedTc &p, int d, int b, int pos0, int len)
     {
         const int32_t *pt = p.page_table + (int64_t)b * p.pt_ld;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int pos = tile * kPtTok + (d >> 3) + 64 * u;
+            const int pos = pos0 + (d >> 3) + 32 * u;
             const int page = checked_page(p, pt, pos, len);
             slot[u] = page < 0 ? -1 : page * p.ps + pos % p.ps;
         }
     }
-    __device__ __forceinline__ void no_rows() { slot[0] = slot[1] = -1; }
-
-    template <int M>
     __device__ __forceinline__ void load(const PagedTc &p, int d)
     {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            w[M][u] = make_uint4(0u, 0u, 0u, 0u);
-            if (M < 4) sc[M & 3][u] = 0.f;
+#pragma unroll
+            for (int m = 0; m < 5; ++m) w[m][u] = make_uint4(0u, 0u, 0u, 0u);
+            sc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (slot[u] >= 0) {
                 const uint8_t *row = p.kv + (int64_t)slot[u] * kPtFp8Row;
-                w[M][u] = __ldg(reinterpret_cast<const uint4 *>(row + (M < 4 ? 128 * M : kPtDl + 16) + 16 * (d & 7)));
-                if (M < 4) sc[M & 3][u] = __ldg(reinterpret_cast<const float *>(row + kPtDl + 4 * M));
+#pragma unroll
+                for (int m = 0; m < 5; ++m)
+                    w[m][u] = __ldg(reinterpret_cast<const uint4 *>(row + (m < 4 ? 128 * m : kPtDl + 16) + 16 * (d & 7)));
+                sc[u] = __ldg(reinterpret_cast<const float4 *>(row + kPtDl));
             }
         }
     }
-
-    static __device__ __forceinline__ void expand8(uint32_t a, uint32_t b, float s, uint4 &out)
+    __device__ __forceinline__ void store(uint8_t *half, int d) const
     {
-        const uint32_t in[2] = {a, b};
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2_raw h =
-                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((in[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
-            // code x scale rounded to fp32, then to bf16: the row's value by definition
-            const float2 f = sm100::mul2(__half22float2(*reinterpret_cast<const __half2 *>(&h)), make_float2(s, s));
-            const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
-            o[i] = *reinterpret_cast<const uint32_t *>(&v);
-        }
-        out = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-
-    // Step M into its blocks (blk1 unused for the rope step).  Codes 16k .. 16k+15 of
-    // a step become chunks 2k, 2k+1 of its 16; lanes with k >= 4 store the odd chunk
-    // first, so that eight neighbouring lanes store to eight distinct bank groups.
-    template <int M>
-    __device__ __forceinline__ void store(int d, uint8_t *blk0, uint8_t *blk1) const
-    {
-        const int k = d & 7;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int r = (d >> 3) + 64 * u;
-            if (M == 4) {
-                *reinterpret_cast<uint4 *>(blk0 + sm100::sw128_offset(r, k)) = w[4][u];
-            } else {
-                uint4 lo, hi;
-                expand8(w[M][u].x, w[M][u].y, sc[M & 3][u], lo);
-                expand8(w[M][u].z, w[M][u].w, sc[M & 3][u], hi);
-                uint8_t *blk = k < 4 ? blk0 : blk1;
-                const int c0 = (2 * k) & 7;
-                *reinterpret_cast<uint4 *>(blk + sm100::sw128_offset(r, k < 4 ? c0 : c0 + 1)) = k < 4 ? lo : hi;
-                *reinterpret_cast<uint4 *>(blk + sm100::sw128_offset(r, k < 4 ? c0 + 1 : c0)) = k < 4 ? hi : lo;
+            uint8_t *row = half + ((d >> 3) + 32 * u) * kScrRow;
+            const float s[4] = {sc[u].x, sc[u].y, sc[u].z, sc[u].w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                uint4 *o = reinterpret_cast<uint4 *>(row + 256 * m + 32 * (d & 7));
+                o[0] = expand8(w[m][u].x, w[m][u].y, s[m]);
+                o[1] = expand8(w[m][u].z, w[m][u].w, s[m]);
             }
+            *reinterpret_cast<uint4 *>(row + 2 * kPtDl + 16 * (d & 7)) = w[4][u];
         }
     }
 };
@@ -246,19 +302,37 @@ inline PagedTc paged_tc_params(const PagedMlaArgs &a)
     return p;
 }
 
-// Maps of the query parts (boxes of 64 columns x `rows` rows over the R * H query
-// heads) and of a bf16 cache (boxes of 64 columns x box_rows rows).
-inline bool paged_tc_maps(const PagedMlaArgs &a, const PagedTc &p, uint32_t rows, CUtensorMap *qn, CUtensorMap *qr,
-                          CUtensorMap *kv)
+// Maps of the query parts: boxes of 64 columns x `rows` rows over the R * H query heads.
+inline bool paged_tc_q_maps(const PagedMlaArgs &a, uint32_t rows, CUtensorMap *qn, CUtensorMap *qr)
 {
     const uint64_t heads = (uint64_t)a.R * a.H;
     return make_tma_2d(qn, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q_nope, kPtDl, heads, (uint64_t)a.nope_ld_h * 2, 64, rows,
                        CU_TENSOR_MAP_SWIZZLE_128B) &&
            make_tma_2d(qr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q_rope, kPtDr, heads, (uint64_t)a.rope_ld_h * 2, 64, rows,
-                       CU_TENSOR_MAP_SWIZZLE_128B) &&
-           (a.kv_dtype != NSA_DT_BF16 ||
-            make_tma_2d(kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, kPtDl + kPtDr, (uint64_t)a.num_pages * a.page_size,
-                        2 * (kPtDl + kPtDr), 64, (uint32_t)p.box_rows, CU_TENSOR_MAP_SWIZZLE_128B));
+                       CU_TENSOR_MAP_SWIZZLE_128B);
 }
+
+// Map of bf16 rows (a bf16 cache, or expanded rows): boxes of 64 columns x box_rows rows.
+inline bool bf16_rows_map(const void *base, uint64_t rows, uint32_t box_rows, CUtensorMap *kv)
+{
+    return make_tma_2d(kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, kPtDl + kPtDr, rows, 2 * (kPtDl + kPtDr), 64, box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Maps of an fp8 cache: codes in boxes of 128 bytes, scales in boxes of 16 bytes (the row
+// seen as bytes) and the rope part in boxes of 64 bf16 (the row seen as 328 bf16; x = 264
+// is byte 528, a multiple of 16).
+inline bool fp8_maps(const PagedMlaArgs &a, uint32_t box_rows, CUtensorMap *codes, CUtensorMap *scales, CUtensorMap *rope)
+{
+    const uint64_t rows = (uint64_t)a.num_pages * a.page_size;
+    return make_tma_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv, kPtFp8Row, rows, kPtFp8Row, 128, box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_NONE) &&
+           make_tma_2d(scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv, kPtFp8Row, rows, kPtFp8Row, 16, box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_NONE) &&
+           make_tma_2d(rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, kPtFp8Row / 2, rows, kPtFp8Row, 64, box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+}
+constexpr int kFp8RopeX = (kPtDl + 16) / 2;
+static_assert(kFp8RopeX * 2 % 16 == 0, "a TMA box starts on a 16-byte boundary");
 
 }  // namespace nsa
