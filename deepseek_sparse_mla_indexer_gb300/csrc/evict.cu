@@ -19,7 +19,7 @@ using namespace sm100;
 //
 // One thread-block cluster per request; its CTAs own equal slices of the
 // positions and its warps contiguous parts of them, a key per lane and step, kept
-// in registers (slices up to 16 K; longer ones are read again from L2).  The
+// in registers (slices up to 32 K; longer ones are read again from L2).  The
 // threshold key of the middle range is found by a radix selection over 11 + 11 +
 // 10 bits of the order-preserving key: each CTA counts its slice's digits in
 // shared memory, and after one cluster barrier every CTA sums all counts
@@ -31,7 +31,7 @@ using namespace sm100;
 // steps, not by its bytes.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelKeys = 16;              // keys a thread holds in registers
+constexpr int kSelKeys = 16;              // keys a thread holds in registers (or twice as many)
 constexpr int kSelMaxCluster = 8;         // the portable limit
 constexpr int kSelSlice = kSelThreads * kSelKeys;
 
@@ -68,8 +68,8 @@ __device__ __forceinline__ void count_digit(uint32_t *hist, uint32_t bin, bool o
     }
 }
 
-// REGS: the slice's keys stay in registers; else they are read from L2 in every pass.
-template <bool REGS>
+// KEYS: keys a thread holds (0: they are read from L2 in every pass).
+template <int KEYS>
 __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, int max_len, int sinks, int recent,
                     int budget, int slice, int32_t *keep, int64_t keep_ld, int32_t *new_len, int32_t *status)
@@ -96,29 +96,34 @@ evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, i
     const int steps = (p1 - p0 + kSelThreads - 1) / kSelThreads;
     const int w0 = p0 + warp * steps * 32 + lane;  // position of this lane in step 0
     auto in_mid = [&](int pos) { return pos < p1 && pos >= mid0 && pos < mid1; };
-    uint32_t key[REGS ? kSelKeys : 1];
-    if (REGS) {
+    constexpr bool REGS = KEYS > 0;
+    uint32_t key[REGS ? KEYS : 1];
+    uint32_t mid_bits = 0;  // steps whose position lies in the middle range
+    if constexpr (REGS) {
 #pragma unroll
-        for (int j = 0; j < kSelKeys; ++j) {
+        for (int j = 0; j < KEYS; ++j) {
             const int pos = w0 + 32 * j;
-            key[j] = j < steps && in_mid(pos) ? __float_as_uint(__ldg(row + pos)) : 0u;
+            const bool on = j < steps && in_mid(pos);
+            mid_bits |= (uint32_t)on << j;
+            key[j] = on ? __float_as_uint(__ldg(row + pos)) : 0u;
         }
     }
     for (int i = tid; i < 3 * 2048 / 4; i += kSelThreads) reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (REGS) {
+    if constexpr (REGS) {
 #pragma unroll
-        for (int j = 0; j < kSelKeys; ++j) key[j] = order_key(__uint_as_float(key[j]));
+        for (int j = 0; j < KEYS; ++j) key[j] = order_key(__uint_as_float(key[j]));
     }
-    // f(position, key) for every step of the warp, all lanes together
+    // f(position, key, whether in the middle range) for every step of the warp, all lanes together
     auto each = [&](auto f) {
         if constexpr (REGS) {
 #pragma unroll
-            for (int j = 0; j < kSelKeys; ++j)
-                if (j < steps) f(w0 + 32 * j, key[j]);
+            for (int j = 0; j < KEYS; ++j)
+                if (j < steps) f(w0 + 32 * j, key[j], (mid_bits >> j & 1) != 0);
         } else {
             for (int j = 0; j < steps; ++j) {
                 const int pos = w0 + 32 * j;
-                f(pos, in_mid(pos) ? order_key(__ldg(row + pos)) : 0u);
+                const bool on = in_mid(pos);
+                f(pos, on ? order_key(__ldg(row + pos)) : 0u, on);
             }
         }
     };
@@ -132,8 +137,8 @@ evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, i
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const uint32_t mask = pass == 2 ? 1023u : 2047u;
             uint32_t *hist = sm.hist[pass];
-            each([&](int pos, uint32_t k) {
-                const bool on = in_mid(pos) && (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == prefix);
+            each([&](int, uint32_t k, bool mid) {
+                const bool on = mid && (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == prefix);
                 if (pass == 0 || __any_sync(0xffffffffu, on)) count_digit(hist, (k >> shift) & mask, on, lane);
             });
             cluster_sync_all();  // every CTA's counts are complete
@@ -168,15 +173,14 @@ evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, i
         }
     }
     const uint32_t threshold = prefix;
-    auto classify = [&](int pos, uint32_t k, bool &sure, bool &eq) {
-        const bool mid = in_mid(pos);
+    auto classify = [&](int pos, uint32_t k, bool mid, bool &sure, bool &eq) {
         sure = pos < p1 && (!mid || (any && k > threshold));
         eq = mid && any && k == threshold;
     };
     uint32_t n_sure = 0, n_eq = 0;
-    each([&](int pos, uint32_t k) {
+    each([&](int pos, uint32_t k, bool mid) {
         bool sure, eq;
-        classify(pos, k, sure, eq);
+        classify(pos, k, mid, sure, eq);
         n_sure += __popc(__ballot_sync(0xffffffffu, sure));
         n_eq += __popc(__ballot_sync(0xffffffffu, eq));
     });
@@ -203,9 +207,9 @@ evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, i
         eq_before += __reduce_add_sync(0xffffffffu, ce);
     }
     // a position's place: the sure ones before it plus the equal ones taken before it
-    each([&](int pos, uint32_t k) {
+    each([&](int pos, uint32_t k, bool mid) {
         bool sure, eq;
-        classify(pos, k, sure, eq);
+        classify(pos, k, mid, sure, eq);
         const uint32_t below = (1u << lane) - 1u;
         const uint32_t bs = __ballot_sync(0xffffffffu, sure), be = __ballot_sync(0xffffffffu, eq);
         const uint32_t e = eq_before + __popc(be & below);
@@ -215,6 +219,33 @@ evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, i
     });
     if (rank == 0 && tid == 0) new_len[b] = budget;
     if (nc > 1) cluster_sync_all();  // a peer may still read this CTA's counts
+}
+
+// Clusters of nc selection CTAs that the current device runs at once (asked once per device).
+int select_clusters(int nc)
+{
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> cache[kMaxDev][kSelMaxCluster + 1];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDev) return 1;
+    n = cache[dev][nc].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)nc);
+    cfg.blockDim = dim3(kSelThreads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)nc;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, evict_select_kernel<kSelKeys>, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();  // a failed query is not the caller's error
+        n = 1;
+    }
+    cache[dev][nc].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 // ------------------------------------------------------------------ compact
@@ -480,8 +511,11 @@ extern "C" nsa_status nsa_evict_select(const float *total_dev, int64_t total_ld,
     if (((uintptr_t)total_dev | (uintptr_t)len_dev | (uintptr_t)keep_dev | (uintptr_t)new_len_dev |
          (uintptr_t)status_dev) & 3)
         return NSA_ERR_INVALID_ARG;
+    // CTAs for slices of 16 K; half as many, of 32 K, where the clusters of all requests then run in one
+    // wave and did not before (16 x 131072 positions: 8 CTAs of 16 K took two waves of 21 us)
     int nc = 1;
     while (nc < kSelMaxCluster && (int64_t)nc * kSelSlice < max_len) nc *= 2;
+    if (nc > 1 && B > select_clusters(nc) && (int64_t)nc * kSelSlice >= max_len) nc /= 2;
     if ((int64_t)B * nc > 0x7fffffffLL) return NSA_ERR_UNSUPPORTED;
     const int slice = max_len > 0 ? (int)ceil_div(max_len, nc) : 1;
     cudaLaunchConfig_t cfg = {};
@@ -495,7 +529,9 @@ extern "C" nsa_status nsa_evict_select(const float *total_dev, int64_t total_ld,
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto kern = slice <= kSelSlice ? evict_select_kernel<true> : evict_select_kernel<false>;
+    auto kern = slice <= kSelSlice       ? evict_select_kernel<kSelKeys>
+                : slice <= 2 * kSelSlice ? evict_select_kernel<2 * kSelKeys>
+                                         : evict_select_kernel<0>;
     NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, total_dev, total_ld, len_dev, max_len, sinks, recent, budget, slice,
                                     keep_dev, keep_ld, new_len_dev, status_dev));
     return NSA_OK;

@@ -123,6 +123,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
             mbar_init(&sm->raw.full[i], 1);
             mbar_init(&sm->raw.empty[i], kDqThreads / 32);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(&sm->raw.tile_full[i], 1);
         mbar_init(&sm->q_full, 1);
         mbar_init(&sm->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
@@ -191,8 +192,11 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                         uint64_t *full = FP8 ? sm->raw.full : sm->full, *empty = FP8 ? sm->raw.empty : sm->empty;
                         if (!mbar_wait(&empty[st], ph ^ 1, kPtWait)) ok = false;
                         if (elect_one()) {
-                            if (FP8 && c == 0) sm->raw.boxes[tile & 1] = live;
-                            mbar_arrive_expect_tx(&full[st], bytes + (FP8 && c == 0 ? bytes / 8 : 0));
+                            if (FP8 && c == 0) {
+                                sm->raw.boxes[tile & 1] = live;
+                                mbar_arrive_expect_tx(&sm->raw.tile_full[tile & 1], bytes / 8);
+                            }
+                            mbar_arrive_expect_tx(&full[st], bytes);
                         }
                         __syncwarp();
                         boxes_of([&](int x, int yb) {
@@ -202,7 +206,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                                 tma_load_2d(raw_s + st * kRawSlot + x * box_bytes, &kv_map, 128 * c, yb, &full[st]);
                                 if (c == 0)
                                     tma_load_2d(sc_s + (tile & 1) * kScaleSlot + x * (box_bytes / 8), &sc_map, kPtDl, yb,
-                                                &full[st]);
+                                                &sm->raw.tile_full[tile & 1]);
                             } else {
                                 tma_load_2d(raw_s + st * kRawSlot + x * box_bytes, &rope_map, kFp8RopeX, yb, &full[st]);
                             }
@@ -222,6 +226,9 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
             if (lane == 0) {
                 for (int i = 0; i < (FP8 ? p.raw : nst); ++i)
                     mbar_wait(FP8 ? &sm->raw.full[i] : &sm->full[i], i < st ? ph : ph ^ 1, kPtWait);
+                if (FP8)
+                    for (uint32_t x = tile > 2 ? tile - 2 : 0; x < tile; ++x)
+                        mbar_wait(&sm->raw.tile_full[x & 1], (x >> 1) & 1, kPtWait);
                 mbar_wait(&sm->q_full, (uses - 1) & 1, kPtWait);
             }
             __syncwarp();
@@ -334,56 +341,49 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
         // ------------------------------------------------------------ raw rows expanded into the ring
         if (work) {
             const int d = threadIdx.x - 256;
-            int st = 0, rs = 0;
+            int st = 0, rs = 0;  // stage and raw slot of the step
             uint32_t ph = 0, rph = 0, tile = 0;
             bool ok = true;
-            auto stage = [&]() -> uint8_t * {  // the next stage once it is empty
-                if (!mbar_wait(&sm->empty[st], ph ^ 1, kPtWait)) ok = false;
-                uint8_t *at = ring + st * kPtBlk;
-                if (++st == nst) {
-                    st = 0;
-                    ph ^= 1;
-                }
-                return at;
-            };
             for (bool more = true; more && ok; more = w.next(p)) {
                 for (int t = w.c0; t < w.c1 && ok; ++t, ++tile) {
-                    uint32_t live = 0;
+                    if (!mbar_wait(&sm->raw.tile_full[tile & 1], (tile >> 1) & 1, kPtWait)) ok = false;
+                    const uint32_t live = live_rows(p.t, sm->raw.boxes[tile & 1], d, t, w.len);
                     const float *scales = reinterpret_cast<const float *>(sc_s + (tile & 1) * kScaleSlot);
 #pragma unroll 1
                     for (int m = 0; m < 5; ++m) {
-                        if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;
-                        if (m == 0) live = live_rows(p.t, sm->raw.boxes[tile & 1], d, t, w.len);
-                        RawStep x;
-                        x.read(raw_s + rs * kRawSlot, scales, m & 3, d, live);
-                        const int s0 = st;
-                        uint8_t *blk0 = stage();
-                        if (m < 4) {
-                            const int s1 = st;
-                            uint8_t *blk1 = stage();
-                            x.store(d, blk0, blk1);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) {
-                                mbar_arrive(&sm->raw.empty[rs]);
-                                mbar_arrive(&sm->full[s0]);
-                                mbar_arrive(&sm->full[s1]);
-                            }
-                        } else {
-                            // the rope part lies in its slot as the operand wants it (swizzled): moved as it is
-#pragma unroll
-                            for (int u = 0; u < 2; ++u)
-                                *reinterpret_cast<uint4 *>(blk0 + ((d >> 3) + 64 * u) * 128 + 16 * (d & 7)) = x.w[u];
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) {
-                                mbar_arrive(&sm->raw.empty[rs]);
-                                mbar_arrive(&sm->full[s0]);
-                            }
+                        const int s0 = st, s1 = st + 1 == nst ? 0 : st + 1;
+                        const uint32_t ph0 = ph, ph1 = st + 1 == nst ? ph ^ 1 : ph;
+                        st += m < 4 ? 2 : 1;
+                        if (st >= nst) {
+                            st -= nst;
+                            ph ^= 1;
                         }
+                        const int r = rs;
+                        const uint32_t rp = rph;
                         if (++rs == p.raw) {
                             rs = 0;
                             rph ^= 1;
+                        }
+                        if (!mbar_wait(&sm->raw.full[r], rp, kPtWait)) ok = false;
+                        RawStep x;
+                        x.read(raw_s + r * kRawSlot, scales, m & 3, d, live);
+                        if (!mbar_wait(&sm->empty[s0], ph0 ^ 1, kPtWait)) ok = false;
+                        if (m < 4) {
+                            if (!mbar_wait(&sm->empty[s1], ph1 ^ 1, kPtWait)) ok = false;
+                            x.store(d, ring + s0 * kPtBlk, ring + s1 * kPtBlk);
+                        } else {
+                            // the rope part lies in its slot as the operand wants it (swizzled): moved as it is
+#pragma unroll
+                            for (int u = 0; u < kDqRows; ++u)
+                                *reinterpret_cast<uint4 *>(ring + s0 * kPtBlk + ((d >> 3) + kPtTok / kDqRows * u) * 128 + 16 * (d & 7)) =
+                                    x.w[u];
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&sm->raw.empty[r]);
+                            mbar_arrive(&sm->full[s0]);
+                            if (m < 4) mbar_arrive(&sm->full[s1]);
                         }
                     }
                     ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;

@@ -43,11 +43,14 @@ constexpr int kMaxTeam = 8;
 // tile and expanded from there; or fp8 rows expanded into the CTA's scratch in global memory
 // (half a tile for each CTA of a pair) and loaded from it as bf16 rows are.
 enum Rows { kBf16Rows, kRawRows, kScratchRows };
-constexpr int threads_of(Rows rows) { return rows == kBf16Rows ? 384 : 384 + (rows == kRawRows ? kDqThreads : kScrThreads); }
-// Registers per thread at launch and per role of the scratch kernel (one control, two softmax
-// and two row warpgroups): the softmax of 64 columns needs more than a fifth of the file.
-constexpr int kRegsLaunch = 96, kRegsCtl = 80, kRegsSoftmax = 120, kRegsRows = 80;
-static_assert(kRegsCtl + 2 * kRegsSoftmax + 2 * kRegsRows <= 5 * kRegsLaunch, "the split fits what the block has");
+// Softmax groups of four warps, one key a thread and kGrp columns a group: 16 columns keep a
+// thread's exponents and sums in 72 registers, which leaves room for the row warps.
+constexpr int grp_of(int nc) { return nc == 16 ? 8 : 16; }
+constexpr int row0_of(int nc) { return 128 + 128 * (nc / grp_of(nc)); }  // first row-expanding thread
+constexpr int threads_of(Rows rows, int nc)
+{
+    return row0_of(nc) + (rows == kRawRows ? kDqThreads : rows == kScratchRows ? kScrThreads : 0);
+}
 
 struct AShared {
     alignas(16) float m_run[kCols];   // running maximum, log2 units
@@ -55,7 +58,7 @@ struct AShared {
     float red[4][kCols];
     float l_col[kCols];
     int len[kCols];                   // positions the column's row sees
-    int min_len[2];
+    int min_len[4];
     uint64_t pair_full[5];            // block pair m of the tile landed (m = 4: the rope block)
     uint64_t pair_free[5];            // its readers are done (m = 4: every product of the tile)
     uint64_t q_full, q_empty, s_full, p_full, o_fin;
@@ -99,7 +102,7 @@ struct Seg {
         b = s.b;
         len = request_len(p.t, b);
         tiles = tiles_of(len);
-        j = (int)(s.off / tiles);
+        j = s.off < 0x100000000LL ? (int)((uint32_t)s.off / (uint32_t)tiles) : (int)(s.off / tiles);
         t0 = (int)(s.off - (int64_t)j * tiles);
         t1 = (int)min((int64_t)tiles, t0 + left);
         return true;
@@ -145,16 +148,16 @@ __device__ __forceinline__ void tmem_stg(uint32_t taddr, const uint32_t (&r)[G])
     else tmem_st8(taddr, r);
 }
 
-// NC: columns of the CTA's products (16, 32 or 64), two softmax groups of half as many.
+// NC: columns of the CTA's products (16, 32 or 64).
 // kv_map: bf16 rows of the cache or of the scratch, or the fp8 codes; sc_map, rope_map: of raw rows.
 template <Rows ROWS, bool PAIR, int NC>
-__global__ void __launch_bounds__(threads_of(ROWS), 1)
+__global__ void __launch_bounds__(threads_of(ROWS, NC), 1)
 paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
                     const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
                     const __grid_constant__ CUtensorMap rope_map)
 {
     constexpr bool RAW = ROWS == kRawRows, SCR = ROWS == kScratchRows;
-    constexpr int kGrp = NC / 2, kRaw = raw_slots(NC);
+    constexpr int kGrp = grp_of(NC), kGroups = NC / kGrp, kRow0 = row0_of(NC), kRaw = raw_slots(NC);
     constexpr uint32_t kQBlk = NC * 128;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *q_s = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -174,12 +177,13 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
         mbar_init(&sm->q_full, 1);
         mbar_init(&sm->q_empty, 1);
         mbar_init(&sm->s_full, 1);
-        mbar_init(&sm->p_full, 256);
+        mbar_init(&sm->p_full, 128 * kGroups);
         mbar_init(&sm->o_fin, 1);
         for (int i = 0; i < kMaxRaw; ++i) {
             mbar_init(&sm->raw.full[i], 1);
             mbar_init(&sm->raw.empty[i], kDqThreads / 32);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(&sm->raw.tile_full[i], 1);
         for (int i = 0; i < kScrSlots; ++i) {
             mbar_init(&sm->scr_full[i], kScrThreads / 32);
             mbar_init(&sm->scr_free[i], 1);
@@ -191,6 +195,12 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
         tmem_alloc(&sm->tmem_base, kTmemCols);
         tmem_relinquish();
     }
+    if (threadIdx.x == 64) {
+        prefetch_tensormap(&qn_map);
+        prefetch_tensormap(&qr_map);
+        prefetch_tensormap(&kv_map);
+    }
+    pdl_trigger();  // the join may be launched while this grid works; it waits for its end
     if (blockIdx.x == 0) report_lengths(p.t);
     tc_fence_before();
     find_share(p.t, p.mult, team, p.teams, &sm->share);  // ends with a block barrier
@@ -205,7 +215,6 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
     const bool work = s.start(p, sm->share);
 
     if (warp < 4) {
-        if (SCR) regs_down<kRegsCtl>();
         if (warp == 0 && work) {
             // -------------------------------------------------------- TMA
             const int boxes = kPtTok / p.t.box_rows;  // at most 16, one a lane
@@ -252,15 +261,18 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         for (int m = 0; m < 4; ++m) {
                             if (!mbar_wait(&sm->raw.empty[rs], rph ^ 1, kPtWait)) ok = false;
                             if (elect_one()) {
-                                if (m == 0) sm->raw.boxes[i & 1] = live;
-                                mbar_arrive_expect_tx(&sm->raw.full[rs], blk_bytes + (m == 0 ? blk_bytes / 8 : 0));
+                                if (m == 0) {
+                                    sm->raw.boxes[i & 1] = live;
+                                    mbar_arrive_expect_tx(&sm->raw.tile_full[i & 1], blk_bytes / 8);
+                                }
+                                mbar_arrive_expect_tx(&sm->raw.full[rs], blk_bytes);
                             }
                             __syncwarp();
                             boxes_of([&](int x, int yb) {
                                 tma_load_2d(raw_s + rs * kRawSlot + x * box_bytes, &kv_map, 128 * m, yb, &sm->raw.full[rs]);
                                 if (m == 0)
                                     tma_load_2d(sc_s + (i & 1) * kScaleSlot + x * (box_bytes / 8), &sc_map, kPtDl, yb,
-                                                &sm->raw.full[rs]);
+                                                &sm->raw.tile_full[i & 1]);
                             });
                             if (++rs == kRaw) {
                                 rs = 0;
@@ -332,8 +344,10 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         mbar_wait(&sm->pair_full[m], (i - 1) & 1, kPtWait);
                         mbar_wait(&sm->pair_free[m], (i - 1) & 1, kPtWait);  // the peer's arrivals too
                     }
-                if (RAW)
+                if (RAW) {
+                    for (uint32_t x = i > 2 ? i - 2 : 0; x < i; ++x) mbar_wait(&sm->raw.tile_full[x & 1], (x >> 1) & 1, kPtWait);
                     for (int x = 0; x < kRaw; ++x) mbar_wait(&sm->raw.full[x], x < rs ? rph : rph ^ 1, kPtWait);
+                }
                 if (seg > 0) mbar_wait(&sm->q_full, (seg - 1) & 1, kPtWait);
             }
             __syncwarp();
@@ -451,10 +465,9 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 for (int c = lane; c < p.cols; c += 32) p.lse[row0 + c] = -INFINITY;
             }
         }
-    } else if (warp < 12) {
-        if (SCR) regs_up<kRegsSoftmax>();
+    } else if (warp < 4 + 4 * kGroups) {
         if (work) {
-            // -------------------------------------------------------- softmax: one key a thread, 32 columns a group
+            // -------------------------------------------------------- softmax: one key a thread, kGrp columns a group
             const int grp = (warp - 4) >> 2, quad = warp & 3, cb = grp * kGrp, bar = 1 + grp;
             const int key = quad * 32 + lane, et = (threadIdx.x - 128) & 127;
             const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -571,10 +584,10 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     }
                     if (ROWS == kBf16Rows && !valid) {
                         // what lies behind the length may be NaN, which a weight of 0 would not hide: this
-                        // group's half of the key's latent blocks becomes 0 (S^T has read them)
+                        // group's share of the key's latent blocks becomes 0 (S^T has read them)
                         for (int m = 0; m < 4; ++m) mbar_wait(&sm->pair_full[m], i & 1, kPtWait);
 #pragma unroll 1
-                        for (int c = 4 * grp; c < 4 * grp + 4; ++c) {
+                        for (int c = grp * (8 / kGroups); c < (grp + 1) * (8 / kGroups); ++c) {
                             uint4 *r = reinterpret_cast<uint4 *>(kv_s + c * kPtBlk + key * 128);
 #pragma unroll
                             for (int k = 0; k < 8; ++k) r[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -655,18 +668,18 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
     } else if constexpr (RAW) {
         if (work) {
             // -------------------------------------------------------- raw rows expanded into the tile
-            const int d = threadIdx.x - 384;
+            const int d = threadIdx.x - kRow0;
             uint32_t i = 0, rph = 0;
             int rs = 0;
             bool ok = true;
             for (bool more = true; more && ok; more = s.next(p)) {
                 for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
-                    uint32_t live = 0;
+                    if (!mbar_wait(&sm->raw.tile_full[i & 1], (i >> 1) & 1, kPtWait)) ok = false;
+                    const uint32_t live = live_rows(p.t, sm->raw.boxes[i & 1], d, t, s.len);
                     const float *scales = reinterpret_cast<const float *>(sc_s + (i & 1) * kScaleSlot);
 #pragma unroll 1
                     for (int m = 0; m < 4; ++m) {
                         if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;
-                        if (m == 0) live = live_rows(p.t, sm->raw.boxes[i & 1], d, t, s.len);
                         RawStep x;
                         x.read(raw_s + rs * kRawSlot, scales, m, d, live);
                         if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) ok = false;
@@ -689,15 +702,14 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             if (!ok && lane == 0) fail();
         }
     } else if constexpr (SCR) {
-        regs_down<kRegsRows>();
         if (work) {
             // -------------------------------------------------------- rows expanded into the scratch
-            const int d = threadIdx.x - 384;
+            const int d = threadIdx.x - kRow0;
             uint8_t *scr = p.scratch + (int64_t)blockIdx.x * kScrSlots * kScrRows * kScrRow;
             const int off = peer * kScrRows;  // this CTA's half of a tile
-            ScrRows x;
-            x.set_rows(p.t, d, s.b, s.t0 * kPtTok + off, s.len);
-            x.load(p.t, d);
+            ScrRows x0, x1;
+            x0.load(p.t, d, 0, s.b, s.t0 * kPtTok + off, s.len);
+            x1.load(p.t, d, 1, s.b, s.t0 * kPtTok + off, s.len);
             uint32_t sph = 0;
             int ss = 0, t = s.t0;
             bool ok = true;
@@ -707,7 +719,10 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     t = s.t0;
                 }
                 if (!mbar_wait(&sm->scr_free[ss], sph ^ 1, kPtWait)) ok = false;
-                x.store(scr + ss * (kScrRows * kScrRow), d);
+                uint8_t *half = scr + ss * (kScrRows * kScrRow);
+                x0.store(half, d, 0);
+                if (more) x0.load(p.t, d, 0, s.b, t * kPtTok + off, s.len);
+                x1.store(half, d, 1);
                 asm volatile("fence.proxy.async.global;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->scr_full[ss]);
@@ -715,10 +730,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     ss = 0;
                     sph ^= 1;
                 }
-                if (more) {
-                    x.set_rows(p.t, d, s.b, t * kPtTok + off, s.len);
-                    x.load(p.t, d);
-                }
+                if (more) x1.load(p.t, d, 1, s.b, t * kPtTok + off, s.len);
                 ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
             }
             if (!ok && lane == 0) fail();
@@ -746,6 +758,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_mla_join_kernel(AParams p)
 {
     __shared__ float4 acc_s[W > 1 ? W - 1 : 1][128];
     __shared__ float wl[W];
+    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * (kJoinThreads / 32 / W) + warp / W;
     if (row >= (int64_t)p.t.B * p.cols) return;  // only with W == 1: whole warps leave, no barrier follows
@@ -856,19 +869,9 @@ nsa_status launch(const AParams &p, const Maps &m, cudaStream_t stream)
     constexpr auto kern = paged_mla_tc_kernel<ROWS, PAIR, NC>;
     constexpr int smem = (int)smem_of(ROWS, NC);
     NSA_CUDA_TRY(max_dynamic_smem<kern>(smem));
-    if (ROWS == kScratchRows) {
-        // the register split needs the registers the kernel was compiled to be launched with
-        static std::atomic<int> regs{0};
-        if (regs.load(std::memory_order_relaxed) == 0) {
-            cudaFuncAttributes fa;
-            NSA_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
-            regs.store(fa.numRegs, std::memory_order_relaxed);
-        }
-        if (regs.load(std::memory_order_relaxed) < kRegsLaunch) return NSA_ERR_UNSUPPORTED;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.teams * p.team));
-    cfg.blockDim = dim3(threads_of(ROWS));
+    cfg.blockDim = dim3(threads_of(ROWS, NC));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -881,11 +884,16 @@ nsa_status launch(const AParams &p, const Maps &m, cudaStream_t stream)
     NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, m.qn, m.qr, m.kv, m.sc, m.rope));
     // shares per request on average: below four, a warp joins a column faster than a block (both measured)
     const int64_t rows = (int64_t)p.t.B * p.cols;
-    if (p.teams < 4 * (int64_t)p.t.B * p.mult)
-        paged_mla_join_kernel<1><<<(unsigned)ceil_div(rows, kJoinThreads / 32), kJoinThreads, 0, stream>>>(p);
-    else
-        paged_mla_join_kernel<8><<<(unsigned)rows, kJoinThreads, 0, stream>>>(p);
-    return launch_status();
+    const bool few = p.teams < 4 * (int64_t)p.t.B * p.mult;
+    cudaLaunchConfig_t jc = {};
+    jc.gridDim = dim3((unsigned)(few ? ceil_div(rows, kJoinThreads / 32) : rows));
+    jc.blockDim = dim3(kJoinThreads);
+    jc.stream = stream;
+    attr[0] = pdl_attribute();
+    jc.attrs = attr;
+    jc.numAttrs = 1;
+    NSA_CUDA_TRY(few ? cudaLaunchKernelEx(&jc, paged_mla_join_kernel<1>, p) : cudaLaunchKernelEx(&jc, paged_mla_join_kernel<8>, p));
+    return NSA_OK;
 }
 
 }  // namespace

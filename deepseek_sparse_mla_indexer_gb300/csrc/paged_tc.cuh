@@ -69,6 +69,14 @@ __device__ __forceinline__ int64_t share_count(int64_t total, int parts)
     return total < 1 ? 1 : total < parts ? total : parts;
 }
 
+// total * k / np without a 64-bit division where the product fits 32 bits (shares of a decode
+// step do; the long division costs a few hundred cycles of every CTA's start).
+__device__ __forceinline__ int64_t share_start(int64_t total, int64_t k, int64_t np)
+{
+    const uint64_t x = (uint64_t)total * (uint64_t)k;
+    return x < 0x100000000ULL ? (int64_t)((uint32_t)x / (uint32_t)np) : (int64_t)(x / (uint64_t)np);
+}
+
 __device__ __forceinline__ void find_share(const PagedTc &p, int mult, int part, int parts, TileShare *sh)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
@@ -82,7 +90,8 @@ __device__ __forceinline__ void find_share(const PagedTc &p, int mult, int part,
     for (int w = 0; w < nw; ++w) total += sh->warp[w];
     // no more shares than tiles, so that every share that has a neighbour has a tile
     const int64_t np = share_count(total, parts);
-    const int64_t g0 = part < np ? total * part / np : total, g1 = part < np ? total * (part + 1) / np : total;
+    const int64_t g0 = part < np ? share_start(total, part, np) : total;
+    const int64_t g1 = part < np ? share_start(total, part + 1, np) : total;
     if (tid == 0) {
         sh->total = total;
         sh->g0 = g0;
@@ -158,27 +167,32 @@ constexpr int kMaxRaw = 4;
 
 struct RawShared {
     uint64_t full[kMaxRaw], empty[kMaxRaw];
-    uint32_t boxes[2];  // boxes of the tile (by parity) that were loaded
+    uint64_t tile_full[2];  // scales (and boxes) of the tile, by parity
+    uint32_t boxes[2];      // boxes of the tile that were loaded
 };
 
 // Thread d of kDqThreads expands rows d / 8 and d / 8 + 64, chunk d % 8 (16 codes) of a
 // step into blocks blk0 (chunks 0..3) and blk1; rows without a key become zeros.  Codes
-// 16k .. 16k+15 become chunks 2k, 2k+1 of the step's 16; lanes with k >= 4 store the
-// odd chunk first, so that eight neighbouring lanes store to eight distinct bank groups.
+// 16k .. 16k+15 become chunks 2k, 2k+1 of the step's 16; lanes with k >= 4 store the odd
+// chunk first, so that eight neighbouring lanes store to eight distinct bank groups.
+// (Two groups of half the threads that take turns by steps were 7 - 9 % slower.)
+constexpr int kDqRows = kPtTok * 8 / kDqThreads;
+
 struct RawStep {
-    uint4 w[2];
-    float sc[2];
+    uint4 w[kDqRows];
+    float sc[kDqRows];
 
     __device__ __forceinline__ void read(const uint8_t *raw, const float *scales, int m, int d, uint32_t live)
     {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = (d >> 3) + 64 * u;
-            w[u] = *reinterpret_cast<const uint4 *>(raw + r * 128 + 16 * (d & 7));
-            sc[u] = scales[4 * r + m];
-            if (!(live >> u & 1)) {
-                w[u] = make_uint4(0u, 0u, 0u, 0u);
-                sc[u] = 0.f;
+        for (int u = 0; u < kDqRows; ++u) {
+            const int r = (d >> 3) + kPtTok / kDqRows * u;
+            const bool on = live >> u & 1;
+            w[u] = make_uint4(0u, 0u, 0u, 0u);
+            sc[u] = 0.f;
+            if (on) {
+                w[u] = *reinterpret_cast<const uint4 *>(raw + r * 128 + 16 * (d & 7));
+                sc[u] = scales[4 * r + m];
             }
         }
     }
@@ -187,8 +201,8 @@ struct RawStep {
         const int k = d & 7, c0 = (2 * k) & 7;
         uint8_t *blk = k < 4 ? blk0 : blk1;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = (d >> 3) + 64 * u;
+        for (int u = 0; u < kDqRows; ++u) {
+            const int r = (d >> 3) + kPtTok / kDqRows * u;
             // the first store's half of the codes is chosen before it is expanded
             const uint2 a = k < 4 ? make_uint2(w[u].x, w[u].y) : make_uint2(w[u].z, w[u].w);
             const uint2 b = k < 4 ? make_uint2(w[u].z, w[u].w) : make_uint2(w[u].x, w[u].y);
@@ -198,13 +212,13 @@ struct RawStep {
     }
 };
 
-// Which of thread d's two rows of a tile hold a key (bit u: row d / 8 + 64 u).
+// Which of thread d's rows of a tile hold a key (bit u: row d / 8 + 64 u).
 __device__ __forceinline__ uint32_t live_rows(const PagedTc &p, uint32_t boxes, int d, int tile, int len)
 {
     uint32_t live = 0;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int r = (d >> 3) + 64 * u;
+    for (int u = 0; u < kDqRows; ++u) {
+        const int r = (d >> 3) + kPtTok / kDqRows * u;
         if (tile * kPtTok + r < len && (boxes >> (r / p.box_rows) & 1)) live |= 1u << u;
     }
     return live;
@@ -212,58 +226,44 @@ __device__ __forceinline__ uint32_t live_rows(const PagedTc &p, uint32_t boxes, 
 
 // Rows expanded from registers into a scratch copy of half a tile in global memory
 // (which stays in L2), for CTA pairs: thread d of kScrThreads owns rows d / 8 and
-// d / 8 + 32 of the CTA's 64 and chunk d % 8 of each step.  A step's registers are
-// loaded with the same step of the next tile as soon as it is stored.
+// d / 8 + 32 of the CTA's 64 and chunk d % 8 of each 128-value block.  A row's registers
+// are loaded with the same row of the next tile as soon as it is stored.
 constexpr int kScrThreads = 256;
 constexpr int kScrSlots = 3;                    // half tiles a CTA's scratch holds
 constexpr int kScrRow = 2 * (kPtDl + kPtDr);    // bytes
 constexpr int kScrRows = kPtTok / 2;
 
 struct ScrRows {
-    uint4 w[5][2];
-    float4 sc[2];
-    int slot[2];  // the rows that loads refer to; -1: a row of zeros
+    uint4 w[5];
+    float4 sc;
 
-    __device__ __forceinline__ void set_rows(const PagedTc &p, int d, int b, int pos0, int len)
+    // row u (0, 1) of thread d; pos0: the half tile's first position
+    __device__ __forceinline__ void load(const PagedTc &p, int d, int u, int b, int pos0, int len)
     {
-        const int32_t *pt = p.page_table + (int64_t)b * p.pt_ld;
+        const int pos = pos0 + (d >> 3) + 32 * u;
+        const int page = checked_page(p, p.page_table + (int64_t)b * p.pt_ld, pos, len);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int pos = pos0 + (d >> 3) + 32 * u;
-            const int page = checked_page(p, pt, pos, len);
-            slot[u] = page < 0 ? -1 : page * p.ps + pos % p.ps;
+        for (int m = 0; m < 5; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
+        sc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (page >= 0) {
+            const uint8_t *row = p.kv + ((int64_t)page * p.ps + pos % p.ps) * kPtFp8Row;
+#pragma unroll
+            for (int m = 0; m < 5; ++m)
+                w[m] = __ldg(reinterpret_cast<const uint4 *>(row + (m < 4 ? 128 * m : kPtDl + 16) + 16 * (d & 7)));
+            sc = __ldg(reinterpret_cast<const float4 *>(row + kPtDl));
         }
     }
-    __device__ __forceinline__ void load(const PagedTc &p, int d)
+    __device__ __forceinline__ void store(uint8_t *half, int d, int u) const
     {
+        uint8_t *row = half + ((d >> 3) + 32 * u) * kScrRow;
+        const float s[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-            for (int m = 0; m < 5; ++m) w[m][u] = make_uint4(0u, 0u, 0u, 0u);
-            sc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (slot[u] >= 0) {
-                const uint8_t *row = p.kv + (int64_t)slot[u] * kPtFp8Row;
-#pragma unroll
-                for (int m = 0; m < 5; ++m)
-                    w[m][u] = __ldg(reinterpret_cast<const uint4 *>(row + (m < 4 ? 128 * m : kPtDl + 16) + 16 * (d & 7)));
-                sc[u] = __ldg(reinterpret_cast<const float4 *>(row + kPtDl));
-            }
+        for (int m = 0; m < 4; ++m) {
+            uint4 *o = reinterpret_cast<uint4 *>(row + 256 * m + 32 * (d & 7));
+            o[0] = expand8(w[m].x, w[m].y, s[m]);
+            o[1] = expand8(w[m].z, w[m].w, s[m]);
         }
-    }
-    __device__ __forceinline__ void store(uint8_t *half, int d) const
-    {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            uint8_t *row = half + ((d >> 3) + 32 * u) * kScrRow;
-            const float s[4] = {sc[u].x, sc[u].y, sc[u].z, sc[u].w};
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                uint4 *o = reinterpret_cast<uint4 *>(row + 256 * m + 32 * (d & 7));
-                o[0] = expand8(w[m][u].x, w[m][u].y, s[m]);
-                o[1] = expand8(w[m][u].z, w[m][u].w, s[m]);
-            }
-            *reinterpret_cast<uint4 *>(row + 2 * kPtDl + 16 * (d & 7)) = w[4][u];
-        }
+        *reinterpret_cast<uint4 *>(row + 2 * kPtDl + 16 * (d & 7)) = w[4];
     }
 };
 

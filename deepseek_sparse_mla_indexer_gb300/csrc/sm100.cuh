@@ -297,21 +297,6 @@ __device__ __forceinline__ void bar_sync(int id, int nthreads)
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// ------------------------------------------------------------------ register split
-
-// Sets the calling warpgroup's registers per thread.  The shares of a block's warpgroups
-// may not exceed what it was launched with: an increase waits for registers others gave up.
-template <int N>
-__device__ __forceinline__ void regs_down()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_up()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // ------------------------------------------------------------------ one lane of a warp
 
 // True in one lane (always the same) of a converged warp.  Around an instruction that
