@@ -137,7 +137,12 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
         tmem_alloc(&sm->tmem_base, kTmemCols);
         tmem_relinquish();
     }
-    if (blockIdx.x == 0) report_lengths(p.t);
+    if (blockIdx.x == 0 && warp == 2) report_lengths(p.t, lane, 32);
+    if (threadIdx.x == 96) {
+        prefetch_tensormap(&qn_map);
+        prefetch_tensormap(&qr_map);
+        prefetch_tensormap(&kv_map);
+    }
     tc_fence_before();
     find_share(p.t, 1, blockIdx.x, gridDim.x, &sm->share);  // ends with a block barrier
     tc_fence_after();

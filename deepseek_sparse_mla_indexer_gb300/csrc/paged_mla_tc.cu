@@ -87,7 +87,7 @@ struct AParams {
     int4 *unit;                    // [B * mult] of each (request, group set): first and last share, whether the first began earlier
     float *part;                   // [2 * CTAs][slot_cols][512] raw accumulators
     float2 *part_ml;               // [2 * CTAs][slot_cols] maximum (log2 units) and sum
-    uint8_t *scratch;              // [CTAs][kScrSlots][64][576] bf16 (fp8 rows of CTA pairs)
+    uint8_t *scratch;              // [CTAs][kScrSlots][128 / cluster][576] bf16 (fp8 rows of clusters)
 };
 
 // The pieces of a share: tiles [t0, t1) of group set j of request b.
@@ -148,15 +148,17 @@ __device__ __forceinline__ void tmem_stg(uint32_t taddr, const uint32_t (&r)[G])
     else tmem_st8(taddr, r);
 }
 
-// NC: columns of the CTA's products (16, 32 or 64).
+// CL: CTAs of a cluster, which share their tiles; NC: columns of the CTA's products (16, 32 or 64).
 // kv_map: bf16 rows of the cache or of the scratch, or the fp8 codes; sc_map, rope_map: of raw rows.
-template <Rows ROWS, bool PAIR, int NC>
+template <Rows ROWS, int CL, int NC>
 __global__ void __launch_bounds__(threads_of(ROWS, NC), 1)
 paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
                     const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
                     const __grid_constant__ CUtensorMap rope_map)
 {
-    constexpr bool RAW = ROWS == kRawRows, SCR = ROWS == kScratchRows;
+    constexpr bool RAW = ROWS == kRawRows, SCR = ROWS == kScratchRows, PAIR = CL > 1;
+    constexpr uint16_t kAll = (1 << CL) - 1;  // every CTA of the cluster
+    constexpr int kScrRows = kPtTok / CL;     // rows of a tile that one CTA expands
     constexpr int kGrp = grp_of(NC), kGroups = NC / kGrp, kRow0 = row0_of(NC), kRaw = raw_slots(NC);
     constexpr uint32_t kQBlk = NC * 128;
     extern __shared__ uint8_t smem_raw[];
@@ -172,7 +174,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
     if (threadIdx.x == 0) {
         for (int m = 0; m < 5; ++m) {
             mbar_init(&sm->pair_full[m], RAW && m < 4 ? kDqThreads / 32 : 1);
-            mbar_init(&sm->pair_free[m], PAIR ? 2 : 1);
+            mbar_init(&sm->pair_free[m], CL);
         }
         mbar_init(&sm->q_full, 1);
         mbar_init(&sm->q_empty, 1);
@@ -201,7 +203,6 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
         prefetch_tensormap(&kv_map);
     }
     pdl_trigger();  // the join may be launched while this grid works; it waits for its end
-    if (blockIdx.x == 0) report_lengths(p.t);
     tc_fence_before();
     find_share(p.t, p.mult, team, p.teams, &sm->share);  // ends with a block barrier
     if (PAIR) cluster_sync_all();  // the peer's barriers are ready before anything reaches them
@@ -219,8 +220,8 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             // -------------------------------------------------------- TMA
             const int boxes = kPtTok / p.t.box_rows;  // at most 16, one a lane
             const uint32_t box_bytes = (uint32_t)p.t.box_rows * 128;
-            // a pair's boxes are shared out by halves of the tile
-            const int box0 = PAIR && peer == 1 ? boxes / 2 : 0, box1 = PAIR && peer == 0 ? boxes / 2 : boxes;
+            // a cluster's CTAs share out the boxes of a tile in order
+            const int box0 = boxes / CL * peer, box1 = boxes / CL * (peer + 1);
             constexpr uint32_t kRowBytes = ROWS == kBf16Rows ? 2 * (kPtDl + kPtDr) : kPtFp8Row;
             uint32_t i = 0, seg = 0, rph = 0, sph = 0;
             int rs = 0, ss = 0;
@@ -287,7 +288,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         });
                     } else {
                         if constexpr (SCR) {
-                            // this CTA's half of the tile is in its scratch: written by the row warps
+                            // this CTA's part of the tile is in its scratch: written by the row warps
                             if (!mbar_wait(&sm->scr_full[ss], sph, kPtWait)) ok = false;
                             asm volatile("fence.proxy.async.global;" ::: "memory");
                         }
@@ -296,7 +297,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                             if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) ok = false;
                             if (elect_one()) {
                                 mbar_arrive_expect_tx(&sm->pair_full[m], (m < 4 ? 2 : 1) * blk_bytes);
-                                // both CTAs are done with the tile before: its scratch may be written again
+                                // every CTA is done with the tile before: its scratch may be written again
                                 if (SCR && m == 4 && i > 0) mbar_arrive(&sm->scr_free[ss == 0 ? kScrSlots - 1 : ss - 1]);
                             }
                             __syncwarp();
@@ -304,9 +305,9 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                                 if (elect_one()) {
 #pragma unroll
                                     for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c)
-                                        tma_load_2d_multicast(kv_s + c * kPtBlk + peer * (kPtBlk / 2), &kv_map, 64 * c,
+                                        tma_load_2d_multicast(kv_s + c * kPtBlk + peer * (kPtBlk / CL), &kv_map, 64 * c,
                                                               ((int)blockIdx.x * kScrSlots + ss) * kScrRows,
-                                                              &sm->pair_full[m], 3);
+                                                              &sm->pair_full[m], kAll);
                                 }
                                 __syncwarp();
                             } else {
@@ -315,7 +316,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                                     for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c) {
                                         uint8_t *dst = kv_s + c * kPtBlk + x * box_bytes;
                                         if (PAIR)
-                                            tma_load_2d_multicast(dst, &kv_map, 64 * c, yb, &sm->pair_full[m], 3);
+                                            tma_load_2d_multicast(dst, &kv_map, 64 * c, yb, &sm->pair_full[m], kAll);
                                         else
                                             tma_load_2d(dst, &kv_map, 64 * c, yb, &sm->pair_full[m]);
                                     }
@@ -363,7 +364,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             const uint64_t p_desc = smem_desc(smem_u32(p_s), kPtBlk, 1024, kSwizzle128B);
             auto free_pair = [&](int m) {
                 if (PAIR)
-                    mma_commit_multicast(&sm->pair_free[m], 3);
+                    mma_commit_multicast(&sm->pair_free[m], kAll);
                 else
                     mma_commit(&sm->pair_free[m]);
             };
@@ -453,7 +454,8 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 before += __shfl_sync(0xffffffffu, inc, 31);
             }
         } else if (warp == 3) {
-            // -------------------------------------------------------- requests without a key
+            // -------------------------------------------------------- bad lengths, requests without a key
+            if (blockIdx.x == 0) report_lengths(p.t, lane, 32);
             for (int b = blockIdx.x; b < p.t.B; b += gridDim.x) {
                 if (request_len(p.t, b) > 0) continue;
                 const int64_t row0 = (int64_t)b * p.cols;
@@ -706,32 +708,52 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             // -------------------------------------------------------- rows expanded into the scratch
             const int d = threadIdx.x - kRow0;
             uint8_t *scr = p.scratch + (int64_t)blockIdx.x * kScrSlots * kScrRows * kScrRow;
-            const int off = peer * kScrRows;  // this CTA's half of a tile
-            ScrRows x0, x1;
-            x0.load(p.t, d, 0, s.b, s.t0 * kPtTok + off, s.len);
-            x1.load(p.t, d, 1, s.b, s.t0 * kPtTok + off, s.len);
+            const int off = peer * kScrRows;     // this CTA's part of a tile
+            constexpr int kSteps = kScrRows / 32;  // steps of 32 rows a tile
+            // the step to load next, two ahead of the one that is stored
+            Seg f = s;
+            int ft = f.t0, fu = 0;
+            bool fetch = true;
+            auto load = [&](ScrRows &x) {
+                if (!fetch) return;
+                x.load(p.t, d, f.b, ft * kPtTok + off + 32 * fu, f.len);
+                if (++fu == kSteps) {
+                    fu = 0;
+                    if (++ft >= f.t1) {
+                        fetch = f.next(p);
+                        ft = f.t0;
+                    }
+                }
+            };
+            int64_t left = (sm->share.g1 - sm->share.g0) * kSteps;
             uint32_t sph = 0;
-            int ss = 0, t = s.t0;
+            int ss = 0, u = 0;
             bool ok = true;
-            for (bool more = true; more && ok;) {
-                if (++t >= s.t1) {
-                    more = s.next(p);
-                    t = s.t0;
+            auto step = [&](ScrRows &x) {
+                if (u == 0 && !mbar_wait(&sm->scr_free[ss], sph ^ 1, kPtWait)) ok = false;
+                x.store(scr + (ss * kScrRows + 32 * u) * kScrRow, d);
+                if (++u == kSteps) {
+                    u = 0;
+                    asm volatile("fence.proxy.async.global;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm->scr_full[ss]);
+                    if (++ss == kScrSlots) {
+                        ss = 0;
+                        sph ^= 1;
+                    }
                 }
-                if (!mbar_wait(&sm->scr_free[ss], sph ^ 1, kPtWait)) ok = false;
-                uint8_t *half = scr + ss * (kScrRows * kScrRow);
-                x0.store(half, d, 0);
-                if (more) x0.load(p.t, d, 0, s.b, t * kPtTok + off, s.len);
-                x1.store(half, d, 1);
-                asm volatile("fence.proxy.async.global;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->scr_full[ss]);
-                if (++ss == kScrSlots) {
-                    ss = 0;
-                    sph ^= 1;
-                }
-                if (more) x1.load(p.t, d, 1, s.b, t * kPtTok + off, s.len);
+                load(x);
                 ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
+            };
+            ScrRows x0, x1;
+            load(x0);
+            load(x1);
+            while (left > 0 && ok) {
+                step(x0);
+                if (--left > 0 && ok) {
+                    step(x1);
+                    --left;
+                }
             }
             if (!ok && lane == 0) fail();
         }
@@ -827,11 +849,45 @@ __global__ void __launch_bounds__(kJoinThreads) paged_mla_join_kernel(AParams p)
     if (lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == l ? -INFINITY : l);
 }
 
+// Clusters of four scratch CTAs that the current device runs at once (asked once per device).
+int clusters_of_four()
+{
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> cache[kMaxDev];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDev) {
+        (void)cudaGetLastError();
+        return 1;
+    }
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    constexpr auto kern = paged_mla_tc_kernel<kScratchRows, 4, kCols>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(4);
+    cfg.blockDim = dim3(threads_of(kScratchRows, kCols));
+    cfg.dynamicSmemBytes = smem_of(kScratchRows, kCols);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 4;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (max_dynamic_smem<kern>((int)cfg.dynamicSmemBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();  // a failed query is not the caller's error
+        return 1;
+    }
+    cache[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // How the columns of a request are spread over CTAs: teams of the largest power of two
 // up to kMaxTeam that divides the number of 64-column groups, as many as the SMs hold and
 // the tiles fill.
 struct Plan {
     Rows rows;
+    int cluster;
     int cols, nc, groups, team, mult, teams, slot_cols;
     size_t head_bytes, ml_bytes, part_bytes, scratch_bytes;
 };
@@ -847,15 +903,19 @@ Plan make_plan(bool fp8, int R, int n, int H, int max_row_len, int sms)
     q.team = 1;
     while (q.team < kMaxTeam && q.groups % (2 * q.team) == 0) q.team *= 2;
     q.mult = q.groups / q.team;
+    // clusters of four halve what each CTA has to expand; bf16 rows gain nothing over pairs
+    q.cluster = q.rows == kScratchRows ? (q.team >= 4 && q.nc == kCols ? 4 : 2) : q.rows == kBf16Rows && q.team >= 2 ? 2 : 1;
     const int64_t most = (int64_t)(R / n) * q.mult * ceil_div(max_row_len, kPtTok);
-    const int fit = sms / q.team > 0 ? sms / q.team : 1;
+    // the CTAs of a wave: clusters of four leave SMs of some GPCs idle
+    const int ctas = q.cluster == 4 ? 4 * clusters_of_four() : sms;
+    const int fit = ctas / q.team > 0 ? ctas / q.team : 1;
     q.teams = (int)(most < fit ? most : fit);
     q.slot_cols = q.cols < q.nc ? q.cols : q.nc;
     const size_t slots = (size_t)q.teams * q.team * 2 * q.slot_cols;
     q.head_bytes = (size_t)(R / n) * q.mult * sizeof(int4);
     q.ml_bytes = (slots * sizeof(float2) + 15) / 16 * 16;
     q.part_bytes = slots * kPtDl * sizeof(float);
-    q.scratch_bytes = q.rows == kScratchRows ? (size_t)q.teams * q.team * kScrSlots * kScrRows * kScrRow : 0;
+    q.scratch_bytes = q.rows == kScratchRows ? (size_t)q.teams * q.team * kScrSlots * (kPtTok / q.cluster) * kScrRow : 0;
     return q;
 }
 
@@ -863,10 +923,10 @@ struct Maps {
     CUtensorMap qn, qr, kv, sc, rope;
 };
 
-template <Rows ROWS, bool PAIR, int NC>
+template <Rows ROWS, int CL, int NC>
 nsa_status launch(const AParams &p, const Maps &m, cudaStream_t stream)
 {
-    constexpr auto kern = paged_mla_tc_kernel<ROWS, PAIR, NC>;
+    constexpr auto kern = paged_mla_tc_kernel<ROWS, CL, NC>;
     constexpr int smem = (int)smem_of(ROWS, NC);
     NSA_CUDA_TRY(max_dynamic_smem<kern>(smem));
     cudaLaunchConfig_t cfg = {};
@@ -876,7 +936,7 @@ nsa_status launch(const AParams &p, const Maps &m, cudaStream_t stream)
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[0].val.clusterDim.x = CL;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -918,7 +978,7 @@ nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse,
     const Plan q = make_plan(fp8, a.R, a.rows_per_req, a.H, a.max_row_len, sms);
     AParams p;
     p.t = paged_tc_params(a);
-    if (p.t.box_rows > 64) p.t.box_rows = 64;  // half a tile for each CTA of a pair
+    while (p.t.box_rows > kPtTok / q.cluster) p.t.box_rows /= 2;  // whole boxes for each CTA of a cluster
     p.cols = q.cols; p.nc = q.nc; p.groups = q.groups; p.team = q.team; p.mult = q.mult; p.teams = q.teams;
     p.slot_cols = q.slot_cols;
     p.out = (__nv_bfloat16 *)out;
@@ -934,18 +994,19 @@ nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse,
         q.rows == kBf16Rows ? bf16_rows_map(a.kv, (uint64_t)a.num_pages * a.page_size, (uint32_t)p.t.box_rows, &m.kv)
         : q.rows == kRawRows
             ? fp8_maps(a, (uint32_t)p.t.box_rows, &m.kv, &m.sc, &m.rope)
-            : bf16_rows_map(p.scratch, (uint64_t)q.teams * q.team * kScrSlots * kScrRows, kScrRows, &m.kv);
+            : bf16_rows_map(p.scratch, (uint64_t)q.teams * q.team * kScrSlots * (kPtTok / q.cluster),
+                            (uint32_t)(kPtTok / q.cluster), &m.kv);
     if (!mapped) return NSA_ERR_CUDA;
-    switch (q.rows) {
-    case kRawRows: return q.nc == 16 ? launch<kRawRows, false, 16>(p, m, stream) : launch<kRawRows, false, 32>(p, m, stream);
-    case kScratchRows:
-        return q.nc == 32 ? launch<kScratchRows, true, 32>(p, m, stream) : launch<kScratchRows, true, 64>(p, m, stream);
-    default: break;
-    }
-    if (q.team >= 2) return launch<kBf16Rows, true, 64>(p, m, stream);
-    return q.nc == 16   ? launch<kBf16Rows, false, 16>(p, m, stream)
-           : q.nc == 32 ? launch<kBf16Rows, false, 32>(p, m, stream)
-                        : launch<kBf16Rows, false, 64>(p, m, stream);
+    if (q.rows == kRawRows)
+        return q.nc == 16 ? launch<kRawRows, 1, 16>(p, m, stream) : launch<kRawRows, 1, 32>(p, m, stream);
+    if (q.rows == kScratchRows)
+        return q.nc == 32          ? launch<kScratchRows, 2, 32>(p, m, stream)
+               : q.cluster == 2 ? launch<kScratchRows, 2, 64>(p, m, stream)
+                                : launch<kScratchRows, 4, 64>(p, m, stream);
+    if (q.cluster == 2) return launch<kBf16Rows, 2, 64>(p, m, stream);
+    return q.nc == 16   ? launch<kBf16Rows, 1, 16>(p, m, stream)
+           : q.nc == 32 ? launch<kBf16Rows, 1, 32>(p, m, stream)
+                        : launch<kBf16Rows, 1, 64>(p, m, stream);
 }
 
 }  // namespace nsa

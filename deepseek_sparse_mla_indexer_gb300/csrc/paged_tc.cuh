@@ -46,10 +46,10 @@ __device__ __forceinline__ int request_len(const PagedTc &p, int b)
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kPtTok - 1) / kPtTok; }
 
-// Reports row lengths out of range (one CTA does it for the launch).
-__device__ __forceinline__ void report_lengths(const PagedTc &p)
+// Reports row lengths out of range (some threads of one CTA do it for the launch).
+__device__ __forceinline__ void report_lengths(const PagedTc &p, int thread, int threads)
 {
-    for (int64_t r = threadIdx.x; r < (int64_t)p.B * p.n; r += blockDim.x) {
+    for (int64_t r = thread; r < (int64_t)p.B * p.n; r += threads) {
         const int L = p.row_len[r];
         if (L < 0 || L > p.max_row_len) set_status(p.status, NSA_ERR_BOUNDS);
     }
@@ -224,23 +224,22 @@ __device__ __forceinline__ uint32_t live_rows(const PagedTc &p, uint32_t boxes, 
     return live;
 }
 
-// Rows expanded from registers into a scratch copy of half a tile in global memory
-// (which stays in L2), for CTA pairs: thread d of kScrThreads owns rows d / 8 and
-// d / 8 + 32 of the CTA's 64 and chunk d % 8 of each 128-value block.  A row's registers
-// are loaded with the same row of the next tile as soon as it is stored.
+// Rows expanded from registers into a scratch copy of a CTA's part of the tile in global
+// memory (which stays in L2), for clusters: thread d of kScrThreads owns chunk d % 8 of each
+// 128-value block of row d / 8 of 32.  Two sets of registers take turns, so a row is loaded
+// while the one before it is expanded.
 constexpr int kScrThreads = 256;
-constexpr int kScrSlots = 3;                    // half tiles a CTA's scratch holds
+constexpr int kScrSlots = 3;                    // parts of tiles a CTA's scratch holds
 constexpr int kScrRow = 2 * (kPtDl + kPtDr);    // bytes
-constexpr int kScrRows = kPtTok / 2;
 
 struct ScrRows {
     uint4 w[5];
     float4 sc;
 
-    // row u (0, 1) of thread d; pos0: the half tile's first position
-    __device__ __forceinline__ void load(const PagedTc &p, int d, int u, int b, int pos0, int len)
+    // pos0: the position of row 0 of the 32
+    __device__ __forceinline__ void load(const PagedTc &p, int d, int b, int pos0, int len)
     {
-        const int pos = pos0 + (d >> 3) + 32 * u;
+        const int pos = pos0 + (d >> 3);
         const int page = checked_page(p, p.page_table + (int64_t)b * p.pt_ld, pos, len);
 #pragma unroll
         for (int m = 0; m < 5; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
@@ -253,9 +252,9 @@ struct ScrRows {
             sc = __ldg(reinterpret_cast<const float4 *>(row + kPtDl));
         }
     }
-    __device__ __forceinline__ void store(uint8_t *half, int d, int u) const
+    __device__ __forceinline__ void store(uint8_t *rows, int d) const
     {
-        uint8_t *row = half + ((d >> 3) + 32 * u) * kScrRow;
+        uint8_t *row = rows + (d >> 3) * kScrRow;
         const float s[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
