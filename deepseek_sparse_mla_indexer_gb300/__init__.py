@@ -433,19 +433,22 @@ def nsa_local_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
 
 # ---------------------------------------------------------------- dense paged MLA attention
 
+_Q_TYPES = {DT_F32: torch.float32, DT_BF16: torch.bfloat16}
+
+
 def _paged_q(q_dtype: int, q_nope: torch.Tensor, q_rope: torch.Tensor):
     """The query arguments of the C calls; a single row's or head's stride, which is
     arbitrary, is replaced by what a packed tensor would have."""
     R, H, dl = q_nope.shape
-    dr = q_rope.shape[2]
-    if tuple(q_rope.shape[:2]) != (R, H):
+    Rr, Hr, dr = q_rope.shape
+    if Rr != R or Hr != H:
         raise ValueError(f"q_rope {tuple(q_rope.shape)} does not match q_nope {tuple(q_nope.shape)}")
-    if (dl > 1 and q_nope.stride(2) != 1) or (dr > 1 and q_rope.stride(2) != 1):
+    sn, sr = q_nope.stride(), q_rope.stride()
+    if (dl > 1 and sn[2] != 1) or (dr > 1 and sr[2] != 1):
         raise ValueError("the elements of each query head must be adjacent (stride 1 in the last dimension)")
-    want = {DT_F32: torch.float32, DT_BF16: torch.bfloat16}.get(q_dtype)
+    want = _Q_TYPES.get(q_dtype)
     if q_nope.dtype != want or q_rope.dtype != want:
         raise ValueError(f"q must be {want} for this q_dtype, got {q_nope.dtype} and {q_rope.dtype}")
-    sn, sr = q_nope.stride(), q_rope.stride()
     hn, hr = (sn[1], sr[1]) if H > 1 else (dl, dr)
     rn, rr = (sn[0], sr[0]) if R > 1 else (H * hn, H * hr)
     return q_nope.data_ptr(), rn, hn, q_rope.data_ptr(), rr, hr
@@ -453,11 +456,14 @@ def _paged_q(q_dtype: int, q_nope: torch.Tensor, q_rope: torch.Tensor):
 
 def _paged_cache(kv_dtype: int, kv: torch.Tensor, page_size: int, d_latent: int, d_rope: int) -> int:
     """Checks a cache of [slots, row] (or [pages, page_size, row]) and returns its page count."""
-    want = {DT_F32: 4 * (d_latent + d_rope), DT_BF16: 2 * (d_latent + d_rope),
-            DT_E4M3: d_latent + 4 * (d_latent // 128) + 2 * d_rope}[kv_dtype]
-    if not kv.is_contiguous() or kv.dim() not in (2, 3) or kv.shape[-1] * kv.element_size() != want:
+    if kv_dtype == DT_E4M3:
+        want = d_latent + 4 * (d_latent // 128) + 2 * d_rope
+    else:
+        want = (4 if kv_dtype == DT_F32 else 2) * (d_latent + d_rope)
+    row = kv.shape[-1]
+    if not kv.is_contiguous() or kv.dim() not in (2, 3) or row * kv.element_size() != want:
         raise ValueError(f"the cache must be contiguous rows of {want} bytes, got shape {tuple(kv.shape)} of {kv.dtype}")
-    slots = kv.numel() // kv.shape[-1]
+    slots = kv.numel() // row
     if page_size < 1 or slots % page_size:
         raise ValueError(f"{slots} slots are no whole pages of {page_size}")
     return slots // page_size

@@ -18,27 +18,30 @@ using namespace sm100;
 // ------------------------------------------------------------------ select
 //
 // One thread-block cluster per request; its CTAs own equal slices of the
-// positions and its warps contiguous parts of them, a key per lane and step, kept
-// in registers (slices up to 32 K; longer ones are read again from L2).  The
+// positions and its warps contiguous parts of them, a key per lane and step.  The
 // threshold key of the middle range is found by a radix selection over 11 + 11 +
-// 10 bits of the order-preserving key: each CTA counts its slice's digits in
-// shared memory, and after one cluster barrier every CTA sums all counts
-// (distributed shared memory) and finds the same digit, so a pass costs one
-// barrier.  Then every CTA writes its kept positions behind those of the CTAs
-// before it: positions above the threshold, and of those equal to it the lowest
-// ones.  The totals are read from HBM once.  Whole numbers throughout: the result
-// does not depend on scheduling.  Bound by the latency of its dozen dependent
-// steps, not by its bytes.
+// 10 bits of the order-preserving key.  Pass 0 counts the leading digits of all
+// keys in shared memory; after a cluster barrier every CTA sums the counts of all
+// (distributed shared memory) and finds the same digit.  The keys with that digit,
+// some per cent of them, go into a list in shared memory, from which passes 1 and 2
+// count; where they do not fit (totals that are mostly equal) the passes run over
+// all keys again.  Then every CTA writes its kept positions behind those of the
+// CTAs before it: positions above the threshold, and of those equal to it the
+// lowest ones.  Keys stay in shared memory (slices up to 40 K; longer ones are read
+// again from L2).  Whole numbers throughout: the result does not depend on
+// scheduling.  Bound by the latency of its dozen dependent steps, not by its bytes.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelKeys = 16;              // keys a thread holds in registers (or twice as many)
 constexpr int kSelMaxCluster = 8;         // the portable limit
-constexpr int kSelSlice = kSelThreads * kSelKeys;
+constexpr int kSelSlice = 16 * 1024;      // positions a CTA takes while the clusters run in one wave
+constexpr int kSelCache = 40 * 1024;      // keys that fit in shared memory
+constexpr int kSelList = 2048;
 
 struct SelShared {
     alignas(16) uint32_t hist[3][2048];    // one per pass: none is cleared while a peer may read it
+    uint32_t list[kSelList];               // keys that share the threshold's first digit
     uint32_t scan[kSelWarps];
-    uint32_t digit, need;
+    uint32_t digit, need, listed;
     uint32_t warp_sure[kSelWarps], warp_eq[kSelWarps];
     uint32_t cta_sure, cta_eq;             // this CTA's counts, read by the others
 };
@@ -68,12 +71,13 @@ __device__ __forceinline__ void count_digit(uint32_t *hist, uint32_t bin, bool o
     }
 }
 
-// KEYS: keys a thread holds (0: they are read from L2 in every pass).
-template <int KEYS>
+// CACHED: the slice's keys are kept in shared memory, [slice rounded up to 1024].
+template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, int max_len, int sinks, int recent,
                     int budget, int slice, int32_t *keep, int64_t keep_ld, int32_t *new_len, int32_t *status)
 {
+    extern __shared__ uint32_t key_s[];
     __shared__ SelShared sm;
     const int nc = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
     const int b = blockIdx.x / nc;
@@ -92,56 +96,82 @@ evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, i
     const float *row = total + (int64_t)b * total_ld;
     const int mid0 = sinks, mid1 = L - recent;  // the middle range; sinks + recent <= budget < L
     const int p0 = min(L, rank * slice), p1 = min(L, p0 + slice);
-    // this warp's part: steps of 32 consecutive positions from w0
+    // this warp's part: steps of 32 consecutive positions; lane's position and key of step j
     const int steps = (p1 - p0 + kSelThreads - 1) / kSelThreads;
-    const int w0 = p0 + warp * steps * 32 + lane;  // position of this lane in step 0
+    const int w0 = p0 + warp * steps * 32 + lane;
+    uint32_t *mine = key_s + warp * steps * 32 + lane;
     auto in_mid = [&](int pos) { return pos < p1 && pos >= mid0 && pos < mid1; };
-    constexpr bool REGS = KEYS > 0;
-    uint32_t key[REGS ? KEYS : 1];
-    uint32_t mid_bits = 0;  // steps whose position lies in the middle range
-    if constexpr (REGS) {
-#pragma unroll
-        for (int j = 0; j < KEYS; ++j) {
-            const int pos = w0 + 32 * j;
-            const bool on = j < steps && in_mid(pos);
-            mid_bits |= (uint32_t)on << j;
-            key[j] = on ? __float_as_uint(__ldg(row + pos)) : 0u;
-        }
-    }
-    for (int i = tid; i < 3 * 2048 / 4; i += kSelThreads) reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (REGS) {
-#pragma unroll
-        for (int j = 0; j < KEYS; ++j) key[j] = order_key(__uint_as_float(key[j]));
-    }
-    // f(position, key, whether in the middle range) for every step of the warp, all lanes together
-    auto each = [&](auto f) {
-        if constexpr (REGS) {
-#pragma unroll
-            for (int j = 0; j < KEYS; ++j)
-                if (j < steps) f(w0 + 32 * j, key[j], (mid_bits >> j & 1) != 0);
-        } else {
-            for (int j = 0; j < steps; ++j) {
-                const int pos = w0 + 32 * j;
-                const bool on = in_mid(pos);
-                f(pos, on ? order_key(__ldg(row + pos)) : 0u, on);
-            }
-        }
+    auto sync_cluster = [&]() {
+        if (nc > 1)
+            cluster_sync_all();
+        else
+            __syncthreads();
     };
+    auto key_at = [&](int j) -> uint32_t {
+        return CACHED ? mine[32 * j] : in_mid(w0 + 32 * j) ? order_key(__ldg(row + w0 + 32 * j)) : 0u;
+    };
+    for (int i = tid; i < 3 * 2048 / 4; i += kSelThreads) reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) sm.listed = 0;
     __syncthreads();
 
     uint32_t need = (uint32_t)(budget - sinks - recent), prefix = 0;
     const bool any = need > 0;  // else nothing between the ends is kept
     if (any) {
+        constexpr int kAhead = 8;  // loads in flight a thread
+        for (int j0 = 0; j0 < steps; j0 += kAhead) {
+            float v[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int pos = w0 + 32 * (j0 + u);
+                v[u] = j0 + u < steps && in_mid(pos) ? __ldg(row + pos) : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (j0 + u >= steps) break;
+                const bool on = in_mid(w0 + 32 * (j0 + u));
+                const uint32_t k = on ? order_key(v[u]) : 0u;
+                if (CACHED) mine[32 * (j0 + u)] = k;
+                count_digit(sm.hist[0], k >> 21, on, lane);
+            }
+        }
+        bool listed = false;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const uint32_t mask = pass == 2 ? 1023u : 2047u;
             uint32_t *hist = sm.hist[pass];
-            each([&](int, uint32_t k, bool mid) {
-                const bool on = mid && (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == prefix);
-                if (pass == 0 || __any_sync(0xffffffffu, on)) count_digit(hist, (k >> shift) & mask, on, lane);
-            });
-            cluster_sync_all();  // every CTA's counts are complete
+            if (pass > 0) {
+                const int shift = pass == 1 ? 10 : 0, above_shift = pass == 1 ? 21 : 10;
+                const uint32_t mask = pass == 1 ? 2047u : 1023u;
+                if (pass == 1) {
+                    // the keys of the threshold's first digit into the list
+#pragma unroll 4
+                    for (int j = 0; j < steps; ++j) {
+                        const uint32_t k = key_at(j);
+                        const bool on = (k >> 21) == prefix && in_mid(w0 + 32 * j);
+                        const uint32_t who = __ballot_sync(0xffffffffu, on);
+                        if (who) {
+                            uint32_t at = 0;
+                            if (lane == 0) at = atomicAdd(&sm.listed, (uint32_t)__popc(who));
+                            at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
+                            if (on && at < kSelList) sm.list[at] = k;
+                        }
+                    }
+                    __syncthreads();
+                    listed = sm.listed <= kSelList;
+                }
+                if (listed) {
+                    for (uint32_t i = tid; i < sm.listed; i += kSelThreads) {
+                        const uint32_t k = sm.list[i];
+                        if ((k >> above_shift) == prefix) atomicAdd(hist + ((k >> shift) & mask), 1u);
+                    }
+                } else {
+                    for (int j = 0; j < steps; ++j) {
+                        const uint32_t k = key_at(j);
+                        const bool on = (k >> above_shift) == prefix && in_mid(w0 + 32 * j);
+                        if (__any_sync(0xffffffffu, on)) count_digit(hist, (k >> shift) & mask, on, lane);
+                    }
+                }
+            }
+            sync_cluster();  // every CTA's counts are complete
             // bins 2 tid, 2 tid + 1 over the cluster, then counts from the top
             uint2 c = make_uint2(0u, 0u);
             for (int q = 0; q < nc; ++q) {
@@ -173,17 +203,23 @@ evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, i
         }
     }
     const uint32_t threshold = prefix;
-    auto classify = [&](int pos, uint32_t k, bool mid, bool &sure, bool &eq) {
+    auto classify = [&](int j, bool &sure, bool &eq) {
+        const int pos = w0 + 32 * j;
+        const bool mid = in_mid(pos);
+        const uint32_t k = any ? key_at(j) : 0u;
         sure = pos < p1 && (!mid || (any && k > threshold));
         eq = mid && any && k == threshold;
     };
     uint32_t n_sure = 0, n_eq = 0;
-    each([&](int pos, uint32_t k, bool mid) {
+#pragma unroll 4
+    for (int j = 0; j < steps; ++j) {
         bool sure, eq;
-        classify(pos, k, mid, sure, eq);
-        n_sure += __popc(__ballot_sync(0xffffffffu, sure));
-        n_eq += __popc(__ballot_sync(0xffffffffu, eq));
-    });
+        classify(j, sure, eq);
+        n_sure += sure;
+        n_eq += eq;
+    }
+    n_sure = __reduce_add_sync(0xffffffffu, n_sure);
+    n_eq = __reduce_add_sync(0xffffffffu, n_eq);
     if (lane == 0) {
         sm.warp_sure[warp] = n_sure;
         sm.warp_eq[warp] = n_eq;
@@ -207,16 +243,17 @@ evict_select_kernel(const float *total, int64_t total_ld, const int32_t *lens, i
         eq_before += __reduce_add_sync(0xffffffffu, ce);
     }
     // a position's place: the sure ones before it plus the equal ones taken before it
-    each([&](int pos, uint32_t k, bool mid) {
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
+    for (int j = 0; j < steps; ++j) {
         bool sure, eq;
-        classify(pos, k, mid, sure, eq);
-        const uint32_t below = (1u << lane) - 1u;
+        classify(j, sure, eq);
         const uint32_t bs = __ballot_sync(0xffffffffu, sure), be = __ballot_sync(0xffffffffu, eq);
         const uint32_t e = eq_before + __popc(be & below);
-        if (sure || (eq && e < need)) out[sure_before + __popc(bs & below) + min(e, need)] = pos;
+        if (sure || (eq && e < need)) out[sure_before + __popc(bs & below) + min(e, need)] = w0 + 32 * j;
         eq_before += __popc(be);
         sure_before += __popc(bs);
-    });
+    }
     if (rank == 0 && tid == 0) new_len[b] = budget;
     if (nc > 1) cluster_sync_all();  // a peer may still read this CTA's counts
 }
@@ -233,6 +270,7 @@ int select_clusters(int nc)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)nc);
     cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = kSelSlice * 4;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)nc;
@@ -240,7 +278,8 @@ int select_clusters(int nc)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, evict_select_kernel<kSelKeys>, &cfg) != cudaSuccess || n < 1) {
+    if (max_dynamic_smem<evict_select_kernel<true>>(kSelCache * 4) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, evict_select_kernel<true>, &cfg) != cudaSuccess || n < 1) {
         (void)cudaGetLastError();  // a failed query is not the caller's error
         n = 1;
     }
@@ -518,9 +557,12 @@ extern "C" nsa_status nsa_evict_select(const float *total_dev, int64_t total_ld,
     if (nc > 1 && B > select_clusters(nc) && (int64_t)nc * kSelSlice >= max_len) nc /= 2;
     if ((int64_t)B * nc > 0x7fffffffLL) return NSA_ERR_UNSUPPORTED;
     const int slice = max_len > 0 ? (int)ceil_div(max_len, nc) : 1;
+    const int cache = (int)ceil_div(slice, kSelThreads) * kSelThreads;
+    const bool cached = cache <= kSelCache;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(B * nc));
     cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = cached ? (size_t)cache * 4 : 0;
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -529,11 +571,10 @@ extern "C" nsa_status nsa_evict_select(const float *total_dev, int64_t total_ld,
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto kern = slice <= kSelSlice       ? evict_select_kernel<kSelKeys>
-                : slice <= 2 * kSelSlice ? evict_select_kernel<2 * kSelKeys>
-                                         : evict_select_kernel<0>;
-    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, total_dev, total_ld, len_dev, max_len, sinks, recent, budget, slice,
-                                    keep_dev, keep_ld, new_len_dev, status_dev));
+    if (cached) NSA_CUDA_TRY(max_dynamic_smem<evict_select_kernel<true>>(kSelCache * 4));
+    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, cached ? evict_select_kernel<true> : evict_select_kernel<false>, total_dev,
+                                    total_ld, len_dev, max_len, sinks, recent, budget, slice, keep_dev, keep_ld,
+                                    new_len_dev, status_dev));
     return NSA_OK;
 }
 

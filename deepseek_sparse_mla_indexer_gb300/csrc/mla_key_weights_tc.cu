@@ -183,6 +183,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                     const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
                     const uint32_t bytes = __popc(live) * box_bytes;
                     const int y_first = __shfl_sync(0xffffffffu, y, 0);
+                    // (bringing later tiles into L2 from here as well made bf16 rows a quarter slower)
                     const int y_next = box_row(t + 1);  // its latency under this tile's waits
                     // one lane issues a box at a time from uniform registers
                     auto boxes_of = [&](auto issue) {

@@ -943,6 +943,7 @@ nsa_status launch(const AParams &p, const Maps &m, cudaStream_t stream)
     cfg.numAttrs = 1;
     NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, m.qn, m.qr, m.kv, m.sc, m.rope));
     // shares per request on average: below four, a warp joins a column faster than a block (both measured)
+    if (p.teams == 1) return NSA_OK;  // every unit was one share's: nothing to join
     const int64_t rows = (int64_t)p.t.B * p.cols;
     const bool few = p.teams < 4 * (int64_t)p.t.B * p.mult;
     cudaLaunchConfig_t jc = {};
