@@ -303,14 +303,16 @@ int select_clusters(int nc)
 //
 // Bound by HBM: every row that moves is read and written once; rows that stay are
 // not touched.  A chunk is a chain of dependent loads (ticket, lengths, kept
-// positions, pages, rows), so the chain of a CTA's next chunk is walked while the
-// rows of the current one are on their way, and several CTAs share an SM.
+// positions, pages, rows).  Four warps walk it for the CTA's next chunk while the
+// other four move the current one, whose rows go through shared memory as bulk
+// copies (a thread issues one copy a row and array), and several CTAs share an SM.
 constexpr int kMaxArrays = 8;
-constexpr int kCpThreads = 256;
+constexpr int kCpThreads = 256;          // warps 0..3 move a chunk, warps 4..7 describe the next one
+constexpr int kMovers = 128;
 constexpr int kCpMinT = 8, kCpMaxT = 128;
 constexpr int kCpTail = 4096;            // totals cleared by one chunk
-constexpr int kCpStage = 44 * 1024;      // bytes staged per CTA: five CTAs per SM
-constexpr int kCpPerSm = 5;
+constexpr int kCpStage = 44 * 1024;      // bytes staged per CTA at most, where a chunk of kCpMinT allows it
+constexpr int kCpPerSm = 8;              // CTAs per SM at most
 constexpr int kCpMaxRow = 24 * 1024;     // bytes of one position over all arrays
 constexpr long long kCpWait = 2000000000LL;  // ~1 s of SM clocks
 
@@ -322,6 +324,7 @@ struct CompactParams {
     uint32_t magic[kMaxArrays]; // ceil(2^32 / per): step / per is its high product; 0: divide
     int offset[kMaxArrays];     // of the array's rows within the stage
     int n_arrays;
+    int bulk_bytes;             // bytes of a position in the arrays of unit 16
     const int32_t *keep;
     int64_t keep_ld;
     const int32_t *new_len, *old_len;
@@ -372,12 +375,13 @@ struct Chunk {
     int lo, hi;                          // destination positions
     int w0, w1;                          // chunks w0 .. w1-1 read from there
     int run;                             // 0: nothing to do
+    int moving;                          // rows that move
 };
 
-// The chunk of `ticket` (all threads; ends without a barrier).
+// The chunk of `ticket`, by warps 4..7: two walk the rows, two look for the chunks to wait for.
 __device__ __forceinline__ void describe(const CompactParams &p, Chunk &k, int ticket)
 {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
     // tickets go round the requests first: a chunk's predecessors are then well ahead of it
     const int rows = p.B * p.chunks;
     const bool tail = ticket >= rows;
@@ -385,73 +389,75 @@ __device__ __forceinline__ void describe(const CompactParams &p, Chunk &k, int t
     const int c = x / p.B, b = x - c * p.B;
     const int old = p.old_len[b], n = p.new_len[b];
     const bool bad = old < 0 || old > p.max_len || n < 0 || n > old || n > p.budget;
-    if (bad && tid == 0 && c == 0 && !tail) set_status(p.status, NSA_ERR_BOUNDS);
     const int lo = tail ? max(n, c * kCpTail) : c * p.T;
     const int hi = tail ? min(old, (c + 1) * kCpTail) : min(n, lo + p.T);
     const bool run = !bad && n < old && lo < hi && (!tail || p.total);
     const int32_t *keep = p.keep + (int64_t)b * p.keep_ld;
-    if (tid < p.T) {
-        int64_t s = -1, d = -1;
-        int32_t from = -2;
-        const int i = lo + tid;
-        if (run && !tail && i < hi) {
-            const int32_t *pt = p.page_table + (int64_t)b * p.pt_ld;
-            const int q = keep[i];
-            from = q;
-            if (q < i || q >= old || (i > 0 && keep[i - 1] >= q)) {
-                set_status(p.status, NSA_ERR_BOUNDS);  // not an ascending list of positions: the row stays
-                from = i;
-            } else if (q != i && p.n_arrays > 0) {
-                const int32_t ps = pt[q / p.page_size], pd = pt[i / p.page_size];
-                if (ps < 0 || ps >= p.num_pages || pd < 0 || pd >= p.num_pages) {
-                    set_status(p.status, NSA_ERR_BOUNDS);
-                } else {
-                    s = (int64_t)ps * p.page_size + q % p.page_size;
-                    d = (int64_t)pd * p.page_size + i % p.page_size;
+    if (warp < 2) {
+        const int32_t *pt = p.page_table + (int64_t)b * p.pt_ld;
+        for (int r = warp * 32 + lane; r < p.T; r += 64) {
+            int64_t s = -1, d = -1;
+            int32_t from = -2;
+            const int i = lo + r;
+            if (run && !tail && i < hi) {
+                const int q = keep[i], before = i > 0 ? keep[i - 1] : -1;
+                from = q;
+                if (q < i || q >= old || before >= q) {
+                    set_status(p.status, NSA_ERR_BOUNDS);  // not an ascending list of positions: the row stays
+                    from = i;
+                } else if (q != i && p.n_arrays > 0) {
+                    const int sp = q / p.page_size, dp = i / p.page_size;
+                    const int32_t ps = pt[sp], pd = pt[dp];
+                    if (ps < 0 || ps >= p.num_pages || pd < 0 || pd >= p.num_pages) {
+                        set_status(p.status, NSA_ERR_BOUNDS);
+                    } else {
+                        s = (int64_t)ps * p.page_size + (q - sp * p.page_size);
+                        d = (int64_t)pd * p.page_size + (i - dp * p.page_size);
+                        atomicAdd(&k.moving, 1);
+                    }
                 }
             }
+            k.src[r] = s;
+            k.dst[r] = d;
+            k.from[r] = from;
         }
-        k.src[tid] = s;
-        k.dst[tid] = d;
-        k.from[tid] = from;
-    }
-    // rows j with lo <= keep[j] < hi are read from the destination range, by chunks j / T
-    int w = 0;
-    if (warp >= kCpThreads / 32 - 2) {
-        const bool second = warp == kCpThreads / 32 - 1;
+    } else {
+        // rows j with lo <= keep[j] < hi are read from the destination range, by chunks j / T
+        const bool second = warp == 3;
         const int j = run ? warp_lower_bound(keep, n, second ? hi : lo, lane) : 0;
-        w = second ? (j + p.T - 1) / p.T : j / p.T;
-        if (lane == 0) (second ? k.w1 : k.w0) = w;
-    }
-    if (tid == 0) {
-        k.b = b;
-        k.c = tail ? -c - 1 : c;
-        k.lo = lo;
-        k.hi = hi;
-        k.run = run ? 1 : 0;
+        if (lane == 0) {
+            if (second) {
+                k.w1 = (j + p.T - 1) / p.T;
+                if (bad && c == 0 && !tail) set_status(p.status, NSA_ERR_BOUNDS);
+            } else {
+                k.w0 = j / p.T;
+                k.b = b;
+                k.c = tail ? -c - 1 : c;
+                k.lo = lo;
+                k.hi = hi;
+                k.run = run ? 1 : 0;
+            }
+        }
     }
 }
 
 template <int UNIT> struct CopyUnit;
-template <> struct CopyUnit<16> { using type = uint4; };
 template <> struct CopyUnit<4> { using type = uint32_t; };
 template <> struct CopyUnit<1> { using type = uint8_t; };
 
-// Rows of one array between the cache and the stage.
+// Rows of one array of 4-byte or odd rows between the cache and the stage.
 template <int UNIT, bool READ>
 __device__ __forceinline__ void move_rows(uint8_t *array, int row_bytes, uint32_t per, uint32_t magic, uint8_t *stage,
                                           const int64_t *slot, int T)
 {
     using U = typename CopyUnit<UNIT>::type;
-    for (uint32_t e = threadIdx.x; e < T * per; e += kCpThreads) {
+    for (uint32_t e = threadIdx.x; e < T * per; e += kMovers) {
         const uint32_t i = magic ? __umulhi(e, magic) : e / per, c = e - i * per;
         const int64_t at = slot[i];
         if (at < 0) continue;
         U *g = reinterpret_cast<U *>(array + at * row_bytes) + c;
         U *s = reinterpret_cast<U *>(stage) + e;  // rows of the stage follow one another
-        if constexpr (READ && UNIT == 16)
-            cp_async16(s, g);
-        else if constexpr (READ && UNIT == 4)
+        if constexpr (READ && UNIT == 4)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s)), "l"(g) : "memory");
         else if constexpr (READ)
             *s = __ldcg(g);
@@ -460,15 +466,27 @@ __device__ __forceinline__ void move_rows(uint8_t *array, int row_bytes, uint32_
     }
 }
 
+// Every array's rows of the chunk, by the movers.
 template <bool READ>
-__device__ __forceinline__ void move_all(const CompactParams &p, uint8_t *stage, const int64_t *slot)
+__device__ __forceinline__ void move_all(const CompactParams &p, uint8_t *stage, const int64_t *slot, uint64_t *bar)
 {
+    if (threadIdx.x < (unsigned)p.T) {
+        const int64_t at = slot[threadIdx.x];
+        if (at >= 0)
+            for (int a = 0; a < p.n_arrays; ++a) {
+                if (p.unit[a] != 16) continue;
+                uint8_t *g = p.array[a] + at * p.row_bytes[a], *s = stage + p.offset[a] + threadIdx.x * p.row_bytes[a];
+                if (READ)
+                    bulk_load(s, g, (uint32_t)p.row_bytes[a], bar);
+                else
+                    bulk_store(g, s, (uint32_t)p.row_bytes[a]);
+            }
+        if (!READ) bulk_commit();
+    }
     for (int a = 0; a < p.n_arrays; ++a) {
-        if (p.unit[a] == 16)
-            move_rows<16, READ>(p.array[a], p.row_bytes[a], p.per[a], p.magic[a], stage + p.offset[a], slot, p.T);
-        else if (p.unit[a] == 4)
+        if (p.unit[a] == 4)
             move_rows<4, READ>(p.array[a], p.row_bytes[a], p.per[a], p.magic[a], stage + p.offset[a], slot, p.T);
-        else
+        else if (p.unit[a] == 1)
             move_rows<1, READ>(p.array[a], p.row_bytes[a], p.per[a], p.magic[a], stage + p.offset[a], slot, p.T);
     }
 }
@@ -477,59 +495,78 @@ __global__ void __launch_bounds__(kCpThreads) evict_compact_kernel(CompactParams
 {
     extern __shared__ __align__(16) uint8_t stage[];
     __shared__ Chunk chunk[2];
-    __shared__ int next_ticket, timed_out;
+    __shared__ uint64_t landed;
+    __shared__ int next_ticket[2], timed_out;  // by parity: one is read while the other is drawn
     const int tid = threadIdx.x;
+    const bool mover = tid < kMovers;
     const int n_tickets = p.B * (p.chunks + p.tails);
     if (tid == 0) {
+        mbar_init(&landed, 1);
+        fence_mbar_init();
         timed_out = 0;
-        next_ticket = atomicAdd(p.ticket, 1);
+        chunk[0].moving = chunk[1].moving = 0;
+        next_ticket[0] = atomicAdd(p.ticket, 1);
     }
     __syncthreads();
-    int ticket = next_ticket;
-    if (ticket < n_tickets) describe(p, chunk[0], ticket);
+    int ticket = next_ticket[0];
+    if (!mover && ticket < n_tickets) describe(p, chunk[0], ticket);
+    __syncthreads();
+    uint32_t phase = 0;
     for (int it = 0; ticket < n_tickets; ++it) {
-        __syncthreads();  // the chunk is described, the stage free, next_ticket read
-        const Chunk &k = chunk[it & 1];
+        Chunk &k = chunk[it & 1], &next = chunk[(it + 1) & 1];
         // a ticket held while this chunk is worked on: it is higher than this one, so no wait on it is circular
-        if (tid == 0) next_ticket = atomicAdd(p.ticket, 1);
-        float t = 0.f;
-        float *total = p.total ? p.total + (int64_t)k.b * p.total_ld : nullptr;
-        if (k.run && k.c >= 0) {
-            move_all<true>(p, stage, k.src);
-            if (total && tid < p.T && k.from[tid] >= 0) t = __ldcg(total + k.from[tid]);
+        if (tid == kMovers) {
+            next_ticket[(it + 1) & 1] = atomicAdd(p.ticket, 1);
+            next.moving = 0;
         }
-        cp_async_commit();
-        __syncthreads();
-        ticket = next_ticket;
-        if (ticket < n_tickets) describe(p, chunk[(it + 1) & 1], ticket);  // while the rows are on their way
-        if (!k.run) continue;
-        cp_async_wait_all();
-        __syncthreads();  // every thread's reads (rows and totals) have arrived
-        int32_t *done = p.read_done + (int64_t)k.b * p.chunks;
-        if (tid == 0 && k.c >= 0) {
-            __threadfence();
-            st_release(done + k.c, 1);
-        }
-        const int w1 = k.c >= 0 ? min(k.w1, k.c) : k.w1;  // later chunks read behind this one's destination
-        for (int x = k.w0 + tid; x < w1; x += kCpThreads) {
-            const long long t0 = clock64();
-            while (!ld_acquire(done + x)) {
-                if (clock64() - t0 > kCpWait) {
+        if (!mover) {
+            bar_sync(2, kCpThreads - kMovers);
+            const int drawn = next_ticket[(it + 1) & 1];
+            if (drawn < n_tickets) describe(p, next, drawn);  // while the rows of this chunk move
+        } else if (k.run) {
+            float t = 0.f;
+            float *total = p.total ? p.total + (int64_t)k.b * p.total_ld : nullptr;
+            if (k.c >= 0) {
+                if (tid == 0) mbar_arrive_expect_tx(&landed, (uint32_t)(k.moving * p.bulk_bytes));
+                move_all<true>(p, stage, k.src, &landed);
+                if (total && tid < p.T && k.from[tid] >= 0) t = __ldcg(total + k.from[tid]);
+                cp_async_commit();
+                cp_async_wait_all();
+                if (!mbar_wait(&landed, phase, kCpWait)) {
                     set_status(p.status, NSA_ERR_TIMEOUT);
                     timed_out = 1;
-                    break;
                 }
-                __nanosleep(32);
+                phase ^= 1;
+            }
+            bar_sync(1, kMovers);  // every mover's reads (rows and totals) have arrived
+            int32_t *done = p.read_done + (int64_t)k.b * p.chunks;
+            if (tid == 0 && k.c >= 0) st_release(done + k.c, 1);
+            const int w1 = k.c >= 0 ? min(k.w1, k.c) : k.w1;  // later chunks read behind this one's destination
+            for (int x = k.w0 + tid; x < w1; x += kMovers) {
+                const long long t0 = clock64();
+                while (!ld_acquire(done + x)) {
+                    if (clock64() - t0 > kCpWait) {
+                        set_status(p.status, NSA_ERR_TIMEOUT);
+                        timed_out = 1;
+                        break;
+                    }
+                    __nanosleep(32);
+                }
+            }
+            bar_sync(1, kMovers);
+            if (!timed_out) {  // else rows that another chunk may not have read are left as they are
+                if (k.c >= 0) {
+                    move_all<false>(p, stage, k.dst, nullptr);
+                    if (total && tid < p.T && k.from[tid] >= 0) total[k.lo + tid] = t;
+                } else {
+                    for (int i = k.lo + tid; i < k.hi; i += kMovers) total[i] = 0.f;
+                }
             }
         }
-        __syncthreads();
-        if (timed_out) return;  // rows that another chunk may not have read are left as they are
-        if (k.c >= 0) {
-            move_all<false>(p, stage, k.dst);
-            if (total && tid < p.T && k.from[tid] >= 0) total[k.lo + tid] = t;
-        } else {
-            for (int i = k.lo + tid; i < k.hi; i += kCpThreads) total[i] = 0.f;
-        }
+        if (mover) bulk_wait_read();  // the rows written last have left the stage
+        __syncthreads();              // and the next chunk is described
+        ticket = next_ticket[(it + 1) & 1];
+        if (timed_out) break;
     }
 }
 
@@ -622,6 +659,7 @@ extern "C" nsa_status nsa_evict_compact(int B, const int32_t *keep_dev, int64_t 
         p.row_bytes[a] = (int)row_bytes[a];
         const uintptr_t both = (uintptr_t)arrays_dev[a] | (uintptr_t)row_bytes[a];
         p.unit[a] = both % 16 == 0 ? 16 : both % 4 == 0 ? 4 : 1;
+        if (p.unit[a] == 16) p.bulk_bytes += p.row_bytes[a];
         p.per[a] = (uint32_t)(row_bytes[a] / p.unit[a]);
         // exact while step * per < 2^32, which short rows keep (at most kCpMinT * kCpMaxRow steps)
         p.magic[a] = p.per[a] > 1 && p.per[a] < 4096 ? (uint32_t)((0x100000000ULL + p.per[a] - 1) / p.per[a]) : 0;
@@ -648,7 +686,8 @@ extern "C" nsa_status nsa_evict_compact(int B, const int32_t *keep_dev, int64_t 
     const cudaStream_t s = (cudaStream_t)stream;
     NSA_CUDA_TRY(cudaMemsetAsync(workspace_dev, 0, 16 + (size_t)B * p.chunks * sizeof(int32_t), s));
     NSA_CUDA_TRY(max_dynamic_smem<evict_compact_kernel>(kCpMinT * kCpMaxRow));
-    const int64_t most = (int64_t)sms * kCpPerSm;
+    const int64_t fit = (227 * 1024) / (stage + (int64_t)sizeof(Chunk) * 2 + 2048);  // by shared memory
+    const int64_t most = (int64_t)sms * (fit < 1 ? 1 : fit < kCpPerSm ? fit : kCpPerSm);
     evict_compact_kernel<<<(unsigned)(tickets < most ? tickets : most), kCpThreads, (size_t)stage, s>>>(p);
     return launch_status();
 }
