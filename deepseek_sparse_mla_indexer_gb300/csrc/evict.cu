@@ -311,7 +311,7 @@ constexpr int kCpThreads = 256;          // warps 0..3 move a chunk, warps 4..7 
 constexpr int kMovers = 128;
 constexpr int kCpMinT = 8, kCpMaxT = 128;
 constexpr int kCpTail = 4096;            // totals cleared by one chunk
-constexpr int kCpStage = 44 * 1024;      // bytes staged per CTA at most, where a chunk of kCpMinT allows it
+constexpr int kCpStage = 52 * 1024;      // bytes staged per CTA at most, where a chunk of kCpMinT allows it
 constexpr int kCpPerSm = 8;              // CTAs per SM at most
 constexpr int kCpMaxRow = 24 * 1024;     // bytes of one position over all arrays
 constexpr long long kCpWait = 2000000000LL;  // ~1 s of SM clocks
@@ -369,7 +369,7 @@ __device__ __forceinline__ int warp_lower_bound(const int32_t *keep, int n, int 
 
 // What a CTA knows of a chunk before it moves its rows.
 struct Chunk {
-    int64_t src[kCpMaxT], dst[kCpMaxT];  // slots; -1: the row does not move
+    int32_t src[kCpMaxT], dst[kCpMaxT];  // slots; -1: the row does not move
     int32_t from[kCpMaxT];               // position whose total moves here, -1: cleared, -2: not of this chunk
     int ticket, b, c;                    // c < 0: tail chunk -c - 1
     int lo, hi;                          // destination positions
@@ -396,8 +396,7 @@ __device__ __forceinline__ void describe(const CompactParams &p, Chunk &k, int t
     if (warp < 2) {
         const int32_t *pt = p.page_table + (int64_t)b * p.pt_ld;
         for (int r = warp * 32 + lane; r < p.T; r += 64) {
-            int64_t s = -1, d = -1;
-            int32_t from = -2;
+            int32_t s = -1, d = -1, from = -2;
             const int i = lo + r;
             if (run && !tail && i < hi) {
                 const int q = keep[i], before = i > 0 ? keep[i - 1] : -1;
@@ -411,8 +410,8 @@ __device__ __forceinline__ void describe(const CompactParams &p, Chunk &k, int t
                     if (ps < 0 || ps >= p.num_pages || pd < 0 || pd >= p.num_pages) {
                         set_status(p.status, NSA_ERR_BOUNDS);
                     } else {
-                        s = (int64_t)ps * p.page_size + (q - sp * p.page_size);
-                        d = (int64_t)pd * p.page_size + (i - dp * p.page_size);
+                        s = ps * p.page_size + (q - sp * p.page_size);
+                        d = pd * p.page_size + (i - dp * p.page_size);
                         atomicAdd(&k.moving, 1);
                     }
                 }
@@ -448,7 +447,7 @@ template <> struct CopyUnit<1> { using type = uint8_t; };
 // Rows of one array of 4-byte or odd rows between the cache and the stage.
 template <int UNIT, bool READ>
 __device__ __forceinline__ void move_rows(uint8_t *array, int row_bytes, uint32_t per, uint32_t magic, uint8_t *stage,
-                                          const int64_t *slot, int T)
+                                          const int32_t *slot, int T)
 {
     using U = typename CopyUnit<UNIT>::type;
     for (uint32_t e = threadIdx.x; e < T * per; e += kMovers) {
@@ -468,7 +467,7 @@ __device__ __forceinline__ void move_rows(uint8_t *array, int row_bytes, uint32_
 
 // Every array's rows of the chunk, by the movers.
 template <bool READ>
-__device__ __forceinline__ void move_all(const CompactParams &p, uint8_t *stage, const int64_t *slot, uint64_t *bar)
+__device__ __forceinline__ void move_all(const CompactParams &p, uint8_t *stage, const int32_t *slot, uint64_t *bar)
 {
     if (threadIdx.x < (unsigned)p.T) {
         const int64_t at = slot[threadIdx.x];

@@ -354,7 +354,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                 for (int t = w.c0; t < w.c1 && ok; ++t, ++tile) {
                     if (!mbar_wait(&sm->raw.tile_full[tile & 1], (tile >> 1) & 1, kPtWait)) ok = false;
                     const uint32_t live = live_rows(p.t, sm->raw.boxes[tile & 1], d, t, w.len);
-                    const float *scales = reinterpret_cast<const float *>(sc_s + (tile & 1) * kScaleSlot);
+                    float *scales = reinterpret_cast<float *>(sc_s + (tile & 1) * kScaleSlot);
 #pragma unroll 1
                     for (int m = 0; m < 5; ++m) {
                         const int s0 = st, s1 = st + 1 == nst ? 0 : st + 1;
@@ -378,11 +378,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                             if (!mbar_wait(&sm->empty[s1], ph1 ^ 1, kPtWait)) ok = false;
                             x.store(d, ring + s0 * kPtBlk, ring + s1 * kPtBlk);
                         } else {
-                            // the rope part lies in its slot as the operand wants it (swizzled): moved as it is
-#pragma unroll
-                            for (int u = 0; u < kDqRows; ++u)
-                                *reinterpret_cast<uint4 *>(ring + s0 * kPtBlk + ((d >> 3) + kPtTok / kDqRows * u) * 128 + 16 * (d & 7)) =
-                                    x.w[u];
+                            x.move(d, ring + s0 * kPtBlk);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();

@@ -678,7 +678,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
                     if (!mbar_wait(&sm->raw.tile_full[i & 1], (i >> 1) & 1, kPtWait)) ok = false;
                     const uint32_t live = live_rows(p.t, sm->raw.boxes[i & 1], d, t, s.len);
-                    const float *scales = reinterpret_cast<const float *>(sc_s + (i & 1) * kScaleSlot);
+                    float *scales = reinterpret_cast<float *>(sc_s + (i & 1) * kScaleSlot);
 #pragma unroll 1
                     for (int m = 0; m < 4; ++m) {
                         if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;

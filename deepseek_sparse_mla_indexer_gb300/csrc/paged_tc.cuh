@@ -140,21 +140,26 @@ __device__ __forceinline__ int checked_page(const PagedTc &p, const int32_t *pt,
 
 // ------------------------------------------------------------------ fp8 rows
 
-// Eight e4m3 codes times their block's scale: code x scale rounded to fp32, then to
-// bf16, the row's values by definition.
+// Four e4m3 codes (one word) times their block's scale as four bf16: code x scale rounded
+// to fp32, then to bf16, the row's values by definition.
+__device__ __forceinline__ uint2 expand4(uint32_t codes, float s)
+{
+    uint32_t h0, h1;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(h0), "=r"(h1)
+        : "r"(codes));
+    const float2 ss = make_float2(s, s);
+    const float2 f0 = sm100::mul2(__half22float2(*reinterpret_cast<const __half2 *>(&h0)), ss);
+    const float2 f1 = sm100::mul2(__half22float2(*reinterpret_cast<const __half2 *>(&h1)), ss);
+    const __nv_bfloat162 b0 = __floats2bfloat162_rn(f0.x, f0.y), b1 = __floats2bfloat162_rn(f1.x, f1.y);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&b0), *reinterpret_cast<const uint32_t *>(&b1));
+}
+
 __device__ __forceinline__ uint4 expand8(uint32_t a, uint32_t b, float s)
 {
-    const uint32_t in[2] = {a, b};
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2_raw h =
-            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((in[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
-        const float2 f = sm100::mul2(__half22float2(*reinterpret_cast<const __half2 *>(&h)), make_float2(s, s));
-        const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
-        o[i] = *reinterpret_cast<const uint32_t *>(&v);
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    const uint2 x = expand4(a, s), y = expand4(b, s);
+    return make_uint4(x.x, x.y, y.x, y.y);
 }
 
 // Raw fp8 rows in shared memory: the codes of one 128-value block of a tile's rows
@@ -173,44 +178,69 @@ struct RawShared {
 
 // Thread d of kDqThreads expands rows d / 8 and d / 8 + 64, chunk d % 8 (16 codes) of a
 // step into blocks blk0 (chunks 0..3) and blk1; rows without a key become zeros.  Codes
-// 16k .. 16k+15 become chunks 2k, 2k+1 of the step's 16; lanes with k >= 4 store the odd
-// chunk first, so that eight neighbouring lanes store to eight distinct bank groups.
+// 16k .. 16k+15 become chunks 2k, 2k+1 of the step's 16.  Which of the two halves a lane
+// takes first alternates with k / 4 and with the row, so that eight neighbouring lanes
+// store to eight distinct bank groups and sixteen read distinct pairs of banks.  The
+// arithmetic is what costs here (ncu: 61 % of issue slots, ALU 52 % busy, in an earlier
+// form that chose the halves after loading them): two conversions, one paired multiply
+// and two widenings for two codes.
 // (Two groups of half the threads that take turns by steps were 7 - 9 % slower.)
 constexpr int kDqRows = kPtTok * 8 / kDqThreads;
+constexpr uint32_t kDqAll = (1u << kDqRows) - 1;
 
 struct RawStep {
-    uint4 w[kDqRows];
+    uint2 w[kDqRows][2];
     float sc[kDqRows];
 
-    __device__ __forceinline__ void read(const uint8_t *raw, const float *scales, int m, int d, uint32_t live)
+    static __device__ __forceinline__ bool swap(int d) { return ((d >> 2) ^ (d >> 3)) & 1; }
+
+    __device__ __forceinline__ void read(uint8_t *raw, float *scales, int m, int d, uint32_t live)
     {
+        uint8_t *at = raw + (d >> 3) * 128 + 16 * (d & 7);
+        float *sp = scales + 4 * (d >> 3) + m;
+        constexpr int kStep = kPtTok / kDqRows;  // rows between a thread's rows
+        if (live != kDqAll) {
+            // what an earlier tile left in the rows without a key may be NaN
+#pragma unroll
+            for (int u = 0; u < kDqRows; ++u)
+                if (!(live >> u & 1)) {
+                    *reinterpret_cast<uint4 *>(at + u * kStep * 128) = make_uint4(0u, 0u, 0u, 0u);
+                    sp[u * kStep * 4] = 0.f;
+                }
+        }
+        const int first = swap(d) ? 8 : 0;
 #pragma unroll
         for (int u = 0; u < kDqRows; ++u) {
-            const int r = (d >> 3) + kPtTok / kDqRows * u;
-            const bool on = live >> u & 1;
-            w[u] = make_uint4(0u, 0u, 0u, 0u);
-            sc[u] = 0.f;
-            if (on) {
-                w[u] = *reinterpret_cast<const uint4 *>(raw + r * 128 + 16 * (d & 7));
-                sc[u] = scales[4 * r + m];
-            }
+            w[u][0] = *reinterpret_cast<const uint2 *>(at + u * kStep * 128 + first);
+            w[u][1] = *reinterpret_cast<const uint2 *>(at + u * kStep * 128 + (first ^ 8));
+            sc[u] = sp[u * kStep * 4];
         }
     }
     __device__ __forceinline__ void store(int d, uint8_t *blk0, uint8_t *blk1) const
     {
-        const int k = d & 7, c0 = (2 * k) & 7;
+        const int k = d & 7, r = d >> 3, c0 = (2 * k) & 7, sw = swap(d) ? 1 : 0;
         uint8_t *blk = k < 4 ? blk0 : blk1;
+        // rows 64 apart have the same swizzle
+        uint8_t *first = blk + sm100::sw128_offset(r, c0 + sw), *second = blk + sm100::sw128_offset(r, c0 + 1 - sw);
 #pragma unroll
         for (int u = 0; u < kDqRows; ++u) {
-            const int r = (d >> 3) + kPtTok / kDqRows * u;
-            // the first store's half of the codes is chosen before it is expanded
-            const uint2 a = k < 4 ? make_uint2(w[u].x, w[u].y) : make_uint2(w[u].z, w[u].w);
-            const uint2 b = k < 4 ? make_uint2(w[u].z, w[u].w) : make_uint2(w[u].x, w[u].y);
-            *reinterpret_cast<uint4 *>(blk + sm100::sw128_offset(r, k < 4 ? c0 : c0 + 1)) = expand8(a.x, a.y, sc[u]);
-            *reinterpret_cast<uint4 *>(blk + sm100::sw128_offset(r, k < 4 ? c0 + 1 : c0)) = expand8(b.x, b.y, sc[u]);
+            *reinterpret_cast<uint4 *>(first + u * (kPtTok / kDqRows) * 128) = expand8(w[u][0].x, w[u][0].y, sc[u]);
+            *reinterpret_cast<uint4 *>(second + u * (kPtTok / kDqRows) * 128) = expand8(w[u][1].x, w[u][1].y, sc[u]);
+        }
+    }
+    // The rope part lies in its slot as the operand wants it (swizzled): moved as it is.
+    __device__ __forceinline__ void move(int d, uint8_t *blk) const
+    {
+        uint8_t *at = blk + (d >> 3) * 128 + 16 * (d & 7);
+        const int first = swap(d) ? 8 : 0;
+#pragma unroll
+        for (int u = 0; u < kDqRows; ++u) {
+            *reinterpret_cast<uint2 *>(at + u * (kPtTok / kDqRows) * 128 + first) = w[u][0];
+            *reinterpret_cast<uint2 *>(at + u * (kPtTok / kDqRows) * 128 + (first ^ 8)) = w[u][1];
         }
     }
 };
+static_assert((kPtTok / kDqRows) % 8 == 0, "a thread's rows share their swizzle");
 
 // Which of thread d's rows of a tile hold a key (bit u: row d / 8 + 64 u).
 __device__ __forceinline__ uint32_t live_rows(const PagedTc &p, uint32_t boxes, int d, int tile, int len)
