@@ -37,8 +37,8 @@ struct WShared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full, q_empty, s_full[2], s_empty[2];
     RawShared raw;
-    float lse2[kCols];   // lse in log2 units; +inf: no weight (padding, an empty row)
-    int len[kCols];      // positions the column's row sees
+    alignas(16) float nlse2[kCols];  // -lse in log2 units; -inf: no weight (padding, an empty row)
+    int len[kCols];      // positions the column's row sees; 0: no weight
     int min_len[4];
     TileShare share;
     uint32_t tmem_base;
@@ -294,18 +294,21 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                 bar_sync(1, 128);  // the previous piece's columns are read out
                 {
                     const int c = w.pass * kCols + key;
-                    float l2 = INFINITY;
-                    int len = 0x7fffffff;
+                    float nl = -INFINITY;
+                    int len = 0;
                     if (c < p.cols) {
                         const int64_t r = (int64_t)w.b * p.t.n + c / p.t.H;
                         const float l = p.lse[r * p.t.H + c % p.t.H];
-                        if (l != -INFINITY) l2 = l * 1.4426950408889634f;
                         const int L = p.t.row_len[r];
-                        len = L >= 0 && L <= p.t.max_row_len ? L : 0;
+                        if (l != -INFINITY && L > 0 && L <= p.t.max_row_len) {
+                            nl = -l * 1.4426950408889634f;
+                            len = L;
+                        }
                     }
-                    sm->lse2[key] = l2;
+                    sm->nlse2[key] = nl;
                     sm->len[key] = len;
-                    const int mn = __reduce_min_sync(0xffffffffu, len);
+                    // columns past the MMA's are never looked at
+                    const int mn = __reduce_min_sync(0xffffffffu, key < p.N ? len : 0x7fffffff);
                     if (lane == 0) sm->min_len[warp & 3] = mn;
                 }
                 bar_sync(1, 128);
@@ -321,19 +324,42 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                     if (!ok) fail();
                     if (bar_red_or(2, 128, !ok || sm->abort)) { more = false; break; }
                     tc_fence_after();
-                    const bool whole = (t + 1) * kPtTok <= min_len;  // every column sees the whole tile
-                    float sum = 0.f;
+                    float sum;
+                    if ((t + 1) * kPtTok <= min_len) {
+                        // every column is a real one and sees the whole tile: nothing to select
+                        const float2 sc = make_float2(p.t.scale_log2, p.t.scale_log2);
+                        const float4 *nl = reinterpret_cast<const float4 *>(sm->nlse2);
+                        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-                    for (int c0 = 0; c0 < p.N; c0 += 32) {
-                        uint32_t s[32];
-                        tmem_ld32(lanes + buf * kCols + c0, s);
-                        tmem_ld_wait();
+                        for (int c0 = 0; c0 < p.N; c0 += 16) {
+                            uint32_t s[16];
+                            tmem_ld16(lanes + buf * kCols + c0, s);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float l2 = sm->lse2[c0 + j];
-                            const float e = ex2_approx(fmaf(__uint_as_float(s[j]), p.t.scale_log2, -l2));
-                            // a column without weight may hold anything: selected away, not multiplied
-                            if (l2 != INFINITY && (whole || pos < sm->len[c0 + j])) sum += e;
+                            for (int j = 0; j < 4; ++j) {
+                                const float4 n = nl[c0 / 4 + j];
+                                const float2 x = fma2(make_float2(__uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1])), sc,
+                                                      make_float2(n.x, n.y));
+                                const float2 y = fma2(make_float2(__uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3])),
+                                                      sc, make_float2(n.z, n.w));
+                                acc[0] = add2(acc[0], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+                                acc[1] = add2(acc[1], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+                            }
+                        }
+                        sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                    } else {
+                        sum = 0.f;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < p.N; c0 += 16) {
+                            uint32_t s[16];
+                            tmem_ld16(lanes + buf * kCols + c0, s);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float e = ex2_approx(fmaf(__uint_as_float(s[j]), p.t.scale_log2, sm->nlse2[c0 + j]));
+                                // a column without weight may hold anything: selected away, not multiplied
+                                sum += pos < sm->len[c0 + j] ? e : 0.f;
+                            }
                         }
                     }
                     tc_fence_before();
