@@ -37,6 +37,7 @@ struct WShared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full, q_empty, s_full[2], s_empty[2];
     RawShared raw;
+    uint64_t rope_full, rope_empty;  // fp8: the rope parts have a stage of their own
     alignas(16) float nlse2[kCols];  // -lse in log2 units; -inf: no weight (padding, an empty row)
     int len[kCols];      // positions the column's row sees; 0: no weight
     int min_len[4];
@@ -108,7 +109,8 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
     uint8_t *q_s = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t q_blk = (uint32_t)p.N * 128;
     uint8_t *ring = q_s + 9 * q_blk;
-    uint8_t *raw_s = ring + (size_t)p.stages * kPtBlk;     // fp8: raw codes, then the scales of two tiles
+    uint8_t *rope_s = ring + (size_t)p.stages * kPtBlk;    // fp8: the rope part, raw codes, the scales of two tiles
+    uint8_t *raw_s = rope_s + (FP8 ? kPtBlk : 0);
     uint8_t *sc_s = raw_s + (FP8 ? p.raw * kRawSlot : 0);
     WShared *sm = (WShared *)(sc_s + (FP8 ? 2 * kScaleSlot : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -124,6 +126,8 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
             mbar_init(&sm->raw.empty[i], kDqThreads / 32);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&sm->raw.tile_full[i], 1);
+        mbar_init(&sm->rope_full, 1);
+        mbar_init(&sm->rope_empty, 1);
         mbar_init(&sm->q_full, 1);
         mbar_init(&sm->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
@@ -159,8 +163,8 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
         if (work) {
             const int boxes = kPtTok / p.t.box_rows;  // at most 16, one a lane
             const uint32_t box_bytes = (uint32_t)p.t.box_rows * 128;
-            int st = 0;
-            uint32_t ph = 0, uses = 0, tile = 0;
+            int st = 0, rs = 0;
+            uint32_t ph = 0, rph = 0, uses = 0, tile = 0;
             bool ok = true;
             for (bool more = true; more && ok; more = w.next(p)) {
                 if (uses > 0 && !mbar_wait(&sm->q_empty, (uses - 1) & 1, kPtWait)) ok = false;
@@ -183,8 +187,11 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                     const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
                     const uint32_t bytes = __popc(live) * box_bytes;
                     const int y_first = __shfl_sync(0xffffffffu, y, 0);
-                    // (bringing later tiles into L2 from here as well made bf16 rows a quarter slower)
                     const int y_next = box_row(t + 1);  // its latency under this tile's waits
+                    // the raw slots alone do not cover HBM's latency: a tile ahead into L2 (bf16 rows have
+                    // the bytes in flight, and became a quarter slower from it)
+                    if (FP8 && y_next >= 0)
+                        prefetch_l2_bulk(p.t.kv + (int64_t)y_next * kPtFp8Row, (uint32_t)p.t.box_rows * kPtFp8Row);
                     // one lane issues a box at a time from uniform registers
                     auto boxes_of = [&](auto issue) {
                         int yb = y_first;
@@ -194,32 +201,47 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                             __syncwarp();
                         }
                     };
-                    for (int c = 0; c < (FP8 ? 5 : 9); ++c) {
-                        uint64_t *full = FP8 ? sm->raw.full : sm->full, *empty = FP8 ? sm->raw.empty : sm->empty;
-                        if (!mbar_wait(&empty[st], ph ^ 1, kPtWait)) ok = false;
-                        if (elect_one()) {
-                            if (FP8 && c == 0) {
-                                sm->raw.boxes[tile & 1] = live;
-                                mbar_arrive_expect_tx(&sm->raw.tile_full[tile & 1], bytes / 8);
+                    if constexpr (FP8) {
+                        for (int m = 0; m < 4; ++m) {
+                            if (!mbar_wait(&sm->raw.empty[rs], rph ^ 1, kPtWait)) ok = false;
+                            if (elect_one()) {
+                                if (m == 0) {
+                                    sm->raw.boxes[tile & 1] = live;
+                                    mbar_arrive_expect_tx(&sm->raw.tile_full[tile & 1], bytes / 8);
+                                }
+                                mbar_arrive_expect_tx(&sm->raw.full[rs], bytes);
                             }
-                            mbar_arrive_expect_tx(&full[st], bytes);
-                        }
-                        __syncwarp();
-                        boxes_of([&](int x, int yb) {
-                            if (!FP8) {
-                                tma_load_2d(ring + st * kPtBlk + x * box_bytes, &kv_map, 64 * c, yb, &full[st]);
-                            } else if (c < 4) {
-                                tma_load_2d(raw_s + st * kRawSlot + x * box_bytes, &kv_map, 128 * c, yb, &full[st]);
-                                if (c == 0)
+                            __syncwarp();
+                            boxes_of([&](int x, int yb) {
+                                tma_load_2d(raw_s + rs * kRawSlot + x * box_bytes, &kv_map, 128 * m, yb, &sm->raw.full[rs]);
+                                if (m == 0)
                                     tma_load_2d(sc_s + (tile & 1) * kScaleSlot + x * (box_bytes / 8), &sc_map, kPtDl, yb,
                                                 &sm->raw.tile_full[tile & 1]);
-                            } else {
-                                tma_load_2d(raw_s + st * kRawSlot + x * box_bytes, &rope_map, kFp8RopeX, yb, &full[st]);
+                            });
+                            if (++rs == p.raw) {
+                                rs = 0;
+                                rph ^= 1;
                             }
+                        }
+                        // the rope part straight into its stage
+                        if (!mbar_wait(&sm->rope_empty, (tile & 1) ^ 1, kPtWait)) ok = false;
+                        if (elect_one()) mbar_arrive_expect_tx(&sm->rope_full, bytes);
+                        __syncwarp();
+                        boxes_of([&](int x, int yb) {
+                            tma_load_2d(rope_s + x * box_bytes, &rope_map, kFp8RopeX, yb, &sm->rope_full);
                         });
-                        if (++st == (FP8 ? p.raw : nst)) {
-                            st = 0;
-                            ph ^= 1;
+                    } else {
+                        for (int c = 0; c < 9; ++c) {
+                            if (!mbar_wait(&sm->empty[st], ph ^ 1, kPtWait)) ok = false;
+                            if (elect_one()) mbar_arrive_expect_tx(&sm->full[st], bytes);
+                            __syncwarp();
+                            boxes_of([&](int x, int yb) {
+                                tma_load_2d(ring + st * kPtBlk + x * box_bytes, &kv_map, 64 * c, yb, &sm->full[st]);
+                            });
+                            if (++st == nst) {
+                                st = 0;
+                                ph ^= 1;
+                            }
                         }
                     }
                     y = y_next;
@@ -230,8 +252,12 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
             if (!ok && lane == 0) fail();
             // nothing is in flight at the end: slots before st were filled last with phase ph, the others before
             if (lane == 0) {
-                for (int i = 0; i < (FP8 ? p.raw : nst); ++i)
-                    mbar_wait(FP8 ? &sm->raw.full[i] : &sm->full[i], i < st ? ph : ph ^ 1, kPtWait);
+                if (FP8) {
+                    for (int i = 0; i < p.raw; ++i) mbar_wait(&sm->raw.full[i], i < rs ? rph : rph ^ 1, kPtWait);
+                    if (tile > 0) mbar_wait(&sm->rope_full, (tile - 1) & 1, kPtWait);
+                } else {
+                    for (int i = 0; i < nst; ++i) mbar_wait(&sm->full[i], i < st ? ph : ph ^ 1, kPtWait);
+                }
                 if (FP8)
                     for (uint32_t x = tile > 2 ? tile - 2 : 0; x < tile; ++x)
                         mbar_wait(&sm->raw.tile_full[x & 1], (x >> 1) & 1, kPtWait);
@@ -246,6 +272,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
             const uint32_t idesc = instr_desc(1, 1, 0, 0, kPtTok, (uint32_t)p.N);
             const uint64_t q_desc = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
             const uint64_t r_desc = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
+            const uint64_t rope_desc = smem_desc(smem_u32(rope_s), 16, 1024, kSwizzle128B);
             int st = 0;
             uint32_t ph = 0, tile = 0, uses = 0;
             bool ok = true;
@@ -256,18 +283,20 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                     const uint32_t buf = tile & 1, bph = (tile >> 1) & 1;
                     if (!mbar_wait(&sm->s_empty[buf], bph ^ 1, kPtWait)) ok = false;
                     for (int c = 0; c < 9; ++c) {
-                        if (!mbar_wait(&sm->full[st], ph, kPtWait)) ok = false;
+                        const bool rope = FP8 && c == 8;
+                        if (!mbar_wait(rope ? &sm->rope_full : &sm->full[st], rope ? tile & 1 : ph, kPtWait)) ok = false;
                         tc_fence_after();
                         if (elect_one()) {
+                            const uint64_t a_desc = rope ? rope_desc : r_desc + st * (kPtBlk / 16);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_f16(tmem + buf * kCols, r_desc + (st * kPtBlk + k * 32) / 16,
-                                        q_desc + (c * q_blk + k * 32) / 16, idesc, (c | k) != 0);
-                            mma_commit(&sm->empty[st]);
+                                mma_f16(tmem + buf * kCols, a_desc + k * 2, q_desc + (c * q_blk + k * 32) / 16, idesc,
+                                        (c | k) != 0);
+                            mma_commit(rope ? &sm->rope_empty : &sm->empty[st]);
                             if (c == 8) mma_commit(&sm->s_full[buf]);
                         }
                         __syncwarp();
-                        if (++st == nst) {
+                        if (!rope && ++st == nst) {
                             st = 0;
                             ph ^= 1;
                         }
@@ -382,36 +411,30 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                     const uint32_t live = live_rows(p.t, sm->raw.boxes[tile & 1], d, t, w.len);
                     float *scales = reinterpret_cast<float *>(sc_s + (tile & 1) * kScaleSlot);
 #pragma unroll 1
-                    for (int m = 0; m < 5; ++m) {
+                    for (int m = 0; m < 4; ++m) {
                         const int s0 = st, s1 = st + 1 == nst ? 0 : st + 1;
                         const uint32_t ph0 = ph, ph1 = st + 1 == nst ? ph ^ 1 : ph;
-                        st += m < 4 ? 2 : 1;
+                        st += 2;
                         if (st >= nst) {
                             st -= nst;
                             ph ^= 1;
                         }
-                        const int r = rs;
-                        const uint32_t rp = rph;
-                        if (++rs == p.raw) {
-                            rs = 0;
-                            rph ^= 1;
-                        }
-                        if (!mbar_wait(&sm->raw.full[r], rp, kPtWait)) ok = false;
+                        if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;
                         RawStep x;
-                        x.read(raw_s + r * kRawSlot, scales, m & 3, d, live);
+                        x.read(raw_s + rs * kRawSlot, scales, m, d, live);
                         if (!mbar_wait(&sm->empty[s0], ph0 ^ 1, kPtWait)) ok = false;
-                        if (m < 4) {
-                            if (!mbar_wait(&sm->empty[s1], ph1 ^ 1, kPtWait)) ok = false;
-                            x.store(d, ring + s0 * kPtBlk, ring + s1 * kPtBlk);
-                        } else {
-                            x.move(d, ring + s0 * kPtBlk);
-                        }
+                        if (!mbar_wait(&sm->empty[s1], ph1 ^ 1, kPtWait)) ok = false;
+                        x.store(d, ring + s0 * kPtBlk, ring + s1 * kPtBlk);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(&sm->raw.empty[r]);
+                            mbar_arrive(&sm->raw.empty[rs]);
                             mbar_arrive(&sm->full[s0]);
-                            if (m < 4) mbar_arrive(&sm->full[s1]);
+                            mbar_arrive(&sm->full[s1]);
+                        }
+                        if (++rs == p.raw) {
+                            rs = 0;
+                            rph ^= 1;
                         }
                     }
                     ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
@@ -448,11 +471,12 @@ nsa_status key_weights_tc_try_launch(const PagedMlaArgs &a, const float *lse, fl
     p.passes = (int)ceil_div(p.cols, kCols);
     p.N = p.passes > 1 ? kCols : (int)ceil_div(p.cols, 16) * 16;
     const size_t q_bytes = (size_t)9 * p.N * 128, left = 232448 - 1024 - kAux - q_bytes;
-    // fp8: about two raw slots to three stages (a step fills two), at least two of each
-    const int blocks = (int)((left - (fp8 ? 2 * kScaleSlot : 0)) / kPtBlk);
-    p.raw = fp8 ? (blocks >= 8 ? 4 : blocks >= 6 ? 3 : 2) : 0;
+    // fp8: a stage for the rope part, about two raw slots to three stages (a step fills two) of the rest
+    const int blocks = (int)((left - (fp8 ? 2 * kScaleSlot + kPtBlk : 0)) / kPtBlk);
+    p.raw = fp8 ? (blocks >= 8 ? 4 : blocks >= 6 ? 3 : blocks >= 4 ? 2 : 1) : 0;
     p.stages = blocks - p.raw < kMaxStages ? blocks - p.raw : kMaxStages;
-    const size_t smem = 1024 + q_bytes + (size_t)(p.stages + p.raw) * kPtBlk + (fp8 ? 2 * kScaleSlot : 0) + kAux;
+    const size_t smem =
+        1024 + q_bytes + (size_t)(p.stages + p.raw + (fp8 ? 1 : 0)) * kPtBlk + (fp8 ? 2 * kScaleSlot : 0) + kAux;
     CUtensorMap qn, qr, kv, sc = {}, rope = {};
     if (!paged_tc_q_maps(a, (uint32_t)p.N, &qn, &qr)) return NSA_ERR_CUDA;
     if (fp8 ? !fp8_maps(a, (uint32_t)p.t.box_rows, &kv, &sc, &rope)

@@ -228,17 +228,6 @@ struct RawStep {
             *reinterpret_cast<uint4 *>(second + u * (kPtTok / kDqRows) * 128) = expand8(w[u][1].x, w[u][1].y, sc[u]);
         }
     }
-    // The rope part lies in its slot as the operand wants it (swizzled): moved as it is.
-    __device__ __forceinline__ void move(int d, uint8_t *blk) const
-    {
-        uint8_t *at = blk + (d >> 3) * 128 + 16 * (d & 7);
-        const int first = swap(d) ? 8 : 0;
-#pragma unroll
-        for (int u = 0; u < kDqRows; ++u) {
-            *reinterpret_cast<uint2 *>(at + u * (kPtTok / kDqRows) * 128 + first) = w[u][0];
-            *reinterpret_cast<uint2 *>(at + u * (kPtTok / kDqRows) * 128 + (first ^ 8)) = w[u][1];
-        }
-    }
 };
 static_assert((kPtTok / kDqRows) % 8 == 0, "a thread's rows share their swizzle");
 
