@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kThreads) key_weights_simt_kernel(PagedMlaArgs
     __shared__ float part[kThreads / 32][kTile];
     const int dq = p.d_latent + p.d_rope, ld = dq + 1;
     float *ks = smem, *qs = ks + kTile * ld;
-    const int b = blockIdx.y, j0 = blockIdx.x * kTile;
+    const int per = (p.max_row_len + kTile - 1) / kTile, b = blockIdx.x / per, j0 = (blockIdx.x - b * per) * kTile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int longest = 0;
     for (int i = 0; i < p.rows_per_req; ++i)
@@ -86,11 +86,11 @@ nsa_status launch_simt(const PagedMlaArgs &a, const float *lse, float *total, in
 {
     const int64_t dq = (int64_t)a.d_latent + a.d_rope;
     const int64_t smem = (int64_t)sizeof(float) * (kTile * (dq + 1) + kHG * dq);
-    if (smem > 224 * 1024 || a.R / a.rows_per_req > 65535) return NSA_ERR_UNSUPPORTED;
+    const int64_t blocks = ceil_div(a.max_row_len, kTile) * (a.R / a.rows_per_req);
+    if (smem > 224 * 1024 || blocks > 2147483647LL) return NSA_ERR_UNSUPPORTED;
     auto k = key_weights_simt_kernel<QDT, KDT>;
     NSA_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    const dim3 grid((unsigned)ceil_div(a.max_row_len, kTile), (unsigned)(a.R / a.rows_per_req));
-    k<<<grid, kThreads, (size_t)smem, stream>>>(a, lse, total, total_ld);
+    k<<<(unsigned)blocks, kThreads, (size_t)smem, stream>>>(a, lse, total, total_ld);
     return launch_status();
 }
 

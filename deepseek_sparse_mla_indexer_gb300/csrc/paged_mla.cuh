@@ -36,7 +36,8 @@ inline nsa_status check_paged_mla(const PagedMlaArgs &a)
     if (!combo_ok) return NSA_ERR_UNSUPPORTED;
     if (a.kv_dtype == NSA_DT_E4M3 && (a.d_latent % 128 != 0 || a.d_rope % 2 != 0)) return NSA_ERR_UNSUPPORTED;
     if (a.H > 65535 || a.page_size > (1 << 24) || a.max_row_len > (1 << 30) ||
-        (int64_t)a.rows_per_req * a.H > (1 << 20) || a.num_pages > 2147483647LL / a.page_size)
+        (int64_t)a.rows_per_req * a.H > (1 << 20) || (int64_t)a.R * a.H > 2147483647LL ||
+        a.num_pages > 2147483647LL / a.page_size)
         return NSA_ERR_UNSUPPORTED;
     if (a.R == 0) return NSA_OK;
     if (!a.q_nope || (a.d_rope > 0 && !a.q_rope) || !a.kv || !a.row_len || (a.max_row_len > 0 && !a.page_table) ||
@@ -47,13 +48,6 @@ inline nsa_status check_paged_mla(const PagedMlaArgs &a)
     if ((uintptr_t)a.kv & (a.kv_dtype == NSA_DT_BF16 ? 1 : 3)) return NSA_ERR_INVALID_ARG;
     if (((uintptr_t)a.page_table | (uintptr_t)a.row_len | (uintptr_t)a.status) & 3) return NSA_ERR_INVALID_ARG;
     return NSA_OK;
-}
-
-// Bytes of one cache row.
-inline int64_t mla_row_bytes(nsa_dtype kv_dtype, int d_latent, int d_rope)
-{
-    if (kv_dtype == NSA_DT_E4M3) return d_latent + 4 * (d_latent / 128) + 2 * d_rope;
-    return (int64_t)(d_latent + d_rope) * (kv_dtype == NSA_DT_F32 ? 4 : 2);
 }
 
 // Length of row r clipped to what the call allows; a length outside

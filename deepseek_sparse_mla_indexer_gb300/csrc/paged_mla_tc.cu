@@ -972,7 +972,6 @@ size_t paged_mla_tc_workspace_bytes(nsa_dtype q_dtype, nsa_dtype kv_dtype, int R
 nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse, void *workspace, cudaStream_t stream)
 {
     if (!paged_tc_applicable(a)) return NSA_ERR_UNSUPPORTED;
-    if ((int64_t)a.R * a.H > 0x7fffffffLL) return NSA_ERR_UNSUPPORTED;
     const int sms = current_sm_count();
     if (sms <= 0) return NSA_ERR_CUDA;
     const bool fp8 = a.kv_dtype == NSA_DT_E4M3;

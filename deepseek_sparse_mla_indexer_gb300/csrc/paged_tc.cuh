@@ -287,12 +287,23 @@ struct ScrRows {
 
 // ------------------------------------------------------------------ host
 
+// One head per row: its rows follow one another at the row stride, whatever ld_h says.
+inline PagedMlaArgs one_head_pitch(PagedMlaArgs a)
+{
+    if (a.H == 1 && a.R > 1) {
+        a.nope_ld_h = a.nope_ld_r;
+        a.rope_ld_h = a.rope_ld_r;
+    }
+    return a;
+}
+
 // Whether the tensor-core kernels take this problem: the 512 + 64 shape with bf16
 // queries, whole boxes of 8 rows in a page, 16-byte aligned buffers and query rows
 // that follow one another at one pitch (contiguous, or the two parts of a
 // concatenated [R, H, 576] query).
-inline bool paged_tc_applicable(const PagedMlaArgs &a)
+inline bool paged_tc_applicable(const PagedMlaArgs &args)
 {
+    const PagedMlaArgs a = one_head_pitch(args);
     return a.q_dtype == NSA_DT_BF16 && (a.kv_dtype == NSA_DT_BF16 || a.kv_dtype == NSA_DT_E4M3) &&
            a.d_latent == kPtDl && a.d_rope == kPtDr && a.page_size % 8 == 0 && a.max_row_len > 0 &&
            (((uintptr_t)a.q_nope | (uintptr_t)a.q_rope | (uintptr_t)a.kv) & 15) == 0 && a.nope_ld_h % 8 == 0 &&
@@ -321,8 +332,9 @@ inline PagedTc paged_tc_params(const PagedMlaArgs &a)
 }
 
 // Maps of the query parts: boxes of 64 columns x `rows` rows over the R * H query heads.
-inline bool paged_tc_q_maps(const PagedMlaArgs &a, uint32_t rows, CUtensorMap *qn, CUtensorMap *qr)
+inline bool paged_tc_q_maps(const PagedMlaArgs &args, uint32_t rows, CUtensorMap *qn, CUtensorMap *qr)
 {
+    const PagedMlaArgs a = one_head_pitch(args);
     const uint64_t heads = (uint64_t)a.R * a.H;
     return make_tma_2d(qn, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q_nope, kPtDl, heads, (uint64_t)a.nope_ld_h * 2, 64, rows,
                        CU_TENSOR_MAP_SWIZZLE_128B) &&

@@ -581,8 +581,14 @@ nsa_status nsa_local_attention(const void *q_dev, int64_t q_ld, const void *k_ca
  * some row of the request does see reaches all rows of that request.
  * Returns NSA_ERR_INVALID_ARG for R not a multiple of rows_per_req, a bad size, a
  * NULL or misaligned buffer, or too small a workspace; NSA_ERR_UNSUPPORTED for a
- * dtype combination or size the kernels do not take (more than 2^30 positions or
- * 2^31 slots, d_latent beyond 8192, E4M3 with d_latent % 128 != 0 or odd d_rope).
+ * dtype combination or size the kernels do not take (more than 2^30 positions,
+ * 2^31 slots or query heads, d_latent beyond 8192, E4M3 with d_latent % 128 != 0 or
+ * odd d_rope).
+ * The 512 + 64 shape with BF16 q runs on the tensor cores (tcgen05) when page_size is a
+ * multiple of 8, q and the cache are 16-byte aligned, and the query heads follow one
+ * another at one pitch (ld_r == H * ld_h, ld_h a multiple of 8: contiguous q, or the two
+ * parts of a concatenated [R, H, 576]).  Everything else runs on the CUDA cores, at a
+ * small fraction of that speed.
  * Device errors (NSA_ERR_BOUNDS): a row_len outside [0, max_row_len] makes its row
  * see no key; the positions of a page outside [0, num_pages) are left out.
  */
