@@ -329,8 +329,8 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         }
                     }
                     // the tile after the next one into L2 while this one is worked on
-                    const int y2 = box_row(t + 2);
-                    if (lane >= box0 && lane < box1 && y2 >= 0)
+                    const int y2 = SCR ? -1 : box_row(t + 2);
+                    if (!SCR && lane >= box0 && lane < box1 && y2 >= 0)
                         prefetch_l2_bulk(p.t.kv + (int64_t)y2 * kRowBytes, (uint32_t)p.t.box_rows * kRowBytes);
                     y = y1;
                     y1 = y2;
@@ -465,6 +465,41 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 else
                     for (int64_t e = lane; e < (int64_t)p.cols * kPtDl; e += 32) p.out[row0 * kPtDl + e] = __float2bfloat16_rn(0.f);
                 for (int c = lane; c < p.cols; c += 32) p.lse[row0 + c] = -INFINITY;
+            }
+            if (SCR && work) {
+                // ---------------------------------------------------- rows into L2 ahead of the row warps
+                constexpr int kAhead = 3;
+                const int per = kScrRows / p.t.box_rows;  // boxes of this CTA's part of a tile
+                Seg f = s;
+                int ft = f.t0;
+                bool fetch = true;
+                auto prefetch = [&]() {
+                    if (!fetch) return;
+                    const int pos = ft * kPtTok + peer * kScrRows + lane * p.t.box_rows;
+                    if (lane < per && pos < f.len) {
+                        const int page = __ldg(p.t.page_table + (int64_t)f.b * p.t.pt_ld + pos / p.t.ps);
+                        if (page >= 0 && page < p.t.num_pages)
+                            prefetch_l2_bulk(p.t.kv + ((int64_t)page * p.t.ps + pos % p.t.ps) * kPtFp8Row,
+                                             (uint32_t)p.t.box_rows * kPtFp8Row);
+                    }
+                    if (++ft >= f.t1) {
+                        fetch = f.next(p);
+                        ft = f.t0;
+                    }
+                };
+                for (int x = 0; x < kAhead; ++x) prefetch();
+                uint32_t sph = 0;
+                int ss = 0;
+                bool ok = true;
+                while (fetch && ok) {
+                    ok = mbar_wait(&sm->scr_full[ss], sph, kPtWait) && !sm->abort;  // a tile further
+                    ok = __all_sync(0xffffffffu, ok) != 0;
+                    prefetch();
+                    if (++ss == kScrSlots) {
+                        ss = 0;
+                        sph ^= 1;
+                    }
+                }
             }
         }
     } else if (warp < 4 + 4 * kGroups) {
@@ -709,14 +744,21 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             const int d = threadIdx.x - kRow0;
             uint8_t *scr = p.scratch + (int64_t)blockIdx.x * kScrSlots * kScrRows * kScrRow;
             const int off = peer * kScrRows;     // this CTA's part of a tile
-            constexpr int kSteps = kScrRows / 32;  // steps of 32 rows a tile
-            // the step to load next, two ahead of the one that is stored
+            constexpr int kSteps = kScrRows / kScrStep;  // steps a tile
+            // The step whose page is asked for next: a step before its rows are loaded, which is two
+            // steps before they are stored.  The page is looked at only then, so nothing waits for it
+            // (a lookup in front of its loads took 2 - 3 thousand cycles a step).
             Seg f = s;
-            int ft = f.t0, fu = 0;
-            bool fetch = true;
-            auto load = [&](ScrRows &x) {
+            int ft = f.t0, fu = 0, page = 0, pos = 0;
+            bool fetch = true, in = false;
+            auto look = [&]() {
+                in = false;
                 if (!fetch) return;
-                x.load(p.t, d, f.b, ft * kPtTok + off + 32 * fu, f.len);
+                pos = ft * kPtTok + off + kScrStep * fu + (d >> 3);
+                if (pos < f.len) {
+                    in = true;
+                    page = __ldg(p.t.page_table + (int64_t)f.b * p.t.pt_ld + pos / p.t.ps);
+                }
                 if (++fu == kSteps) {
                     fu = 0;
                     if (++ft >= f.t1) {
@@ -725,13 +767,25 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     }
                 }
             };
+            auto load = [&](ScrRows &x) {
+                int slot = -1;
+                if (in) {
+                    if (page >= 0 && page < p.t.num_pages)
+                        slot = page * p.t.ps + pos % p.t.ps;
+                    else
+                        set_status(p.t.status, NSA_ERR_BOUNDS);
+                }
+                x.load(p.t, d, slot);
+                look();
+            };
+            look();
             int64_t left = (sm->share.g1 - sm->share.g0) * kSteps;
             uint32_t sph = 0;
             int ss = 0, u = 0;
             bool ok = true;
             auto step = [&](ScrRows &x) {
                 if (u == 0 && !mbar_wait(&sm->scr_free[ss], sph ^ 1, kPtWait)) ok = false;
-                x.store(scr + (ss * kScrRows + 32 * u) * kScrRow, d);
+                x.store(scr + (ss * kScrRows + kScrStep * u) * kScrRow, d);
                 if (++u == kSteps) {
                     u = 0;
                     asm volatile("fence.proxy.async.global;" ::: "memory");

@@ -245,9 +245,10 @@ __device__ __forceinline__ uint32_t live_rows(const PagedTc &p, uint32_t boxes, 
 
 // Rows expanded from registers into a scratch copy of a CTA's part of the tile in global
 // memory (which stays in L2), for clusters: thread d of kScrThreads owns chunk d % 8 of each
-// 128-value block of row d / 8 of 32.  Two sets of registers take turns, so a row is loaded
-// while the one before it is expanded.
-constexpr int kScrThreads = 256;
+// 128-value block of row d / 8 of a step's kScrStep.  Two sets of registers take turns, so a
+// row is loaded while the one before it is expanded.
+constexpr int kScrThreads = 128;
+constexpr int kScrStep = kScrThreads / 8;       // rows at a time
 constexpr int kScrSlots = 3;                    // parts of tiles a CTA's scratch holds
 constexpr int kScrRow = 2 * (kPtDl + kPtDr);    // bytes
 
@@ -255,16 +256,14 @@ struct ScrRows {
     uint4 w[5];
     float4 sc;
 
-    // pos0: the position of row 0 of the 32
-    __device__ __forceinline__ void load(const PagedTc &p, int d, int b, int pos0, int len)
+    // slot: the row's slot, or -1 for a row of zeros
+    __device__ __forceinline__ void load(const PagedTc &p, int d, int slot)
     {
-        const int pos = pos0 + (d >> 3);
-        const int page = checked_page(p, p.page_table + (int64_t)b * p.pt_ld, pos, len);
 #pragma unroll
         for (int m = 0; m < 5; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
         sc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (page >= 0) {
-            const uint8_t *row = p.kv + ((int64_t)page * p.ps + pos % p.ps) * kPtFp8Row;
+        if (slot >= 0) {
+            const uint8_t *row = p.kv + (int64_t)slot * kPtFp8Row;
 #pragma unroll
             for (int m = 0; m < 5; ++m)
                 w[m] = __ldg(reinterpret_cast<const uint4 *>(row + (m < 4 ? 128 * m : kPtDl + 16) + 16 * (d & 7)));
