@@ -8,7 +8,7 @@
 // totals prefer the lower position, -0 equals +0, NaN ranks lowest, as the
 // top-k ranks scores).
 #include "nsa_internal.cuh"
-#include "sm100.cuh"
+#include "sm100_paged.cuh"
 
 namespace nsa {
 namespace {

@@ -9,7 +9,7 @@
 #pragma once
 
 #include "paged_mla.cuh"
-#include "sm100.cuh"
+#include "sm100_paged.cuh"
 #include "tma_host.h"
 
 namespace nsa {
