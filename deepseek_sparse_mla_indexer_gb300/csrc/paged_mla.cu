@@ -110,7 +110,7 @@ paged_mla_simt_kernel(PagedMlaArgs p, int HG, void *out, float *lse)
         const int e = threadIdx.x + i * kThreads;
         if (i < n_acc && e < hg * p.d_latent) {
             const int h = e / p.d_latent, d = e - h * p.d_latent;
-            const float l = l_run[h], v = l > 0.f ? acc[i] / l : 0.f;
+            const float l = l_run[h], v = l > 0.f ? acc[i] / l : l == l ? 0.f : l;
             const int64_t o = ((int64_t)r * p.H + h0 + h) * p.d_latent + d;
             if (QDT == NSA_DT_BF16)
                 ((__nv_bfloat16 *)out)[o] = __float2bfloat16_rn(v);  // the result's type
@@ -118,8 +118,10 @@ paged_mla_simt_kernel(PagedMlaArgs p, int HG, void *out, float *lse)
                 ((float *)out)[o] = v;
         }
     }
-    for (int h = threadIdx.x; h < hg; h += kThreads)
-        lse[(int64_t)r * p.H + h0 + h] = l_run[h] > 0.f ? m_run[h] + logf(l_run[h]) : -INFINITY;
+    for (int h = threadIdx.x; h < hg; h += kThreads) {
+        const float l = l_run[h];
+        lse[(int64_t)r * p.H + h0 + h] = l > 0.f ? m_run[h] + logf(l) : l == l ? -INFINITY : l;
+    }
 }
 
 template <int QDT, int KDT>

@@ -58,7 +58,7 @@ struct AShared {
     float red[4][kCols];
     float l_col[kCols];
     int len[kCols];                   // positions the column's row sees
-    int min_len[4];
+    int min_len[4];                   // shortest of all the CTA's columns, one copy a group
     uint64_t pair_full[5];            // block pair m of the tile landed (m = 4: the rope block)
     uint64_t pair_free[5];            // its readers are done (m = 4: every product of the tile)
     uint64_t q_full, q_empty, s_full, p_full, o_fin;
@@ -66,6 +66,7 @@ struct AShared {
     uint64_t scr_full[kScrSlots], scr_free[kScrSlots];  // half tiles of the scratch
     TileShare share;
     uint32_t tmem_base;
+    volatile uint32_t scr_tiles;      // parts of tiles that the row warps have expanded
     volatile int abort;
 };
 constexpr int raw_slots(int nc) { return nc == 16 ? 3 : 2; }  // as many as fit beside Q and the tile
@@ -131,6 +132,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+__device__ __forceinline__ bool not_finite(uint32_t f32) { return (f32 & 0x7f800000u) == 0x7f800000u; }
+// Two bf16 with what is not finite replaced by 0.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w)
+{
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+    if ((w & 0x00007f80u) == 0x00007f80u) w &= 0xffff0000u;
+    return w;
+}
+
 // G columns of the accumulator at `taddr` from or into TMEM, one lane a thread.
 template <int G>
 __device__ __forceinline__ void tmem_ldg(uint32_t taddr, uint32_t (&r)[G])
@@ -190,6 +200,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             mbar_init(&sm->scr_full[i], kScrThreads / 32);
             mbar_init(&sm->scr_free[i], 1);
         }
+        sm->scr_tiles = 0;
         sm->abort = 0;
         fence_mbar_init();
     }
@@ -469,14 +480,14 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             if (SCR && work) {
                 // ---------------------------------------------------- rows into L2 ahead of the row warps
                 constexpr int kAhead = 3;
+                constexpr int kPolls = 1 << 22;  // about a second
                 const int per = kScrRows / p.t.box_rows;  // boxes of this CTA's part of a tile
                 Seg f = s;
                 int ft = f.t0;
                 bool fetch = true;
-                auto prefetch = [&]() {
-                    if (!fetch) return;
+                auto prefetch = [&](bool wanted) {
                     const int pos = ft * kPtTok + peer * kScrRows + lane * p.t.box_rows;
-                    if (lane < per && pos < f.len) {
+                    if (wanted && lane < per && pos < f.len) {
                         const int page = __ldg(p.t.page_table + (int64_t)f.b * p.t.pt_ld + pos / p.t.ps);
                         if (page >= 0 && page < p.t.num_pages)
                             prefetch_l2_bulk(p.t.kv + ((int64_t)page * p.t.ps + pos % p.t.ps) * kPtFp8Row,
@@ -487,19 +498,18 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         ft = f.t0;
                     }
                 };
-                for (int x = 0; x < kAhead; ++x) prefetch();
-                uint32_t sph = 0;
-                int ss = 0;
-                bool ok = true;
-                while (fetch && ok) {
-                    ok = mbar_wait(&sm->scr_full[ss], sph, kPtWait) && !sm->abort;  // a tile further
-                    ok = __all_sync(0xffffffffu, ok) != 0;
-                    prefetch();
-                    if (++ss == kScrSlots) {
-                        ss = 0;
-                        sph ^= 1;
+                // Paced by a count, not by the barriers' phases: the requests without a key may have
+                // kept this warp busy for several tiles, which it then passes over.
+                for (uint32_t n = 0; fetch; ++n) {
+                    uint32_t done = sm->scr_tiles;
+                    for (int x = 0; done + kAhead <= n && !sm->abort && x < kPolls; ++x) {
+                        __nanosleep(200);
+                        done = sm->scr_tiles;
                     }
+                    if (done + kAhead <= n) break;
+                    prefetch(n >= done);
                 }
+                __syncwarp();
             }
         }
     } else if (warp < 4 + 4 * kGroups) {
@@ -513,18 +523,23 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             bool ok = true;
             for (bool more = true; more && ok; more = s.next(p), ++seg) {
                 const int col0 = (s.j * p.team + rank) * NC;  // first column of this CTA in the request
-                if (et == 0) sm->min_len[grp] = 0x7fffffff;
-                __syncwarp();  // et 0 .. kGrp-1 are lanes of one warp
-                if (et < kGrp) {
-                    const int c = col0 + cb + et;
-                    int len = 0x7fffffff;  // padding: never masked, never written
-                    if (c < p.cols) {
-                        const int L = p.t.row_len[(int64_t)s.b * p.t.n + c / p.t.H];
-                        len = L >= 0 && L <= p.t.max_row_len ? L : 0;
+                if (et < 32) {
+                    int shortest = 0x7fffffff;
+                    for (int cc = lane; cc < NC; cc += 32) {
+                        const int c = col0 + cc;
+                        int len = 0x7fffffff;  // padding: never masked, never written
+                        if (c < p.cols) {
+                            const int L = p.t.row_len[(int64_t)s.b * p.t.n + c / p.t.H];
+                            len = L >= 0 && L <= p.t.max_row_len ? L : 0;
+                        }
+                        shortest = min(shortest, len);
+                        if (cc >= cb && cc < cb + kGrp) {
+                            sm->len[cc] = len;
+                            sm->m_run[cc] = -INFINITY;
+                        }
                     }
-                    sm->len[cb + et] = len;
-                    sm->m_run[cb + et] = -INFINITY;
-                    atomicMin(&sm->min_len[grp], len);
+                    shortest = __reduce_min_sync(0xffffffffu, shortest);
+                    if (lane == 0) sm->min_len[grp] = shortest;
                 }
                 bar_sync(bar, 128);
                 const int min_len = sm->min_len[grp];
@@ -539,6 +554,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     if (!ok) fail();
                     tc_fence_after();
                     const bool whole = (t + 1) * kPtTok <= min_len && __all_sync(0xffffffffu, valid);
+                    bool odd = false;  // a score of this key is not finite (looked at where columns are masked)
                     // exponents d = x - m; a key above its column's maximum by 2^8 asks for new maxima
                     float2 d[kGrp / 2];
                     auto exponents = [&]() {
@@ -554,6 +570,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                                                 sc, make_float2(-m.z, -m.w));
                         }
                         if (!whole) {
+                            odd = not_finite(sa[0]);
 #pragma unroll
                             for (int c = 0; c < kGrp / 2; ++c) {
                                 if (!valid || pos >= sm->len[cb + 2 * c]) d[c].x = -INFINITY;
@@ -619,15 +636,29 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         }
                         *reinterpret_cast<uint4 *>(p_s + sw128_offset(key, cb / 8 + c8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
-                    if (ROWS == kBf16Rows && !valid) {
-                        // what lies behind the length may be NaN, which a weight of 0 would not hide: this
-                        // group's share of the key's latent blocks becomes 0 (S^T has read them)
+                    // A weight of 0 does not hide what is not finite, so it is taken out of this group's share
+                    // of the key's latent blocks (S^T has read them): all of a row that is not there, and from
+                    // a row that only some columns see the values that are not finite.  Such a value makes every
+                    // column's score of the key not finite, which is how it is noticed and what the columns
+                    // that see the key get it from.
+                    const bool absent = ROWS == kBf16Rows && !valid;
+                    if (absent || (odd && valid && pos >= min_len)) {
                         for (int m = 0; m < 4; ++m) mbar_wait(&sm->pair_full[m], i & 1, kPtWait);
 #pragma unroll 1
                         for (int c = grp * (8 / kGroups); c < (grp + 1) * (8 / kGroups); ++c) {
                             uint4 *r = reinterpret_cast<uint4 *>(kv_s + c * kPtBlk + key * 128);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) r[k] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+                            for (int k = 0; k < 8; ++k) {
+                                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                                if (!absent) {
+                                    v = r[k];
+                                    v.x = finite_pair(v.x);
+                                    v.y = finite_pair(v.y);
+                                    v.z = finite_pair(v.z);
+                                    v.w = finite_pair(v.w);
+                                }
+                                r[k] = v;
+                            }
                         }
                     }
                     fence_proxy_async_smem();
@@ -791,6 +822,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     asm volatile("fence.proxy.async.global;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm->scr_full[ss]);
+                    if (d == 0) sm->scr_tiles = sm->scr_tiles + 1;
                     if (++ss == kScrSlots) {
                         ss = 0;
                         sph ^= 1;

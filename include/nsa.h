@@ -576,9 +576,8 @@ nsa_status nsa_local_attention(const void *q_dev, int64_t q_ld, const void *k_ca
  *                      (may be NULL if that is 0).  Calls that may overlap on the GPU need
  *                      workspaces of their own; nothing in it needs to start at zero and
  *                      nothing is kept in it between calls
- * Positions at or past row_len are never used, whatever they hold, as long as no
- * other row of the same request sees them: a NaN or infinity at a position that
- * some row of the request does see reaches all rows of that request.
+ * Positions at or past row_len are never used, whatever they hold: a NaN or infinity
+ * at a position that only some rows of a request see reaches those rows alone.
  * Returns NSA_ERR_INVALID_ARG for R not a multiple of rows_per_req, a bad size, a
  * NULL or misaligned buffer, or too small a workspace; NSA_ERR_UNSUPPORTED for a
  * dtype combination or size the kernels do not take (more than 2^30 positions,
