@@ -31,14 +31,22 @@ using namespace sm100;
 constexpr int kCols = 128;       // columns of one pass
 constexpr int kMaxStages = 12;   // ring stages: as many as shared memory holds beside Q
 constexpr int kPassTiles = 4;    // tiles per round of passes, when there are several
-constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kBufCols = 256;   // of one of the two score buffers
+// Up to kSplitCols columns, a score is summed in four accumulators (two or three blocks of the
+// row each) that the epilogue adds.  The accumulation truncates: a chain of 36 products left
+// scores 4.5e-7 of themselves too small, one-sided, which the sum over few heads does not average.
+// More columns have no room for four, and less need.
+constexpr int kSplitCols = 64;
+constexpr float kLog2eLow = 1.92596299e-8f;  // log2(e) less its fp32 value
 
 struct WShared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full, q_empty, s_full[2], s_empty[2];
     RawShared raw;
     uint64_t rope_full, rope_empty;  // fp8: the rope parts have a stage of their own
-    alignas(16) float nlse2[kCols];  // -lse in log2 units; -inf: no weight (padding, an empty row)
+    alignas(16) float nlse2[kCols];  // -lse in log2 units; -inf: no weight (padding, an empty row);
+                                     // split scores: behind kSplitCols of them, the columns' factors
     int len[kCols];      // positions the column's row sees; 0: no weight
     int min_len[4];
     TileShare share;
@@ -46,12 +54,14 @@ struct WShared {
     volatile int abort;
 };
 constexpr size_t kAux = (sizeof(WShared) + 15) / 16 * 16;
+static_assert(232448 - 1024 - 9 * kCols * 128 - kAux >= 5 * kPtBlk, "five stages beside 128 columns (four: 4 % slower)");
 
 struct WParams {
     PagedTc t;
     const float *lse;
     float *total;
     int64_t total_ld;
+    float scale_err;  // relative error of t.scale_log2
     int cols, passes, N, stages;  // columns per request, passes, MMA columns of a pass, ring stages
     int raw;                      // fp8: slots of raw codes
 };
@@ -99,7 +109,8 @@ struct Walk {
     }
 };
 
-template <bool FP8>
+// SPLIT: scores in four accumulators (N <= kSplitCols).
+template <bool FP8, bool SPLIT>
 __global__ void __launch_bounds__(FP8 ? 256 + kDqThreads : 256, 1)
 key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
                       const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
@@ -284,14 +295,16 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                     if (!mbar_wait(&sm->s_empty[buf], bph ^ 1, kPtWait)) ok = false;
                     for (int c = 0; c < 9; ++c) {
                         const bool rope = FP8 && c == 8;
+                        const int acc = SPLIT ? min(c >> 1, 3) : 0;
+                        const bool first = SPLIT ? c < 8 && (c & 1) == 0 : c == 0;
                         if (!mbar_wait(rope ? &sm->rope_full : &sm->full[st], rope ? tile & 1 : ph, kPtWait)) ok = false;
                         tc_fence_after();
                         if (elect_one()) {
                             const uint64_t a_desc = rope ? rope_desc : r_desc + st * (kPtBlk / 16);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_f16(tmem + buf * kCols, a_desc + k * 2, q_desc + (c * q_blk + k * 32) / 16, idesc,
-                                        (c | k) != 0);
+                                mma_f16(tmem + buf * kBufCols + acc * kSplitCols, a_desc + k * 2,
+                                        q_desc + (c * q_blk + k * 32) / 16, idesc, k > 0 || !first);
                             mma_commit(rope ? &sm->rope_empty : &sm->empty[st]);
                             if (c == 8) mma_commit(&sm->s_full[buf]);
                         }
@@ -323,18 +336,31 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                 bar_sync(1, 128);  // the previous piece's columns are read out
                 {
                     const int c = w.pass * kCols + key;
-                    float nl = -INFINITY;
+                    float nl = -INFINITY, fac = 1.f;
                     int len = 0;
                     if (c < p.cols) {
                         const int64_t r = (int64_t)w.b * p.t.n + c / p.t.H;
                         const float l = p.lse[r * p.t.H + c % p.t.H];
                         const int L = p.t.row_len[r];
                         if (l != -INFINITY && L > 0 && L <= p.t.max_row_len) {
-                            nl = -l * 1.4426950408889634f;
+                            // x - lse2 in log2 units with the rounded scale and lse2: what the scale's rounding
+                            // takes from x (of about lse2 where the weight counts) goes into nl, and what nl then
+                            // loses to its own rounding, up to 2^-20, into a factor near 1
+                            const float nl0 = -l * 1.4426950408889634f;
+                            const float lost = fmaf(l, 1.4426950408889634f, nl0) + l * kLog2eLow;
+                            const float give = -fmaf(nl0, p.scale_err, lost);
+                            nl = nl0 + give;
+                            const float rest = give - (nl - nl0);
+                            if (fabsf(rest) < 0.1f) fac = fmaf(rest, 0.69314718055994531f, 1.f);
                             len = L;
                         }
                     }
-                    sm->nlse2[key] = nl;
+                    if (!SPLIT) {
+                        sm->nlse2[key] = nl;
+                    } else if (key < kSplitCols) {
+                        sm->nlse2[key] = nl;
+                        sm->nlse2[kSplitCols + key] = fac;
+                    }
                     sm->len[key] = len;
                     // columns past the MMA's are never looked at
                     const int mn = __reduce_min_sync(0xffffffffu, key < p.N ? len : 0x7fffffff);
@@ -353,41 +379,66 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                     if (!ok) fail();
                     if (bar_red_or(2, 128, !ok || sm->abort)) { more = false; break; }
                     tc_fence_after();
-                    float sum;
+                    float sum = 0.f;
+                    constexpr int kW = SPLIT ? 8 : 16;  // columns a step
+                    auto scores = [&](int c0, uint32_t (&s)[kW]) {
+                        const uint32_t at = lanes + buf * kBufCols + c0;
+                        if constexpr (SPLIT) {
+                            uint32_t u[3][kW];
+                            tmem_ld8(at, s);
+#pragma unroll
+                            for (int a = 0; a < 3; ++a) tmem_ld8(at + (a + 1) * kSplitCols, u[a]);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < kW; ++j)
+                                s[j] = __float_as_uint((__uint_as_float(s[j]) + __uint_as_float(u[0][j])) +
+                                                       (__uint_as_float(u[1][j]) + __uint_as_float(u[2][j])));
+                        } else {
+                            tmem_ld16(at, s);
+                            tmem_ld_wait();
+                        }
+                    };
                     if ((t + 1) * kPtTok <= min_len) {
                         // every column is a real one and sees the whole tile: nothing to select
                         const float2 sc = make_float2(p.t.scale_log2, p.t.scale_log2);
                         const float4 *nl = reinterpret_cast<const float4 *>(sm->nlse2);
+                        const float4 *fc = reinterpret_cast<const float4 *>(sm->nlse2 + kSplitCols);
                         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-                        for (int c0 = 0; c0 < p.N; c0 += 16) {
-                            uint32_t s[16];
-                            tmem_ld16(lanes + buf * kCols + c0, s);
-                            tmem_ld_wait();
+                        for (int c0 = 0; c0 < p.N; c0 += kW) {
+                            uint32_t s[kW];
+                            scores(c0, s);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
+                            for (int j = 0; j < kW / 4; ++j) {
                                 const float4 n = nl[c0 / 4 + j];
-                                const float2 x = fma2(make_float2(__uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1])), sc,
-                                                      make_float2(n.x, n.y));
-                                const float2 y = fma2(make_float2(__uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3])),
-                                                      sc, make_float2(n.z, n.w));
-                                acc[0] = add2(acc[0], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
-                                acc[1] = add2(acc[1], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+                                float2 x = fma2(make_float2(__uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1])), sc,
+                                                make_float2(n.x, n.y));
+                                float2 y = fma2(make_float2(__uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3])), sc,
+                                                make_float2(n.z, n.w));
+                                x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                                y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                                if constexpr (SPLIT) {
+                                    const float4 f = fc[c0 / 4 + j];
+                                    acc[0] = fma2(x, make_float2(f.x, f.y), acc[0]);
+                                    acc[1] = fma2(y, make_float2(f.z, f.w), acc[1]);
+                                } else {  // over more columns these roundings average out (the factors took 6 %)
+                                    acc[0] = add2(acc[0], x);
+                                    acc[1] = add2(acc[1], y);
+                                }
                             }
                         }
                         sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
                     } else {
-                        sum = 0.f;
 #pragma unroll 1
-                        for (int c0 = 0; c0 < p.N; c0 += 16) {
-                            uint32_t s[16];
-                            tmem_ld16(lanes + buf * kCols + c0, s);
-                            tmem_ld_wait();
+                        for (int c0 = 0; c0 < p.N; c0 += kW) {
+                            uint32_t s[kW];
+                            scores(c0, s);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
+                            for (int j = 0; j < kW; ++j) {
                                 const float e = ex2_approx(fmaf(__uint_as_float(s[j]), p.t.scale_log2, sm->nlse2[c0 + j]));
                                 // a column without weight may hold anything: selected away, not multiplied
-                                sum += pos < sm->len[c0 + j] ? e : 0.f;
+                                const float v = pos < sm->len[c0 + j] ? e : 0.f;
+                                sum = SPLIT ? fmaf(v, sm->nlse2[kSplitCols + c0 + j], sum) : sum + v;
                             }
                         }
                     }
@@ -453,6 +504,16 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
     }
 }
 
+template <bool FP8, bool SPLIT>
+nsa_status launch(const WParams &p, const CUtensorMap &qn, const CUtensorMap &qr, const CUtensorMap &kv,
+                  const CUtensorMap &sc, const CUtensorMap &rope, unsigned grid, size_t smem, cudaStream_t stream)
+{
+    constexpr auto kern = key_weights_tc_kernel<FP8, SPLIT>;
+    NSA_CUDA_TRY(max_dynamic_smem<kern>(232448));
+    kern<<<grid, FP8 ? 256 + kDqThreads : 256, smem, stream>>>(p, qn, qr, kv, sc, rope);
+    return launch_status();
+}
+
 }  // namespace
 
 nsa_status key_weights_tc_try_launch(const PagedMlaArgs &a, const float *lse, float *total, int64_t total_ld,
@@ -467,6 +528,7 @@ nsa_status key_weights_tc_try_launch(const PagedMlaArgs &a, const float *lse, fl
     p.lse = lse;
     p.total = total;
     p.total_ld = total_ld;
+    p.scale_err = (float)((double)a.sm_scale * 1.4426950408889634 / p.t.scale_log2 - 1.0);
     p.cols = a.rows_per_req * a.H;
     p.passes = (int)ceil_div(p.cols, kCols);
     p.N = p.passes > 1 ? kCols : (int)ceil_div(p.cols, 16) * 16;
@@ -484,14 +546,11 @@ nsa_status key_weights_tc_try_launch(const PagedMlaArgs &a, const float *lse, fl
         return NSA_ERR_CUDA;
     const int64_t tiles = (int64_t)p.t.B * ceil_div(a.max_row_len, kPtTok);
     const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
-    if (fp8) {
-        NSA_CUDA_TRY(max_dynamic_smem<key_weights_tc_kernel<true>>(232448));
-        key_weights_tc_kernel<true><<<grid, 256 + kDqThreads, smem, stream>>>(p, qn, qr, kv, sc, rope);
-    } else {
-        NSA_CUDA_TRY(max_dynamic_smem<key_weights_tc_kernel<false>>(232448));
-        key_weights_tc_kernel<false><<<grid, 256, smem, stream>>>(p, qn, qr, kv, sc, rope);
-    }
-    return launch_status();
+    const bool split = p.N <= kSplitCols;
+    if (fp8) return split ? launch<true, true>(p, qn, qr, kv, sc, rope, grid, smem, stream)
+                          : launch<true, false>(p, qn, qr, kv, sc, rope, grid, smem, stream);
+    return split ? launch<false, true>(p, qn, qr, kv, sc, rope, grid, smem, stream)
+                 : launch<false, false>(p, qn, qr, kv, sc, rope, grid, smem, stream);
 }
 
 }  // namespace nsa
