@@ -33,10 +33,10 @@ constexpr int kMaxStages = 12;   // ring stages: as many as shared memory holds 
 constexpr int kPassTiles = 4;    // tiles per round of passes, when there are several
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBufCols = 256;   // of one of the two score buffers
-// Up to kSplitCols columns, a score is summed in four accumulators (two or three blocks of the
-// row each) that the epilogue adds.  The accumulation truncates: a chain of 36 products left
-// scores 4.5e-7 of themselves too small, one-sided, which the sum over few heads does not average.
-// More columns have no room for four, and less need.
+// A score is summed in four accumulators (two or three blocks of the row each) up to kSplitCols
+// columns and in two beyond, which is what TMEM holds twice; the epilogue adds them.  The tensor
+// core's accumulation truncates: a single chain of 36 products left scores 4.5e-7 of themselves
+// too small, one-sided, and weights 1.6e-6 off (128 heads; two: 0.7e-6 at 1 % of the time).
 constexpr int kSplitCols = 64;
 constexpr float kLog2eLow = 1.92596299e-8f;  // log2(e) less its fp32 value
 
@@ -116,6 +116,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                       const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
                       const __grid_constant__ CUtensorMap rope_map)
 {
+    constexpr uint32_t kAccCols = SPLIT ? kSplitCols : kCols;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *q_s = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t q_blk = (uint32_t)p.N * 128;
@@ -295,15 +296,15 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                     if (!mbar_wait(&sm->s_empty[buf], bph ^ 1, kPtWait)) ok = false;
                     for (int c = 0; c < 9; ++c) {
                         const bool rope = FP8 && c == 8;
-                        const int acc = SPLIT ? min(c >> 1, 3) : 0;
-                        const bool first = SPLIT ? c < 8 && (c & 1) == 0 : c == 0;
+                        const int acc = SPLIT ? min(c >> 1, 3) : c >> 2 ? 1 : 0;
+                        const bool first = SPLIT ? c < 8 && (c & 1) == 0 : c < 8 && (c & 3) == 0;
                         if (!mbar_wait(rope ? &sm->rope_full : &sm->full[st], rope ? tile & 1 : ph, kPtWait)) ok = false;
                         tc_fence_after();
                         if (elect_one()) {
                             const uint64_t a_desc = rope ? rope_desc : r_desc + st * (kPtBlk / 16);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_f16(tmem + buf * kBufCols + acc * kSplitCols, a_desc + k * 2,
+                                mma_f16(tmem + buf * kBufCols + acc * kAccCols, a_desc + k * 2,
                                         q_desc + (c * q_blk + k * 32) / 16, idesc, k > 0 || !first);
                             mma_commit(rope ? &sm->rope_empty : &sm->empty[st]);
                             if (c == 8) mma_commit(&sm->s_full[buf]);
@@ -383,19 +384,24 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                     constexpr int kW = SPLIT ? 8 : 16;  // columns a step
                     auto scores = [&](int c0, uint32_t (&s)[kW]) {
                         const uint32_t at = lanes + buf * kBufCols + c0;
+                        auto sum_of = [](uint32_t a, uint32_t b) {
+                            return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+                        };
                         if constexpr (SPLIT) {
                             uint32_t u[3][kW];
                             tmem_ld8(at, s);
 #pragma unroll
-                            for (int a = 0; a < 3; ++a) tmem_ld8(at + (a + 1) * kSplitCols, u[a]);
+                            for (int a = 0; a < 3; ++a) tmem_ld8(at + (a + 1) * kAccCols, u[a]);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < kW; ++j)
-                                s[j] = __float_as_uint((__uint_as_float(s[j]) + __uint_as_float(u[0][j])) +
-                                                       (__uint_as_float(u[1][j]) + __uint_as_float(u[2][j])));
+                            for (int j = 0; j < kW; ++j) s[j] = sum_of(sum_of(s[j], u[0][j]), sum_of(u[1][j], u[2][j]));
                         } else {
+                            uint32_t u[kW];
                             tmem_ld16(at, s);
+                            tmem_ld16(at + kAccCols, u);
                             tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < kW; ++j) s[j] = sum_of(s[j], u[j]);
                         }
                     };
                     if ((t + 1) * kPtTok <= min_len) {
@@ -421,7 +427,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                                     const float4 f = fc[c0 / 4 + j];
                                     acc[0] = fma2(x, make_float2(f.x, f.y), acc[0]);
                                     acc[1] = fma2(y, make_float2(f.z, f.w), acc[1]);
-                                } else {  // over more columns these roundings average out (the factors took 6 %)
+                                } else {  // over more columns nl's roundings average out
                                     acc[0] = add2(acc[0], x);
                                     acc[1] = add2(acc[1], y);
                                 }
