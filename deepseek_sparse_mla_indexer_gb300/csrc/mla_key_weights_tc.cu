@@ -30,6 +30,7 @@ using namespace sm100;
 
 constexpr int kCols = 128;       // columns of one pass
 constexpr int kMaxStages = 12;   // ring stages: as many as shared memory holds beside Q
+constexpr int kPiece = 2;        // what a further request in a share costs, in tiles
 constexpr int kPassTiles = 4;    // tiles per round of passes, when there are several
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBufCols = 256;   // of one of the two score buffers
@@ -68,44 +69,47 @@ struct WParams {
 
 // The tiles of a share as (request, pass, tile range) pieces, the same for every role.
 struct Walk {
-    int b, t0, t1, c0, c1, pass, tiles, len;
-    int64_t left;  // tiles of the share from c0 on
+    int b, t0, t1, c0, c1, pass, tiles, len, piece;
+    int64_t left;  // places of the share behind tile t1
 
     __device__ __forceinline__ bool start(const WParams &p, const TileShare &s)
     {
         left = s.g1 - s.g0;
         if (left <= 0) return false;
         b = s.b;
-        t0 = (int)s.off;
-        enter(p);
-        return true;
-    }
-    __device__ __forceinline__ void enter(const WParams &p)
-    {
+        piece = s.piece;
         len = request_len(p.t, b);
         tiles = tiles_of(len);
-        t1 = (int)min((int64_t)tiles, t0 + left);
+        return enter(p, (int)s.off);
+    }
+    // the request from place `at` on; false if the share ends before its next tile
+    __device__ __forceinline__ bool enter(const WParams &p, int at)
+    {
+        const int end = (int)min((int64_t)(tiles + piece), at + left);
+        left -= end - at;
+        t0 = max(0, at - piece);
+        t1 = max(0, end - piece);
         c0 = t0;
         c1 = p.passes == 1 ? t1 : min(t1, c0 + kPassTiles);
         pass = 0;
+        return t1 > t0;
     }
     __device__ __forceinline__ bool next(const WParams &p)
     {
         if (++pass < p.passes) return true;
         pass = 0;
-        left -= c1 - c0;
-        if (left <= 0) return false;
         if (c1 < t1) {
             c0 = c1;
             c1 = min(t1, c0 + kPassTiles);
             return true;
         }
+        if (left <= 0) return false;
         do {
-            ++b;
-            t0 = 0;
-            enter(p);
-        } while (tiles == 0 && b + 1 < p.t.B);
-        return tiles > 0;
+            if (++b >= p.t.B) return false;
+            len = request_len(p.t, b);
+            tiles = tiles_of(len);
+        } while (tiles == 0);
+        return enter(p, 0);
     }
 };
 
@@ -160,7 +164,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
         prefetch_tensormap(&kv_map);
     }
     tc_fence_before();
-    find_share(p.t, 1, blockIdx.x, gridDim.x, &sm->share);  // ends with a block barrier
+    find_share(p.t, 1, kPiece, blockIdx.x, gridDim.x, &sm->share);  // ends with a block barrier
     tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
     auto fail = [&]() {

@@ -43,6 +43,11 @@ constexpr int kMaxTeam = 8;
 // tile and expanded from there; or fp8 rows expanded into the CTA's scratch in global memory
 // (half a tile for each CTA of a pair) and loaded from it as bf16 rows are.
 enum Rows { kBf16Rows, kRawRows, kScratchRows };
+// What a further request in a share costs, in tiles: its epilogue, the loads that find it and its
+// first tiles from HBM took 18 - 22 thousand cycles against 5.2 a tile (32 requests of 128 heads:
+// the last share ended at 163 us, the median at 145, when shares were cut by tiles alone; 2 and 3
+// tiles instead of 4 were 4 % and 1 % slower).  fp8 tiles take longer, and their first ones do not.
+constexpr int piece_of(Rows rows) { return rows == kBf16Rows ? 4 : 2; }
 // Softmax groups of four warps, one key a thread and kGrp columns a group: 16 columns keep a
 // thread's exponents and sums in 72 registers, which leaves room for the row warps.
 constexpr int grp_of(int nc) { return nc == 16 ? 8 : 16; }
@@ -93,38 +98,43 @@ struct AParams {
 
 // The pieces of a share: tiles [t0, t1) of group set j of request b.
 struct Seg {
-    int b, j, t0, t1, tiles, len;
-    int64_t left;
+    int b, j, t0, t1, len;
+    int left;  // places of the share behind this piece
 
     __device__ __forceinline__ bool start(const AParams &p, const TileShare &s)
     {
-        left = s.g1 - s.g0;
+        left = (int)(s.g1 - s.g0);
         if (left <= 0) return false;
         b = s.b;
         len = request_len(p.t, b);
-        tiles = tiles_of(len);
-        j = s.off < 0x100000000LL ? (int)((uint32_t)s.off / (uint32_t)tiles) : (int)(s.off / tiles);
-        t0 = (int)(s.off - (int64_t)j * tiles);
-        t1 = (int)min((int64_t)tiles, t0 + left);
-        return true;
+        const int places = tiles_of(len) + s.piece;
+        j = s.off < 0x100000000LL ? (int)((uint32_t)s.off / (uint32_t)places) : (int)(s.off / places);
+        return enter((int)(s.off - (int64_t)j * places), s.piece);
     }
-    __device__ __forceinline__ bool next(const AParams &p)
+    // the unit from place `at` on; false if the share ends before its next tile
+    __device__ __forceinline__ bool enter(int at, int piece)
     {
-        left -= t1 - t0;
+        const int end = min(tiles_of(len) + piece, at + left);
+        left -= end - at;
+        t0 = max(0, at - piece);
+        t1 = max(0, end - piece);
+        return t1 > t0;
+    }
+    __device__ __forceinline__ bool next(const AParams &p, const TileShare &s)
+    {
         if (left <= 0) return false;
-        t0 = 0;
         if (++j == p.mult) {
             j = 0;
             do {
-                ++b;
+                if (++b >= p.t.B) return false;
                 len = request_len(p.t, b);
-                tiles = tiles_of(len);
-            } while (tiles == 0 && b + 1 < p.t.B);
+            } while (len == 0);
         }
-        t1 = (int)min((int64_t)tiles, left);
-        return tiles > 0;
+        return enter(0, s.piece);
     }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles_of(len); }
 };
+constexpr int64_t kMaxShare = 1 << 30;  // places of a share, so that a place and `left` stay ints
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -215,7 +225,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
     }
     pdl_trigger();  // the join may be launched while this grid works; it waits for its end
     tc_fence_before();
-    find_share(p.t, p.mult, team, p.teams, &sm->share);  // ends with a block barrier
+    find_share(p.t, p.mult, piece_of(ROWS), team, p.teams, &sm->share);  // ends with a block barrier
     if (PAIR) cluster_sync_all();  // the peer's barriers are ready before anything reaches them
     tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
@@ -234,10 +244,10 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             // a cluster's CTAs share out the boxes of a tile in order
             const int box0 = boxes / CL * peer, box1 = boxes / CL * (peer + 1);
             constexpr uint32_t kRowBytes = ROWS == kBf16Rows ? 2 * (kPtDl + kPtDr) : kPtFp8Row;
-            uint32_t i = 0, seg = 0, rph = 0, sph = 0;
-            int rs = 0, ss = 0;
+            uint32_t i = 0, seg = 0, rph = 0;
+            int rs = 0;
             bool ok = true;
-            for (bool more = true; more && ok; more = s.next(p), ++seg) {
+            for (bool more = true; more && ok; more = s.next(p, sm->share), ++seg) {
                 if (seg > 0 && !mbar_wait(&sm->q_empty, (seg - 1) & 1, kPtWait)) ok = false;
                 const int row = s.b * p.cols + (s.j * p.team + rank) * NC;
                 if (elect_one()) {
@@ -298,9 +308,10 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                             tma_load_2d(kv_s + 8 * kPtBlk + x * box_bytes, &rope_map, kFp8RopeX, yb, &sm->pair_full[4]);
                         });
                     } else {
+                        const uint32_t ss = i % kScrSlots;
                         if constexpr (SCR) {
                             // this CTA's part of the tile is in its scratch: written by the row warps
-                            if (!mbar_wait(&sm->scr_full[ss], sph, kPtWait)) ok = false;
+                            if (!mbar_wait(&sm->scr_full[ss], i / kScrSlots & 1, kPtWait)) ok = false;
                             asm volatile("fence.proxy.async.global;" ::: "memory");
                         }
 #pragma unroll
@@ -309,7 +320,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                             if (elect_one()) {
                                 mbar_arrive_expect_tx(&sm->pair_full[m], (m < 4 ? 2 : 1) * blk_bytes);
                                 // every CTA is done with the tile before: its scratch may be written again
-                                if (SCR && m == 4 && i > 0) mbar_arrive(&sm->scr_free[ss == 0 ? kScrSlots - 1 : ss - 1]);
+                                if (SCR && m == 4 && i > 0) mbar_arrive(&sm->scr_free[(i - 1) % kScrSlots]);
                             }
                             __syncwarp();
                             if constexpr (SCR) {
@@ -317,7 +328,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
 #pragma unroll
                                     for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c)
                                         tma_load_2d_multicast(kv_s + c * kPtBlk + peer * (kPtBlk / CL), &kv_map, 64 * c,
-                                                              ((int)blockIdx.x * kScrSlots + ss) * kScrRows,
+                                                              (int)(blockIdx.x * kScrSlots + ss) * kScrRows,
                                                               &sm->pair_full[m], kAll);
                                 }
                                 __syncwarp();
@@ -333,10 +344,6 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                                     }
                                 });
                             }
-                        }
-                        if (SCR && ++ss == kScrSlots) {
-                            ss = 0;
-                            sph ^= 1;
                         }
                     }
                     // the tile after the next one into L2 while this one is worked on
@@ -381,7 +388,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             };
             uint32_t i = 0, seg = 0;
             bool ok = true;
-            for (bool more = true; more && ok; more = s.next(p), ++seg) {
+            for (bool more = true; more && ok; more = s.next(p, sm->share), ++seg) {
                 if (!mbar_wait(&sm->q_full, seg & 1, kPtWait)) ok = false;
                 for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
 #pragma unroll
@@ -432,7 +439,8 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             __syncwarp();
         } else if (warp == 2 && blockIdx.x == 0) {
             // -------------------------------------------------------- the shares of every unit, for the join
-            const int64_t total = sm->share.total, np = share_count(total, p.teams);
+            const int64_t total = sm->share.total, np = sm->share.np;
+            const int piece = sm->share.piece;
             // share k is [total * k / np, total * (k + 1) / np)
             auto share_of = [&](int64_t g) -> int {
                 int k = (int)(g * np / total);
@@ -443,7 +451,8 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             int64_t before = 0;
             for (int base = 0; base < p.t.B; base += 32) {
                 const int b = base + lane;
-                const int64_t v = b < p.t.B ? (int64_t)tiles_of(request_len(p.t, b)) : 0;
+                const int tiles = b < p.t.B ? tiles_of(request_len(p.t, b)) : 0;
+                const int64_t v = tiles > 0 ? tiles + piece : 0;
                 int64_t inc = v;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -455,7 +464,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     for (int j = 0; j < p.mult; ++j, u0 += v) {
                         int4 u = make_int4(0, 0, 0, 0);
                         if (v > 0) {
-                            u.x = share_of(u0);
+                            u.x = share_of(u0 + piece);
                             u.y = share_of(u0 + v - 1);
                             u.z = total * u.x / np < u0 ? 1 : 0;
                         }
@@ -494,7 +503,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                                              (uint32_t)p.t.box_rows * kPtFp8Row);
                     }
                     if (++ft >= f.t1) {
-                        fetch = f.next(p);
+                        fetch = f.next(p, sm->share);
                         ft = f.t0;
                     }
                 };
@@ -521,7 +530,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             const float4 *m4 = reinterpret_cast<const float4 *>(sm->m_run + cb);
             uint32_t i = 0, seg = 0;
             bool ok = true;
-            for (bool more = true; more && ok; more = s.next(p), ++seg) {
+            for (bool more = true; more && ok; more = s.next(p, sm->share), ++seg) {
                 const int col0 = (s.j * p.team + rank) * NC;  // first column of this CTA in the request
                 if (et < 32) {
                     int shortest = 0x7fffffff;
@@ -688,7 +697,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 for (int o = kGrp; o < 32; o <<= 1) ls[0] += __shfl_xor_sync(0xffffffffu, ls[0], o);
                 if (lane < kGrp) sm->red[quad][cb + lane] = ls[0];
                 bar_sync(bar, 128);
-                const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+                const bool whole = s.whole();
                 const int nc = min(kGrp, p.cols - col0 - cb);  // real columns of this group (may be <= 0)
                 const int64_t row0 = (int64_t)s.b * p.cols + col0 + cb;
                 const int64_t slot = (int64_t)blockIdx.x * 2 + (seg > 0 ? 1 : 0);
@@ -740,7 +749,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             uint32_t i = 0, rph = 0;
             int rs = 0;
             bool ok = true;
-            for (bool more = true; more && ok; more = s.next(p)) {
+            for (bool more = true; more && ok; more = s.next(p, sm->share)) {
                 for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
                     if (!mbar_wait(&sm->raw.tile_full[i & 1], (i >> 1) & 1, kPtWait)) ok = false;
                     const uint32_t live = live_rows(p.t, sm->raw.boxes[i & 1], d, t, s.len);
@@ -780,27 +789,30 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             // steps before they are stored.  The page is looked at only then, so nothing waits for it
             // (a lookup in front of its loads took 2 - 3 thousand cycles a step).
             Seg f = s;
-            int ft = f.t0, fu = 0, page = 0, pos = 0;
-            bool fetch = true, in = false;
+            int ft = f.t0, fu = 0, page = 0;
+            int pos;  // of the row; -1: it holds no key, -2: there is no further step
+            bool fetch = true;
             auto look = [&]() {
-                in = false;
+                pos = -2;
                 if (!fetch) return;
                 pos = ft * kPtTok + off + kScrStep * fu + (d >> 3);
-                if (pos < f.len) {
-                    in = true;
+                if (pos < f.len)
                     page = __ldg(p.t.page_table + (int64_t)f.b * p.t.pt_ld + pos / p.t.ps);
-                }
+                else
+                    pos = -1;
                 if (++fu == kSteps) {
                     fu = 0;
                     if (++ft >= f.t1) {
-                        fetch = f.next(p);
+                        fetch = f.next(p, sm->share);
                         ft = f.t0;
                     }
                 }
             };
+            int left = 0;  // steps loaded and not yet stored
             auto load = [&](ScrRows &x) {
                 int slot = -1;
-                if (in) {
+                if (pos != -2) ++left;
+                if (pos >= 0) {
                     if (page >= 0 && page < p.t.num_pages)
                         slot = page * p.t.ps + pos % p.t.ps;
                     else
@@ -810,23 +822,19 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 look();
             };
             look();
-            int64_t left = (sm->share.g1 - sm->share.g0) * kSteps;
-            uint32_t sph = 0;
-            int ss = 0, u = 0;
+            uint32_t n = 0;  // steps stored
             bool ok = true;
             auto step = [&](ScrRows &x) {
-                if (u == 0 && !mbar_wait(&sm->scr_free[ss], sph ^ 1, kPtWait)) ok = false;
+                const uint32_t tile = n / kSteps, u = n % kSteps, ss = tile % kScrSlots;
+                if (u == 0 && !mbar_wait(&sm->scr_free[ss], (tile / kScrSlots & 1) ^ 1, kPtWait)) ok = false;
                 x.store(scr + (ss * kScrRows + kScrStep * u) * kScrRow, d);
-                if (++u == kSteps) {
-                    u = 0;
+                --left;
+                ++n;
+                if (u == kSteps - 1) {
                     asm volatile("fence.proxy.async.global;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm->scr_full[ss]);
-                    if (d == 0) sm->scr_tiles = sm->scr_tiles + 1;
-                    if (++ss == kScrSlots) {
-                        ss = 0;
-                        sph ^= 1;
-                    }
+                    if (d == 0) sm->scr_tiles = tile + 1;
                 }
                 load(x);
                 ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
@@ -836,10 +844,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             load(x1);
             while (left > 0 && ok) {
                 step(x0);
-                if (--left > 0 && ok) {
-                    step(x1);
-                    --left;
-                }
+                if (left > 0 && ok) step(x1);
             }
             if (!ok && lane == 0) fail();
         }
@@ -1062,6 +1067,8 @@ nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse,
     if (sms <= 0) return NSA_ERR_CUDA;
     const bool fp8 = a.kv_dtype == NSA_DT_E4M3;
     const Plan q = make_plan(fp8, a.R, a.rows_per_req, a.H, a.max_row_len, sms);
+    if ((int64_t)(a.R / a.rows_per_req) * q.mult * (ceil_div(a.max_row_len, kPtTok) + piece_of(q.rows)) / q.teams >= kMaxShare)
+        return NSA_ERR_UNSUPPORTED;
     AParams p;
     p.t = paged_tc_params(a);
     while (p.t.box_rows > kPtTok / q.cluster) p.t.box_rows /= 2;  // whole boxes for each CTA of a cluster

@@ -55,13 +55,18 @@ __device__ __forceinline__ void report_lengths(const PagedTc &p, int thread, int
     }
 }
 
-// Where a share of the launch's tiles starts.  The tiles of all requests (each
-// counted `mult` times) in request order are cut into up to `parts` equal shares;
-// share `part` is [g0, g1) and its first tile is tile `off` of request `b`.
+// Where a share of the launch's work starts.  The tiles of all requests (each counted
+// `mult` times, once for every unit of columns) lie in request order; in front of the tiles
+// of a unit `piece` places are left for what starting and ending a unit costs a CTA.  These
+// places are cut into up to `parts` equal shares; share `part` is [g0, g1) and begins at
+// place `off` of request `b`.
 struct TileShare {
     int64_t warp[32];
-    int64_t total, g0, g1, off;
-    int b;
+    int32_t units[32];
+    unsigned long long later;    // of the requests that are not scanned at once
+    int32_t later_units;
+    int64_t total, g0, g1, off;  // total: places
+    int b, piece, np;            // np: shares
 };
 
 __device__ __forceinline__ int64_t share_count(int64_t total, int parts)
@@ -77,53 +82,114 @@ __device__ __forceinline__ int64_t share_start(int64_t total, int64_t k, int64_t
     return x < 0x100000000ULL ? (int64_t)((uint32_t)x / (uint32_t)np) : (int64_t)(x / (uint64_t)np);
 }
 
-__device__ __forceinline__ void find_share(const PagedTc &p, int mult, int part, int parts, TileShare *sh)
+__device__ __forceinline__ void find_share(const PagedTc &p, int mult, int max_piece, int part, int parts, TileShare *sh)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-    int64_t sum = 0;
-    for (int b = tid; b < p.B; b += blockDim.x) sum += (int64_t)tiles_of(request_len(p, b)) * mult;
+    const int n0 = blockDim.x;  // the first n0 requests are scanned, one a thread; more are rare
+    auto tiles = [&](int b) -> int64_t { return b < p.B ? (int64_t)tiles_of(request_len(p, b)) * mult : 0; };
+    const int64_t v = tiles(tid);
+    const int c = v > 0 ? mult : 0;
+    int64_t v_inc = v;
+    int c_inc = c;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) sh->warp[warp] = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v_inc, o);
+        const int y = __shfl_up_sync(0xffffffffu, c_inc, o);
+        if (lane >= o) {
+            v_inc += x;
+            c_inc += y;
+        }
+    }
+    if (lane == 31) {
+        sh->warp[warp] = v_inc;
+        sh->units[warp] = c_inc;
+    }
+    if (p.B > n0) {
+        if (tid == 0) {
+            sh->later = 0;
+            sh->later_units = 0;
+        }
+        __syncthreads();
+        int64_t sum = 0;
+        int units = 0;
+        for (int b = n0 + tid; b < p.B; b += n0) {
+            const int64_t x = tiles(b);
+            sum += x;
+            units += x > 0 ? mult : 0;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            units += __shfl_xor_sync(0xffffffffu, units, o);
+        }
+        if (lane == 0) {
+            atomicAdd(&sh->later, (unsigned long long)sum);
+            atomicAdd(&sh->later_units, units);
+        }
+    }
+    if (tid == 0) {
+        sh->b = p.B;
+        sh->off = 0;
+    }
     __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < nw; ++w) total += sh->warp[w];
-    // no more shares than tiles, so that every share that has a neighbour has a tile
+    int64_t total = 0, units = 0, lo = 0, lo_units = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w == warp) {
+            lo = total;
+            lo_units = units;
+        }
+        total += sh->warp[w];
+        units += sh->units[w];
+    }
+    const int64_t first = total, first_units = units;
+    if (p.B > n0) {
+        total += (int64_t)sh->later;
+        units += sh->later_units;
+    }
+    // no more shares than tiles, and four times as many tiles as places of a piece in a share:
+    // every share has a tile
     const int64_t np = share_count(total, parts);
+    const int piece = (int)min((int64_t)max_piece, share_start(total, 1, 4 * np));
+    total += piece * units;
     const int64_t g0 = part < np ? share_start(total, part, np) : total;
     const int64_t g1 = part < np ? share_start(total, part + 1, np) : total;
     if (tid == 0) {
         sh->total = total;
+        sh->np = (int)np;
+        sh->piece = piece;
         sh->g0 = g0;
         sh->g1 = g1;
-        sh->b = p.B;
-        sh->off = 0;
     }
-    int64_t before = 0;  // tiles of the requests below `base`
-    for (int base = 0; base < p.B && g0 < g1; base += blockDim.x) {
+    lo += v_inc - v + piece * (lo_units + c_inc - c);
+    const int64_t places = v + (int64_t)piece * c;
+    if (g0 < g1 && places > 0 && g0 >= lo && g0 < lo + places) {
+        sh->b = tid;
+        sh->off = g0 - lo;
+    }
+    int64_t before = first + piece * first_units;  // places of the requests below `base`
+    for (int base = n0; base < p.B && g0 < g1 && before <= g0; base += n0) {
         __syncthreads();  // warp[] is free
         const int b = base + tid;
-        const int64_t v = b < p.B ? (int64_t)tiles_of(request_len(p, b)) * mult : 0;
-        int64_t inc = v;
+        const int64_t t = tiles(b), x = t > 0 ? t + (int64_t)piece * mult : 0;
+        int64_t inc = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += x;
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
         }
         if (lane == 31) sh->warp[warp] = inc;
         __syncthreads();
-        int64_t lo = before, all = 0;
+        int64_t at = before, all = 0;
         for (int w = 0; w < nw; ++w) {
-            if (w < warp) lo += sh->warp[w];
+            if (w < warp) at += sh->warp[w];
             all += sh->warp[w];
         }
-        lo += inc - v;
-        if (v > 0 && g0 >= lo && g0 < lo + v) {
+        at += inc - x;
+        if (x > 0 && g0 >= at && g0 < at + x) {
             sh->b = b;
-            sh->off = g0 - lo;
+            sh->off = g0 - at;
         }
         before += all;
-        if (before > g0) break;  // uniform
     }
     __syncthreads();
 }
@@ -249,7 +315,7 @@ __device__ __forceinline__ uint32_t live_rows(const PagedTc &p, uint32_t boxes, 
 // row is loaded while the one before it is expanded.
 constexpr int kScrThreads = 128;
 constexpr int kScrStep = kScrThreads / 8;       // rows at a time
-constexpr int kScrSlots = 3;                    // parts of tiles a CTA's scratch holds
+constexpr int kScrSlots = 4;                    // parts of tiles a CTA's scratch holds
 constexpr int kScrRow = 2 * (kPtDl + kPtDr);    // bytes
 
 struct ScrRows {
