@@ -78,7 +78,7 @@ struct Walk {
         if (left <= 0) return false;
         b = s.b;
         piece = s.piece;
-        len = request_len(p.t, b);
+        len = s.len;
         tiles = tiles_of(len);
         return enter(p, (int)s.off);
     }

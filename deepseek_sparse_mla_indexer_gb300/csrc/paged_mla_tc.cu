@@ -106,7 +106,7 @@ struct Seg {
         left = (int)(s.g1 - s.g0);
         if (left <= 0) return false;
         b = s.b;
-        len = request_len(p.t, b);
+        len = s.len;
         const int places = tiles_of(len) + s.piece;
         j = s.off < 0x100000000LL ? (int)((uint32_t)s.off / (uint32_t)places) : (int)(s.off / places);
         return enter((int)(s.off - (int64_t)j * places), s.piece);
@@ -149,6 +149,25 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w)
     if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
     if ((w & 0x00007f80u) == 0x00007f80u) w &= 0xffff0000u;
     return w;
+}
+
+// A column's values of all lanes joined, by halving exchanges: lane x gets that of column x % G.
+template <int G, class Join>
+__device__ __forceinline__ float over_lanes(float (&v)[G], int lane, Join join)
+{
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int c = 0; c < o; ++c) {
+            const float give = up ? v[c] : v[c + o];
+            const float got = __shfl_xor_sync(0xffffffffu, give, o);
+            v[c] = join(up ? v[c + o] : v[c], got);
+        }
+    }
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1) v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    return v[0];
 }
 
 // G columns of the accumulator at `taddr` from or into TMEM, one lane a thread.
@@ -597,13 +616,12 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         {
                             uint32_t sa[kGrp];
                             tmem_ldg<kGrp>(lanes + kColS + cb, sa);
+                            float v[kGrp];
 #pragma unroll
-                            for (int c = 0; c < kGrp; ++c) {
-                                float v = valid && pos < sm->len[cb + c] ? __uint_as_float(sa[c]) * p.t.scale_log2 : -INFINITY;
-#pragma unroll
-                                for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                                if (lane == 0) sm->red[quad][cb + c] = v;
-                            }
+                            for (int c = 0; c < kGrp; ++c)
+                                v[c] = valid && pos < sm->len[cb + c] ? __uint_as_float(sa[c]) * p.t.scale_log2 : -INFINITY;
+                            const float top = over_lanes(v, lane, [](float x, float y) { return fmaxf(x, y); });
+                            if (lane < kGrp) sm->red[quad][cb + lane] = top;
                         }
                         bar_sync(bar, 128);
                         if (et < kGrp) {
@@ -676,26 +694,14 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 }
                 if (!ok) break;
                 // ---------------------------------------------------- the piece's sums and accumulators
-                // column sums over the lanes, by halving exchanges: lane x ends with column x % kGrp
                 float ls[kGrp];
 #pragma unroll
                 for (int c = 0; c < kGrp / 2; ++c) {
                     ls[2 * c] = l[c].x;
                     ls[2 * c + 1] = l[c].y;
                 }
-#pragma unroll
-                for (int o = kGrp / 2; o > 0; o >>= 1) {
-                    const bool up = (lane & o) != 0;
-#pragma unroll
-                    for (int c = 0; c < o; ++c) {
-                        const float give = up ? ls[c] : ls[c + o];
-                        const float got = __shfl_xor_sync(0xffffffffu, give, o);
-                        ls[c] = (up ? ls[c + o] : ls[c]) + got;
-                    }
-                }
-#pragma unroll
-                for (int o = kGrp; o < 32; o <<= 1) ls[0] += __shfl_xor_sync(0xffffffffu, ls[0], o);
-                if (lane < kGrp) sm->red[quad][cb + lane] = ls[0];
+                const float part = over_lanes(ls, lane, [](float x, float y) { return x + y; });
+                if (lane < kGrp) sm->red[quad][cb + lane] = part;
                 bar_sync(bar, 128);
                 const bool whole = s.whole();
                 const int nc = min(kGrp, p.cols - col0 - cb);  // real columns of this group (may be <= 0)

@@ -66,7 +66,7 @@ struct TileShare {
     unsigned long long later;    // of the requests that are not scanned at once
     int32_t later_units;
     int64_t total, g0, g1, off;  // total: places
-    int b, piece, np;            // np: shares
+    int b, len, piece, np;       // len: of request b; np: shares
 };
 
 __device__ __forceinline__ int64_t share_count(int64_t total, int parts)
@@ -86,8 +86,9 @@ __device__ __forceinline__ void find_share(const PagedTc &p, int mult, int max_p
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
     const int n0 = blockDim.x;  // the first n0 requests are scanned, one a thread; more are rare
-    auto tiles = [&](int b) -> int64_t { return b < p.B ? (int64_t)tiles_of(request_len(p, b)) * mult : 0; };
-    const int64_t v = tiles(tid);
+    auto len_of = [&](int b) { return b < p.B ? request_len(p, b) : 0; };
+    const int len = len_of(tid);
+    const int64_t v = (int64_t)tiles_of(len) * mult;
     const int c = v > 0 ? mult : 0;
     int64_t v_inc = v;
     int c_inc = c;
@@ -113,7 +114,7 @@ __device__ __forceinline__ void find_share(const PagedTc &p, int mult, int max_p
         int64_t sum = 0;
         int units = 0;
         for (int b = n0 + tid; b < p.B; b += n0) {
-            const int64_t x = tiles(b);
+            const int64_t x = (int64_t)tiles_of(len_of(b)) * mult;
             sum += x;
             units += x > 0 ? mult : 0;
         }
@@ -164,13 +165,15 @@ __device__ __forceinline__ void find_share(const PagedTc &p, int mult, int max_p
     const int64_t places = v + (int64_t)piece * c;
     if (g0 < g1 && places > 0 && g0 >= lo && g0 < lo + places) {
         sh->b = tid;
+        sh->len = len;
         sh->off = g0 - lo;
     }
     int64_t before = first + piece * first_units;  // places of the requests below `base`
     for (int base = n0; base < p.B && g0 < g1 && before <= g0; base += n0) {
         __syncthreads();  // warp[] is free
         const int b = base + tid;
-        const int64_t t = tiles(b), x = t > 0 ? t + (int64_t)piece * mult : 0;
+        const int l = len_of(b);
+        const int64_t x = l > 0 ? (int64_t)(tiles_of(l) + piece) * mult : 0;
         int64_t inc = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -187,6 +190,7 @@ __device__ __forceinline__ void find_share(const PagedTc &p, int mult, int max_p
         at += inc - x;
         if (x > 0 && g0 >= at && g0 < at + x) {
             sh->b = b;
+            sh->len = l;
             sh->off = g0 - at;
         }
         before += all;
