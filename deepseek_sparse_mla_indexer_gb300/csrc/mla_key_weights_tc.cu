@@ -121,13 +121,16 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                       const __grid_constant__ CUtensorMap rope_map)
 {
     constexpr uint32_t kAccCols = SPLIT ? kSplitCols : kCols;
+    constexpr bool HALF = FP8 && !SPLIT;  // Q leaves little shared memory: steps of 64 codes
+    constexpr int kSteps = HALF ? 8 : 4, kStepCodes = kPtDl / kSteps;
+    constexpr uint32_t kSlot = HALF ? kRawHalf : kRawSlot;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *q_s = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t q_blk = (uint32_t)p.N * 128;
     uint8_t *ring = q_s + 9 * q_blk;
     uint8_t *rope_s = ring + (size_t)p.stages * kPtBlk;    // fp8: the rope part, raw codes, the scales of two tiles
     uint8_t *raw_s = rope_s + (FP8 ? kPtBlk : 0);
-    uint8_t *sc_s = raw_s + (FP8 ? p.raw * kRawSlot : 0);
+    uint8_t *sc_s = raw_s + (FP8 ? p.raw * kSlot : 0);
     WShared *sm = (WShared *)(sc_s + (FP8 ? 2 * kScaleSlot : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nst = p.stages;
@@ -218,18 +221,19 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                         }
                     };
                     if constexpr (FP8) {
-                        for (int m = 0; m < 4; ++m) {
+                        for (int m = 0; m < kSteps; ++m) {
                             if (!mbar_wait(&sm->raw.empty[rs], rph ^ 1, kPtWait)) ok = false;
                             if (elect_one()) {
                                 if (m == 0) {
                                     sm->raw.boxes[tile & 1] = live;
                                     mbar_arrive_expect_tx(&sm->raw.tile_full[tile & 1], bytes / 8);
                                 }
-                                mbar_arrive_expect_tx(&sm->raw.full[rs], bytes);
+                                mbar_arrive_expect_tx(&sm->raw.full[rs], bytes * kStepCodes / 128);
                             }
                             __syncwarp();
                             boxes_of([&](int x, int yb) {
-                                tma_load_2d(raw_s + rs * kRawSlot + x * box_bytes, &kv_map, 128 * m, yb, &sm->raw.full[rs]);
+                                tma_load_2d(raw_s + rs * kSlot + x * (box_bytes * kStepCodes / 128), &kv_map, kStepCodes * m, yb,
+                                            &sm->raw.full[rs]);
                                 if (m == 0)
                                     tma_load_2d(sc_s + (tile & 1) * kScaleSlot + x * (box_bytes / 8), &sc_map, kPtDl, yb,
                                                 &sm->raw.tile_full[tile & 1]);
@@ -469,33 +473,61 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
             for (bool more = true; more && ok; more = w.next(p)) {
                 for (int t = w.c0; t < w.c1 && ok; ++t, ++tile) {
                     if (!mbar_wait(&sm->raw.tile_full[tile & 1], (tile >> 1) & 1, kPtWait)) ok = false;
-                    const uint32_t live = live_rows(p.t, sm->raw.boxes[tile & 1], d, t, w.len);
+                    const uint32_t boxes = sm->raw.boxes[tile & 1];
                     float *scales = reinterpret_cast<float *>(sc_s + (tile & 1) * kScaleSlot);
+                    if constexpr (HALF) {
+                        const int r = d >> 2;
+                        const bool live = t * kPtTok + r < w.len && (boxes >> (r / p.t.box_rows) & 1);
 #pragma unroll 1
-                    for (int m = 0; m < 4; ++m) {
-                        const int s0 = st, s1 = st + 1 == nst ? 0 : st + 1;
-                        const uint32_t ph0 = ph, ph1 = st + 1 == nst ? ph ^ 1 : ph;
-                        st += 2;
-                        if (st >= nst) {
-                            st -= nst;
-                            ph ^= 1;
+                        for (int m = 0; m < kSteps; ++m) {
+                            if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;
+                            RawHalfStep x;
+                            x.read(raw_s + rs * kSlot, scales, m, d, live);
+                            if (!mbar_wait(&sm->empty[st], ph ^ 1, kPtWait)) ok = false;
+                            x.store(d, ring + st * kPtBlk);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(&sm->raw.empty[rs]);
+                                mbar_arrive(&sm->full[st]);
+                            }
+                            if (++st == nst) {
+                                st = 0;
+                                ph ^= 1;
+                            }
+                            if (++rs == p.raw) {
+                                rs = 0;
+                                rph ^= 1;
+                            }
                         }
-                        if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;
-                        RawStep x;
-                        x.read(raw_s + rs * kRawSlot, scales, m, d, live);
-                        if (!mbar_wait(&sm->empty[s0], ph0 ^ 1, kPtWait)) ok = false;
-                        if (!mbar_wait(&sm->empty[s1], ph1 ^ 1, kPtWait)) ok = false;
-                        x.store(d, ring + s0 * kPtBlk, ring + s1 * kPtBlk);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&sm->raw.empty[rs]);
-                            mbar_arrive(&sm->full[s0]);
-                            mbar_arrive(&sm->full[s1]);
-                        }
-                        if (++rs == p.raw) {
-                            rs = 0;
-                            rph ^= 1;
+                    } else {
+                        const uint32_t live = live_rows(p.t, boxes, d, t, w.len);
+#pragma unroll 1
+                        for (int m = 0; m < 4; ++m) {
+                            const int s0 = st, s1 = st + 1 == nst ? 0 : st + 1;
+                            const uint32_t ph0 = ph, ph1 = st + 1 == nst ? ph ^ 1 : ph;
+                            st += 2;
+                            if (st >= nst) {
+                                st -= nst;
+                                ph ^= 1;
+                            }
+                            if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;
+                            RawStep x;
+                            x.read(raw_s + rs * kRawSlot, scales, m, d, live);
+                            if (!mbar_wait(&sm->empty[s0], ph0 ^ 1, kPtWait)) ok = false;
+                            if (!mbar_wait(&sm->empty[s1], ph1 ^ 1, kPtWait)) ok = false;
+                            x.store(d, ring + s0 * kPtBlk, ring + s1 * kPtBlk);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(&sm->raw.empty[rs]);
+                                mbar_arrive(&sm->full[s0]);
+                                mbar_arrive(&sm->full[s1]);
+                            }
+                            if (++rs == p.raw) {
+                                rs = 0;
+                                rph ^= 1;
+                            }
                         }
                     }
                     ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
@@ -543,20 +575,22 @@ nsa_status key_weights_tc_try_launch(const PagedMlaArgs &a, const float *lse, fl
     p.passes = (int)ceil_div(p.cols, kCols);
     p.N = p.passes > 1 ? kCols : (int)ceil_div(p.cols, 16) * 16;
     const size_t q_bytes = (size_t)9 * p.N * 128, left = 232448 - 1024 - kAux - q_bytes;
-    // fp8: a stage for the rope part, about two raw slots to three stages (a step fills two) of the rest
-    const int blocks = (int)((left - (fp8 ? 2 * kScaleSlot + kPtBlk : 0)) / kPtBlk);
-    p.raw = fp8 ? (blocks >= 8 ? 4 : blocks >= 6 ? 3 : blocks >= 4 ? 2 : 1) : 0;
-    p.stages = blocks - p.raw < kMaxStages ? blocks - p.raw : kMaxStages;
-    const size_t smem =
-        1024 + q_bytes + (size_t)(p.stages + p.raw + (fp8 ? 1 : 0)) * kPtBlk + (fp8 ? 2 * kScaleSlot : 0) + kAux;
+    // fp8: a stage for the rope part; of the rest about two raw slots to three stages (a step fills two),
+    // or with steps of 64 codes (half a slot, one stage) three or four raw slots
+    const bool split = p.N <= kSplitCols, half = fp8 && !split;
+    const size_t fixed = fp8 ? 2 * kScaleSlot + kPtBlk : 0, slot = half ? kRawHalf : kRawSlot;
+    const int blocks = (int)((left - fixed) / slot);
+    p.raw = !fp8 ? 0 : half ? (blocks >= 8 ? 4 : 3) : blocks >= 8 ? 4 : blocks >= 6 ? 3 : 2;
+    p.stages = (int)((left - fixed - p.raw * slot) / kPtBlk);
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    const size_t smem = 1024 + q_bytes + fixed + p.raw * slot + (size_t)p.stages * kPtBlk + kAux;
     CUtensorMap qn, qr, kv, sc = {}, rope = {};
     if (!paged_tc_q_maps(a, (uint32_t)p.N, &qn, &qr)) return NSA_ERR_CUDA;
-    if (fp8 ? !fp8_maps(a, (uint32_t)p.t.box_rows, &kv, &sc, &rope)
+    if (fp8 ? !fp8_maps(a, (uint32_t)p.t.box_rows, half ? 64 : 128, &kv, &sc, &rope)
             : !bf16_rows_map(a.kv, (uint64_t)a.num_pages * a.page_size, (uint32_t)p.t.box_rows, &kv))
         return NSA_ERR_CUDA;
     const int64_t tiles = (int64_t)p.t.B * ceil_div(a.max_row_len, kPtTok);
     const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
-    const bool split = p.N <= kSplitCols;
     if (fp8) return split ? launch<true, true>(p, qn, qr, kv, sc, rope, grid, smem, stream)
                           : launch<true, false>(p, qn, qr, kv, sc, rope, grid, smem, stream);
     return split ? launch<false, true>(p, qn, qr, kv, sc, rope, grid, smem, stream)

@@ -1092,7 +1092,7 @@ nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse,
     const bool mapped =
         q.rows == kBf16Rows ? bf16_rows_map(a.kv, (uint64_t)a.num_pages * a.page_size, (uint32_t)p.t.box_rows, &m.kv)
         : q.rows == kRawRows
-            ? fp8_maps(a, (uint32_t)p.t.box_rows, &m.kv, &m.sc, &m.rope)
+            ? fp8_maps(a, (uint32_t)p.t.box_rows, 128, &m.kv, &m.sc, &m.rope)
             : bf16_rows_map(p.scratch, (uint64_t)q.teams * q.team * kScrSlots * (kPtTok / q.cluster),
                             (uint32_t)(kPtTok / q.cluster), &m.kv);
     if (!mapped) return NSA_ERR_CUDA;

@@ -301,6 +301,35 @@ struct RawStep {
 };
 static_assert((kPtTok / kDqRows) % 8 == 0, "a thread's rows share their swizzle");
 
+// The same for a step of 64 codes (slots of 128 x 64 bytes, one block a step), where shared
+// memory is short: thread d expands chunk d % 4 of row d / 4.  Eight neighbouring lanes read
+// 128 bytes in a row and store to eight distinct bank groups.
+constexpr uint32_t kRawHalf = kPtTok * 64;
+
+struct RawHalfStep {
+    uint4 w;
+    float sc;
+
+    __device__ __forceinline__ void read(uint8_t *raw, float *scales, int m, int d, bool live)
+    {
+        uint4 *at = reinterpret_cast<uint4 *>(raw + 16 * d);
+        float *sp = scales + 4 * (d >> 2) + (m >> 1);
+        if (!live) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+            *sp = 0.f;
+        }
+        w = *at;
+        sc = *sp;
+    }
+    __device__ __forceinline__ void store(int d, uint8_t *blk) const
+    {
+        const int r = d >> 2, c = 2 * (d & 3);
+        *reinterpret_cast<uint4 *>(blk + sm100::sw128_offset(r, c)) = expand8(w.x, w.y, sc);
+        *reinterpret_cast<uint4 *>(blk + sm100::sw128_offset(r, c + 1)) = expand8(w.z, w.w, sc);
+    }
+};
+static_assert(kDqThreads == 4 * kPtTok, "a thread a chunk");
+
 // Which of thread d's rows of a tile hold a key (bit u: row d / 8 + 64 u).
 __device__ __forceinline__ uint32_t live_rows(const PagedTc &p, uint32_t boxes, int d, int tile, int len)
 {
@@ -418,13 +447,14 @@ inline bool bf16_rows_map(const void *base, uint64_t rows, uint32_t box_rows, CU
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Maps of an fp8 cache: codes in boxes of 128 bytes, scales in boxes of 16 bytes (the row
+// Maps of an fp8 cache: codes in boxes of box_codes bytes, scales in boxes of 16 bytes (the row
 // seen as bytes) and the rope part in boxes of 64 bf16 (the row seen as 328 bf16; x = 264
 // is byte 528, a multiple of 16).
-inline bool fp8_maps(const PagedMlaArgs &a, uint32_t box_rows, CUtensorMap *codes, CUtensorMap *scales, CUtensorMap *rope)
+inline bool fp8_maps(const PagedMlaArgs &a, uint32_t box_rows, uint32_t box_codes, CUtensorMap *codes, CUtensorMap *scales,
+                     CUtensorMap *rope)
 {
     const uint64_t rows = (uint64_t)a.num_pages * a.page_size;
-    return make_tma_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv, kPtFp8Row, rows, kPtFp8Row, 128, box_rows,
+    return make_tma_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv, kPtFp8Row, rows, kPtFp8Row, box_codes, box_rows,
                        CU_TENSOR_MAP_SWIZZLE_NONE) &&
            make_tma_2d(scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv, kPtFp8Row, rows, kPtFp8Row, 16, box_rows,
                        CU_TENSOR_MAP_SWIZZLE_NONE) &&
