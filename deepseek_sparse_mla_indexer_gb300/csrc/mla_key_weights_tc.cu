@@ -122,8 +122,9 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
 {
     constexpr uint32_t kAccCols = SPLIT ? kSplitCols : kCols;
     constexpr bool HALF = FP8 && !SPLIT;  // Q leaves little shared memory: steps of 64 codes
-    constexpr int kSteps = HALF ? 8 : 4, kStepCodes = kPtDl / kSteps;
-    constexpr uint32_t kSlot = HALF ? kRawHalf : kRawSlot;
+    constexpr int kSteps = 8, kStepCodes = kPtDl / kSteps;  // of HALF
+    constexpr bool WIDE = FP8 && SPLIT;   // else slots of half rows
+    constexpr uint32_t kSlot = HALF ? kRawHalf : kHalfRowSlot;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *q_s = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t q_blk = (uint32_t)p.N * 128;
@@ -131,7 +132,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
     uint8_t *rope_s = ring + (size_t)p.stages * kPtBlk;    // fp8: the rope part, raw codes, the scales of two tiles
     uint8_t *raw_s = rope_s + (FP8 ? kPtBlk : 0);
     uint8_t *sc_s = raw_s + (FP8 ? p.raw * kSlot : 0);
-    WShared *sm = (WShared *)(sc_s + (FP8 ? 2 * kScaleSlot : 0));
+    WShared *sm = (WShared *)(sc_s + (HALF ? 2 * kScaleSlot : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nst = p.stages;
 
@@ -220,7 +221,26 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                             __syncwarp();
                         }
                     };
-                    if constexpr (FP8) {
+                    if constexpr (WIDE) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!mbar_wait(&sm->raw.empty[rs], rph ^ 1, kPtWait)) ok = false;
+                            constexpr uint32_t kRow[2] = {kUpperRow, kLowerRow};
+                            if (elect_one()) {
+                                if (h == 0) sm->raw.boxes[tile & 1] = live;
+                                mbar_arrive_expect_tx(&sm->raw.full[rs], bytes / 128 * kRow[h]);
+                            }
+                            __syncwarp();
+                            boxes_of([&](int x, int yb) {
+                                tma_load_2d(raw_s + rs * kSlot + x * p.t.box_rows * kRow[h], h == 0 ? &sc_map : &kv_map,
+                                            h == 0 ? kUpperX : 0, yb, &sm->raw.full[rs]);
+                            });
+                            if (++rs == p.raw) {
+                                rs = 0;
+                                rph ^= 1;
+                            }
+                        }
+                    } else if constexpr (HALF) {
                         for (int m = 0; m < kSteps; ++m) {
                             if (!mbar_wait(&sm->raw.empty[rs], rph ^ 1, kPtWait)) ok = false;
                             if (elect_one()) {
@@ -243,13 +263,6 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                                 rph ^= 1;
                             }
                         }
-                        // the rope part straight into its stage
-                        if (!mbar_wait(&sm->rope_empty, (tile & 1) ^ 1, kPtWait)) ok = false;
-                        if (elect_one()) mbar_arrive_expect_tx(&sm->rope_full, bytes);
-                        __syncwarp();
-                        boxes_of([&](int x, int yb) {
-                            tma_load_2d(rope_s + x * box_bytes, &rope_map, kFp8RopeX, yb, &sm->rope_full);
-                        });
                     } else {
                         for (int c = 0; c < 9; ++c) {
                             if (!mbar_wait(&sm->empty[st], ph ^ 1, kPtWait)) ok = false;
@@ -263,6 +276,15 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                                 ph ^= 1;
                             }
                         }
+                    }
+                    if constexpr (FP8) {
+                        // the rope part straight into its stage
+                        if (!mbar_wait(&sm->rope_empty, (tile & 1) ^ 1, kPtWait)) ok = false;
+                        if (elect_one()) mbar_arrive_expect_tx(&sm->rope_full, bytes);
+                        __syncwarp();
+                        boxes_of([&](int x, int yb) {
+                            tma_load_2d(rope_s + x * box_bytes, &rope_map, kFp8RopeX, yb, &sm->rope_full);
+                        });
                     }
                     y = y_next;
                     ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
@@ -278,7 +300,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                 } else {
                     for (int i = 0; i < nst; ++i) mbar_wait(&sm->full[i], i < st ? ph : ph ^ 1, kPtWait);
                 }
-                if (FP8)
+                if (HALF)
                     for (uint32_t x = tile > 2 ? tile - 2 : 0; x < tile; ++x)
                         mbar_wait(&sm->raw.tile_full[x & 1], (x >> 1) & 1, kPtWait);
                 mbar_wait(&sm->q_full, (uses - 1) & 1, kPtWait);
@@ -304,6 +326,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                     if (!mbar_wait(&sm->s_empty[buf], bph ^ 1, kPtWait)) ok = false;
                     for (int c = 0; c < 9; ++c) {
                         const bool rope = FP8 && c == 8;
+                        const int qb = WIDE && !rope ? (c + 4) & 7 : c;  // the upper half of the row comes first
                         const int acc = SPLIT ? min(c >> 1, 3) : c >> 2 ? 1 : 0;
                         const bool first = SPLIT ? c < 8 && (c & 1) == 0 : c < 8 && (c & 3) == 0;
                         if (!mbar_wait(rope ? &sm->rope_full : &sm->full[st], rope ? tile & 1 : ph, kPtWait)) ok = false;
@@ -313,7 +336,7 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 mma_f16(tmem + buf * kBufCols + acc * kAccCols, a_desc + k * 2,
-                                        q_desc + (c * q_blk + k * 32) / 16, idesc, k > 0 || !first);
+                                        q_desc + (qb * q_blk + k * 32) / 16, idesc, k > 0 || !first);
                             mma_commit(rope ? &sm->rope_empty : &sm->empty[st]);
                             if (c == 8) mma_commit(&sm->s_full[buf]);
                         }
@@ -472,10 +495,10 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
             bool ok = true;
             for (bool more = true; more && ok; more = w.next(p)) {
                 for (int t = w.c0; t < w.c1 && ok; ++t, ++tile) {
-                    if (!mbar_wait(&sm->raw.tile_full[tile & 1], (tile >> 1) & 1, kPtWait)) ok = false;
-                    const uint32_t boxes = sm->raw.boxes[tile & 1];
-                    float *scales = reinterpret_cast<float *>(sc_s + (tile & 1) * kScaleSlot);
                     if constexpr (HALF) {
+                        if (!mbar_wait(&sm->raw.tile_full[tile & 1], (tile >> 1) & 1, kPtWait)) ok = false;
+                        float *scales = reinterpret_cast<float *>(sc_s + (tile & 1) * kScaleSlot);
+                        const uint32_t boxes = sm->raw.boxes[tile & 1];
                         const int r = d >> 2;
                         const bool live = t * kPtTok + r < w.len && (boxes >> (r / p.t.box_rows) & 1);
 #pragma unroll 1
@@ -501,28 +524,46 @@ key_weights_tc_kernel(WParams p, const __grid_constant__ CUtensorMap qn_map, con
                             }
                         }
                     } else {
-                        const uint32_t live = live_rows(p.t, boxes, d, t, w.len);
-#pragma unroll 1
-                        for (int m = 0; m < 4; ++m) {
-                            const int s0 = st, s1 = st + 1 == nst ? 0 : st + 1;
-                            const uint32_t ph0 = ph, ph1 = st + 1 == nst ? ph ^ 1 : ph;
-                            st += 2;
-                            if (st >= nst) {
-                                st -= nst;
-                                ph ^= 1;
-                            }
+                        uint32_t live = 0;
+                        float4 sc[kDqRows];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
                             if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;
-                            RawStep x;
-                            x.read(raw_s + rs * kRawSlot, scales, m, d, live);
-                            if (!mbar_wait(&sm->empty[s0], ph0 ^ 1, kPtWait)) ok = false;
-                            if (!mbar_wait(&sm->empty[s1], ph1 ^ 1, kPtWait)) ok = false;
-                            x.store(d, ring + s0 * kPtBlk, ring + s1 * kPtBlk);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) {
-                                mbar_arrive(&sm->raw.empty[rs]);
-                                mbar_arrive(&sm->full[s0]);
-                                mbar_arrive(&sm->full[s1]);
+                            uint8_t *slot = raw_s + rs * kSlot;
+                            if (h == 0) {
+                                live = live_rows(p.t, sm->raw.boxes[tile & 1], d, t, w.len);
+#pragma unroll
+                                for (int u = 0; u < kDqRows; ++u) {
+                                    const int r = (d >> 3) + u * (kPtTok / kDqRows);
+                                    sc[u] = *reinterpret_cast<const float4 *>(slot + r * kUpperRow + 256);
+                                    if (!(live >> u & 1)) sc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                }
+                            }
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                const int s0 = st, s1 = st + 1 == nst ? 0 : st + 1;
+                                const uint32_t ph0 = ph, ph1 = st + 1 == nst ? ph ^ 1 : ph;
+                                st += 2;
+                                if (st >= nst) {
+                                    st -= nst;
+                                    ph ^= 1;
+                                }
+                                float s[kDqRows];
+#pragma unroll
+                                for (int u = 0; u < kDqRows; ++u)
+                                    s[u] = h == 0 ? (m == 0 ? sc[u].z : sc[u].w) : (m == 0 ? sc[u].x : sc[u].y);
+                                RawStep x;
+                                x.read_wide(slot + 128 * m, h == 0 ? kUpperRow : kLowerRow, s, d, live);
+                                if (!mbar_wait(&sm->empty[s0], ph0 ^ 1, kPtWait)) ok = false;
+                                if (!mbar_wait(&sm->empty[s1], ph1 ^ 1, kPtWait)) ok = false;
+                                x.store(d, ring + s0 * kPtBlk, ring + s1 * kPtBlk);
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                                if (lane == 0) {
+                                    if (m == 1) mbar_arrive(&sm->raw.empty[rs]);
+                                    mbar_arrive(&sm->full[s0]);
+                                    mbar_arrive(&sm->full[s1]);
+                                }
                             }
                             if (++rs == p.raw) {
                                 rs = 0;
@@ -575,19 +616,20 @@ nsa_status key_weights_tc_try_launch(const PagedMlaArgs &a, const float *lse, fl
     p.passes = (int)ceil_div(p.cols, kCols);
     p.N = p.passes > 1 ? kCols : (int)ceil_div(p.cols, 16) * 16;
     const size_t q_bytes = (size_t)9 * p.N * 128, left = 232448 - 1024 - kAux - q_bytes;
-    // fp8: a stage for the rope part; of the rest about two raw slots to three stages (a step fills two),
-    // or with steps of 64 codes (half a slot, one stage) three or four raw slots
+    // fp8: a stage for the rope part; of the rest two or three slots of half rows (a step fills two stages),
+    // or with steps of 64 codes (one stage a step) three or four small ones
     const bool split = p.N <= kSplitCols, half = fp8 && !split;
-    const size_t fixed = fp8 ? 2 * kScaleSlot + kPtBlk : 0, slot = half ? kRawHalf : kRawSlot;
-    const int blocks = (int)((left - fixed) / slot);
-    p.raw = !fp8 ? 0 : half ? (blocks >= 8 ? 4 : 3) : blocks >= 8 ? 4 : blocks >= 6 ? 3 : 2;
-    p.stages = (int)((left - fixed - p.raw * slot) / kPtBlk);
+    const size_t fixed = fp8 ? kPtBlk + (half ? 2 * kScaleSlot : 0) : 0, slot = half ? kRawHalf : kHalfRowSlot;
+    const size_t rest = left - fixed;
+    p.raw = !fp8 ? 0 : half ? (rest >= 8 * slot ? 4 : 3) : rest >= 3 * slot + 5 * kPtBlk ? 3 : 2;
+    p.stages = (int)((rest - p.raw * slot) / kPtBlk);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     const size_t smem = 1024 + q_bytes + fixed + p.raw * slot + (size_t)p.stages * kPtBlk + kAux;
     CUtensorMap qn, qr, kv, sc = {}, rope = {};
     if (!paged_tc_q_maps(a, (uint32_t)p.N, &qn, &qr)) return NSA_ERR_CUDA;
-    if (fp8 ? !fp8_maps(a, (uint32_t)p.t.box_rows, half ? 64 : 128, &kv, &sc, &rope)
-            : !bf16_rows_map(a.kv, (uint64_t)a.num_pages * a.page_size, (uint32_t)p.t.box_rows, &kv))
+    if (half  ? !fp8_maps(a, (uint32_t)p.t.box_rows, 64, &kv, &sc, &rope)
+        : fp8 ? !fp8_half_maps(a, (uint32_t)p.t.box_rows, &kv, &sc, &rope)
+              : !bf16_rows_map(a.kv, (uint64_t)a.num_pages * a.page_size, (uint32_t)p.t.box_rows, &kv))
         return NSA_ERR_CUDA;
     const int64_t tiles = (int64_t)p.t.B * ceil_div(a.max_row_len, kPtTok);
     const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);

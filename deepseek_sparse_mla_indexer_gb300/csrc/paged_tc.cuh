@@ -286,6 +286,21 @@ struct RawStep {
             sc[u] = sp[u * kStep * 4];
         }
     }
+    // The same from rows of `pitch` bytes that hold more than the step's 128 codes (`raw` is the first
+    // of them), with the rows' scales at hand.
+    __device__ __forceinline__ void read_wide(uint8_t *raw, int pitch, const float (&scales)[kDqRows], int d, uint32_t live)
+    {
+        constexpr int kStep = kPtTok / kDqRows;
+        uint8_t *at = raw + (d >> 3) * pitch + 16 * (d & 7);
+        const int first = swap(d) ? 8 : 0;
+#pragma unroll
+        for (int u = 0; u < kDqRows; ++u) {
+            if (!(live >> u & 1)) *reinterpret_cast<uint4 *>(at + u * kStep * pitch) = make_uint4(0u, 0u, 0u, 0u);
+            w[u][0] = *reinterpret_cast<const uint2 *>(at + u * kStep * pitch + first);
+            w[u][1] = *reinterpret_cast<const uint2 *>(at + u * kStep * pitch + (first ^ 8));
+            sc[u] = scales[u];
+        }
+    }
     __device__ __forceinline__ void store(int d, uint8_t *blk0, uint8_t *blk1) const
     {
         const int k = d & 7, r = d >> 3, c0 = (2 * k) & 7, sw = swap(d) ? 1 : 0;
@@ -329,6 +344,12 @@ struct RawHalfStep {
     }
 };
 static_assert(kDqThreads == 4 * kPtTok, "a thread a chunk");
+
+// Half rows: bytes 256 .. 527 (the codes from 256 on and the scales) and bytes 0 .. 255 of a tile's
+// rows, a slot each.  TMA fetches a box row by row and a row line by line, and rows of 656 bytes lie
+// across lines, so the fewer and longer the boxes' rows the better.
+constexpr int kUpperRow = 256 + 16, kLowerRow = 256;
+constexpr uint32_t kHalfRowSlot = kPtTok * kUpperRow;
 
 // Which of thread d's rows of a tile hold a key (bit u: row d / 8 + 64 u).
 __device__ __forceinline__ uint32_t live_rows(const PagedTc &p, uint32_t boxes, int d, int tile, int len)
@@ -461,6 +482,19 @@ inline bool fp8_maps(const PagedMlaArgs &a, uint32_t box_rows, uint32_t box_code
            make_tma_2d(rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, kPtFp8Row / 2, rows, kPtFp8Row, 64, box_rows,
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
+
+// Maps of the half rows of an fp8 cache (the row seen as 164 words).
+inline bool fp8_half_maps(const PagedMlaArgs &a, uint32_t box_rows, CUtensorMap *lower, CUtensorMap *upper, CUtensorMap *rope)
+{
+    const uint64_t rows = (uint64_t)a.num_pages * a.page_size;
+    return make_tma_2d(lower, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.kv, kPtFp8Row / 4, rows, kPtFp8Row, kLowerRow / 4, box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_NONE) &&
+           make_tma_2d(upper, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.kv, kPtFp8Row / 4, rows, kPtFp8Row, kUpperRow / 4, box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_NONE) &&
+           make_tma_2d(rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, kPtFp8Row / 2, rows, kPtFp8Row, 64, box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+}
+constexpr int kUpperX = 256 / 4;  // word
 constexpr int kFp8RopeX = (kPtDl + 16) / 2;
 static_assert(kFp8RopeX * 2 % 16 == 0, "a TMA box starts on a 16-byte boundary");
 

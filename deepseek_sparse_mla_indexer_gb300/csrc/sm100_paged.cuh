@@ -8,6 +8,17 @@
 namespace nsa {
 namespace sm100 {
 
+// Whether the phase with the given parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+
 // The box into the same offset of every CTA of the cluster named by `mask`, each of whose
 // barriers at `bar`'s offset counts the bytes.
 __device__ __forceinline__ void tma_load_2d_multicast(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar,
