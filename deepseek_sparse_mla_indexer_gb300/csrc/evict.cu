@@ -29,7 +29,8 @@ using namespace sm100;
 // CTAs before it: positions above the threshold, and of those equal to it the
 // lowest ones.  Keys stay in shared memory (slices up to 40 K; longer ones are read
 // again from L2).  Whole numbers throughout: the result does not depend on
-// scheduling.  Bound by the latency of its dozen dependent steps, not by its bytes.
+// scheduling.  Bound by the latency of its dozen dependent steps, not by its bytes:
+// 31 us for 16 requests of 50000 .. 131072 totals (7.5 MB), 13 - 16 us for one of 4099.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMaxCluster = 8;         // the portable limit
@@ -306,6 +307,9 @@ int select_clusters(int nc)
 // positions, pages, rows).  Four warps walk it for the CTA's next chunk while the
 // other four move the current one, whose rows go through shared memory as bulk
 // copies (a thread issues one copy a row and array), and several CTAs share an SM.
+// Measured (GB300): 4 requests of 65536 .. 131072 positions cut to 50000, bf16 rows, indexer keys
+// and scales (518 MB moved): 105 us, 4.9 TB/s, 73 % of the copy rate; 32 requests of 4096 .. 32768
+// cut to 5001, fp8 rows (232 MB): 57 us, 60 %; one of 4099: 15 us.
 constexpr int kMaxArrays = 8;
 constexpr int kCpThreads = 256;          // warps 0..3 move a chunk, warps 4..7 describe the next one
 constexpr int kMovers = 128;

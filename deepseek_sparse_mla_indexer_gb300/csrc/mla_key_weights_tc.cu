@@ -17,7 +17,16 @@
 // Roles: warp 0 issues TMA loads of Q and (bf16) of the tiles' blocks into a ring of
 // 16 KB stages; warp 1 issues the MMAs into two TMEM buffers; warps 4..7 are the
 // epilogue; fp8 rows come raw into slots of their own, from which warps 8..23 expand
-// them into the ring.
+// them into the ring (half rows up to 64 columns, blocks of 64 codes beyond, where Q
+// leaves less room).
+//
+// Measured (GB300, a pass among others):
+//   32 requests x 128 heads, bf16, 4096 .. 32768     95 us: 5.6 TB/s, 84 % of the copy rate
+//   16 x 4 tokens x 16 heads, fp8, 16384 .. 65536   110 us: 3.5 TB/s
+//   32 x 128 heads, fp8, 4096 .. 32768              127 us
+//   2 x 16 heads, bf16, 700 and 2111                 13 us
+// fp8 is bound by the expansion (issue slots 61 %, its steps a chain of waits, reads, conversions
+// and a proxy fence): steps of 64 codes took 147 us where those of 128 take 110.
 #include <cstddef>
 
 #include "mla_key_weights_tc.cuh"

@@ -1,28 +1,43 @@
 // Tensor-core kernel of nsa_paged_mla for the 512 + 64 latent cache.
 //
-// A column is one (row, head) of a request; a CTA owns 64 columns.  Per tile of
-// 128 positions, as the sparse kernel does for its gathered rows:
-//   S^T[128 keys, 64 cols] = K_tile . Q^T                       (tcgen05, bf16)
+// A column is one (row, head) of a request; a CTA owns NC (16, 32 or 64) columns.  Per tile
+// of 128 positions, as the sparse kernel does for its gathered rows:
+//   S^T[128 keys, NC cols] = K_tile . Q^T                       (tcgen05, bf16)
 //   P^T = 2^(scale S^T - m), m a lazily refreshed running maximum per column
-//   O^T[512, 64 cols] += V^T . P^T, V the first eight blocks of the same tile
+//   O^T[512, NC cols] += V^T . P^T, V the first eight blocks of the same tile
 // with O^T and S^T in TMEM (256 + 64 columns).  The sums of the unrounded P stay in
 // fp32 registers (each thread its key's part) and are joined once at the end, so
 // lse is good to fp32; P itself is rounded to bf16 for the product with V, whose
 // operands must have one type (each weight off by at most 2^-8 of itself).
 //
-// Shared memory holds Q (72 KB) and one tile (144 KB), so tiles are pipelined by
-// block pairs: pair m is loaded again as soon as O^T's d-block m, its last reader,
+// Shared memory holds Q (72 KB of 64 columns) and one tile (144 KB), so tiles are pipelined
+// by block pairs: pair m is loaded again as soon as O^T's d-block m, its last reader,
 // is done, and S^T of the next tile starts on the pairs that have landed.  P^T lies
-// in the rope block, which S^T has finished with.  Two CTAs with neighbouring
-// columns of the same request run as a cluster: each loads half of every tile into
-// both (TMA multicast), which halves the traffic from L2; a pair is loaded again
-// when both are done with it.  fp8 rows are expanded into the tile by 512 threads
-// of each CTA from registers that hold the whole next tile.
+// in the rope block, which S^T has finished with.  CTAs with neighbouring columns of the
+// same request run as a cluster of two (fp8 of 256 columns and more: four): each loads its
+// part of every tile into all of them (TMA multicast), which divides the traffic from L2; a
+// pair is loaded again when all are done with it.
+//
+// fp8 rows become bf16 in the CTA.  Up to 32 columns, Q leaves room for slots of raw codes,
+// which TMA fills and 512 threads expand into the tile.  More columns leave none, and sharing
+// the expansion pays: 128 threads of each CTA of a cluster expand their part of the tile from
+// registers into a scratch in global memory that stays in L2, and TMA multicasts it from there
+// as it does bf16 rows.
 //
 // The tiles of all requests are cut into equal shares over the CTAs (teams of up to
 // eight CTAs take the same tiles for different columns, so that a tile is read from
 // HBM once).  A share that covers a request's columns only in part leaves raw sums,
 // maxima and fp32 accumulators in the workspace, which paged_mla_join_kernel joins.
+//
+// Measured (GB300, a pass among others, positions 4096 .. 32768 unless said):
+//   32 requests x 128 heads, bf16   157 us: 3.4 TB/s, 0.82 PF
+//   128 x 16 heads, fp8, 1024 ..    154 us: 3.1 TB/s
+//   8 x 4 tokens x 128 heads, fp8, 16384 .. 131072   697 us: 0.77 PF
+//   1 x 16 heads, bf16, 501         23 us
+// Bound by the chain of a tile: 5200 cycles (bf16, 64 columns), of which the products take 3640
+// (N = 64 is bound by the tensor core's reads of shared memory: 48 cycles a product, not 32),
+// the softmax 900 and the next tile's load behind its last reader the rest; fp8 adds the expansion
+// (6500 cycles of 16 columns).  17 thousand cycles pass before the first product.
 #include <cstddef>
 
 #include "paged_mla_tc.cuh"
@@ -41,7 +56,7 @@ constexpr float kRescale = 8.0f;          // log2 units
 constexpr int kMaxTeam = 8;
 // How the tile's rows come: a bf16 cache by TMA; raw fp8 rows by TMA into slots beside the
 // tile and expanded from there; or fp8 rows expanded into the CTA's scratch in global memory
-// (half a tile for each CTA of a pair) and loaded from it as bf16 rows are.
+// (each CTA of a cluster its part of the tile) and loaded from it as bf16 rows are.
 enum Rows { kBf16Rows, kRawRows, kScratchRows };
 // What a further request in a share costs, in tiles: its epilogue, the loads that find it and its
 // first tiles from HBM took 18 - 22 thousand cycles against 5.2 a tile (32 requests of 128 heads:
