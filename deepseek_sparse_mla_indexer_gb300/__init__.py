@@ -608,9 +608,11 @@ def nsa_evict_compact(keep: torch.Tensor, new_len: torch.Tensor, old_len: torch.
     if keep.dtype != torch.int32 or keep.dim() != 2 or keep.shape[0] != B:
         raise ValueError(f"keep must be int32 [{B}, budget], got shape {tuple(keep.shape)} of {keep.dtype}")
     pt = _table(page_table, B)
+    if page_size < 1:
+        raise ValueError(f"page_size must be positive, got {page_size}")
     slots = arrays[0].shape[0] if len(arrays) else pt.shape[1] * page_size
     for a in arrays:
-        if not a.is_contiguous() or a.shape[0] != slots or slots % page_size:
+        if not a.is_contiguous() or a.shape[0] != slots or slots < 1 or slots % page_size:
             raise ValueError(f"the arrays must be contiguous with one first dimension of whole pages of {page_size}, "
                              f"got shape {tuple(a.shape)}")
     total_ld = 0 if total is None else _total_ld(total, B, max_len)
