@@ -31,7 +31,7 @@
 //
 // Measured (GB300, a pass among others, positions 4096 .. 32768 unless said):
 //   32 requests x 128 heads, bf16   157 us: 3.4 TB/s, 0.82 PF
-//   128 x 16 heads, fp8, 1024 ..    154 us: 3.1 TB/s
+//   128 x 16 heads, fp8, 1024 ..    152 us: 3.1 TB/s
 //   8 x 4 tokens x 128 heads, fp8, 16384 .. 131072   697 us: 0.77 PF
 //   1 x 16 heads, bf16, 501         23 us
 // Bound by the chain of a tile: 5200 cycles (bf16, 64 columns), of which the products take 3640
@@ -780,8 +780,15 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         if (!mbar_wait(&sm->raw.full[rs], rph, kPtWait)) ok = false;
                         RawStep x;
                         x.read(raw_s + rs * kRawSlot, scales, m, d, live);
-                        if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) ok = false;
-                        x.store(d, kv_s + 2 * m * kPtBlk, kv_s + (2 * m + 1) * kPtBlk);
+                        if constexpr (NC == 16) {  // expanded ahead of the wait (2 %); 32 columns leave no registers for it
+                            uint4 e[kDqRows][2];
+                            x.expand(e);
+                            if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) ok = false;
+                            x.store(e, d, kv_s + 2 * m * kPtBlk, kv_s + (2 * m + 1) * kPtBlk);
+                        } else {
+                            if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) ok = false;
+                            x.store(d, kv_s + 2 * m * kPtBlk, kv_s + (2 * m + 1) * kPtBlk);
+                        }
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {

@@ -301,6 +301,26 @@ struct RawStep {
             sc[u] = scales[u];
         }
     }
+    // The step's values, ahead of a wait for the blocks they go to.
+    __device__ __forceinline__ void expand(uint4 (&e)[kDqRows][2]) const
+    {
+#pragma unroll
+        for (int u = 0; u < kDqRows; ++u) {
+            e[u][0] = expand8(w[u][0].x, w[u][0].y, sc[u]);
+            e[u][1] = expand8(w[u][1].x, w[u][1].y, sc[u]);
+        }
+    }
+    static __device__ __forceinline__ void store(const uint4 (&e)[kDqRows][2], int d, uint8_t *blk0, uint8_t *blk1)
+    {
+        const int k = d & 7, r = d >> 3, c0 = (2 * k) & 7, sw = swap(d) ? 1 : 0;
+        uint8_t *blk = k < 4 ? blk0 : blk1;
+        uint8_t *first = blk + sm100::sw128_offset(r, c0 + sw), *second = blk + sm100::sw128_offset(r, c0 + 1 - sw);
+#pragma unroll
+        for (int u = 0; u < kDqRows; ++u) {
+            *reinterpret_cast<uint4 *>(first + u * (kPtTok / kDqRows) * 128) = e[u][0];
+            *reinterpret_cast<uint4 *>(second + u * (kPtTok / kDqRows) * 128) = e[u][1];
+        }
+    }
     __device__ __forceinline__ void store(int d, uint8_t *blk0, uint8_t *blk1) const
     {
         const int k = d & 7, r = d >> 3, c0 = (2 * k) & 7, sw = swap(d) ? 1 : 0;
