@@ -32,7 +32,7 @@
 // Measured (GB300, a pass among others, positions 4096 .. 32768 unless said):
 //   32 requests x 128 heads, bf16   157 us: 3.4 TB/s, 0.82 PF
 //   128 x 16 heads, fp8, 1024 ..    152 us: 3.1 TB/s
-//   8 x 4 tokens x 128 heads, fp8, 16384 .. 131072   697 us: 0.77 PF
+//   8 x 4 tokens x 128 heads, fp8, 16384 .. 131072   704 us: 0.76 PF
 //   1 x 16 heads, bf16, 501         23 us
 // Bound by the chain of a tile: 5200 cycles (bf16, 64 columns), of which the products take 3640
 // (N = 64 is bound by the tensor core's reads of shared memory: 48 cycles a product, not 32),
@@ -76,7 +76,7 @@ struct AShared {
     alignas(16) float m_run[kCols];   // running maximum, log2 units
     alignas(16) float alpha[kCols];
     float red[4][kCols];
-    float l_col[kCols];
+    float inv[kCols];                 // 1 / sum; 0: no key
     int len[kCols];                   // positions the column's row sees
     int min_len[4];                   // shortest of all the CTA's columns, one copy a group
     uint64_t pair_full[5];            // block pair m of the tile landed (m = 4: the rope block)
@@ -725,7 +725,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 if (et < kGrp) {
                     const int c = cb + et;
                     const float sum = (sm->red[0][c] + sm->red[1][c]) + (sm->red[2][c] + sm->red[3][c]);
-                    sm->l_col[c] = sum;
+                    sm->inv[c] = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
                     if (et < nc) {
                         if (whole)
                             p.lse[row0 + et] = sum > 0.f ? (sm->m_run[c] + log2f(sum)) * 0.69314718055994531f
@@ -749,8 +749,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         __nv_bfloat16 *o = p.out + row0 * kPtDl + m * 128 + key;
 #pragma unroll
                         for (int c = 0; c < kGrp; ++c) {
-                            const float sum = sm->l_col[cb + c];
-                            const float r = sum > 0.f ? __uint_as_float(v[c]) / sum : (sum == sum ? 0.f : sum);
+                            const float r = __uint_as_float(v[c]) * sm->inv[cb + c];  // a column without a key: 0 times 0
                             if (c < nc) o[(int64_t)c * kPtDl] = __float2bfloat16_rn(r);
                         }
                     } else {
