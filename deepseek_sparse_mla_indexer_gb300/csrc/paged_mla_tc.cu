@@ -13,16 +13,17 @@
 // Shared memory holds Q (72 KB of 64 columns) and one tile (144 KB), so tiles are pipelined
 // by block pairs: pair m is loaded again as soon as O^T's d-block m, its last reader,
 // is done, and S^T of the next tile starts on the pairs that have landed.  P^T lies
-// in the rope block, which S^T has finished with.  CTAs with neighbouring columns of the
-// same request run as a cluster of two (fp8 of 256 columns and more: four): each loads its
-// part of every tile into all of them (TMA multicast), which divides the traffic from L2; a
-// pair is loaded again when all are done with it.
+// in the rope block, which S^T has finished with.
 //
 // fp8 rows become bf16 in the CTA.  Up to 32 columns, Q leaves room for slots of raw codes,
 // which TMA fills and 512 threads expand into the tile.  More columns leave none, and sharing
-// the expansion pays: 128 threads of each CTA of a cluster expand their part of the tile from
-// registers into a scratch in global memory that stays in L2, and TMA multicasts it from there
-// as it does bf16 rows.
+// the expansion pays: CTAs with neighbouring columns of the same request run as a cluster of two
+// or four (make_plan), 128 threads of each expand their part of the tile from registers into a
+// scratch in global memory that stays in L2, and every CTA of the cluster loads the tile from there.
+//
+// Every load goes into the CTA that issues it.  One load into all CTAs of a cluster took less
+// from L2 (32 x 128 heads bf16 157 us, now 163; fp8 248, now 256; 8 x 4 x 128 heads fp8 704, now 694),
+// but it is safe only on this GPU's own memory and in programs on one GPU, which a call cannot see.
 //
 // The tiles of all requests are cut into equal shares over the CTAs (teams of up to
 // eight CTAs take the same tiles for different columns, so that a tile is read from
@@ -56,7 +57,7 @@ constexpr float kRescale = 8.0f;          // log2 units
 constexpr int kMaxTeam = 8;
 // How the tile's rows come: a bf16 cache by TMA; raw fp8 rows by TMA into slots beside the
 // tile and expanded from there; or fp8 rows expanded into the CTA's scratch in global memory
-// (each CTA of a cluster its part of the tile) and loaded from it as bf16 rows are.
+// (each CTA of a cluster its part of the tile) and loaded from it in whole blocks.
 enum Rows { kBf16Rows, kRawRows, kScratchRows };
 // What a further request in a share costs, in tiles: its epilogue, the loads that find it and its
 // first tiles from HBM took 18 - 22 thousand cycles against 5.2 a tile (32 requests of 128 heads:
@@ -83,7 +84,8 @@ struct AShared {
     uint64_t pair_free[5];            // its readers are done (m = 4: every product of the tile)
     uint64_t q_full, q_empty, s_full, p_full, o_fin;
     RawShared raw;
-    uint64_t scr_full[kScrSlots], scr_free[kScrSlots];  // half tiles of the scratch
+    // tiles of the scratch: this CTA's part written (its row warps), every CTA's part written, the tile loaded into this CTA
+    uint64_t scr_part[kScrMaxSlots], scr_full[kScrMaxSlots], scr_loaded[kScrMaxSlots];
     TileShare share;
     uint32_t tmem_base;
     volatile uint32_t scr_tiles;      // parts of tiles that the row warps have expanded
@@ -108,7 +110,7 @@ struct AParams {
     int4 *unit;                    // [B * mult] of each (request, group set): first and last share, whether the first began earlier
     float *part;                   // [2 * CTAs][slot_cols][512] raw accumulators
     float2 *part_ml;               // [2 * CTAs][slot_cols] maximum (log2 units) and sum
-    uint8_t *scratch;              // [CTAs][kScrSlots][128 / cluster][576] bf16 (fp8 rows of clusters)
+    uint8_t *scratch;              // [clusters][scr_slots] tiles of bf16 (fp8 rows of clusters)
 };
 
 // The pieces of a share: tiles [t0, t1) of group set j of request b.
@@ -202,17 +204,17 @@ __device__ __forceinline__ void tmem_stg(uint32_t taddr, const uint32_t (&r)[G])
     else tmem_st8(taddr, r);
 }
 
-// CL: CTAs of a cluster, which share their tiles; NC: columns of the CTA's products (16, 32 or 64).
-// kv_map: bf16 rows of the cache or of the scratch, or the fp8 codes; sc_map, rope_map: of raw rows.
+// CL: CTAs of a cluster, which share the expansion of their tiles; NC: columns of the CTA's products (16, 32 or 64).
+// kv_map: bf16 rows of the cache, or the fp8 codes; sc_map, rope_map: of raw rows.  Scratch rows need none.
 template <Rows ROWS, int CL, int NC>
 __global__ void __launch_bounds__(threads_of(ROWS, NC), 1)
 paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
                     const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
                     const __grid_constant__ CUtensorMap rope_map)
 {
-    constexpr bool RAW = ROWS == kRawRows, SCR = ROWS == kScratchRows, PAIR = CL > 1;
-    constexpr uint16_t kAll = (1 << CL) - 1;  // every CTA of the cluster
+    constexpr bool RAW = ROWS == kRawRows, SCR = ROWS == kScratchRows;
     constexpr int kScrRows = kPtTok / CL;     // rows of a tile that one CTA expands
+    constexpr int kScrAhead = scr_ahead(CL), kScrSlots = scr_slots(CL);
     constexpr int kGrp = grp_of(NC), kGroups = NC / kGrp, kRow0 = row0_of(NC), kRaw = raw_slots(NC);
     constexpr uint32_t kQBlk = NC * 128;
     extern __shared__ uint8_t smem_raw[];
@@ -223,12 +225,13 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
     AShared *sm = (AShared *)(sc_s + (RAW ? 2 * kScaleSlot : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = blockIdx.x / p.team, rank = blockIdx.x - team * p.team;  // rank: column group in the set
-    const int peer = PAIR ? (int)cluster_ctarank() : 0;
+    const int peer = CL > 1 ? (int)cluster_ctarank() : 0;
+    uint8_t *scr = SCR ? p.scratch + (int64_t)(blockIdx.x / CL) * kScrSlots * kScrTile : nullptr;  // of the cluster
 
     if (threadIdx.x == 0) {
         for (int m = 0; m < 5; ++m) {
             mbar_init(&sm->pair_full[m], RAW && m < 4 ? kDqThreads / 32 : 1);
-            mbar_init(&sm->pair_free[m], CL);
+            mbar_init(&sm->pair_free[m], 1);
         }
         mbar_init(&sm->q_full, 1);
         mbar_init(&sm->q_empty, 1);
@@ -240,9 +243,10 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             mbar_init(&sm->raw.empty[i], kDqThreads / 32);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&sm->raw.tile_full[i], 1);
-        for (int i = 0; i < kScrSlots; ++i) {
-            mbar_init(&sm->scr_full[i], kScrThreads / 32);
-            mbar_init(&sm->scr_free[i], 1);
+        for (int i = 0; i < kScrMaxSlots; ++i) {
+            mbar_init(&sm->scr_part[i], kScrThreads / 32);
+            mbar_init(&sm->scr_full[i], CL);
+            mbar_init(&sm->scr_loaded[i], 1);
         }
         sm->scr_tiles = 0;
         sm->abort = 0;
@@ -255,17 +259,54 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
     if (threadIdx.x == 64) {
         prefetch_tensormap(&qn_map);
         prefetch_tensormap(&qr_map);
-        prefetch_tensormap(&kv_map);
+        if (!SCR) prefetch_tensormap(&kv_map);
     }
     pdl_trigger();  // the join may be launched while this grid works; it waits for its end
     tc_fence_before();
     find_share(p.t, p.mult, piece_of(ROWS), team, p.teams, &sm->share);  // ends with a block barrier
-    if (PAIR) cluster_sync_all();  // the peer's barriers are ready before anything reaches them
+    if (CL > 1) cluster_sync_all();  // the peers' barriers are ready before anything reaches them
     tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
     auto fail = [&]() {
         sm->abort = 1;
         set_status(p.t.status, NSA_ERR_TIMEOUT);
+    };
+    // The shares of every unit, for the join (one warp of the launch).
+    auto write_units = [&]() {
+        const int64_t total = sm->share.total, np = sm->share.np;
+        const int piece = sm->share.piece;
+        // share k is [total * k / np, total * (k + 1) / np)
+        auto share_of = [&](int64_t g) -> int {
+            int k = (int)(g * np / total);
+            while (k + 1 < np && total * (k + 1) / np <= g) ++k;
+            while (k > 0 && total * k / np > g) --k;
+            return k;
+        };
+        int64_t before = 0;
+        for (int base = 0; base < p.t.B; base += 32) {
+            const int b = base + lane;
+            const int tiles = b < p.t.B ? tiles_of(request_len(p.t, b)) : 0;
+            const int64_t v = tiles > 0 ? tiles + piece : 0;
+            int64_t inc = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            if (b < p.t.B) {
+                int64_t u0 = (before + inc - v) * p.mult;
+                for (int j = 0; j < p.mult; ++j, u0 += v) {
+                    int4 u = make_int4(0, 0, 0, 0);
+                    if (v > 0) {
+                        u.x = share_of(u0 + piece);
+                        u.y = share_of(u0 + v - 1);
+                        u.z = total * u.x / np < u0 ? 1 : 0;
+                    }
+                    p.unit[(int64_t)b * p.mult + j] = u;
+                }
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31);
+        }
     };
     Seg s;
     const bool work = s.start(p, sm->share);
@@ -275,8 +316,6 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             // -------------------------------------------------------- TMA
             const int boxes = kPtTok / p.t.box_rows;  // at most 16, one a lane
             const uint32_t box_bytes = (uint32_t)p.t.box_rows * 128;
-            // a cluster's CTAs share out the boxes of a tile in order
-            const int box0 = boxes / CL * peer, box1 = boxes / CL * (peer + 1);
             constexpr uint32_t kRowBytes = ROWS == kBf16Rows ? 2 * (kPtDl + kPtDr) : kPtFp8Row;
             uint32_t i = 0, seg = 0, rph = 0;
             int rs = 0;
@@ -303,11 +342,11 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     const uint32_t blk_bytes = SCR ? kPtBlk : __popc(live) * box_bytes;
                     // one lane issues a box at a time from uniform registers: a box's coordinates and
                     // addresses per lane took 350 cycles a pair
-                    const int y_first = __shfl_sync(0xffffffffu, y, box0);
+                    const int y_first = __shfl_sync(0xffffffffu, y, 0);
                     auto boxes_of = [&](auto issue) {
                         int yb = y_first;
-                        for (int x = box0; x < box1; ++x) {
-                            if (x > box0) yb = __shfl_sync(0xffffffffu, y, x);
+                        for (int x = 0; x < boxes; ++x) {
+                            if (x > 0) yb = __shfl_sync(0xffffffffu, y, x);
                             if (yb >= 0 && elect_one()) issue(x, yb);
                             __syncwarp();
                         }
@@ -344,8 +383,8 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     } else {
                         const uint32_t ss = i % kScrSlots;
                         if constexpr (SCR) {
-                            // this CTA's part of the tile is in its scratch: written by the row warps
-                            if (!mbar_wait(&sm->scr_full[ss], i / kScrSlots & 1, kPtWait)) ok = false;
+                            // every CTA's row warps have written their part of the tile to its scratch
+                            if (!mbar_wait_cluster(&sm->scr_full[ss], i / kScrSlots & 1, kPtWait)) ok = false;
                             asm volatile("fence.proxy.async.global;" ::: "memory");
                         }
 #pragma unroll
@@ -353,36 +392,26 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                             if (!mbar_wait(&sm->pair_free[m], (i & 1) ^ 1, kPtWait)) ok = false;
                             if (elect_one()) {
                                 mbar_arrive_expect_tx(&sm->pair_full[m], (m < 4 ? 2 : 1) * blk_bytes);
-                                // every CTA is done with the tile before: its scratch may be written again
-                                if (SCR && m == 4 && i > 0) mbar_arrive(&sm->scr_free[(i - 1) % kScrSlots]);
+                                if (SCR && CL == 4 && m == 4 && i > 0) mbar_arrive(&sm->scr_loaded[(i - 1) % kScrSlots]);
                             }
                             __syncwarp();
                             if constexpr (SCR) {
-                                if (elect_one()) {
-#pragma unroll
-                                    for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c)
-                                        tma_load_2d_multicast(kv_s + c * kPtBlk + peer * (kPtBlk / CL), &kv_map, 64 * c,
-                                                              (int)(blockIdx.x * kScrSlots + ss) * kScrRows,
-                                                              &sm->pair_full[m], kAll);
-                                }
+                                if (elect_one())
+                                    bulk_load(kv_s + 2 * m * kPtBlk, scr + ss * kScrTile + 2 * m * kPtBlk,
+                                              (m < 4 ? 2 : 1) * kPtBlk, &sm->pair_full[m]);
                                 __syncwarp();
                             } else {
                                 boxes_of([&](int x, int yb) {
 #pragma unroll
-                                    for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c) {
-                                        uint8_t *dst = kv_s + c * kPtBlk + x * box_bytes;
-                                        if (PAIR)
-                                            tma_load_2d_multicast(dst, &kv_map, 64 * c, yb, &sm->pair_full[m], kAll);
-                                        else
-                                            tma_load_2d(dst, &kv_map, 64 * c, yb, &sm->pair_full[m]);
-                                    }
+                                    for (int c = 2 * m; c < (m < 4 ? 2 * m + 2 : 9); ++c)
+                                        tma_load_2d(kv_s + c * kPtBlk + x * box_bytes, &kv_map, 64 * c, yb, &sm->pair_full[m]);
                                 });
                             }
                         }
                     }
                     // the tile after the next one into L2 while this one is worked on
                     const int y2 = SCR ? -1 : box_row(t + 2);
-                    if (!SCR && lane >= box0 && lane < box1 && y2 >= 0)
+                    if (!SCR && y2 >= 0)
                         prefetch_l2_bulk(p.t.kv + (int64_t)y2 * kRowBytes, (uint32_t)p.t.box_rows * kRowBytes);
                     y = y1;
                     y1 = y2;
@@ -395,7 +424,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 if (i > 0)
                     for (int m = 0; m < 5; ++m) {
                         mbar_wait(&sm->pair_full[m], (i - 1) & 1, kPtWait);
-                        mbar_wait(&sm->pair_free[m], (i - 1) & 1, kPtWait);  // the peer's arrivals too
+                        mbar_wait(&sm->pair_free[m], (i - 1) & 1, kPtWait);
                     }
                 if (RAW) {
                     for (uint32_t x = i > 2 ? i - 2 : 0; x < i; ++x) mbar_wait(&sm->raw.tile_full[x & 1], (x >> 1) & 1, kPtWait);
@@ -414,12 +443,6 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             const uint64_t q_desc = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
             const uint64_t v_desc = smem_desc(smem_u32(kv_s), kPtBlk, 1024, kSwizzle128B);
             const uint64_t p_desc = smem_desc(smem_u32(p_s), kPtBlk, 1024, kSwizzle128B);
-            auto free_pair = [&](int m) {
-                if (PAIR)
-                    mma_commit_multicast(&sm->pair_free[m], kAll);
-                else
-                    mma_commit(&sm->pair_free[m]);
-            };
             uint32_t i = 0, seg = 0;
             bool ok = true;
             for (bool more = true; more && ok; more = s.next(p, sm->share), ++seg) {
@@ -454,9 +477,9 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                             for (int k = 0; k < kPtTok / 16; ++k)
                                 mma_f16(tmem + m * NC, v_desc + (2 * m * kPtBlk + k * 2048) / 16, p_desc + k * 2048 / 16,
                                         idesc_o, k > 0 ? 1u : (uint32_t)(t > s.t0));
-                            free_pair(m);
+                            mma_commit(&sm->pair_free[m]);
                         }
-                        free_pair(4);
+                        mma_commit(&sm->pair_free[4]);
                         if (t + 1 == s.t1) mma_commit(&sm->o_fin);
                     }
                     __syncwarp();
@@ -471,44 +494,27 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 for (int w = 0; w < 2; ++w) mbar_wait(&sm->o_fin, w, kPtWait / 100);
             }
             __syncwarp();
-        } else if (warp == 2 && blockIdx.x == 0) {
-            // -------------------------------------------------------- the shares of every unit, for the join
-            const int64_t total = sm->share.total, np = sm->share.np;
-            const int piece = sm->share.piece;
-            // share k is [total * k / np, total * (k + 1) / np)
-            auto share_of = [&](int64_t g) -> int {
-                int k = (int)(g * np / total);
-                while (k + 1 < np && total * (k + 1) / np <= g) ++k;
-                while (k > 0 && total * k / np > g) --k;
-                return k;
-            };
-            int64_t before = 0;
-            for (int base = 0; base < p.t.B; base += 32) {
-                const int b = base + lane;
-                const int tiles = b < p.t.B ? tiles_of(request_len(p.t, b)) : 0;
-                const int64_t v = tiles > 0 ? tiles + piece : 0;
-                int64_t inc = v;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += x;
-                }
-                if (b < p.t.B) {
-                    int64_t u0 = (before + inc - v) * p.mult;
-                    for (int j = 0; j < p.mult; ++j, u0 += v) {
-                        int4 u = make_int4(0, 0, 0, 0);
-                        if (v > 0) {
-                            u.x = share_of(u0 + piece);
-                            u.y = share_of(u0 + v - 1);
-                            u.z = total * u.x / np < u0 ? 1 : 0;
-                        }
-                        p.unit[(int64_t)b * p.mult + j] = u;
+        } else if (warp == 2) {
+            if constexpr (SCR) {
+                // ---------------------------------------------------- tells the cluster of this CTA's parts of tiles
+                // A warp of its own: a release to other CTAs waits until the row warps' stores have arrived, a
+                // thousand cycles and more, which they need not spend (279 us for 32 x 128 heads when they did).
+                uint32_t i = 0;
+                bool ok = true;
+                for (bool more = work; more && ok; more = s.next(p, sm->share))
+                    for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
+                        const uint32_t ss = i % kScrSlots;
+                        if (!mbar_wait(&sm->scr_part[ss], i / kScrSlots & 1, kPtWait)) ok = false;
+                        if (lane < CL) mbar_arrive_cluster(&sm->scr_full[ss], lane);
+                        ok = __all_sync(0xffffffffu, ok && !sm->abort) != 0;
                     }
-                }
-                before += __shfl_sync(0xffffffffu, inc, 31);
+                if (!ok && lane == 0) fail();
+            } else if (blockIdx.x == 0) {
+                write_units();
             }
         } else if (warp == 3) {
             // -------------------------------------------------------- bad lengths, requests without a key
+            if (SCR && blockIdx.x == 0) write_units();
             if (blockIdx.x == 0) report_lengths(p.t, lane, 32);
             for (int b = blockIdx.x; b < p.t.B; b += gridDim.x) {
                 if (request_len(p.t, b) > 0) continue;
@@ -595,6 +601,8 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     const bool valid = checked_page(p.t, pt, pos, s.len) >= 0;
                     ok = mbar_wait(&sm->s_full, i & 1, kPtWait);
                     if (!ok) fail();
+                    // S^T is done, so the tile was loaded (clusters of four: told by the TMA warp, later)
+                    if (SCR && CL == 2 && threadIdx.x == 128 && ok) mbar_arrive(&sm->scr_loaded[i % kScrSlots]);
                     tc_fence_after();
                     const bool whole = (t + 1) * kPtTok <= min_len && __all_sync(0xffffffffu, valid);
                     bool odd = false;  // a score of this key is not finite (looked at where columns are masked)
@@ -809,7 +817,6 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
         if (work) {
             // -------------------------------------------------------- rows expanded into the scratch
             const int d = threadIdx.x - kRow0;
-            uint8_t *scr = p.scratch + (int64_t)blockIdx.x * kScrSlots * kScrRows * kScrRow;
             const int off = peer * kScrRows;     // this CTA's part of a tile
             constexpr int kSteps = kScrRows / kScrStep;  // steps a tile
             // The step whose page is asked for next: a step before its rows are loaded, which is two
@@ -853,14 +860,20 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
             bool ok = true;
             auto step = [&](ScrRows &x) {
                 const uint32_t tile = n / kSteps, u = n % kSteps, ss = tile % kScrSlots;
-                if (u == 0 && !mbar_wait(&sm->scr_free[ss], (tile / kScrSlots & 1) ^ 1, kPtWait)) ok = false;
-                x.store(scr + (ss * kScrRows + kScrStep * u) * kScrRow, d);
+                if (u == 0 && tile >= kScrAhead) {
+                    // This CTA has loaded tile - kScrAhead, and every CTA has written its part of it, which it does
+                    // when it has loaded tile - 2 kScrAhead: nobody reads this slot any more.
+                    const uint32_t s2 = (tile - kScrAhead) % kScrSlots, ph = (tile - kScrAhead) / kScrSlots & 1;
+                    if (!mbar_wait(&sm->scr_loaded[s2], ph, kPtWait) || !mbar_wait_cluster(&sm->scr_full[s2], ph, kPtWait))
+                        ok = false;
+                }
+                x.store(scr + ss * kScrTile, off + kScrStep * u + (d >> 3), d);
                 --left;
                 ++n;
                 if (u == kSteps - 1) {
                     asm volatile("fence.proxy.async.global;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm->scr_full[ss]);
+                    if (lane == 0) mbar_arrive(&sm->scr_part[ss]);
                     if (d == 0) sm->scr_tiles = tile + 1;
                 }
                 load(x);
@@ -883,7 +896,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
-    if (PAIR) cluster_sync_all();  // the peer's copies and arrivals into this CTA are over
+    if (CL > 1) cluster_sync_all();  // the peers' arrivals in this CTA are over
 }
 
 // Columns that several shares worked on: with M the largest maximum,
@@ -1021,8 +1034,8 @@ Plan make_plan(bool fp8, int R, int n, int H, int max_row_len, int sms)
     q.team = 1;
     while (q.team < kMaxTeam && q.groups % (2 * q.team) == 0) q.team *= 2;
     q.mult = q.groups / q.team;
-    // clusters of four halve what each CTA has to expand; bf16 rows gain nothing over pairs
-    q.cluster = q.rows == kScratchRows ? (q.team >= 4 && q.nc == kCols ? 4 : 2) : q.rows == kBf16Rows && q.team >= 2 ? 2 : 1;
+    // clusters of four halve what each CTA has to expand
+    q.cluster = q.rows == kScratchRows ? (q.team >= 4 && q.nc == kCols ? 4 : 2) : 1;
     const int64_t most = (int64_t)(R / n) * q.mult * ceil_div(max_row_len, kPtTok);
     // the CTAs of a wave: clusters of four leave SMs of some GPCs idle
     const int ctas = q.cluster == 4 ? 4 * clusters_of_four() : sms;
@@ -1033,7 +1046,7 @@ Plan make_plan(bool fp8, int R, int n, int H, int max_row_len, int sms)
     q.head_bytes = (size_t)(R / n) * q.mult * sizeof(int4);
     q.ml_bytes = (slots * sizeof(float2) + 15) / 16 * 16;
     q.part_bytes = slots * kPtDl * sizeof(float);
-    q.scratch_bytes = q.rows == kScratchRows ? (size_t)q.teams * q.team * kScrSlots * (kPtTok / q.cluster) * kScrRow : 0;
+    q.scratch_bytes = q.rows == kScratchRows ? (size_t)q.teams * q.team / q.cluster * scr_slots(q.cluster) * kScrTile : 0;
     return q;
 }
 
@@ -1054,7 +1067,8 @@ nsa_status launch(const AParams &p, const Maps &m, cudaStream_t stream)
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CL;
+    // bf16: pairs of a team side by side read a tile through the same part of L2 (169 -> 163 us, 32 x 128 heads)
+    attr[0].val.clusterDim.x = ROWS == kBf16Rows && p.team % 2 == 0 ? 2 : CL;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -1114,8 +1128,7 @@ nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse,
         q.rows == kBf16Rows ? bf16_rows_map(a.kv, (uint64_t)a.num_pages * a.page_size, (uint32_t)p.t.box_rows, &m.kv)
         : q.rows == kRawRows
             ? fp8_maps(a, (uint32_t)p.t.box_rows, 128, &m.kv, &m.sc, &m.rope)
-            : bf16_rows_map(p.scratch, (uint64_t)q.teams * q.team * kScrSlots * (kPtTok / q.cluster),
-                            (uint32_t)(kPtTok / q.cluster), &m.kv);
+            : true;
     if (!mapped) return NSA_ERR_CUDA;
     if (q.rows == kRawRows)
         return q.nc == 16 ? launch<kRawRows, 1, 16>(p, m, stream) : launch<kRawRows, 1, 32>(p, m, stream);
@@ -1123,7 +1136,6 @@ nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse,
         return q.nc == 32          ? launch<kScratchRows, 2, 32>(p, m, stream)
                : q.cluster == 2 ? launch<kScratchRows, 2, 64>(p, m, stream)
                                 : launch<kScratchRows, 4, 64>(p, m, stream);
-    if (q.cluster == 2) return launch<kBf16Rows, 2, 64>(p, m, stream);
     return q.nc == 16   ? launch<kBf16Rows, 1, 16>(p, m, stream)
            : q.nc == 32 ? launch<kBf16Rows, 1, 32>(p, m, stream)
                         : launch<kBf16Rows, 1, 64>(p, m, stream);

@@ -383,14 +383,22 @@ __device__ __forceinline__ uint32_t live_rows(const PagedTc &p, uint32_t boxes, 
     return live;
 }
 
-// Rows expanded from registers into a scratch copy of a CTA's part of the tile in global
-// memory (which stays in L2), for clusters: thread d of kScrThreads owns chunk d % 8 of each
-// 128-value block of row d / 8 of a step's kScrStep.  Two sets of registers take turns, so a
-// row is loaded while the one before it is expanded.
+// Rows expanded from registers into a scratch copy of the tile in global memory (which stays in
+// L2), one copy a cluster: thread d of kScrThreads owns chunk d % 8 of each 128-value block of row
+// d / 8 of a step's kScrStep.  The copy has the layout of the tile in shared memory (blocks of
+// 128 x 128 bytes, swizzled), so that a pair of blocks comes from there as one run of bytes.  Two sets
+// of registers take turns, so a row is loaded while the one before it is expanded.
 constexpr int kScrThreads = 128;
 constexpr int kScrStep = kScrThreads / 8;       // rows at a time
-constexpr int kScrSlots = 4;                    // parts of tiles a CTA's scratch holds
-constexpr int kScrRow = 2 * (kPtDl + kPtDr);    // bytes
+// Tiles that are expanded ahead of the loaded ones, by the cluster's size; a cluster's scratch holds
+// twice as many.  Pairs expand four steps a tile and want to be told of a loaded tile at once, with a
+// small scratch (32 x 128 heads: 256 us; three ahead 274).  Clusters of four expand two steps, which
+// fit beside the next tile's first products: told only when the tile is done, three ahead, they
+// stay out of the softmax's way (8 x 4 x 128 heads: 694 us; two ahead 772, told at once 777 - 793).
+constexpr int scr_ahead(int cl) { return cl == 4 ? 3 : 2; }
+constexpr int scr_slots(int cl) { return 2 * scr_ahead(cl); }
+constexpr int kScrMaxSlots = scr_slots(4);
+constexpr uint32_t kScrTile = 9 * kPtBlk;       // bytes of a tile's copy
 
 struct ScrRows {
     uint4 w[5];
@@ -410,17 +418,20 @@ struct ScrRows {
             sc = __ldg(reinterpret_cast<const float4 *>(row + kPtDl));
         }
     }
-    __device__ __forceinline__ void store(uint8_t *rows, int d) const
+    // into row `row` of the tile's copy
+    __device__ __forceinline__ void store(uint8_t *tile, int row, int d) const
     {
-        uint8_t *row = rows + (d >> 3) * kScrRow;
+        const int k = d & 7;
         const float s[4] = {sc.x, sc.y, sc.z, sc.w};
+        // codes 16k .. 16k+15 of a 128-value block become chunks 2k, 2k + 1 of its sixteen
+        uint8_t *o0 = tile + (k >> 2) * kPtBlk + sm100::sw128_offset(row, (2 * k) & 7);
+        uint8_t *o1 = tile + (k >> 2) * kPtBlk + sm100::sw128_offset(row, (2 * k + 1) & 7);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            uint4 *o = reinterpret_cast<uint4 *>(row + 256 * m + 32 * (d & 7));
-            o[0] = expand8(w[m].x, w[m].y, s[m]);
-            o[1] = expand8(w[m].z, w[m].w, s[m]);
+            *reinterpret_cast<uint4 *>(o0 + 2 * m * kPtBlk) = expand8(w[m].x, w[m].y, s[m]);
+            *reinterpret_cast<uint4 *>(o1 + 2 * m * kPtBlk) = expand8(w[m].z, w[m].w, s[m]);
         }
-        *reinterpret_cast<uint4 *>(row + 2 * kPtDl + 16 * (d & 7)) = w[4];
+        *reinterpret_cast<uint4 *>(tile + 8 * kPtBlk + sm100::sw128_offset(row, k)) = w[4];
     }
 };
 
@@ -481,7 +492,7 @@ inline bool paged_tc_q_maps(const PagedMlaArgs &args, uint32_t rows, CUtensorMap
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Map of bf16 rows (a bf16 cache, or expanded rows): boxes of 64 columns x box_rows rows.
+// Map of the rows of a bf16 cache: boxes of 64 columns x box_rows rows.
 inline bool bf16_rows_map(const void *base, uint64_t rows, uint32_t box_rows, CUtensorMap *kv)
 {
     return make_tma_2d(kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, kPtDl + kPtDr, rows, 2 * (kPtDl + kPtDr), 64, box_rows,
