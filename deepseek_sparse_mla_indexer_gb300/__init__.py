@@ -513,7 +513,8 @@ def nsa_paged_mla_workspace_bytes(q_dtype: int, kv_dtype: int, R: int, rows_per_
 
 def alloc_paged_mla_workspace(q_dtype: int, kv_dtype: int, R: int, rows_per_req: int, H: int, max_row_len: int,
                               d_latent: int = 512, d_rope: int = 64, device="cuda") -> Optional[torch.Tensor]:
-    """Scratch for nsa_paged_mla calls of this shape (None if they need none)."""
+    """Scratch for nsa_paged_mla calls of these types and at most this shape (no more rows, rows a request,
+    heads or positions; None if they need none)."""
     n = nsa_paged_mla_workspace_bytes(q_dtype, kv_dtype, R, rows_per_req, H, max_row_len, d_latent, d_rope)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
@@ -524,7 +525,7 @@ def nsa_paged_mla(q_dtype: int, kv_dtype: int, q_nope: torch.Tensor, q_rope: tor
                   status: Optional[torch.Tensor] = None, stream=None) -> None:
     """q_nope [R, H, d_latent] and q_rope [R, H, d_rope] (any row / head strides); kv [slots, row];
     page_table int32 [R / rows_per_req, pages]; row_len int32 [R]; out [R, H, d_latent] (q's type) and
-    lse float32 [R, H].  workspace: alloc_paged_mla_workspace's, for this shape or a larger one."""
+    lse float32 [R, H].  workspace: alloc_paged_mla_workspace's, for this shape or a larger one (see there)."""
     R, H, dl = q_nope.shape
     dr = q_rope.shape[2]
     if rows_per_req < 1 or R % rows_per_req:

@@ -169,7 +169,7 @@ extern "C" nsa_status nsa_paged_mla(nsa_dtype q_dtype, nsa_dtype kv_dtype, const
     if (need > 0 && (workspace_bytes < need || !workspace_dev || ((uintptr_t)workspace_dev & 15)))
         return NSA_ERR_INVALID_ARG;
     const cudaStream_t s = (cudaStream_t)stream;
-    const nsa_status st = paged_mla_tc_try_launch(a, out_dev, lse_dev, workspace_dev, s);
+    const nsa_status st = paged_mla_tc_try_launch(a, out_dev, lse_dev, workspace_dev, workspace_bytes, s);
     if (st != NSA_ERR_UNSUPPORTED) return st;
     if (q_dtype == NSA_DT_F32) return launch_simt<NSA_DT_F32, NSA_DT_F32>(a, out_dev, lse_dev, s);
     if (kv_dtype == NSA_DT_BF16) return launch_simt<NSA_DT_BF16, NSA_DT_BF16>(a, out_dev, lse_dev, s);

@@ -22,6 +22,13 @@ struct PagedMlaArgs {
     int32_t *status;
 };
 
+// Sizes that the kernels index with 32 bits.
+inline bool paged_mla_sizes_ok(int R, int rows_per_req, int H, int max_row_len)
+{
+    return H <= 65535 && max_row_len <= (1 << 30) && (int64_t)rows_per_req * H <= (1 << 20) &&
+           (int64_t)R * H <= 2147483647LL;
+}
+
 // Host-side checks that both entry points make.  NSA_OK also for R == 0.
 inline nsa_status check_paged_mla(const PagedMlaArgs &a)
 {
@@ -35,8 +42,7 @@ inline nsa_status check_paged_mla(const PagedMlaArgs &a)
         (a.q_dtype == NSA_DT_BF16 && (a.kv_dtype == NSA_DT_BF16 || a.kv_dtype == NSA_DT_E4M3));
     if (!combo_ok) return NSA_ERR_UNSUPPORTED;
     if (a.kv_dtype == NSA_DT_E4M3 && (a.d_latent % 128 != 0 || a.d_rope % 2 != 0)) return NSA_ERR_UNSUPPORTED;
-    if (a.H > 65535 || a.page_size > (1 << 24) || a.max_row_len > (1 << 30) ||
-        (int64_t)a.rows_per_req * a.H > (1 << 20) || (int64_t)a.R * a.H > 2147483647LL ||
+    if (!paged_mla_sizes_ok(a.R, a.rows_per_req, a.H, a.max_row_len) || a.page_size > (1 << 24) ||
         a.num_pages > 2147483647LL / a.page_size)
         return NSA_ERR_UNSUPPORTED;
     if (a.R == 0) return NSA_OK;

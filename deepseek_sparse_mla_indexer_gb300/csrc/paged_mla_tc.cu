@@ -1095,19 +1095,31 @@ size_t paged_mla_tc_workspace_bytes(nsa_dtype q_dtype, nsa_dtype kv_dtype, int R
                                     int d_rope, int max_row_len)
 {
     if (q_dtype != NSA_DT_BF16 || (kv_dtype != NSA_DT_BF16 && kv_dtype != NSA_DT_E4M3) || d_latent != kPtDl ||
-        d_rope != kPtDr || R <= 0 || rows_per_req <= 0 || R % rows_per_req != 0 || H <= 0 || max_row_len <= 0)
+        d_rope != kPtDr || R <= 0 || rows_per_req <= 0 || R % rows_per_req != 0 || H <= 0 || max_row_len <= 0 ||
+        !paged_mla_sizes_ok(R, rows_per_req, H, max_row_len))
         return 0;
-    const Plan q = make_plan(kv_dtype == NSA_DT_E4M3, R, rows_per_req, H, max_row_len, current_sm_count());
-    return q.head_bytes + q.ml_bytes + q.part_bytes + q.scratch_bytes;
+    // A bound on make_plan's sizes that grows with each argument, which they do not (fp8: clusters of four
+    // need less scratch than pairs), so that a workspace for the largest shape of a loop serves all of it.
+    const size_t units = (size_t)R * (size_t)ceil_div(H, 16);  // at least the group sets of all requests
+    const size_t work = units * (size_t)ceil_div(max_row_len, kPtTok);
+    const int sms = current_sm_count();
+    const size_t most = (size_t)(sms > kMaxTeam ? sms : kMaxTeam), ctas = work < most ? work : most;
+    const int64_t cols = (int64_t)rows_per_req * H;
+    const size_t slots = ctas * 2 * (size_t)(cols < kCols ? cols : kCols);
+    static_assert(scr_slots(2) >= scr_slots(4) / 2, "a CTA of a pair has the larger part of a scratch");
+    return units * sizeof(int4) + (slots * sizeof(float2) + 15) / 16 * 16 + slots * kPtDl * sizeof(float) +
+           (kv_dtype == NSA_DT_E4M3 && cols > 32 ? ctas * (scr_slots(2) / 2) * kScrTile : 0);
 }
 
-nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse, void *workspace, cudaStream_t stream)
+nsa_status paged_mla_tc_try_launch(const PagedMlaArgs &a, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                   cudaStream_t stream)
 {
     if (!paged_tc_applicable(a)) return NSA_ERR_UNSUPPORTED;
     const int sms = current_sm_count();
     if (sms <= 0) return NSA_ERR_CUDA;
     const bool fp8 = a.kv_dtype == NSA_DT_E4M3;
     const Plan q = make_plan(fp8, a.R, a.rows_per_req, a.H, a.max_row_len, sms);
+    if (q.head_bytes + q.ml_bytes + q.part_bytes + q.scratch_bytes > workspace_bytes) return NSA_ERR_INVALID_ARG;
     if ((int64_t)(a.R / a.rows_per_req) * q.mult * (ceil_div(a.max_row_len, kPtTok) + piece_of(q.rows)) / q.teams >= kMaxShare)
         return NSA_ERR_UNSUPPORTED;
     AParams p;

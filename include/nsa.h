@@ -600,7 +600,9 @@ nsa_status nsa_paged_mla(nsa_dtype q_dtype, nsa_dtype kv_dtype, const void *q_no
 
 /* Scratch bytes nsa_paged_mla needs on the current device for this problem (0 if
  * none, and for arguments the call would refuse).  A workspace serves every call
- * that needs no more than its size. */
+ * that needs no more than its size; for the same types the size does not shrink
+ * when R, rows_per_req, H or max_row_len grow, so one for the largest shape of a
+ * serving loop serves the whole loop. */
 size_t nsa_paged_mla_workspace_bytes(nsa_dtype q_dtype, nsa_dtype kv_dtype, int R, int rows_per_req, int H,
                                      int d_latent, int d_rope, int max_row_len);
 
