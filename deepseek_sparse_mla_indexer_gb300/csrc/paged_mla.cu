@@ -110,7 +110,8 @@ paged_mla_simt_kernel(PagedMlaArgs p, int HG, void *out, float *lse)
         const int e = threadIdx.x + i * kThreads;
         if (i < n_acc && e < hg * p.d_latent) {
             const int h = e / p.d_latent, d = e - h * p.d_latent;
-            const float l = l_run[h], v = l > 0.f ? acc[i] / l : l == l ? 0.f : l;
+            // all scores -inf, or none: acc holds zeros, or the NaN of 0 x inf
+            const float l = l_run[h], v = l > 0.f ? acc[i] / l : l == l ? acc[i] : l;
             const int64_t o = ((int64_t)r * p.H + h0 + h) * p.d_latent + d;
             if (QDT == NSA_DT_BF16)
                 ((__nv_bfloat16 *)out)[o] = __float2bfloat16_rn(v);  // the result's type

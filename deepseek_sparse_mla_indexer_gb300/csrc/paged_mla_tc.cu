@@ -54,6 +54,9 @@ constexpr uint32_t kKvBytes = 9 * kPtBlk;
 constexpr uint32_t kColS = 256;           // S^T behind O^T's four blocks
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f;          // log2 units
+// The running maximum of a column that has seen no score yet: finite, so that a score of -inf gets the
+// exponent -inf (weight 0) from it and not NaN, and so low that any other score asks for a new maximum.
+constexpr float kNoMax = -3.402823466e38f;
 constexpr int kMaxTeam = 8;
 // How the tile's rows come: a bf16 cache by TMA; raw fp8 rows by TMA into slots beside the
 // tile and expanded from there; or fp8 rows expanded into the CTA's scratch in global memory
@@ -80,6 +83,7 @@ struct AShared {
     float inv[kCols];                 // 1 / sum; 0: no key
     int len[kCols];                   // positions the column's row sees
     int min_len[4];                   // shortest of all the CTA's columns, one copy a group
+    int odd0[4], odd1[4];             // first and last position of the piece whose row was made finite (one copy a group)
     uint64_t pair_full[5];            // block pair m of the tile landed (m = 4: the rope block)
     uint64_t pair_free[5];            // its readers are done (m = 4: every product of the tile)
     uint64_t q_full, q_empty, s_full, p_full, o_fin;
@@ -202,6 +206,29 @@ __device__ __forceinline__ void tmem_stg(uint32_t taddr, const uint32_t (&r)[G])
     if constexpr (G == 32) tmem_st32(taddr, r);
     else if constexpr (G == 16) tmem_st16(taddr, r);
     else tmem_st8(taddr, r);
+}
+
+// Which columns of a group (`len`: what they see) see a value that is not finite among components d, d + 128,
+// d + 256 and d + 384 of positions pos0 .. pos1: bit 16 m + c for component d + 128 m and column c.  Not
+// inlined: it is rarely called, and its registers would be taken from the tile loop.
+template <int KDT, int G>
+__device__ __noinline__ uint64_t hidden_values(const uint8_t *kv, int64_t num_pages, int ps, const int32_t *pt, int pos0,
+                                               int pos1, const int *len, int d)
+{
+    uint64_t bits = 0;
+#pragma unroll 1
+    for (int pos = pos0; pos <= pos1; ++pos) {
+        const int page = __ldg(pt + pos / ps);
+        if (page < 0 || page >= num_pages) continue;
+        const int64_t slot = (int64_t)page * ps + pos % ps;
+        uint32_t see = 0;
+        for (int c = 0; c < G; ++c) see |= (pos < len[c] ? 1u : 0u) << c;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            if (not_finite(__float_as_uint(load_cache<KDT>(kv, slot, m * 128 + d, kPtDl, kPtDr))))
+                bits |= (uint64_t)see << (16 * m);
+    }
+    return bits;
 }
 
 // CL: CTAs of a cluster, which share the expansion of their tiles; NC: columns of the CTA's products (16, 32 or 64).
@@ -584,11 +611,15 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                         shortest = min(shortest, len);
                         if (cc >= cb && cc < cb + kGrp) {
                             sm->len[cc] = len;
-                            sm->m_run[cc] = -INFINITY;
+                            sm->m_run[cc] = kNoMax;
                         }
                     }
                     shortest = __reduce_min_sync(0xffffffffu, shortest);
-                    if (lane == 0) sm->min_len[grp] = shortest;
+                    if (lane == 0) {
+                        sm->min_len[grp] = shortest;
+                        sm->odd0[grp] = 0x7fffffff;
+                        sm->odd1[grp] = -1;
+                    }
                 }
                 bar_sync(bar, 128);
                 const int min_len = sm->min_len[grp];
@@ -651,7 +682,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                             const int c = cb + et;
                             const float cm = fmaxf(fmaxf(sm->red[0][c], sm->red[1][c]), fmaxf(sm->red[2][c], sm->red[3][c]));
                             const float mo = sm->m_run[c], mn = fmaxf(mo, cm);
-                            sm->alpha[c] = mn == -INFINITY ? 1.f : exp2f(mo - mn);
+                            sm->alpha[c] = exp2f(mo - mn);
                             sm->m_run[c] = mn;
                         }
                         bar_sync(bar, 128);
@@ -689,10 +720,15 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                     // A weight of 0 does not hide what is not finite, so it is taken out of this group's share
                     // of the key's latent blocks (S^T has read them): all of a row that is not there, and from
                     // a row that only some columns see the values that are not finite.  Such a value makes every
-                    // column's score of the key not finite, which is how it is noticed and what the columns
-                    // that see the key get it from.
+                    // column's score of the key not finite, which is how it is noticed.  The columns that see the
+                    // key get NaN sums from a score of NaN or +inf; what 0 x inf gives those whose score is -inf
+                    // is put back at the end of the piece.
                     const bool absent = ROWS == kBf16Rows && !valid;
                     if (absent || (odd && valid && pos >= min_len)) {
+                        if (!absent) {
+                            atomicMin(&sm->odd0[grp], pos);
+                            atomicMax(&sm->odd1[grp], pos);
+                        }
                         for (int m = 0; m < 4; ++m) mbar_wait(&sm->pair_full[m], i & 1, kPtWait);
 #pragma unroll 1
                         for (int c = grp * (8 / kGroups); c < (grp + 1) * (8 / kGroups); ++c) {
@@ -726,6 +762,7 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 const float part = over_lanes(ls, lane, [](float x, float y) { return x + y; });
                 if (lane < kGrp) sm->red[quad][cb + lane] = part;
                 bar_sync(bar, 128);
+                const int odd0 = sm->odd0[grp], odd1 = sm->odd1[grp];
                 const bool whole = s.whole();
                 const int nc = min(kGrp, p.cols - col0 - cb);  // real columns of this group (may be <= 0)
                 const int64_t row0 = (int64_t)s.b * p.cols + col0 + cb;
@@ -749,10 +786,20 @@ paged_mla_tc_kernel(AParams p, const __grid_constant__ CUtensorMap qn_map, const
                 }
                 if (bar_red_or(bar, 128, !ok)) { ok = false; break; }
                 tc_fence_after();
+                uint64_t not_fin = 0;  // of rows that were made finite (rare)
+                if (odd1 >= 0)
+                    not_fin = hidden_values<ROWS == kBf16Rows ? NSA_DT_BF16 : NSA_DT_E4M3, kGrp>(
+                        p.t.kv, p.t.num_pages, p.t.ps, pt, odd0, min(odd1, s.len - 1), sm->len + cb, key);
 #pragma unroll 1
                 for (int m = 0; m < 4; ++m) {
                     uint32_t v[kGrp];
                     tmem_ldg<kGrp>(lanes + m * NC + cb, v);
+                    if (not_fin) {
+#pragma unroll
+                        for (int c = 0; c < kGrp; ++c)
+                            if (not_fin >> (16 * m + c) & 1) v[c] = 0x7fffffffu;
+                    }
+                    __syncwarp();
                     if (whole) {
                         __nv_bfloat16 *o = p.out + row0 * kPtDl + m * 128 + key;
 #pragma unroll
@@ -937,8 +984,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_mla_join_kernel(AParams p)
         const int64_t s = slot_of(q);
         const float2 ml = p.part_ml[s];
         const float4 *src = reinterpret_cast<const float4 *>(p.part + s * kPtDl) + lane;
-        // a share whose keys were all masked has maximum -inf and zeros
-        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+        const float w = exp2f(ml.x - m);  // a share without a score: kNoMax, 0 and zeros (NaN for 0 x inf)
         l += w * ml.y;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {

@@ -578,6 +578,10 @@ nsa_status nsa_local_attention(const void *q_dev, int64_t q_ld, const void *k_ca
  *                      nothing is kept in it between calls
  * Positions at or past row_len are never used, whatever they hold: a NaN or infinity
  * at a position that only some rows of a request see reaches those rows alone.
+ * A score of -inf has weight 0, as in the formula: lse is that of the other
+ * positions, and a component of out is NaN (0 x inf) where the position's latent is
+ * not finite.  A row all of whose scores are -inf has lse -inf and zeros elsewhere.
+ * A score of NaN or +inf makes the row's out and lse NaN.
  * Returns NSA_ERR_INVALID_ARG for R not a multiple of rows_per_req, a bad size, a
  * NULL or misaligned buffer, or too small a workspace; NSA_ERR_UNSUPPORTED for a
  * dtype combination or size the kernels do not take (more than 2^30 positions,
