@@ -406,13 +406,14 @@ __device__ __forceinline__ void describe(const CompactParams &p, Chunk &k, int t
                 const int q = keep[i], before = i > 0 ? keep[i - 1] : -1;
                 from = q;
                 if (q < i || q >= old || before >= q) {
-                    set_status(p.status, NSA_ERR_BOUNDS);  // not an ascending list of positions: the row stays
+                    set_status(p.status, NSA_ERR_BOUNDS);  // not an ascending list of positions: likewise
                     from = i;
                 } else if (q != i && p.n_arrays > 0) {
                     const int sp = q / p.page_size, dp = i / p.page_size;
                     const int32_t ps = pt[sp], pd = pt[dp];
                     if (ps < 0 || ps >= p.num_pages || pd < 0 || pd >= p.num_pages) {
-                        set_status(p.status, NSA_ERR_BOUNDS);
+                        set_status(p.status, NSA_ERR_BOUNDS);  // a page outside the cache: the row stays, and its total
+                        from = i;
                     } else {
                         s = ps * p.page_size + (q - sp * p.page_size);
                         d = pd * p.page_size + (i - dp * p.page_size);

@@ -664,9 +664,12 @@ nsa_status nsa_evict_select(const float *total_dev, int64_t total_ld, const int3
  *                   the call clears what it uses.  Calls that may overlap on the GPU need
  *                   workspaces of their own
  * NSA_ERR_UNSUPPORTED when the rows of one position take more than 24 KB.  Device
- * errors (NSA_ERR_BOUNDS): lengths out of range (the request is left as it is), a
- * keep list that does not ascend within old_len or a page outside the cache (that
- * row stays); NSA_ERR_TIMEOUT if a bounded wait between blocks runs out (the
+ * errors (NSA_ERR_BOUNDS): lengths out of range (the request is left as it is); a
+ * source or destination page outside the cache (that row and its total stay); a keep
+ * list that does not ascend within old_len (an entry at or past old_len, or not above
+ * the one before it, leaves its row and total as they are; which rows of that request
+ * the entries around one that goes back take is then not specified, and no other
+ * request is touched); NSA_ERR_TIMEOUT if a bounded wait between blocks runs out (the
  * request's rows are then partly moved).
  */
 nsa_status nsa_evict_compact(int B, const int32_t *keep_dev, int64_t keep_ld, int budget, const int32_t *new_len_dev,
