@@ -19,6 +19,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 32;  // keys per CTA, one per lane
 constexpr int kHG = 16;    // heads staged at once
+constexpr int kMaxSmem = 224 * 1024;  // dynamic; the kernel is allowed all of it, whatever a call needs
 
 // One CTA per (request, 32 keys).  Every warp takes every eighth head of each
 // row; the warps' sums are joined in a fixed order, so the result does not
@@ -87,9 +88,9 @@ nsa_status launch_simt(const PagedMlaArgs &a, const float *lse, float *total, in
     const int64_t dq = (int64_t)a.d_latent + a.d_rope;
     const int64_t smem = (int64_t)sizeof(float) * (kTile * (dq + 1) + kHG * dq);
     const int64_t blocks = ceil_div(a.max_row_len, kTile) * (a.R / a.rows_per_req);
-    if (smem > 224 * 1024 || blocks > 2147483647LL) return NSA_ERR_UNSUPPORTED;
-    auto k = key_weights_simt_kernel<QDT, KDT>;
-    NSA_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    if (smem > kMaxSmem || blocks > 2147483647LL) return NSA_ERR_UNSUPPORTED;
+    constexpr auto k = key_weights_simt_kernel<QDT, KDT>;
+    NSA_CUDA_TRY(max_dynamic_smem<k>(kMaxSmem));
     k<<<(unsigned)blocks, kThreads, (size_t)smem, stream>>>(a, lse, total, total_ld);
     return launch_status();
 }

@@ -90,7 +90,9 @@ inline int current_sm_count()
     return n > 0 ? n : 0;
 }
 
-// Allows `Kern` that much dynamic shared memory, asked of the runtime once per device.
+// Allows `Kern` that much dynamic shared memory, asked of the runtime once per device.  Every call for
+// a kernel passes the same, largest, size: what one host thread allows for its launch would otherwise
+// be lowered by another's between the two (a launch beyond what is allowed is refused).
 template <auto Kern>
 inline cudaError_t max_dynamic_smem(int bytes)
 {

@@ -20,6 +20,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 32;    // keys per tile (one per lane in the softmax)
 constexpr int kMaxAcc = 32;  // accumulator entries per thread: heads per block * d_latent <= 8192
+constexpr int kMaxSmem = 226 * 1024;  // dynamic; the kernel is allowed all of it, whatever a call needs
 
 // One CTA per (row, group of HG heads): a streaming softmax over tiles of 32
 // keys held in shared memory as fp32.  Simple and exact in fp32; bound by
@@ -133,9 +134,9 @@ nsa_status launch_simt(const PagedMlaArgs &a, void *out, float *lse, cudaStream_
     if (HG * (int64_t)a.d_latent > kThreads * kMaxAcc) return NSA_ERR_UNSUPPORTED;
     const int64_t ld = (int64_t)a.d_latent + a.d_rope + 1;
     const int64_t smem = (int64_t)sizeof(float) * ((HG + kTile) * ld + HG * kTile + 3 * HG);
-    if (smem > 226 * 1024) return NSA_ERR_UNSUPPORTED;
-    auto k = paged_mla_simt_kernel<QDT, KDT>;
-    NSA_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    if (smem > kMaxSmem) return NSA_ERR_UNSUPPORTED;
+    constexpr auto k = paged_mla_simt_kernel<QDT, KDT>;
+    NSA_CUDA_TRY(max_dynamic_smem<k>(kMaxSmem));
     k<<<dim3((unsigned)a.R, (unsigned)ceil_div(a.H, HG)), kThreads, (size_t)smem, stream>>>(a, HG, out, lse);
     return launch_status();
 }
