@@ -18,19 +18,24 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 32;  // keys per CTA, one per lane
-constexpr int kHG = 16;    // heads staged at once
-constexpr int kMaxSmem = 224 * 1024;  // dynamic; the kernel is allowed all of it, whatever a call needs
+constexpr int kHG = 16;    // heads staged at once, at most
+constexpr int kMaxSmem = kPagedSimtSmem;  // dynamic; the kernel is allowed all of it, whatever a call needs
+
+constexpr int64_t smem_of(int heads, int dq)
+{
+    return (int64_t)sizeof(float) * (kTile * (int64_t)(dq + 1) + (int64_t)heads * dq);
+}
+static_assert(smem_of(1, kPagedMaxRow) <= kMaxSmem, "one head fits");
 
 // One CTA per (request, 32 keys).  Every warp takes every eighth head of each
 // row; the warps' sums are joined in a fixed order, so the result does not
 // depend on scheduling.
 template <int QDT, int KDT>
-__global__ void __launch_bounds__(kThreads) key_weights_simt_kernel(PagedMlaArgs p, const float *lse, float *total,
-                                                                    int64_t total_ld)
+__global__ void __launch_bounds__(kThreads) key_weights_simt_kernel(PagedMlaArgs p, int HG, const float *lse,
+                                                                    float *total, int64_t total_ld)
 {
     extern __shared__ float smem[];
     __shared__ int64_t slot[kTile];
-    __shared__ float part[kThreads / 32][kTile];
     const int dq = p.d_latent + p.d_rope, ld = dq + 1;
     float *ks = smem, *qs = ks + kTile * ld;
     const int per = (p.max_row_len + kTile - 1) / kTile, b = blockIdx.x / per, j0 = (blockIdx.x - b * per) * kTile;
@@ -54,8 +59,8 @@ __global__ void __launch_bounds__(kThreads) key_weights_simt_kernel(PagedMlaArgs
         const int64_t r = (int64_t)b * p.rows_per_req + i;
         const int L = p.row_len[r];
         if (L < 0 || L > p.max_row_len) continue;
-        for (int h0 = 0; h0 < p.H; h0 += kHG) {
-            const int hg = min(kHG, p.H - h0);
+        for (int h0 = 0; h0 < p.H; h0 += HG) {
+            const int hg = min(HG, p.H - h0);
             __syncthreads();
             for (int e = threadIdx.x; e < hg * dq; e += kThreads) {
                 const int h = e / dq, d = e - h * dq;
@@ -73,11 +78,13 @@ __global__ void __launch_bounds__(kThreads) key_weights_simt_kernel(PagedMlaArgs
             }
         }
     }
-    part[warp][lane] = sum;
+    float *part = smem;  // [warps][kTile], where the keys were
+    __syncthreads();
+    part[warp * kTile + lane] = sum;
     __syncthreads();
     if (threadIdx.x < kTile && slot[threadIdx.x] >= 0) {
         float w = 0.f;
-        for (int k = 0; k < kThreads / 32; ++k) w += part[k][threadIdx.x];
+        for (int k = 0; k < kThreads / 32; ++k) w += part[k * kTile + threadIdx.x];
         total[b * total_ld + j0 + threadIdx.x] += w;
     }
 }
@@ -85,13 +92,16 @@ __global__ void __launch_bounds__(kThreads) key_weights_simt_kernel(PagedMlaArgs
 template <int QDT, int KDT>
 nsa_status launch_simt(const PagedMlaArgs &a, const float *lse, float *total, int64_t total_ld, cudaStream_t stream)
 {
-    const int64_t dq = (int64_t)a.d_latent + a.d_rope;
-    const int64_t smem = (int64_t)sizeof(float) * (kTile * (dq + 1) + kHG * dq);
+    const int dq = a.d_latent + a.d_rope;
+    int HG = a.H < kHG ? a.H : kHG;
+    while (HG > 1 && smem_of(HG, dq) > kMaxSmem) --HG;
+    const int64_t part = (int64_t)sizeof(float) * kThreads;
+    const int64_t smem = smem_of(HG, dq) > part ? smem_of(HG, dq) : part;
     const int64_t blocks = ceil_div(a.max_row_len, kTile) * (a.R / a.rows_per_req);
-    if (smem > kMaxSmem || blocks > 2147483647LL) return NSA_ERR_UNSUPPORTED;
+    if (blocks > 2147483647LL) return NSA_ERR_UNSUPPORTED;
     constexpr auto k = key_weights_simt_kernel<QDT, KDT>;
     NSA_CUDA_TRY(max_dynamic_smem<k>(kMaxSmem));
-    k<<<(unsigned)blocks, kThreads, (size_t)smem, stream>>>(a, lse, total, total_ld);
+    k<<<(unsigned)blocks, kThreads, (size_t)smem, stream>>>(a, HG, lse, total, total_ld);
     return launch_status();
 }
 

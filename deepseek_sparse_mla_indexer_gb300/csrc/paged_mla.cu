@@ -20,7 +20,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 32;    // keys per tile (one per lane in the softmax)
 constexpr int kMaxAcc = 32;  // accumulator entries per thread: heads per block * d_latent <= 8192
-constexpr int kMaxSmem = 226 * 1024;  // dynamic; the kernel is allowed all of it, whatever a call needs
+constexpr int kMaxSmem = kPagedSimtSmem;  // dynamic; the kernel is allowed all of it, whatever a call needs
+
+constexpr int64_t smem_of(int heads, int dq)
+{
+    return (int64_t)sizeof(float) * ((heads + kTile) * (int64_t)(dq + 1) + heads * kTile + 3 * heads);
+}
+static_assert(smem_of(1, kPagedMaxRow) <= kMaxSmem && kPagedMaxRow <= kThreads * kMaxAcc, "one head fits");
 
 // One CTA per (row, group of HG heads): a streaming softmax over tiles of 32
 // keys held in shared memory as fp32.  Simple and exact in fp32; bound by
@@ -129,12 +135,10 @@ paged_mla_simt_kernel(PagedMlaArgs p, int HG, void *out, float *lse)
 template <int QDT, int KDT>
 nsa_status launch_simt(const PagedMlaArgs &a, void *out, float *lse, cudaStream_t stream)
 {
+    // as many heads as the accumulators and shared memory hold: one at least (kPagedMaxRow)
     int HG = a.H < 16 ? a.H : 16;
-    while (HG > 1 && HG * (int64_t)a.d_latent > kThreads * kMaxAcc) --HG;
-    if (HG * (int64_t)a.d_latent > kThreads * kMaxAcc) return NSA_ERR_UNSUPPORTED;
-    const int64_t ld = (int64_t)a.d_latent + a.d_rope + 1;
-    const int64_t smem = (int64_t)sizeof(float) * ((HG + kTile) * ld + HG * kTile + 3 * HG);
-    if (smem > kMaxSmem) return NSA_ERR_UNSUPPORTED;
+    while (HG > 1 && (HG * a.d_latent > kThreads * kMaxAcc || smem_of(HG, a.d_latent + a.d_rope) > kMaxSmem)) --HG;
+    const int64_t smem = smem_of(HG, a.d_latent + a.d_rope);
     constexpr auto k = paged_mla_simt_kernel<QDT, KDT>;
     NSA_CUDA_TRY(max_dynamic_smem<k>(kMaxSmem));
     k<<<dim3((unsigned)a.R, (unsigned)ceil_div(a.H, HG)), kThreads, (size_t)smem, stream>>>(a, HG, out, lse);

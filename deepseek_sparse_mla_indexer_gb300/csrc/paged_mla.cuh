@@ -22,6 +22,10 @@ struct PagedMlaArgs {
     int32_t *status;
 };
 
+// The CUDA-core kernels hold 32 cache rows and at least one head's query in shared memory as fp32.
+constexpr int kPagedSimtSmem = 226 * 1024;
+constexpr int kPagedMaxRow = 1751;  // d_latent + d_rope
+
 // Sizes that the kernels index with 32 bits.
 inline bool paged_mla_sizes_ok(int R, int rows_per_req, int H, int max_row_len)
 {
@@ -42,6 +46,7 @@ inline nsa_status check_paged_mla(const PagedMlaArgs &a)
         (a.q_dtype == NSA_DT_BF16 && (a.kv_dtype == NSA_DT_BF16 || a.kv_dtype == NSA_DT_E4M3));
     if (!combo_ok) return NSA_ERR_UNSUPPORTED;
     if (a.kv_dtype == NSA_DT_E4M3 && (a.d_latent % 128 != 0 || a.d_rope % 2 != 0)) return NSA_ERR_UNSUPPORTED;
+    if ((int64_t)a.d_latent + a.d_rope > kPagedMaxRow) return NSA_ERR_UNSUPPORTED;
     if (!paged_mla_sizes_ok(a.R, a.rows_per_req, a.H, a.max_row_len) || a.page_size > (1 << 24) ||
         a.num_pages > 2147483647LL / a.page_size)
         return NSA_ERR_UNSUPPORTED;

@@ -585,8 +585,8 @@ nsa_status nsa_local_attention(const void *q_dev, int64_t q_ld, const void *k_ca
  * Returns NSA_ERR_INVALID_ARG for R not a multiple of rows_per_req, a bad size, a
  * NULL or misaligned buffer, or too small a workspace; NSA_ERR_UNSUPPORTED for a
  * dtype combination or size the kernels do not take (more than 2^30 positions,
- * 2^31 slots or query heads, d_latent beyond 8192, E4M3 with d_latent % 128 != 0 or
- * odd d_rope).
+ * 2^31 slots or query heads, d_latent + d_rope beyond 1751, E4M3 with d_latent % 128
+ * != 0 or odd d_rope).
  * The 512 + 64 shape with BF16 q runs on the tensor cores (tcgen05) when page_size is a
  * multiple of 8, q and the cache are 16-byte aligned, and the query heads follow one
  * another at one pitch (ld_r == H * ld_h, ld_h a multiple of 8: contiguous q, or the two
