@@ -434,6 +434,7 @@ def nsa_local_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
 # ---------------------------------------------------------------- dense paged MLA attention
 
 _Q_TYPES = {DT_F32: torch.float32, DT_BF16: torch.bfloat16}
+_CACHE_TYPES = {**_Q_TYPES, DT_E4M3: torch.float8_e4m3fn}
 
 
 def _paged_q(q_dtype: int, q_nope: torch.Tensor, q_rope: torch.Tensor):
@@ -455,7 +456,11 @@ def _paged_q(q_dtype: int, q_nope: torch.Tensor, q_rope: torch.Tensor):
 
 
 def _paged_cache(kv_dtype: int, kv: torch.Tensor, page_size: int, d_latent: int, d_rope: int) -> int:
-    """Checks a cache of [slots, row] (or [pages, page_size, row]) and returns its page count."""
+    """Checks a cache of [slots, row] (or [pages, page_size, row]; of its own type, or raw bytes in an
+    integer type) and returns its page count."""
+    dtype = kv.dtype
+    if dtype is not _CACHE_TYPES.get(kv_dtype) and dtype.is_floating_point:
+        raise ValueError(f"the cache must be {_CACHE_TYPES.get(kv_dtype)} (or bytes) for this kv_dtype, got {dtype}")
     if kv_dtype == DT_E4M3:
         want = d_latent + 4 * (d_latent // 128) + 2 * d_rope
     else:
@@ -470,18 +475,34 @@ def _paged_cache(kv_dtype: int, kv: torch.Tensor, page_size: int, d_latent: int,
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# without the check for an initialised CUDA that a CUDA tensor makes superfluous
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch_on(stream, *tensors: Optional[torch.Tensor]):
     """The stream handle of a call on these tensors, which must live on the current device (the
     library launches there)."""
-    dev = torch.cuda.current_device() if tensors[0].is_cuda else -1
+    dev = _current_device() if tensors[0].is_cuda else -1
     for t in tensors:
         if t is not None and (t.get_device() != dev or dev < 0):
             raise ValueError(f"expected CUDA tensors on the current device, got one on {t.device}")
     if stream is None and _raw_stream is not None:  # the current stream without building its object
         return _raw_stream(dev)
     return _stream(stream)
+
+
+def _scratch(t: Optional[torch.Tensor]) -> int:
+    """The bytes of a workspace."""
+    if t is None:
+        return 0
+    if not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return t.numel() * t.element_size()
+
+
+def _status_word(t: Optional[torch.Tensor]) -> None:
+    if t is not None and (t.dtype is not torch.int32 or t.numel() < 1):
+        raise ValueError(f"status must be an int32 word, got shape {tuple(t.shape)} of {t.dtype}")
 
 
 def _at(t: Optional[torch.Tensor]):
@@ -535,12 +556,13 @@ def nsa_paged_mla(q_dtype: int, kv_dtype: int, q_nope: torch.Tensor, q_rope: tor
     if tuple(out.shape) != (R, H, dl) or tuple(lse.shape) != (R, H) or lse.dtype != torch.float32 or \
             out.dtype != q_nope.dtype or not out.is_contiguous() or not lse.is_contiguous():
         raise ValueError("out must be [R, H, d_latent] in q's type and lse float32 [R, H], both contiguous")
+    q_args, pt_ld, ws_bytes = _paged_q(q_dtype, q_nope, q_rope), _table_ld(pt, max_row_len, page_size), _scratch(workspace)
+    _i32("row_len", row_len, R)
+    _status_word(status)
     handle = _launch_on(stream, q_nope, q_rope, kv, page_table, row_len, out, lse, workspace, status)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    rc = load().nsa_paged_mla(q_dtype, kv_dtype, *_paged_q(q_dtype, q_nope, q_rope), _at(kv), pages, page_size, _at(pt),
-                              _table_ld(pt, max_row_len, page_size), _at(_i32("row_len", row_len, R)), R, rows_per_req,
-                              H, dl, dr, max_row_len, float(sm_scale), _at(out), _at(lse), _at(workspace), ws_bytes,
-                              _at(status), handle)
+    rc = load().nsa_paged_mla(q_dtype, kv_dtype, *q_args, _at(kv), pages, page_size, _at(pt), pt_ld, _at(row_len), R,
+                              rows_per_req, H, dl, dr, max_row_len, float(sm_scale), _at(out), _at(lse), _at(workspace),
+                              ws_bytes, _at(status), handle)
     _check("nsa_paged_mla", rc)
 
 
@@ -561,10 +583,12 @@ def nsa_mla_key_weights(q_dtype: int, kv_dtype: int, q_nope: torch.Tensor, q_rop
     pt = _table(page_table, B)
     if tuple(lse.shape) != (R, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [R, H]")
+    q_args, pt_ld = _paged_q(q_dtype, q_nope, q_rope), _table_ld(pt, max_row_len, page_size)
     total_ld = _total_ld(total, B, max_row_len)
+    _i32("row_len", row_len, R)
+    _status_word(status)
     handle = _launch_on(stream, q_nope, q_rope, kv, page_table, row_len, lse, total, status)
-    rc = load().nsa_mla_key_weights(q_dtype, kv_dtype, *_paged_q(q_dtype, q_nope, q_rope), _at(kv), pages, page_size,
-                                    _at(pt), _table_ld(pt, max_row_len, page_size), _at(_i32("row_len", row_len, R)), R,
+    rc = load().nsa_mla_key_weights(q_dtype, kv_dtype, *q_args, _at(kv), pages, page_size, _at(pt), pt_ld, _at(row_len), R,
                                     rows_per_req, H, dl, dr, max_row_len, float(sm_scale), _at(lse), _at(total),
                                     total_ld, _at(status), handle)
     _check("nsa_mla_key_weights", rc)
@@ -583,10 +607,13 @@ def nsa_evict_select(total: torch.Tensor, lens: torch.Tensor, max_len: int, sink
     B = lens.shape[0]
     if keep.dtype != torch.int32 or keep.dim() != 2 or keep.shape[0] != B or keep.shape[1] < budget:
         raise ValueError(f"keep must be int32 [{B}, >= {budget}], got shape {tuple(keep.shape)} of {keep.dtype}")
-    total_ld = _total_ld(total, B, max_len)
+    total_ld, keep_ld = _total_ld(total, B, max_len), _ld(keep)
+    _i32("lens", lens, B)
+    _i32("new_len", new_len, B)
+    _status_word(status)
     handle = _launch_on(stream, total, lens, keep, new_len, status)
-    rc = load().nsa_evict_select(_at(total), total_ld, _at(_i32("lens", lens, B)), B, max_len, sinks, recent, budget,
-                                 _at(keep), _ld(keep), _at(_i32("new_len", new_len, B)), _at(status), handle)
+    rc = load().nsa_evict_select(_at(total), total_ld, _at(lens), B, max_len, sinks, recent, budget, _at(keep), keep_ld,
+                                 _at(new_len), _at(status), handle)
     _check("nsa_evict_select", rc)
 
 
@@ -617,12 +644,15 @@ def nsa_evict_compact(keep: torch.Tensor, new_len: torch.Tensor, old_len: torch.
             raise ValueError(f"the arrays must be contiguous with one first dimension of whole pages of {page_size}, "
                              f"got shape {tuple(a.shape)}")
     total_ld = 0 if total is None else _total_ld(total, B, max_len)
+    keep_ld, pt_ld, ws_bytes = _ld(keep), _table_ld(pt, max_len, page_size), _scratch(workspace)
+    _i32("new_len", new_len, B)
+    _i32("old_len", old_len, B)
+    _status_word(status)
     handle = _launch_on(stream, keep, new_len, old_len, page_table, total, workspace, status, *arrays)
     n = len(arrays)
     ptrs = (C.c_void_p * max(1, n))(*[a.data_ptr() for a in arrays])
     nb = (C.c_int64 * max(1, n))(*[a.numel() * a.element_size() // slots for a in arrays])
-    rc = load().nsa_evict_compact(B, _at(keep), _ld(keep), keep.shape[1], _at(_i32("new_len", new_len, B)),
-                                  _at(_i32("old_len", old_len, B)), max_len, _at(pt), _table_ld(pt, max_len, page_size),
-                                  page_size, slots // page_size, n, ptrs, nb, _at(total), total_ld, _at(workspace),
-                                  workspace.numel() * workspace.element_size(), _at(status), handle)
+    rc = load().nsa_evict_compact(B, _at(keep), keep_ld, keep.shape[1], _at(new_len), _at(old_len), max_len, _at(pt),
+                                  pt_ld, page_size, slots // page_size, n, ptrs, nb, _at(total), total_ld, _at(workspace),
+                                  ws_bytes, _at(status), handle)
     _check("nsa_evict_compact", rc)
