@@ -29,8 +29,9 @@ using namespace sm100;
 // CTAs before it: positions above the threshold, and of those equal to it the
 // lowest ones.  Keys stay in shared memory (slices up to 40 K; longer ones are read
 // again from L2).  Whole numbers throughout: the result does not depend on
-// scheduling.  Bound by the latency of its dozen dependent steps, not by its bytes:
-// 31 us for 16 requests of 50000 .. 131072 totals (7.5 MB), 13 - 16 us for one of 4099.
+// scheduling.  Not bound by its bytes: 31 us for 16 requests of 50000 .. 131072 totals
+// (7.5 MB), whose 64 CTAs leave 88 SMs idle and walk 32 keys a thread four times between a
+// dozen barriers.  One request of 4099 takes 14 - 17 us, the host's part of a call; 8 us in a graph.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMaxCluster = 8;         // the portable limit
@@ -309,7 +310,7 @@ int select_clusters(int nc)
 // copies (a thread issues one copy a row and array), and several CTAs share an SM.
 // Measured (GB300): 4 requests of 65536 .. 131072 positions cut to 50000, bf16 rows, indexer keys
 // and scales (518 MB moved): 105 us, 4.9 TB/s, 73 % of the copy rate; 32 requests of 4096 .. 32768
-// cut to 5001, fp8 rows (232 MB): 57 us, 60 %; one of 4099: 15 us.
+// cut to 5001, fp8 rows (232 MB): 57 us, 60 %; one of 4099: 16 us (12 in a graph).
 constexpr int kMaxArrays = 8;
 constexpr int kCpThreads = 256;          // warps 0..3 move a chunk, warps 4..7 describe the next one
 constexpr int kMovers = 128;

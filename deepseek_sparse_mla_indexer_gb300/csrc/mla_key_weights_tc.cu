@@ -21,12 +21,12 @@
 // leaves less room).
 //
 // Measured (GB300, a pass among others):
-//   32 requests x 128 heads, bf16, 4096 .. 32768     95 us: 5.6 TB/s, 84 % of the copy rate
+//   32 requests x 128 heads, bf16, 4096 .. 32768     97 us: 5.5 TB/s, 83 % of the copy rate
 //   16 x 4 tokens x 16 heads, fp8, 16384 .. 65536   110 us: 3.5 TB/s
 //   32 x 128 heads, fp8, 4096 .. 32768              127 us
-//   2 x 16 heads, bf16, 700 and 2111                 13 us
-// fp8 is bound by the expansion (issue slots 61 %, its steps a chain of waits, reads, conversions
-// and a proxy fence): steps of 64 codes took 147 us where those of 128 take 110.
+//   2 x 16 heads, bf16, 700 and 2111                 13 us, the host's part of a call; 9 in a graph
+// fp8 is bound by the chain of an expansion step (a wait, reads, conversions, stores, a proxy fence;
+// issue slots 55 %): steps of 64 codes took 147 us where those of 128 take 110.
 #include <cstddef>
 
 #include "mla_key_weights_tc.cuh"

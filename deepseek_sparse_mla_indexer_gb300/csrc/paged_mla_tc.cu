@@ -22,7 +22,7 @@
 // scratch in global memory that stays in L2, and every CTA of the cluster loads the tile from there.
 //
 // Every load goes into the CTA that issues it.  One load into all CTAs of a cluster took less
-// from L2 (32 x 128 heads bf16 157 us, now 163; fp8 248, now 256; 8 x 4 x 128 heads fp8 704, now 694),
+// from L2 (32 x 128 heads bf16 157 us, now 163; fp8 248, now 263; 8 x 4 x 128 heads fp8 704, now 683),
 // but it is safe only on this GPU's own memory and in programs on one GPU, which a call cannot see.
 //
 // The tiles of all requests are cut into equal shares over the CTAs (teams of up to
@@ -31,14 +31,15 @@
 // maxima and fp32 accumulators in the workspace, which paged_mla_join_kernel joins.
 //
 // Measured (GB300, a pass among others, positions 4096 .. 32768 unless said):
-//   32 requests x 128 heads, bf16   157 us: 3.4 TB/s, 0.82 PF
-//   128 x 16 heads, fp8, 1024 ..    152 us: 3.1 TB/s
-//   8 x 4 tokens x 128 heads, fp8, 16384 .. 131072   704 us: 0.76 PF
-//   1 x 16 heads, bf16, 501         23 us
-// Bound by the chain of a tile: 5200 cycles (bf16, 64 columns), of which the products take 3640
+//   32 requests x 128 heads, bf16   163 us: 3.3 TB/s, 0.79 PF
+//   128 x 16 heads, fp8, 1024 .. 16384    150 us: 3.2 TB/s
+//   8 x 4 tokens x 128 heads, fp8, 16384 .. 131072   683 us: 0.78 PF
+//   1 x 16 heads, bf16, 501         24 us, of which the host's part of a call; 12 us in a graph
+// Bound by the chain of a tile: 5400 cycles (bf16, 64 columns), of which the products take 3640
 // (N = 64 is bound by the tensor core's reads of shared memory: 48 cycles a product, not 32),
-// the softmax 900 and the next tile's load behind its last reader the rest; fp8 adds the expansion
-// (6500 cycles of 16 columns).  17 thousand cycles pass before the first product.
+// the softmax 900 and the next tile's load behind its last reader the rest.  fp8 rows of up to 32
+// columns: 6500 cycles, in which the threads that expand wait for the products of the one tile
+// that shared memory holds.  17 thousand cycles pass before the first product.
 #include <cstddef>
 
 #include "paged_mla_tc.cuh"

@@ -552,7 +552,8 @@ nsa_status nsa_local_attention(const void *q_dev, int64_t q_ld, const void *k_ca
 /*
  * Attention of each request's newest token(s) over its whole paged cache.
  * Row r belongs to request b = r / rows_per_req (decode: rows_per_req 1;
- * target-verify: n_draft, with nsa_metadata's seqlens_expanded as row_len) and
+ * target-verify: n_draft, with nsa_metadata's seqlens_expanded as row_len; requests
+ * with fewer rows than others are padded with rows of length 0) and
  * sees the positions s < row_len[r], kept at slot
  * page_table[b, s / page_size] * page_size + s % page_size.  Per head h:
  *   x_s      = sm_scale * (q_nope[r,h] . K_s[0:d_latent] + q_rope[r,h] . K_s[d_latent:])
@@ -563,7 +564,10 @@ nsa_status nsa_local_attention(const void *q_dev, int64_t q_ld, const void *k_ca
  *                      E4M3 rows); `out` has q's dtype.  An E4M3 row stands for the
  *                      values nsa_dequantize_kv_paged gives (code x scale rounded to
  *                      fp32, then to bf16), so attending a quantised cache equals
- *                      attending its dequantised copy
+ *                      attending its dequantised copy.  With BF16 q the scores, sums and
+ *                      lse are fp32; on the tensor cores each weight is rounded to bf16
+ *                      (2^-8 of itself at most) for its product with the latent, as
+ *                      nsa_sparse_mla does, and the result once more.  F32 q rounds neither
  *   q_nope_dev, q_rope_dev  [R, H, d_latent] and [R, H, d_rope] with element strides
  *                      (ld_r, ld_h, 1), as nsa_sparse_mla
  *   kv_dev             [num_pages, page_size, row] in the row layouts of nsa_sparse_mla
@@ -590,8 +594,10 @@ nsa_status nsa_local_attention(const void *q_dev, int64_t q_ld, const void *k_ca
  * The 512 + 64 shape with BF16 q runs on the tensor cores (tcgen05) when page_size is a
  * multiple of 8, q and the cache are 16-byte aligned, and the query heads follow one
  * another at one pitch (ld_r == H * ld_h, ld_h a multiple of 8: contiguous q, or the two
- * parts of a concatenated [R, H, 576]).  Everything else runs on the CUDA cores, at a
- * small fraction of that speed.
+ * parts of a concatenated [R, H, 576]).  Everything else runs on the CUDA cores, a
+ * thread block for each row and 16 heads: meant for checks and small models, since it
+ * takes 49 ms where the tensor cores take 0.16 (32 requests of 4096 .. 32768 positions,
+ * 128 heads), more than library matrix products on gathered rows would (8 ms).
  * Device errors (NSA_ERR_BOUNDS): a row_len outside [0, max_row_len] makes its row
  * see no key; the positions of a page outside [0, num_pages) are left out.
  */
@@ -612,7 +618,9 @@ size_t nsa_paged_mla_workspace_bytes(nsa_dtype q_dtype, nsa_dtype kv_dtype, int 
 
 /*
  * The attention weight each cached position received from its request's rows,
- * added to a running total:
+ * added to a running total (the rows' weights sum to one a head only with the lse of
+ * nsa_paged_mla; nsa_sparse_mla's covers the selected positions alone and would give
+ * more than one):
  *   total[b, s] += sum_{rows r of b with s < row_len[r]} sum_h exp(x_{r,h,s} - lse[r,h])
  * with x as in nsa_paged_mla and lse [R, H] as that call wrote it (a row whose
  * lse is -inf gives no weight).  total_dev is [R / rows_per_req, total_ld] float32
@@ -655,7 +663,7 @@ nsa_status nsa_evict_select(const float *total_dev, int64_t total_ld, const int3
  *                   nsa_evict_select (any strictly ascending positions below old_len);
  *                   `budget` (<= keep_ld) bounds new_len
  *   page_table_dev  [B, pt_ld] page ids, pt_ld >= ceil(max_len / page_size).  No page
- *                   may belong to two requests of the call
+ *                   may belong to two requests of the call, or twice to one
  *   arrays_dev      host array of n_arrays (at most 8) device pointers, each to
  *                   [num_pages * page_size] rows of row_bytes[i] bytes (the KV cache, the
  *                   indexer's keys, their scales, ...), not overlapping
