@@ -34,7 +34,7 @@
 //   32 requests x 128 heads, bf16   163 us: 3.3 TB/s, 0.79 PF
 //   128 x 16 heads, fp8, 1024 .. 16384    150 us: 3.2 TB/s
 //   8 x 4 tokens x 128 heads, fp8, 16384 .. 131072   683 us: 0.78 PF
-//   1 x 16 heads, bf16, 501         24 us, of which the host's part of a call; 12 us in a graph
+//   1 x 16 heads, bf16, 501         24 us, the host's part of a call; 12 us in a graph
 // Bound by the chain of a tile: 5400 cycles (bf16, 64 columns), of which the products take 3640
 // (N = 64 is bound by the tensor core's reads of shared memory: 48 cycles a product, not 32),
 // the softmax 900 and the next tile's load behind its last reader the rest.  fp8 rows of up to 32
