@@ -25,7 +25,10 @@ __all__ = [
     "nsa_set_index_k", "nsa_topk_transform_ragged", "nsa_flatten_page_table", "nsa_copy_buffers",
     "nsa_check_bounded_wait", "nsa_local_attention", "nsa_paged_mla", "nsa_paged_mla_workspace_bytes",
     "alloc_paged_mla_workspace", "nsa_mla_key_weights", "nsa_evict_select", "nsa_evict_compact",
-    "nsa_evict_compact_workspace_bytes", "alloc_evict_workspace", "nsa_status_read", "nsa_status_string", "nsa_abi_version",
+    "nsa_evict_compact_workspace_bytes", "alloc_evict_workspace", "nsa_mla_expand_kv",
+    "nsa_mla_expand_kv_workspace_bytes", "alloc_mla_expand_workspace", "nsa_mla_prefill",
+    "nsa_mla_prefill_workspace_bytes", "alloc_mla_prefill_workspace", "nsa_merge_attention", "nsa_mla_absorb_q",
+    "nsa_mla_project_v", "nsa_status_read", "nsa_status_string", "nsa_abi_version",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -42,6 +45,8 @@ EXPORTED_SYMBOLS = [
     "nsa_topk_transform_ragged", "nsa_flatten_page_table", "nsa_copy_buffers",
     "nsa_check_bounded_wait", "nsa_local_attention", "nsa_paged_mla", "nsa_paged_mla_workspace_bytes",
     "nsa_mla_key_weights", "nsa_evict_select", "nsa_evict_compact", "nsa_evict_compact_workspace_bytes",
+    "nsa_mla_expand_kv", "nsa_mla_expand_kv_workspace_bytes", "nsa_mla_prefill", "nsa_mla_prefill_workspace_bytes",
+    "nsa_merge_attention", "nsa_mla_absorb_q", "nsa_mla_project_v",
 ]
 
 _lib = None
@@ -94,6 +99,13 @@ def load(build_if_missing: bool = True):
         "nsa_evict_select": ([P, L, P, I, I, I, I, I, P, L, P, P, P], I),
         "nsa_evict_compact": ([I, P, L, I, P, P, I, P, L, I, L, I, P, P, P, L, P, S, P, P], I),
         "nsa_evict_compact_workspace_bytes": ([I, I], S),
+        "nsa_mla_expand_kv": ([I, P, L, P, I, P, I, I, I, I, I, P, P, P, S, P, P], I),
+        "nsa_mla_expand_kv_workspace_bytes": ([I], S),
+        "nsa_mla_prefill": ([P, L, L, P, L, L, P, L, L, P, L, P, L, L, P, P, I, I, I, I, I, I, I, I, F, P, P, P, S, P, P], I),
+        "nsa_mla_prefill_workspace_bytes": ([], S),
+        "nsa_merge_attention": ([I, I, I, P, P, L, I, P, P, P], I),
+        "nsa_mla_absorb_q": ([P, L, L, P, I, I, I, I, I, P, P, P], I),
+        "nsa_mla_project_v": ([P, L, L, P, I, I, I, I, I, P, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -656,3 +668,140 @@ def nsa_evict_compact(keep: torch.Tensor, new_len: torch.Tensor, old_len: torch.
                                   pt_ld, page_size, slots // page_size, n, ptrs, nb, _at(total), total_ld, _at(workspace),
                                   ws_bytes, _at(status), handle)
     _check("nsa_evict_compact", rc)
+
+
+# ---------------------------------------------------------------- latent attention's two forms
+
+_D_LATENT, _D_ROPE, _D_NOPE, _D_V = 512, 64, 128, 128
+
+
+def _bf16(name: str, t: torch.Tensor, shape, contiguous: bool = True) -> torch.Tensor:
+    """A bf16 tensor of this shape (None: any size there), contiguous or with an adjacent last dimension."""
+    packed = t.is_contiguous() if contiguous else t.dim() > 0 and (t.shape[-1] <= 1 or t.stride(-1) == 1)
+    if t.dtype != torch.bfloat16 or t.dim() != len(shape) or not packed or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        want = ", ".join("any" if n is None else str(n) for n in shape)
+        raise ValueError(f"{name} must be bf16 [{want}], {'contiguous' if contiguous else 'its last dimension adjacent'}, "
+                         f"got shape {tuple(t.shape)}, strides {t.stride()} of {t.dtype}")
+    return t
+
+
+def _heads_of(w: torch.Tensor) -> int:
+    """The heads of an up-projection."""
+    if w.dim() != 2 or w.shape[0] < 1 or w.shape[0] % (_D_NOPE + _D_V):
+        raise ValueError(f"w must be bf16 [heads * {_D_NOPE + _D_V}, {_D_LATENT}], got shape {tuple(w.shape)}")
+    _bf16("w", w, (None, _D_LATENT))
+    return w.shape[0] // (_D_NOPE + _D_V)
+
+
+def nsa_mla_expand_kv_workspace_bytes(m: int) -> int:
+    return int(load().nsa_mla_expand_kv_workspace_bytes(m))
+
+
+def alloc_mla_expand_workspace(m: int, device="cuda") -> torch.Tensor:
+    """Scratch for nsa_mla_expand_kv calls of at most m rows."""
+    return torch.empty(max(16, nsa_mla_expand_kv_workspace_bytes(m)), dtype=torch.uint8, device=device)
+
+
+def nsa_mla_expand_kv(kv_dtype: int, kv: torch.Tensor, slots: torch.Tensor, w: torch.Tensor, kv_out: torch.Tensor,
+                      k_rope_out: torch.Tensor, workspace: torch.Tensor, status: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """Rows `slots` (int32 [m]) of the cache [slots, row] through w [H * 256, 512]: kv_out [m, H, 256] (a head's
+    128 key values, then its 128 values) and k_rope_out [m, 64].  workspace: alloc_mla_expand_workspace's."""
+    H, m = _heads_of(w), slots.numel()
+    num_slots = _paged_cache(kv_dtype, kv, 1, _D_LATENT, _D_ROPE)
+    _i32("slots", slots, m)
+    _bf16("kv_out", kv_out, (m, H, _D_NOPE + _D_V))
+    _bf16("k_rope_out", k_rope_out, (m, _D_ROPE))
+    ws_bytes = _scratch(workspace)
+    _status_word(status)
+    handle = _launch_on(stream, kv, slots, w, kv_out, k_rope_out, workspace, status)
+    rc = load().nsa_mla_expand_kv(kv_dtype, _at(kv), num_slots, _at(slots), m, _at(w), H, _D_LATENT, _D_ROPE, _D_NOPE, _D_V,
+                                  _at(kv_out), _at(k_rope_out), _at(workspace), ws_bytes, _at(status), handle)
+    _check("nsa_mla_expand_kv", rc)
+
+
+def nsa_mla_prefill_workspace_bytes() -> int:
+    return int(load().nsa_mla_prefill_workspace_bytes())
+
+
+def alloc_mla_prefill_workspace(device="cuda") -> torch.Tensor:
+    """Scratch for nsa_mla_prefill calls of any shape on this device."""
+    with torch.cuda.device(device):
+        n = nsa_mla_prefill_workspace_bytes()
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def nsa_mla_prefill(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
+                    v: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor, causal: bool,
+                    sm_scale: float, out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                    status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q_nope [total_q, H, 128], q_rope [total_q, H, 64], k_nope and v [total_k, H, 128] (any row / head strides),
+    k_rope [total_k, 64]; cu_seqlens_q / cu_seqlens_k int32 [B + 1]; out bf16 [total_q, H, 128], lse float32
+    [total_q, H].  workspace: alloc_mla_prefill_workspace's."""
+    total_q, H, _ = _bf16("q_nope", q_nope, (None, None, _D_NOPE), False).shape
+    total_k, B = _bf16("k_rope", k_rope, (None, _D_ROPE), False).shape[0], cu_seqlens_q.numel() - 1
+    _bf16("q_rope", q_rope, (total_q, H, _D_ROPE), False)
+    _bf16("k_nope", k_nope, (total_k, H, _D_NOPE), False)
+    _bf16("v", v, (total_k, H, _D_V), False)
+    _bf16("out", out, (total_q, H, _D_V))
+    if tuple(lse.shape) != (total_q, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous float32 [{total_q}, {H}], got shape {tuple(lse.shape)} of {lse.dtype}")
+    _i32("cu_seqlens_q", cu_seqlens_q, max(B, 0) + 1)
+    _i32("cu_seqlens_k", cu_seqlens_k, B + 1)
+    ws_bytes = _scratch(workspace)
+    _status_word(status)
+    handle = _launch_on(stream, q_nope, q_rope, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace, status)
+    rc = load().nsa_mla_prefill(_at(q_nope), q_nope.stride(0), q_nope.stride(1), _at(q_rope), q_rope.stride(0),
+                                q_rope.stride(1), _at(k_nope), k_nope.stride(0), k_nope.stride(1), _at(k_rope),
+                                k_rope.stride(0), _at(v), v.stride(0), v.stride(1), _at(cu_seqlens_q), _at(cu_seqlens_k), B,
+                                total_q, total_k, H, _D_NOPE, _D_ROPE, _D_V, 1 if causal else 0, float(sm_scale), _at(out),
+                                _at(lse), _at(workspace), ws_bytes, _at(status), handle)
+    _check("nsa_mla_prefill", rc)
+
+
+_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+
+
+def nsa_merge_attention(parts, lses, out: torch.Tensor, lse: torch.Tensor, stream=None) -> None:
+    """parts: tensors [..., D] (all bf16 or all float32), lses: float32 tensors [...], one each; out (parts' type, or
+    bf16) and lse get the attention over all parts' keys, and may be a part's own tensors."""
+    n = len(parts)
+    if n < 1 or len(lses) != n:
+        raise ValueError(f"expected as many lse as parts, at least one: got {len(lses)} and {n}")
+    shape, dtype = tuple(out.shape), parts[0].dtype
+    if dtype not in _DTYPES or out.dtype not in _DTYPES:
+        raise ValueError(f"parts and out must be float32 or bf16, got {dtype} and {out.dtype}")
+    for p, l in zip(list(parts) + [out], list(lses) + [lse]):
+        if tuple(p.shape) != shape or tuple(l.shape) != shape[:-1] or len(shape) < 1 or not p.is_contiguous() or \
+                not l.is_contiguous() or l.dtype != torch.float32 or (p is not out and p.dtype != dtype):
+            raise ValueError(f"parts must be contiguous {dtype} {list(shape)} and lses contiguous float32 {list(shape[:-1])}, "
+                             f"got {p.dtype} {list(p.shape)} and {l.dtype} {list(l.shape)}")
+    handle = _launch_on(stream, out, lse, *parts, *lses)
+    ptrs, lptrs = (C.c_void_p * n)(*[p.data_ptr() for p in parts]), (C.c_void_p * n)(*[l.data_ptr() for l in lses])
+    _check("nsa_merge_attention", load().nsa_merge_attention(_DTYPES[dtype], _DTYPES[out.dtype], n, ptrs, lptrs, lse.numel(),
+                                                             shape[-1], _at(out), _at(lse), handle))
+
+
+def nsa_mla_absorb_q(q_nope: torch.Tensor, w: torch.Tensor, out: torch.Tensor, status: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """q_nope [R, H, 128] (any row / head strides) through each head's W_k: out [R, H, 512]."""
+    H = _heads_of(w)
+    R = _bf16("q_nope", q_nope, (None, H, _D_NOPE), False).shape[0]
+    _bf16("out", out, (R, H, _D_LATENT))
+    _status_word(status)
+    handle = _launch_on(stream, q_nope, w, out, status)
+    _check("nsa_mla_absorb_q", load().nsa_mla_absorb_q(_at(q_nope), q_nope.stride(0), q_nope.stride(1), _at(w), R, H, _D_NOPE,
+                                                       _D_V, _D_LATENT, _at(out), _at(status), handle))
+
+
+def nsa_mla_project_v(latent: torch.Tensor, w: torch.Tensor, out: torch.Tensor, status: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """latent [R, H, 512] (any row / head strides) through each head's W_v: out [R, H, 128]."""
+    H = _heads_of(w)
+    R = _bf16("latent", latent, (None, H, _D_LATENT), False).shape[0]
+    _bf16("out", out, (R, H, _D_V))
+    _status_word(status)
+    handle = _launch_on(stream, latent, w, out, status)
+    _check("nsa_mla_project_v", load().nsa_mla_project_v(_at(latent), latent.stride(0), latent.stride(1), _at(w), R, H,
+                                                         _D_NOPE, _D_V, _D_LATENT, _at(out), _at(status), handle))

@@ -1,0 +1,748 @@
+// nsa_mla_prefill: attention of ragged prompts over expanded keys and values.  Per request, head h
+// and query i, over the keys j that i sees (all n_k, or the first n_k - n_q + i + 1):
+//   x_ij = sm_scale (q_nope[i,h] . k_nope[j,h] + q_rope[i,h] . k_rope[j])
+//   lse  = ln sum_j exp(x_ij)        out = sum_j exp(x_ij - lse) v[j,h]
+//
+// A work item is 256 queries of one request and head, two tiles of 128, and a CTA (one an SM,
+// persistent) takes one item after the other.  Per 128 keys and tile, on tcgen05:
+//   S[128 q, 128 keys] = Q K^T        12 products, both operands in shared memory
+//   P = 2^(c S - c m)                 128 threads, a query each; m a lazily refreshed maximum
+//   O[128 q, 128]     += P V          8 products, P (bf16) in TMEM in the place of S
+// S, P and O of both tiles fill TMEM (512 columns).  While 128 threads turn one tile's scores into
+// P, the tensor core works on the other tile: PV of the keys before, QK of the next.  A row's
+// maximum is only refreshed, and O rescaled by the threads themselves, when it has grown by more
+// than 2^8: until then the weights are up to 2^8 and nothing is lost, since sums are fp32.
+// Weights are rounded to bf16 (2^-8 of themselves at most) for the product with V, whose type the operands
+// share; their sum, and so lse, is taken before that rounding.
+//
+// Keys and values come by TMA through a ring of eight 16 KB slots (a K tile takes three: two halves
+// of the nope part and the rope part that all heads share; a V tile two, of 64 keys each), Q has
+// its own 96 KB.  A warp decodes the items from the sequences' starts and issues the loads, one
+// issues the products, two look through the V tiles that not every query of the item sees: what
+// is not finite there would reach rows that do not see it as 0 x inf, so it is replaced by 0, and
+// the rows that do see it add it at the end.
+//
+// Few items (a short prompt over a long prefix, few heads) are cut along the keys; the parts'
+// fp32 results go to the workspace and merge_launch joins them.
+#include "mla_forms.cuh"
+
+namespace nsa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kTile = 128;                 // queries of a tile, keys of a step
+constexpr int kBlock = 2 * kTile;          // queries of an item
+constexpr uint32_t kSlot = kTile * 128;    // 128 rows (K, Q) or 2 x 64 rows (V) of 128 bytes
+constexpr int kSlots = 8;
+constexpr int kKSlots = 3, kVSlots = 2, kStepSlots = kKSlots + kVSlots;
+constexpr uint32_t kQTile = 3 * kSlot;
+constexpr int kMasked = 3;                 // steps that only some queries of an item see wholly, at most
+
+constexpr int kSoftmaxWarps = 8;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kScanWarp = 10, kScanWarps = 2;
+constexpr int kThreads = 32 * (kScanWarp + kScanWarps);
+constexpr uint32_t kTmemCols = 512;        // S / P of tile t at 128 t, O at 256 + 128 t
+constexpr float kRescale = 8.0f;           // log2 units
+
+// One work item, as the loading warp hands it to the others.
+struct Item {
+    int head;          // < 0: no more
+    int rows;          // queries, 1 .. 256
+    int64_t row0;      // of the first query
+    int64_t key0;      // of the request's first key
+    int keys;          // of the request
+    int vis0;          // keys that the first query sees (causal: one more each further query); may be negative
+    int j0, j1;        // steps of this share, none if j0 >= j1
+    int n[2];          // steps that each tile needs at most
+    int part;
+};
+
+struct Shared {
+    uint64_t slot_full[kSlots], slot_empty[kSlots];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t item_full[2], item_empty[2];
+    uint64_t v_here, v_ok, scanned[2], drained;  // v_here / v_ok: the next masked step's values have landed / are looked through
+    Item item[2];
+    uint32_t odd[2][kMasked][4];  // masked step -> keys whose values are not all finite
+    uint32_t tmem;
+    volatile int abort;
+};
+constexpr uint32_t kSmem = 1024 + 2 * kQTile + kSlots * kSlot + 1024;
+static_assert(sizeof(Shared) <= 1024, "the struct has 1 KB");
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+struct Params {
+    const int32_t *cu_q, *cu_k;
+    int B, total_q, total_k, H, causal;
+    int heads_at_once;   // heads whose keys and values stay in L2 while all queries pass
+    int parts;
+    float scale, scale_log2;
+    // for the values that are not finite
+    const __nv_bfloat16 *q_nope, *q_rope, *k_nope, *k_rope, *v;
+    int64_t qn_r, qn_h, qr_r, qr_h, kn_r, kn_h, kr_r, v_r, v_h;
+    __nv_bfloat16 *out;
+    float *lse;
+    float *part_out, *part_lse;
+    int32_t *status;
+};
+
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Queries and keys of request b; a request whose ranges are not in order is reported and has no queries.
+__device__ __forceinline__ int4 request(const Params &p, int b)
+{
+    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k) {
+        set_status(p.status, NSA_ERR_BOUNDS);
+        return make_int4(0, 0, 0, 0);
+    }
+    return make_int4(q0, q1 - q0, k0, k1 - k0);
+}
+
+// The blocks of 256 queries that requests b0 .. b0 + 31 have up to and with this lane's.
+__device__ __forceinline__ int scan_blocks(int blocks, int lane)
+{
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, blocks, o);
+        if (lane >= o) blocks += v;
+    }
+    return blocks;
+}
+
+__device__ int64_t count_blocks(const Params &p, int lane)
+{
+    int64_t n = 0;
+    for (int b = lane; b < p.B; b += 32) n += (request(p, b).y + kBlock - 1) / kBlock;
+    for (int o = 16; o > 0; o /= 2) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+
+// Item w of blocks x H x parts.  Heads go in sections; in a section all heads of a block of queries
+// follow one another, and a request's blocks go from its last, which sees most keys, to its first.
+__device__ Item decode(const Params &p, int64_t w, int64_t blocks, int lane)
+{
+    Item it;
+    it.part = (int)(w % p.parts);
+    w /= p.parts;
+    const int64_t per = blocks * p.heads_at_once;
+    const int section = (int)(w / per);
+    w -= section * per;
+    const int h0 = section * p.heads_at_once, hs = min(p.heads_at_once, p.H - h0);
+    int64_t block = w / hs;
+    it.head = h0 + (int)(w - block * hs);
+    for (int b0 = 0;; b0 += 32) {
+        const int b = b0 + lane;
+        const int4 r = b < p.B ? request(p, b) : make_int4(0, 0, 0, 0);
+        const int mine = (r.y + kBlock - 1) / kBlock, upto = scan_blocks(mine, lane);
+        const unsigned found = __ballot_sync(0xffffffffu, block < upto);
+        if (!found && b0 + 32 < p.B) {
+            block -= __shfl_sync(0xffffffffu, upto, 31);
+            continue;
+        }
+        const int src = found ? __ffs(found) - 1 : 0;  // found, unless the starts changed under the call
+        const int q0 = __shfl_sync(0xffffffffu, r.x, src), nq = __shfl_sync(0xffffffffu, r.y, src);
+        const int k0 = __shfl_sync(0xffffffffu, r.z, src), nk = __shfl_sync(0xffffffffu, r.w, src);
+        const int last = __shfl_sync(0xffffffffu, upto, src) - 1;
+        const int first = max(0, last - (int)block) * kBlock;
+        it.row0 = (int64_t)q0 + first;
+        it.rows = found ? min(kBlock, nq - first) : 0;
+        it.key0 = k0;
+        it.keys = nk;
+        it.vis0 = p.causal ? nk - nq + first + 1 : nk;
+        break;
+    }
+    int all = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int rows = min(it.rows, kTile * (t + 1));  // the tile's last query sees most
+        const int vis = p.causal ? min(it.keys, it.vis0 + rows - 1) : it.keys;
+        it.n[t] = rows > kTile * t && vis > 0 ? (vis + kTile - 1) / kTile : 0;
+        all = max(all, it.n[t]);
+    }
+    it.j0 = (int)((int64_t)all * it.part / p.parts);
+    it.j1 = (int)((int64_t)all * (it.part + 1) / p.parts);
+    return it;
+}
+
+// The first step that some query of the item does not see wholly.
+__device__ __forceinline__ int first_masked(const Item &it) { return max(it.vis0, 0) / kTile; }
+
+// Adds what the zeroed values of this share's masked steps give to columns col .. col + 31 of a query's sum.
+__device__ __noinline__ void add_odd(const Params &p, const Item &it, const uint32_t (*odd)[4], int row, int vis, float m,
+                                     int col, float (&o)[32])
+{
+    const int64_t q = it.row0 + row;
+    for (int x = 0; x < kMasked; ++x) {
+        for (int pos = 0; pos < kTile; ++pos) {
+            const int j = (first_masked(it) + x) * kTile + pos;
+            if (j >= vis) return;
+            if (!(odd[x][pos / 32] >> (pos % 32) & 1)) continue;
+            const int64_t k = it.key0 + j;
+            float s = 0.f;
+            for (int d = 0; d < kMlaNope; ++d)
+                s = fmaf(__bfloat162float(p.q_nope[q * p.qn_r + it.head * p.qn_h + d]),
+                         __bfloat162float(p.k_nope[k * p.kn_r + it.head * p.kn_h + d]), s);
+            for (int d = 0; d < kMlaRope; ++d)
+                s = fmaf(__bfloat162float(p.q_rope[q * p.qr_r + it.head * p.qr_h + d]),
+                         __bfloat162float(p.k_rope[k * p.kr_r + d]), s);
+            const float w = ex2_approx(fmaf(s, p.scale_log2, m == -INFINITY ? 0.f : -m * p.scale_log2));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                const float v = __bfloat162float(p.v[k * p.v_r + it.head * p.v_h + col + c]);
+                if (!(fabsf(v) < INFINITY)) o[c] = fmaf(w, v, o[c]);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
+                   const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap kr_map,
+                   const __grid_constant__ CUtensorMap v_map, const Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *q_s = base, *ring = q_s + 2 * kQTile;
+    Shared *sm = (Shared *)(ring + kSlots * kSlot);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&sm->slot_full[i], 1);
+            mbar_init(&sm->slot_empty[i], 1);
+        }
+        mbar_init(&sm->q_full, 1);
+        mbar_init(&sm->q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->s_full[i], 1);
+            mbar_init(&sm->p_full[i], 4);
+            mbar_init(&sm->o_full[i], 1);
+            mbar_init(&sm->item_full[i], 1);
+            mbar_init(&sm->item_empty[i], kSoftmaxWarps + 1 + kScanWarps);
+            mbar_init(&sm->scanned[i], kScanWarps);
+        }
+        mbar_init(&sm->v_here, 1);
+        mbar_init(&sm->v_ok, kScanWarps);
+        mbar_init(&sm->drained, 1);
+        sm->abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&qn_map);
+        prefetch_tensormap(&qr_map);
+        prefetch_tensormap(&kn_map);
+        prefetch_tensormap(&kr_map);
+        prefetch_tensormap(&v_map);
+    }
+    if (warp == kMmaWarp) tmem_alloc(&sm->tmem, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem;
+    volatile int *abort = &sm->abort;
+    bool ok = true;
+
+    // Item i as the loading warp published it; its place is given back with item_done.
+    const auto item_wait = [&](int i) { return mla_wait(&sm->item_full[i & 1], (i >> 1) & 1, abort); };
+    const auto item_done = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->item_empty[i & 1]);
+    };
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ items and loads
+        const int64_t blocks = count_blocks(p, lane), total = blocks * p.H * p.parts;
+        uint32_t c = 0, q_uses = 0;  // slots and Q buffers filled so far
+        int64_t w = blockIdx.x;
+        for (int i = 0; ok; ++i, w += gridDim.x) {
+            Item it;
+            it.head = -1;
+            if (w < total) it = decode(p, w, blocks, lane);
+            ok = __all_sync(0xffffffffu, mla_wait(&sm->item_empty[i & 1], ((i >> 1) & 1) ^ 1, abort));
+            if (!ok) break;
+            if (lane < kMasked * 4) sm->odd[i & 1][lane / 4][lane % 4] = 0;
+            __syncwarp();
+            if (lane == 0) {
+                sm->item[i & 1] = it;
+                mbar_arrive(&sm->item_full[i & 1]);
+            }
+            if (w >= total) break;
+            if (it.j0 >= it.j1) continue;
+            if (lane == 0) {
+                ok = mla_wait(&sm->q_empty, (q_uses & 1) ^ 1, abort);
+                const int tiles = it.rows > kTile ? 2 : 1;
+                if (ok) {
+                    mbar_arrive_expect_tx(&sm->q_full, tiles * kQTile);
+                    for (int t = 0; t < tiles; ++t) {
+                        uint8_t *q = q_s + t * kQTile;
+                        const int r = (int)it.row0 + t * kTile;
+                        tma_load_3d(q, &qn_map, 0, it.head, r, &sm->q_full);
+                        tma_load_3d(q + kSlot, &qn_map, 64, it.head, r, &sm->q_full);
+                        tma_load_3d(q + 2 * kSlot, &qr_map, 0, it.head, r, &sm->q_full);
+                    }
+                    ++q_uses;
+                }
+                for (int j = it.j0; j < it.j1 && ok; ++j) {
+                    const int r = (int)it.key0 + j * kTile;
+                    for (int x = 0; x < kStepSlots; ++x, ++c) {
+                        const uint32_t s = c % kSlots;
+                        if (!(ok = mla_wait(&sm->slot_empty[s], ((c / kSlots) & 1) ^ 1, abort))) break;
+                        uint8_t *dst = ring + s * kSlot;
+                        mbar_arrive_expect_tx(&sm->slot_full[s], kSlot);
+                        if (x < 2) {
+                            tma_load_3d(dst, &kn_map, 64 * x, it.head, r, &sm->slot_full[s]);
+                        } else if (x == 2) {
+                            tma_load_2d(dst, &kr_map, 0, r, &sm->slot_full[s]);
+                        } else {
+                            tma_load_3d(dst, &v_map, 0, it.head, r + 64 * (x - 3), &sm->slot_full[s]);
+                            tma_load_3d(dst + kSlot / 2, &v_map, 64, it.head, r + 64 * (x - 3), &sm->slot_full[s]);
+                        }
+                    }
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        if (!ok && lane == 0) {
+            set_status(p.status, NSA_ERR_TIMEOUT);
+            // copies in flight end before the block does
+            for (uint32_t x = c > kSlots ? c - kSlots : 0; x < c; ++x)
+                mbar_wait(&sm->slot_full[x % kSlots], (x / kSlots) & 1, kMlaWait);
+            if (q_uses > 0) mbar_wait(&sm->q_full, (q_uses - 1) & 1, kMlaWait);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ products
+        const uint32_t idesc_s = instr_desc(1, 1, 0, 0, kTile, kTile);   // K-major both
+        const uint32_t idesc_o = instr_desc(1, 1, 0, 1, kTile, kMlaV);   // P in TMEM, V MN-major
+        const uint64_t q_desc = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
+        const uint64_t k_desc = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
+        const uint64_t v_desc = smem_desc(smem_u32(ring), kSlot / 2, 1024, kSwizzle128B);
+        uint32_t c = 0, q_uses = 0, checks = 0, p_uses[2] = {0, 0};
+        const auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && mla_wait(bar, parity, abort));
+            tc_fence_after();
+        };
+        const auto slots_wait = [&](uint32_t c0, int n) {
+            for (uint32_t x = c0; x < c0 + n && ok; ++x) wait(&sm->slot_full[x % kSlots], (x / kSlots) & 1);
+        };
+        const auto slots_free = [&](uint32_t c0, int n) {
+            if (elect_one())
+                for (uint32_t x = c0; x < c0 + n; ++x) mma_commit(&sm->slot_empty[x % kSlots]);
+            __syncwarp();
+        };
+        for (int i = 0; ok; ++i) {
+            ok = __all_sync(0xffffffffu, item_wait(i));
+            if (!ok) break;
+            const Item it = sm->item[i & 1];
+            item_done(i);
+            if (it.head < 0) break;
+            if (it.j0 >= it.j1) continue;
+            const int masked = first_masked(it);
+            wait(&sm->q_full, q_uses++ & 1);
+            const auto qk = [&](int t, uint32_t kc) {  // S_t = Q_t K^T, K in slots kc .. kc + 2
+                if (elect_one()) {
+#pragma unroll
+                    for (int x = 0; x < kKSlots; ++x) {
+                        const uint64_t a = q_desc + (t * kQTile + x * kSlot) / 16;
+                        const uint64_t b = k_desc + (kc + x) % kSlots * (kSlot / 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_f16(tmem + t * kTile, a + 2 * k, b + 2 * k, idesc_s, x > 0 || k > 0);
+                    }
+                    mma_commit(&sm->s_full[t]);
+                }
+                __syncwarp();
+            };
+            const auto pv = [&](int t, uint32_t vc, bool first, bool last) {  // O_t += P_t V, V in slots vc, vc + 1
+                if (elect_one()) {
+#pragma unroll
+                    for (int x = 0; x < kVSlots; ++x) {
+                        const uint64_t b = v_desc + (vc + x) % kSlots * (kSlot / 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16_ts(tmem + 2 * kTile + t * kMlaV, tmem + t * kTile + x * 32 + k * 8, b + k * (2048 / 16),
+                                       idesc_o, !first || x > 0 || k > 0);
+                    }
+                    if (last) mma_commit(&sm->o_full[t]);
+                }
+                __syncwarp();
+            };
+            slots_wait(c, kKSlots);
+            for (int t = 0; t < 2 && ok; ++t)
+                if (it.j0 < it.n[t]) qk(t, c);
+            slots_free(c, kKSlots);
+            const auto q_free = [&] {  // behind the item's last product with Q
+                if (elect_one()) mma_commit(&sm->q_empty);
+                __syncwarp();
+            };
+            if (it.j1 - it.j0 == 1) q_free();
+            for (int j = it.j0; j < it.j1 && ok; ++j) {
+                const uint32_t vc = c + kKSlots, kc = c + kStepSlots;
+                const bool more = j + 1 < it.j1;
+                bool have_v = false, have_k = false;
+                if (j >= masked) {
+                    // the scanning warps could not tell this filling of the slots from an earlier one
+                    slots_wait(vc, kVSlots);
+                    if (ok && elect_one()) mbar_arrive(&sm->v_here);
+                    __syncwarp();
+                }
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (j < it.n[t]) {
+                        wait(&sm->p_full[t], p_uses[t]++ & 1);
+                        if (!have_v) {
+                            if (j < masked) slots_wait(vc, kVSlots);
+                            if (j >= masked) wait(&sm->v_ok, checks++ & 1);
+                            have_v = true;
+                        }
+                        if (!ok) break;
+                        pv(t, vc, j == it.j0, !(more && j + 1 < it.n[t]));
+                    }
+                    if (t == 1) slots_free(vc, kVSlots);
+                    if (more) {
+                        if (!have_k) slots_wait(kc, kKSlots);
+                        have_k = true;
+                        if (!ok) break;
+                        if (j + 1 < it.n[t]) qk(t, kc);
+                    }
+                }
+                if (more) slots_free(kc, kKSlots);
+                if (j + 2 == it.j1) q_free();
+                c += kStepSlots;
+            }
+        }
+        if (!ok && lane == 0) {
+            set_status(p.status, NSA_ERR_TIMEOUT);
+            mma_commit(&sm->drained);  // products in flight end before the block does
+            mbar_wait(&sm->drained, 0, kMlaWait);
+        }
+        __syncwarp();
+    } else if (warp >= kScanWarp) {
+        // ------------------------------------------------------------ values that some queries must not see
+        uint32_t c = 0, checks = 0;
+        for (int i = 0; ok; ++i) {
+            ok = __all_sync(0xffffffffu, item_wait(i));
+            if (!ok) break;
+            const Item it = sm->item[i & 1];
+            if (it.head < 0) break;
+            const int masked = first_masked(it);
+            for (int j = it.j0; j < it.j1 && ok; ++j, c += kStepSlots) {
+                if (j < masked) continue;
+                // each warp one slot: 64 keys, eight lanes a row of 128 bytes
+                const uint32_t vc = c + kKSlots + (warp - kScanWarp), s = vc % kSlots;
+                ok = __all_sync(0xffffffffu, mla_wait(&sm->v_here, checks & 1, abort) &&
+                                                 mla_wait(&sm->slot_full[s], (vc / kSlots) & 1, abort));
+                uint32_t odd[2] = {0, 0};
+                for (int r = 0; r < 2 * 64 && ok; r += 4) {  // rows of both halves of the value
+                    uint4 *at = (uint4 *)(ring + s * kSlot + (r + lane / 8) * 128 + (lane % 8) * 16);
+                    uint4 v = *at;
+                    uint32_t *u = &v.x;
+                    bool any = false;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const bool lo = (u[x] & 0x7F80u) == 0x7F80u, hi = (u[x] & 0x7F800000u) == 0x7F800000u;
+                        if (lo) u[x] &= 0xFFFF0000u;
+                        if (hi) u[x] &= 0x0000FFFFu;
+                        any |= lo || hi;
+                    }
+                    if (any) *at = v;
+                    const uint32_t lanes = __ballot_sync(0xffffffffu, any);
+                    for (int x = 0; x < 4; ++x)
+                        if (lanes >> (8 * x) & 0xff) odd[(r & 63) / 32] |= 1u << ((r + x) & 31);
+                }
+                if (ok && (odd[0] | odd[1])) {
+                    if (lane < 2) sm->odd[i & 1][j - masked][(warp - kScanWarp) * 2 + lane] = lane ? odd[1] : odd[0];
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->v_ok);
+                ++checks;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm->scanned[i & 1]);
+            item_done(i);
+        }
+        if (!ok && lane == 0) set_status(p.status, NSA_ERR_TIMEOUT);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax: one query a thread
+        const int t = warp / 4, row = (warp & 3) * 32 + lane;  // of tile t
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_at = lanes + t * kTile, o_at = lanes + 2 * kTile + t * kMlaV;
+        uint32_t s_uses = 0, o_uses = 0;
+        const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
+        for (int i = 0; ok; ++i) {
+            ok = __all_sync(0xffffffffu, item_wait(i));
+            if (!ok) break;
+            const Item it = sm->item[i & 1];
+            if (it.head < 0) break;
+            const int r = t * kTile + row;
+            const int vis = p.causal ? min(it.keys, it.vis0 + r) : it.keys;
+            const int j_end = min(it.j1, it.n[t]);
+            float m = -INFINITY, l = 0.f;
+            for (int j = it.j0; j < j_end; ++j) {
+                ok = __all_sync(0xffffffffu, mla_wait(&sm->s_full[t], s_uses++ & 1, abort));
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tmem_ld32(s_at + 32 * x, s[x]);
+                tmem_ld_wait();
+                const int seen = vis - j * kTile;
+                if (seen < kTile) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int y = 0; y < 32; ++y)
+                            if (32 * x + y >= seen) s[x][y] = 0xFF800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    mx[x] = __uint_as_float(s[x][0]);
+#pragma unroll
+                    for (int y = 1; y < 31; y += 2)
+                        mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[x][y])), __uint_as_float(s[x][y + 1]));
+                    mx[x] = fmaxf(mx[x], __uint_as_float(s[x][31]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (j == it.j0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, (top - m) * p.scale_log2 > kRescale)) {
+                    // QK of this step was issued behind PV of the one before, so O is at rest.  Each row by
+                    // its own scores: a neighbour's, which may be infinite, do not change its roundings
+                    const float fresh = (top - m) * p.scale_log2 > kRescale ? top : m;
+                    const float f = fresh == m ? 1.f : ex2_approx((m - fresh) * p.scale_log2);
+                    m = fresh;
+                    l *= f;
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + 32 * x, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                        tmem_st32(o_at + 32 * x, o);
+                    }
+                }
+                const float nm = m == -INFINITY ? 0.f : -m * p.scale_log2;
+                const float2 nm2 = make_float2(nm, nm);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        float2 e = fma2(make_float2(__uint_as_float(s[x][2 * y]), __uint_as_float(s[x][2 * y + 1])), c2, nm2);
+                        e.x = ex2_approx(e.x);
+                        e.y = ex2_approx(e.y);
+                        sum[y & 1] = add2(sum[y & 1], e);
+                        w[y] = pack_bf16(e.x, e.y);
+                    }
+                    tmem_st16(s_at + 16 * x, w);
+                }
+                const float2 part = add2(sum[0], sum[1]);
+                l += part.x + part.y;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->p_full[t]);
+            }
+            if (!ok) break;
+            // ---- the query's result
+            const bool any = it.j0 < j_end;
+            ok = __all_sync(0xffffffffu, mla_wait(&sm->scanned[i & 1], (i >> 1) & 1, abort));
+            if (ok && any) ok = __all_sync(0xffffffffu, mla_wait(&sm->o_full[t], o_uses++ & 1, abort));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t odd = 0;
+            for (int x = 0; x < kMasked * 4; ++x) odd |= sm->odd[i & 1][x / 4][x % 4];
+            const bool mine = r < it.rows;
+            const int64_t at = (it.row0 + r) * p.H + it.head;
+            const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
+            if (t * kTile < it.rows) {
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x) {
+                    float o[32];
+                    if (any) {
+                        uint32_t u[32];
+                        tmem_ld32(o_at + 32 * x, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = __uint_as_float(u[y]);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = 0.f;
+                    }
+                    if (mine) {
+                        if (odd && any) add_odd(p, it, sm->odd[i & 1], r, min(vis, j_end * kTile), m, 32 * x, o);
+                        if (l == 0.f) {
+                            // no weight at all: 0, and not 0 x NaN
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) o[y] = 0.f;
+                        }
+                        if (p.parts > 1) {
+                            float4 *dst = (float4 *)(p.part_out + ((int64_t)it.part * p.total_q * p.H + at) * kMlaV + 32 * x);
+#pragma unroll
+                            for (int y = 0; y < 8; ++y)
+                                dst[y] = make_float4(o[4 * y] * inv, o[4 * y + 1] * inv, o[4 * y + 2] * inv, o[4 * y + 3] * inv);
+                        } else {
+                            uint4 *dst = (uint4 *)(p.out + at * kMlaV + 32 * x);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                dst[y] = make_uint4(pack_bf16(o[8 * y] * inv, o[8 * y + 1] * inv),
+                                                    pack_bf16(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
+                                                    pack_bf16(o[8 * y + 4] * inv, o[8 * y + 5] * inv),
+                                                    pack_bf16(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (mine) {
+                    const float lse = l > 0.f ? fmaf(m, p.scale, logf(l)) : l == l ? -INFINITY : l;
+                    if (p.parts > 1) p.part_lse[(int64_t)it.part * p.total_q * p.H + at] = lse;
+                    else p.lse[at] = lse;
+                }
+            }
+            tc_fence_before();
+            item_done(i);
+        }
+        if (!ok && lane == 0) set_status(p.status, NSA_ERR_TIMEOUT);
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) {
+        tmem_relinquish();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Blocks of 256 queries that B requests of total_q queries have at most.
+int64_t most_blocks(int B, int total_q)
+{
+    const int64_t n = ((int64_t)total_q + (int64_t)(kBlock - 1) * B) / kBlock;
+    return n < total_q ? n : total_q;
+}
+
+// Shares that the keys of an item are cut into: as many as leave no SM twice an item, each of kPartSteps
+// steps at least, and no more than the join takes.
+constexpr int kPartSteps = 4;
+int parts_of(int64_t items, int total_k, int sms)
+{
+    int64_t n = sms / items;
+    const int64_t steps = total_k / (kPartSteps * kTile);
+    if (n > steps) n = steps;
+    if (n > kMaxMergeParts) n = kMaxMergeParts;
+    return n < 1 ? 1 : (int)n;
+}
+
+// Heads whose keys and values (512 bytes a key) are to stay in L2 together.
+constexpr int64_t kL2Keys = 40LL << 20;
+
+}  // namespace
+}  // namespace nsa
+
+extern "C" size_t nsa_mla_prefill_workspace_bytes(void)
+{
+    // parts_of: parts x items <= SMs, of 256 queries each
+    const int sms = nsa::current_sm_count();
+    return (size_t)(sms > 0 ? sms : 0) * nsa::kBlock * (nsa::kMlaV + 1) * sizeof(float);
+}
+
+extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, int64_t qn_ld_h, const void *q_rope_dev,
+                                      int64_t qr_ld_r, int64_t qr_ld_h, const void *k_nope_dev, int64_t kn_ld_r,
+                                      int64_t kn_ld_h, const void *k_rope_dev, int64_t kr_ld_r, const void *v_dev,
+                                      int64_t v_ld_r, int64_t v_ld_h, const int32_t *cu_seqlens_q_dev,
+                                      const int32_t *cu_seqlens_k_dev, int B, int total_q, int total_k, int H, int d_nope,
+                                      int d_rope, int d_v, int causal, float sm_scale, void *out_dev, float *lse_dev,
+                                      void *workspace_dev, size_t workspace_bytes, int32_t *status_dev, nsa_stream_t stream)
+{
+    using namespace nsa;
+    if (B < 0 || total_q < 0 || total_k < 0 || H < 1 || causal < 0 || causal > 1) return NSA_ERR_INVALID_ARG;
+    if (!(sm_scale > 0.f) || !(sm_scale < INFINITY)) return NSA_ERR_INVALID_ARG;
+    if (d_nope != kMlaNope || d_rope != kMlaRope || d_v != kMlaV || H > 65535 || total_k > (1 << 30) || total_q > (1 << 30))
+        return NSA_ERR_UNSUPPORTED;
+    if (B == 0 || total_q == 0) return NSA_OK;
+    if (!q_nope_dev || !q_rope_dev || !cu_seqlens_q_dev || !cu_seqlens_k_dev || !out_dev || !lse_dev || !workspace_dev ||
+        (total_k > 0 && (!k_nope_dev || !k_rope_dev || !v_dev)))
+        return NSA_ERR_INVALID_ARG;
+    const uintptr_t wide = (uintptr_t)q_nope_dev | (uintptr_t)q_rope_dev | (uintptr_t)k_nope_dev | (uintptr_t)k_rope_dev |
+                           (uintptr_t)v_dev | (uintptr_t)out_dev | (uintptr_t)workspace_dev;
+    const uintptr_t word = (uintptr_t)cu_seqlens_q_dev | (uintptr_t)cu_seqlens_k_dev | (uintptr_t)lse_dev | (uintptr_t)status_dev;
+    if ((wide & 15) || (word & 3)) return NSA_ERR_INVALID_ARG;
+    // [rows][heads][d] with strides that TMA can step over; a single row's or head's stride is arbitrary
+    struct Strided { int64_t *r, *h; int rows, d; };
+    Strided all[5] = {{&qn_ld_r, &qn_ld_h, total_q, kMlaNope}, {&qr_ld_r, &qr_ld_h, total_q, kMlaRope},
+                      {&kn_ld_r, &kn_ld_h, total_k, kMlaNope}, {&kr_ld_r, nullptr, total_k, kMlaRope},
+                      {&v_ld_r, &v_ld_h, total_k, kMlaV}};
+    for (const Strided &x : all) {
+        if (x.h && H == 1) *x.h = x.d;
+        if (x.rows <= 1) *x.r = x.h ? *x.h * H : x.d;
+        if (*x.r < x.d || (x.h && *x.h < x.d) || *x.r % 8 || (x.h && *x.h % 8)) return NSA_ERR_INVALID_ARG;
+        if (*x.r >= ((int64_t)1 << 38) || (x.h && *x.h >= ((int64_t)1 << 38))) return NSA_ERR_UNSUPPORTED;
+    }
+    if (workspace_bytes < nsa_mla_prefill_workspace_bytes()) return NSA_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return NSA_ERR_CUDA;
+
+    Params p;
+    p.cu_q = cu_seqlens_q_dev; p.cu_k = cu_seqlens_k_dev;
+    p.B = B; p.total_q = total_q; p.total_k = total_k; p.H = H; p.causal = causal;
+    const int64_t items = most_blocks(B, total_q) * H;
+    p.parts = parts_of(items, total_k, sms);
+    const int64_t fit = kL2Keys / ((int64_t)(total_k > 0 ? total_k : 1) * 2 * (kMlaNope + kMlaV));
+    p.heads_at_once = (int)(fit < 1 ? 1 : fit < H ? fit : H);
+    p.scale = sm_scale;
+    p.scale_log2 = sm_scale * 1.4426950408889634f;
+    p.q_nope = (const __nv_bfloat16 *)q_nope_dev; p.q_rope = (const __nv_bfloat16 *)q_rope_dev;
+    p.k_nope = (const __nv_bfloat16 *)k_nope_dev; p.k_rope = (const __nv_bfloat16 *)k_rope_dev;
+    p.v = (const __nv_bfloat16 *)v_dev;
+    p.qn_r = qn_ld_r; p.qn_h = qn_ld_h; p.qr_r = qr_ld_r; p.qr_h = qr_ld_h;
+    p.kn_r = kn_ld_r; p.kn_h = kn_ld_h; p.kr_r = kr_ld_r; p.v_r = v_ld_r; p.v_h = v_ld_h;
+    p.out = (__nv_bfloat16 *)out_dev; p.lse = lse_dev;
+    p.part_out = (float *)workspace_dev;
+    p.part_lse = p.part_out + (int64_t)p.parts * total_q * H * kMlaV;
+    p.status = status_dev;
+
+    CUtensorMap qn, qr, kn, kr, v;
+    const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    const uint64_t h = (uint64_t)H, tq = (uint64_t)total_q;
+    // without a key no load is issued: the maps then describe the queries
+    const bool keys = total_k > 0;
+    const uint64_t tk = keys ? (uint64_t)total_k : tq;
+    const bool mapped =
+        make_tma_3d(&qn, bf, q_nope_dev, kMlaNope, h, tq, qn_ld_h * 2, qn_ld_r * 2, 64, 1, kTile, sw) &&
+        make_tma_3d(&qr, bf, q_rope_dev, kMlaRope, h, tq, qr_ld_h * 2, qr_ld_r * 2, 64, 1, kTile, sw) &&
+        (keys ? make_tma_3d(&kn, bf, k_nope_dev, kMlaNope, h, tk, kn_ld_h * 2, kn_ld_r * 2, 64, 1, kTile, sw) &&
+                    make_tma_2d(&kr, bf, k_rope_dev, kMlaRope, tk, kr_ld_r * 2, 64, kTile, sw) &&
+                    make_tma_3d(&v, bf, v_dev, kMlaV, h, tk, v_ld_h * 2, v_ld_r * 2, 64, 1, kTile / 2, sw)
+              : make_tma_3d(&kn, bf, q_nope_dev, kMlaNope, h, tk, qn_ld_h * 2, qn_ld_r * 2, 64, 1, kTile, sw) &&
+                    make_tma_2d(&kr, bf, q_rope_dev, kMlaRope, tk, qr_ld_r * 2, 64, kTile, sw) &&
+                    make_tma_3d(&v, bf, q_nope_dev, kMlaNope, h, tk, qn_ld_h * 2, qn_ld_r * 2, 64, 1, kTile / 2, sw));
+    if (!mapped) return NSA_ERR_CUDA;
+    NSA_CUDA_TRY(max_dynamic_smem<mla_prefill_kernel>((int)kSmem));
+    const cudaStream_t s = (cudaStream_t)stream;
+    const int64_t work = items * p.parts;
+    mla_prefill_kernel<<<(unsigned)(work < sms ? work : sms), kThreads, kSmem, s>>>(qn, qr, kn, kr, v, p);
+    if (launch_status() != NSA_OK) return NSA_ERR_CUDA;
+    if (p.parts == 1) return NSA_OK;
+    MergeParts parts = {};
+    for (int i = 0; i < p.parts; ++i) {
+        parts.out[i] = p.part_out + (int64_t)i * total_q * H * kMlaV;
+        parts.lse[i] = p.part_lse + (int64_t)i * total_q * H;
+    }
+    parts.live_from = cu_seqlens_q_dev;
+    parts.live_to = cu_seqlens_q_dev + B;
+    parts.live_rows = H;
+    return merge_launch(NSA_DT_F32, NSA_DT_BF16, p.parts, parts, (int64_t)total_q * H, kMlaV, out_dev, lse_dev, true, s);
+}

@@ -10,6 +10,11 @@
  *   nsa_paged_mla       MLA attention over the whole paged cache, and the eviction
  *                       of its least attended positions (nsa_mla_key_weights,
  *                       nsa_evict_select, nsa_evict_compact)
+ *   nsa_mla_prefill     attention of prompts over expanded keys and values, which
+ *                       nsa_mla_expand_kv makes of cached rows; nsa_merge_attention
+ *                       joins attention over parts of the keys
+ *   nsa_mla_absorb_q, nsa_mla_project_v   the products around attention in the
+ *                       latent space
  *
  * Sources, cited by page title and the function shown on the page:
  *   [NSA-diff] "sglang 0.5.3rc2 -> 0.5.4 diff: sglang/srt/layers/attention/nsa_backend.py"
@@ -687,6 +692,114 @@ nsa_status nsa_evict_compact(int B, const int32_t *keep_dev, int64_t keep_ld, in
                              size_t workspace_bytes, int32_t *status_dev, nsa_stream_t stream);
 
 size_t nsa_evict_compact_workspace_bytes(int B, int max_len);
+
+/* ------------------------------------------------------------------------
+ * The two forms of latent attention.
+ *
+ * The up-projection w [H * (d_nope + d_v), d_latent] (bf16, contiguous: the weight
+ * of the layer that makes keys and values of a latent) holds for each head h
+ * d_nope rows W_k[h] and then d_v rows W_v[h].  With a cached latent c_j:
+ *   expanded   k_nope[j,h] = W_k[h] c_j, v[j,h] = W_v[h] c_j; attention per head over
+ *              192-wide keys and 128-wide values.  320 multiply-adds a pair and head:
+ *              what prompts use (nsa_mla_expand_kv, nsa_mla_prefill)
+ *   absorbed   q_lat[r,h] = q_nope[r,h] W_k[h]; attention in the latent space (nsa_sparse_mla,
+ *              nsa_paged_mla: 1088 a pair and head, but one row of the cache serves all
+ *              heads); out[r,h] = W_v[h] lat[r,h].  What tokens use (nsa_mla_absorb_q,
+ *              nsa_mla_project_v)
+ * Both give the same attention.  d_latent 512, d_rope 64, d_nope 128, d_v 128 only
+ * (else NSA_ERR_UNSUPPORTED), bf16 in and out with fp32 sums, rounded once.  The
+ * pages have no counterpart of these calls: their framework makes the products with
+ * library GEMMs and attends prompts with FlashAttention.
+ *
+ * All calls are asynchronous on `stream` and allocate nothing.  Matrix operands and
+ * outputs are 16-byte aligned and row and head strides multiples of 8 elements, no
+ * smaller than what they step over (a single row's or head's stride is not looked at); else
+ * NSA_ERR_INVALID_ARG before any launch, as for NULL, misaligned words, bad sizes or
+ * too small a workspace.  NSA_ERR_UNSUPPORTED for more than 65535 heads or 2^30 rows.
+ * A bounded wait inside a kernel that runs out sets NSA_ERR_TIMEOUT.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Cached rows, gathered and expanded: row i < m is slot slots_dev[i] of kv_dev (bf16 or
+ * e4m3 rows; the latter stand for what nsa_dequantize_kv_paged gives):
+ *   kv_out_dev      [m, H, d_nope + d_v]  w[h] c: a head's key part, then its values
+ *   k_rope_out_dev  [m, d_rope]           the row's rope values
+ *   slots_dev       [m] int32 (nsa_flatten_page_table's list); a negative slot is padding and
+ *                   gives zero rows; one at or past num_slots too, with NSA_ERR_BOUNDS
+ *   workspace_dev   nsa_mla_expand_kv_workspace_bytes(m) bytes (the gathered latents; one for the
+ *                   largest m serves smaller ones).  Calls that may overlap on the GPU need
+ *                   workspaces of their own; nothing is kept in it between calls
+ */
+nsa_status nsa_mla_expand_kv(nsa_dtype kv_dtype, const void *kv_dev, int64_t num_slots, const int32_t *slots_dev,
+                             int m, const void *w_dev, int H, int d_latent, int d_rope, int d_nope, int d_v,
+                             void *kv_out_dev, void *k_rope_out_dev, void *workspace_dev, size_t workspace_bytes,
+                             int32_t *status_dev, nsa_stream_t stream);
+
+size_t nsa_mla_expand_kv_workspace_bytes(int m);
+
+/*
+ * Attention of ragged prompts over expanded keys and values.  Request b has the query
+ * rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 and the keys cu_seqlens_k[b] ..
+ * cu_seqlens_k[b+1]-1; n_q and n_k are their numbers.  Query i of a request sees all its keys
+ * (causal 0: the chunk of a prefix), or the keys 0 .. n_k - n_q + i (causal 1: the prompt
+ * itself, with or without its prefix before it).  Per head h:
+ *   x_ij = sm_scale * (q_nope[i,h] . k_nope[j,h] + q_rope[i,h] . k_rope[j])
+ *   lse[i,h] = ln sum_j exp(x_ij)         (natural log; -inf if the row sees no key)
+ *   out[i,h] = sum_j exp(x_ij - lse) v[j,h]     (0 if the row sees no key)
+ *
+ *   q_nope_dev, q_rope_dev  [total_q, H, d_nope], [total_q, H, d_rope] bf16, element strides (ld_r, ld_h, 1)
+ *   k_nope_dev, v_dev       [total_k, H, d_nope], [total_k, H, d_v] bf16, likewise (parts of
+ *                           nsa_mla_expand_kv's kv_out, or arrays of their own)
+ *   k_rope_dev              [total_k, d_rope] bf16, row stride kr_ld_r: one for all heads
+ *   cu_seqlens_q_dev, cu_seqlens_k_dev  [B + 1] int32, non-decreasing (nsa_metadata's); rows before
+ *                           the first and behind the last request's are left as they are
+ *   out_dev [total_q, H, d_v] bf16, lse_dev [total_q, H] float32, contiguous
+ *   workspace_dev           nsa_mla_prefill_workspace_bytes() bytes on the current device, for any shape
+ *                           (the parts of long rows).  Calls that may overlap on the GPU need workspaces
+ *                           of their own; nothing is kept in it between calls
+ * Each weight is rounded to bf16 (2^-8 of itself at most) for its product with the values; lse and the
+ * sum that divides are taken before that.  What a row does not see is never used, whatever it
+ * holds: a NaN or infinity at a key reaches only the rows that see it.  A score of -inf has weight 0,
+ * as in the formula (a component of out is NaN, 0 x inf, where that key's value is not finite); a row
+ * all of whose scores are -inf has lse -inf and zeros.  A score of NaN or +inf makes the row NaN.
+ * Device error (NSA_ERR_BOUNDS): a request whose starts decrease or leave [0, total] is left out.
+ */
+nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, int64_t qn_ld_h, const void *q_rope_dev,
+                           int64_t qr_ld_r, int64_t qr_ld_h, const void *k_nope_dev, int64_t kn_ld_r, int64_t kn_ld_h,
+                           const void *k_rope_dev, int64_t kr_ld_r, const void *v_dev, int64_t v_ld_r, int64_t v_ld_h,
+                           const int32_t *cu_seqlens_q_dev, const int32_t *cu_seqlens_k_dev, int B, int total_q,
+                           int total_k, int H, int d_nope, int d_rope, int d_v, int causal, float sm_scale,
+                           void *out_dev, float *lse_dev, void *workspace_dev, size_t workspace_bytes,
+                           int32_t *status_dev, nsa_stream_t stream);
+
+size_t nsa_mla_prefill_workspace_bytes(void);
+
+/*
+ * Attention over parts of the keys, joined: with each part's out [rows, D] and lse [rows] (natural
+ * log; rows = query rows x heads),
+ *   lse = ln sum_p exp(lse_p)      out = sum_p exp(lse_p - lse) out_p
+ * A part with lse -inf saw no key: its values are not looked at.  A row without a key in any part
+ * gets out 0 and lse -inf.  NaN or +inf in a row's lse makes the row NaN.
+ *   parts_dev, lses_dev  host arrays of n_parts (at most 8) device pointers; part_dtype BF16 or F32
+ *   out_dev, lse_dev     out_dtype BF16, or F32 for F32 parts.  They may be a part's own arrays (of the same
+ *                        type), but may not overlap one otherwise
+ * D a multiple of 8, at most 2048 (else NSA_ERR_UNSUPPORTED).
+ */
+nsa_status nsa_merge_attention(nsa_dtype part_dtype, nsa_dtype out_dtype, int n_parts, const void *const *parts_dev,
+                               const float *const *lses_dev, int64_t rows, int D, void *out_dev, float *lse_dev,
+                               nsa_stream_t stream);
+
+/* out[r, h, :] = q_nope[r, h, :] W_k[h]: queries [R, H, d_nope] (strides ld_r, ld_h, 1) into the
+ * latent space, out_dev [R, H, d_latent] contiguous (q_nope of nsa_sparse_mla and nsa_paged_mla). */
+nsa_status nsa_mla_absorb_q(const void *q_nope_dev, int64_t nope_ld_r, int64_t nope_ld_h, const void *w_dev, int R,
+                            int H, int d_nope, int d_v, int d_latent, void *out_dev, int32_t *status_dev,
+                            nsa_stream_t stream);
+
+/* out[r, h, :] = W_v[h] latent[r, h, :]: attended latents [R, H, d_latent] (strides ld_r, ld_h, 1; out of
+ * nsa_sparse_mla and nsa_paged_mla) to values, out_dev [R, H, d_v] contiguous. */
+nsa_status nsa_mla_project_v(const void *latent_dev, int64_t latent_ld_r, int64_t latent_ld_h, const void *w_dev,
+                             int R, int H, int d_nope, int d_v, int d_latent, void *out_dev, int32_t *status_dev,
+                             nsa_stream_t stream);
 
 #ifdef __cplusplus
 }
