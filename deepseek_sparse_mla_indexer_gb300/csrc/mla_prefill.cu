@@ -39,9 +39,10 @@ constexpr int kKSlots = 3, kVSlots = 2, kStepSlots = kKSlots + kVSlots;
 constexpr uint32_t kQTile = 3 * kSlot;
 constexpr int kMasked = 3;                 // steps that only some queries of an item see wholly, at most
 
-constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kScanWarp = 10, kScanWarps = 2;
-constexpr int kThreads = 32 * (kScanWarp + kScanWarps);
+constexpr int kSoftmaxWarps = 16;          // per tile eight: two threads a query, 64 keys of a step each
+constexpr int kHalf = kTile / 2;
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kScanWarp = 18, kScanWarps = 2;
+constexpr int kThreads = 32 * (kScanWarp + kScanWarps);  // 20 warps: a 21st would leave each thread 80 registers instead of 96
 constexpr uint32_t kTmemCols = 512;        // S / P of tile t at 128 t, O at 256 + 128 t
 constexpr float kRescale = 8.0f;           // log2 units
 
@@ -59,18 +60,21 @@ struct Item {
 };
 
 struct Shared {
-    uint64_t slot_full[kSlots], slot_empty[kSlots];
+    // of every other step: its keys / values have landed, and are no longer needed
+    uint64_t k_full[2], v_full[2], k_free[2], v_free[2];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], go[2], o_full[2];  // go: P, and the values that it is multiplied with
     uint64_t item_full[2], item_empty[2];
-    uint64_t v_here, v_ok, scanned[2], drained;  // v_here / v_ok: the next masked step's values have landed / are looked through
+    uint64_t scanned[2], drained;
     Item item[2];
     uint32_t odd[2][kMasked][4];  // masked step -> keys whose values are not all finite
     uint32_t tmem;
     volatile int abort;
+    // [tile][half]: a query's maximum over its half of the step, at the end its sum of weights.  The next
+    // step's scores come behind all P of this one, so nobody still reads when they are written
+    float top[2][2][kTile];
 };
-constexpr uint32_t kSmem = 1024 + 2 * kQTile + kSlots * kSlot + 1024;
-static_assert(sizeof(Shared) <= 1024, "the struct has 1 KB");
+constexpr uint32_t kSmem = 2 * kQTile + kSlots * kSlot + sizeof(Shared);
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct Params {
@@ -78,6 +82,7 @@ struct Params {
     int B, total_q, total_k, H, causal;
     int heads_at_once;   // heads whose keys and values stay in L2 while all queries pass
     int parts;
+    int wide;            // the results' addresses are multiples of 32 bytes
     float scale, scale_log2;
     // for the values that are not finite
     const __nv_bfloat16 *q_nope, *q_rope, *k_nope, *k_rope, *v;
@@ -85,6 +90,7 @@ struct Params {
     __nv_bfloat16 *out;
     float *lse;
     float *part_out, *part_lse;
+    unsigned long long *next;  // the items taken beyond each CTA's first; NULL: one each is all
     int32_t *status;
 };
 
@@ -97,6 +103,19 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// 32 bytes: one whole sector of L2 where the address allows it, since every thread of a warp writes a row of its own.
+__device__ __forceinline__ void store_sector(void *p, const uint32_t (&v)[8], bool wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        *(uint4 *)p = make_uint4(v[0], v[1], v[2], v[3]);
+        *((uint4 *)p + 1) = make_uint4(v[4], v[5], v[6], v[7]);
+    }
 }
 
 // Queries and keys of request b; a request whose ranges are not in order is reported and has no queries.
@@ -211,29 +230,26 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                    const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap kr_map,
                    const __grid_constant__ CUtensorMap v_map, const Params p)
 {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t *q_s = base, *ring = q_s + 2 * kQTile;
+    extern __shared__ __align__(1024) uint8_t q_s[];
+    uint8_t *ring = q_s + 2 * kQTile;
     Shared *sm = (Shared *)(ring + kSlots * kSlot);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&sm->slot_full[i], 1);
-            mbar_init(&sm->slot_empty[i], 1);
-        }
         mbar_init(&sm->q_full, 1);
         mbar_init(&sm->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->k_full[i], 1);
+            mbar_init(&sm->v_full[i], 1);
+            mbar_init(&sm->k_free[i], 1);
+            mbar_init(&sm->v_free[i], 1);
             mbar_init(&sm->s_full[i], 1);
-            mbar_init(&sm->p_full[i], 4);
+            mbar_init(&sm->go[i], kSoftmaxWarps / 2 + kScanWarps);
             mbar_init(&sm->o_full[i], 1);
             mbar_init(&sm->item_full[i], 1);
             mbar_init(&sm->item_empty[i], kSoftmaxWarps + 1 + kScanWarps);
             mbar_init(&sm->scanned[i], kScanWarps);
         }
-        mbar_init(&sm->v_here, 1);
-        mbar_init(&sm->v_ok, kScanWarps);
         mbar_init(&sm->drained, 1);
         sm->abort = 0;
         fence_mbar_init();
@@ -261,12 +277,41 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ items and loads
         const int64_t blocks = count_blocks(p, lane), total = blocks * p.H * p.parts;
-        uint32_t c = 0, q_uses = 0;  // slots and Q buffers filled so far
+        uint32_t g = 0, q_uses = 0;  // steps and Q buffers filled so far
         int64_t w = blockIdx.x;
-        for (int i = 0; ok; ++i, w += gridDim.x) {
-            Item it;
-            it.head = -1;
-            if (w < total) it = decode(p, w, blocks, lane);
+        Item next;
+        next.head = -1;
+        if (w < total) next = decode(p, w, blocks, lane);
+        // K of step g takes the slots of K (its last) and V of step g - 2, V those of K of step g - 1
+        uint32_t k_sent = 0, v_sent = 0;
+        const auto load_k = [&](const Item &it, int j) {
+            if (!ok) return;
+            const int r = (int)it.key0 + j * kTile;
+            uint64_t *bar = &sm->k_full[g & 1];
+            const auto slot = [&](int x) { return ring + (kStepSlots * g + x) % kSlots * kSlot; };
+            mbar_arrive_expect_tx(bar, kKSlots * kSlot);
+            ++k_sent;
+            tma_load_3d(slot(0), &kn_map, 0, it.head, r, bar);
+            if (g >= 2) ok = mla_wait(&sm->v_free[g & 1], ((g - 2) >> 1) & 1, abort);
+            // (given up or not: what the barrier expects is sent)
+            tma_load_3d(slot(1), &kn_map, 64, it.head, r, bar);
+            tma_load_2d(slot(2), &kr_map, 0, r, bar);
+        };
+        const auto load_v = [&](const Item &it, int j) {
+            const int r = (int)it.key0 + j * kTile;
+            uint64_t *bar = &sm->v_full[g & 1];
+            if (g >= 1) ok = ok && mla_wait(&sm->k_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort);
+            if (!ok) return;
+            mbar_arrive_expect_tx(bar, kVSlots * kSlot);
+            ++v_sent;
+            for (int x = 0; x < kVSlots; ++x) {
+                uint8_t *dst = ring + (kStepSlots * g + kKSlots + x) % kSlots * kSlot;
+                tma_load_3d(dst, &v_map, 0, it.head, r + 64 * x, bar);
+                tma_load_3d(dst + kSlot / 2, &v_map, 64, it.head, r + 64 * x, bar);
+            }
+        };
+        for (int i = 0; ok; ++i) {
+            const Item it = next;
             ok = __all_sync(0xffffffffu, mla_wait(&sm->item_empty[i & 1], ((i >> 1) & 1) ^ 1, abort));
             if (!ok) break;
             if (lane < kMasked * 4) sm->odd[i & 1][lane / 4][lane % 4] = 0;
@@ -275,12 +320,13 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 sm->item[i & 1] = it;
                 mbar_arrive(&sm->item_full[i & 1]);
             }
-            if (w >= total) break;
-            if (it.j0 >= it.j1) continue;
-            if (lane == 0) {
-                ok = mla_wait(&sm->q_empty, (q_uses & 1) ^ 1, abort);
-                const int tiles = it.rows > kTile ? 2 : 1;
+            if (it.head < 0) break;
+            const bool some = it.j0 < it.j1;
+            if (some && lane == 0) {
+                load_k(it, it.j0);
+                ok = ok && mla_wait(&sm->q_empty, (q_uses & 1) ^ 1, abort);
                 if (ok) {
+                    const int tiles = it.rows > kTile ? 2 : 1;
                     mbar_arrive_expect_tx(&sm->q_full, tiles * kQTile);
                     for (int t = 0; t < tiles; ++t) {
                         uint8_t *q = q_s + t * kQTile;
@@ -291,22 +337,23 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                     }
                     ++q_uses;
                 }
-                for (int j = it.j0; j < it.j1 && ok; ++j) {
-                    const int r = (int)it.key0 + j * kTile;
-                    for (int x = 0; x < kStepSlots; ++x, ++c) {
-                        const uint32_t s = c % kSlots;
-                        if (!(ok = mla_wait(&sm->slot_empty[s], ((c / kSlots) & 1) ^ 1, abort))) break;
-                        uint8_t *dst = ring + s * kSlot;
-                        mbar_arrive_expect_tx(&sm->slot_full[s], kSlot);
-                        if (x < 2) {
-                            tma_load_3d(dst, &kn_map, 64 * x, it.head, r, &sm->slot_full[s]);
-                        } else if (x == 2) {
-                            tma_load_2d(dst, &kr_map, 0, r, &sm->slot_full[s]);
-                        } else {
-                            tma_load_3d(dst, &v_map, 0, it.head, r + 64 * (x - 3), &sm->slot_full[s]);
-                            tma_load_3d(dst + kSlot / 2, &v_map, 64, it.head, r + 64 * (x - 3), &sm->slot_full[s]);
-                        }
-                    }
+                load_v(it, it.j0);
+                ++g;
+            }
+            // the item after this one is looked up while this one's steps run
+            if (p.next) {
+                unsigned long long n = 0;
+                if (lane == 0) n = atomicAdd(p.next, 1ULL);
+                w = gridDim.x + (int64_t)__shfl_sync(0xffffffffu, n, 0);
+            } else {
+                w += gridDim.x;
+            }
+            next.head = -1;
+            if (w < total) next = decode(p, w, blocks, lane);
+            if (some && lane == 0) {
+                for (int j = it.j0 + 1; j < it.j1 && ok; ++j, ++g) {
+                    load_k(it, j);
+                    load_v(it, j);
                 }
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -314,8 +361,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
         if (!ok && lane == 0) {
             set_status(p.status, NSA_ERR_TIMEOUT);
             // copies in flight end before the block does
-            for (uint32_t x = c > kSlots ? c - kSlots : 0; x < c; ++x)
-                mbar_wait(&sm->slot_full[x % kSlots], (x / kSlots) & 1, kMlaWait);
+            for (uint32_t x = k_sent > 2 ? k_sent - 2 : 0; x < k_sent; ++x) mbar_wait(&sm->k_full[x & 1], (x >> 1) & 1, kMlaWait);
+            for (uint32_t x = v_sent > 2 ? v_sent - 2 : 0; x < v_sent; ++x) mbar_wait(&sm->v_full[x & 1], (x >> 1) & 1, kMlaWait);
             if (q_uses > 0) mbar_wait(&sm->q_full, (q_uses - 1) & 1, kMlaWait);
         }
         __syncwarp();
@@ -326,96 +373,76 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
         const uint64_t q_desc = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
         const uint64_t k_desc = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
         const uint64_t v_desc = smem_desc(smem_u32(ring), kSlot / 2, 1024, kSwizzle128B);
-        uint32_t c = 0, q_uses = 0, checks = 0, p_uses[2] = {0, 0};
-        const auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, ok && mla_wait(bar, parity, abort));
-            tc_fence_after();
+        // What this warp does between products leaves the tensor core without work, so one barrier a tile and
+        // step tells it that P and V are there
+        uint32_t g = 0, q_uses = 0, go_uses[2] = {0, 0};
+        // a wait that gave up lets the warp go on to the step's end, where the lanes agree to stop
+        const auto wait = [&](uint64_t *bar, uint32_t parity) { ok = mla_wait(bar, parity, abort) && ok; };
+        // (one elected lane) S_t = Q_t K^T, K of step `at`; O_t += P_t V, V of step g
+        const auto qk = [&](int t, uint32_t at) {
+#pragma unroll
+            for (int x = 0; x < kKSlots; ++x) {
+                const uint64_t a = q_desc + (t * kQTile + x * kSlot) / 16;
+                const uint64_t b = k_desc + (kStepSlots * at + x) % kSlots * (kSlot / 16);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_f16(tmem + t * kTile, a + 2 * k, b + 2 * k, idesc_s, x > 0 || k > 0);
+            }
+            mma_commit(&sm->s_full[t]);
         };
-        const auto slots_wait = [&](uint32_t c0, int n) {
-            for (uint32_t x = c0; x < c0 + n && ok; ++x) wait(&sm->slot_full[x % kSlots], (x / kSlots) & 1);
-        };
-        const auto slots_free = [&](uint32_t c0, int n) {
-            if (elect_one())
-                for (uint32_t x = c0; x < c0 + n; ++x) mma_commit(&sm->slot_empty[x % kSlots]);
-            __syncwarp();
+        const auto pv = [&](int t, bool first, bool last) {
+#pragma unroll
+            for (int x = 0; x < kVSlots; ++x) {
+                const uint64_t b = v_desc + (kStepSlots * g + kKSlots + x) % kSlots * (kSlot / 16);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f16_ts(tmem + 2 * kTile + t * kMlaV, tmem + t * kTile + x * 32 + k * 8, b + k * (2048 / 16), idesc_o,
+                               !first || x > 0 || k > 0);
+            }
+            if (last) mma_commit(&sm->o_full[t]);
         };
         for (int i = 0; ok; ++i) {
             ok = __all_sync(0xffffffffu, item_wait(i));
             if (!ok) break;
-            const Item it = sm->item[i & 1];
+            const int head = sm->item[i & 1].head, j0 = sm->item[i & 1].j0, j1 = sm->item[i & 1].j1;
+            const int n[2] = {sm->item[i & 1].n[0], sm->item[i & 1].n[1]};
             item_done(i);
-            if (it.head < 0) break;
-            if (it.j0 >= it.j1) continue;
-            const int masked = first_masked(it);
+            if (head < 0) break;
+            if (j0 >= j1) continue;
+            wait(&sm->k_full[g & 1], (g >> 1) & 1);
             wait(&sm->q_full, q_uses++ & 1);
-            const auto qk = [&](int t, uint32_t kc) {  // S_t = Q_t K^T, K in slots kc .. kc + 2
-                if (elect_one()) {
+            __syncwarp();
+            if (elect_one()) {
 #pragma unroll
-                    for (int x = 0; x < kKSlots; ++x) {
-                        const uint64_t a = q_desc + (t * kQTile + x * kSlot) / 16;
-                        const uint64_t b = k_desc + (kc + x) % kSlots * (kSlot / 16);
+                for (int t = 0; t < 2; ++t)
+                    if (j0 < n[t]) qk(t, g);
+                mma_commit(&sm->k_free[g & 1]);
+                if (j1 - j0 == 1) mma_commit(&sm->q_empty);  // behind the item's last product with Q
+            }
+            for (int j = j0; j < j1; ++j) {
+                const bool more = j + 1 < j1;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_f16(tmem + t * kTile, a + 2 * k, b + 2 * k, idesc_s, x > 0 || k > 0);
+                for (int t = 0; t < 2; ++t) {
+                    if (j < n[t]) {
+                        wait(&sm->go[t], go_uses[t]++ & 1);
+                        __syncwarp();
+                        tc_fence_after();
                     }
-                    mma_commit(&sm->s_full[t]);
-                }
-                __syncwarp();
-            };
-            const auto pv = [&](int t, uint32_t vc, bool first, bool last) {  // O_t += P_t V, V in slots vc, vc + 1
-                if (elect_one()) {
-#pragma unroll
-                    for (int x = 0; x < kVSlots; ++x) {
-                        const uint64_t b = v_desc + (vc + x) % kSlots * (kSlot / 16);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16_ts(tmem + 2 * kTile + t * kMlaV, tmem + t * kTile + x * 32 + k * 8, b + k * (2048 / 16),
-                                       idesc_o, !first || x > 0 || k > 0);
+                    if (elect_one()) {
+                        if (j < n[t]) pv(t, j == j0, !(more && j + 1 < n[t]));
+                        if (t == 1) mma_commit(&sm->v_free[g & 1]);
                     }
-                    if (last) mma_commit(&sm->o_full[t]);
-                }
-                __syncwarp();
-            };
-            slots_wait(c, kKSlots);
-            for (int t = 0; t < 2 && ok; ++t)
-                if (it.j0 < it.n[t]) qk(t, c);
-            slots_free(c, kKSlots);
-            const auto q_free = [&] {  // behind the item's last product with Q
-                if (elect_one()) mma_commit(&sm->q_empty);
-                __syncwarp();
-            };
-            if (it.j1 - it.j0 == 1) q_free();
-            for (int j = it.j0; j < it.j1 && ok; ++j) {
-                const uint32_t vc = c + kKSlots, kc = c + kStepSlots;
-                const bool more = j + 1 < it.j1;
-                bool have_v = false, have_k = false;
-                if (j >= masked) {
-                    // the scanning warps could not tell this filling of the slots from an earlier one
-                    slots_wait(vc, kVSlots);
-                    if (ok && elect_one()) mbar_arrive(&sm->v_here);
+                    if (t == 0 && more) wait(&sm->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
+                    __syncwarp();
+                    if (elect_one()) {
+                        if (more && j + 1 < n[t]) qk(t, g + 1);
+                        if (t == 1 && more) mma_commit(&sm->k_free[(g + 1) & 1]);
+                        if (t == 1 && j + 2 == j1) mma_commit(&sm->q_empty);
+                    }
                     __syncwarp();
                 }
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (j < it.n[t]) {
-                        wait(&sm->p_full[t], p_uses[t]++ & 1);
-                        if (!have_v) {
-                            if (j < masked) slots_wait(vc, kVSlots);
-                            if (j >= masked) wait(&sm->v_ok, checks++ & 1);
-                            have_v = true;
-                        }
-                        if (!ok) break;
-                        pv(t, vc, j == it.j0, !(more && j + 1 < it.n[t]));
-                    }
-                    if (t == 1) slots_free(vc, kVSlots);
-                    if (more) {
-                        if (!have_k) slots_wait(kc, kKSlots);
-                        have_k = true;
-                        if (!ok) break;
-                        if (j + 1 < it.n[t]) qk(t, kc);
-                    }
-                }
-                if (more) slots_free(kc, kKSlots);
-                if (j + 2 == it.j1) q_free();
-                c += kStepSlots;
+                ++g;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
             }
         }
         if (!ok && lane == 0) {
@@ -425,45 +452,65 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
         }
         __syncwarp();
     } else if (warp >= kScanWarp) {
-        // ------------------------------------------------------------ values that some queries must not see
-        uint32_t c = 0, checks = 0;
+        // ------------------------------------------------------------ what has landed, for the products
+        // A step's values; those that some queries must not see are looked through
+        uint32_t g = 0;
         for (int i = 0; ok; ++i) {
             ok = __all_sync(0xffffffffu, item_wait(i));
             if (!ok) break;
             const Item it = sm->item[i & 1];
             if (it.head < 0) break;
             const int masked = first_masked(it);
-            for (int j = it.j0; j < it.j1 && ok; ++j, c += kStepSlots) {
-                if (j < masked) continue;
-                // each warp one slot: 64 keys, eight lanes a row of 128 bytes
-                const uint32_t vc = c + kKSlots + (warp - kScanWarp), s = vc % kSlots;
-                ok = __all_sync(0xffffffffu, mla_wait(&sm->v_here, checks & 1, abort) &&
-                                                 mla_wait(&sm->slot_full[s], (vc / kSlots) & 1, abort));
-                uint32_t odd[2] = {0, 0};
-                for (int r = 0; r < 2 * 64 && ok; r += 4) {  // rows of both halves of the value
-                    uint4 *at = (uint4 *)(ring + s * kSlot + (r + lane / 8) * 128 + (lane % 8) * 16);
-                    uint4 v = *at;
-                    uint32_t *u = &v.x;
-                    bool any = false;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const bool lo = (u[x] & 0x7F80u) == 0x7F80u, hi = (u[x] & 0x7F800000u) == 0x7F800000u;
-                        if (lo) u[x] &= 0xFFFF0000u;
-                        if (hi) u[x] &= 0x0000FFFFu;
-                        any |= lo || hi;
-                    }
-                    if (any) *at = v;
-                    const uint32_t lanes = __ballot_sync(0xffffffffu, any);
-                    for (int x = 0; x < 4; ++x)
-                        if (lanes >> (8 * x) & 0xff) odd[(r & 63) / 32] |= 1u << ((r + x) & 31);
+            for (int j = it.j0; j < it.j1 && ok; ++j, ++g) {
+                // behind the products of the step before, so that its `go` is over
+                ok = g == 0 || mla_wait(&sm->v_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort);
+                ok = ok && mla_wait(&sm->v_full[g & 1], (g >> 1) & 1, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                const auto go = [&] {
+                    __syncwarp();
+                    if (lane < 2 && j < it.n[lane]) mbar_arrive(&sm->go[lane]);
+                };
+                if (j < masked) {
+                    go();
+                    continue;
                 }
-                if (ok && (odd[0] | odd[1])) {
-                    if (lane < 2) sm->odd[i & 1][j - masked][(warp - kScanWarp) * 2 + lane] = lane ? odd[1] : odd[0];
+                // a slot has 64 keys' rows of 128 bytes, one half of the value behind the other; eight lanes a row
+                for (int x = warp - kScanWarp; x < kVSlots && ok; x += kScanWarps) {
+                    uint8_t *slot = ring + (kStepSlots * g + kKSlots + x) % kSlots * kSlot;
+                    const uint32_t at0 = smem_u32(slot) + lane * 16;
+                    uint32_t seen = 0;
+                    // an exponent of ones carries into the sign's place
+#pragma unroll 8
+                    for (int r = 0; r < 2 * 64; r += 4) {
+                        uint32_t u[4];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at0 + r * 128));
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) seen |= (u[y] & 0x7FFF7FFFu) + 0x00800080u;
+                    }
+                    if (!__any_sync(0xffffffffu, seen & 0x80008000u)) continue;
+                    uint32_t odd[2] = {0, 0};
+                    for (int r = 0; r < 2 * 64; r += 4) {
+                        uint4 *at = (uint4 *)(slot + (r + lane / 8) * 128 + (lane % 8) * 16);
+                        uint4 v = *at;
+                        uint32_t *u = &v.x;
+                        bool any = false;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const bool lo = (u[y] & 0x7F80u) == 0x7F80u, hi = (u[y] & 0x7F800000u) == 0x7F800000u;
+                            if (lo) u[y] &= 0xFFFF0000u;
+                            if (hi) u[y] &= 0x0000FFFFu;
+                            any |= lo || hi;
+                        }
+                        if (any) *at = v;
+                        const uint32_t lanes = __ballot_sync(0xffffffffu, any);
+                        for (int y = 0; y < 4; ++y)
+                            if (lanes >> (8 * y) & 0xff) odd[(r & 63) / 32] |= 1u << ((r + y) & 31);
+                    }
+                    if (lane < 2) sm->odd[i & 1][j - masked][x * 2 + lane] = lane ? odd[1] : odd[0];
                     fence_proxy_async_smem();
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->v_ok);
-                ++checks;
+                go();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->scanned[i & 1]);
@@ -472,94 +519,133 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
         if (!ok && lane == 0) set_status(p.status, NSA_ERR_TIMEOUT);
         __syncwarp();
     } else {
-        // ------------------------------------------------------------ softmax: one query a thread
-        const int t = warp / 4, row = (warp & 3) * 32 + lane;  // of tile t
+        // ------------------------------------------------------------ softmax: two threads a query, 64 keys each
+        const int t = (warp / 4) & 1, half = warp / 8, row = (warp & 3) * 32 + lane;  // of tile t
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t s_at = lanes + t * kTile, o_at = lanes + 2 * kTile + t * kMlaV;
+        const uint32_t s_at = lanes + t * kTile + half * kHalf, p_at = lanes + t * kTile + half * (kHalf / 2);
+        const uint32_t o_at = lanes + 2 * kTile + t * kMlaV + half * kHalf;
         uint32_t s_uses = 0, o_uses = 0;
         const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
         for (int i = 0; ok; ++i) {
             ok = __all_sync(0xffffffffu, item_wait(i));
             if (!ok) break;
-            const Item it = sm->item[i & 1];
+            const Item &it = sm->item[i & 1];
             if (it.head < 0) break;
             const int r = t * kTile + row;
             const int vis = p.causal ? min(it.keys, it.vis0 + r) : it.keys;
-            const int j_end = min(it.j1, it.n[t]);
+            const int j0 = it.j0, j_end = min(it.j1, it.n[t]);
             float m = -INFINITY, l = 0.f;
-            for (int j = it.j0; j < j_end; ++j) {
-                ok = __all_sync(0xffffffffu, mla_wait(&sm->s_full[t], s_uses++ & 1, abort));
-                if (!ok) break;
+            for (int j = j0; j < j_end; ++j, ++s_uses) {
+                ok = mla_wait(&sm->s_full[t], s_uses & 1, abort);
+                __syncwarp();
                 tc_fence_after();
-                uint32_t s[4][32];
+                const int seen = vis - j * kTile - half * kHalf;  // of this thread's 64 keys
+                uint32_t s[2][32];
+                float top = -INFINITY;
+                float2 sum[2];
+                const auto load = [&] {
+                    tmem_ld32(s_at, s[0]);
+                    tmem_ld32(s_at + 32, s[1]);
+                    tmem_ld_wait();
+                    if (seen < kHalf) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) tmem_ld32(s_at + 32 * x, s[x]);
-                tmem_ld_wait();
-                const int seen = vis - j * kTile;
-                if (seen < kTile) {
+                        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-#pragma unroll
-                        for (int y = 0; y < 32; ++y)
-                            if (32 * x + y >= seen) s[x][y] = 0xFF800000u;
-                }
-                float mx[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    mx[x] = __uint_as_float(s[x][0]);
-#pragma unroll
-                    for (int y = 1; y < 31; y += 2)
-                        mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[x][y])), __uint_as_float(s[x][y + 1]));
-                    mx[x] = fmaxf(mx[x], __uint_as_float(s[x][31]));
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if (j == it.j0) {
-                    m = top;
-                } else if (__any_sync(0xffffffffu, (top - m) * p.scale_log2 > kRescale)) {
-                    // QK of this step was issued behind PV of the one before, so O is at rest.  Each row by
-                    // its own scores: a neighbour's, which may be infinite, do not change its roundings
-                    const float fresh = (top - m) * p.scale_log2 > kRescale ? top : m;
-                    const float f = fresh == m ? 1.f : ex2_approx((m - fresh) * p.scale_log2);
-                    m = fresh;
-                    l *= f;
-#pragma unroll 1
-                    for (int x = 0; x < 4; ++x) {
-                        uint32_t o[32];
-                        tmem_ld32(o_at + 32 * x, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                        tmem_st32(o_at + 32 * x, o);
+                            for (int y = 0; y < 32; ++y)
+                                if (32 * x + y >= seen) s[x][y] = 0xFF800000u;
                     }
-                }
-                const float nm = m == -INFINITY ? 0.f : -m * p.scale_log2;
-                const float2 nm2 = make_float2(nm, nm);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                };
+                // scores to weights, in bf16 in the first half of their registers, and their sum
+                const auto weigh = [&](bool with_top) {
+                    const float nm = m == -INFINITY ? 0.f : -m * p.scale_log2;
+                    const float2 nm2 = make_float2(nm, nm);
+                    float tops[2] = {-INFINITY, -INFINITY};
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) {
+                            const float a = __uint_as_float(s[x][2 * y]), b = __uint_as_float(s[x][2 * y + 1]);
+                            if (with_top) tops[y & 1] = fmaxf(fmaxf(tops[y & 1], a), b);
+                            float2 e = fma2(make_float2(a, b), c2, nm2);
+                            e.x = ex2_approx(e.x);
+                            e.y = ex2_approx(e.y);
+                            sum[y & 1] = add2(sum[y & 1], e);
+                            s[x][y] = pack_bf16(e.x, e.y);
+                        }
+                    if (with_top) top = fmaxf(tops[0], tops[1]);
+                };
+                load();
+                bool again = true;
+                if (j > j0) {
+                    // With the maximum of the steps before, which hardly ever has to be refreshed.  Each row by
+                    // its own scores: a neighbour's, which may be infinite, do not change its roundings.  Behind
+                    // the barrier all scores of the tile are read, and P may take their place
+                    weigh(true);
+                    again = bar_red_or(1 + t, 256, !ok || (top - m) * p.scale_log2 > kRescale);
+                    if (again) load();
+                }
+                if (again) {
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int y = 0; y < 32; y += 2)
+                            mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[x][y])), __uint_as_float(s[x][y + 1]));
+                    float *tops = &sm->top[t][0][row];
+                    tops[half * kTile] = fmaxf(mx[0], mx[1]);
+                    if (bar_red_or(1 + t, 256, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    top = fmaxf(tops[0], tops[kTile]);
+                    if (j == j0) {
+                        m = top;
+                    } else if (__any_sync(0xffffffffu, (top - m) * p.scale_log2 > kRescale)) {
+                        // QK of this step was issued behind PV of the one before, so O is at rest
+                        const float fresh = (top - m) * p.scale_log2 > kRescale ? top : m;
+                        const float f = fresh == m ? 1.f : ex2_approx((m - fresh) * p.scale_log2);
+                        m = fresh;
+                        l *= f;
+#pragma unroll 1
+                        for (int x = 0; x < kHalf; x += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(o_at + x, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                            tmem_st16(o_at + x, o);
+                        }
+                    }
+                    weigh(false);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
                     uint32_t w[16];
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        float2 e = fma2(make_float2(__uint_as_float(s[x][2 * y]), __uint_as_float(s[x][2 * y + 1])), c2, nm2);
-                        e.x = ex2_approx(e.x);
-                        e.y = ex2_approx(e.y);
-                        sum[y & 1] = add2(sum[y & 1], e);
-                        w[y] = pack_bf16(e.x, e.y);
-                    }
-                    tmem_st16(s_at + 16 * x, w);
+                    for (int y = 0; y < 16; ++y) w[y] = s[x][y];
+                    tmem_st16(p_at + 16 * x, w);
                 }
                 const float2 part = add2(sum[0], sum[1]);
                 l += part.x + part.y;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->p_full[t]);
+                if (lane == 0) mbar_arrive(&sm->go[t]);
             }
             if (!ok) break;
-            // ---- the query's result
-            const bool any = it.j0 < j_end;
-            ok = __all_sync(0xffffffffu, mla_wait(&sm->scanned[i & 1], (i >> 1) & 1, abort));
-            if (ok && any) ok = __all_sync(0xffffffffu, mla_wait(&sm->o_full[t], o_uses++ & 1, abort));
+            // ---- the query's result: its sum, then 64 of its values a thread
+            const bool any = j0 < j_end;
+            ok = mla_wait(&sm->scanned[i & 1], (i >> 1) & 1, abort);
+            if (any) ok = mla_wait(&sm->o_full[t], o_uses++ & 1, abort) && ok;
+            if (any) {
+                sm->top[t][half][row] = l;
+                __syncwarp();
+                ok = !bar_red_or(1 + t, 256, !ok);
+                l = sm->top[t][0][row] + sm->top[t][1][row];
+                bar_sync(1 + t, 256);
+            }
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
             uint32_t odd = 0;
@@ -569,11 +655,11 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
             if (t * kTile < it.rows) {
 #pragma unroll 1
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < kHalf; x += 32) {
                     float o[32];
                     if (any) {
                         uint32_t u[32];
-                        tmem_ld32(o_at + 32 * x, u);
+                        tmem_ld32(o_at + x, u);
                         tmem_ld_wait();
 #pragma unroll
                         for (int y = 0; y < 32; ++y) o[y] = __uint_as_float(u[y]);
@@ -582,30 +668,43 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                         for (int y = 0; y < 32; ++y) o[y] = 0.f;
                     }
                     if (mine) {
-                        if (odd && any) add_odd(p, it, sm->odd[i & 1], r, min(vis, j_end * kTile), m, 32 * x, o);
+                        const int col = half * kHalf + x;
+                        if (odd && any) {
+                            float with[32];
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) with[y] = o[y];
+                            add_odd(p, it, sm->odd[i & 1], r, min(vis, j_end * kTile), m, col, with);
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) o[y] = with[y];
+                        }
                         if (l == 0.f) {
                             // no weight at all: 0, and not 0 x NaN
 #pragma unroll
                             for (int y = 0; y < 32; ++y) o[y] = 0.f;
                         }
                         if (p.parts > 1) {
-                            float4 *dst = (float4 *)(p.part_out + ((int64_t)it.part * p.total_q * p.H + at) * kMlaV + 32 * x);
+                            float *dst = p.part_out + ((int64_t)it.part * p.total_q * p.H + at) * kMlaV + col;
 #pragma unroll
-                            for (int y = 0; y < 8; ++y)
-                                dst[y] = make_float4(o[4 * y] * inv, o[4 * y + 1] * inv, o[4 * y + 2] * inv, o[4 * y + 3] * inv);
+                            for (int y = 0; y < 4; ++y) {
+                                uint32_t v[8];
+#pragma unroll
+                                for (int z = 0; z < 8; ++z) v[z] = __float_as_uint(o[8 * y + z] * inv);
+                                store_sector(dst + 8 * y, v, p.wide);
+                            }
                         } else {
-                            uint4 *dst = (uint4 *)(p.out + at * kMlaV + 32 * x);
+                            __nv_bfloat16 *dst = p.out + at * kMlaV + col;
 #pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                dst[y] = make_uint4(pack_bf16(o[8 * y] * inv, o[8 * y + 1] * inv),
-                                                    pack_bf16(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
-                                                    pack_bf16(o[8 * y + 4] * inv, o[8 * y + 5] * inv),
-                                                    pack_bf16(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
+                            for (int y = 0; y < 2; ++y) {
+                                uint32_t v[8];
+#pragma unroll
+                                for (int z = 0; z < 8; ++z) v[z] = pack_bf16(o[16 * y + 2 * z] * inv, o[16 * y + 2 * z + 1] * inv);
+                                store_sector(dst + 16 * y, v, p.wide);
+                            }
                         }
                     }
                     __syncwarp();
                 }
-                if (mine) {
+                if (mine && half == 0) {
                     const float lse = l > 0.f ? fmaf(m, p.scale, logf(l)) : l == l ? -INFINITY : l;
                     if (p.parts > 1) p.part_lse[(int64_t)it.part * p.total_q * p.H + at] = lse;
                     else p.lse[at] = lse;
@@ -633,17 +732,25 @@ int64_t most_blocks(int B, int total_q)
     return n < total_q ? n : total_q;
 }
 
-// Shares that the keys of an item are cut into: as many as leave no SM twice an item, each of kPartSteps
-// steps at least, and no more than the join takes.
-constexpr int kPartSteps = 4;
-int parts_of(int64_t items, int total_k, int sms)
+// Shares that the keys of an item are cut into where there are fewer than kPartItems items an SM: those
+// whose rounds over the SMs take the fewest steps, an item counted with two steps beside its own and
+// the join with kJoinSteps.  At least kPartSteps steps a share.
+constexpr int kPartItems = 4, kPartSteps = 4, kJoinSteps = 6;
+int parts_of(int64_t items, int B, int total_k, int sms)
 {
-    int64_t n = sms / items;
-    const int64_t steps = total_k / (kPartSteps * kTile);
-    if (n > steps) n = steps;
-    if (n > kMaxMergeParts) n = kMaxMergeParts;
-    return n < 1 ? 1 : (int)n;
+    const int64_t steps = ceil_div(total_k, (int64_t)kTile * B);
+    int best = 1;
+    int64_t cost = ceil_div(items, sms) * (steps + 2);
+    for (int n = 2; n <= kMaxMergeParts && items * n <= (int64_t)kPartItems * sms && steps >= n * kPartSteps; ++n) {
+        const int64_t c = ceil_div(items * n, sms) * (ceil_div(steps, n) + 2) + kJoinSteps;
+        if (c < cost) {
+            cost = c;
+            best = n;
+        }
+    }
+    return best;
 }
+constexpr size_t kCounterBytes = 256;  // of the workspace, before the parts
 
 // Heads whose keys and values (512 bytes a key) are to stay in L2 together.
 constexpr int64_t kL2Keys = 40LL << 20;
@@ -653,9 +760,9 @@ constexpr int64_t kL2Keys = 40LL << 20;
 
 extern "C" size_t nsa_mla_prefill_workspace_bytes(void)
 {
-    // parts_of: parts x items <= SMs, of 256 queries each
+    // parts_of: parts x items <= kPartItems x SMs, of 256 queries each
     const int sms = nsa::current_sm_count();
-    return (size_t)(sms > 0 ? sms : 0) * nsa::kBlock * (nsa::kMlaV + 1) * sizeof(float);
+    return nsa::kCounterBytes + (size_t)(sms > 0 ? sms : 0) * nsa::kPartItems * nsa::kBlock * (nsa::kMlaV + 1) * sizeof(float);
 }
 
 extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, int64_t qn_ld_h, const void *q_rope_dev,
@@ -698,7 +805,7 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     p.cu_q = cu_seqlens_q_dev; p.cu_k = cu_seqlens_k_dev;
     p.B = B; p.total_q = total_q; p.total_k = total_k; p.H = H; p.causal = causal;
     const int64_t items = most_blocks(B, total_q) * H;
-    p.parts = parts_of(items, total_k, sms);
+    p.parts = parts_of(items, B, total_k, sms);
     const int64_t fit = kL2Keys / ((int64_t)(total_k > 0 ? total_k : 1) * 2 * (kMlaNope + kMlaV));
     p.heads_at_once = (int)(fit < 1 ? 1 : fit < H ? fit : H);
     p.scale = sm_scale;
@@ -709,8 +816,9 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     p.qn_r = qn_ld_r; p.qn_h = qn_ld_h; p.qr_r = qr_ld_r; p.qr_h = qr_ld_h;
     p.kn_r = kn_ld_r; p.kn_h = kn_ld_h; p.kr_r = kr_ld_r; p.v_r = v_ld_r; p.v_h = v_ld_h;
     p.out = (__nv_bfloat16 *)out_dev; p.lse = lse_dev;
-    p.part_out = (float *)workspace_dev;
+    p.part_out = (float *)((uint8_t *)workspace_dev + kCounterBytes);
     p.part_lse = p.part_out + (int64_t)p.parts * total_q * H * kMlaV;
+    p.wide = (((uintptr_t)(p.parts > 1 ? (void *)p.part_out : out_dev)) & 31) == 0;
     p.status = status_dev;
 
     CUtensorMap qn, qr, kn, kr, v;
@@ -733,6 +841,11 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     NSA_CUDA_TRY(max_dynamic_smem<mla_prefill_kernel>((int)kSmem));
     const cudaStream_t s = (cudaStream_t)stream;
     const int64_t work = items * p.parts;
+    p.next = nullptr;
+    if (work > sms) {
+        p.next = (unsigned long long *)workspace_dev;
+        NSA_CUDA_TRY(cudaMemsetAsync(p.next, 0, sizeof(*p.next), s));
+    }
     mla_prefill_kernel<<<(unsigned)(work < sms ? work : sms), kThreads, kSmem, s>>>(qn, qr, kn, kr, v, p);
     if (launch_status() != NSA_OK) return NSA_ERR_CUDA;
     if (p.parts == 1) return NSA_OK;
