@@ -48,6 +48,11 @@ merge_kernel(const MergeParts parts, int64_t rows, int units, Out *out, float *l
     const int per = kThreads / units, r = threadIdx.x / units, u = threadIdx.x - r * units;
     const int64_t row = (int64_t)blockIdx.x * per + r;
     int64_t from = 0;
+    int n = NP;
+    if (parts.used) {
+        n = *parts.used;
+        if (n <= 1) return;
+    }
     if (parts.live_to) {
         from = (int64_t)*parts.live_from * parts.live_rows;
         rows = min(rows, (int64_t)*parts.live_to * parts.live_rows);
@@ -57,7 +62,7 @@ merge_kernel(const MergeParts parts, int64_t rows, int units, Out *out, float *l
     float l[NP], x[NP][kVec], o[kVec], top = -INFINITY, total = 0.f;
     if (live) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) l[i] = parts.lse[i][row];
+        for (int i = 0; i < NP; ++i) l[i] = i < n ? parts.lse[i][row] : -INFINITY;
         // a part that saw no key is not looked at: its values have weight 0, whatever they are
 #pragma unroll
         for (int i = 0; i < NP; ++i) {

@@ -56,6 +56,8 @@ struct MergeParts {
     // NULL, or on the device: only rows from *live_from x live_rows up to *live_to x live_rows are written
     const int32_t *live_from, *live_to;
     int live_rows;
+    // NULL, or on the device: how many of the parts there are; nothing is written if there is one
+    const int32_t *used;
 };
 nsa_status merge_launch(nsa_dtype part_dtype, nsa_dtype out_dtype, int n, const MergeParts &parts, int64_t rows, int D,
                         void *out, float *lse, bool behind_previous, cudaStream_t stream);

@@ -44,6 +44,7 @@ constexpr int kHalf = kTile / 2;
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kScanWarp = 18, kScanWarps = 2;
 constexpr int kThreads = 32 * (kScanWarp + kScanWarps);  // 20 warps: a 21st would leave each thread 80 registers instead of 96
 constexpr uint32_t kTmemCols = 512;        // S / P of tile t at 128 t, O at 256 + 128 t
+constexpr float kJoinCost = 1.5f;           // steps
 constexpr float kRescale = 8.0f;           // log2 units
 
 // One work item, as the loading warp hands it to the others.
@@ -56,7 +57,7 @@ struct Item {
     int vis0;          // keys that the first query sees (causal: one more each further query); may be negative
     int j0, j1;        // steps of this share, none if j0 >= j1
     int n[2];          // steps that each tile needs at most
-    int part;
+    int part, parts;
 };
 
 struct Shared {
@@ -81,15 +82,16 @@ struct Params {
     const int32_t *cu_q, *cu_k;
     int B, total_q, total_k, H, causal;
     int heads_at_once;   // heads whose keys and values stay in L2 while all queries pass
-    int parts;
-    int wide;            // the results' addresses are multiples of 32 bytes
+    int most_parts;      // 1, or as many as the workspace holds
+    int wide;            // the results' addresses are multiples of 32 bytes: out's (bit 0), the parts' (bit 1)
     float scale, scale_log2;
     // for the values that are not finite
     const __nv_bfloat16 *q_nope, *q_rope, *k_nope, *k_rope, *v;
     int64_t qn_r, qn_h, qr_r, qr_h, kn_r, kn_h, kr_r, v_r, v_h;
     __nv_bfloat16 *out;
     float *lse;
-    float *part_out, *part_lse;
+    float *part_out, *part_lse;  // [parts][total_q][H][128], [most_parts][total_q][H]
+    int32_t *parts_used;         // for the join; NULL: most_parts is 1
     unsigned long long *next;  // the items taken beyond each CTA's first; NULL: one each is all
     int32_t *status;
 };
@@ -139,22 +141,58 @@ __device__ __forceinline__ int scan_blocks(int blocks, int lane)
     return blocks;
 }
 
-__device__ int64_t count_blocks(const Params &p, int lane)
+// What a call has to do, from the sequences' starts.
+struct Work {
+    int64_t blocks;  // of 256 queries
+    int parts;       // that the keys of each are cut into
+};
+
+// Parts: where there are few items, or a few long ones, their keys are cut into shares.  In units of a
+// step (1.9 us): the SMs' even share of all steps, the longest share as what the last of them may
+// be late by, two steps an item for its start and end, and for the join its launch and the fp32
+// results that it reads (0.13 us for 6 items on 152 SMs).
+__device__ Work plan(const Params &p, int lane)
 {
-    int64_t n = 0;
-    for (int b = lane; b < p.B; b += 32) n += (request(p, b).y + kBlock - 1) / kBlock;
-    for (int o = 16; o > 0; o /= 2) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
+    int64_t n = 0, steps = 0, longest = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const int4 r = request(p, b);
+        const int blocks = (r.y + kBlock - 1) / kBlock;
+        n += blocks;
+        if (p.most_parts == 1) continue;
+        for (int i = 0; i < blocks; ++i) {  // few: the launch allows parts for few items alone
+            const int vis = p.causal ? min(r.w, r.w - r.y + min(r.y, (i + 1) * kBlock)) : r.w;
+            const int64_t s = vis > 0 ? (vis + kTile - 1) / kTile : 0;
+            steps += s;
+            longest = max(longest, s);
+        }
+    }
+    for (int o = 16; o > 0; o /= 2) {
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+        steps += __shfl_xor_sync(0xffffffffu, steps, o);
+        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    }
+    Work w = {n, 1};
+    const float items = (float)(n * p.H), all = (float)(steps * p.H), sms = (float)gridDim.x;
+    float best = INFINITY;
+    for (int c = 1; c <= p.most_parts && (c == 1 || c <= longest); ++c) {
+        const float share = ceilf((float)longest / c), each = items * c;
+        const float cost = (each <= sms ? share + 2.f : (all + 2.f * each) / sms + share) + (c > 1 ? kJoinCost + each / 90.f : 0.f);
+        if (cost < best) {
+            best = cost;
+            w.parts = c;
+        }
+    }
+    return w;
 }
 
 // Item w of blocks x H x parts.  Heads go in sections; in a section all heads of a block of queries
 // follow one another, and a request's blocks go from its last, which sees most keys, to its first.
-__device__ Item decode(const Params &p, int64_t w, int64_t blocks, int lane)
+__device__ Item decode(const Params &p, int64_t w, const Work &todo, int lane)
 {
     Item it;
-    it.part = (int)(w % p.parts);
-    w /= p.parts;
-    const int64_t per = blocks * p.heads_at_once;
+    it.part = (int)(w % todo.parts);
+    w /= todo.parts;
+    const int64_t per = todo.blocks * p.heads_at_once;
     const int section = (int)(w / per);
     w -= section * per;
     const int h0 = section * p.heads_at_once, hs = min(p.heads_at_once, p.H - h0);
@@ -189,8 +227,9 @@ __device__ Item decode(const Params &p, int64_t w, int64_t blocks, int lane)
         it.n[t] = rows > kTile * t && vis > 0 ? (vis + kTile - 1) / kTile : 0;
         all = max(all, it.n[t]);
     }
-    it.j0 = (int)((int64_t)all * it.part / p.parts);
-    it.j1 = (int)((int64_t)all * (it.part + 1) / p.parts);
+    it.j0 = (int)((int64_t)all * it.part / todo.parts);
+    it.j1 = (int)((int64_t)all * (it.part + 1) / todo.parts);
+    it.parts = todo.parts;
     return it;
 }
 
@@ -276,12 +315,14 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ items and loads
-        const int64_t blocks = count_blocks(p, lane), total = blocks * p.H * p.parts;
+        const Work todo = plan(p, lane);
+        const int64_t total = todo.blocks * p.H * todo.parts;
+        if (p.parts_used && blockIdx.x == 0 && lane == 0) *p.parts_used = todo.parts;
         uint32_t g = 0, q_uses = 0;  // steps and Q buffers filled so far
         int64_t w = blockIdx.x;
         Item next;
         next.head = -1;
-        if (w < total) next = decode(p, w, blocks, lane);
+        if (w < total) next = decode(p, w, todo, lane);
         // K of step g takes the slots of K (its last) and V of step g - 2, V those of K of step g - 1
         uint32_t k_sent = 0, v_sent = 0;
         const auto load_k = [&](const Item &it, int j) {
@@ -349,7 +390,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 w += gridDim.x;
             }
             next.head = -1;
-            if (w < total) next = decode(p, w, blocks, lane);
+            if (w < total) next = decode(p, w, todo, lane);
             if (some && lane == 0) {
                 for (int j = it.j0 + 1; j < it.j1 && ok; ++j, ++g) {
                     load_k(it, j);
@@ -682,14 +723,14 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
 #pragma unroll
                             for (int y = 0; y < 32; ++y) o[y] = 0.f;
                         }
-                        if (p.parts > 1) {
+                        if (it.parts > 1) {
                             float *dst = p.part_out + ((int64_t)it.part * p.total_q * p.H + at) * kMlaV + col;
 #pragma unroll
                             for (int y = 0; y < 4; ++y) {
                                 uint32_t v[8];
 #pragma unroll
                                 for (int z = 0; z < 8; ++z) v[z] = __float_as_uint(o[8 * y + z] * inv);
-                                store_sector(dst + 8 * y, v, p.wide);
+                                store_sector(dst + 8 * y, v, p.wide & 2);
                             }
                         } else {
                             __nv_bfloat16 *dst = p.out + at * kMlaV + col;
@@ -698,7 +739,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                                 uint32_t v[8];
 #pragma unroll
                                 for (int z = 0; z < 8; ++z) v[z] = pack_bf16(o[16 * y + 2 * z] * inv, o[16 * y + 2 * z + 1] * inv);
-                                store_sector(dst + 16 * y, v, p.wide);
+                                store_sector(dst + 16 * y, v, p.wide & 1);
                             }
                         }
                     }
@@ -706,7 +747,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 }
                 if (mine && half == 0) {
                     const float lse = l > 0.f ? fmaf(m, p.scale, logf(l)) : l == l ? -INFINITY : l;
-                    if (p.parts > 1) p.part_lse[(int64_t)it.part * p.total_q * p.H + at] = lse;
+                    if (it.parts > 1) p.part_lse[(int64_t)it.part * p.total_q * p.H + at] = lse;
                     else p.lse[at] = lse;
                 }
             }
@@ -732,25 +773,17 @@ int64_t most_blocks(int B, int total_q)
     return n < total_q ? n : total_q;
 }
 
-// Shares that the keys of an item are cut into where there are fewer than kPartItems items an SM: those
-// whose rounds over the SMs take the fewest steps, an item counted with two steps beside its own and
-// the join with kJoinSteps.  At least kPartSteps steps a share.
-constexpr int kPartItems = 4, kPartSteps = 4, kJoinSteps = 6;
-int parts_of(int64_t items, int B, int total_k, int sms)
+// Parts are for calls of fewer items an SM than this, which bounds the workspace.
+constexpr int kPartItems = 8;
+constexpr size_t kHeadBytes = 256;  // of the workspace, before the parts: the items taken, the parts made
+
+int most_parts_of(int total_q, int total_k, int H, int sms)
 {
-    const int64_t steps = ceil_div(total_k, (int64_t)kTile * B);
-    int best = 1;
-    int64_t cost = ceil_div(items, sms) * (steps + 2);
-    for (int n = 2; n <= kMaxMergeParts && items * n <= (int64_t)kPartItems * sms && steps >= n * kPartSteps; ++n) {
-        const int64_t c = ceil_div(items * n, sms) * (ceil_div(steps, n) + 2) + kJoinSteps;
-        if (c < cost) {
-            cost = c;
-            best = n;
-        }
-    }
-    return best;
+    const int64_t items = ceil_div(total_q, kBlock) * H;  // at least
+    if (items >= (int64_t)kPartItems * sms || total_k <= 2 * kTile) return 1;
+    const int64_t fit = (int64_t)kPartItems * sms * kBlock / ((int64_t)total_q * H);
+    return (int)(fit < 1 ? 1 : fit < kMaxMergeParts ? fit : kMaxMergeParts);
 }
-constexpr size_t kCounterBytes = 256;  // of the workspace, before the parts
 
 // Heads whose keys and values (512 bytes a key) are to stay in L2 together.
 constexpr int64_t kL2Keys = 40LL << 20;
@@ -760,9 +793,9 @@ constexpr int64_t kL2Keys = 40LL << 20;
 
 extern "C" size_t nsa_mla_prefill_workspace_bytes(void)
 {
-    // parts_of: parts x items <= kPartItems x SMs, of 256 queries each
+    // most_parts_of: parts x queries x heads <= kPartItems x SMs x 256
     const int sms = nsa::current_sm_count();
-    return nsa::kCounterBytes + (size_t)(sms > 0 ? sms : 0) * nsa::kPartItems * nsa::kBlock * (nsa::kMlaV + 1) * sizeof(float);
+    return nsa::kHeadBytes + (size_t)(sms > 0 ? sms : 0) * nsa::kPartItems * nsa::kBlock * (nsa::kMlaV + 1) * sizeof(float);
 }
 
 extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, int64_t qn_ld_h, const void *q_rope_dev,
@@ -805,7 +838,7 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     p.cu_q = cu_seqlens_q_dev; p.cu_k = cu_seqlens_k_dev;
     p.B = B; p.total_q = total_q; p.total_k = total_k; p.H = H; p.causal = causal;
     const int64_t items = most_blocks(B, total_q) * H;
-    p.parts = parts_of(items, B, total_k, sms);
+    p.most_parts = most_parts_of(total_q, total_k, H, sms);
     const int64_t fit = kL2Keys / ((int64_t)(total_k > 0 ? total_k : 1) * 2 * (kMlaNope + kMlaV));
     p.heads_at_once = (int)(fit < 1 ? 1 : fit < H ? fit : H);
     p.scale = sm_scale;
@@ -816,9 +849,10 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     p.qn_r = qn_ld_r; p.qn_h = qn_ld_h; p.qr_r = qr_ld_r; p.qr_h = qr_ld_h;
     p.kn_r = kn_ld_r; p.kn_h = kn_ld_h; p.kr_r = kr_ld_r; p.v_r = v_ld_r; p.v_h = v_ld_h;
     p.out = (__nv_bfloat16 *)out_dev; p.lse = lse_dev;
-    p.part_out = (float *)((uint8_t *)workspace_dev + kCounterBytes);
-    p.part_lse = p.part_out + (int64_t)p.parts * total_q * H * kMlaV;
-    p.wide = (((uintptr_t)(p.parts > 1 ? (void *)p.part_out : out_dev)) & 31) == 0;
+    p.part_out = (float *)((uint8_t *)workspace_dev + kHeadBytes);
+    p.part_lse = p.part_out + (int64_t)p.most_parts * total_q * H * kMlaV;
+    p.wide = (((uintptr_t)out_dev & 31) == 0 ? 1 : 0) | (((uintptr_t)p.part_out & 31) == 0 ? 2 : 0);
+    p.parts_used = p.most_parts > 1 ? (int32_t *)workspace_dev + 16 : nullptr;
     p.status = status_dev;
 
     CUtensorMap qn, qr, kn, kr, v;
@@ -840,7 +874,7 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     if (!mapped) return NSA_ERR_CUDA;
     NSA_CUDA_TRY(max_dynamic_smem<mla_prefill_kernel>((int)kSmem));
     const cudaStream_t s = (cudaStream_t)stream;
-    const int64_t work = items * p.parts;
+    const int64_t work = items * p.most_parts;
     p.next = nullptr;
     if (work > sms) {
         p.next = (unsigned long long *)workspace_dev;
@@ -848,14 +882,15 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     }
     mla_prefill_kernel<<<(unsigned)(work < sms ? work : sms), kThreads, kSmem, s>>>(qn, qr, kn, kr, v, p);
     if (launch_status() != NSA_OK) return NSA_ERR_CUDA;
-    if (p.parts == 1) return NSA_OK;
+    if (p.most_parts == 1) return NSA_OK;
     MergeParts parts = {};
-    for (int i = 0; i < p.parts; ++i) {
+    for (int i = 0; i < p.most_parts; ++i) {
         parts.out[i] = p.part_out + (int64_t)i * total_q * H * kMlaV;
         parts.lse[i] = p.part_lse + (int64_t)i * total_q * H;
     }
     parts.live_from = cu_seqlens_q_dev;
     parts.live_to = cu_seqlens_q_dev + B;
     parts.live_rows = H;
-    return merge_launch(NSA_DT_F32, NSA_DT_BF16, p.parts, parts, (int64_t)total_q * H, kMlaV, out_dev, lse_dev, true, s);
+    parts.used = p.parts_used;
+    return merge_launch(NSA_DT_F32, NSA_DT_BF16, p.most_parts, parts, (int64_t)total_q * H, kMlaV, out_dev, lse_dev, true, s);
 }
