@@ -677,21 +677,32 @@ _D_LATENT, _D_ROPE, _D_NOPE, _D_V = 512, 64, 128, 128
 
 def _bf16(name: str, t: torch.Tensor, shape, contiguous: bool = True) -> torch.Tensor:
     """A bf16 tensor of this shape (None: any size there), contiguous or with an adjacent last dimension."""
-    packed = t.is_contiguous() if contiguous else t.dim() > 0 and (t.shape[-1] <= 1 or t.stride(-1) == 1)
-    if t.dtype != torch.bfloat16 or t.dim() != len(shape) or not packed or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        want = ", ".join("any" if n is None else str(n) for n in shape)
-        raise ValueError(f"{name} must be bf16 [{want}], {'contiguous' if contiguous else 'its last dimension adjacent'}, "
-                         f"got shape {tuple(t.shape)}, strides {t.stride()} of {t.dtype}")
-    return t
+    if t.dtype is torch.bfloat16 and (t.shape == shape or (
+            None in shape and t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)))):
+        if t.is_contiguous() or (not contiguous and (t.stride(-1) == 1 or t.shape[-1] <= 1)):
+            return t
+    want = ", ".join("any" if n is None else str(n) for n in shape)
+    raise ValueError(f"{name} must be bf16 [{want}], {'contiguous' if contiguous else 'its last dimension adjacent'}, "
+                     f"got shape {tuple(t.shape)}, strides {t.stride()} of {t.dtype}")
+
+
+def _rows(name: str, t: torch.Tensor, d: int, heads: Optional[int] = None):
+    """(rows, heads) of a bf16 tensor [rows, heads, d] (None: any number) whose last dimension is adjacent."""
+    shape = t.shape
+    if len(shape) == 3 and shape[2] == d and (heads is None or shape[1] == heads) and t.dtype is torch.bfloat16 and \
+            t.stride(2) == 1:
+        return shape[0], shape[1]
+    return _bf16(name, t, (None, heads, d), False).shape[:2]
 
 
 def _heads_of(w: torch.Tensor) -> int:
     """The heads of an up-projection."""
-    if w.dim() != 2 or w.shape[0] < 1 or w.shape[0] % (_D_NOPE + _D_V):
+    n = w.shape[0] if w.dim() == 2 else 0
+    if n < 1 or n % (_D_NOPE + _D_V):
         raise ValueError(f"w must be bf16 [heads * {_D_NOPE + _D_V}, {_D_LATENT}], got shape {tuple(w.shape)}")
-    _bf16("w", w, (None, _D_LATENT))
-    return w.shape[0] // (_D_NOPE + _D_V)
+    if w.shape[1] != _D_LATENT or w.dtype is not torch.bfloat16 or not w.is_contiguous():
+        _bf16("w", w, (None, _D_LATENT))
+    return n // (_D_NOPE + _D_V)
 
 
 def nsa_mla_expand_kv_workspace_bytes(m: int) -> int:
@@ -739,24 +750,25 @@ def nsa_mla_prefill(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Te
     """q_nope [total_q, H, 128], q_rope [total_q, H, 64], k_nope and v [total_k, H, 128] (any row / head strides),
     k_rope [total_k, 64]; cu_seqlens_q / cu_seqlens_k int32 [B + 1]; out bf16 [total_q, H, 128], lse float32
     [total_q, H].  workspace: alloc_mla_prefill_workspace's."""
-    total_q, H, _ = _bf16("q_nope", q_nope, (None, None, _D_NOPE), False).shape
+    total_q, H = _rows("q_nope", q_nope, _D_NOPE)
     total_k, B = _bf16("k_rope", k_rope, (None, _D_ROPE), False).shape[0], cu_seqlens_q.numel() - 1
     _bf16("q_rope", q_rope, (total_q, H, _D_ROPE), False)
     _bf16("k_nope", k_nope, (total_k, H, _D_NOPE), False)
     _bf16("v", v, (total_k, H, _D_V), False)
     _bf16("out", out, (total_q, H, _D_V))
-    if tuple(lse.shape) != (total_q, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    if lse.shape != (total_q, H) or lse.dtype is not torch.float32 or not lse.is_contiguous():
         raise ValueError(f"lse must be contiguous float32 [{total_q}, {H}], got shape {tuple(lse.shape)} of {lse.dtype}")
     _i32("cu_seqlens_q", cu_seqlens_q, max(B, 0) + 1)
     _i32("cu_seqlens_k", cu_seqlens_k, B + 1)
     ws_bytes = _scratch(workspace)
     _status_word(status)
     handle = _launch_on(stream, q_nope, q_rope, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace, status)
-    rc = load().nsa_mla_prefill(_at(q_nope), q_nope.stride(0), q_nope.stride(1), _at(q_rope), q_rope.stride(0),
-                                q_rope.stride(1), _at(k_nope), k_nope.stride(0), k_nope.stride(1), _at(k_rope),
-                                k_rope.stride(0), _at(v), v.stride(0), v.stride(1), _at(cu_seqlens_q), _at(cu_seqlens_k), B,
-                                total_q, total_k, H, _D_NOPE, _D_ROPE, _D_V, 1 if causal else 0, float(sm_scale), _at(out),
-                                _at(lse), _at(workspace), ws_bytes, _at(status), handle)
+    qn, qr, kn, vv = q_nope.stride(), q_rope.stride(), k_nope.stride(), v.stride()
+    rc = load().nsa_mla_prefill(q_nope.data_ptr(), qn[0], qn[1], q_rope.data_ptr(), qr[0], qr[1], k_nope.data_ptr(), kn[0],
+                                kn[1], k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), vv[0], vv[1],
+                                cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, total_q, total_k, H, _D_NOPE, _D_ROPE,
+                                _D_V, 1 if causal else 0, sm_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                ws_bytes, _at(status), handle)
     _check("nsa_mla_prefill", rc)
 
 
@@ -769,13 +781,14 @@ def nsa_merge_attention(parts, lses, out: torch.Tensor, lse: torch.Tensor, strea
     n = len(parts)
     if n < 1 or len(lses) != n:
         raise ValueError(f"expected as many lse as parts, at least one: got {len(lses)} and {n}")
-    shape, dtype = tuple(out.shape), parts[0].dtype
+    shape, dtype = out.shape, parts[0].dtype
+    rows = shape[:-1]
     if dtype not in _DTYPES or out.dtype not in _DTYPES:
         raise ValueError(f"parts and out must be float32 or bf16, got {dtype} and {out.dtype}")
-    for p, l in zip(list(parts) + [out], list(lses) + [lse]):
-        if tuple(p.shape) != shape or tuple(l.shape) != shape[:-1] or len(shape) < 1 or not p.is_contiguous() or \
-                not l.is_contiguous() or l.dtype != torch.float32 or (p is not out and p.dtype != dtype):
-            raise ValueError(f"parts must be contiguous {dtype} {list(shape)} and lses contiguous float32 {list(shape[:-1])}, "
+    for p, l in ((out, lse), *zip(parts, lses)):
+        if p.shape != shape or l.shape != rows or len(shape) < 1 or not p.is_contiguous() or not l.is_contiguous() or \
+                l.dtype is not torch.float32 or (p is not out and p.dtype is not dtype):
+            raise ValueError(f"parts must be contiguous {dtype} {list(shape)} and lses contiguous float32 {list(rows)}, "
                              f"got {p.dtype} {list(p.shape)} and {l.dtype} {list(l.shape)}")
     handle = _launch_on(stream, out, lse, *parts, *lses)
     ptrs, lptrs = (C.c_void_p * n)(*[p.data_ptr() for p in parts]), (C.c_void_p * n)(*[l.data_ptr() for l in lses])
@@ -787,7 +800,7 @@ def nsa_mla_absorb_q(q_nope: torch.Tensor, w: torch.Tensor, out: torch.Tensor, s
                      stream=None) -> None:
     """q_nope [R, H, 128] (any row / head strides) through each head's W_k: out [R, H, 512]."""
     H = _heads_of(w)
-    R = _bf16("q_nope", q_nope, (None, H, _D_NOPE), False).shape[0]
+    R, _ = _rows("q_nope", q_nope, _D_NOPE, H)
     _bf16("out", out, (R, H, _D_LATENT))
     _status_word(status)
     handle = _launch_on(stream, q_nope, w, out, status)
@@ -799,7 +812,7 @@ def nsa_mla_project_v(latent: torch.Tensor, w: torch.Tensor, out: torch.Tensor, 
                       stream=None) -> None:
     """latent [R, H, 512] (any row / head strides) through each head's W_v: out [R, H, 128]."""
     H = _heads_of(w)
-    R = _bf16("latent", latent, (None, H, _D_LATENT), False).shape[0]
+    R, _ = _rows("latent", latent, _D_LATENT, H)
     _bf16("out", out, (R, H, _D_V))
     _status_word(status)
     handle = _launch_on(stream, latent, w, out, status)

@@ -15,13 +15,13 @@ constexpr int kVec = 8;  // values a thread
 
 __device__ __forceinline__ void load8(const float *p, float (&v)[kVec])
 {
-    const float4 a = *(const float4 *)p, b = *(const float4 *)(p + 4);
+    const float4 a = __ldcs((const float4 *)p), b = __ldcs((const float4 *)(p + 4));
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[kVec])
 {
-    const uint4 w = *(const uint4 *)p;
+    const uint4 w = __ldcs((const uint4 *)p);
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -63,12 +63,13 @@ merge_kernel(const MergeParts parts, int64_t rows, int units, Out *out, float *l
     if (live) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) l[i] = i < n ? parts.lse[i][row] : -INFINITY;
-        // a part that saw no key is not looked at: its values have weight 0, whatever they are
+        // (read without a look at the lse, so that one latency covers both)
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            if (i < n) load8((const In *)parts.out[i] + at, x[i]);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            if (l[i] != -INFINITY) {
-                load8((const In *)parts.out[i] + at, x[i]);
-            } else {
+            if (l[i] == -INFINITY) {  // a part that saw no key has weight 0, whatever its values are
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) x[i][j] = 0.f;
             }

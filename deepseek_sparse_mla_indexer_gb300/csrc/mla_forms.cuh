@@ -29,6 +29,14 @@ __device__ __forceinline__ bool mla_wait(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 
+// Arrives on the barrier at this offset in CTA `rank` of the cluster, as word that tensor-core or TMA operations are
+// done: no thread's own writes go with it, so it and its wait keep to the scope of a CTA (with the cluster's,
+// each of them orders all memory and takes as long as a product of 256 x 256 x 64).
+__device__ __forceinline__ void mbar_tell(uint64_t *bar, uint32_t rank)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(sm100::dsmem_addr(bar, rank)) : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     uint32_t r;

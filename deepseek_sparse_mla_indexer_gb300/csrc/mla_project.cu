@@ -26,7 +26,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
 constexpr int kSmemMax = 227 * 1024;
 
-constexpr int chunk_of(int N) { return N >= 64 ? 32 : 16; }  // rows that a group of four warps stages
+constexpr int chunk_of(int N) { return N >= 64 ? 32 : 16; }  // rows that a group of four warps stages at a time
 constexpr uint32_t x_stage(int N) { return (uint32_t)N * kStep * 2; }
 constexpr uint32_t staging_of(int N) { return 2 * 2 * chunk_of(N) * kFeat * 2; }  // two groups, two buffers
 constexpr int kMaxStages = 12;
@@ -56,13 +56,86 @@ struct PParams {
     int32_t *status;
 };
 
+// ------------------------------------------------------------ accumulators to rows
+
+// 16 lanes x 8 CH / 8 columns of the warp's 32 lanes: thread i gets lanes i / 4 and i / 4 + 8, of every eight
+// columns 2 (i % 4) and the one behind it (registers 4 b .. 4 b + 3 of columns 8 b ..).
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit values, each turned over: a block's columns become the 16-byte rows whose addresses
+// lanes 8 b .. 8 b + 7 give.
+__device__ __forceinline__ void store_blocks_turned(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+// One tile's accumulator (128 features in the lanes, N rows in the columns from `acc` on) as bf16 rows to
+// out[row0 ..][head][feat0 ..].  A group of four warps takes every other CH rows: through two staging buffers of
+// [2][CH][64 features], 128-byte swizzled so that the turned blocks' rows fall into different banks.
+template <int N>
+__device__ __forceinline__ void rows_out(const CUtensorMap &out_map, uint32_t acc, uint8_t *stage_s, int &n_store, int feat0,
+                                         int head, int row0)
+{
+    constexpr int CH = chunk_of(N);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, group = warp >> 2, quarter = warp & 3;
+    const bool leader = (threadIdx.x & 127) == 0;
+    const uint32_t lanes = acc + ((uint32_t)(quarter * 32) << 16);
+    for (int k = group; k < N / CH; k += 2, ++n_store) {
+        uint8_t *o = stage_s + (group * 2 + (n_store & 1)) * (CH * kFeat * 2);
+        uint32_t v[2][CH / 2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) tmem_ld_16x256(lanes + ((uint32_t)(16 * x) << 16) + k * CH, v[x]);
+        if (leader) bulk_wait_read_1();  // the store before last has read this buffer
+        __syncwarp();
+        tmem_ld_wait();
+        bar_sync(1 + group, 128);
+        // blocks of 8 features x 8 rows: lanes 0 .. 7, 8 .. 15 of this half; rows 8 b .., 8 b + 8 ..
+        const uint32_t half = smem_u32(o) + (quarter >> 1) * (CH * 128);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int b = 0; b < CH / 8; b += 2) {
+                const int r = 8 * b + (lane & 7) + (lane >= 16 ? 8 : 0), c16 = (quarter & 1) * 4 + x * 2 + (lane >> 3 & 1);
+                const uint32_t *u = &v[x][4 * b];
+                store_blocks_turned(half + sw128_offset(r, c16), pack_bf16(__uint_as_float(u[0]), __uint_as_float(u[1])),
+                                    pack_bf16(__uint_as_float(u[2]), __uint_as_float(u[3])),
+                                    pack_bf16(__uint_as_float(u[4]), __uint_as_float(u[5])),
+                                    pack_bf16(__uint_as_float(u[6]), __uint_as_float(u[7])));
+            }
+        fence_proxy_async_smem();
+        bar_sync(1 + group, 128);
+        if (leader) {
+            tma_store_3d(&out_map, feat0, head, row0 + k * CH, o);
+            tma_store_3d(&out_map, feat0 + 64, head, row0 + k * CH, o + CH * 128);
+            bulk_commit();
+        }
+        __syncwarp();
+    }
+}
+
 // MN_W: W_k, whose tile of 128 features x 64 is two boxes of 64 features, [64][64 features].
 template <int N, bool MN_W>
 __global__ void __launch_bounds__(kThreads, 1)
 head_product_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
                     const __grid_constant__ CUtensorMap out_map, PParams p)
 {
-    constexpr int ST = stages_of(N), CH = chunk_of(N);
+    constexpr int ST = stages_of(N);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *w_s = base, *x_s = w_s + ST * kWStage, *stage_s = x_s + ST * x_stage(N);
@@ -165,12 +238,9 @@ head_product_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_cons
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------------------ one feature a thread, out through shared memory
+        // ------------------------------------------------------------ rows out
         const int group = warp >> 2;
         const bool leader = (threadIdx.x & 127) == 0;
-        uint8_t *out_s = stage_s + group * (2 * CH * kFeat * 2);
-        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const int feat = (warp & 3) * 32 + lane;
         int i = 0, n_store = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
@@ -185,26 +255,7 @@ head_product_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_cons
                 ok = false;
                 break;
             }
-            for (int k = group; k < N / CH; k += 2, ++n_store) {
-                uint8_t *o = out_s + (n_store & 1) * (CH * kFeat * 2);
-                uint32_t v[CH];
-                if constexpr (CH == 32) tmem_ld32(lanes + buf * N + k * CH, v);
-                else tmem_ld16(lanes + buf * N + k * CH, v);
-                if (leader) bulk_wait_read_1();  // the store before last has read this buffer
-                __syncwarp();
-                tmem_ld_wait();
-                bar_sync(1 + group, 128);
-#pragma unroll
-                for (int r = 0; r < CH; ++r)
-                    *(__nv_bfloat16 *)(o + r * (kFeat * 2) + feat * 2) = __float2bfloat16_rn(__uint_as_float(v[r]));
-                fence_proxy_async_smem();
-                bar_sync(1 + group, 128);
-                if (leader) {
-                    tma_store_3d(&out_map, c * kFeat, h, rt * N + k * CH, o);
-                    bulk_commit();
-                }
-                __syncwarp();
-            }
+            rows_out<N>(out_map, tmem + buf * N, stage_s, n_store, c * kFeat, h, rt * N);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->acc_empty[buf]);
@@ -218,6 +269,220 @@ head_product_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_cons
     if (warp == kEpiWarps) {
         tmem_relinquish();
         tmem_dealloc(tmem, tmem_cols_of(N));
+    }
+}
+
+// ---------------------------------------------------------------- pairs of CTAs
+
+// Large products (nsa_mla_expand_kv of many rows): a 128 x 256 tile a CTA asks L2 for 96 bytes a cycle and SM at
+// the tensor core's rate, more than it gives (8192 rows, 128 heads: 203 us, 55 bytes a cycle).  Two CTAs
+// (cta_group::2) make a 256 x 256 tile together: each loads 128 rows of W and 128 rows of X, the
+// products read the other half of X from the pair's other shared memory, and it is 64.
+// CTA 0 issues for both.  CTA 1's loads count on CTA 0's barriers; what CTA 0 has to tell CTA 1 (a stage is free, an
+// accumulator is complete) goes from barrier to barrier by a warp of its own.
+constexpr int kPairRows = 256;
+constexpr uint32_t kPairStage = 2 * kWStage;  // a CTA's 128 rows of W and of X, 64 along the product's axis
+constexpr int kPairThreads = 32 * (kEpiWarps + 3);
+constexpr int kPairStages = (int)((kSmemMax - 2048 - staging_of(kPairRows)) / kPairStage);
+constexpr uint32_t kPairSmem = 1024 + kPairStages * kPairStage + staging_of(kPairRows) + 1024;
+static_assert(kPairSmem <= kSmemMax, "shared memory");
+
+struct PairShared {
+    uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2], drained;
+    uint32_t tmem;
+    volatile int abort;
+};
+static_assert(sizeof(PairShared) <= 1024, "the struct has 1 KB");
+
+// D[tmem of both CTAs] (+)= A B^T, each CTA's half of A and of B at the same place in its shared memory.
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+// TMA loads into this CTA that count on a barrier of either CTA of the pair (its address in the cluster).
+__device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+pair_product_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
+                    const __grid_constant__ CUtensorMap out_map, PParams p)
+{
+    constexpr int ST = kPairStages, N = kPairRows;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *w_s = base, *x_s = w_s + ST * kWStage, *stage_s = x_s + ST * kWStage;
+    PairShared *sm = (PairShared *)(stage_s + staging_of(N));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)cluster_ctarank();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&sm->full[i], 1);
+            mbar_init(&sm->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->acc_full[i], 1);
+            mbar_init(&sm->acc_empty[i], 2 * kEpiWarps);
+        }
+        mbar_init(&sm->drained, 1);
+        sm->abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&w_map);
+        prefetch_tensormap(&x_map);
+        prefetch_tensormap(&out_map);
+    }
+    if (warp == kEpiWarps) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(512)
+                     : "memory");
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();  // barriers of both CTAs before any arrival from the other
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem;
+    const int tiles = p.n_ft * p.n_rt, step = gridDim.x / 2;
+    volatile int *abort = &sm->abort;
+    bool ok = true;
+
+    if (warp == kEpiWarps) {
+        // ------------------------------------------------------------ loads of this CTA's halves
+        pdl_wait();
+        if (lane == 0) {
+            int st = 0;
+            uint32_t ph = 0;
+            for (int t = blockIdx.x / 2; t < tiles && ok; t += step) {
+                const int rt = t / p.n_ft, ft = t - rt * p.n_ft;
+                for (int s = 0; s < p.steps; ++s) {
+                    if (!(ok = mla_wait(&sm->empty[st], ph ^ 1, abort))) break;
+                    // CTA 0 expects both CTAs' halves; this stage's next round needs both, so no count runs ahead
+                    if (rank == 0) mbar_arrive_expect_tx(&sm->full[st], 2 * kPairStage);
+                    const uint32_t bar = dsmem_addr(&sm->full[st], 0);
+                    pair_load_2d(w_s + st * kWStage, &w_map, s * kStep, (2 * ft + rank) * kFeat, bar);
+                    pair_load_3d(x_s + st * kWStage, &x_map, s * kStep, 0, rt * N + rank * (N / 2), bar);
+                    if (++st == ST) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                set_status(p.status, NSA_ERR_TIMEOUT);
+                if (rank == 0)
+                    for (int i = 0; i < ST; ++i) mbar_wait(&sm->full[i], i < st ? ph : ph ^ 1, kMlaWait);
+            }
+        }
+    } else if (warp == kEpiWarps + 1 && rank == 0) {
+        // ------------------------------------------------------------ products of both CTAs
+        const uint32_t idesc = instr_desc(1, 1, 0, 0, 2 * kFeat, N);
+        const uint64_t w_desc = smem_desc(smem_u32(w_s), 16, 1024, kSwizzle128B);
+        const uint64_t x_desc = smem_desc(smem_u32(x_s), 16, 1024, kSwizzle128B);
+        int st = 0, i = 0;
+        uint32_t ph = 0;
+        for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++i) {
+            const uint32_t buf = i & 1, bph = (i >> 1) & 1;
+            ok = __all_sync(0xffffffffu, mla_wait(&sm->acc_empty[buf], bph ^ 1, abort));
+            for (int s = 0; s < p.steps && ok; ++s) {
+                ok = __all_sync(0xffffffffu, mla_wait(&sm->full[st], ph, abort));
+                tc_fence_after();
+                if (ok && elect_one()) {
+                    const uint64_t wd = w_desc + st * (kWStage / 16), xd = x_desc + st * (kWStage / 16);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mma_f16_pair(tmem + buf * N, wd + k * 2, xd + k * 2, idesc, s > 0 || k > 0);
+                    mma_commit_pair(&sm->empty[st]);
+                    if (s == p.steps - 1) mma_commit_pair(&sm->acc_full[buf]);
+                }
+                __syncwarp();
+                if (++st == ST) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            set_status(p.status, NSA_ERR_TIMEOUT);
+            mma_commit_pair(&sm->drained);  // products in flight end before the block does
+            mbar_wait(&sm->drained, 0, kMlaWait);
+        }
+        __syncwarp();
+    } else if (warp == kEpiWarps + 2 && rank == 0) {
+        // ------------------------------------------------------------ word to the other CTA
+        if (lane == 0) {
+            int st = 0, i = 0;
+            uint32_t ph = 0;
+            for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++i) {
+                for (int s = 0; s < p.steps && ok; ++s) {
+                    ok = mla_wait(&sm->empty[st], ph, abort);
+                    if (ok) mbar_tell(&sm->empty[st], 1);
+                    if (++st == ST) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+                if (ok) {
+                    ok = mla_wait(&sm->acc_full[i & 1], (i >> 1) & 1, abort);
+                    if (ok) mbar_tell(&sm->acc_full[i & 1], 1);
+                }
+            }
+            if (!ok) set_status(p.status, NSA_ERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp < kEpiWarps) {
+        // ------------------------------------------------------------ rows out
+        const int group = warp >> 2;
+        const bool leader = (threadIdx.x & 127) == 0;
+        int i = 0, n_store = 0;
+        for (int t = blockIdx.x / 2; t < tiles; t += step, ++i) {
+            const int rt = t / p.n_ft, ft = t - rt * p.n_ft;
+            const uint32_t buf = i & 1, bph = (i >> 1) & 1;
+            ok = mla_wait(&sm->acc_full[buf], bph, abort);
+            __syncwarp();
+            tc_fence_after();
+            if (bar_red_or(1 + group, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            rows_out<N>(out_map, tmem + buf * N, stage_s, n_store, (2 * ft + rank) * kFeat, 0, rt * N);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(&sm->acc_empty[buf]);
+                else mbar_tell(&sm->acc_empty[buf], 0);
+            }
+        }
+        if (!ok && lane == 0) set_status(p.status, NSA_ERR_TIMEOUT);
+        if (leader) bulk_wait_read();
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();  // neither CTA's shared memory or TMEM goes before the other is done with it
+    tc_fence_after();
+    if (warp == kEpiWarps) {
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 
@@ -262,7 +527,7 @@ nsa_status launch(const Problem &q, int sms, cudaStream_t stream)
         make_tma_3d(&x_map, bf, q.x, (uint64_t)q.K, (uint64_t)q.Hx, (uint64_t)q.R, (uint64_t)q.x_ld_h * 2,
                     (uint64_t)q.x_ld_r * 2, kStep, 1, N, CU_TENSOR_MAP_SWIZZLE_128B) &&
         make_tma_3d(&out_map, bf, q.out, (uint64_t)q.F, (uint64_t)q.Hx, (uint64_t)q.R, (uint64_t)q.F * 2,
-                    (uint64_t)q.F * q.Hx * 2, kFeat, 1, chunk_of(N), CU_TENSOR_MAP_SWIZZLE_NONE);
+                    (uint64_t)q.F * q.Hx * 2, 64, 1, chunk_of(N), CU_TENSOR_MAP_SWIZZLE_128B);
     if (!mapped) return NSA_ERR_CUDA;
     PParams p;
     p.ft_per_head = q.F / kFeat;
@@ -288,11 +553,50 @@ nsa_status launch(const Problem &q, int sms, cudaStream_t stream)
     return NSA_OK;
 }
 
+nsa_status launch_pairs(const Problem &q, int sms, cudaStream_t stream)
+{
+    CUtensorMap w_map, x_map, out_map;
+    const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const bool mapped =
+        make_tma_2d(&w_map, bf, q.w, kMlaLatent, (uint64_t)q.H * kMlaHeadRows, kMlaLatent * 2, 64, kFeat, CU_TENSOR_MAP_SWIZZLE_128B) &&
+        make_tma_3d(&x_map, bf, q.x, (uint64_t)q.K, 1, (uint64_t)q.R, (uint64_t)q.x_ld_h * 2, (uint64_t)q.x_ld_r * 2, kStep, 1,
+                    kPairRows / 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
+        make_tma_3d(&out_map, bf, q.out, (uint64_t)q.F, 1, (uint64_t)q.R, (uint64_t)q.F * 2, (uint64_t)q.F * 2, 64, 1,
+                    chunk_of(kPairRows), CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!mapped) return NSA_ERR_CUDA;
+    PParams p = {};
+    p.n_ft = q.F / (2 * kFeat);
+    p.n_rt = (int)ceil_div(q.R, kPairRows);
+    p.steps = q.K / kStep;
+    p.status = q.status;
+    const int64_t tiles = (int64_t)p.n_ft * p.n_rt;
+    if (tiles > (1 << 30)) return NSA_ERR_UNSUPPORTED;
+    NSA_CUDA_TRY(max_dynamic_smem<pair_product_kernel>(kPairSmem));
+    const int pairs = sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, pair_product_kernel, w_map, x_map, out_map, p));
+    return NSA_OK;
+}
+
+// Whether nsa_mla_expand_kv's product goes to pairs: from three rounds of their tiles on.
+bool pairs_for(const Problem &q, int sms)
+{
+    return q.after_gather && sms >= 2 && (int64_t)(q.F / (2 * kFeat)) * ceil_div(q.R, kPairRows) >= 3 * (sms / 2);
+}
+
 template <bool MN_W>
 nsa_status launch_n(const Problem &q, cudaStream_t stream)
 {
     const int sms = current_sm_count();
     if (sms <= 0) return NSA_ERR_CUDA;
+    if (pairs_for(q, sms)) return launch_pairs(q, sms, stream);
     switch (pick_n(q, sms)) {
     case 16: return launch<16, MN_W>(q, sms, stream);
     case 32: return launch<32, MN_W>(q, sms, stream);

@@ -17,7 +17,8 @@ def _cache(g, kv, slots):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
-@pytest.mark.parametrize("m,H", [(m, 1) for m in ROWS] + [(1, 16), (77, 5), (300, 3), (700, 16)])
+@pytest.mark.parametrize("m,H", [(m, 1) for m in ROWS] + [(1, 16), (77, 5), (300, 3), (700, 16)] +
+                         [(257, 128), (3651, 16), (2050, 27)])  # these on pairs of CTAs
 def test_expand(kv, m, H):
     g = torch.Generator().manual_seed(m)
     cache, w = _cache(g, kv, m + 9), F.weight(g, H)
