@@ -66,7 +66,7 @@ struct Shared {
     uint64_t q_full, q_empty;
     uint64_t s_full[2], go[2], o_full[2];  // go: P, and the values that it is multiplied with
     uint64_t item_full[2], item_empty[2];
-    uint64_t scanned[2], drained;
+    uint64_t drained;
     Item item[2];
     uint32_t odd[2][kMasked][4];  // masked step -> keys whose values are not all finite
     uint32_t tmem;
@@ -92,7 +92,7 @@ struct Params {
     float *lse;
     float *part_out, *part_lse;  // [parts][total_q][H][128], [most_parts][total_q][H]
     int32_t *parts_used;         // for the join; NULL: most_parts is 1
-    unsigned long long *next;  // the items taken beyond each CTA's first; NULL: one each is all
+    int *next;  // the items taken beyond each CTA's first; NULL: one each is all
     int32_t *status;
 };
 
@@ -143,7 +143,7 @@ __device__ __forceinline__ int scan_blocks(int blocks, int lane)
 
 // What a call has to do, from the sequences' starts.
 struct Work {
-    int64_t blocks;  // of 256 queries
+    int blocks;      // of 256 queries
     int parts;       // that the keys of each are cut into
 };
 
@@ -153,7 +153,8 @@ struct Work {
 // results that it reads (0.13 us for 6 items on 152 SMs).
 __device__ Work plan(const Params &p, int lane)
 {
-    int64_t n = 0, steps = 0, longest = 0;
+    int n = 0;
+    int64_t steps = 0, longest = 0;
     for (int b = lane; b < p.B; b += 32) {
         const int4 r = request(p, b);
         const int blocks = (r.y + kBlock - 1) / kBlock;
@@ -172,7 +173,7 @@ __device__ Work plan(const Params &p, int lane)
         longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
     }
     Work w = {n, 1};
-    const float items = (float)(n * p.H), all = (float)(steps * p.H), sms = (float)gridDim.x;
+    const float items = (float)n * (float)p.H, all = (float)(steps * p.H), sms = (float)gridDim.x;
     float best = INFINITY;
     for (int c = 1; c <= p.most_parts && (c == 1 || c <= longest); ++c) {
         const float share = ceilf((float)longest / c), each = items * c;
@@ -185,22 +186,25 @@ __device__ Work plan(const Params &p, int lane)
     return w;
 }
 
-// Item w of blocks x H x parts.  Heads go in sections; in a section all heads of a block of queries
+// Item w of blocks x H x parts (below 2^31: the launch checks); first_requests: request `lane`, kept between calls.  Heads go in sections; in a section all heads of a block of queries
 // follow one another, and a request's blocks go from its last, which sees most keys, to its first.
-__device__ Item decode(const Params &p, int64_t w, const Work &todo, int lane)
+__device__ Item decode(const Params &p, int w, const Work &todo, int4 first_requests, int lane)
 {
     Item it;
-    it.part = (int)(w % todo.parts);
-    w /= todo.parts;
-    const int64_t per = todo.blocks * p.heads_at_once;
-    const int section = (int)(w / per);
+    it.part = 0;
+    if (todo.parts > 1) {
+        const int all = w / todo.parts;
+        it.part = w - all * todo.parts;
+        w = all;
+    }
+    const int per = todo.blocks * p.heads_at_once, section = w / per;
     w -= section * per;
     const int h0 = section * p.heads_at_once, hs = min(p.heads_at_once, p.H - h0);
-    int64_t block = w / hs;
-    it.head = h0 + (int)(w - block * hs);
+    int block = w / hs;
+    it.head = h0 + (w - block * hs);
     for (int b0 = 0;; b0 += 32) {
         const int b = b0 + lane;
-        const int4 r = b < p.B ? request(p, b) : make_int4(0, 0, 0, 0);
+        const int4 r = b0 == 0 ? first_requests : b < p.B ? request(p, b) : make_int4(0, 0, 0, 0);
         const int mine = (r.y + kBlock - 1) / kBlock, upto = scan_blocks(mine, lane);
         const unsigned found = __ballot_sync(0xffffffffu, block < upto);
         if (!found && b0 + 32 < p.B) {
@@ -211,7 +215,7 @@ __device__ Item decode(const Params &p, int64_t w, const Work &todo, int lane)
         const int q0 = __shfl_sync(0xffffffffu, r.x, src), nq = __shfl_sync(0xffffffffu, r.y, src);
         const int k0 = __shfl_sync(0xffffffffu, r.z, src), nk = __shfl_sync(0xffffffffu, r.w, src);
         const int last = __shfl_sync(0xffffffffu, upto, src) - 1;
-        const int first = max(0, last - (int)block) * kBlock;
+        const int first = max(0, last - block) * kBlock;
         it.row0 = (int64_t)q0 + first;
         it.rows = found ? min(kBlock, nq - first) : 0;
         it.key0 = k0;
@@ -236,38 +240,94 @@ __device__ Item decode(const Params &p, int64_t w, const Work &todo, int lane)
 // The first step that some query of the item does not see wholly.
 __device__ __forceinline__ int first_masked(const Item &it) { return max(it.vis0, 0) / kTile; }
 
-// Adds what the zeroed values of this share's masked steps give to columns col .. col + 31 of a query's sum.
-__device__ __noinline__ void add_odd(const Params &p, const Item &it, const uint32_t (*odd)[4], int row, int vis, float m,
-                                     int col, float (&o)[32])
+// Where a query's result goes: 64 values from `col` on, times inv.
+struct Place {
+    void *dst;    // bf16 values of the result, or fp32 ones of a part
+    float inv;
+    bool whole, wide;
+};
+
+__device__ __forceinline__ Place place(const Params &p, const Item &it, int row, int col, float inv)
+{
+    const int64_t at = (it.row0 + row) * p.H + it.head;
+    Place to;
+    to.inv = inv;
+    to.whole = it.parts == 1;
+    to.wide = (p.wide & (to.whole ? 1 : 2)) != 0;
+    to.dst = to.whole ? (void *)(p.out + at * kMlaV + col)
+                      : (void *)(p.part_out + ((int64_t)it.part * p.total_q * p.H + at) * kMlaV + col);
+    return to;
+}
+
+// Values 32 x .. of the 64.
+__device__ __forceinline__ void store32(const Place &to, int x, const uint32_t (&o)[32])
+{
+    if (to.whole) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            uint32_t v[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+                v[z] = pack_bf16(__uint_as_float(o[16 * y + 2 * z]) * to.inv, __uint_as_float(o[16 * y + 2 * z + 1]) * to.inv);
+            store_sector((__nv_bfloat16 *)to.dst + 32 * x + 16 * y, v, to.wide);
+        }
+    } else {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            uint32_t v[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) v[z] = __float_as_uint(__uint_as_float(o[8 * y + z]) * to.inv);
+            store_sector((float *)to.dst + 32 * x + 8 * y, v, to.wide);
+        }
+    }
+}
+
+// The result of a warp's queries (64 values from `col` on a thread, sums at o_at) where values of this share's masked
+// steps were taken out as not finite: the queries that see them add them here, times their weights.
+__device__ __noinline__ void rows_with_odd(const Params &p, const Item &it, const uint32_t (*odd)[4], int row, int vis, float m,
+                                           float l, int col, uint32_t o_at)
 {
     const int64_t q = it.row0 + row;
-    for (int x = 0; x < kMasked; ++x) {
-        for (int pos = 0; pos < kTile; ++pos) {
-            const int j = (first_masked(it) + x) * kTile + pos;
-            if (j >= vis) return;
-            if (!(odd[x][pos / 32] >> (pos % 32) & 1)) continue;
-            const int64_t k = it.key0 + j;
-            float s = 0.f;
-            for (int d = 0; d < kMlaNope; ++d)
-                s = fmaf(__bfloat162float(p.q_nope[q * p.qn_r + it.head * p.qn_h + d]),
-                         __bfloat162float(p.k_nope[k * p.kn_r + it.head * p.kn_h + d]), s);
-            for (int d = 0; d < kMlaRope; ++d)
-                s = fmaf(__bfloat162float(p.q_rope[q * p.qr_r + it.head * p.qr_h + d]),
-                         __bfloat162float(p.k_rope[k * p.kr_r + d]), s);
-            const float w = ex2_approx(fmaf(s, p.scale_log2, m == -INFINITY ? 0.f : -m * p.scale_log2));
+    const Place to = place(p, it, row, col, l > 0.f ? 1.f / l : l == l ? 0.f : l);
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+        uint32_t o[32];
+        tmem_ld32(o_at + 32 * x, o);
+        tmem_ld_wait();
+        if (row < it.rows) {
+            for (int i = 0; i < kMasked * kTile; ++i) {
+                const int j = first_masked(it) * kTile + i;
+                if (j >= vis) break;
+                if (!(odd[i / kTile][i % kTile / 32] >> (i % 32) & 1)) continue;
+                const int64_t k = it.key0 + j;
+                float s = 0.f;
+                for (int d = 0; d < kMlaNope; ++d)
+                    s = fmaf(__bfloat162float(p.q_nope[q * p.qn_r + it.head * p.qn_h + d]),
+                             __bfloat162float(p.k_nope[k * p.kn_r + it.head * p.kn_h + d]), s);
+                for (int d = 0; d < kMlaRope; ++d)
+                    s = fmaf(__bfloat162float(p.q_rope[q * p.qr_r + it.head * p.qr_h + d]),
+                             __bfloat162float(p.k_rope[k * p.kr_r + d]), s);
+                const float w = ex2_approx(fmaf(s, p.scale_log2, m == -INFINITY ? 0.f : -m * p.scale_log2));
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const float v = __bfloat162float(p.v[k * p.v_r + it.head * p.v_h + col + c]);
-                if (!(fabsf(v) < INFINITY)) o[c] = fmaf(w, v, o[c]);
+                for (int c = 0; c < 32; ++c) {
+                    const float v = __bfloat162float(p.v[k * p.v_r + it.head * p.v_h + col + 32 * x + c]);
+                    if (!(fabsf(v) < INFINITY)) o[c] = __float_as_uint(fmaf(w, v, __uint_as_float(o[c])));
+                }
             }
+            if (l == 0.f) {  // no weight at all: 0, and not 0 x NaN
+#pragma unroll
+                for (int c = 0; c < 32; ++c) o[c] = 0u;
+            }
+            store32(to, x, o);
         }
+        __syncwarp();
     }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
 mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
                    const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap kr_map,
-                   const __grid_constant__ CUtensorMap v_map, const Params p)
+                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ Params p)
 {
     extern __shared__ __align__(1024) uint8_t q_s[];
     uint8_t *ring = q_s + 2 * kQTile;
@@ -287,7 +347,6 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             mbar_init(&sm->o_full[i], 1);
             mbar_init(&sm->item_full[i], 1);
             mbar_init(&sm->item_empty[i], kSoftmaxWarps + 1 + kScanWarps);
-            mbar_init(&sm->scanned[i], kScanWarps);
         }
         mbar_init(&sm->drained, 1);
         sm->abort = 0;
@@ -316,13 +375,14 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ items and loads
         const Work todo = plan(p, lane);
-        const int64_t total = todo.blocks * p.H * todo.parts;
+        const int total = todo.blocks * p.H * todo.parts;
+        const int4 first_requests = lane < p.B ? request(p, lane) : make_int4(0, 0, 0, 0);
         if (p.parts_used && blockIdx.x == 0 && lane == 0) *p.parts_used = todo.parts;
         uint32_t g = 0, q_uses = 0;  // steps and Q buffers filled so far
-        int64_t w = blockIdx.x;
+        int w = blockIdx.x;
         Item next;
         next.head = -1;
-        if (w < total) next = decode(p, w, todo, lane);
+        if (w < total) next = decode(p, w, todo, first_requests, lane);
         // K of step g takes the slots of K (its last) and V of step g - 2, V those of K of step g - 1
         uint32_t k_sent = 0, v_sent = 0;
         const auto load_k = [&](const Item &it, int j) {
@@ -383,14 +443,14 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             }
             // the item after this one is looked up while this one's steps run
             if (p.next) {
-                unsigned long long n = 0;
-                if (lane == 0) n = atomicAdd(p.next, 1ULL);
-                w = gridDim.x + (int64_t)__shfl_sync(0xffffffffu, n, 0);
+                int n = 0;
+                if (lane == 0) n = atomicAdd(p.next, 1);
+                w = gridDim.x + __shfl_sync(0xffffffffu, n, 0);
             } else {
                 w += gridDim.x;
             }
             next.head = -1;
-            if (w < total) next = decode(p, w, todo, lane);
+            if (w < total) next = decode(p, w, todo, first_requests, lane);
             if (some && lane == 0) {
                 for (int j = it.j0 + 1; j < it.j1 && ok; ++j, ++g) {
                     load_k(it, j);
@@ -553,8 +613,6 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 }
                 go();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->scanned[i & 1]);
             item_done(i);
         }
         if (!ok && lane == 0) set_status(p.status, NSA_ERR_TIMEOUT);
@@ -677,8 +735,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             if (!ok) break;
             // ---- the query's result: its sum, then 64 of its values a thread
             const bool any = j0 < j_end;
-            ok = mla_wait(&sm->scanned[i & 1], (i >> 1) & 1, abort);
-            if (any) ok = mla_wait(&sm->o_full[t], o_uses++ & 1, abort) && ok;
+            // (the last `go` is over then, and behind it what the scanning warps wrote of this tile's steps)
+            if (any) ok = mla_wait(&sm->o_full[t], o_uses++ & 1, abort) && mla_wait(&sm->go[t], (s_uses - 1) & 1, abort);
             if (any) {
                 sm->top[t][half][row] = l;
                 __syncwarp();
@@ -690,69 +748,36 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             if (!ok) break;
             tc_fence_after();
             uint32_t odd = 0;
-            for (int x = 0; x < kMasked * 4; ++x) odd |= sm->odd[i & 1][x / 4][x % 4];
+            const int masked = first_masked(it);
+            for (int x = 0; x < kMasked && masked + x < j_end; ++x)
+                for (int y = 0; y < 4; ++y) odd |= sm->odd[i & 1][x][y];
             const bool mine = r < it.rows;
-            const int64_t at = (it.row0 + r) * p.H + it.head;
-            const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
-            if (t * kTile < it.rows) {
-#pragma unroll 1
-                for (int x = 0; x < kHalf; x += 32) {
-                    float o[32];
-                    if (any) {
-                        uint32_t u[32];
-                        tmem_ld32(o_at + x, u);
-                        tmem_ld_wait();
+            const int col = half * kHalf;
+            const int64_t at = ((int64_t)(it.parts > 1 ? it.part : 0) * p.total_q + it.row0 + r) * p.H + it.head;
+            float *lse_out = it.parts > 1 ? p.part_lse : p.lse;
+            if (odd && any) {
+                rows_with_odd(p, it, sm->odd[i & 1], r, min(vis, j_end * kTile), m, l, col, o_at);
+                tc_fence_before();
+                item_done(i);
+            } else {
+                const Place to = place(p, it, r, col, l > 0.f ? 1.f / l : l == l ? 0.f : l);
+                uint32_t o[2][32];  // (without a step whatever is there: l is 0 then)
+                tmem_ld32(o_at, o[0]);
+                tmem_ld32(o_at + 32, o[1]);
+                tmem_ld_wait();
+                tc_fence_before();
+                item_done(i);  // before the stores, whose end it would otherwise wait for
+                if (l == 0.f) {  // no weight at all, or nothing to weigh: 0, and not 0 x NaN
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] = __uint_as_float(u[y]);
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] = 0.f;
-                    }
-                    if (mine) {
-                        const int col = half * kHalf + x;
-                        if (odd && any) {
-                            float with[32];
-#pragma unroll
-                            for (int y = 0; y < 32; ++y) with[y] = o[y];
-                            add_odd(p, it, sm->odd[i & 1], r, min(vis, j_end * kTile), m, col, with);
-#pragma unroll
-                            for (int y = 0; y < 32; ++y) o[y] = with[y];
-                        }
-                        if (l == 0.f) {
-                            // no weight at all: 0, and not 0 x NaN
-#pragma unroll
-                            for (int y = 0; y < 32; ++y) o[y] = 0.f;
-                        }
-                        if (it.parts > 1) {
-                            float *dst = p.part_out + ((int64_t)it.part * p.total_q * p.H + at) * kMlaV + col;
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                uint32_t v[8];
-#pragma unroll
-                                for (int z = 0; z < 8; ++z) v[z] = __float_as_uint(o[8 * y + z] * inv);
-                                store_sector(dst + 8 * y, v, p.wide & 2);
-                            }
-                        } else {
-                            __nv_bfloat16 *dst = p.out + at * kMlaV + col;
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                uint32_t v[8];
-#pragma unroll
-                                for (int z = 0; z < 8; ++z) v[z] = pack_bf16(o[16 * y + 2 * z] * inv, o[16 * y + 2 * z + 1] * inv);
-                                store_sector(dst + 16 * y, v, p.wide & 1);
-                            }
-                        }
-                    }
-                    __syncwarp();
+                    for (int x = 0; x < 64; ++x) o[x / 32][x % 32] = 0u;
                 }
-                if (mine && half == 0) {
-                    const float lse = l > 0.f ? fmaf(m, p.scale, logf(l)) : l == l ? -INFINITY : l;
-                    if (it.parts > 1) p.part_lse[(int64_t)it.part * p.total_q * p.H + at] = lse;
-                    else p.lse[at] = lse;
+                if (mine) {
+                    store32(to, 0, o[0]);
+                    store32(to, 1, o[1]);
                 }
             }
-            tc_fence_before();
-            item_done(i);
+            if (mine && half == 0) lse_out[at] = l > 0.f ? fmaf(m, p.scale, logf(l)) : l == l ? -INFINITY : l;
+            __syncwarp();
         }
         if (!ok && lane == 0) set_status(p.status, NSA_ERR_TIMEOUT);
         __syncwarp();
@@ -875,9 +900,10 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     NSA_CUDA_TRY(max_dynamic_smem<mla_prefill_kernel>((int)kSmem));
     const cudaStream_t s = (cudaStream_t)stream;
     const int64_t work = items * p.most_parts;
+    if (work > 2147483647LL - 65536) return NSA_ERR_UNSUPPORTED;
     p.next = nullptr;
     if (work > sms) {
-        p.next = (unsigned long long *)workspace_dev;
+        p.next = (int *)workspace_dev;
         NSA_CUDA_TRY(cudaMemsetAsync(p.next, 0, sizeof(*p.next), s));
     }
     mla_prefill_kernel<<<(unsigned)(work < sms ? work : sms), kThreads, kSmem, s>>>(qn, qr, kn, kr, v, p);
