@@ -563,11 +563,10 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             if (it.head < 0) break;
             const int masked = first_masked(it);
             for (int j = it.j0; j < it.j1 && ok; ++j, ++g) {
-                // behind the products of the step before, so that its `go` is over
-                ok = g == 0 || mla_wait(&sm->v_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort);
-                ok = ok && mla_wait(&sm->v_full[g & 1], (g >> 1) & 1, abort);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, mla_wait(&sm->v_full[g & 1], (g >> 1) & 1, abort));
                 const auto go = [&] {
+                    // behind the products of the step before, so that its `go` is over
+                    if (g > 0) ok = ok && mla_wait(&sm->v_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort);
                     __syncwarp();
                     if (lane < 2 && j < it.n[lane]) mbar_arrive(&sm->go[lane]);
                 };
