@@ -752,10 +752,16 @@ def nsa_mla_prefill(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Te
     [total_q, H].  workspace: alloc_mla_prefill_workspace's."""
     total_q, H = _rows("q_nope", q_nope, _D_NOPE)
     total_k, B = _bf16("k_rope", k_rope, (None, _D_ROPE), False).shape[0], cu_seqlens_q.numel() - 1
-    _bf16("q_rope", q_rope, (total_q, H, _D_ROPE), False)
-    _bf16("k_nope", k_nope, (total_k, H, _D_NOPE), False)
-    _bf16("v", v, (total_k, H, _D_V), False)
-    _bf16("out", out, (total_q, H, _D_V))
+    bf16, heads_k = torch.bfloat16, (total_k, H, _D_NOPE)
+    qn, qr, kn, vv = q_nope.stride(), q_rope.stride(), k_nope.stride(), v.stride()
+    if not (q_rope.shape == (total_q, H, _D_ROPE) and k_nope.shape == heads_k and v.shape == heads_k and
+            out.shape == q_nope.shape and q_rope.dtype is bf16 and k_nope.dtype is bf16 and v.dtype is bf16 and
+            out.dtype is bf16 and qr[2] == 1 and kn[2] == 1 and vv[2] == 1 and out.is_contiguous()):
+        # (something is not as it should be: which)
+        _bf16("q_rope", q_rope, (total_q, H, _D_ROPE), False)
+        _bf16("k_nope", k_nope, (total_k, H, _D_NOPE), False)
+        _bf16("v", v, (total_k, H, _D_V), False)
+        _bf16("out", out, (total_q, H, _D_V))
     if lse.shape != (total_q, H) or lse.dtype is not torch.float32 or not lse.is_contiguous():
         raise ValueError(f"lse must be contiguous float32 [{total_q}, {H}], got shape {tuple(lse.shape)} of {lse.dtype}")
     _i32("cu_seqlens_q", cu_seqlens_q, max(B, 0) + 1)
@@ -763,7 +769,6 @@ def nsa_mla_prefill(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Te
     ws_bytes = _scratch(workspace)
     _status_word(status)
     handle = _launch_on(stream, q_nope, q_rope, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace, status)
-    qn, qr, kn, vv = q_nope.stride(), q_rope.stride(), k_nope.stride(), v.stride()
     rc = load().nsa_mla_prefill(q_nope.data_ptr(), qn[0], qn[1], q_rope.data_ptr(), qr[0], qr[1], k_nope.data_ptr(), kn[0],
                                 kn[1], k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), vv[0], vv[1],
                                 cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, total_q, total_k, H, _D_NOPE, _D_ROPE,
@@ -773,6 +778,7 @@ def nsa_mla_prefill(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Te
 
 
 _DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+_POINTERS = [C.c_void_p * n for n in range(9)]
 
 
 def nsa_merge_attention(parts, lses, out: torch.Tensor, lse: torch.Tensor, stream=None) -> None:
@@ -791,7 +797,8 @@ def nsa_merge_attention(parts, lses, out: torch.Tensor, lse: torch.Tensor, strea
             raise ValueError(f"parts must be contiguous {dtype} {list(shape)} and lses contiguous float32 {list(rows)}, "
                              f"got {p.dtype} {list(p.shape)} and {l.dtype} {list(l.shape)}")
     handle = _launch_on(stream, out, lse, *parts, *lses)
-    ptrs, lptrs = (C.c_void_p * n)(*[p.data_ptr() for p in parts]), (C.c_void_p * n)(*[l.data_ptr() for l in lses])
+    array = _POINTERS[n] if n < len(_POINTERS) else C.c_void_p * n
+    ptrs, lptrs = array(*[p.data_ptr() for p in parts]), array(*[l.data_ptr() for l in lses])
     _check("nsa_merge_attention", load().nsa_merge_attention(_DTYPES[dtype], _DTYPES[out.dtype], n, ptrs, lptrs, lse.numel(),
                                                              shape[-1], _at(out), _at(lse), handle))
 

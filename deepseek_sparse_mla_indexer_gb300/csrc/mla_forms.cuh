@@ -15,13 +15,13 @@ constexpr int kMlaHeadRows = kMlaNope + kMlaV;  // of the up-projection, per hea
 // Longest wait inside a kernel, in SM clocks (about a second); then it gives up (NSA_ERR_TIMEOUT).
 constexpr long long kMlaWait = 2000000000LL;
 
-// Waits for a phase, at most kMlaWait, and no longer than until another warp of the block gave up.
-__device__ __forceinline__ bool mla_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+// Waits for a phase, at most `most` clocks, and no longer than until another warp of the block gave up.
+__device__ __forceinline__ bool mla_wait(uint64_t *bar, uint32_t parity, volatile int *abort, long long most = kMlaWait)
 {
     if (sm100::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!sm100::mbar_try_wait(bar, parity)) {
-        if (*abort || clock64() - t0 > kMlaWait) {
+        if (*abort || clock64() - t0 > most) {
             *abort = 1;
             return false;
         }

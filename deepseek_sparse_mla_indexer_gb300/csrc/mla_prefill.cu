@@ -44,6 +44,7 @@ constexpr int kHalf = kTile / 2;
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kScanWarp = 18, kScanWarps = 2;
 constexpr int kThreads = 32 * (kScanWarp + kScanWarps);  // 20 warps: a 21st would leave each thread 80 registers instead of 96
 constexpr uint32_t kTmemCols = 512;        // S / P of tile t at 128 t, O at 256 + 128 t
+constexpr long long kItemWait = 64 * kMlaWait;
 constexpr float kJoinCost = 1.5f;           // steps
 constexpr float kRescale = 8.0f;           // log2 units
 
@@ -82,6 +83,7 @@ struct Params {
     const int32_t *cu_q, *cu_k;
     int B, total_q, total_k, H, causal;
     int heads_at_once;   // heads whose keys and values stay in L2 while all queries pass
+    int most_blocks;     // of 256 queries, that requests in order have
     int most_parts;      // 1, or as many as the workspace holds
     int wide;            // the results' addresses are multiples of 32 bytes: out's (bit 0), the parts' (bit 1)
     float scale, scale_log2;
@@ -153,8 +155,7 @@ struct Work {
 // results that it reads (0.13 us for 6 items on 152 SMs).
 __device__ Work plan(const Params &p, int lane)
 {
-    int n = 0;
-    int64_t steps = 0, longest = 0;
+    int64_t n = 0, steps = 0, longest = 0;
     for (int b = lane; b < p.B; b += 32) {
         const int4 r = request(p, b);
         const int blocks = (r.y + kBlock - 1) / kBlock;
@@ -172,7 +173,11 @@ __device__ Work plan(const Params &p, int lane)
         steps += __shfl_xor_sync(0xffffffffu, steps, o);
         longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
     }
-    Work w = {n, 1};
+    if (n > p.most_blocks) {  // requests that overlap: more items than the launch counted on
+        if (lane == 0) set_status(p.status, NSA_ERR_BOUNDS);
+        n = 0;
+    }
+    Work w = {(int)n, 1};
     const float items = (float)n * (float)p.H, all = (float)(steps * p.H), sms = (float)gridDim.x;
     float best = INFINITY;
     for (int c = 1; c <= p.most_parts && (c == 1 || c <= longest); ++c) {
@@ -366,7 +371,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
     bool ok = true;
 
     // Item i as the loading warp published it; its place is given back with item_done.
-    const auto item_wait = [&](int i) { return mla_wait(&sm->item_full[i & 1], (i >> 1) & 1, abort); };
+    // (Warps without work in an item wait for the next one as long as it takes.)
+    const auto item_wait = [&](int i) { return mla_wait(&sm->item_full[i & 1], (i >> 1) & 1, abort, kItemWait); };
     const auto item_done = [&](int i) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->item_empty[i & 1]);
@@ -624,9 +630,15 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
         const uint32_t o_at = lanes + 2 * kTile + t * kMlaV + half * kHalf;
         uint32_t s_uses = 0, o_uses = 0;
         const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
-        for (int i = 0; ok; ++i) {
-            ok = __all_sync(0xffffffffu, item_wait(i));
-            if (!ok) break;
+        for (int i = 0;; ++i) {
+            // The eight warps of a tile meet at barriers, so they give up together: where a wait ran out they go
+            // on to here (the waits that follow return at once)
+            ok = item_wait(i) && ok;
+            __syncwarp();
+            if (bar_red_or(1 + t, 256, !ok)) {
+                ok = false;
+                break;
+            }
             const Item &it = sm->item[i & 1];
             if (it.head < 0) break;
             const int r = t * kTile + row;
@@ -634,14 +646,15 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             const int j0 = it.j0, j_end = min(it.j1, it.n[t]);
             float m = -INFINITY, l = 0.f;
             for (int j = j0; j < j_end; ++j, ++s_uses) {
-                ok = mla_wait(&sm->s_full[t], s_uses & 1, abort);
+                ok = mla_wait(&sm->s_full[t], s_uses & 1, abort) && ok;
                 __syncwarp();
                 tc_fence_after();
                 const int seen = vis - j * kTile - half * kHalf;  // of this thread's 64 keys
                 uint32_t s[2][32];
-                float top = -INFINITY;
                 float2 sum[2];
-                const auto load = [&] {
+                // Weights with the maximum of the steps before, which hardly ever has to be refreshed; at the first
+                // step, and where some row's has grown too far, with one that is looked for first
+                for (bool look = j == j0;; look = true) {
                     tmem_ld32(s_at, s[0]);
                     tmem_ld32(s_at + 32, s[1]);
                     tmem_ld_wait();
@@ -652,9 +665,36 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                             for (int y = 0; y < 32; ++y)
                                 if (32 * x + y >= seen) s[x][y] = 0xFF800000u;
                     }
-                };
-                // scores to weights, in bf16 in the first half of their registers, and their sum
-                const auto weigh = [&](bool with_top) {
+                    if (look) {
+                        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int y = 0; y < 32; y += 2)
+                                mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[x][y])), __uint_as_float(s[x][y + 1]));
+                        sm->top[t][half][row] = fmaxf(mx[0], mx[1]);
+                        bar_sync(1 + t, 256);
+                        const float top = fmaxf(sm->top[t][0][row], sm->top[t][1][row]);
+                        if (j == j0) {
+                            m = top;
+                        } else if (__any_sync(0xffffffffu, (top - m) * p.scale_log2 > kRescale)) {
+                            // Each row by its own scores: a neighbour's, which may be infinite, do not change its
+                            // roundings.  QK of this step was issued behind PV of the one before, so O is at rest
+                            const float fresh = (top - m) * p.scale_log2 > kRescale ? top : m;
+                            const float f = fresh == m ? 1.f : ex2_approx((m - fresh) * p.scale_log2);
+                            m = fresh;
+                            l *= f;
+#pragma unroll 1
+                            for (int x = 0; x < kHalf; x += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(o_at + x, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                                tmem_st16(o_at + x, o);
+                            }
+                        }
+                    }
                     const float nm = m == -INFINITY ? 0.f : -m * p.scale_log2;
                     const float2 nm2 = make_float2(nm, nm);
                     float tops[2] = {-INFINITY, -INFINITY};
@@ -664,58 +704,15 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
                             const float a = __uint_as_float(s[x][2 * y]), b = __uint_as_float(s[x][2 * y + 1]);
-                            if (with_top) tops[y & 1] = fmaxf(fmaxf(tops[y & 1], a), b);
+                            tops[y & 1] = fmaxf(fmaxf(tops[y & 1], a), b);
                             float2 e = fma2(make_float2(a, b), c2, nm2);
                             e.x = ex2_approx(e.x);
                             e.y = ex2_approx(e.y);
                             sum[y & 1] = add2(sum[y & 1], e);
                             s[x][y] = pack_bf16(e.x, e.y);
                         }
-                    if (with_top) top = fmaxf(tops[0], tops[1]);
-                };
-                load();
-                bool again = true;
-                if (j > j0) {
-                    // With the maximum of the steps before, which hardly ever has to be refreshed.  Each row by
-                    // its own scores: a neighbour's, which may be infinite, do not change its roundings.  Behind
-                    // the barrier all scores of the tile are read, and P may take their place
-                    weigh(true);
-                    again = bar_red_or(1 + t, 256, !ok || (top - m) * p.scale_log2 > kRescale);
-                    if (again) load();
-                }
-                if (again) {
-                    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int y = 0; y < 32; y += 2)
-                            mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[x][y])), __uint_as_float(s[x][y + 1]));
-                    float *tops = &sm->top[t][0][row];
-                    tops[half * kTile] = fmaxf(mx[0], mx[1]);
-                    if (bar_red_or(1 + t, 256, !ok)) {
-                        ok = false;
-                        break;
-                    }
-                    top = fmaxf(tops[0], tops[kTile]);
-                    if (j == j0) {
-                        m = top;
-                    } else if (__any_sync(0xffffffffu, (top - m) * p.scale_log2 > kRescale)) {
-                        // QK of this step was issued behind PV of the one before, so O is at rest
-                        const float fresh = (top - m) * p.scale_log2 > kRescale ? top : m;
-                        const float f = fresh == m ? 1.f : ex2_approx((m - fresh) * p.scale_log2);
-                        m = fresh;
-                        l *= f;
-#pragma unroll 1
-                        for (int x = 0; x < kHalf; x += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(o_at + x, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                            tmem_st16(o_at + x, o);
-                        }
-                    }
-                    weigh(false);
+                    // Behind this barrier all scores of the tile are read, and P may take their place
+                    if (!bar_red_or(1 + t, 256, !ok || (fmaxf(tops[0], tops[1]) - m) * p.scale_log2 > kRescale) || look) break;
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -731,20 +728,17 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->go[t]);
             }
-            if (!ok) break;
             // ---- the query's result: its sum, then 64 of its values a thread
             const bool any = j0 < j_end;
             // (the last `go` is over then, and behind it what the scanning warps wrote of this tile's steps)
-            if (any) ok = mla_wait(&sm->o_full[t], o_uses++ & 1, abort) && mla_wait(&sm->go[t], (s_uses - 1) & 1, abort);
             if (any) {
+                ok = mla_wait(&sm->o_full[t], o_uses++ & 1, abort) && mla_wait(&sm->go[t], (s_uses - 1) & 1, abort) && ok;
                 sm->top[t][half][row] = l;
                 __syncwarp();
-                ok = !bar_red_or(1 + t, 256, !ok);
+                bar_sync(1 + t, 256);
                 l = sm->top[t][0][row] + sm->top[t][1][row];
                 bar_sync(1 + t, 256);
             }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
             tc_fence_after();
             uint32_t odd = 0;
             const int masked = first_masked(it);
@@ -862,6 +856,7 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     p.cu_q = cu_seqlens_q_dev; p.cu_k = cu_seqlens_k_dev;
     p.B = B; p.total_q = total_q; p.total_k = total_k; p.H = H; p.causal = causal;
     const int64_t items = most_blocks(B, total_q) * H;
+    p.most_blocks = (int)most_blocks(B, total_q);
     p.most_parts = most_parts_of(total_q, total_k, H, sms);
     const int64_t fit = kL2Keys / ((int64_t)(total_k > 0 ? total_k : 1) * 2 * (kMlaNope + kMlaV));
     p.heads_at_once = (int)(fit < 1 ? 1 : fit < H ? fit : H);
