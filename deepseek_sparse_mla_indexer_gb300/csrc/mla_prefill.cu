@@ -59,6 +59,7 @@ struct Item {
     int j0, j1;        // steps of this share, none if j0 >= j1
     int n[2];          // steps that each tile needs at most
     int part, parts;
+    int careful;       // its masked steps' values are looked through (a second time for this item)
 };
 
 struct Shared {
@@ -70,6 +71,7 @@ struct Shared {
     uint64_t drained;
     Item item[2];
     uint32_t odd[2][kMasked][4];  // masked step -> keys whose values are not all finite
+    int again[2];                 // the item is to be done once more, with care
     uint32_t tmem;
     volatile int abort;
     // [tile][half]: a query's maximum over its half of the step, at the end its sum of weights.  The next
@@ -98,14 +100,26 @@ struct Params {
     int32_t *status;
 };
 
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate)
+// Products whose operands' descriptors share the upper word: what issues them is on the tensor core's path, and
+// adds one word instead of two.  A in shared memory; A in TMEM.
+__device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                       uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_lo_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                          uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -239,6 +253,7 @@ __device__ Item decode(const Params &p, int w, const Work &todo, int4 first_requ
     it.j0 = (int)((int64_t)all * it.part / todo.parts);
     it.j1 = (int)((int64_t)all * (it.part + 1) / todo.parts);
     it.parts = todo.parts;
+    it.careful = 0;
     return it;
 }
 
@@ -355,6 +370,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
         }
         mbar_init(&sm->drained, 1);
         sm->abort = 0;
+        sm->again[0] = sm->again[1] = 0;
         fence_mbar_init();
         prefetch_tensormap(&qn_map);
         prefetch_tensormap(&qr_map);
@@ -418,10 +434,18 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             }
         };
         for (int i = 0; ok; ++i) {
-            const Item it = next;
-            ok = __all_sync(0xffffffffu, mla_wait(&sm->item_empty[i & 1], ((i >> 1) & 1) ^ 1, abort));
+            ok = __all_sync(0xffffffffu, mla_wait(&sm->item_empty[i & 1], ((i >> 1) & 1) ^ 1, abort, kItemWait));
+            // (behind the last item, the one in the other place may still ask to be done again)
+            if (ok && next.head < 0 && !sm->again[i & 1] && i > 0) {
+                ok = __all_sync(0xffffffffu, mla_wait(&sm->item_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, abort, kItemWait));
+            }
             if (!ok) break;
+            const bool mine = sm->again[i & 1], other = next.head < 0 && sm->again[(i & 1) ^ 1], again = mine || other;
+            Item it = again ? sm->item[mine ? i & 1 : (i & 1) ^ 1] : next;
+            __syncwarp();
+            if (again) it.careful = 1;
             if (lane < kMasked * 4) sm->odd[i & 1][lane / 4][lane % 4] = 0;
+            if (lane == 0) sm->again[mine ? i & 1 : other ? (i & 1) ^ 1 : i & 1] = 0;
             __syncwarp();
             if (lane == 0) {
                 sm->item[i & 1] = it;
@@ -448,15 +472,19 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 ++g;
             }
             // the item after this one is looked up while this one's steps run
-            if (p.next) {
+            if (again) {
+                // (the next one waits)
+            } else if (p.next) {
                 int n = 0;
                 if (lane == 0) n = atomicAdd(p.next, 1);
                 w = gridDim.x + __shfl_sync(0xffffffffu, n, 0);
             } else {
                 w += gridDim.x;
             }
-            next.head = -1;
-            if (w < total) next = decode(p, w, todo, first_requests, lane);
+            if (!again) {
+                next.head = -1;
+                if (w < total) next = decode(p, w, todo, first_requests, lane);
+            }
             if (some && lane == 0) {
                 for (int j = it.j0 + 1; j < it.j1 && ok; ++j, ++g) {
                     load_k(it, j);
@@ -480,30 +508,31 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
         const uint64_t q_desc = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
         const uint64_t k_desc = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
         const uint64_t v_desc = smem_desc(smem_u32(ring), kSlot / 2, 1024, kSwizzle128B);
+        const uint32_t k_hi = (uint32_t)(k_desc >> 32), v_hi = (uint32_t)(v_desc >> 32);  // (q_desc's is k_desc's)
         // What this warp does between products leaves the tensor core without work, so one barrier a tile and
         // step tells it that P and V are there
         uint32_t g = 0, q_uses = 0, go_uses[2] = {0, 0};
         // a wait that gave up lets the warp go on to the step's end, where the lanes agree to stop
         const auto wait = [&](uint64_t *bar, uint32_t parity) { ok = mla_wait(bar, parity, abort) && ok; };
-        // (one elected lane) S_t = Q_t K^T, K of step `at`; O_t += P_t V, V of step g
+        // (one elected lane) S_t = Q_t K^T, O_t += P_t V, K and V of this CTA's step `at`
         const auto qk = [&](int t, uint32_t at) {
 #pragma unroll
             for (int x = 0; x < kKSlots; ++x) {
-                const uint64_t a = q_desc + (t * kQTile + x * kSlot) / 16;
-                const uint64_t b = k_desc + (kStepSlots * at + x) % kSlots * (kSlot / 16);
+                const uint32_t a = (uint32_t)q_desc + (t * kQTile + x * kSlot) / 16;
+                const uint32_t b = (uint32_t)k_desc + (kStepSlots * at + x) % kSlots * (kSlot / 16);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f16(tmem + t * kTile, a + 2 * k, b + 2 * k, idesc_s, x > 0 || k > 0);
+                for (int k = 0; k < 4; ++k) mma_lo(tmem + t * kTile, a + 2 * k, b + 2 * k, k_hi, idesc_s, x > 0 || k > 0);
             }
             mma_commit(&sm->s_full[t]);
         };
-        const auto pv = [&](int t, bool first, bool last) {
+        const auto pv = [&](int t, uint32_t at, bool first, bool last) {
 #pragma unroll
             for (int x = 0; x < kVSlots; ++x) {
-                const uint64_t b = v_desc + (kStepSlots * g + kKSlots + x) % kSlots * (kSlot / 16);
+                const uint32_t b = (uint32_t)v_desc + (kStepSlots * at + kKSlots + x) % kSlots * (kSlot / 16);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_f16_ts(tmem + 2 * kTile + t * kMlaV, tmem + t * kTile + x * 32 + k * 8, b + k * (2048 / 16), idesc_o,
-                               !first || x > 0 || k > 0);
+                    mma_lo_ts(tmem + 2 * kTile + t * kMlaV, tmem + t * kTile + x * 32 + k * 8, b + k * (2048 / 16), v_hi, idesc_o,
+                              !first || x > 0 || k > 0);
             }
             if (last) mma_commit(&sm->o_full[t]);
         };
@@ -527,6 +556,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             }
             for (int j = j0; j < j1; ++j) {
                 const bool more = j + 1 < j1;
+                bool have_k = more && mbar_test(&sm->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (j < n[t]) {
@@ -535,10 +565,10 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                         tc_fence_after();
                     }
                     if (elect_one()) {
-                        if (j < n[t]) pv(t, j == j0, !(more && j + 1 < n[t]));
+                        if (j < n[t]) pv(t, g, j == j0, !(more && j + 1 < n[t]));
                         if (t == 1) mma_commit(&sm->v_free[g & 1]);
                     }
-                    if (t == 0 && more) wait(&sm->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
+                    if (t == 0 && more && !have_k) wait(&sm->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
                     __syncwarp();
                     if (elect_one()) {
                         if (more && j + 1 < n[t]) qk(t, g + 1);
@@ -576,7 +606,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                     __syncwarp();
                     if (lane < 2 && j < it.n[lane]) mbar_arrive(&sm->go[lane]);
                 };
-                if (j < masked) {
+                if (j < masked || !it.careful) {
                     go();
                     continue;
                 }
@@ -731,34 +761,47 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             // ---- the query's result: its sum, then 64 of its values a thread
             const bool any = j0 < j_end;
             // (the last `go` is over then, and behind it what the scanning warps wrote of this tile's steps)
+            const bool mine = r < it.rows;
+            const int col = half * kHalf, masked = first_masked(it);
+            uint32_t o[2][32];  // (without a step whatever is there: l is 0 then)
+            bool again = false;
+            if (any) ok = mla_wait(&sm->o_full[t], o_uses++ & 1, abort) && mla_wait(&sm->go[t], (s_uses - 1) & 1, abort) && ok;
+            __syncwarp();
+            tc_fence_after();
+            tmem_ld32(o_at, o[0]);
+            tmem_ld32(o_at + 32, o[1]);
+            tmem_ld_wait();
             if (any) {
-                ok = mla_wait(&sm->o_full[t], o_uses++ & 1, abort) && mla_wait(&sm->go[t], (s_uses - 1) & 1, abort) && ok;
+                // A value that is not finite, at a key of a masked step, reaches queries that do not see it (as
+                // 0 x inf).  That shows in the result; then the item is done again, with such values taken out
+                float2 z = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    z = fma2(make_float2(__uint_as_float(o[x / 16][x % 16 * 2]), __uint_as_float(o[x / 16][x % 16 * 2 + 1])),
+                             make_float2(0.f, 0.f), z);
                 sm->top[t][half][row] = l;
-                __syncwarp();
-                bar_sync(1 + t, 256);
+                again = bar_red_or(1 + t, 256, mine && !(z.x + z.y == 0.f)) && j_end > masked && !it.careful;
                 l = sm->top[t][0][row] + sm->top[t][1][row];
                 bar_sync(1 + t, 256);
             }
-            tc_fence_after();
             uint32_t odd = 0;
-            const int masked = first_masked(it);
-            for (int x = 0; x < kMasked && masked + x < j_end; ++x)
-                for (int y = 0; y < 4; ++y) odd |= sm->odd[i & 1][x][y];
-            const bool mine = r < it.rows;
-            const int col = half * kHalf;
+            if (it.careful)
+                for (int x = 0; x < kMasked && masked + x < j_end; ++x)
+                    for (int y = 0; y < 4; ++y) odd |= sm->odd[i & 1][x][y];
             const int64_t at = ((int64_t)(it.parts > 1 ? it.part : 0) * p.total_q + it.row0 + r) * p.H + it.head;
             float *lse_out = it.parts > 1 ? p.part_lse : p.lse;
+            tc_fence_before();
+            if (again) {
+                if (row == 0) sm->again[i & 1] = 1;
+                item_done(i);
+                continue;
+            }
             if (odd && any) {
                 rows_with_odd(p, it, sm->odd[i & 1], r, min(vis, j_end * kTile), m, l, col, o_at);
                 tc_fence_before();
                 item_done(i);
             } else {
                 const Place to = place(p, it, r, col, l > 0.f ? 1.f / l : l == l ? 0.f : l);
-                uint32_t o[2][32];  // (without a step whatever is there: l is 0 then)
-                tmem_ld32(o_at, o[0]);
-                tmem_ld32(o_at + 32, o[1]);
-                tmem_ld_wait();
-                tc_fence_before();
                 item_done(i);  // before the stores, whose end it would otherwise wait for
                 if (l == 0.f) {  // no weight at all, or nothing to weigh: 0, and not 0 x NaN
 #pragma unroll
