@@ -4,26 +4,43 @@
 //   lse  = ln sum_j exp(x_ij)        out = sum_j exp(x_ij - lse) v[j,h]
 //
 // A work item is 256 queries of one request and head, two tiles of 128, and a CTA (one an SM,
-// persistent) takes one item after the other.  Per 128 keys and tile, on tcgen05:
+// persistent) takes one item after the other.  Per step of 128 keys and tile, on tcgen05:
 //   S[128 q, 128 keys] = Q K^T        12 products, both operands in shared memory
-//   P = 2^(c S - c m)                 128 threads, a query each; m a lazily refreshed maximum
+//   P = 2^(c S - c m)                 256 threads, two a query; m a lazily refreshed maximum
 //   O[128 q, 128]     += P V          8 products, P (bf16) in TMEM in the place of S
-// S, P and O of both tiles fill TMEM (512 columns).  While 128 threads turn one tile's scores into
-// P, the tensor core works on the other tile: PV of the keys before, QK of the next.  A row's
+// S, P and O of both tiles fill TMEM (512 columns).  While 256 threads turn one tile's scores into
+// P, the tensor core works on the other tile: PV of the step before, QK of the next.  A row's
 // maximum is only refreshed, and O rescaled by the threads themselves, when it has grown by more
-// than 2^8: until then the weights are up to 2^8 and nothing is lost, since sums are fp32.
-// Weights are rounded to bf16 (2^-8 of themselves at most) for the product with V, whose type the operands
-// share; their sum, and so lse, is taken before that rounding.
+// than 2^8: until then weights are up to 2^8 and nothing is lost, since sums are fp32.  So a step's
+// weights are taken with the old maximum right away, and its own maximum only says afterwards
+// whether that was right.  Weights are rounded to bf16 (2^-8 of themselves at most) for the product
+// with V, whose type the operands share; their sum, and so lse, is taken before that rounding.
 //
-// Keys and values come by TMA through a ring of eight 16 KB slots (a K tile takes three: two halves
-// of the nope part and the rope part that all heads share; a V tile two, of 64 keys each), Q has
-// its own 96 KB.  A warp decodes the items from the sequences' starts and issues the loads, one
-// issues the products, two look through the V tiles that not every query of the item sees: what
-// is not finite there would reach rows that do not see it as 0 x inf, so it is replaced by 0, and
-// the rows that do see it add it at the end.
+// Keys and values come by TMA through a ring of eight 16 KB slots (a step takes five: two halves of
+// the keys' nope part, the rope part that all heads share, and 64 keys' values each), Q has its own
+// 96 KB.  One warp decodes the items from the sequences' starts, hands them out longest first per
+// request, and issues the loads; one issues the products; two tell it what has landed.
 //
-// Few items (a short prompt over a long prefix, few heads) are cut along the keys; the parts'
-// fp32 results go to the workspace and merge_launch joins them.
+// A value that is not finite, at a key that a query must not see, reaches that query as 0 x inf.  It
+// shows in the result: an item whose last steps hide keys from some of its queries (causal diagonal,
+// the end of a request inside a step) and whose result is not finite is done a second time, with
+// care: such values are replaced by 0 in shared memory, and the queries that see them add them.
+//
+// Few items (a short prompt over a long prefix, few heads) are cut along the keys; how often is
+// chosen on the device, where the lengths are.  The parts' fp32 results go to the workspace, and
+// merge_launch joins them.
+//
+// Measured (GB300, a pass among others; of 1969 TFLOP/s):
+//   one causal prompt of 8192, 128 heads       1650 us   1.66 PFLOP/s, 84 %
+//   eight prompts of 189 .. 2000, 128 heads     329 us   0.97, 49 % (1.16 with the hidden parts of the tiles)
+//   1001 / 768 over 40000 / 26651, 16 heads     470 us   1.32, 67 %
+//   37 after 600, 16 heads                       11.5 us in a graph, 39 with the host's part of the call
+// A step of both tiles takes 3310 cycles where its products alone take 2560: the tensor core reads
+// shared memory at its full rate during QK (8 KB a product of 64 cycles), and the 80 KB that TMA writes a
+// step come on top (640 cycles).  The long prompt runs at the power limit (1.9 GHz at 1375 W when
+// repeated for seconds: 1.46 PFLOP/s, 84 % of what library products sustain).  Short prompts pay
+// about 3.5 us an item beside its steps: the last step's softmax, which only one tile still has,
+// the result's way out and the first step's softmax have no products beside them.
 #include "mla_forms.cuh"
 
 namespace nsa {
@@ -164,7 +181,7 @@ struct Work {
 };
 
 // Parts: where there are few items, or a few long ones, their keys are cut into shares.  In units of a
-// step (1.9 us): the SMs' even share of all steps, the longest share as what the last of them may
+// step (1.75 us): the SMs' even share of all steps, the longest share as what the last of them may
 // be late by, two steps an item for its start and end, and for the join its launch and the fp32
 // results that it reads (0.13 us for 6 items on 152 SMs).
 __device__ Work plan(const Params &p, int lane)
@@ -205,8 +222,9 @@ __device__ Work plan(const Params &p, int lane)
     return w;
 }
 
-// Item w of blocks x H x parts (below 2^31: the launch checks); first_requests: request `lane`, kept between calls.  Heads go in sections; in a section all heads of a block of queries
-// follow one another, and a request's blocks go from its last, which sees most keys, to its first.
+// Item w of blocks x H x parts (below 2^31: the launch checks); first_requests: request `lane`, kept between
+// calls.  Heads go in sections; in a section all heads of a block of queries follow one another, and a
+// request's blocks go from its last, which sees most keys, to its first.
 __device__ Item decode(const Params &p, int w, const Work &todo, int4 first_requests, int lane)
 {
     Item it;
