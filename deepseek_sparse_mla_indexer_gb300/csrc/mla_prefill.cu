@@ -864,8 +864,19 @@ int most_parts_of(int total_q, int total_k, int H, int sms)
     return (int)(fit < 1 ? 1 : fit < kMaxMergeParts ? fit : kMaxMergeParts);
 }
 
-// Heads whose keys and values (512 bytes a key) are to stay in L2 together.
+// Heads of a section (decode): as many as leave their keys and values (512 bytes a key) in L2, but enough for
+// kSectionItems items an SM, since a section's items end with the short ones, which even the SMs out; and sections of
+// one size, so that the last one is no rest of a few long items.
 constexpr int64_t kL2Keys = 40LL << 20;
+constexpr int kSectionItems = 4;
+
+int heads_at_once_of(int64_t blocks, int total_k, int H, int sms)
+{
+    const int64_t fit = kL2Keys / ((int64_t)(total_k > 0 ? total_k : 1) * 2 * (kMlaNope + kMlaV));
+    const int64_t fill = ceil_div((int64_t)kSectionItems * sms, blocks);
+    const int64_t most = fit > fill ? fit : fill;
+    return most >= H ? H : (int)ceil_div(H, ceil_div(H, most));
+}
 
 }  // namespace
 }  // namespace nsa
@@ -919,8 +930,7 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     const int64_t items = most_blocks(B, total_q) * H;
     p.most_blocks = (int)most_blocks(B, total_q);
     p.most_parts = most_parts_of(total_q, total_k, H, sms);
-    const int64_t fit = kL2Keys / ((int64_t)(total_k > 0 ? total_k : 1) * 2 * (kMlaNope + kMlaV));
-    p.heads_at_once = (int)(fit < 1 ? 1 : fit < H ? fit : H);
+    p.heads_at_once = heads_at_once_of(p.most_blocks, total_k, H, sms);
     p.scale = sm_scale;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.q_nope = (const __nv_bfloat16 *)q_nope_dev; p.q_rope = (const __nv_bfloat16 *)q_rope_dev;
