@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kVec = 8;  // values a thread
+constexpr int kJoinBlocks = 4;  // an SM
 
 __device__ __forceinline__ void load8(const float *p, float (&v)[kVec])
 {
@@ -39,104 +40,111 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[kVec])
     *(uint4 *)p = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
-// units: threads a row (D / 8); a block has kThreads / units rows.
-template <typename In, typename Out, int NP>
+// units: threads a row (D / 8); a block has kThreads / units rows.  USED: as many parts as the device says, and each
+// block more than one lot of rows (which costs the other form 3 %).
+template <typename In, typename Out, int NP, bool USED>
 __global__ void __launch_bounds__(kThreads)
 merge_kernel(const MergeParts parts, int64_t rows, int units, Out *out, float *lse)
 {
     pdl_wait();
-    const int per = kThreads / units, r = threadIdx.x / units, u = threadIdx.x - r * units;
-    const int64_t row = (int64_t)blockIdx.x * per + r;
-    int64_t from = 0;
     int n = NP;
-    if (parts.used) {
+    int64_t from = 0;
+    if constexpr (USED) {
         n = *parts.used;
         if (n <= 1) return;
-    }
-    if (parts.live_to) {
         from = (int64_t)*parts.live_from * parts.live_rows;
         rows = min(rows, (int64_t)*parts.live_to * parts.live_rows);
     }
-    const bool live = r < per && row >= from && row < rows;
-    const int64_t at = (row * units + u) * kVec;
-    float l[NP], x[NP][kVec], o[kVec], top = -INFINITY, total = 0.f;
-    if (live) {
+    const int per = kThreads / units, r = threadIdx.x / units, u = threadIdx.x - r * units;
+    for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < rows; row0 += (int64_t)gridDim.x * per) {
+        const int64_t row = row0 + r, at = (row * units + u) * kVec;
+        const bool live = r < per && row >= from && row < rows;
+        float l[NP], x[NP][kVec], o[kVec], top = -INFINITY, total = 0.f;
+        if (live) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) l[i] = i < n ? parts.lse[i][row] : -INFINITY;
-        // (read without a look at the lse, so that one latency covers both)
+            for (int i = 0; i < NP; ++i) l[i] = i < n ? parts.lse[i][row] : -INFINITY;
+            // (read without a look at the lse, so that one latency covers both)
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-            if (i < n) load8((const In *)parts.out[i] + at, x[i]);
+            for (int i = 0; i < NP; ++i)
+                if (i < n) load8((const In *)parts.out[i] + at, x[i]);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            if (l[i] == -INFINITY) {  // a part that saw no key has weight 0, whatever its values are
+            for (int i = 0; i < NP; ++i) {
+                if (l[i] == -INFINITY) {  // a part that saw no key has weight 0, whatever its values are
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) x[i][j] = 0.f;
+                    for (int j = 0; j < kVec; ++j) x[i][j] = 0.f;
+                }
+                top = fmaxf(top, l[i]);
             }
-            top = fmaxf(top, l[i]);
-        }
-        if (top == -INFINITY) top = 0.f;  // no key in any part, or NaN
+            if (top == -INFINITY) top = 0.f;  // no key in any part, or NaN
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            l[i] = expf(l[i] - top);
-            total += l[i];
-        }
-        const float inv = total > 0.f ? 1.f / total : total;  // 0 without a key, NaN stays
+            for (int i = 0; i < NP; ++i) {
+                l[i] = expf(l[i] - top);
+                total += l[i];
+            }
+            const float inv = total > 0.f ? 1.f / total : total;  // 0 without a key, NaN stays
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            o[j] = 0.f;
+            for (int j = 0; j < kVec; ++j) {
+                o[j] = 0.f;
 #pragma unroll
-            for (int i = 0; i < NP; ++i) o[j] = fmaf(l[i], x[i][j], o[j]);
-            o[j] *= inv;
+                for (int i = 0; i < NP; ++i) o[j] = fmaf(l[i], x[i][j], o[j]);
+                o[j] *= inv;
+            }
         }
-    }
-    __syncthreads();  // every lse of the block's rows is read
-    if (live) {
-        store8(out + at, o);
-        if (u == 0) lse[row] = total == 0.f ? -INFINITY : top + logf(total);
+        __syncthreads();  // every lse of the block's rows is read
+        if (live) {
+            store8(out + at, o);
+            if (u == 0) lse[row] = total == 0.f ? -INFINITY : top + logf(total);
+        }
+        if constexpr (!USED) break;
     }
 }
 
-template <typename In, typename Out, int NP>
-nsa_status launch(const MergeParts &parts, int64_t rows, int D, Out *out, float *lse, bool behind_previous,
-                  cudaStream_t stream)
+template <typename In, typename Out, int NP, bool USED = false>
+nsa_status launch(const MergeParts &parts, int64_t rows, int D, Out *out, float *lse, cudaStream_t stream)
 {
     const int units = D / kVec;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ceil_div(rows, kThreads / units));
+    int64_t blocks = ceil_div(rows, kThreads / units);
+    if (USED) {  // there may be nothing to join: no more blocks than find that out at once
+        const int sms = current_sm_count();
+        if (blocks > (int64_t)sms * kJoinBlocks) blocks = (int64_t)sms * kJoinBlocks;
+    }
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
-    cfg.numAttrs = behind_previous ? 1 : 0;
-    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, merge_kernel<In, Out, NP>, parts, rows, units, out, lse));
+    cfg.numAttrs = USED ? 1 : 0;
+    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, merge_kernel<In, Out, NP, USED>, parts, rows, units, out, lse));
     return NSA_OK;
 }
 
 template <typename In, typename Out>
-nsa_status launch_n(int n, const MergeParts &parts, int64_t rows, int D, void *out, float *lse, bool behind, cudaStream_t s)
+nsa_status launch_n(int n, const MergeParts &parts, int64_t rows, int D, void *out, float *lse, cudaStream_t s)
 {
     Out *o = (Out *)out;
     switch (n) {
-    case 1: return launch<In, Out, 1>(parts, rows, D, o, lse, behind, s);
-    case 2: return launch<In, Out, 2>(parts, rows, D, o, lse, behind, s);
-    case 3: return launch<In, Out, 3>(parts, rows, D, o, lse, behind, s);
-    case 4: return launch<In, Out, 4>(parts, rows, D, o, lse, behind, s);
-    case 5: return launch<In, Out, 5>(parts, rows, D, o, lse, behind, s);
-    case 6: return launch<In, Out, 6>(parts, rows, D, o, lse, behind, s);
-    case 7: return launch<In, Out, 7>(parts, rows, D, o, lse, behind, s);
-    default: return launch<In, Out, 8>(parts, rows, D, o, lse, behind, s);
+    case 1: return launch<In, Out, 1>(parts, rows, D, o, lse, s);
+    case 2: return launch<In, Out, 2>(parts, rows, D, o, lse, s);
+    case 3: return launch<In, Out, 3>(parts, rows, D, o, lse, s);
+    case 4: return launch<In, Out, 4>(parts, rows, D, o, lse, s);
+    case 5: return launch<In, Out, 5>(parts, rows, D, o, lse, s);
+    case 6: return launch<In, Out, 6>(parts, rows, D, o, lse, s);
+    case 7: return launch<In, Out, 7>(parts, rows, D, o, lse, s);
+    default: return launch<In, Out, 8>(parts, rows, D, o, lse, s);
     }
 }
 
 }  // namespace
 
 nsa_status merge_launch(nsa_dtype part_dtype, nsa_dtype out_dtype, int n, const MergeParts &parts, int64_t rows, int D,
-                        void *out, float *lse, bool behind_previous, cudaStream_t s)
+                        void *out, float *lse, cudaStream_t s)
 {
-    if (part_dtype == NSA_DT_BF16) return launch_n<__nv_bfloat16, __nv_bfloat16>(n, parts, rows, D, out, lse, behind_previous, s);
-    if (out_dtype == NSA_DT_BF16) return launch_n<float, __nv_bfloat16>(n, parts, rows, D, out, lse, behind_previous, s);
-    return launch_n<float, float>(n, parts, rows, D, out, lse, behind_previous, s);
+    if (parts.used)
+        return launch<float, __nv_bfloat16, kMaxMergeParts, true>(parts, rows, D, (__nv_bfloat16 *)out, lse, s);
+    if (part_dtype == NSA_DT_BF16) return launch_n<__nv_bfloat16, __nv_bfloat16>(n, parts, rows, D, out, lse, s);
+    if (out_dtype == NSA_DT_BF16) return launch_n<float, __nv_bfloat16>(n, parts, rows, D, out, lse, s);
+    return launch_n<float, float>(n, parts, rows, D, out, lse, s);
 }
 
 }  // namespace nsa
@@ -163,5 +171,5 @@ extern "C" nsa_status nsa_merge_attention(nsa_dtype part_dtype, nsa_dtype out_dt
         word |= (uintptr_t)lses_dev[i];
     }
     if ((wide & 15) || (word & 3)) return NSA_ERR_INVALID_ARG;
-    return merge_launch(part_dtype, out_dtype, n_parts, parts, rows, D, out_dev, lse_dev, false, (cudaStream_t)stream);
+    return merge_launch(part_dtype, out_dtype, n_parts, parts, rows, D, out_dev, lse_dev, (cudaStream_t)stream);
 }

@@ -56,18 +56,17 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int 
 __device__ __forceinline__ void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
 // Joins `n` parts ([rows, D] values, [rows] lse) into out and lse, as nsa_merge_attention does.
-// behind_previous: the launch may begin while the one before it, which writes the parts, ends.
 constexpr int kMaxMergeParts = 8;
 struct MergeParts {
     const void *out[kMaxMergeParts];
     const float *lse[kMaxMergeParts];
-    // NULL, or on the device: only rows from *live_from x live_rows up to *live_to x live_rows are written
-    const int32_t *live_from, *live_to;
+    // Or, for what the launch before this one leaves (fp32 parts, a bf16 result), on the device: how many of the
+    // parts there are (nothing is written if there is one), and of the rows only those from *live_from x live_rows
+    // up to *live_to x live_rows are.  NULL: all
+    const int32_t *used, *live_from, *live_to;
     int live_rows;
-    // NULL, or on the device: how many of the parts there are; nothing is written if there is one
-    const int32_t *used;
 };
 nsa_status merge_launch(nsa_dtype part_dtype, nsa_dtype out_dtype, int n, const MergeParts &parts, int64_t rows, int D,
-                        void *out, float *lse, bool behind_previous, cudaStream_t stream);
+                        void *out, float *lse, cudaStream_t stream);
 
 }  // namespace nsa

@@ -180,10 +180,34 @@ struct Work {
     int parts;       // that the keys of each are cut into
 };
 
-// Parts: where there are few items, or a few long ones, their keys are cut into shares.  In units of a
-// step (1.75 us): the SMs' even share of all steps, the longest share as what the last of them may
-// be late by, two steps an item for its start and end, and for the join its launch and the fp32
-// results that it reads (0.13 us for 6 items on 152 SMs).
+// Parts: where there are few items, or a few long ones, their keys are cut into shares.  What c shares cost, in units
+// of a step (1.75 us): items of about one length go in rounds over the SMs; of different lengths, handed out longest
+// first per request, they end within half a long one of each other.  An item takes two steps beside its own for
+// its start and end; the join its launch and the fp32 results that it reads (0.12 us for 6 items on 152 SMs).
+__host__ __device__ inline float parts_cost(int c, float items, float steps, float longest, float sms)
+{
+    const float share = ceilf(longest / c) + 2.f, each = items * c;
+    const float even = (steps + 2.f * each) / sms;
+    const float join = c > 1 ? kJoinCost + each / 90.f : 0.f;
+    if (each <= sms) return join + share;
+    return join + (steps >= 0.8f * items * longest ? ceilf(each / sms) * share : fmaxf(share, even + 0.5f * share));
+}
+__host__ __device__ inline int best_parts(int most, float items, float steps, float longest, float sms)
+{
+    int best = 1;
+    for (int c = 2; c <= most && c <= longest; ++c)
+        if (parts_cost(c, items, steps, longest, sms) < parts_cost(best, items, steps, longest, sms)) best = c;
+    return best;
+}
+
+// Keys that block i of 256 queries of a request sees at most, in steps.
+__host__ __device__ inline int block_steps(int nq, int nk, bool causal, int i)
+{
+    const int last = (i + 1) * kBlock < nq ? (i + 1) * kBlock : nq;
+    const int vis = causal && nk - nq + last < nk ? nk - nq + last : nk;
+    return vis > 0 ? (vis + kTile - 1) / kTile : 0;
+}
+
 __device__ Work plan(const Params &p, int lane)
 {
     int64_t n = 0, steps = 0, longest = 0;
@@ -193,10 +217,9 @@ __device__ Work plan(const Params &p, int lane)
         n += blocks;
         if (p.most_parts == 1) continue;
         for (int i = 0; i < blocks; ++i) {  // few: the launch allows parts for few items alone
-            const int vis = p.causal ? min(r.w, r.w - r.y + min(r.y, (i + 1) * kBlock)) : r.w;
-            const int64_t s = vis > 0 ? (vis + kTile - 1) / kTile : 0;
-            steps += s;
-            longest = max(longest, s);
+            const int64_t k = block_steps(r.y, r.w, p.causal, i);
+            steps += k;
+            longest = max(longest, k);
         }
     }
     for (int o = 16; o > 0; o /= 2) {
@@ -208,18 +231,7 @@ __device__ Work plan(const Params &p, int lane)
         if (lane == 0) set_status(p.status, NSA_ERR_BOUNDS);
         n = 0;
     }
-    Work w = {(int)n, 1};
-    const float items = (float)n * (float)p.H, all = (float)(steps * p.H), sms = (float)gridDim.x;
-    float best = INFINITY;
-    for (int c = 1; c <= p.most_parts && (c == 1 || c <= longest); ++c) {
-        const float share = ceilf((float)longest / c), each = items * c;
-        const float cost = (each <= sms ? share + 2.f : (all + 2.f * each) / sms + share) + (c > 1 ? kJoinCost + each / 90.f : 0.f);
-        if (cost < best) {
-            best = cost;
-            w.parts = c;
-        }
-    }
-    return w;
+    return {(int)n, best_parts(p.most_parts, (float)n * (float)p.H, (float)(steps * p.H), (float)longest, (float)gridDim.x)};
 }
 
 // Item w of blocks x H x parts (below 2^31: the launch checks); first_requests: request `lane`, kept between
@@ -853,15 +865,23 @@ int64_t most_blocks(int B, int total_q)
 }
 
 // Parts are for calls of fewer items an SM than this, which bounds the workspace.
-constexpr int kPartItems = 8;
+constexpr int kPartItems = 4;
 constexpr size_t kHeadBytes = 256;  // of the workspace, before the parts: the items taken, the parts made
 
-int most_parts_of(int total_q, int total_k, int H, int sms)
+int most_parts_of(int B, int total_q, int total_k, int H, bool causal, int sms)
 {
     const int64_t items = ceil_div(total_q, kBlock) * H;  // at least
     if (items >= (int64_t)kPartItems * sms || total_k <= 2 * kTile) return 1;
     const int64_t fit = (int64_t)kPartItems * sms * kBlock / ((int64_t)total_q * H);
-    return (int)(fit < 1 ? 1 : fit < kMaxMergeParts ? fit : kMaxMergeParts);
+    const int most = (int)(fit < 1 ? 1 : fit < kMaxMergeParts ? fit : kMaxMergeParts);
+    if (B > 1) return most;  // the device knows the lengths
+    int64_t steps = 0, longest = 0;
+    for (int i = 0; i < (int)ceil_div(total_q, kBlock); ++i) {
+        const int64_t k = block_steps(total_q, total_k, causal, i);
+        steps += k;
+        longest = longest > k ? longest : k;
+    }
+    return best_parts(most, (float)items, (float)(steps * H), (float)longest, (float)sms);
 }
 
 // Heads of a section (decode): as many as leave their keys and values (512 bytes a key) in L2, but enough for
@@ -929,7 +949,7 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     p.B = B; p.total_q = total_q; p.total_k = total_k; p.H = H; p.causal = causal;
     const int64_t items = most_blocks(B, total_q) * H;
     p.most_blocks = (int)most_blocks(B, total_q);
-    p.most_parts = most_parts_of(total_q, total_k, H, sms);
+    p.most_parts = most_parts_of(B, total_q, total_k, H, causal, sms);
     p.heads_at_once = heads_at_once_of(p.most_blocks, total_k, H, sms);
     p.scale = sm_scale;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
@@ -983,5 +1003,5 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
     parts.live_to = cu_seqlens_q_dev + B;
     parts.live_rows = H;
     parts.used = p.parts_used;
-    return merge_launch(NSA_DT_F32, NSA_DT_BF16, p.most_parts, parts, (int64_t)total_q * H, kMlaV, out_dev, lse_dev, true, s);
+    return merge_launch(NSA_DT_F32, NSA_DT_BF16, p.most_parts, parts, (int64_t)total_q * H, kMlaV, out_dev, lse_dev, s);
 }
