@@ -3,7 +3,8 @@
 // as the chunks of a long prefix, or the shares of a row's keys, leave it.
 //
 // Bound by memory: every part is read once and the result written once, 16 bytes and more a
-// thread and part, all parts' loads in flight together.  A thread block holds whole rows, so that
+// thread and part, all parts' loads in flight together (three bf16 parts of 8192 x 128 rows of 128:
+// 180 us, 6.1 TB/s, 91 % of a copy; 213 us when the values waited for their lse).  A thread block holds whole rows, so that
 // the result may take the place of a part: every lse is read before any is written.
 #include "mla_forms.cuh"
 

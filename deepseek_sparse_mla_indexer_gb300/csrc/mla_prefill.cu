@@ -31,9 +31,10 @@
 // merge_launch joins them.
 //
 // Measured (GB300, a pass among others; of 1969 TFLOP/s):
-//   one causal prompt of 8192, 128 heads       1650 us   1.66 PFLOP/s, 84 %
-//   eight prompts of 189 .. 2000, 128 heads     329 us   0.97, 49 % (1.16 with the hidden parts of the tiles)
-//   1001 / 768 over 40000 / 26651, 16 heads     470 us   1.32, 67 %
+//   one causal prompt of 8192, 128 heads       1650 us   1.67 PFLOP/s, 85 %
+//   the same with 32 heads                      431 us   1.59, 81 %
+//   eight prompts of 189 .. 2000, 128 heads     324 us   0.99, 50 % (1.18 with the hidden parts of the tiles)
+//   1001 / 768 over 40000 / 26651, 16 heads     424 us   1.46, 74 %
 //   37 after 600, 16 heads                       11.5 us in a graph, 39 with the host's part of the call
 // A step of both tiles takes 3310 cycles where its products alone take 2560: the tensor core reads
 // shared memory at its full rate during QK (8 KB a product of 64 cycles), and the 80 KB that TMA writes a
@@ -153,13 +154,13 @@ __device__ __forceinline__ void store_sector(void *p, const uint32_t (&v)[8], bo
     }
 }
 
-// Queries and keys of request b; a request whose ranges are not in order is reported and has no queries.
+// Queries and keys of request b; a request whose ranges are not in order is reported and has -1 queries (no block).
 __device__ __forceinline__ int4 request(const Params &p, int b)
 {
     const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
     if (q0 < 0 || q1 < q0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k) {
         set_status(p.status, NSA_ERR_BOUNDS);
-        return make_int4(0, 0, 0, 0);
+        return make_int4(0, -1, 0, 0);
     }
     return make_int4(q0, q1 - q0, k0, k1 - k0);
 }
@@ -211,10 +212,12 @@ __host__ __device__ inline int block_steps(int nq, int nk, bool causal, int i)
 __device__ Work plan(const Params &p, int lane)
 {
     int64_t n = 0, steps = 0, longest = 0;
+    bool bad = false;
     for (int b = lane; b < p.B; b += 32) {
         const int4 r = request(p, b);
         const int blocks = (r.y + kBlock - 1) / kBlock;
         n += blocks;
+        bad |= r.y < 0;
         if (p.most_parts == 1) continue;
         for (int i = 0; i < blocks; ++i) {  // few: the launch allows parts for few items alone
             const int64_t k = block_steps(r.y, r.w, p.causal, i);
@@ -231,6 +234,8 @@ __device__ Work plan(const Params &p, int lane)
         if (lane == 0) set_status(p.status, NSA_ERR_BOUNDS);
         n = 0;
     }
+    // (the join would write the rows of a request that is left out)
+    if (n == 0 || __any_sync(0xffffffffu, bad)) return {(int)n, 1};
     return {(int)n, best_parts(p.most_parts, (float)n * (float)p.H, (float)(steps * p.H), (float)longest, (float)gridDim.x)};
 }
 

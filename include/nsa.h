@@ -716,7 +716,8 @@ size_t nsa_evict_compact_workspace_bytes(int B, int max_len);
  * smaller than what they step over (a single row's or head's stride is not looked at); else
  * NSA_ERR_INVALID_ARG before any launch, as for NULL, misaligned words, bad sizes or
  * too small a workspace.  NSA_ERR_UNSUPPORTED for more than 65535 heads or 2^30 rows.
- * A bounded wait inside a kernel that runs out sets NSA_ERR_TIMEOUT.
+ * Outputs and workspaces may not overlap inputs (but for nsa_merge_attention's).  A bounded
+ * wait inside a kernel that runs out sets NSA_ERR_TIMEOUT.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -759,7 +760,8 @@ size_t nsa_mla_expand_kv_workspace_bytes(int m);
  *                           of their own; nothing is kept in it between calls
  * Each weight is rounded to bf16 (2^-8 of itself at most) for its product with the values; lse and the
  * sum that divides are taken before that.  What a row does not see is never used, whatever it
- * holds: a NaN or infinity at a key reaches only the rows that see it.  A score of -inf has weight 0,
+ * holds: a NaN or infinity at a key reaches only the rows that see it (a block of 256 rows some of
+ * which do not see all keys takes twice as long if a result of it is not finite).  A score of -inf has weight 0,
  * as in the formula (a component of out is NaN, 0 x inf, where that key's value is not finite); a row
  * all of whose scores are -inf has lse -inf and zeros.  A score of NaN or +inf makes the row NaN.
  * Device error (NSA_ERR_BOUNDS): a request whose starts decrease or leave [0, total] is left out.
@@ -778,7 +780,7 @@ size_t nsa_mla_prefill_workspace_bytes(void);
  * Attention over parts of the keys, joined: with each part's out [rows, D] and lse [rows] (natural
  * log; rows = query rows x heads),
  *   lse = ln sum_p exp(lse_p)      out = sum_p exp(lse_p - lse) out_p
- * A part with lse -inf saw no key: its values are not looked at.  A row without a key in any part
+ * A part with lse -inf saw no key: its values are not used, whatever they are.  A row without a key in any part
  * gets out 0 and lse -inf.  NaN or +inf in a row's lse makes the row NaN.
  *   parts_dev, lses_dev  host arrays of n_parts (at most 8) device pointers; part_dtype BF16 or F32
  *   out_dev, lse_dev     out_dtype BF16, or F32 for F32 parts.  They may be a part's own arrays (of the same

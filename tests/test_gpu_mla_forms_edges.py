@@ -98,6 +98,31 @@ def test_overlapping_requests_are_reported():
     assert nsa.nsa_status_read(status) == nsa.ERR_BOUNDS
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_request_left_out_of_long_ones(causal):
+    # few items over long rows, whose keys a good call cuts into parts
+    g = torch.Generator().manual_seed(8)
+    nq, nk = [40, 30, 50], [5000, 3000, 4000]
+    q, kv, rope = F.rand(g, 120, 1, 192), F.rand(g, 12000, 1, 256), F.rand(g, 12000, 64)
+    o, l, to, tl = F.attention(q, kv, rope, nq, nk, causal)
+    for bad, left in ([0, 5000, 8000, 12001], slice(70, 120)), ([-1, 5000, 8000, 12000], slice(0, 40)), \
+            ([0, 5000, 4999, 12000], slice(40, 120)):
+        out, lse = torch.full((120, 1, 128), 7.0, dtype=F.BF, device=D), torch.full((120, 1), 7.0, device=D)
+        status = torch.zeros(1, dtype=torch.int32, device=D)
+        ws = nsa.alloc_mla_prefill_workspace()
+        nsa.nsa_mla_prefill(q.to(D)[..., :128], q.to(D)[..., 128:], kv.to(D)[..., :128], rope.to(D), kv.to(D)[..., 128:],
+                            F.starts(nq).to(D), torch.tensor(bad, dtype=torch.int32, device=D), causal, F.SCALE, out, lse, ws, status)
+        assert nsa.nsa_status_read(status) == nsa.ERR_BOUNDS
+        keep = torch.ones(120, dtype=torch.bool)
+        keep[left] = False
+        if bad[2] == 4999:  # (request 2 is in order, but has other keys)
+            assert (out[40:70] == 7).all() and (lse[40:70] == 7).all() and not (lse[70:] == 7).any()
+        else:
+            assert (out[left] == 7).all() and (lse[left] == 7).all()
+        F.close(lse.cpu()[keep], l[keep], tl[keep], "lse")
+        F.close(out.cpu()[keep], o[keep], to[keep], "out")
+
+
 def test_one_row_and_one_head_of_any_stride():
     g = torch.Generator().manual_seed(7)
     q, kv, rope = F.rand(g, 9, 1, 192).to(D), F.rand(g, 30, 1, 256).to(D), F.rand(g, 30, 64).to(D)

@@ -213,3 +213,11 @@ def test_merge_abi(nsa):
     for kw in (dict(dt=2), dict(dt=1, odt=0), dict(dt=0, odt=2), dict(n=9), dict(D=12), dict(D=2056)):
         assert call(**kw) == UNSUPPORTED, kw
     assert call(rows=0) == 0
+
+
+def test_rows_past_32_bit_coordinates(nsa):
+    big = (1 << 30) + 1
+    expand = [1, A, 64, A, big, A, 2, 512, 64, 128, 128, A, A, A, big * 1024, 0, 0]
+    assert _status(nsa, "nsa_mla_expand_kv", expand) == UNSUPPORTED
+    for fn, ld in ("nsa_mla_absorb_q", 128), ("nsa_mla_project_v", 512):
+        assert _status(nsa, fn, [A, 2 * ld, ld, A, big, 2, 128, 128, 512, A, 0, 0]) == UNSUPPORTED
