@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Dict, Optional
 
 import numpy as np
@@ -778,7 +779,6 @@ def nsa_mla_prefill(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Te
 
 
 _DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
-_POINTERS = [C.c_void_p * n for n in range(9)]
 
 
 def nsa_merge_attention(parts, lses, out: torch.Tensor, lse: torch.Tensor, stream=None) -> None:
@@ -791,16 +791,24 @@ def nsa_merge_attention(parts, lses, out: torch.Tensor, lse: torch.Tensor, strea
     rows = shape[:-1]
     if dtype not in _DTYPES or out.dtype not in _DTYPES:
         raise ValueError(f"parts and out must be float32 or bf16, got {dtype} and {out.dtype}")
-    for p, l in ((out, lse), *zip(parts, lses)):
-        if p.shape != shape or l.shape != rows or len(shape) < 1 or not p.is_contiguous() or not l.is_contiguous() or \
-                l.dtype is not torch.float32 or (p is not out and p.dtype is not dtype):
-            raise ValueError(f"parts must be contiguous {dtype} {list(shape)} and lses contiguous float32 {list(rows)}, "
-                             f"got {p.dtype} {list(p.shape)} and {l.dtype} {list(l.shape)}")
+    ptrs, lptrs = [], []  # (addresses; this call is as short as its checks)
+    for p, l in zip(parts, lses):
+        if p.shape != shape or l.shape != rows or p.dtype is not dtype or l.dtype is not torch.float32 or \
+                not p.is_contiguous() or not l.is_contiguous():
+            _refuse_part(p, l, dtype, shape)
+        ptrs.append(p.data_ptr())
+        lptrs.append(l.data_ptr())
+    if not shape or lse.shape != rows or lse.dtype is not torch.float32 or not out.is_contiguous() or not lse.is_contiguous():
+        _refuse_part(out, lse, out.dtype, shape)
     handle = _launch_on(stream, out, lse, *parts, *lses)
-    array = _POINTERS[n] if n < len(_POINTERS) else C.c_void_p * n
-    ptrs, lptrs = array(*[p.data_ptr() for p in parts]), array(*[l.data_ptr() for l in lses])
-    _check("nsa_merge_attention", load().nsa_merge_attention(_DTYPES[dtype], _DTYPES[out.dtype], n, ptrs, lptrs, lse.numel(),
-                                                             shape[-1], _at(out), _at(lse), handle))
+    _check("nsa_merge_attention", load().nsa_merge_attention(
+        _DTYPES[dtype], _DTYPES[out.dtype], n, struct.pack(f"{n}P", *ptrs), struct.pack(f"{n}P", *lptrs), lse.numel(), shape[-1],
+        _at(out), _at(lse), handle))
+
+
+def _refuse_part(p: torch.Tensor, l: torch.Tensor, dtype, shape):
+    raise ValueError(f"parts must be contiguous {dtype} {list(shape)} and lses contiguous float32 {list(shape[:-1])}, "
+                     f"got {p.dtype} {list(p.shape)} and {l.dtype} {list(l.shape)}")
 
 
 def nsa_mla_absorb_q(q_nope: torch.Tensor, w: torch.Tensor, out: torch.Tensor, status: Optional[torch.Tensor] = None,

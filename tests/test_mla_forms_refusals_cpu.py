@@ -221,3 +221,11 @@ def test_rows_past_32_bit_coordinates(nsa):
     assert _status(nsa, "nsa_mla_expand_kv", expand) == UNSUPPORTED
     for fn, ld in ("nsa_mla_absorb_q", 128), ("nsa_mla_project_v", 512):
         assert _status(nsa, fn, [A, 2 * ld, ld, A, big, 2, 128, 128, 512, A, 0, 0]) == UNSUPPORTED
+
+
+def test_merge_of_a_part_of_another_type_that_is_the_result(nsa):
+    a, b, l = z(4, 16, d=F32), z(4, 16), z(4, d=F32)
+    with pytest.raises(ValueError, match="parts must be contiguous"):
+        nsa.nsa_merge_attention([a, b], [l, l], b, l)
+    with pytest.raises(ValueError, match="parts must be contiguous"):
+        nsa.nsa_merge_attention([z(d=F32)], [l], z(d=F32), l)
