@@ -10,10 +10,11 @@
 //   O[128 q, 128]     += P V          8 products, P (bf16) in TMEM in the place of S
 // S, P and O of both tiles fill TMEM (512 columns).  While 256 threads turn one tile's scores into
 // P, the tensor core works on the other tile: PV of the step before, QK of the next.  A row's
-// maximum is only refreshed, and O rescaled by the threads themselves, when it has grown by more
-// than 2^8: until then weights are up to 2^8 and nothing is lost, since sums are fp32.  So a step's
-// weights are taken with the old maximum right away, and its own maximum only says afterwards
-// whether that was right.  Weights are rounded to bf16 (2^-8 of themselves at most) for the product
+// maximum is only refreshed, and O rescaled by the threads themselves, when a thread's 64 weights add up
+// to more than 2^8: until then weights are up to 2^8 and nothing is lost, since sums are fp32.  So a
+// step's weights are taken with the old maximum right away, and their sum, which is needed anyway, says
+// afterwards whether that was right (one 8192-token prompt of 128 heads: 1598 us, and 1660 with every
+// step's own maximum beside it).  Weights are rounded to bf16 (2^-8 of themselves at most) for the product
 // with V, whose type the operands share; their sum, and so lse, is taken before that rounding.
 //
 // Keys and values come by TMA through a ring of eight 16 KB slots (a step takes five: two halves of
@@ -61,10 +62,10 @@ constexpr int kSoftmaxWarps = 16;          // per tile eight: two threads a quer
 constexpr int kHalf = kTile / 2;
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kScanWarp = 18, kScanWarps = 2;
 constexpr int kThreads = 32 * (kScanWarp + kScanWarps);  // 20 warps: a 21st would leave each thread 80 registers instead of 96
-constexpr uint32_t kTmemCols = 512;        // S / P of tile t at 128 t, O at 256 + 128 t
+constexpr uint32_t kTmemCols = 512;        // S of tile t at 128 t, each half's P in its first 32 columns; O at 256 + 128 t
 constexpr long long kItemWait = 64 * kMlaWait;
 constexpr float kJoinCost = 1.5f;           // steps
-constexpr float kRescale = 8.0f;           // log2 units
+constexpr float kGrown = 256.0f;           // sum of a thread's weights that asks for a fresh maximum
 
 // One work item, as the loading warp hands it to the others.
 struct Item {
@@ -92,8 +93,8 @@ struct Shared {
     int again[2];                 // the item is to be done once more, with care
     uint32_t tmem;
     volatile int abort;
-    // [tile][half]: a query's maximum over its half of the step, at the end its sum of weights.  The next
-    // step's scores come behind all P of this one, so nobody still reads when they are written
+    // [tile][half]: a query's maximum over its half of the step, at the end its sum of weights, for the thread of
+    // its other half
     float top[2][2][kTile];
 };
 constexpr uint32_t kSmem = 2 * kQTile + kSlots * kSlot + sizeof(Shared);
@@ -141,11 +142,12 @@ __device__ __forceinline__ void mma_lo_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
-// 32 bytes: one whole sector of L2 where the address allows it, since every thread of a warp writes a row of its own.
+// 32 bytes: one whole sector of L2 where the address allows it, since every thread of a warp writes a row of its own
+// (past L1: one 8192-token prompt of 128 heads 1548 us, and 1555 through it).
 __device__ __forceinline__ void store_sector(void *p, const uint32_t (&v)[8], bool wide)
 {
     if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+        asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                      "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                      : "memory");
     } else {
@@ -566,7 +568,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 const uint32_t b = (uint32_t)v_desc + (kStepSlots * at + kKSlots + x) % kSlots * (kSlot / 16);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_lo_ts(tmem + 2 * kTile + t * kMlaV, tmem + t * kTile + x * 32 + k * 8, b + k * (2048 / 16), v_hi, idesc_o,
+                    mma_lo_ts(tmem + 2 * kTile + t * kMlaV, tmem + t * kTile + x * kHalf + k * 8, b + k * (2048 / 16), v_hi, idesc_o,
                               !first || x > 0 || k > 0);
             }
             if (last) mma_commit(&sm->o_full[t]);
@@ -690,17 +692,18 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
     } else {
         // ------------------------------------------------------------ softmax: two threads a query, 64 keys each
         const int t = (warp / 4) & 1, half = warp / 8, row = (warp & 3) * 32 + lane;  // of tile t
+        const int two = 1 + t * 4 + (warp & 3);  // the barrier of the two warps that share their queries
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t s_at = lanes + t * kTile + half * kHalf, p_at = lanes + t * kTile + half * (kHalf / 2);
+        const uint32_t s_at = lanes + t * kTile + half * kHalf;
         const uint32_t o_at = lanes + 2 * kTile + t * kMlaV + half * kHalf;
         uint32_t s_uses = 0, o_uses = 0;
         const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
         for (int i = 0;; ++i) {
-            // The eight warps of a tile meet at barriers, so they give up together: where a wait ran out they go
-            // on to here (the waits that follow return at once)
+            // The two warps of a row meet at barriers, so they give up together: where a wait ran out they go on to
+            // here (the waits that follow return at once)
             ok = item_wait(i) && ok;
             __syncwarp();
-            if (bar_red_or(1 + t, 256, !ok)) {
+            if (bar_red_or(two, 64, !ok)) {
                 ok = false;
                 break;
             }
@@ -719,6 +722,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 float2 sum[2];
                 // Weights with the maximum of the steps before, which hardly ever has to be refreshed; at the first
                 // step, and where some row's has grown too far, with one that is looked for first
+                bool grown = true;
                 for (bool look = j == j0;; look = true) {
                     tmem_ld32(s_at, s[0]);
                     tmem_ld32(s_at + 32, s[1]);
@@ -737,15 +741,15 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
 #pragma unroll
                             for (int y = 0; y < 32; y += 2)
                                 mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[x][y])), __uint_as_float(s[x][y + 1]));
-                        sm->top[t][half][row] = fmaxf(mx[0], mx[1]);
-                        bar_sync(1 + t, 256);
+                        sm->top[t][half][row] = grown ? fmaxf(mx[0], mx[1]) : -INFINITY;
+                        bar_sync(two, 64);
                         const float top = fmaxf(sm->top[t][0][row], sm->top[t][1][row]);
                         if (j == j0) {
                             m = top;
-                        } else if (__any_sync(0xffffffffu, (top - m) * p.scale_log2 > kRescale)) {
+                        } else if (__any_sync(0xffffffffu, top > m)) {
                             // Each row by its own scores: a neighbour's, which may be infinite, do not change its
                             // roundings.  QK of this step was issued behind PV of the one before, so O is at rest
-                            const float fresh = (top - m) * p.scale_log2 > kRescale ? top : m;
+                            const float fresh = fmaxf(top, m);
                             const float f = fresh == m ? 1.f : ex2_approx((m - fresh) * p.scale_log2);
                             m = fresh;
                             l *= f;
@@ -762,72 +766,76 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                     }
                     const float nm = m == -INFINITY ? 0.f : -m * p.scale_log2;
                     const float2 nm2 = make_float2(nm, nm);
-                    float tops[2] = {-INFINITY, -INFINITY};
                     sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
                             const float a = __uint_as_float(s[x][2 * y]), b = __uint_as_float(s[x][2 * y + 1]);
-                            tops[y & 1] = fmaxf(fmaxf(tops[y & 1], a), b);
                             float2 e = fma2(make_float2(a, b), c2, nm2);
                             e.x = ex2_approx(e.x);
                             e.y = ex2_approx(e.y);
                             sum[y & 1] = add2(sum[y & 1], e);
                             s[x][y] = pack_bf16(e.x, e.y);
                         }
-                    // Behind this barrier all scores of the tile are read, and P may take their place
-                    if (!bar_red_or(1 + t, 256, !ok || (fmaxf(tops[0], tops[1]) - m) * p.scale_log2 > kRescale) || look) break;
+                    sum[0] = add2(sum[0], sum[1]);
+                    // Their sum says whether weights are too large; a row without a maximum needs one at its first scores.
+                    // The row's two threads agree
+                    grown = sum[0].x + sum[0].y > kGrown || (m == -INFINITY && seen > 0);
+                    if (!bar_red_or(two, 64, grown) || look) break;
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     uint32_t w[16];
 #pragma unroll
                     for (int y = 0; y < 16; ++y) w[y] = s[x][y];
-                    tmem_st16(p_at + 16 * x, w);
+                    tmem_st16(s_at + 16 * x, w);
                 }
-                const float2 part = add2(sum[0], sum[1]);
-                l += part.x + part.y;
+                l += sum[0].x + sum[0].y;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->go[t]);
             }
-            // ---- the query's result: its sum, then 64 of its values a thread
-            const bool any = j0 < j_end;
-            // (the last `go` is over then, and behind it what the scanning warps wrote of this tile's steps)
-            const bool mine = r < it.rows;
+            // ---- the query's result: its sum, then 64 of its values a thread.  What does not need the last
+            // product comes before it
+            const bool any = j0 < j_end, mine = r < it.rows;
             const int col = half * kHalf, masked = first_masked(it);
+            if (any) {
+                sm->top[t][half][row] = l;
+                bar_sync(two, 64);
+                l = sm->top[t][0][row] + sm->top[t][1][row];  // (written again behind the next item's first barrier)
+            }
+            const float lse = l > 0.f ? fmaf(m, p.scale, logf(l)) : l == l ? -INFINITY : l;
+            const Place to = place(p, it, r, col, l > 0.f ? 1.f / l : l == l ? 0.f : l);
+            float *lse_at = (it.parts > 1 ? p.part_lse + (int64_t)it.part * p.total_q * p.H : p.lse) + (it.row0 + r) * p.H + it.head;
             uint32_t o[2][32];  // (without a step whatever is there: l is 0 then)
             bool again = false;
+            // (the last `go` is over then, and behind it what the scanning warps wrote of this tile's steps)
             if (any) ok = mla_wait(&sm->o_full[t], o_uses++ & 1, abort) && mla_wait(&sm->go[t], (s_uses - 1) & 1, abort) && ok;
             __syncwarp();
             tc_fence_after();
             tmem_ld32(o_at, o[0]);
             tmem_ld32(o_at + 32, o[1]);
             tmem_ld_wait();
-            if (any) {
+            if (any && j_end > masked && !it.careful) {
                 // A value that is not finite, at a key of a masked step, reaches queries that do not see it (as
                 // 0 x inf).  That shows in the result; then the item is done again, with such values taken out
-                float2 z = make_float2(0.f, 0.f);
+                float2 z[4] = {};
 #pragma unroll
                 for (int x = 0; x < 32; ++x)
-                    z = fma2(make_float2(__uint_as_float(o[x / 16][x % 16 * 2]), __uint_as_float(o[x / 16][x % 16 * 2 + 1])),
-                             make_float2(0.f, 0.f), z);
-                sm->top[t][half][row] = l;
-                again = bar_red_or(1 + t, 256, mine && !(z.x + z.y == 0.f)) && j_end > masked && !it.careful;
-                l = sm->top[t][0][row] + sm->top[t][1][row];
-                bar_sync(1 + t, 256);
+                    z[x % 4] = fma2(make_float2(__uint_as_float(o[x / 16][x % 16 * 2]), __uint_as_float(o[x / 16][x % 16 * 2 + 1])),
+                                    make_float2(0.f, 0.f), z[x % 4]);
+                z[0] = add2(add2(z[0], z[1]), add2(z[2], z[3]));
+                again = bar_red_or(two, 64, mine && !(z[0].x + z[0].y == 0.f));
             }
             uint32_t odd = 0;
             if (it.careful)
                 for (int x = 0; x < kMasked && masked + x < j_end; ++x)
                     for (int y = 0; y < 4; ++y) odd |= sm->odd[i & 1][x][y];
-            const int64_t at = ((int64_t)(it.parts > 1 ? it.part : 0) * p.total_q + it.row0 + r) * p.H + it.head;
-            float *lse_out = it.parts > 1 ? p.part_lse : p.lse;
             tc_fence_before();
             if (again) {
-                if (row == 0) sm->again[i & 1] = 1;
+                if (lane == 0) sm->again[i & 1] = 1;
                 item_done(i);
                 continue;
             }
@@ -836,7 +844,6 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 tc_fence_before();
                 item_done(i);
             } else {
-                const Place to = place(p, it, r, col, l > 0.f ? 1.f / l : l == l ? 0.f : l);
                 item_done(i);  // before the stores, whose end it would otherwise wait for
                 if (l == 0.f) {  // no weight at all, or nothing to weigh: 0, and not 0 x NaN
 #pragma unroll
@@ -847,7 +854,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                     store32(to, 1, o[1]);
                 }
             }
-            if (mine && half == 0) lse_out[at] = l > 0.f ? fmaf(m, p.scale, logf(l)) : l == l ? -INFINITY : l;
+            if (mine && half == 0) *lse_at = lse;
             __syncwarp();
         }
         if (!ok && lane == 0) set_status(p.status, NSA_ERR_TIMEOUT);

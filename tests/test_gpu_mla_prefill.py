@@ -221,6 +221,35 @@ def test_far_apart_maxima_and_first_steps_of_minus_infinity():
     F.close(out, o, to, "out")
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("slope", [0.02, 0.2, 3.0, -0.2])
+def test_scores_that_grow_along_the_keys(slope, causal):
+    # the rows' maxima are refreshed again and again, in one half of a step or in both, by some rows only
+    nq, nk, H = [300, 5], [900, 700], 2
+    q, kv, k_rope = _inputs(nq, nk, H, 21)
+    q[..., 0] = torch.arange(305)[:, None] % 7 / F.SCALE / 4
+    kv[..., 0] = (torch.arange(1600) * slope)[:, None]
+    out, lse, status = _run(q, kv, k_rope, nq, nk, causal)
+    assert status == 0
+    o, l, to, tl = F.attention(q, kv, k_rope, nq, nk, causal)
+    F.close(lse, l, tl, "lse")
+    F.close(out, o, to, "out")
+
+
+def test_a_row_does_not_depend_on_its_neighbours():
+    # rows whose maxima are refreshed at other steps, or are not numbers, in the same block
+    nq, nk, H = [256], [1000], 1
+    q, kv, k_rope = _inputs(nq, nk, H, 22)
+    kv[..., 0] = (torch.arange(1000) * 0.1)[:, None]
+    q[..., 0] = 0.0
+    want = _run(q, kv, k_rope, nq, nk, False)
+    q[::2, :, 0] = 40.0
+    q[::16, :, 1] = float("nan")
+    got = _run(q, kv, k_rope, nq, nk, False)
+    assert torch.equal(got[0][1::2], want[0][1::2]) and torch.equal(got[1][1::2], want[1][1::2])
+    assert not torch.equal(got[0][2::16], want[0][2::16]) and torch.isnan(got[0][::16]).all()
+
+
 def test_bad_starts_are_reported_and_left_out():
     nq, nk, H = [4, 5, 6], [4, 5, 6], 2
     q, kv, k_rope = _inputs(nq, nk, H, 14)
