@@ -77,7 +77,8 @@ struct Item {
     int vis0;          // keys that the first query sees (causal: one more each further query); may be negative
     int j0, j1;        // steps of this share, none if j0 >= j1
     int n[2];          // steps that each tile needs at most
-    int part, parts;
+    int part, parts;   // of its request's keys
+    int joined;        // parts that the join reads of each row; 0: the result is whole
     int careful;       // its masked steps' values are looked through (a second time for this item)
 };
 
@@ -167,7 +168,7 @@ __device__ __forceinline__ int4 request(const Params &p, int b)
     return make_int4(q0, q1 - q0, k0, k1 - k0);
 }
 
-// The blocks of 256 queries that requests b0 .. b0 + 31 have up to and with this lane's.
+// The items a head that requests b0 .. b0 + 31 have up to and with this lane's.
 __device__ __forceinline__ int scan_blocks(int blocks, int lane)
 {
     for (int o = 1; o < 32; o *= 2) {
@@ -179,28 +180,21 @@ __device__ __forceinline__ int scan_blocks(int blocks, int lane)
 
 // What a call has to do, from the sequences' starts.
 struct Work {
-    int blocks;      // of 256 queries
-    int parts;       // that the keys of each are cut into
+    int units;       // items a head
+    int parts;       // that the longest request's keys are cut into; 1: none are cut
+    int share;       // steps of such a part; the other requests' are no longer (0: all requests have `parts`)
 };
 
-// Parts: where there are few items, or a few long ones, their keys are cut into shares.  What c shares cost, in units
-// of a step (1.75 us): items of about one length go in rounds over the SMs; of different lengths, handed out longest
-// first per request, they end within half a long one of each other.  An item takes two steps beside its own for
-// its start and end; the join its launch and the fp32 results that it reads (0.12 us for 6 items on 152 SMs).
-__host__ __device__ inline float parts_cost(int c, float items, float steps, float longest, float sms)
+// Parts: where there are few items, or a few long ones, their keys are cut into shares.  What so many shares of a
+// length cost, in units of a step (1.65 us): items of about one length go in rounds over the SMs; of different lengths,
+// handed out longest first per request, they end within half a long one of each other.  An item takes two steps beside
+// its own for its start and end; the join its launch and the fp32 results that it reads (0.12 us for 6 items on 152 SMs).
+__host__ __device__ inline float parts_cost(float items, int longest, float steps, bool cut, float sms)
 {
-    const float share = ceilf(longest / c) + 2.f, each = items * c;
-    const float even = (steps + 2.f * each) / sms;
-    const float join = c > 1 ? kJoinCost + each / 90.f : 0.f;
-    if (each <= sms) return join + share;
-    return join + (steps >= 0.8f * items * longest ? ceilf(each / sms) * share : fmaxf(share, even + 0.5f * share));
-}
-__host__ __device__ inline int best_parts(int most, float items, float steps, float longest, float sms)
-{
-    int best = 1;
-    for (int c = 2; c <= most && c <= longest; ++c)
-        if (parts_cost(c, items, steps, longest, sms) < parts_cost(best, items, steps, longest, sms)) best = c;
-    return best;
+    const float share = longest + 2.f, even = (steps + 2.f * items) / sms;
+    const float join = cut ? kJoinCost + items / 90.f : 0.f;
+    if (items <= sms) return join + share;
+    return join + (steps >= 0.8f * items * longest ? ceilf(items / sms) * share : fmaxf(share, even + 0.5f * share));
 }
 
 // Keys that block i of 256 queries of a request sees at most, in steps.
@@ -211,67 +205,97 @@ __host__ __device__ inline int block_steps(int nq, int nk, bool causal, int i)
     return vis > 0 ? (vis + kTile - 1) / kTile : 0;
 }
 
+__host__ __device__ inline int ceil_of(int a, int b) { return (a + b - 1) / b; }
+
+// Parts of a request, from the steps of its longest block.
+__device__ __forceinline__ int parts_of(const Work &todo, int longest)
+{
+    return todo.parts == 1 || todo.share == 0 ? todo.parts : max(1, ceil_of(longest, todo.share));
+}
+
 __device__ Work plan(const Params &p, int lane)
 {
-    int64_t n = 0, steps = 0, longest = 0;
+    int64_t n = 0, steps = 0;
+    int longest = 0, first_blocks = 0, first_longest = 0;  // (of request `lane`)
     bool bad = false;
     for (int b = lane; b < p.B; b += 32) {
         const int4 r = request(p, b);
-        const int blocks = (r.y + kBlock - 1) / kBlock;
+        const int blocks = ceil_of(r.y, kBlock);
         n += blocks;
         bad |= r.y < 0;
         if (p.most_parts == 1) continue;
-        for (int i = 0; i < blocks; ++i) {  // few: the launch allows parts for few items alone
-            const int64_t k = block_steps(r.y, r.w, p.causal, i);
-            steps += k;
-            longest = max(longest, k);
+        for (int i = 0; i < blocks; ++i)  // few: the launch allows parts for few items alone
+            steps += block_steps(r.y, r.w, p.causal, i);
+        const int last = blocks > 0 ? block_steps(r.y, r.w, p.causal, blocks - 1) : 0;
+        longest = max(longest, last);
+        if (b == lane) {
+            first_blocks = blocks;
+            first_longest = last;
         }
     }
     for (int o = 16; o > 0; o /= 2) {
         n += __shfl_xor_sync(0xffffffffu, n, o);
         steps += __shfl_xor_sync(0xffffffffu, steps, o);
-        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
     }
+    longest = __reduce_max_sync(0xffffffffu, longest);
     if (n > p.most_blocks) {  // requests that overlap: more items than the launch counted on
         if (lane == 0) set_status(p.status, NSA_ERR_BOUNDS);
         n = 0;
     }
+    Work best = {(int)n, 1, 0};
     // (the join would write the rows of a request that is left out)
-    if (n == 0 || __any_sync(0xffffffffu, bad)) return {(int)n, 1};
-    return {(int)n, best_parts(p.most_parts, (float)n * (float)p.H, (float)(steps * p.H), (float)longest, (float)gridDim.x)};
+    if (n == 0 || __any_sync(0xffffffffu, bad)) return best;
+    // All shares of about one length: a short request is cut into fewer than a long one (many requests, into as many)
+    if (p.B == 1) {  // the launch knew the lengths
+        best.parts = longest > 0 ? min(p.most_parts, longest) : 1;
+        best.units = (int)n * best.parts;
+        return best;
+    }
+    const float H = (float)p.H, sms = (float)gridDim.x;
+    float cost = parts_cost((float)n * H, longest, (float)steps * H, false, sms);
+    for (int c = 2; c <= p.most_parts && c <= longest; ++c) {
+        const int share = ceil_of(longest, c);
+        const int units = p.B > 32 ? (int)n * c
+                                   : __reduce_add_sync(0xffffffffu, first_blocks * max(1, ceil_of(first_longest, share)));
+        const float x = parts_cost((float)units * H, share, (float)steps * H, true, sms);
+        if (x < cost) {
+            cost = x;
+            best = {units, p.B > 32 ? c : ceil_of(longest, share), p.B > 32 ? 0 : share};
+        }
+    }
+    return best;
 }
 
-// Item w of blocks x H x parts (below 2^31: the launch checks); first_requests: request `lane`, kept between
+// Item w of units x H (below 2^31: the launch checks); first_requests: request `lane`, kept between
 // calls.  Heads go in sections; in a section all heads of a block of queries follow one another, and a
 // request's blocks go from its last, which sees most keys, to its first.
 __device__ Item decode(const Params &p, int w, const Work &todo, int4 first_requests, int lane)
 {
     Item it;
-    it.part = 0;
-    if (todo.parts > 1) {
-        const int all = w / todo.parts;
-        it.part = w - all * todo.parts;
-        w = all;
-    }
-    const int per = todo.blocks * p.heads_at_once, section = w / per;
+    const int per = todo.units * p.heads_at_once, section = w / per;
     w -= section * per;
     const int h0 = section * p.heads_at_once, hs = min(p.heads_at_once, p.H - h0);
-    int block = w / hs;
-    it.head = h0 + (w - block * hs);
     for (int b0 = 0;; b0 += 32) {
         const int b = b0 + lane;
         const int4 r = b0 == 0 ? first_requests : b < p.B ? request(p, b) : make_int4(0, 0, 0, 0);
-        const int mine = (r.y + kBlock - 1) / kBlock, upto = scan_blocks(mine, lane);
-        const unsigned found = __ballot_sync(0xffffffffu, block < upto);
+        const int blocks = ceil_of(r.y, kBlock);
+        const int parts = blocks > 0 && todo.parts > 1 ? parts_of(todo, block_steps(r.y, r.w, p.causal, blocks - 1)) : 1;
+        const int upto = scan_blocks(blocks * parts, lane);
+        const unsigned found = __ballot_sync(0xffffffffu, w / hs < upto);
         if (!found && b0 + 32 < p.B) {
-            block -= __shfl_sync(0xffffffffu, upto, 31);
+            w -= __shfl_sync(0xffffffffu, upto, 31) * hs;
             continue;
         }
         const int src = found ? __ffs(found) - 1 : 0;  // found, unless the starts changed under the call
         const int q0 = __shfl_sync(0xffffffffu, r.x, src), nq = __shfl_sync(0xffffffffu, r.y, src);
         const int k0 = __shfl_sync(0xffffffffu, r.z, src), nk = __shfl_sync(0xffffffffu, r.w, src);
-        const int last = __shfl_sync(0xffffffffu, upto, src) - 1;
-        const int first = max(0, last - block) * kBlock;
+        const int nb = __shfl_sync(0xffffffffu, blocks, src);
+        it.parts = __shfl_sync(0xffffffffu, parts, src);
+        w -= (__shfl_sync(0xffffffffu, upto, src) - nb * it.parts) * hs;
+        const int all = w / it.parts, block = all / hs;
+        it.part = w - all * it.parts;
+        it.head = h0 + (all - block * hs);
+        const int first = max(0, nb - 1 - block) * kBlock;
         it.row0 = (int64_t)q0 + first;
         it.rows = found ? min(kBlock, nq - first) : 0;
         it.key0 = k0;
@@ -287,9 +311,9 @@ __device__ Item decode(const Params &p, int w, const Work &todo, int4 first_requ
         it.n[t] = rows > kTile * t && vis > 0 ? (vis + kTile - 1) / kTile : 0;
         all = max(all, it.n[t]);
     }
-    it.j0 = (int)((int64_t)all * it.part / todo.parts);
-    it.j1 = (int)((int64_t)all * (it.part + 1) / todo.parts);
-    it.parts = todo.parts;
+    it.j0 = (int)((int64_t)all * it.part / it.parts);
+    it.j1 = (int)((int64_t)all * (it.part + 1) / it.parts);
+    it.joined = todo.parts > 1 ? todo.parts : 0;
     it.careful = 0;
     return it;
 }
@@ -309,7 +333,7 @@ __device__ __forceinline__ Place place(const Params &p, const Item &it, int row,
     const int64_t at = (it.row0 + row) * p.H + it.head;
     Place to;
     to.inv = inv;
-    to.whole = it.parts == 1;
+    to.whole = it.joined == 0;
     to.wide = (p.wide & (to.whole ? 1 : 2)) != 0;
     to.dst = to.whole ? (void *)(p.out + at * kMlaV + col)
                       : (void *)(p.part_out + ((int64_t)it.part * p.total_q * p.H + at) * kMlaV + col);
@@ -434,7 +458,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ items and loads
         const Work todo = plan(p, lane);
-        const int total = todo.blocks * p.H * todo.parts;
+        const int total = todo.units * p.H;
         const int4 first_requests = lane < p.B ? request(p, lane) : make_int4(0, 0, 0, 0);
         if (p.parts_used && blockIdx.x == 0 && lane == 0) *p.parts_used = todo.parts;
         uint32_t g = 0, q_uses = 0;  // steps and Q buffers filled so far
@@ -808,7 +832,9 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             }
             const float lse = l > 0.f ? fmaf(m, p.scale, logf(l)) : l == l ? -INFINITY : l;
             const Place to = place(p, it, r, col, l > 0.f ? 1.f / l : l == l ? 0.f : l);
-            float *lse_at = (it.parts > 1 ? p.part_lse + (int64_t)it.part * p.total_q * p.H : p.lse) + (it.row0 + r) * p.H + it.head;
+            float *lse_at = (it.joined ? p.part_lse + (int64_t)it.part * p.total_q * p.H : p.lse) + (it.row0 + r) * p.H + it.head;
+            if (mine && half == 0 && it.part == 0)  // the join sees nothing in parts that this request does not have
+                for (int x = it.parts; x < it.joined; ++x) lse_at[(int64_t)x * p.total_q * p.H] = -INFINITY;
             uint32_t o[2][32];  // (without a step whatever is there: l is 0 then)
             bool again = false;
             // (the last `go` is over then, and behind it what the scanning warps wrote of this tile's steps)
@@ -887,13 +913,20 @@ int most_parts_of(int B, int total_q, int total_k, int H, bool causal, int sms)
     const int64_t fit = (int64_t)kPartItems * sms * kBlock / ((int64_t)total_q * H);
     const int most = (int)(fit < 1 ? 1 : fit < kMaxMergeParts ? fit : kMaxMergeParts);
     if (B > 1) return most;  // the device knows the lengths
-    int64_t steps = 0, longest = 0;
-    for (int i = 0; i < (int)ceil_div(total_q, kBlock); ++i) {
-        const int64_t k = block_steps(total_q, total_k, causal, i);
-        steps += k;
-        longest = longest > k ? longest : k;
+    const int blocks = ceil_of(total_q, kBlock), longest = block_steps(total_q, total_k, causal, blocks - 1);
+    int64_t steps = 0;
+    for (int i = 0; i < blocks; ++i) steps += block_steps(total_q, total_k, causal, i);
+    int best = 1;
+    float cost = parts_cost((float)items, longest, (float)(steps * H), false, (float)sms);
+    for (int c = 2; c <= most && c <= longest; ++c) {
+        const int share = ceil_of(longest, c);
+        const float x = parts_cost((float)items * ceil_of(longest, share), share, (float)(steps * H), true, (float)sms);
+        if (x < cost) {
+            cost = x;
+            best = c;
+        }
     }
-    return best_parts(most, (float)items, (float)(steps * H), (float)longest, (float)sms);
+    return best;
 }
 
 // Heads of a section (decode): as many as leave their keys and values (512 bytes a key) in L2, but enough for

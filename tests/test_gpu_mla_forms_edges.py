@@ -99,6 +99,28 @@ def test_overlapping_requests_are_reported():
 
 
 @pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,nq,nk", [
+    (2, [300, 5, 0, 1, 260], [9000, 700, 40, 5, 3100]),   # other numbers of parts, and none, in one call
+    (1, [7, 1, 9], [6000, 0, 300]),                        # a request without a key beside a long one
+    (3, [2] * 33 + [40], [900] * 33 + [5000]),             # more requests than a warp has lanes
+    (16, [500], [2700]),
+])
+def test_parts_of_requests_of_other_lengths(H, nq, nk, causal):
+    g = torch.Generator().manual_seed(9)
+    q, kv, rope = F.rand(g, sum(nq), H, 192), F.rand(g, sum(nk), H, 256), F.rand(g, sum(nk), 64)
+    ws = nsa.alloc_mla_prefill_workspace()
+    ws.fill_(255)  # (NaN in every part that is not written)
+    out, lse = torch.full((sum(nq), H, 128), 7.0, dtype=F.BF, device=D), torch.full((sum(nq), H), 7.0, device=D)
+    status = torch.zeros(1, dtype=torch.int32, device=D)
+    nsa.nsa_mla_prefill(q.to(D)[..., :128], q.to(D)[..., 128:], kv.to(D)[..., :128], rope.to(D), kv.to(D)[..., 128:], F.starts(nq).to(D),
+                        F.starts(nk).to(D), causal, F.SCALE, out, lse, ws, status)
+    assert nsa.nsa_status_read(status) == 0
+    o, l, to, tl = F.attention(q, kv, rope, nq, nk, causal)
+    F.close(lse, l, tl, "lse")
+    F.close(out, o, to, "out")
+
+
+@pytest.mark.parametrize("causal", [True, False])
 def test_a_request_left_out_of_long_ones(causal):
     # few items over long rows, whose keys a good call cuts into parts
     g = torch.Generator().manual_seed(8)
