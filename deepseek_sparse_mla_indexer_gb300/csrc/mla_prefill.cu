@@ -32,17 +32,17 @@
 // merge_launch joins them.
 //
 // Measured (GB300, a pass among others; of 1969 TFLOP/s):
-//   one causal prompt of 8192, 128 heads       1650 us   1.67 PFLOP/s, 85 %
-//   the same with 32 heads                      431 us   1.59, 81 %
-//   eight prompts of 189 .. 2000, 128 heads     324 us   0.99, 50 % (1.18 with the hidden parts of the tiles)
-//   1001 / 768 over 40000 / 26651, 16 heads     424 us   1.46, 74 %
-//   37 after 600, 16 heads                       11.5 us in a graph, 39 with the host's part of the call
-// A step of both tiles takes 3310 cycles where its products alone take 2560: the tensor core reads
+//   one causal prompt of 8192, 128 heads       1545 us   1.78 PFLOP/s, 90 %
+//   the same with 32 heads                      405 us   1.70, 86 %
+//   eight prompts of 189 .. 2000, 128 heads     325 us   0.99, 50 % (1.18 with the hidden parts of the tiles)
+//   1001 / 768 over 40000 / 26651, 16 heads     388 us   1.60, 81 %
+//   37 after 600, 16 heads                       11.0 us in a graph, 38 with the host's part of the call
+// A step of both tiles takes 3170 cycles where its products alone take 2560: the tensor core reads
 // shared memory at its full rate during QK (8 KB a product of 64 cycles), and the 80 KB that TMA writes a
 // step come on top (640 cycles).  The long prompt runs at the power limit (1.9 GHz at 1375 W when
-// repeated for seconds: 1.46 PFLOP/s, 84 % of what library products sustain).  Short prompts pay
-// about 3.5 us an item beside its steps: the last step's softmax, which only one tile still has,
-// the result's way out and the first step's softmax have no products beside them.
+// repeated for seconds: 1.57 PFLOP/s).  Short prompts pay about 3.8 us an item beside its steps: the last
+// step's softmax, which only one tile still has, the result's way out and the first step's softmax have no
+// products beside them.
 #include "mla_forms.cuh"
 
 namespace nsa {
