@@ -752,8 +752,11 @@ def nsa_mla_prefill(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Te
     k_rope [total_k, 64]; cu_seqlens_q / cu_seqlens_k int32 [B + 1]; out bf16 [total_q, H, 128], lse float32
     [total_q, H].  workspace: alloc_mla_prefill_workspace's."""
     total_q, H = _rows("q_nope", q_nope, _D_NOPE)
-    total_k, B = _bf16("k_rope", k_rope, (None, _D_ROPE), False).shape[0], cu_seqlens_q.numel() - 1
-    bf16, heads_k = torch.bfloat16, (total_k, H, _D_NOPE)
+    bf16, kr = torch.bfloat16, k_rope.shape
+    if len(kr) != 2 or kr[1] != _D_ROPE or k_rope.dtype is not bf16 or k_rope.stride(1) != 1:
+        _bf16("k_rope", k_rope, (None, _D_ROPE), False)
+    total_k, B = kr[0], cu_seqlens_q.numel() - 1
+    heads_k = (total_k, H, _D_NOPE)
     qn, qr, kn, vv = q_nope.stride(), q_rope.stride(), k_nope.stride(), v.stride()
     if not (q_rope.shape == (total_q, H, _D_ROPE) and k_nope.shape == heads_k and v.shape == heads_k and
             out.shape == q_nope.shape and q_rope.dtype is bf16 and k_nope.dtype is bf16 and v.dtype is bf16 and
