@@ -188,11 +188,12 @@ struct Work {
 // Parts: where there are few items, or a few long ones, their keys are cut into shares.  What so many shares of a
 // length cost, in units of a step (1.65 us): items of about one length go in rounds over the SMs; of different lengths,
 // handed out longest first per request, they end within half a long one of each other.  An item takes two steps beside
-// its own for its start and end; the join its launch and the fp32 results that it reads (0.12 us for 6 items on 152 SMs).
-__host__ __device__ inline float parts_cost(float items, int longest, float steps, bool cut, float sms)
+// its own for its start and end; the join its launch and the fp32 results that it reads (`rows` of all parts; 0.12 us for
+// 6 x 256 on 152 SMs; 0: there is no join).
+__host__ __device__ inline float parts_cost(float items, int longest, float steps, float rows, float sms)
 {
     const float share = longest + 2.f, even = (steps + 2.f * items) / sms;
-    const float join = cut ? kJoinCost + items / 90.f : 0.f;
+    const float join = rows > 0.f ? kJoinCost + rows / (90.f * kBlock) : 0.f;
     if (items <= sms) return join + share;
     return join + (steps >= 0.8f * items * longest ? ceilf(items / sms) * share : fmaxf(share, even + 0.5f * share));
 }
@@ -215,7 +216,7 @@ __device__ __forceinline__ int parts_of(const Work &todo, int longest)
 
 __device__ Work plan(const Params &p, int lane)
 {
-    int64_t n = 0, steps = 0;
+    int64_t n = 0, steps = 0, rows = 0;
     int longest = 0, first_blocks = 0, first_longest = 0;  // (of request `lane`)
     bool bad = false;
     for (int b = lane; b < p.B; b += 32) {
@@ -224,6 +225,7 @@ __device__ Work plan(const Params &p, int lane)
         n += blocks;
         bad |= r.y < 0;
         if (p.most_parts == 1) continue;
+        rows += r.y;
         for (int i = 0; i < blocks; ++i)  // few: the launch allows parts for few items alone
             steps += block_steps(r.y, r.w, p.causal, i);
         const int last = blocks > 0 ? block_steps(r.y, r.w, p.causal, blocks - 1) : 0;
@@ -236,6 +238,7 @@ __device__ Work plan(const Params &p, int lane)
     for (int o = 16; o > 0; o /= 2) {
         n += __shfl_xor_sync(0xffffffffu, n, o);
         steps += __shfl_xor_sync(0xffffffffu, steps, o);
+        rows += __shfl_xor_sync(0xffffffffu, rows, o);
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (n > p.most_blocks) {  // requests that overlap: more items than the launch counted on
@@ -252,15 +255,16 @@ __device__ Work plan(const Params &p, int lane)
         return best;
     }
     const float H = (float)p.H, sms = (float)gridDim.x;
-    float cost = parts_cost((float)n * H, longest, (float)steps * H, false, sms);
+    float cost = parts_cost((float)n * H, longest, (float)steps * H, 0.f, sms);
     for (int c = 2; c <= p.most_parts && c <= longest; ++c) {
         const int share = ceil_of(longest, c);
         const int units = p.B > 32 ? (int)n * c
                                    : __reduce_add_sync(0xffffffffu, first_blocks * max(1, ceil_of(first_longest, share)));
-        const float x = parts_cost((float)units * H, share, (float)steps * H, true, sms);
+        const int parts = p.B > 32 ? c : ceil_of(longest, share);
+        const float x = parts_cost((float)units * H, share, (float)steps * H, (float)rows * H * parts, sms);
         if (x < cost) {
             cost = x;
-            best = {units, p.B > 32 ? c : ceil_of(longest, share), p.B > 32 ? 0 : share};
+            best = {units, parts, p.B > 32 ? 0 : share};
         }
     }
     return best;
@@ -917,10 +921,10 @@ int most_parts_of(int B, int total_q, int total_k, int H, bool causal, int sms)
     int64_t steps = 0;
     for (int i = 0; i < blocks; ++i) steps += block_steps(total_q, total_k, causal, i);
     int best = 1;
-    float cost = parts_cost((float)items, longest, (float)(steps * H), false, (float)sms);
+    float cost = parts_cost((float)items, longest, (float)(steps * H), 0.f, (float)sms);
     for (int c = 2; c <= most && c <= longest; ++c) {
         const int share = ceil_of(longest, c);
-        const float x = parts_cost((float)items * ceil_of(longest, share), share, (float)(steps * H), true, (float)sms);
+        const float x = parts_cost((float)items * c, share, (float)(steps * H), (float)total_q * H * c, (float)sms);
         if (x < cost) {
             cost = x;
             best = c;
