@@ -115,7 +115,7 @@ nsa_status launch(const MergeParts &parts, int64_t rows, int D, Out *out, float 
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
-    cfg.numAttrs = USED ? 1 : 0;
+    cfg.numAttrs = 1;
     NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, merge_kernel<In, Out, NP, USED>, parts, rows, units, out, lse));
     return NSA_OK;
 }

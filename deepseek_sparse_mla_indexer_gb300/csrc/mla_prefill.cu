@@ -461,6 +461,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ items and loads
+        pdl_wait();  // (all that the other warps read or write comes behind an item)
         const Work todo = plan(p, lane);
         const int total = todo.units * p.H;
         const int4 first_requests = lane < p.B ? request(p, lane) : make_int4(0, 0, 0, 0);
@@ -1040,8 +1041,15 @@ extern "C" nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, i
         p.next = (int *)workspace_dev;
         NSA_CUDA_TRY(cudaMemsetAsync(p.next, 0, sizeof(*p.next), s));
     }
-    mla_prefill_kernel<<<(unsigned)(work < sms ? work : sms), kThreads, kSmem, s>>>(qn, qr, kn, kr, v, p);
-    if (launch_status() != NSA_OK) return NSA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(work < sms ? work : sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, mla_prefill_kernel, qn, qr, kn, kr, v, p));
     if (p.most_parts == 1) return NSA_OK;
     MergeParts parts = {};
     for (int i = 0; i < p.most_parts; ++i) {

@@ -60,7 +60,6 @@ struct PParams {
     int ft_per_head;   // feature tiles of a head (of X's rows); expand: all, for one head
     int w_head_rows;   // rows of w a head and its first one
     int w_row0;
-    int after_gather;  // X is written by the launch before this one, which may still run
     int32_t *status;
 };
 
@@ -175,7 +174,7 @@ head_product_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_cons
 
     if (warp == kEpiWarps) {
         // ------------------------------------------------------------ loads
-        if (p.after_gather) pdl_wait();
+        pdl_wait();  // (the launch before this one may still run: its last blocks leave room for this one's start)
         if (lane == 0) {
             int st = 0;
             uint32_t ph = 0;
@@ -501,7 +500,7 @@ struct Problem {
     void *out;          // [R, Ho, F] contiguous
     int H, Hx, R, K, F; // F: features of a head (of Hx)
     int w_head_rows, w_row0;
-    bool mn_w, after_gather;
+    bool mn_w, all_heads;  // all_heads: X has none, and all heads' features are one row (expand)
     int32_t *status;
 };
 
@@ -544,7 +543,6 @@ nsa_status launch(const Problem &q, int sms, cudaStream_t stream)
     p.steps = q.K / kStep;
     p.w_head_rows = q.w_head_rows;
     p.w_row0 = q.w_row0;
-    p.after_gather = q.after_gather;
     p.status = q.status;
     const int64_t tiles = (int64_t)p.n_ft * p.n_rt;
     if (tiles > (1 << 30)) return NSA_ERR_UNSUPPORTED;
@@ -556,7 +554,7 @@ nsa_status launch(const Problem &q, int sms, cudaStream_t stream)
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
-    cfg.numAttrs = q.after_gather ? 1 : 0;
+    cfg.numAttrs = 1;
     NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, w_map, x_map, out_map, p));
     return NSA_OK;
 }
@@ -596,7 +594,7 @@ nsa_status launch_pairs(const Problem &q, int sms, cudaStream_t stream)
 // Whether nsa_mla_expand_kv's product goes to pairs: from three rounds of their tiles on.
 bool pairs_for(const Problem &q, int sms)
 {
-    return q.after_gather && sms >= 2 && (int64_t)(q.F / (2 * kFeat)) * ceil_div(q.R, kPairRows) >= 3 * (sms / 2);
+    return q.all_heads && sms >= 2 && (int64_t)(q.F / (2 * kFeat)) * ceil_div(q.R, kPairRows) >= 3 * (sms / 2);
 }
 
 template <bool MN_W>
@@ -632,6 +630,7 @@ gather_rows_kernel(const uint8_t *kv, int64_t num_slots, const int32_t *slots, i
                    int32_t *status)
 {
     pdl_trigger();  // the products' launch waits for this grid's end before it reads `latent`
+    pdl_wait();
     const int i = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
     if (i >= m) return;
     const int64_t slot = slots[i];
@@ -712,14 +711,16 @@ extern "C" nsa_status nsa_mla_expand_kv(nsa_dtype kv_dtype, const void *kv_dev, 
         workspace_bytes < nsa_mla_expand_kv_workspace_bytes(m))
         return NSA_ERR_INVALID_ARG;
     const cudaStream_t s = (cudaStream_t)stream;
-    const unsigned blocks = (unsigned)ceil_div(m, 8);
-    if (kv_dtype == NSA_DT_E4M3)
-        gather_rows_kernel<true><<<blocks, 256, 0, s>>>((const uint8_t *)kv_dev, num_slots, slots_dev, m,
-                                                        (uint8_t *)workspace_dev, (uint8_t *)k_rope_out_dev, status_dev);
-    else
-        gather_rows_kernel<false><<<blocks, 256, 0, s>>>((const uint8_t *)kv_dev, num_slots, slots_dev, m,
-                                                         (uint8_t *)workspace_dev, (uint8_t *)k_rope_out_dev, status_dev);
-    if (launch_status() != NSA_OK) return NSA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ceil_div(m, 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    NSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kv_dtype == NSA_DT_E4M3 ? gather_rows_kernel<true> : gather_rows_kernel<false>,
+                                    (const uint8_t *)kv_dev, num_slots, slots_dev, m, (uint8_t *)workspace_dev,
+                                    (uint8_t *)k_rope_out_dev, status_dev));
     // all heads' 256 features are one row of H * 256 values
     const Problem q = {w_dev, workspace_dev, kMlaLatent, kMlaLatent, kv_out_dev, H, 1, m, kMlaLatent, H * kMlaHeadRows,
                        0, 0, false, true, status_dev};
