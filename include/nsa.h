@@ -759,11 +759,13 @@ size_t nsa_mla_expand_kv_workspace_bytes(int m);
  *                           (the parts of long rows).  Calls that may overlap on the GPU need workspaces
  *                           of their own; nothing is kept in it between calls
  * Each weight is rounded to bf16 (2^-8 of itself at most) for its product with the values; lse and the
- * sum that divides are taken before that.  What a row does not see is never used, whatever it
- * holds: a NaN or infinity at a key reaches only the rows that see it (a block of 256 rows some of
- * which do not see all keys takes twice as long if a result of it is not finite).  A score of -inf has weight 0,
- * as in the formula (a component of out is NaN, 0 x inf, where that key's value is not finite); a row
- * all of whose scores are -inf has lse -inf and zeros.  A score of NaN or +inf makes the row NaN.
+ * sum that divides are taken before that.  The division comes last, and weights are up to 2^8 before it:
+ * values near the end of fp32's range overflow (up to 2^100 there is room for 2^19 keys).
+ * What a row does not see is never used, whatever it holds: a NaN or infinity at a key reaches only the
+ * rows that see it (a block of 256 rows some of which do not see all keys takes twice as long if a result
+ * of it is not finite).  A score of -inf has weight 0, as in the formula (a component of out is NaN,
+ * 0 x inf, where that key's value is not finite); a row all of whose scores are -inf has lse -inf and
+ * zeros.  A score of NaN or +inf makes the row NaN.
  * Device error (NSA_ERR_BOUNDS): a request whose starts decrease or leave [0, total] is left out.
  */
 nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, int64_t qn_ld_h, const void *q_rope_dev,

@@ -174,3 +174,50 @@ def test_queries_that_are_not_finite_stay_alone():
     for a, b in ((out, clean[0]), (lse, clean[1])):
         a[3, 1], a[140, 0] = b[3, 1], b[140, 0]
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_right_behind_what_writes_their_inputs(captured):
+    # one set of buffers, written and read again and again without a wait: a call that began too early shows
+    g = torch.Generator().manual_seed(10)
+    N, R, H, keys = 24, 33, 4, 300
+    src = F.rand(g, N, R, H, 192).to(D)
+    caches, w = F.rand(g, N, keys, 576).to(D), F.weight(g, H).to(D)
+    slots = torch.arange(keys, dtype=torch.int32, device=D)
+    cq, ck = F.starts([R]).to(D), F.starts([keys]).to(D)
+    q, kv = torch.empty_like(src[0]), torch.empty_like(caches[0])
+    kv_new, rope = torch.empty((keys, H, 256), dtype=F.BF, device=D), torch.empty((keys, 64), dtype=F.BF, device=D)
+    lat, out, lse = torch.empty((R, H, 512), dtype=F.BF, device=D), torch.empty((R, H, 128), dtype=F.BF, device=D), torch.empty((R, H), device=D)
+    back, joined, jl = torch.empty_like(out), torch.empty_like(out), torch.empty_like(lse)
+    ws, wse = nsa.alloc_mla_prefill_workspace(), nsa.alloc_mla_expand_workspace(keys)
+
+    def run(i, wait, into):
+        for f in (lambda: q.copy_(src[i]), lambda: kv.copy_(caches[i]),
+                  lambda: nsa.nsa_mla_expand_kv(nsa.DT_BF16, kv, slots, w, kv_new, rope, wse),
+                  lambda: nsa.nsa_mla_prefill(q[..., :128], q[..., 128:], kv_new[..., :128], rope, kv_new[..., 128:], cq, ck, True,
+                                              F.SCALE, out, lse, ws),
+                  lambda: nsa.nsa_mla_absorb_q(q[..., :128], w, lat), lambda: nsa.nsa_mla_project_v(lat, w, back),
+                  lambda: nsa.nsa_merge_attention([out, back], [lse, lse], joined, jl),
+                  lambda: [a.copy_(b) for a, b in zip(into, (out, lat, back, joined, jl))]):
+            f()
+            if wait:
+                torch.cuda.synchronize()
+
+    results = lambda: [tuple(torch.empty_like(t) for t in (out, lat, back, joined, jl)) for _ in range(N)]
+    want, got = results(), results()
+    for i in range(N):
+        run(i, True, want[i])
+    if captured:
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=s):
+            for i in range(N):
+                run(i, False, got[i])
+        graph.replay()
+        graph.replay()
+    else:
+        for i in range(N):
+            run(i, False, got[i])
+    torch.cuda.synchronize()
+    for i in range(N):
+        for a, b in zip(got[i], want[i]):
+            assert torch.equal(a, b)

@@ -236,6 +236,18 @@ def test_scores_that_grow_along_the_keys(slope, causal):
     F.close(out, o, to, "out")
 
 
+def test_large_values_scale_the_result():
+    # a power of two is exact everywhere, before a maximum is refreshed and behind it
+    nq, nk, H = [300], [900], 2
+    q, kv, k_rope = _inputs(nq, nk, H, 23)
+    q[..., 0] = 40.0
+    kv[..., 0] = (torch.arange(900) * 0.05)[:, None]
+    want = _run(q, kv, k_rope, nq, nk, True)
+    kv[..., 128:] *= 2.0 ** 100
+    got = _run(q, kv, k_rope, nq, nk, True)
+    assert torch.equal(got[0], want[0] * 2.0 ** 100) and torch.equal(got[1], want[1])
+
+
 def test_a_row_does_not_depend_on_its_neighbours():
     # rows whose maxima are refreshed at other steps, or are not numbers, in the same block
     nq, nk, H = [256], [1000], 1
