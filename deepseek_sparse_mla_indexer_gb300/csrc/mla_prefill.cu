@@ -450,6 +450,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
     const uint32_t tmem = sm->tmem;
     volatile int *abort = &sm->abort;
     bool ok = true;
+    pdl_wait();  // every warp, so that no bounded wait counts the time of the launch before this one
 
     // Item i as the loading warp published it; its place is given back with item_done.
     // (Warps without work in an item wait for the next one as long as it takes.)
@@ -461,7 +462,6 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ items and loads
-        pdl_wait();  // (all that the other warps read or write comes behind an item)
         const Work todo = plan(p, lane);
         const int total = todo.units * p.H;
         const int4 first_requests = lane < p.B ? request(p, lane) : make_int4(0, 0, 0, 0);

@@ -173,10 +173,12 @@ head_product_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_cons
     tc_fence_after();
     const uint32_t tmem = sm->tmem;
     const int tiles = p.n_ft * p.n_rt;  // at most 2^30 (the launch checks)
+    // The launch before this one may still run (its last blocks leave room for this one's start).  Every warp waits for
+    // its end here, so that none of the bounded waits below counts its time
+    pdl_wait();
 
     if (warp == kEpiWarps) {
         // ------------------------------------------------------------ loads
-        pdl_wait();  // (the launch before this one may still run: its last blocks leave room for this one's start)
         if (lane == 0) {
             int st = 0;
             uint32_t ph = 0;
@@ -376,10 +378,10 @@ pair_product_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_cons
     const int tiles = p.n_ft * p.n_rt, step = gridDim.x / 2;
     volatile int *abort = &sm->abort;
     bool ok = true;
+    pdl_wait();  // every warp, as above
 
     if (warp == kEpiWarps) {
         // ------------------------------------------------------------ loads of this CTA's halves
-        pdl_wait();
         if (lane == 0) {
             int st = 0;
             uint32_t ph = 0;

@@ -1,6 +1,8 @@
 // Self-test of the bounded wait every tensor-core kernel of the library uses:
 // one block waits on an mbarrier that nothing arrives on, with a caller-given
 // cycle budget, and must give up and report NSA_ERR_TIMEOUT instead of hanging.
+// It lets the launch behind it start at once, as a collective may that waits for a slower
+// rank, and so also shows that no call's own bounded waits count such a launch's time.
 #include "nsa_internal.cuh"
 #include "sm100.cuh"
 
@@ -10,6 +12,7 @@ namespace {
 __global__ void bounded_wait_kernel(int32_t *status, long long budget_cycles)
 {
     __shared__ uint64_t bar;
+    pdl_trigger();
     if (threadIdx.x == 0) {
         sm100::mbar_init(&bar, 1);  // one arrival expected; none will come
         sm100::fence_mbar_init();

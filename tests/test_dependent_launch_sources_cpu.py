@@ -24,3 +24,12 @@ def _body(name, kernel):
 def test_sparse_attention_reads_behind_its_wait(array):
     workers = _body("sparse_mla_tc.cu", "sparse_mla_tc_kernel").split("} else {", 1)[1]  # warp 1 reads no global memory
     assert workers.index("pdl_wait()") < workers.index("p." + array)
+
+
+@pytest.mark.parametrize("name,kernel", [("mla_project.cu", "head_product_kernel"), ("mla_project.cu", "pair_product_kernel"),
+                                         ("mla_prefill.cu", "mla_prefill_kernel")])
+def test_bounded_waits_begin_behind_the_launch_before(name, kernel):
+    # every warp passes the wait (it stands outside any branch) before its first wait that may run out
+    body = _body(name, kernel)
+    at = body.index("pdl_wait()")
+    assert body[:at].count("{") == body[:at].count("}") and "mla_wait(" not in body[:at]

@@ -67,3 +67,44 @@ def test_absorb_sparse_attention_project(name, order, captured):
     for i in range(N):
         for a, b in zip(got[i], want[i]):
             assert torch.equal(a, b)
+
+
+def _long_calls():
+    """Calls with bounded waits: (results, call)."""
+    g = torch.Generator().manual_seed(3)
+    H, R = 4, 33
+    empty = lambda *s: torch.empty(s, dtype=F.BF, device=D)
+    q, w, cache = F.rand(g, R, H, 192).to(D), F.weight(g, H).to(D), F.rand(g, 300, 576).to(D)
+    lat, back, out = F.rand(g, R, H, 512).to(D), empty(R, H, 128), empty(R, H, 128)
+    q_lat, lse, ws = empty(R, H, 512), torch.empty((R, H), device=D), nsa.alloc_mla_prefill_workspace()
+    kv, rope, cq, ck = F.rand(g, 300, H, 256).to(D), F.rand(g, 300, 64).to(D), F.starts([R]).to(D), F.starts([300]).to(D)
+
+    def expand(m, H, w):
+        slots = (torch.arange(m) % 300).to(torch.int32).to(D)
+        kv_out, rope_out, ws = empty(m, H, 256), empty(m, 64), nsa.alloc_mla_expand_workspace(m)
+        return (kv_out, rope_out), lambda st: nsa.nsa_mla_expand_kv(nsa.DT_BF16, cache, slots, w, kv_out, rope_out, ws, st)
+
+    return {
+        "absorb": ((q_lat,), lambda st: nsa.nsa_mla_absorb_q(q[..., :128], w, q_lat, st)),
+        "project": ((back,), lambda st: nsa.nsa_mla_project_v(lat, w, back, st)),
+        "expand": expand(100, H, w),
+        "expand on pairs of CTAs": expand(2050, 27, F.weight(g, 27).to(D)),
+        "prefill": ((out, lse), lambda st: nsa.nsa_mla_prefill(q[..., :128], q[..., 128:], kv[..., :128], rope, kv[..., 128:], cq, ck,
+                                                               True, F.SCALE, out, lse, ws, st)),
+    }
+
+
+@pytest.mark.parametrize("name", ["absorb", "project", "expand", "expand on pairs of CTAs", "prefill"])
+def test_behind_a_launch_that_lets_it_start_and_runs_on(name):
+    results, call = _long_calls()[name]
+    waited, status = (torch.zeros(1, dtype=torch.int32, device=D) for _ in range(2))
+    call(status)
+    want = [t.clone() for t in results]
+    for t in results:
+        t.fill_(7)
+    nsa.nsa_check_bounded_wait(waited, 3_000_000_000)  # 1.5 s; the kernels' own waits give up after 2e9 clocks
+    call(status)
+    torch.cuda.synchronize()
+    assert nsa.nsa_status_read(waited) == nsa.ERR_TIMEOUT and nsa.nsa_status_read(status) == 0
+    for a, b in zip(results, want):
+        assert torch.equal(a, b)
