@@ -25,7 +25,11 @@
 // A value that is not finite, at a key that a query must not see, reaches that query as 0 x inf.  It
 // shows in the result: an item whose last steps hide keys from some of its queries (causal diagonal,
 // the end of a request inside a step) and whose result is not finite is done a second time, with
-// care: such values are replaced by 0 in shared memory, and the queries that see them add them.
+// care: such values are replaced by 0 in shared memory, and the queries that see them add them.  What
+// they add needs no weights: with a positive one, whatever it is, a component becomes the value that is not
+// finite (or NaN, from infinities of both signs), and a query sees a prefix of the keys.  So for a
+// component the first key with each kind of such a value says all (every value NaN: 1238 us for 8192 tokens of 32 heads,
+// 447 finite; one item of 256 tokens 110 us, 49 finite, and 15300 with weights taken again for each component).
 //
 // Few items (a short prompt over a long prefix, few heads) are cut along the keys; how often is
 // chosen on the device, where the lengths are.  The parts' fp32 results go to the workspace, and
@@ -56,7 +60,6 @@ constexpr uint32_t kSlot = kTile * 128;    // 128 rows (K, Q) or 2 x 64 rows (V)
 constexpr int kSlots = 8;
 constexpr int kKSlots = 3, kVSlots = 2, kStepSlots = kKSlots + kVSlots;
 constexpr uint32_t kQTile = 3 * kSlot;
-constexpr int kMasked = 3;                 // steps that only some queries of an item see wholly, at most
 
 constexpr int kSoftmaxWarps = 16;          // per tile eight: two threads a query, 64 keys of a step each
 constexpr int kHalf = kTile / 2;
@@ -90,8 +93,8 @@ struct Shared {
     uint64_t item_full[2], item_empty[2];
     uint64_t drained;
     Item item[2];
-    uint32_t odd[2][kMasked][4];  // masked step -> keys whose values are not all finite
     int again[2];                 // the item is to be done once more, with care
+    int odd[2];                   // and then: some value of its masked steps is not finite
     uint32_t tmem;
     volatile int abort;
     // [tile][half]: a query's maximum over its half of the step, at the end its sum of weights, for the thread of
@@ -367,44 +370,49 @@ __device__ __forceinline__ void store32(const Place &to, int x, const uint32_t (
     }
 }
 
-// The result of a warp's queries (64 values from `col` on a thread, sums at o_at) where values of this share's masked
-// steps were taken out as not finite: the queries that see them add them here, times their weights.
-__device__ __noinline__ void rows_with_odd(const Params &p, const Item &it, const uint32_t (*odd)[4], int row, int vis, float m,
-                                           float l, int col, uint32_t o_at)
+// The result of a warp's queries (64 values from `col` on a thread, sums at o_at) where values at the keys from .. to - 1
+// of the request, this share's masked steps, were taken out as not finite: the queries that see them (their first
+// `vis` keys) add them here.
+__device__ __noinline__ void rows_with_odd(const Params &p, const Item &it, int row, int vis, int from, int to, float l, int col,
+                                           uint32_t o_at)
 {
-    const int64_t q = it.row0 + row;
-    const Place to = place(p, it, row, col, l > 0.f ? 1.f / l : l == l ? 0.f : l);
+    // A lane looks through two components: the first key (counted from `from`) whose value is an infinity, with the sign
+    // in the lowest bit, and the first one from which on the component is NaN
+    const int lane = threadIdx.x % 32, none = 1 << 20;
+    int pos[2] = {none, none}, neg[2] = {none, none}, nan[2] = {none, none}, inf[2];
+    const __nv_bfloat16 *v = p.v + (it.key0 + from) * p.v_r + it.head * p.v_h + col + 2 * lane;
+#pragma unroll 8
+    for (int j = 0; j < to - from; ++j) {
+        const uint32_t u = *(const uint32_t *)(v + j * p.v_r);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const uint32_t x = (y ? u : u << 16) & 0xFFFF0000u;
+            if (x << 1 > 0xFF000000u) nan[y] = min(nan[y], j);
+            if (x == 0x7F800000u) pos[y] = min(pos[y], j);
+            if (x == 0xFF800000u) neg[y] = min(neg[y], j);
+        }
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        inf[y] = 2 * min(pos[y], neg[y]) + (neg[y] < pos[y] ? 1 : 0);
+        nan[y] = min(nan[y], max(pos[y], neg[y]));
+    }
+    const Place to_row = place(p, it, row, col, l > 0.f ? 1.f / l : l == l ? 0.f : l);
+    const int seen = vis - from;
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
         uint32_t o[32];
         tmem_ld32(o_at + 32 * x, o);
         tmem_ld_wait();
-        if (row < it.rows) {
-            for (int i = 0; i < kMasked * kTile; ++i) {
-                const int j = first_masked(it) * kTile + i;
-                if (j >= vis) break;
-                if (!(odd[i / kTile][i % kTile / 32] >> (i % 32) & 1)) continue;
-                const int64_t k = it.key0 + j;
-                float s = 0.f;
-                for (int d = 0; d < kMlaNope; ++d)
-                    s = fmaf(__bfloat162float(p.q_nope[q * p.qn_r + it.head * p.qn_h + d]),
-                             __bfloat162float(p.k_nope[k * p.kn_r + it.head * p.kn_h + d]), s);
-                for (int d = 0; d < kMlaRope; ++d)
-                    s = fmaf(__bfloat162float(p.q_rope[q * p.qr_r + it.head * p.qr_h + d]),
-                             __bfloat162float(p.k_rope[k * p.kr_r + d]), s);
-                const float w = ex2_approx(fmaf(s, p.scale_log2, m == -INFINITY ? 0.f : -m * p.scale_log2));
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float v = __bfloat162float(p.v[k * p.v_r + it.head * p.v_h + col + 32 * x + c]);
-                    if (!(fabsf(v) < INFINITY)) o[c] = __float_as_uint(fmaf(w, v, __uint_as_float(o[c])));
-                }
-            }
-            if (l == 0.f) {  // no weight at all: 0, and not 0 x NaN
-#pragma unroll
-                for (int c = 0; c < 32; ++c) o[c] = 0u;
-            }
-            store32(to, x, o);
+        for (int c = 0; c < 32; ++c) {
+            const int f = __shfl_sync(0xffffffffu, inf[c % 2], 16 * x + c / 2), n = __shfl_sync(0xffffffffu, nan[c % 2], 16 * x + c / 2);
+            const uint32_t add = n < seen ? 0x7FC00000u : f & 1 ? 0xFF800000u : 0x7F800000u;
+            // (added, since the steps that all queries see may have left an infinity too)
+            if (n < seen || f / 2 < seen) o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(add));
+            if (l == 0.f) o[c] = 0u;  // no weight at all: 0, and not 0 x NaN
         }
+        if (row < it.rows) store32(to_row, x, o);
         __syncwarp();
     }
 }
@@ -510,8 +518,10 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
             Item it = again ? sm->item[mine ? i & 1 : (i & 1) ^ 1] : next;
             __syncwarp();
             if (again) it.careful = 1;
-            if (lane < kMasked * 4) sm->odd[i & 1][lane / 4][lane % 4] = 0;
-            if (lane == 0) sm->again[mine ? i & 1 : other ? (i & 1) ^ 1 : i & 1] = 0;
+            if (lane == 0) {
+                sm->odd[i & 1] = 0;
+                sm->again[mine ? i & 1 : other ? (i & 1) ^ 1 : i & 1] = 0;
+            }
             __syncwarp();
             if (lane == 0) {
                 sm->item[i & 1] = it;
@@ -691,7 +701,6 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                         for (int y = 0; y < 4; ++y) seen |= (u[y] & 0x7FFF7FFFu) + 0x00800080u;
                     }
                     if (!__any_sync(0xffffffffu, seen & 0x80008000u)) continue;
-                    uint32_t odd[2] = {0, 0};
                     for (int r = 0; r < 2 * 64; r += 4) {
                         uint4 *at = (uint4 *)(slot + (r + lane / 8) * 128 + (lane % 8) * 16);
                         uint4 v = *at;
@@ -705,11 +714,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                             any |= lo || hi;
                         }
                         if (any) *at = v;
-                        const uint32_t lanes = __ballot_sync(0xffffffffu, any);
-                        for (int y = 0; y < 4; ++y)
-                            if (lanes >> (8 * y) & 0xff) odd[(r & 63) / 32] |= 1u << ((r + y) & 31);
                     }
-                    if (lane < 2) sm->odd[i & 1][j - masked][x * 2 + lane] = lane ? odd[1] : odd[0];
+                    if (lane == 0) sm->odd[i & 1] = 1;
                     fence_proxy_async_smem();
                 }
                 go();
@@ -860,10 +866,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 z[0] = add2(add2(z[0], z[1]), add2(z[2], z[3]));
                 again = bar_red_or(two, 64, mine && !(z[0].x + z[0].y == 0.f));
             }
-            uint32_t odd = 0;
-            if (it.careful)
-                for (int x = 0; x < kMasked && masked + x < j_end; ++x)
-                    for (int y = 0; y < 4; ++y) odd |= sm->odd[i & 1][x][y];
+            const bool odd = it.careful && sm->odd[i & 1];
             tc_fence_before();
             if (again) {
                 if (lane == 0) sm->again[i & 1] = 1;
@@ -871,7 +874,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_cons
                 continue;
             }
             if (odd && any) {
-                rows_with_odd(p, it, sm->odd[i & 1], r, min(vis, j_end * kTile), m, l, col, o_at);
+                rows_with_odd(p, it, r, min(vis, j_end * kTile), max(masked, j0) * kTile, min(j_end * kTile, it.keys), l, col, o_at);
                 tc_fence_before();
                 item_done(i);
             } else {

@@ -762,8 +762,8 @@ size_t nsa_mla_expand_kv_workspace_bytes(int m);
  * sum that divides are taken before that.  The division comes last, and weights are up to 2^8 before it:
  * values near the end of fp32's range overflow (up to 2^100 there is room for 2^19 keys).
  * What a row does not see is never used, whatever it holds: a NaN or infinity at a key reaches only the
- * rows that see it (a block of 256 rows some of which do not see all keys takes twice as long if a result
- * of it is not finite).  A score of -inf has weight 0, as in the formula (a component of out is NaN,
+ * rows that see it (a block of 256 rows some of which do not see all keys is done twice if a result of it is
+ * not finite, and rows whose scores are NaN look for their maximum at every step: up to three times as long).  A score of -inf has weight 0, as in the formula (a component of out is NaN,
  * 0 x inf, where that key's value is not finite); a row all of whose scores are -inf has lse -inf and
  * zeros.  A score of NaN or +inf makes the row NaN.
  * Device error (NSA_ERR_BOUNDS): a request whose starts decrease or leave [0, total] is left out.
