@@ -763,9 +763,11 @@ size_t nsa_mla_expand_kv_workspace_bytes(int m);
  * values near the end of fp32's range overflow (up to 2^100 there is room for 2^19 keys).
  * What a row does not see is never used, whatever it holds: a NaN or infinity at a key reaches only the
  * rows that see it (a block of 256 rows some of which do not see all keys is done twice if a result of it is
- * not finite, and rows whose scores are NaN look for their maximum at every step: up to three times as long).  A score of -inf has weight 0, as in the formula (a component of out is NaN,
- * 0 x inf, where that key's value is not finite); a row all of whose scores are -inf has lse -inf and
- * zeros.  A score of NaN or +inf makes the row NaN.
+ * not finite, and rows whose scores are NaN look for their maximum at every step: up to three times as long).
+ * A score of -inf has weight 0, as in the formula: lse and the components with finite values are those of
+ * the other keys.  Where the value under that weight is not finite, the component is not defined: it is NaN,
+ * an infinity or that of the other keys, by how the keys were cut into shares and steps.  A row all of whose
+ * scores are -inf has lse -inf and zeros.  A score of NaN or +inf makes the row NaN.
  * Device error (NSA_ERR_BOUNDS): a request whose starts decrease or leave [0, total] is left out.
  */
 nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, int64_t qn_ld_h, const void *q_rope_dev,

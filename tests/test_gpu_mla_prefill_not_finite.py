@@ -98,3 +98,24 @@ def test_the_call_takes_a_small_multiple_of_its_time(what):
     clean = best(kv.to(D))
     CHANGES[what](kv[..., 128:], g)
     assert best(kv.to(D)) < 5 * clean
+
+
+@pytest.mark.parametrize("name,nq,nk,causal,at", [
+    ("in one part", [300], [300], True, 3), ("in steps that all rows see", [130], [700], False, 5),
+    ("in a share that sees nothing else", [3], [5000], False, slice(0, 900)), ("the last key", [40], [2100], True, 2060),
+])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_weight_0_and_a_value_that_is_not_finite(name, nq, nk, causal, at, bad):
+    # whether that component shows it is not defined; the others, and lse, are those of the other keys
+    q, kv, k_rope, _ = _inputs(nq, nk, 2, 43)
+    q[..., 0] = q[..., 0].abs() + 0.1
+    kv[at, :, 0] = -INF
+    finite = kv.clone()
+    kv[at, :, 128 + 9] = bad
+    ws, cu_q, cu_k = nsa.alloc_mla_prefill_workspace(), F.starts(nq).to(D), F.starts(nk).to(D)
+    want, got = (_call(q.to(D), x.to(D), k_rope.to(D), cu_q, cu_k, causal, ws) for x in (finite, kv))
+    assert torch.equal(got[1], want[1])
+    other = torch.arange(128) != 9
+    assert torch.equal(got[0][..., other], want[0][..., other])
+    a, b = got[0][..., 9], want[0][..., 9]
+    assert (~torch.isfinite(a) | (a == b)).all() and torch.isfinite(want[0]).all()
