@@ -79,3 +79,17 @@ def test_far_apart_and_equal_calls():
 def test_no_rows():
     e, l = torch.empty((0, 128), dtype=F.BF, device="cuda"), torch.empty(0, device="cuda")
     nsa.nsa_merge_attention([e, e], [l, l], e.clone(), l.clone())
+
+
+@pytest.mark.parametrize("dtypes", [(F.BF, F.BF), (F.F32, F.F32), (F.F32, F.BF)], ids=["bf16", "f32", "f32 to bf16"])
+@pytest.mark.parametrize("n", [2, 3, 8])
+def test_values_near_the_end_of_the_range(n, dtypes):
+    # an average of finite values is finite, although their sum is not
+    g = torch.Generator().manual_seed(n)
+    parts = [(F.rand(g, 9, 64).sign() * 2.0 ** 127 * (1 + torch.rand((9, 1), generator=g) / 2)).to(dtypes[0]) for _ in range(n)]
+    parts[1:4] = [parts[0].clone() for _ in parts[1:4]]
+    lses = [torch.randn(9, generator=g) for _ in range(n)]
+    out, lse = torch.empty((9, 64), dtype=dtypes[1], device="cuda"), torch.empty(9, device="cuda")
+    nsa.nsa_merge_attention([p.cuda() for p in parts], [l.cuda() for l in lses], out, lse)
+    assert torch.isfinite(out).all()
+    _check(out, lse, parts, lses, dtypes[1])
