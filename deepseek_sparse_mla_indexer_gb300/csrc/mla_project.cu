@@ -668,7 +668,7 @@ nsa_status check_strides(const void *x, int64_t ld_r, int64_t ld_h, int R, int H
 {
     if ((H > 1 && ld_h < d) || (R > 1 && ld_r < d)) return NSA_ERR_INVALID_ARG;
     if (!aligned16(x) || (H > 1 && ld_h % 8) || (R > 1 && ld_r % 8)) return NSA_ERR_INVALID_ARG;
-    if (ld_r >= ((int64_t)1 << 38) || ld_h >= ((int64_t)1 << 38)) return NSA_ERR_UNSUPPORTED;
+    if ((R > 1 && ld_r >= ((int64_t)1 << 38)) || (H > 1 && ld_h >= ((int64_t)1 << 38))) return NSA_ERR_UNSUPPORTED;
     return NSA_OK;
 }
 

@@ -229,3 +229,13 @@ def test_merge_of_a_part_of_another_type_that_is_the_result(nsa):
         nsa.nsa_merge_attention([a, b], [l, l], b, l)
     with pytest.raises(ValueError, match="parts must be contiguous"):
         nsa.nsa_merge_attention([z(d=F32)], [l], z(d=F32), l)
+
+
+@pytest.mark.parametrize("fn,ld", [("nsa_mla_absorb_q", 128), ("nsa_mla_project_v", 512)])
+def test_the_stride_of_a_single_row_or_head_is_not_looked_at(nsa, fn, ld):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are none; without a GPU a call that nothing refuses ends where it asks for the device")
+    for far in (1 << 39, 1 << 62, -8, 0, 3):
+        for R, H, ld_r, ld_h in ((5, 1, ld, far), (1, 2, far, ld), (1, 1, far, far)):
+            got = _status(nsa, fn, [A, ld_r, ld_h, A, R, H, 128, 128, 512, A, 0, 0])
+            assert got not in (0, INVALID, UNSUPPORTED), (R, H, far)
