@@ -372,7 +372,9 @@ nsa_status nsa_sparse_mla_plan(nsa_dtype q_dtype, nsa_dtype kv_dtype, int R, int
  * no counterpart): one block waits for `budget_cycles` SM clocks on an
  * mbarrier that nothing arrives on, gives up and writes NSA_ERR_TIMEOUT into
  * the caller-zeroed status word, the way every tensor-core kernel here reports
- * a wait that ran out instead of hanging.  budget_cycles in [1, 4e9].
+ * a wait that ran out instead of hanging.  budget_cycles in [1, 4e9].  A call behind it
+ * may be launched while it waits (programmatic dependent launch); the time counts for
+ * none of that call's own bounded waits.
  */
 nsa_status nsa_check_bounded_wait(int32_t *status_dev, long long budget_cycles, nsa_stream_t stream);
 
@@ -768,6 +770,7 @@ size_t nsa_mla_expand_kv_workspace_bytes(int m);
  * the other keys.  Where the value under that weight is not finite, the component is not defined: it is NaN,
  * an infinity or that of the other keys, by how the keys were cut into shares and steps.  A row all of whose
  * scores are -inf has lse -inf and zeros.  A score of NaN or +inf makes the row NaN.
+ * sm_scale is positive and finite, else NSA_ERR_INVALID_ARG.
  * Device error (NSA_ERR_BOUNDS): a request whose starts decrease or leave [0, total] is left out.
  */
 nsa_status nsa_mla_prefill(const void *q_nope_dev, int64_t qn_ld_r, int64_t qn_ld_h, const void *q_rope_dev,

@@ -239,3 +239,7 @@ def test_the_stride_of_a_single_row_or_head_is_not_looked_at(nsa, fn, ld):
         for R, H, ld_r, ld_h in ((5, 1, ld, far), (1, 2, far, ld), (1, 1, far, far)):
             got = _status(nsa, fn, [A, ld_r, ld_h, A, R, H, 128, 128, 512, A, 0, 0])
             assert got not in (0, INVALID, UNSUPPORTED), (R, H, far)
+
+
+def test_the_version_tells_a_library_with_these_calls(nsa):
+    assert nsa.nsa_abi_version() >= 104
