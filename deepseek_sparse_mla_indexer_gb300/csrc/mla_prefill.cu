@@ -35,16 +35,17 @@
 // chosen on the device, where the lengths are.  The parts' fp32 results go to the workspace, and
 // merge_launch joins them.
 //
-// Measured (GB300, a pass among others; of 1969 TFLOP/s):
-//   one causal prompt of 8192, 128 heads       1545 us   1.78 PFLOP/s, 90 %
-//   the same with 32 heads                      405 us   1.70, 86 %
-//   eight prompts of 189 .. 2000, 128 heads     325 us   0.99, 50 % (1.18 with the hidden parts of the tiles)
-//   1001 / 768 over 40000 / 26651, 16 heads     388 us   1.60, 81 %
-//   37 after 600, 16 heads                       11.0 us in a graph, 38 with the host's part of the call
+// Measured (GB300, us in a graph on the same inputs / among passes whose inputs change; the latter of 1969 TFLOP/s):
+//   one causal prompt of 8192, 128 heads       1556 - 1598 / 1725   1.59 PFLOP/s, 81 %
+//   the same with 32 heads                      405 - 411 / -
+//   eight prompts of 189 .. 2000, 128 heads     300 - 362 / 318     1.01, 51 % (1.20 with the hidden parts of the tiles)
+//   1001 / 768 over 40000 / 26651, 16 heads     408 - 423 / 419     1.48, 75 %
+//   37 after 600, 16 heads                      9.4 - 11.7 / 39: the host's part of the call
+// (Ranges: between processes.)
 // A step of both tiles takes 3170 cycles where its products alone take 2560: the tensor core reads
 // shared memory at its full rate during QK (8 KB a product of 64 cycles), and the 80 KB that TMA writes a
 // step come on top (640 cycles).  The long prompt runs at the power limit (1.9 GHz at 1375 W when
-// repeated for seconds: 1.57 PFLOP/s).  Short prompts pay about 3.8 us an item beside its steps: the last
+// repeated for seconds: 1.56 PFLOP/s).  Short prompts pay about 3.8 us an item beside its steps: the last
 // step's softmax, which only one tile still has, the result's way out and the first step's softmax have no
 // products beside them.
 #include "mla_forms.cuh"
@@ -190,7 +191,8 @@ struct Work {
 
 // Parts: where there are few items, or a few long ones, their keys are cut into shares.  What so many shares of a
 // length cost, in units of a step (1.65 us): items of about one length go in rounds over the SMs; of different lengths,
-// handed out longest first per request, they end within half a long one of each other.  An item takes two steps beside
+// handed out longest first per request, they end within half a long one of each other where the long requests come
+// first (requests go in the caller's order: a long last one ends up to a whole item behind the others).  An item takes two steps beside
 // its own for its start and end; the join its launch and the fp32 results that it reads (`rows` of all parts; 0.12 us for
 // 6 x 256 on 152 SMs; 0: there is no join).
 __host__ __device__ inline float parts_cost(float items, int longest, float steps, float rows, float sms)

@@ -14,14 +14,14 @@
 // Persistent: one CTA an SM walks the tiles.  Sums are fp32, rounded to bf16 once.
 //
 // Measured (GB300, calls in a graph):
-//   expand, 8192 bf16 rows, 128 heads (pairs of CTAs, below)     173 us   1.59 PFLOP/s, 81 % of 1969 TFLOP/s
-//   expand, 1037 fp8 rows, 16 heads                                8.6 us, of which the gather is 2.5
-//   absorb / project, 32 rows, 128 heads                           4.7 / 4.3 us: 22 MB, mostly weights; the start
-//   absorb, 4001 rows, 16 heads                                   15.6 us: 84 MB, 5.4 TB/s; seven rounds of tiles, bound by
+//   expand, 8192 bf16 rows, 128 heads (pairs of CTAs, below)     169 us   1.63 PFLOP/s, 83 % of 1969 TFLOP/s
+//   expand, 1037 fp8 rows, 16 heads                                8.7 us, of which the gather is 2.5
+//   absorb / project, 32 rows, 128 heads                           4.6 / 4.1 us: 22 MB, mostly weights; the start
+//   absorb, 4001 rows, 16 heads                                   15.4 us: 84 MB, 5.5 TB/s; seven rounds of tiles, bound by
 //                                                                 what an SM moves between L2 and shared memory
-//   project, 4001 rows, 16 heads                                  10.3 us with its 66 MB of input in L2, 15.5 from HBM
+//   project, 4001 rows, 16 heads                                  10.5 us with its 66 MB of input in L2, 15.5 from HBM
 // Each launch starts under the end of the one before it and then waits for it (absorb of 4001 rows among other
-// calls: 16.4 us, and 18.8 started behind it).
+// calls: 16.8 us, and 18.8 started behind it).
 #include "mla_forms.cuh"
 
 namespace nsa {
