@@ -767,9 +767,10 @@ size_t nsa_mla_expand_kv_workspace_bytes(int m);
  * rows that see it (a block of 256 rows some of which do not see all keys is done twice if a result of it is
  * not finite, and rows whose scores are NaN look for their maximum at every step: up to three times as long).
  * A score of -inf has weight 0, as in the formula: lse and the components with finite values are those of
- * the other keys.  Where the value under that weight is not finite, the component is not defined: it is NaN,
- * an infinity or that of the other keys, by how the keys were cut into shares and steps.  A row all of whose
- * scores are -inf has lse -inf and zeros.  A score of NaN or +inf makes the row NaN.
+ * the other keys.  Where the value under that weight, or under one that is 0 in fp32 (a score 80 and more below
+ * the row's largest), is not finite, the component is not defined: it is NaN, an infinity or that of the other
+ * keys, by how the keys were cut into shares and steps.  A row all of whose scores are -inf has lse -inf and
+ * zeros.  A score of NaN or +inf makes the row NaN.
  * sm_scale is positive and finite, else NSA_ERR_INVALID_ARG.
  * Device error (NSA_ERR_BOUNDS): a request whose starts decrease or leave [0, total] is left out.
  */

@@ -119,3 +119,21 @@ def test_weight_0_and_a_value_that_is_not_finite(name, nq, nk, causal, at, bad):
     assert torch.equal(got[0][..., other], want[0][..., other])
     a, b = got[0][..., 9], want[0][..., 9]
     assert (~torch.isfinite(a) | (a == b)).all() and torch.isfinite(want[0]).all()
+
+
+@pytest.mark.parametrize("nq,nk,causal,at", [([300], [300], True, 3), ([130], [700], False, 5), ([3], [5000], False, slice(0, 900)),
+                                             ([40], [2100], True, 2060)])
+def test_a_weight_that_is_0_in_32_bits_and_an_infinity(nq, nk, causal, at):
+    # scores about 300 below the others: the formula's weight is not 0, that of 32 bits is
+    q, kv, k_rope, _ = _inputs(nq, nk, 2, 44)
+    q[..., 0] = 16.0
+    kv[at, :, 0] = -300.0
+    finite = kv.clone()
+    kv[at, :, 128 + 9] = INF
+    ws, cu_q, cu_k = nsa.alloc_mla_prefill_workspace(), F.starts(nq).to(D), F.starts(nk).to(D)
+    want, got = (_call(q.to(D), x.to(D), k_rope.to(D), cu_q, cu_k, causal, ws) for x in (finite, kv))
+    assert torch.equal(got[1], want[1]) and torch.isfinite(want[0]).all()
+    other = torch.arange(128) != 9
+    assert torch.equal(got[0][..., other], want[0][..., other])
+    a, b = got[0][..., 9], want[0][..., 9]
+    assert (~torch.isfinite(a) | (a == b)).all()
